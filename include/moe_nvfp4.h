@@ -305,6 +305,199 @@ MOE_API moe_status moe_nvfp4_forward_noalloc(const moe_nvfp4_config *config, con
                                              const uint16_t *x, const int32_t *topk_ids, const float *topk_weights,
                                              uint16_t *dst, int32_t n_tokens, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the layer in a decoder's MoE block.  They need no
+ * handle and allocate nothing; a call that needs scratch memory takes a
+ * device workspace of at least its _workspace_bytes, 16-byte aligned, whose
+ * contents it does not rely on and which is free again once the call's work
+ * on `stream` is done (calls whose work overlaps need workspaces of their
+ * own).  Results are bitwise the same on every run.
+ * ------------------------------------------------------------------------ */
+
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F32 1
+
+/* What the gate of a block is broadcast over. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1 /* [hidden], param_dtype: one value per channel */
+#define MOE_GATE_TOKEN 2   /* [n], fp32: one value per token */
+#define MOE_GATE_FULL 3    /* [n][hidden], branch_dtype */
+
+/* n rows of a matrix: row i starts at data + i * stride elements (stride 0:
+ * rows are contiguous).  data and the stride in bytes are multiples of 16. */
+typedef struct moe_rows {
+  void *data;
+  int64_t stride;
+} moe_rows;
+
+/* The norms before and after a block, with the block's gate and the scaled
+ * residual, in one call:
+ *     z = y * rp * (weight_offset + post_weight),  rp = 1 / sqrt(mean(y^2) + eps)
+ *         (z = y where post_weight is NULL)
+ *     u = residual_scale * residual + branch_scale * gate * z
+ *     x = u * ru * (weight_offset + pre_weight),   ru = 1 / sqrt(mean(u^2) + eps)
+ * with y the block's output (branch) and gate as given or, with gate_sigmoid,
+ * 1 / (1 + exp(-gate)).  residual_out receives u and x_out x; x is computed
+ * from u before u is rounded, so each output is rounded once.  Without branch
+ * (data NULL; then no gate, post_weight or rstd_post) the call is the norm
+ * before a block, without pre_weight (then no x_out or rstd_pre) the norm and
+ * gate after one; with both it is what runs between two blocks. */
+typedef struct moe_block_norm_args {
+  int32_t n;              /* tokens */
+  int32_t hidden;         /* multiple of 8, at most 8192 */
+  int32_t residual_dtype; /* MOE_DTYPE_ of residual and residual_out */
+  int32_t branch_dtype;   /* MOE_DTYPE_ of branch and of a MOE_GATE_FULL gate */
+  int32_t param_dtype;    /* MOE_DTYPE_ of the weights and of a MOE_GATE_CHANNEL gate */
+  int32_t gate_kind;      /* MOE_GATE_ */
+  int32_t gate_sigmoid;   /* 0 or 1 */
+  float eps;              /* > 0 */
+  float residual_scale;
+  float branch_scale;
+  float weight_offset;
+  moe_rows residual;
+  moe_rows branch;
+  moe_rows gate;          /* stride used by MOE_GATE_FULL alone */
+  const void *post_weight; /* [hidden] or NULL */
+  const void *pre_weight;  /* [hidden] or NULL */
+  moe_rows residual_out;   /* data may be NULL, or residual's (in place) */
+  moe_rows x_out;          /* bf16 */
+  float *rstd_post;        /* [n] receives rp; may be NULL */
+  float *rstd_pre;         /* [n] receives ru; may be NULL */
+} moe_block_norm_args;
+
+/* Enqueues the forward pass on `stream`; one launch, no workspace.
+ * Errors: MOE_ERR_INVALID_ARG (null, misaligned or missing pointer, negative
+ * n, bad enum value, eps not above zero, a stride below hidden),
+ * MOE_ERR_UNSUPPORTED (hidden), MOE_ERR_CUDA.  n = 0 enqueues nothing. */
+MOE_API moe_status moe_block_norm(const moe_block_norm_args *args, moe_stream_t stream);
+
+/* The backward pass.  G is the gradient that reaches u: with w = weight_offset
+ * + pre_weight and h = u * ru,
+ *     G = d_residual_out + ru * (w * d_x - h * mean(w * d_x * h))
+ *     d_residual    = residual_scale * G
+ *     dz            = branch_scale * gate * G
+ *     d_branch      = rp * (w' * dz - y rp * mean(w' * dz * y rp)),  w' of post_weight
+ *     d_gate        = branch_scale * z * G (times gate * (1 - gate) for a
+ *                     sigmoid), summed over what the gate is broadcast over
+ *     d_post_weight = sum over tokens of dz * y * rp
+ *     d_pre_weight  = sum over tokens of d_x * u * ru
+ * args holds the forward's inputs (residual itself is not read: data may be
+ * NULL), with residual_out, rstd_post and rstd_pre as the forward left them
+ * (here read).  Gradients have the type of what they belong to, but for
+ * d_post_weight, d_pre_weight and the d_gate of MOE_GATE_CHANNEL and
+ * MOE_GATE_TOKEN, which are fp32.  The sums over tokens run in fp32 in a fixed
+ * order.  A NULL d_residual_out or d_x is a zero gradient; a NULL output is
+ * not computed.  d_residual may be d_residual_out and d_branch may be branch
+ * (in place). */
+typedef struct moe_block_norm_grads {
+  moe_rows d_residual_out; /* in */
+  moe_rows d_x;            /* in, bf16 */
+  moe_rows d_residual;     /* out */
+  moe_rows d_branch;       /* out */
+  moe_rows d_gate;         /* out; stride used by MOE_GATE_FULL alone */
+  float *d_post_weight;    /* out [hidden] */
+  float *d_pre_weight;     /* out [hidden] */
+} moe_block_norm_grads;
+
+/* Errors: as moe_block_norm, and MOE_ERR_CAPACITY (workspace too small).
+ * n = 0 writes zeros to the gradients that are sums over tokens. */
+MOE_API moe_status moe_block_norm_backward(const moe_block_norm_args *args, const moe_block_norm_grads *grads,
+                                           void *workspace, size_t workspace_bytes, moe_stream_t stream);
+MOE_API size_t moe_block_norm_workspace_bytes(int32_t n, int32_t hidden);
+
+/* The router's balance loss.  z = logits + bias (one fp32 addition; bias may
+ * be NULL), p = softmax(z) over all experts.  Token t belongs to sequence s
+ * for seq_offsets[s] <= t < seq_offsets[s + 1] (NULL: one sequence of all n
+ * tokens); a token whose token_mask byte is 0 takes no part.  With N_s tokens
+ * that take part in s and N in all,
+ *     counts[s][e]    = picks of e among topk_ids of those tokens (ids outside
+ *                       [0, n_experts) count nowhere)
+ *     prob_sums[s][e] = sum of p over those tokens
+ *     tokens[s]       = N_s, tokens[n_seqs] = N
+ *     loss            = coef * n_experts / (N * top_k)
+ *                       * sum_s (1 / N_s) sum_e counts[s][e] * prob_sums[s][e]
+ * that is, coef times the token-weighted mean over the sequences of
+ * n_experts * sum_e f_e P_e with f the share of picks and P the mean
+ * probability; 0 when no token takes part.  A logit of -inf gives its expert
+ * probability 0, a row of nothing else adds no probability; the logits of
+ * masked tokens are not looked at.  Other infinities and NaN are outside the
+ * contract. */
+typedef struct moe_router_args {
+  int32_t n;                  /* tokens */
+  int32_t n_experts;          /* 1..1024 */
+  int32_t top_k;              /* 1..32 */
+  int32_t n_seqs;             /* >= 1; 1 where seq_offsets is NULL */
+  float coef;
+  const float *logits;        /* [n][n_experts] */
+  const float *bias;          /* [n_experts] or NULL */
+  const int32_t *topk_ids;    /* [n][top_k] */
+  const uint8_t *token_mask;  /* [n] or NULL */
+  const int32_t *seq_offsets; /* [n_seqs + 1], ascending, from 0 to n; or NULL */
+  int32_t *counts;            /* [n_seqs][n_experts] */
+  int32_t *tokens;            /* [n_seqs + 1] */
+} moe_router_args;
+
+/* Writes counts and tokens of args, prob_sums fp32 [n_seqs][n_experts] and
+ * loss fp32 [1].  seq_offsets that are not ascending give undefined results
+ * (no fault).  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (n_experts >
+ * 1024 or top_k > 32), MOE_ERR_CAPACITY (workspace too small), MOE_ERR_CUDA. */
+MOE_API moe_status moe_balance_loss(const moe_router_args *args, float *prob_sums, float *loss, void *workspace,
+                                    size_t workspace_bytes, moe_stream_t stream);
+
+/* The router's backward pass: the gradient of d_loss[0] * loss (NULL d_loss:
+ * 1) and of the top-k weights, with counts and tokens as moe_balance_loss
+ * left them (here read):
+ *     g[e]           = d_loss * coef * n_experts * counts[s][e] / (N * top_k * N_s)
+ *                      for a token that takes part in sequence s, else 0
+ *     d_logits[t][e] = p_e * (g_e - sum_i g_i p_i)
+ *                      + sum over j with topk_ids[t][j] = e of
+ *                        w_j * (d_w_j - sum_i w_i d_w_i)
+ *     d_bias[e]      = sum over tokens of d_logits[t][e]   (fixed order)
+ * topk_weights w and d_weights d_w are fp32 [n][top_k] (both NULL: no such
+ * term; token_mask does not touch it), d_logits fp32 [n][n_experts], d_bias
+ * fp32 [n_experts] or NULL.  counts NULL (then tokens too): no loss term.
+ * Errors: as moe_balance_loss. */
+MOE_API moe_status moe_router_backward(const moe_router_args *args, const float *topk_weights, const float *d_weights,
+                                       const float *d_loss, float *d_logits, float *d_bias, void *workspace,
+                                       size_t workspace_bytes, moe_stream_t stream);
+/* One size serves both calls. */
+MOE_API size_t moe_router_workspace_bytes(int32_t n, int32_t n_experts, int32_t n_seqs);
+
+/* Low-rank adapters of many requests at once, added to a shared projection's
+ * result.  Token t uses adapter l = adapter_ids[t] (an id outside [0,
+ * n_adapters), such as -1, uses none):
+ *     v[i]      = sum_c a[l][i][c] * x[t][c]        i < ranks[l]
+ *     out[t][o] = y[t][o] + scale[l] * sum_i b[l][o][i] * v[i]
+ * for every token and out[t] = y[t] without an adapter.  Products of bf16 are
+ * exact and summed in fp32; v is not rounded to fewer than 16 bits of
+ * mantissa on the way to the second product (24 for an fp32 out), and the
+ * result is rounded once. */
+typedef struct moe_lora_args {
+  int32_t n;            /* tokens */
+  int32_t in_features;  /* multiple of 8 */
+  int32_t out_features; /* multiple of 8 */
+  int32_t n_adapters;   /* 1..1024 */
+  int32_t max_rank;     /* multiple of 8, at most 128 */
+  int32_t y_dtype;      /* MOE_DTYPE_ of y */
+  int32_t out_dtype;    /* MOE_DTYPE_ of out */
+  const uint16_t *a;    /* bf16 [n_adapters][max_rank][in_features] */
+  const uint16_t *b;    /* bf16 [n_adapters][out_features][max_rank] */
+  const float *scale;   /* [n_adapters] or NULL: 1 */
+  const int32_t *ranks; /* [n_adapters], clamped to 0..max_rank; or NULL: max_rank.  What lies beyond an adapter's
+                           rank may hold anything */
+  const int32_t *adapter_ids; /* [n] */
+  moe_rows x;           /* bf16 [n][in_features] */
+  moe_rows y;           /* [n][out_features]; data may be NULL: zero */
+  moe_rows out;         /* [n][out_features]; data may be y's where the types and strides are the same */
+} moe_lora_args;
+
+/* Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (sizes outside the above),
+ * MOE_ERR_CAPACITY (workspace too small), MOE_ERR_CUDA.  n = 0 enqueues
+ * nothing. */
+MOE_API moe_status moe_lora_apply(const moe_lora_args *args, void *workspace, size_t workspace_bytes,
+                                  moe_stream_t stream);
+MOE_API size_t moe_lora_workspace_bytes(int32_t n, int32_t n_adapters);
+
 #ifdef __cplusplus
 }
 #endif

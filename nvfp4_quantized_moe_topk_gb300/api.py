@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -25,16 +26,18 @@ ENTRY_POINTS = ("moe_nvfp4_status_string", "moe_nvfp4_create", "moe_nvfp4_destro
                 "moe_nvfp4_forward_host", "moe_nvfp4_get_device_error", "moe_nvfp4_debug_routing",
                 "moe_nvfp4_debug_intermediates", "moe_nvfp4_set_timing", "moe_nvfp4_kernel_times",
                 "nvfp4_matmul", "weighted_row_sum", "moe_nvfp4_forward_noalloc", "moe_router_topk",
-                "moe_nvfp4_shared_expert_forward", "moe_nvfp4_debug_offset_grid_barrier")
+                "moe_nvfp4_shared_expert_forward", "moe_nvfp4_debug_offset_grid_barrier", "moe_block_norm",
+                "moe_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_balance_loss", "moe_router_backward",
+                "moe_router_workspace_bytes", "moe_lora_apply", "moe_lora_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
 
 
 class MoeError(RuntimeError):
-    def __init__(self, status: int, where: str):
+    def __init__(self, status: int, where: str, why: str = ""):
         self.status = status
-        super().__init__(f"{where}: {STATUS.get(status, status)} ({status_string(status)})")
+        super().__init__(f"{where}: {STATUS.get(status, status)} ({why or status_string(status)})")
 
 
 class Config(ctypes.Structure):
@@ -89,8 +92,19 @@ def load(build_if_missing: bool = False):
         L.moe_router_topk.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp]
         L.moe_nvfp4_forward_noalloc.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(Weights), vp, vp, vp, vp,
                                                 i32, vp]
+        sz = ctypes.c_size_t
+        L.moe_block_norm.argtypes = [vp, vp]
+        L.moe_block_norm_backward.argtypes = [vp, vp, vp, sz, vp]
+        L.moe_block_norm_workspace_bytes.argtypes = [i32, i32]
+        L.moe_balance_loss.argtypes = [vp, vp, vp, vp, sz, vp]
+        L.moe_router_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_router_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_lora_apply.argtypes = [vp, vp, sz, vp]
+        L.moe_lora_workspace_bytes.argtypes = [i32, i32]
         for name in ENTRY_POINTS:
-            if name != "moe_nvfp4_status_string":
+            if name.endswith("_workspace_bytes"):
+                getattr(L, name).restype = sz
+            elif name != "moe_nvfp4_status_string":
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
         return L
@@ -252,3 +266,315 @@ def forward_noalloc(hidden, inter, n_experts, top_k, up_codes, up_scales, down_c
                                             _ptr(topk_weights), _ptr(dst), n, _stream(stream)),
            "moe_nvfp4_forward_noalloc")
     return dst
+
+
+# ---------------------------------------------------------------- operators around the layer
+# The argument structs of the C header, packed in one step (their layouts are
+# checked against the header's by a test).
+_NORM_ARGS = struct.Struct("@7i4f4xPqPqPqPPPqPqPP")
+_NORM_GRADS = struct.Struct("@PqPqPqPqPqPP")
+_ROUTER_ARGS = struct.Struct("@4if4xPPPPPPP")
+_LORA_ARGS = struct.Struct("@7i4xPPPPPPqPqPq")
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+MAX_HIDDEN, MAX_EXPERTS, MAX_TOP_K = 8192, 1024, 32
+
+
+def _refuse(where: str, why: str):
+    raise MoeError(1, where, why)
+
+
+def _dtype_code(t, where, name):
+    """MOE_DTYPE_ of a tensor that may be bf16 or fp32."""
+    import torch
+
+    d = t.dtype
+    if d is torch.bfloat16:
+        return 0
+    if d is torch.float32:
+        return 1
+    _refuse(where, f"{name} is {d}; bfloat16 or float32 is supported")
+
+
+def _is(t, where, name, dtype, device):
+    if t.dtype is not dtype:
+        _refuse(where, f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != device or device < 0:
+        _refuse(where, f"{name} is not on the call's CUDA device")
+
+
+def _rows(t, where, name, dtype, device, n, cols):
+    """(address, row stride in elements, 0: contiguous) of an [n, cols] matrix; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    _is(t, where, name, dtype, device)
+    if tuple(t.shape) != (n, cols):
+        _refuse(where, f"{name} is {tuple(t.shape)}, not {(n, cols)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    step, inner = t.stride()
+    if (cols > 1 and inner != 1) or (n > 1 and step < cols):
+        _refuse(where, f"{name} has strides {t.stride()}: rows must be contiguous and must not overlap")
+    return t.data_ptr(), step if n > 1 else 0
+
+
+def _array(t, where, name, dtype, device, shape):
+    """Address of a contiguous array; 0 for None."""
+    if t is None:
+        return 0
+    _is(t, where, name, dtype, device)
+    if tuple(t.shape) != shape:
+        _refuse(where, f"{name} is {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        _refuse(where, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _workspace(workspace, need, where, device, stream):
+    """(tensor, address, bytes): the caller's, or one of this call allocated on its stream."""
+    import torch
+
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=f"cuda:{device}")
+        else:
+            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=f"cuda:{device}")
+    else:
+        _is(workspace, where, "workspace", torch.uint8, device)
+        if not workspace.is_contiguous():
+            _refuse(where, "workspace is not contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _on(device, where):
+    """The call's device is the current one (its kernels are launched there)."""
+    import torch
+
+    if device < 0 or device != torch.cuda.current_device():
+        _refuse(where, "the tensors are not on the current CUDA device")
+
+
+def _norm_gate(gate, n, hidden, act, par, device, where, name="gate", grad=False):
+    """(kind, address, stride) of a gate [hidden], [n, 1] or [n, hidden]; its gradient is fp32 where it is a sum."""
+    import torch
+
+    if gate is None:
+        return GATE_NONE, 0, 0
+    shape = tuple(gate.shape)
+    if shape == (hidden,):
+        return GATE_CHANNEL, _array(gate, where, name, torch.float32 if grad else par, device, shape), 0
+    if shape == (n, 1):
+        return GATE_TOKEN, _array(gate, where, name, torch.float32, device, shape), 0
+    if shape != (n, hidden):
+        _refuse(where, f"{name} is {shape}; {(hidden,)}, {(n, 1)} or {(n, hidden)} is supported")
+    p, step = _rows(gate, where, name, act, device, n, hidden)
+    return GATE_FULL, p, step
+
+
+def _norm_pack(where, n, hidden, device, res, act, par, residual, branch, gate, post_weight, pre_weight, residual_out,
+               x_out, rstd_post, rstd_pre, eps, residual_scale, branch_scale, weight_offset, gate_sigmoid):
+    import torch
+
+    kinds = (torch.bfloat16, torch.float32)
+    kind, gp, gs = _norm_gate(gate, n, hidden, kinds[act], kinds[par], device, where)
+    vec = (hidden,)
+    return kind, _NORM_ARGS.pack(
+        n, hidden, res, act, par, kind, 1 if gate_sigmoid and kind else 0, eps, residual_scale, branch_scale,
+        weight_offset, *_rows(residual, where, "residual", kinds[res], device, n, hidden),
+        *_rows(branch, where, "branch", kinds[act], device, n, hidden), gp, gs,
+        _array(post_weight, where, "post_weight", kinds[par], device, vec),
+        _array(pre_weight, where, "pre_weight", kinds[par], device, vec),
+        *_rows(residual_out, where, "residual_out", kinds[res], device, n, hidden),
+        *_rows(x_out, where, "x_out", torch.bfloat16, device, n, hidden),
+        _array(rstd_post, where, "rstd_post", torch.float32, device, (n,)),
+        _array(rstd_pre, where, "rstd_pre", torch.float32, device, (n,)))
+
+
+def _param_code(where, post_weight, pre_weight, gate, hidden):
+    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if t is not None:
+            return _dtype_code(t, where, name)
+    return _dtype_code(gate, where, "gate") if gate is not None and tuple(gate.shape) == (hidden,) else 1
+
+
+def block_norm(residual, branch=None, gate=None, post_weight=None, pre_weight=None, residual_out=None, x_out=None,
+               rstd_post=None, rstd_pre=None, *, eps: float = 1e-6, residual_scale: float = 1.0,
+               branch_scale: float = 1.0, weight_offset: float = 0.0, gate_sigmoid: bool = False, stream=None):
+    """``moe_block_norm``: the norms before and after a block with its gate and residual, in one call.
+
+    residual_out = residual_scale * residual + branch_scale * gate * norm(branch, post_weight) and
+    x_out = norm(residual_out, pre_weight).  Tensors are [n, hidden]; the gate is [hidden], [n, 1] (fp32) or
+    [n, hidden]; without ``branch`` it is the norm before a block, without ``pre_weight`` the norm after one."""
+    where = "moe_block_norm"
+    if residual is None or residual.dim() != 2:
+        _refuse(where, "residual is not an [n, hidden] tensor")
+    n, hidden = residual.shape
+    device = residual.get_device()
+    _on(device, where)
+    res = _dtype_code(residual, where, "residual")
+    act = res if branch is None else _dtype_code(branch, where, "branch")
+    par = _param_code(where, post_weight, pre_weight, gate, hidden)
+    _, args = _norm_pack(where, n, hidden, device, res, act, par, residual, branch, gate, post_weight, pre_weight,
+                         residual_out, x_out, rstd_post, rstd_pre, eps, residual_scale, branch_scale, weight_offset,
+                         gate_sigmoid)
+    _check(load().moe_block_norm(args, _stream(stream)), where)
+    return residual_out, x_out
+
+
+def block_norm_workspace(n: int, hidden: int):
+    """A workspace for block_norm_backward of up to n tokens."""
+    import torch
+
+    return torch.empty(max(16, load().moe_block_norm_workspace_bytes(n, hidden)), dtype=torch.uint8, device="cuda")
+
+
+def block_norm_backward(d_residual_out, d_x, residual_out, branch=None, gate=None, post_weight=None, pre_weight=None,
+                        rstd_post=None, rstd_pre=None, d_residual=None, d_branch=None, d_gate=None,
+                        d_post_weight=None, d_pre_weight=None, *, eps: float = 1e-6, residual_scale: float = 1.0,
+                        branch_scale: float = 1.0, weight_offset: float = 0.0, gate_sigmoid: bool = False,
+                        workspace=None, stream=None):
+    """``moe_block_norm_backward``: fills the given gradients from those of residual_out and x_out (either may be
+    None: zero).  residual_out, rstd_post and rstd_pre are what block_norm left."""
+    import torch
+
+    where = "moe_block_norm_backward"
+    lead = next((t for t in (d_residual_out, d_x, residual_out, branch) if t is not None), None)
+    if lead is None or lead.dim() != 2:
+        _refuse(where, "no [n, hidden] gradient is given")
+    n, hidden = lead.shape
+    device = lead.get_device()
+    _on(device, where)
+    stream_of = next((t for t in (d_residual_out, residual_out, d_residual) if t is not None), None)
+    res = 1 if stream_of is None else _dtype_code(stream_of, where, "residual")
+    act = res if branch is None else _dtype_code(branch, where, "branch")
+    par = _param_code(where, post_weight, pre_weight, gate, hidden)
+    kind, args = _norm_pack(where, n, hidden, device, res, act, par, None, branch, gate, post_weight, pre_weight,
+                            residual_out, None, rstd_post, rstd_pre, eps, residual_scale, branch_scale, weight_offset,
+                            gate_sigmoid)
+    kinds = (torch.bfloat16, torch.float32)
+    dk, dgp, dgs = _norm_gate(d_gate, n, hidden, kinds[act], kinds[par], device, where, "d_gate", grad=True)
+    if dk not in (GATE_NONE, kind):
+        _refuse(where, f"d_gate is {tuple(d_gate.shape)}, the gate another shape")
+    grads = _NORM_GRADS.pack(
+        *_rows(d_residual_out, where, "d_residual_out", kinds[res], device, n, hidden),
+        *_rows(d_x, where, "d_x", torch.bfloat16, device, n, hidden),
+        *_rows(d_residual, where, "d_residual", kinds[res], device, n, hidden),
+        *_rows(d_branch, where, "d_branch", kinds[act], device, n, hidden), dgp, dgs,
+        _array(d_post_weight, where, "d_post_weight", torch.float32, device, (hidden,)),
+        _array(d_pre_weight, where, "d_pre_weight", torch.float32, device, (hidden,)))
+    L = load()
+    need = 0 if workspace is not None else L.moe_block_norm_workspace_bytes(n, hidden)
+    keep, wp, wb = _workspace(workspace, need, where, device, stream)
+    _check(L.moe_block_norm_backward(args, grads, wp, wb, _stream(stream)), where)
+    return d_residual, d_branch
+
+
+def router_workspace(n: int, n_experts: int, n_seqs: int = 1):
+    """A workspace for balance_loss and router_backward of up to n tokens in n_seqs sequences."""
+    import torch
+
+    return torch.empty(max(16, load().moe_router_workspace_bytes(n, n_experts, n_seqs)), dtype=torch.uint8,
+                       device="cuda")
+
+
+def _router_pack(where, logits, bias, topk_ids, counts, tokens, coef, mask, seq_offsets):
+    import torch
+
+    if logits is None or logits.dim() != 2 or topk_ids is None or topk_ids.dim() != 2:
+        _refuse(where, "logits are not [n, n_experts] or topk_ids not [n, top_k]")
+    n, E = logits.shape
+    k = topk_ids.shape[1]
+    device = logits.get_device()
+    _on(device, where)
+    S = 1
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        if S < 1:
+            _refuse(where, "seq_offsets holds no sequence")
+    if mask is not None and mask.dtype is torch.bool:
+        mask = mask.view(torch.uint8)
+    f, i = torch.float32, torch.int32
+    args = _ROUTER_ARGS.pack(
+        n, E, k, S, coef, _array(logits, where, "logits", f, device, (n, E)),
+        _array(bias, where, "bias", f, device, (E,)), _array(topk_ids, where, "topk_ids", i, device, (n, k)),
+        _array(mask, where, "mask", torch.uint8, device, (n,)),
+        _array(seq_offsets, where, "seq_offsets", i, device, (S + 1,)),
+        _array(counts, where, "counts", i, device, (S, E)), _array(tokens, where, "tokens", i, device, (S + 1,)))
+    return n, E, k, S, device, args
+
+
+def balance_loss(logits, bias, topk_ids, loss, counts, prob_sums, tokens, *, coef: float, mask=None,
+                 seq_offsets=None, workspace=None, stream=None):
+    """``moe_balance_loss``: fills loss [1], counts [S, E] int32, prob_sums [S, E] and tokens [S + 1] int32 (each
+    sequence's tokens, then all) from logits [n, E] (+ bias [E]) and topk_ids [n, k].  ``mask`` [n] (bool or uint8)
+    leaves tokens out; ``seq_offsets`` [S + 1] int32 cuts the batch into sequences (None: one)."""
+    import torch
+
+    where = "moe_balance_loss"
+    n, E, _, S, device, args = _router_pack(where, logits, bias, topk_ids, counts, tokens, coef, mask, seq_offsets)
+    L = load()
+    need = 0 if workspace is not None else L.moe_router_workspace_bytes(n, E, S)
+    keep, wp, wb = _workspace(workspace, need, where, device, stream)
+    f = torch.float32
+    _check(L.moe_balance_loss(args, _array(prob_sums, where, "prob_sums", f, device, (S, E)),
+                              _array(loss, where, "loss", f, device, (1,)), wp, wb, _stream(stream)), where)
+    return loss
+
+
+def router_backward(logits, bias, topk_ids, topk_weights, d_weights, counts, tokens, d_logits, d_bias=None, *,
+                    d_loss=None, coef: float, mask=None, seq_offsets=None, workspace=None, stream=None):
+    """``moe_router_backward``: d_logits [n, E] (and d_bias [E]) of d_loss [1] times the balance loss (counts and
+    tokens as balance_loss left them; None: no loss) and of the top-k weights (d_weights [n, k]; None: none)."""
+    import torch
+
+    where = "moe_router_backward"
+    n, E, k, S, device, args = _router_pack(where, logits, bias, topk_ids, counts, tokens, coef, mask, seq_offsets)
+    L = load()
+    need = 0 if workspace is not None else L.moe_router_workspace_bytes(n, E, S)
+    keep, wp, wb = _workspace(workspace, need, where, device, stream)
+    f = torch.float32
+    _check(L.moe_router_backward(args, _array(topk_weights, where, "topk_weights", f, device, (n, k)),
+                                 _array(d_weights, where, "d_weights", f, device, (n, k)),
+                                 _array(d_loss, where, "d_loss", f, device, (1,)),
+                                 _array(d_logits, where, "d_logits", f, device, (n, E)),
+                                 _array(d_bias, where, "d_bias", f, device, (E,)), wp, wb, _stream(stream)), where)
+    return d_logits
+
+
+def lora_workspace(n: int, n_adapters: int):
+    """A workspace for lora_apply of up to n tokens over n_adapters adapters."""
+    import torch
+
+    return torch.empty(max(16, load().moe_lora_workspace_bytes(n, n_adapters)), dtype=torch.uint8, device="cuda")
+
+
+def lora_apply(x, adapter_ids, a, b, y, out, *, scale=None, ranks=None, workspace=None, stream=None):
+    """``moe_lora_apply``: out[t] = y[t] + scale[l] * B[l] (A[l] x[t]) with l = adapter_ids[t] (an id outside the
+    bank, such as -1: out[t] = y[t]).  x [n, in] bf16, a [L, R, in] and b [L, out, R] bf16, y [n, out] (None: zero)
+    and out [n, out] bf16 or fp32 (out may be y), scale [L] fp32, ranks [L] int32."""
+    import torch
+
+    where = "moe_lora_apply"
+    if x is None or x.dim() != 2 or a is None or a.dim() != 3 or b is None or b.dim() != 3 or out is None:
+        _refuse(where, "x is not [n, in], a not [L, R, in], b not [L, out, R], or out is missing")
+    n, inp = x.shape
+    L_, R, _ = a.shape
+    o = b.shape[1]
+    device = x.get_device()
+    _on(device, where)
+    yd = 0 if y is None else _dtype_code(y, where, "y")
+    od = _dtype_code(out, where, "out")
+    kinds = (torch.bfloat16, torch.float32)
+    bf, f, i = torch.bfloat16, torch.float32, torch.int32
+    args = _LORA_ARGS.pack(
+        n, inp, o, L_, R, yd, od, _array(a, where, "a", bf, device, (L_, R, inp)),
+        _array(b, where, "b", bf, device, (L_, o, R)), _array(scale, where, "scale", f, device, (L_,)),
+        _array(ranks, where, "ranks", i, device, (L_,)), _array(adapter_ids, where, "adapter_ids", i, device, (n,)),
+        *_rows(x, where, "x", bf, device, n, inp), *_rows(y, where, "y", kinds[yd], device, n, o),
+        *_rows(out, where, "out", kinds[od], device, n, o))
+    L = load()
+    need = 0 if workspace is not None else L.moe_lora_workspace_bytes(n, L_)
+    keep, wp, wb = _workspace(workspace, need, where, device, stream)
+    _check(L.moe_lora_apply(args, wp, wb, _stream(stream)), where)
+    return out

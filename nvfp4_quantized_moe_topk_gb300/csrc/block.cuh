@@ -1,0 +1,61 @@
+// block.cuh -- loads and stores shared by the kernels around the layer
+// (block_norm.cu, lora.cu): rows with a stride, 8 values at a time, bf16 or
+// fp32 in memory and fp32 in registers.
+#pragma once
+
+#include "../../include/moe_nvfp4.h"
+#include "common.cuh"
+
+namespace moe {
+
+// Row t of a moe_rows whose contiguous row holds `cols` elements of T.
+template <typename T>
+__device__ __forceinline__ T* row_ptr(const moe_rows& r, int64_t t, int64_t cols) {
+  return static_cast<T*>(r.data) + t * (r.stride ? r.stride : cols);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& d, float (&v)[8]) {
+  v[0] = bf16lo(d.x);
+  v[1] = bf16hi(d.x);
+  v[2] = bf16lo(d.y);
+  v[3] = bf16hi(d.y);
+  v[4] = bf16lo(d.z);
+  v[5] = bf16hi(d.z);
+  v[6] = bf16lo(d.w);
+  v[7] = bf16hi(d.w);
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = a.z;
+  v[3] = a.w;
+  v[4] = b.x;
+  v[5] = b.y;
+  v[6] = b.z;
+  v[7] = b.w;
+}
+// 8 parameters from column c on, of a type known at run time.
+__device__ __forceinline__ void load8_param(const void* p, int32_t dtype, int32_t c, float (&v)[8]) {
+  if (dtype == MOE_DTYPE_BF16)
+    load8(static_cast<const uint16_t*>(p) + c, v);
+  else
+    load8(static_cast<const float*>(p) + c, v);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  uint4 d;
+  d.x = pack_bf16x2(v[0], v[1]);
+  d.y = pack_bf16x2(v[2], v[3]);
+  d.z = pack_bf16x2(v[4], v[5]);
+  d.w = pack_bf16x2(v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = d;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+}  // namespace moe

@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "../../include/moe_nvfp4.h"
+
 namespace moe {
 
 // Raises a kernel's dynamic shared-memory limit on the current device, once
@@ -218,6 +220,27 @@ DecLayout decode_layout(int32_t E, int32_t R, bool can_stage);
 // external routing); one-token batches take the per-chunk kernel alone.
 inline bool decode_can_stage(int32_t n, int32_t ext) { return n > 1 || ext; }
 cudaError_t launch_decode(const DecodeArgs& args, int num_sms, cudaStream_t s);
+
+// ------------------------------------------------- operators around the layer
+constexpr int kNormMaxHidden = 8192;
+constexpr int kNormBackwardBlocks = 304;  // CTAs of the norms' backward pass, each with a slot of column sums
+int block_norm_backward_blocks(int32_t n);
+cudaError_t launch_block_norm(const moe_block_norm_args& a, cudaStream_t s);
+// part: [block_norm_backward_blocks(n)][3][hidden] floats.
+cudaError_t launch_block_norm_backward(const moe_block_norm_args& a, const moe_block_norm_grads& d, float* part,
+                                       cudaStream_t s);
+
+constexpr int kRouterLossBlocks = 304;  // blocks of the balance loss and the router's backward pass
+int32_t router_loss_blocks(int32_t n);
+size_t router_loss_workspace(int32_t n, int32_t E, int32_t S);  // bytes
+cudaError_t launch_balance_loss(const moe_router_args& a, float* prob_sums, float* loss, void* workspace,
+                                cudaStream_t s);
+cudaError_t launch_router_backward(const moe_router_args& a, const float* w, const float* dw, const float* d_loss,
+                                   float* d_logits, float* d_bias, void* workspace, cudaStream_t s);
+
+constexpr int kLoraMaxRank = 128;
+size_t lora_workspace(int32_t n, int32_t n_adapters);  // bytes
+cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s);
 
 // Host helpers for tensor maps (driver entry point resolved at run time).
 cudaError_t make_tmap_act(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K);
