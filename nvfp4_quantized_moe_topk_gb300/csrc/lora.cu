@@ -1,10 +1,33 @@
 // lora.cu -- low-rank adapters of many requests at once, added to a shared
 // projection's result (moe_lora_apply).
 //
-//   v = A[l] x (over the adapter's rank),  out = y + scale[l] B[l] v
+//   v = A[l] x (over the adapter's rank),  out = y + B[l] (scale[l] v)
 //
-// One CTA per token: its warps form the rank's dot products over x, then its
-// threads the outputs from v in shared memory.
+// Tokens are grouped by adapter into tiles of 16, 32 or 64, and one CTA (or a
+// cluster of CTAs, where there are few tiles) takes a tile through both
+// products: v never leaves the SM.  Both are bf16 warp matrix instructions
+// with tokens as rows.  At ranks up to 128 they are far below the tensor
+// cores' rate; what bounds the call is moving x, y and out, so the operands go
+// straight from global memory to registers: a lane's 16 bytes of a row are
+// the k elements of two matrix instructions (the order of k inside a window
+// of 32 is free as long as both operands use it), every byte of x is loaded
+// by one warp, and no shared-memory stage or barrier stands in the loops.
+//
+//   first product:  the warps (and the cluster's CTAs) split in_features in
+//     windows of 32; their partial sums meet in shared memory (and in the
+//     cluster's shared memories), added in a fixed order.
+//   second product: the warps split out_features in blocks of 32 columns.  The
+//     columns of a block are dealt to the four 8-column instructions so that
+//     a lane ends up with 8 neighbouring columns of a token: y comes in and
+//     out goes out as 16-byte vectors.  v enters as the sum of two bf16 terms
+//     (16 bits of mantissa), three for an fp32 out (24 bits).
+//
+// Grouping: up to kFusedTokens tokens every CTA ranks the ids itself; beyond,
+// a one-CTA kernel (two kernels past kPlanSlice tokens) sorts the tokens by
+// adapter into the workspace.  A token's row of the products depends on no
+// other token, so the order inside a group does not matter to the result.
+#include <algorithm>
+
 #include "block.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -14,72 +37,498 @@ namespace moe {
 namespace {
 
 constexpr int kLoraThreads = 256;
+constexpr int kLoraWarps = kLoraThreads / 32;
+constexpr int kFusedTokens = 256;         // at most one token a thread
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanPer = 16;              // tokens a thread of the sorting kernel
+constexpr int kPlanSlice = kPlanThreads * kPlanPer;
 
-template <typename YT, typename OT>
-__global__ void __launch_bounds__(kLoraThreads) lora_token_kernel(const moe_lora_args a) {
-  __shared__ float v[128];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x;
-  const int32_t l = a.adapter_ids[t];
-  int32_t rank = 0;
-  float scale = 0.f;
-  if (l >= 0 && l < a.n_adapters) {
-    rank = a.ranks ? min(max(a.ranks[l], 0), a.max_rank) : a.max_rank;
-    scale = a.scale ? a.scale[l] : 1.f;
-  }
-  const uint16_t* x = row_ptr<const uint16_t>(a.x, t, a.in_features);
-  for (int32_t i = warp; i < rank; i += kLoraThreads / 32) {
-    const uint16_t* w = a.a + ((int64_t)l * a.max_rank + i) * a.in_features;
-    float sum = 0.f;
-    for (int32_t c = lane * 8; c < a.in_features; c += 256) {
-      float p[8], q[8];
-      load8(x + c, p);
-      load8(w + c, q);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(p[j], q[j], sum);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) v[i] = sum;
+// Sorted tokens and group starts; bucket n_adapters holds the tokens without
+// an adapter.
+struct LoraPlan {
+  int32_t* order;      // [n] tokens by bucket
+  int32_t* starts;     // [n_adapters + 2] first entry of each bucket in order
+  int32_t* tile_base;  // [n_adapters + 2] first tile of each bucket
+  int32_t* hist;       // [slices][n_adapters + 1], several slices only
+};
+
+int64_t up4(int64_t v) { return (v + 3) & ~int64_t(3); }
+int32_t plan_slices(int32_t n) { return (int32_t)(((int64_t)n + kPlanSlice - 1) / kPlanSlice); }
+
+LoraPlan lora_plan(void* ws, int32_t n, int32_t L) {
+  LoraPlan p;
+  p.order = static_cast<int32_t*>(ws);
+  p.starts = p.order + up4(n);
+  p.tile_base = p.starts + up4(L + 2);
+  p.hist = p.tile_base + up4(L + 2);
+  return p;
+}
+
+__device__ __forceinline__ int32_t bucket_of(int32_t id, int32_t L) { return id >= 0 && id < L ? id : L; }
+
+__global__ void __launch_bounds__(kPlanThreads)
+    lora_hist_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t L, int32_t* __restrict__ hist) {
+  extern __shared__ int32_t sm_hist[];  // [L + 1]
+  for (int32_t l = threadIdx.x; l <= L; l += kPlanThreads) sm_hist[l] = 0;
+  __syncthreads();
+  const int64_t beg = (int64_t)blockIdx.x * kPlanSlice;
+#pragma unroll 4
+  for (int j = 0; j < kPlanPer; ++j) {
+    const int64_t i = beg + threadIdx.x + j * kPlanThreads;
+    const int32_t key = i < n ? bucket_of(ids[i], L) : -1;
+    const uint32_t peers = __match_any_sync(0xffffffffu, key);
+    if (key >= 0 && (int)(threadIdx.x & 31) == __ffs(peers) - 1) atomicAdd(&sm_hist[key], __popc(peers));
   }
   __syncthreads();
-  for (int32_t o = threadIdx.x * 8; o < a.out_features; o += kLoraThreads * 8) {
-    float r[8] = {};
-    if (a.y.data) load8(row_ptr<const YT>(a.y, t, a.out_features) + o, r);
-    if (rank > 0) {
+  for (int32_t l = threadIdx.x; l <= L; l += kPlanThreads) hist[(int64_t)blockIdx.x * (L + 1) + l] = sm_hist[l];
+}
+
+// Sorts slice blockIdx.x (hist: the slices' histograms, nullptr for one slice).
+__global__ void __launch_bounds__(kPlanThreads)
+    lora_plan_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t L, int32_t tile, LoraPlan p,
+                     const int32_t* __restrict__ hist) {
+  extern __shared__ int32_t sm_plan[];  // count, then first position, of each of this slice's buckets: [L + 1]
+  __shared__ int32_t warp_cnt[32], warp_tiles[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int64_t beg = (int64_t)blockIdx.x * kPlanSlice;
+  pdl_launch_dependents();
+  int32_t key[kPlanPer], rank[kPlanPer];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint16_t* w = a.b + ((int64_t)l * a.out_features + o + j) * a.max_rank;
-        float sum = 0.f;
-        for (int32_t i = 0; i < rank; ++i) sum = fmaf(v[i], bf16lo(w[i]), sum);
-        r[j] = fmaf(scale, sum, r[j]);
+  for (int j = 0; j < kPlanPer; ++j) {
+    const int64_t i = beg + tid + j * kPlanThreads;
+    key[j] = i < n ? ids[i] : 0;
+  }
+  for (int32_t l = tid; l <= L; l += kPlanThreads) sm_plan[l] = 0;
+  __syncthreads();
+  const int steps = (int)min((int64_t)kPlanPer, ((int64_t)n - beg + kPlanThreads - 1) / kPlanThreads);
+#pragma unroll
+  for (int j = 0; j < kPlanPer; ++j) {
+    if (j >= steps) break;
+    key[j] = beg + tid + j * kPlanThreads < n ? bucket_of(key[j], L) : -1;
+    const uint32_t peers = __match_any_sync(0xffffffffu, key[j]);
+    const int leader = __ffs(peers) - 1;
+    int32_t base = 0;
+    if (key[j] >= 0 && lane == leader) base = atomicAdd(&sm_plan[key[j]], __popc(peers));
+    rank[j] = __shfl_sync(0xffffffffu, base, leader) + __popc(peers & ((1u << lane) - 1u));
+  }
+  __syncthreads();
+  // adapter tid: its tokens in all slices and in those before this one
+  int32_t total = 0, before = 0, none_before = 0;
+  if (tid < L) total = sm_plan[tid];
+  if (hist) {
+    if (tid < L) {
+      total = 0;
+      for (int32_t b = 0; b < (int32_t)gridDim.x; ++b) {
+        const int32_t v = hist[(int64_t)b * (L + 1) + tid];
+        total += v;
+        before += b < (int32_t)blockIdx.x ? v : 0;
       }
     }
-    store8(row_ptr<OT>(a.out, t, a.out_features) + o, r);
+    for (int32_t b = 0; b < (int32_t)blockIdx.x; ++b) none_before += hist[(int64_t)b * (L + 1) + L];
   }
+  const int32_t tiles = (total + tile - 1) / tile;
+  int32_t ic = total, it = tiles;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t vc = __shfl_up_sync(0xffffffffu, ic, d), vt = __shfl_up_sync(0xffffffffu, it, d);
+    if (lane >= d) {
+      ic += vc;
+      it += vt;
+    }
+  }
+  if (lane == 31) {
+    warp_cnt[warp] = ic;
+    warp_tiles[warp] = it;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int32_t c = warp_cnt[lane], t = warp_tiles[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t vc = __shfl_up_sync(0xffffffffu, c, d), vt = __shfl_up_sync(0xffffffffu, t, d);
+      if (lane >= d) {
+        c += vc;
+        t += vt;
+      }
+    }
+    warp_cnt[lane] = c;
+    warp_tiles[lane] = t;
+  }
+  __syncthreads();
+  const int32_t start = ic - total + (warp ? warp_cnt[warp - 1] : 0);
+  const int32_t tbase = it - tiles + (warp ? warp_tiles[warp - 1] : 0);
+  if (tid < L) sm_plan[tid] = start + before;
+  if (tid == 0) sm_plan[L] = warp_cnt[31] + none_before;
+  if (blockIdx.x == 0) {
+    if (tid < L) {
+      p.starts[tid] = start;
+      p.tile_base[tid] = tbase;
+    }
+    if (tid == 0) {
+      p.starts[L] = warp_cnt[31];
+      p.starts[L + 1] = n;
+      p.tile_base[L] = warp_tiles[31];
+      p.tile_base[L + 1] = warp_tiles[31] + (n - warp_cnt[31] + tile - 1) / tile;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPlanPer; ++j) {
+    if (j >= steps) break;
+    if (key[j] >= 0) p.order[sm_plan[key[j]] + rank[j]] = (int32_t)(beg + tid + j * kPlanThreads);
+  }
+}
+
+// ------------------------------------------------------------ the products
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at this CTA's shared address `p`, in CTA `rank` of the cluster.
+__device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
+  uint32_t addr;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// What a CTA works on.
+struct Tile {
+  int32_t adapter, count;
+};
+
+// Finds this CTA's tile and its tokens (row[i], -1 past the count).  Returns
+// false, for the whole cluster alike, where there is none left.
+template <int MT>
+__device__ __forceinline__ bool find_tile(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tile,
+                                          int32_t* row, int32_t* scratch, Tile& t) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, L = a.n_adapters;
+  __shared__ int32_t found[3];
+  if (tid == 0) found[0] = -1;
+  if (tid < MT) row[tid] = -1;
+  if (!fused) {
+    pdl_wait();
+    __syncthreads();
+    for (int32_t l = tid; l <= L; l += kLoraThreads) {
+      const int32_t b0 = p.tile_base[l], b1 = p.tile_base[l + 1];
+      if (tile >= b0 && tile < b1) {
+        const int32_t first = p.starts[l] + (tile - b0) * MT;
+        found[0] = l;
+        found[1] = first;
+        found[2] = min(MT, p.starts[l + 1] - first);
+      }
+    }
+    __syncthreads();
+    t.adapter = found[0];
+    if (t.adapter < 0) return false;
+    t.count = found[2];
+    if (tid < t.count) row[tid] = p.order[found[1] + tid];
+    __syncthreads();
+    return true;
+  }
+  // ids in shared memory; a token whose rank among its adapter's is a multiple
+  // of MT leads a tile, tiles in the order of their leaders
+  const int32_t n = a.n;
+  int32_t* leaders = scratch + kFusedTokens;  // per warp
+  const int32_t mine = tid < n ? bucket_of(a.adapter_ids[tid], L) : -1;
+  scratch[tid] = mine;
+  __syncthreads();
+  int32_t rank = 0;
+  const int4* ids4 = reinterpret_cast<const int4*>(scratch);
+  for (int32_t i = 0; i < (tid & ~31); i += 4) {  // the warps before this one
+    const int4 v = ids4[i >> 2];
+    rank += (v.x == mine) + (v.y == mine) + (v.z == mine) + (v.w == mine);
+  }
+  rank += __popc(__match_any_sync(0xffffffffu, mine) & ((1u << lane) - 1u));
+  const bool leads = mine >= 0 && rank % MT == 0;
+  const uint32_t lead = __ballot_sync(0xffffffffu, leads);
+  if (lane == 0) leaders[warp] = __popc(lead);
+  __syncthreads();
+  int32_t at = __popc(lead & ((1u << lane) - 1u));
+  for (int w = 0; w < warp; ++w) at += leaders[w];
+  if (leads && at == tile) {
+    found[0] = mine;
+    found[1] = rank / MT;
+  }
+  __syncthreads();
+  t.adapter = found[0];
+  if (t.adapter < 0) return false;
+  const bool in = mine == t.adapter && rank / MT == found[1];
+  if (in) row[rank % MT] = tid;
+  t.count = __syncthreads_count(in);
+  return true;
+}
+
+// MW 16-token groups a warp, MSPLIT such warps side by side (the other warps
+// split in_features), NT groups of 8 ranks a pass of the first product.
+template <int MW, int MSPLIT, int NT>
+__global__ void __launch_bounds__(kLoraThreads, 2)
+    lora_kernel(const moe_lora_args a, const LoraPlan plan, int32_t fused, int32_t terms) {
+  constexpr int MT = 16 * MW * MSPLIT, KG = kLoraWarps / MSPLIT;
+  constexpr int RPASS = 8 * NT, RP = RPASS + 8;  // ranks of a pass; row pitch of the partial sums
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int32_t row[MT];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const uint32_t C = cluster_size(), cr = cluster_rank();
+  Tile t;
+  // [KG][MT][RP] partial sums; [MT][RP] the CTA's sum; then v, [terms][MT][VP] bf16
+  float* part = sm;
+  float* sum = sm + KG * MT * RP;
+  uint16_t* v = reinterpret_cast<uint16_t*>(sum + MT * RP);
+  if (!find_tile<MT>(a, plan, fused != 0, (int32_t)(blockIdx.x / C), row, reinterpret_cast<int32_t*>(sm), t)) return;
+  int32_t rank = 0;
+  float scale = 0.f;
+  if (t.adapter < a.n_adapters) {
+    rank = a.ranks ? min(max(a.ranks[t.adapter], 0), a.max_rank) : a.max_rank;
+    scale = a.scale ? a.scale[t.adapter] : 1.f;
+  }
+  const int32_t R32 = (rank + 31) & ~31;
+  const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;  // pitch of v: rows 64 bytes apart mod 128
+  const int mg = warp % MSPLIT, kg = warp / MSPLIT;
+
+  if (rank > 0) {
+    const uint16_t* A = a.a + (int64_t)t.adapter * a.max_rank * a.in_features;
+    const uint16_t* xr[MW][2];
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int32_t tok = row[(mg * MW + m) * 16 + h * 8 + g];
+        xr[m][h] = tok >= 0 ? row_ptr<const uint16_t>(a.x, tok, a.in_features) : nullptr;
+      }
+    for (int32_t r0 = 0; r0 < rank; r0 += RPASS) {
+      float acc[MW][NT][4] = {};
+      for (int32_t c = ((int32_t)(cr * KG) + kg) * 32 + 8 * q; c - 8 * q < a.in_features; c += (int32_t)C * KG * 32) {
+        const bool in = c < a.in_features;
+        uint4 xa[MW][2], av[NT];
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            xa[m][h] = make_uint4(0, 0, 0, 0);
+            if (in && xr[m][h]) xa[m][h] = *reinterpret_cast<const uint4*>(xr[m][h] + c);
+          }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          av[j] = make_uint4(0, 0, 0, 0);
+          const int32_t i = r0 + 8 * j + g;
+          if (in && i < rank) av[j] = __ldg(reinterpret_cast<const uint4*>(A + (int64_t)i * a.in_features + c));
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (r0 + 8 * j >= rank) break;
+#pragma unroll
+          for (int m = 0; m < MW; ++m) {
+            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, av[j].x, av[j].y);
+            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, av[j].z, av[j].w);
+          }
+        }
+      }
+      if (r0 > 0) __syncthreads();  // the last pass's sums have been read
+#pragma unroll
+      for (int m = 0; m < MW; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(part + (kg * MT + (mg * MW + m) * 16 + h * 8 + g) * RP + 8 * j + 2 * q) =
+                make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+      __syncthreads();
+      for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
+        const int m = i / RPASS, r = i % RPASS;
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) s += part[(k * MT + m) * RP + r];
+        sum[m * RP + r] = s;
+      }
+      if (C > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+      for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
+        const int m = i / RPASS, r = i % RPASS;
+        float s = 0.f;
+        if (C > 1) {
+          for (uint32_t k = 0; k < C; ++k) s += peer_float(sum + m * RP + r, k);
+        } else {
+          s = sum[m * RP + r];
+        }
+        s = r0 + r < rank ? s * scale : 0.f;
+        if (r0 + r < R32)
+          for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
+            const uint16_t b = f2bf_rn(s);
+            v[(k * MT + m) * VP + r0 + r] = b;
+            s -= bf16lo(b);
+          }
+      }
+      if (C > 1)
+        cluster_sync();  // the peers have read this CTA's sums
+      else
+        __syncthreads();
+    }
+    // what the last pass does not reach up to the next window of 32
+    const int32_t done = (rank + RPASS - 1) / RPASS * RPASS;
+    if (done < R32) {
+      for (int i = tid; i < terms * MT * (R32 - done); i += kLoraThreads)
+        v[i / (R32 - done) * VP + done + i % (R32 - done)] = 0;
+      __syncthreads();
+    }
+  }
+
+  // out = y + B v
+  const uint16_t* B = a.b + (rank > 0 ? (int64_t)t.adapter * a.out_features * a.max_rank : 0);
+  const int32_t blocks = (a.out_features + 31) / 32;
+  for (int32_t ob = (int32_t)cr * kLoraWarps + warp; ob < blocks; ob += (int32_t)C * kLoraWarps) {
+    const int32_t o0 = ob * 32;
+    const bool mine = o0 + 8 * q < a.out_features;  // the lane's 8 columns
+#pragma unroll
+    for (int mh = 0; mh < MSPLIT; ++mh) {
+      __syncwarp();
+      float acc[MW][4][4] = {};
+      for (int32_t k0 = 0; k0 < R32; k0 += 32) {
+        uint4 bv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int32_t o = o0 + 8 * (g >> 1) + 2 * j + (g & 1), i = k0 + 8 * q;
+          bv[j] = make_uint4(0, 0, 0, 0);
+          if (o < a.out_features && i < rank) {
+            bv[j] = __ldg(reinterpret_cast<const uint4*>(B + (int64_t)o * a.max_rank + i));
+            const int32_t left = rank - i;
+            if (left < 8) {  // what lies beyond the rank may hold anything
+              bv[j].x &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+              bv[j].y &= left >= 4 ? 0xffffffffu : left == 3 ? 0xffffu : 0u;
+              bv[j].z &= left >= 6 ? 0xffffffffu : left == 5 ? 0xffffu : 0u;
+              bv[j].w &= left == 7 ? 0xffffu : 0u;
+            }
+          }
+        }
+        for (int k = 0; k < terms; ++k)
+#pragma unroll
+          for (int m = 0; m < MW; ++m) {
+            const uint16_t* vr = v + (k * MT + (mh * MW + m) * 16 + g) * VP + k0 + 8 * q;
+            const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * VP);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, bv[j].x, bv[j].y);
+              mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, bv[j].z, bv[j].w);
+            }
+          }
+      }
+      if (!mine) continue;
+#pragma unroll
+      for (int m = 0; m < MW; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int32_t tok = row[(mh * MW + m) * 16 + h * 8 + g];
+          if (tok < 0) continue;
+          float r[8] = {};
+          if (a.y.data) {
+            if (a.y_dtype == MOE_DTYPE_BF16)
+              load8(row_ptr<const uint16_t>(a.y, tok, a.out_features) + o0 + 8 * q, r);
+            else
+              load8(row_ptr<const float>(a.y, tok, a.out_features) + o0 + 8 * q, r);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            r[2 * j] += acc[m][j][2 * h];
+            r[2 * j + 1] += acc[m][j][2 * h + 1];
+          }
+          if (a.out_dtype == MOE_DTYPE_BF16)
+            store8(row_ptr<uint16_t>(a.out, tok, a.out_features) + o0 + 8 * q, r);
+          else
+            store8(row_ptr<float>(a.out, tok, a.out_features) + o0 + 8 * q, r);
+        }
+    }
+  }
+}
+
+template <int MW, int MSPLIT, int NT>
+cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tiles, int32_t cluster,
+                        cudaStream_t s) {
+  constexpr int MT = 16 * MW * MSPLIT, KG = kLoraWarps / MSPLIT, RP = 8 * NT + 8;
+  const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
+  const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;
+  const size_t smem = std::max<size_t>((size_t)(KG + 1) * MT * RP * 4 + (size_t)terms * MT * VP * 2,
+                                       (kFusedTokens + kLoraWarps) * 4);
+  static std::atomic<bool> configured[kMaxDevices];
+  cudaError_t e = raise_smem_limit(lora_kernel<MW, MSPLIT, NT>, 200 * 1024, configured);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * cluster));
+  cfg.blockDim = dim3(kLoraThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = fused ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, lora_kernel<MW, MSPLIT, NT>, a, p, (int32_t)fused, terms);
+}
+
+template <int MW, int MSPLIT>
+cudaError_t lora_rank(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tiles, int32_t cluster,
+                      cudaStream_t s) {
+  if (a.max_rank <= 16) return lora_launch<MW, MSPLIT, 2>(a, p, fused, tiles, cluster, s);
+  if (a.max_rank <= 32) return lora_launch<MW, MSPLIT, 4>(a, p, fused, tiles, cluster, s);
+  return lora_launch<MW, MSPLIT, 8>(a, p, fused, tiles, cluster, s);
 }
 
 }  // namespace
 
 size_t lora_workspace(int32_t n, int32_t n_adapters) {
-  (void)n;
-  (void)n_adapters;
-  return 0;
+  const int64_t L = n_adapters;
+  if (n <= kFusedTokens) return 0;
+  const int64_t slices = plan_slices(n);
+  return (size_t)(up4(n) + 2 * up4(L + 2) + (slices > 1 ? slices * (L + 1) : 0)) * 4;
 }
 
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s) {
-  (void)workspace;
-  const bool yb = a.y_dtype == MOE_DTYPE_BF16, ob = a.out_dtype == MOE_DTYPE_BF16;
-  const unsigned n = (unsigned)a.n;
-  if (yb && ob)
-    lora_token_kernel<uint16_t, uint16_t><<<n, kLoraThreads, 0, s>>>(a);
-  else if (yb)
-    lora_token_kernel<uint16_t, float><<<n, kLoraThreads, 0, s>>>(a);
-  else if (ob)
-    lora_token_kernel<float, uint16_t><<<n, kLoraThreads, 0, s>>>(a);
-  else
-    lora_token_kernel<float, float><<<n, kLoraThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const int32_t n = a.n, L = a.n_adapters;
+  const bool fused = n <= kFusedTokens;
+  const int32_t mt = n <= 1024 ? 16 : n <= 8192 ? 32 : 64;
+  const LoraPlan p = fused ? LoraPlan{} : lora_plan(workspace, n, L);
+  if (!fused) {
+    const int32_t slices = plan_slices(n);
+    const size_t smem = (size_t)(L + 1) * 4;
+    if (slices > 1) {
+      lora_hist_kernel<<<slices, kPlanThreads, smem, s>>>(a.adapter_ids, n, L, p.hist);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    lora_plan_kernel<<<slices, kPlanThreads, smem, s>>>(a.adapter_ids, n, L, mt, p, slices > 1 ? p.hist : nullptr);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  // every group has at most one tile that is not full
+  const int32_t tiles = n / mt + std::min(n, L + 1);
+  int32_t cluster = 1;
+  while (cluster < 8 && tiles * cluster * 2 <= 608) cluster *= 2;
+  if (mt == 16) return lora_rank<1, 1>(a, p, fused, tiles, cluster, s);
+  if (mt == 32) return lora_rank<2, 1>(a, p, fused, tiles, cluster, s);
+  return lora_rank<2, 2>(a, p, fused, tiles, cluster, s);
 }
 
 }  // namespace moe
