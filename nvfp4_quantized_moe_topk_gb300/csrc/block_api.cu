@@ -16,10 +16,12 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 bool is_dtype(int32_t d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
 int64_t dtype_bytes(int32_t d) { return d == MOE_DTYPE_BF16 ? 2 : 4; }
 
-// A row array whose data may be NULL: aligned, rows that do not overlap.
+// A row array whose data may be NULL: aligned, rows that do not overlap (and
+// a stride below 2^31 vectors of 16 bytes, as the kernels address them).
 bool rows_ok(const moe_rows& r, int64_t cols, int32_t dtype) {
   if (!r.data) return true;
-  return aligned(r.data, 16) && (r.stride == 0 || (r.stride >= cols && r.stride * dtype_bytes(dtype) % 16 == 0));
+  return aligned(r.data, 16) && (r.stride == 0 || (r.stride >= cols && r.stride <= (int64_t(1) << 31) &&
+                                                   r.stride * dtype_bytes(dtype) % 16 == 0));
 }
 
 moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -76,7 +78,7 @@ moe_status moe_block_norm(const moe_block_norm_args* args, moe_stream_t stream) 
 
 size_t moe_block_norm_workspace_bytes(int32_t n, int32_t hidden) {
   if (n < 0 || hidden <= 0) return 0;
-  return (size_t)block_norm_backward_blocks(n) * 3 * (size_t)hidden * sizeof(float);
+  return (size_t)block_norm_backward_groups(n) * 2 * (size_t)hidden * sizeof(float);
 }
 
 moe_status moe_block_norm_backward(const moe_block_norm_args* args, const moe_block_norm_grads* grads, void* workspace,

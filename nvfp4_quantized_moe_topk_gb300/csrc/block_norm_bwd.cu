@@ -1,0 +1,297 @@
+// block_norm_bwd.cu -- backward pass of the norms around a block
+// (moe_block_norm_backward).
+//
+// With p = w dx and c = beta g w' (w, w' the two norms' weights, g the gate):
+//   q  = dr + ru p                       the gradient at u but for its mean term
+//   G  = q - m1 u                        m1 = ru^3 mean(p u)
+//   dy = rp (c G - m2 y)                 m2 = rp^2 mean(c y G)
+// G is linear in m1, so sum(c y G) = sum(c y q) - m1 sum(c y u), and one
+// reduction of three sums that do not wait for one another serves the row.
+// For a gate per token its factor stays out of c, and sum(c y G) rp is that
+// gate's gradient.  Of the sums over tokens two are kept, sum(dx u ru) and
+// S = sum(gt G y rp g) (without the channel's factors, which the join applies):
+//   d_pre_weight is the first, d_post_weight = beta g S, d_gate = beta w' S.
+//
+// Memory bounds it: two gradients, u and y in, two gradients out.  Persistent
+// groups of threads and rings in shared memory as in the forward pass.  A
+// row's vectors are read twice from the ring, before and after the reduction,
+// which is cheaper than holding them in registers beside the channels' sums.
+// Each group writes its sums, and column_sum_kernel joins them in a fixed order.
+#include "block_norm.cuh"
+
+namespace moe {
+
+namespace {
+
+struct NormGrads {
+  NormRows dr, dx, d_residual, d_branch, d_gate;
+  float *d_post, *d_pre;
+};
+
+template <typename RT, typename YT, int ITERS, int MAXT, int MODE>
+__global__ void __launch_bounds__(MAXT, 768 / MAXT)
+    block_norm_backward_kernel(const NormParams a, const NormGrads d, float* __restrict__ part, int32_t stages,
+                               int32_t stage_vecs) {
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float red[kNormMaxGroups][2][3 * (kNormMaxThreads / 32)];
+  const bool branch = MODE != kNormAny || a.branch.p != nullptr;
+  const bool post = MODE != kNormAny || a.post != nullptr, pre = MODE != kNormAny || (a.pre && d.dx.p);
+  const bool full = MODE == kNormAny ? a.gate_kind == MOE_GATE_FULL : MODE == kNormFull;
+  const bool channel = MODE == kNormAny ? a.gate_kind == MOE_GATE_CHANNEL : MODE == kNormChannel;
+  const bool token = (MODE == kNormAny || MODE == kNormScalar) && a.gate_kind == MOE_GATE_TOKEN;
+  const uint32_t pitch = blockDim.x * blockDim.y * 16;
+  const uint32_t mine = smem_u32(ring) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+  const uint32_t iter_bytes = stage_vecs / ITERS * pitch, stage_bytes = stage_vecs * pitch;
+  const int32_t step = gridDim.x * blockDim.y, t0 = blockIdx.x * blockDim.y + threadIdx.y;
+  float acc_pre[ITERS][8] = {}, acc_post[ITERS][8] = {};
+  float wx[ITERS][8], c[ITERS][8];  // o + w_pre; beta g (o + w_post), without a full gate
+  int32_t vec[ITERS];
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    vec[i] = threadIdx.x + i * blockDim.x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      wx[i][j] = 0.f;
+      c[i][j] = a.beta;
+    }
+    if (vec[i] * 8 >= a.H) continue;
+    float w[8];
+    if (pre) {
+      load8_param(a.pre, a.param_dtype, vec[i] * 8, wx[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wx[i][j] += a.offset;
+    }
+    if (post) {
+      load8_param(a.post, a.param_dtype, vec[i] * 8, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[i][j] *= a.offset + w[j];
+    }
+    if (channel) {
+      load8_param(a.gate.p, a.param_dtype, vec[i] * 8, w);
+      if (a.gate_sigmoid) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = sigmoid(w[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[i][j] *= w[j];
+    }
+  }
+  // ring order: d_residual_out, residual_out, d_x, branch, full gate
+  constexpr int kR = Vec8<RT>::kVecs, kY = Vec8<YT>::kVecs;
+  constexpr uint32_t kU = kR, kDx = 2 * kR, kB = kDx + 1, kG = kB + kY;
+  auto fetch = [&](int64_t t64, int stage) {
+    if (t64 < a.n) {
+      const int32_t t = (int32_t)t64;
+#pragma unroll
+      for (int i = 0; i < ITERS; ++i) {
+        if (vec[i] * 8 >= a.H) continue;
+        const uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
+        if (d.dr.p) ring_copy<RT>(at, pitch, d.dr.at(t, vec[i] * kR));
+        if (pre) {
+          ring_copy<RT>(at + kU * pitch, pitch, a.residual_out.at(t, vec[i] * kR));
+          ring_copy<uint16_t>(at + kDx * pitch, pitch, d.dx.at(t, vec[i]));
+        }
+        if (branch) ring_copy<YT>(at + kB * pitch, pitch, a.branch.at(t, vec[i] * kY));
+        if (full) ring_copy<YT>(at + kG * pitch, pitch, a.gate.at(t, vec[i] * kY));
+      }
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s + 1 < stages; ++s) fetch((int64_t)t0 + (int64_t)s * step, s);
+  int stage = 0, buf = 0;
+  for (int64_t t64 = t0; t64 < a.n; t64 += step, stage = stage + 1 == stages ? 0 : stage + 1, buf ^= 1) {
+    const int32_t t = (int32_t)t64;
+    fetch(t64 + (int64_t)(stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    const float ru = pre ? a.rstd_pre[t] : 0.f;
+    const float rp = post ? a.rstd_post[t] : 1.f;
+    float gt = 1.f;
+    if (token) {
+      gt = reinterpret_cast<const float*>(a.gate.p)[t];
+      if (a.gate_sigmoid) gt = sigmoid(gt);
+    }
+    cp_async_wait(stages - 1);
+    const uint32_t at = mine + stage * stage_bytes;
+    float q[8], u[8], dx[8], y[8], g[8];
+    auto read = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        q[j] = u[j] = dx[j] = y[j] = 0.f;
+        g[j] = 1.f;
+      }
+      const uint32_t v = at + i * iter_bytes;
+      if (d.dr.p) ring_read<RT>(v, pitch, q);
+      if (pre) {
+        ring_read<RT>(v + kU * pitch, pitch, u);
+        ring_read<uint16_t>(v + kDx * pitch, pitch, dx);
+      }
+      if (branch) ring_read<YT>(v + kB * pitch, pitch, y);
+      if (full) {
+        ring_read<YT>(v + kG * pitch, pitch, g);
+        if (a.gate_sigmoid) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = sigmoid(g[j]);
+        }
+      }
+    };
+    float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      if (vec[i] * 8 >= a.H) continue;
+      read(i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = dx[j] * wx[i][j];
+        const float e = full ? c[i][j] * g[j] * y[j] : c[i][j] * y[j];
+        s[0] = fmaf(p, u[j], s[0]);
+        s[1] = fmaf(e, fmaf(ru, p, q[j]), s[1]);
+        s[2] = fmaf(e, u[j], s[2]);
+      }
+    }
+    group_sums<3>(s, red[threadIdx.y][buf]);
+    const float m1 = ru * ru * ru * (s[0] * a.inv_h);
+    const float T = rp * (s[1] - s[2] * m1);  // sum(c y rp G)
+    if (token && d.d_gate.p && threadIdx.x == 0)
+      reinterpret_cast<float*>(d.d_gate.p)[t] = a.gate_sigmoid ? T * gt * (1.f - gt) : T;
+    const float kc = rp * gt, ky = post ? rp * rp * gt * T * a.inv_h : 0.f;
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      if (vec[i] * 8 >= a.H) continue;
+      read(i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        q[j] = fmaf(-m1, u[j], fmaf(ru, dx[j] * wx[i][j], q[j]));  // G
+        acc_pre[i][j] = fmaf(ru * dx[j], u[j], acc_pre[i][j]);
+        dx[j] = a.alpha * q[j];
+      }
+      if (d.d_residual.p) store8(reinterpret_cast<RT*>(d.d_residual.at(t, vec[i] * kR)), dx);
+      if (!branch) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float yG = kc * y[j] * q[j];
+        acc_post[i][j] = full ? fmaf(g[j], yG, acc_post[i][j]) : acc_post[i][j] + yG;
+        u[j] = c[i][j] * yG;  // d_gate of this element (full)
+        q[j] *= kc * c[i][j];
+        if (full) q[j] *= g[j];
+        q[j] = fmaf(-ky, y[j], q[j]);
+        if (full && a.gate_sigmoid) u[j] *= g[j] * (1.f - g[j]);
+      }
+      if (d.d_branch.p) store8(reinterpret_cast<YT*>(d.d_branch.at(t, vec[i] * kY)), q);
+      if (full && d.d_gate.p) store8(reinterpret_cast<YT*>(d.d_gate.at(t, vec[i] * kY)), u);
+    }
+  }
+  // part[group][0..1][H]
+  float* own = part + (size_t)t0 * 2 * a.H;
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    if (vec[i] * 8 >= a.H) continue;
+    if (d.d_pre) store8(own + vec[i] * 8, acc_pre[i]);
+    if (d.d_post || channel) store8(own + a.H + vec[i] * 8, acc_post[i]);
+  }
+}
+
+// Joins the groups' sums: warp w of a 32-column CTA adds groups w, w + warps,
+// ... and warp 0 the warps in order.
+constexpr int kColWarps = 16;
+__global__ void __launch_bounds__(32 * kColWarps)
+    column_sum_kernel(const NormParams a, const NormGrads d, const float* __restrict__ part, int32_t groups) {
+  __shared__ float sum[kColWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, H = a.H;
+  const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
+  float* d_gate = channel ? reinterpret_cast<float*>(d.d_gate.p) : nullptr;
+  if (which == 0 ? !d.d_pre : !d.d_post && !d_gate) return;
+  const int32_t c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < H)
+    for (int32_t b = warp; b < groups; b += kColWarps) v += part[((size_t)b * 2 + which) * H + c];
+  sum[warp][lane] = v;
+  __syncthreads();
+  if (warp || c >= H) return;
+  v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kColWarps; ++i) v += sum[i][lane];
+  if (which == 0) {
+    d.d_pre[c] = v;
+    return;
+  }
+  auto param = [&](const void* p) {
+    return a.param_dtype == MOE_DTYPE_BF16 ? bf16lo(static_cast<const uint16_t*>(p)[c])
+                                           : static_cast<const float*>(p)[c];
+  };
+  v *= a.beta;
+  float g = 1.f;
+  if (channel) {
+    g = param(a.gate.p);
+    if (a.gate_sigmoid) g = sigmoid(g);
+  }
+  if (d_gate) {
+    float o = a.post ? v * (a.offset + param(a.post)) : v;
+    if (a.gate_sigmoid) o *= g * (1.f - g);
+    d_gate[c] = o;
+  }
+  if (d.d_post) d.d_post[c] = v * g;
+}
+
+template <typename RT, typename YT, int ITERS, int MAXT, int MODE>
+cudaError_t norm_backward_m(const NormParams& a, const NormGrads& d, float* part, int* groups, cudaStream_t s) {
+  const int vecs = ITERS * (2 * Vec8<RT>::kVecs + 1 + Vec8<YT>::kVecs * (a.gate_kind == MOE_GATE_FULL ? 2 : 1));
+  NormPlan p = norm_plan(a.n, a.H, vecs, 768);
+  const int slots = block_norm_backward_groups(a.n);  // of the workspace
+  if ((int)p.block.y > slots) p.block.y = slots;
+  p.ctas = std::min(p.ctas, slots / (int)p.block.y);
+  *groups = p.ctas * (int)p.block.y;
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = raise_smem_limit(block_norm_backward_kernel<RT, YT, ITERS, MAXT, MODE>, kNormSmem, configured);
+  if (e != cudaSuccess) return e;
+  block_norm_backward_kernel<RT, YT, ITERS, MAXT, MODE><<<p.ctas, p.block, p.smem, s>>>(a, d, part, p.stages, vecs);
+  return cudaGetLastError();
+}
+
+template <typename RT, typename YT, int ITERS, int MAXT>
+cudaError_t norm_backward_i(const NormParams& a, const NormGrads& d, float* part, int* groups, cudaStream_t s) {
+  if (!a.branch.p || !a.post || !a.pre || !d.dx.p)
+    return norm_backward_m<RT, YT, ITERS, MAXT, kNormAny>(a, d, part, groups, s);
+  if (a.gate_kind == MOE_GATE_CHANNEL) return norm_backward_m<RT, YT, ITERS, MAXT, kNormChannel>(a, d, part, groups, s);
+  if (a.gate_kind == MOE_GATE_FULL) return norm_backward_m<RT, YT, ITERS, MAXT, kNormFull>(a, d, part, groups, s);
+  return norm_backward_m<RT, YT, ITERS, MAXT, kNormScalar>(a, d, part, groups, s);
+}
+
+template <typename RT, typename YT>
+cudaError_t norm_backward_t(const NormParams& a, const NormGrads& d, float* part, int* groups, cudaStream_t s) {
+  if (norm_iters(a.H) == 2) return norm_backward_i<RT, YT, 2, 512>(a, d, part, groups, s);
+  if (norm_threads(a.H) <= 384) return norm_backward_i<RT, YT, 1, 384>(a, d, part, groups, s);
+  return norm_backward_i<RT, YT, 1, 512>(a, d, part, groups, s);
+}
+
+}  // namespace
+
+int block_norm_backward_groups(int32_t n) { return std::max(1, std::min<int32_t>(n, kNormBackwardGroups)); }
+
+cudaError_t launch_block_norm_backward(const moe_block_norm_args& args, const moe_block_norm_grads& grads, float* part,
+                                       cudaStream_t s) {
+  const NormParams a = norm_params(args);
+  const bool rb = args.residual_dtype == MOE_DTYPE_BF16, yb = args.branch_dtype == MOE_DTYPE_BF16;
+  NormGrads d;
+  d.dr = norm_rows(grads.d_residual_out, a.H, rb ? 2 : 4);
+  d.dx = norm_rows(grads.d_x, a.H, 2);
+  d.d_residual = norm_rows(grads.d_residual, a.H, rb ? 2 : 4);
+  d.d_branch = norm_rows(grads.d_branch, a.H, yb ? 2 : 4);
+  d.d_gate = norm_rows(grads.d_gate, a.H, yb ? 2 : 4);
+  d.d_post = grads.d_post_weight;
+  d.d_pre = grads.d_pre_weight;
+  int groups = 0;
+  if (a.n > 0) {
+    cudaError_t e;
+    if (rb)
+      e = yb ? norm_backward_t<uint16_t, uint16_t>(a, d, part, &groups, s)
+             : norm_backward_t<uint16_t, float>(a, d, part, &groups, s);
+    else
+      e = yb ? norm_backward_t<float, uint16_t>(a, d, part, &groups, s)
+             : norm_backward_t<float, float>(a, d, part, &groups, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (!d.d_pre && !d.d_post && !(a.gate_kind == MOE_GATE_CHANNEL && d.d_gate.p)) return cudaSuccess;
+  column_sum_kernel<<<dim3((a.H + 31) / 32, 2), 32 * kColWarps, 0, s>>>(a, d, part, groups);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -90,7 +90,7 @@ def test_norm_null_and_empty(lib):
     assert lib.moe_block_norm(None, None) == 1
     assert lib.moe_block_norm(norm(n=0, residual=0, branch=0, out=0, x=0), None) == 0
     assert lib.moe_block_norm_workspace_bytes(-1, 64) == 0
-    assert lib.moe_block_norm_workspace_bytes(10 ** 6, 4096) >= 3 * 4096 * 4
+    assert lib.moe_block_norm_workspace_bytes(10 ** 6, 4096) >= 2 * 4096 * 4
 
 
 @pytest.mark.parametrize("want,kw,gk", [
