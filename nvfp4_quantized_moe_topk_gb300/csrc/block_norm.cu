@@ -22,63 +22,75 @@ namespace moe {
 namespace {
 
 // The channels' factors: cz = beta g (o + w_post) without the row's factors, wx = o + w_pre.
-template <int MODE>
-__device__ __forceinline__ void channel_factors(const NormParams& a, int32_t c, float (&cz)[8], float (&wx)[8]) {
+template <int MODE, bool QUADS>
+__device__ __forceinline__ void channel_factors(const NormParams& a, const Lane<QUADS>& l, F2 (&cz)[4], F2 (&wx)[4]) {
   const bool channel = MODE == kNormAny ? a.gate_kind == MOE_GATE_CHANNEL : MODE == kNormChannel;
-  float w[8];
+  F2 w[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    cz[j] = a.beta;
-    wx[j] = 0.f;
+  for (int j = 0; j < 4; ++j) {
+    cz[j] = f2(a.beta);
+    wx[j] = f2(0.f);
   }
   if (MODE != kNormAny || a.post) {
-    load8_param(a.post, a.param_dtype, c, w);
+    load_param(a.post, a.param_dtype, l, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cz[j] *= a.offset + w[j];
+    for (int j = 0; j < 4; ++j) cz[j] = mul2(cz[j], add2(f2(a.offset), w[j]));
   }
   if (channel) {
-    load8_param(a.gate.p, a.param_dtype, c, w);
-    if (a.gate_sigmoid) {
+    load_param(a.gate.p, a.param_dtype, l, w);
+    if (a.gate_sigmoid) sigmoid2(w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = sigmoid(w[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cz[j] *= w[j];
+    for (int j = 0; j < 4; ++j) cz[j] = mul2(cz[j], w[j]);
   }
   if (MODE != kNormAny || a.pre) {
-    load8_param(a.pre, a.param_dtype, c, wx);
+    load_param(a.pre, a.param_dtype, l, wx);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) wx[j] += a.offset;
+    for (int j = 0; j < 4; ++j) wx[j] = add2(wx[j], f2(a.offset));
   }
+}
+
+// A lane's values of a row from global memory, 0 where it has no channel.
+template <typename T, bool QUADS>
+__device__ __forceinline__ void row_load(const NormRows& r, int32_t t, const Lane<QUADS>& l, F2 (&v)[4]) {
+  load_param(r.at(t, 0), Vec8<T>::kVecs == 1 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, l, v);
+}
+
+// z <- gate * z
+__device__ __forceinline__ void apply_gate(const NormParams& a, F2 (&z)[4], F2 (&g)[4]) {
+  if (a.gate_sigmoid) sigmoid2(g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) z[j] = mul2(z[j], g[j]);
+}
+
+__device__ __forceinline__ float squares(const F2 (&v)[4]) {
+  F2 s = mul2(v[0], v[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) s = fma2(v[j], v[j], s);
+  return s.x + s.y;
 }
 
 // One row per CTA: batches too small for the persistent groups.
 template <typename RT, typename YT, int ITERS>
 __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormParams a) {
   __shared__ float red[2][kNormMaxThreads / 32];
+  constexpr bool Q = Vec8<RT>::kVecs + Vec8<YT>::kVecs > 2;
   const int32_t t = blockIdx.x;
   const bool branch = a.branch.p != nullptr;
-  constexpr int kR = Vec8<RT>::kVecs, kY = Vec8<YT>::kVecs;
-  float u[ITERS][8], z[ITERS][8], cz[ITERS][8], wx[ITERS][8];
-  int32_t vec[ITERS];  // index of the thread's group of 8 channels
+  F2 u[ITERS][4], z[ITERS][4], cz[ITERS][4], wx[ITERS][4];
   float ss[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    vec[i] = threadIdx.x + i * blockDim.x;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[i][j] = z[i][j] = 0.f;
-    if (vec[i] * 8 >= a.H) continue;
-    load8(reinterpret_cast<const RT*>(a.residual.at(t, vec[i] * kR)), u[i]);
-    if (branch) load8(reinterpret_cast<const YT*>(a.branch.at(t, vec[i] * kY)), z[i]);
-    channel_factors<kNormAny>(a, vec[i] * 8, cz[i], wx[i]);
+    const Lane<Q> l(i, a.H);
+    if (!l.ok0) continue;
+    row_load<RT>(a.residual, t, l, u[i]);
+    if (branch) row_load<YT>(a.branch, t, l, z[i]);
+    channel_factors<kNormAny>(a, l, cz[i], wx[i]);
+    if (a.post) ss[0] += squares(z[i]);
     if (a.gate_kind == MOE_GATE_FULL) {
-      float g[8];
-      load8(reinterpret_cast<const YT*>(a.gate.at(t, vec[i] * kY)), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) cz[i][j] *= a.gate_sigmoid ? sigmoid(g[j]) : g[j];
+      F2 g[4];
+      row_load<YT>(a.gate, t, l, g);
+      apply_gate(a, z[i], g);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss[0] = fmaf(z[i][j], z[i][j], ss[0]);
   }
   float f = 1.f;
   if (a.gate_kind == MOE_GATE_TOKEN) {
@@ -94,14 +106,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
   ss[0] = 0.f;
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    if (vec[i] * 8 >= a.H) continue;
+    const Lane<Q> l(i, a.H);
+    if (!l.ok0) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      u[i][j] *= a.alpha;
-      if (branch) u[i][j] = fmaf(cz[i][j], f * z[i][j], u[i][j]);
-      ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+    for (int j = 0; j < 4; ++j) {
+      u[i][j] = mul2(u[i][j], f2(a.alpha));
+      if (branch) u[i][j] = fma2(cz[i][j], mul2(f2(f), z[i][j]), u[i][j]);
     }
-    if (a.residual_out.p) store8(reinterpret_cast<RT*>(a.residual_out.at(t, vec[i] * kR)), u[i]);
+    ss[0] += squares(u[i]);
+    if (a.residual_out.p) row_store<RT>(a.residual_out, t, l, u[i]);
   }
   if (!a.pre) return;
   group_sums<1>(ss, red[1]);
@@ -109,10 +122,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
   if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = ru;
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    if (vec[i] * 8 >= a.H) continue;
+    const Lane<Q> l(i, a.H);
+    if (!l.ok0) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[i][j] *= ru * wx[i][j];
-    store8(reinterpret_cast<uint16_t*>(a.x_out.at(t, vec[i])), u[i]);
+    for (int j = 0; j < 4; ++j) u[i][j] = mul2(u[i][j], mul2(f2(ru), wx[i][j]));
+    row_store<uint16_t>(a.x_out, t, l, u[i]);
   }
 }
 
@@ -124,6 +138,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
   extern __shared__ __align__(16) char ring[];
   __shared__ float red[kNormMaxGroups][4][kNormMaxThreads / 32];
   constexpr int kR = Vec8<RT>::kVecs, kY = Vec8<YT>::kVecs;
+  constexpr bool Q = kR + kY > 2;
   const bool branch = MODE != kNormAny || a.branch.p != nullptr;
   const bool post = MODE != kNormAny || a.post != nullptr, pre = MODE != kNormAny || a.pre != nullptr;
   const bool full = MODE == kNormAny ? a.gate_kind == MOE_GATE_FULL : MODE == kNormFull;
@@ -132,48 +147,52 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
   const uint32_t mine = smem_u32(ring) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
   const uint32_t iter_bytes = stage_vecs / ITERS * pitch, stage_bytes = stage_vecs * pitch;
   const int32_t step = gridDim.x * blockDim.y, t0 = blockIdx.x * blockDim.y + threadIdx.y;
-  int32_t vec[ITERS];
-  float cz[ITERS][8], wx[ITERS][8];
+  F2 cz[ITERS][4], wx[ITERS][4];
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    vec[i] = threadIdx.x + i * blockDim.x;
-    if (vec[i] * 8 < a.H) channel_factors<MODE>(a, vec[i] * 8, cz[i], wx[i]);
+    const Lane<Q> l(i, a.H);
+    if (l.ok0) channel_factors<MODE>(a, l, cz[i], wx[i]);
   }
-  auto fetch = [&](int64_t t, int stage) {
-    if (t < a.n) {
+  auto fetch = [&](int64_t t64, int stage) {
+    if (t64 < a.n) {
+      const int32_t t = (int32_t)t64;
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
-        if (vec[i] * 8 >= a.H) continue;
-        uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
-        ring_copy<RT>(at, pitch, a.residual.at((int32_t)t, vec[i] * kR));
-        if (branch) ring_copy<YT>(at + kR * pitch, pitch, a.branch.at((int32_t)t, vec[i] * kY));
-        if (full) ring_copy<YT>(at + (kR + kY) * pitch, pitch, a.gate.at((int32_t)t, vec[i] * kY));
+        const uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
+        ring_copy<RT, Q>(at, pitch, a.residual.at(t, 0), i, a.H);
+        if (branch) ring_copy<YT, Q>(at + kR * pitch, pitch, a.branch.at(t, 0), i, a.H);
+        if (full) ring_copy<YT, Q>(at + (kR + kY) * pitch, pitch, a.gate.at(t, 0), i, a.H);
       }
     }
     cp_async_commit();  // one group a row, empty past the end
   };
+  // a token's gate is loaded one row ahead
+  auto token_gate = [&](int64_t t64) {
+    return token && t64 < a.n ? reinterpret_cast<const float*>(a.gate.p)[t64] : 1.f;
+  };
   for (int s = 0; s + 1 < stages; ++s) fetch((int64_t)t0 + (int64_t)s * step, s);
+  float next_gate = token_gate(t0);
   int stage = 0, buf = 0;
   for (int64_t t64 = t0; t64 < a.n; t64 += step, stage = stage + 1 == stages ? 0 : stage + 1, buf ^= 2) {
     const int32_t t = (int32_t)t64;
+    __syncwarp();  // the warp has read the slot that is filled next
     fetch(t64 + (int64_t)(stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
-    float f = 1.f;
-    if (token) {
-      f = reinterpret_cast<const float*>(a.gate.p)[t];
-      if (a.gate_sigmoid) f = sigmoid(f);
-    }
+    float f = next_gate;
+    next_gate = token_gate(t64 + step);
+    if (token && a.gate_sigmoid) f = sigmoid(f);
     cp_async_wait(stages - 1);
+    __syncwarp();
     const uint32_t at = mine + stage * stage_bytes;
-    float u[ITERS][8], z[ITERS][8];
+    F2 u[ITERS][4], z[ITERS][4];
     float ss[1] = {0.f};
+    if (branch) {
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] = z[i][j] = 0.f;
-      if (!branch || vec[i] * 8 >= a.H) continue;
-      ring_read<YT>(at + i * iter_bytes + kR * pitch, pitch, z[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] = fmaf(z[i][j], z[i][j], ss[0]);
+      for (int i = 0; i < ITERS; ++i) {
+        const Lane<Q> l(i, a.H);
+        if (!l.ok0) continue;
+        ring_read<YT>(at + i * iter_bytes + kR * pitch, pitch, l, z[i]);
+        ss[0] += squares(z[i]);
+      }
     }
     if (post) {
       group_sums<1>(ss, red[threadIdx.y][buf]);
@@ -184,25 +203,21 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
     ss[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
-      if (vec[i] * 8 >= a.H) continue;
-      ring_read<RT>(at + i * iter_bytes, pitch, u[i]);
+      const Lane<Q> l(i, a.H);
+      if (!l.ok0) continue;
+      ring_read<RT>(at + i * iter_bytes, pitch, l, u[i]);
       if (full) {
-        float g[8];
-        ring_read<YT>(at + i * iter_bytes + (kR + kY) * pitch, pitch, g);
-        if (a.gate_sigmoid) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = sigmoid(g[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] *= g[j];
+        F2 g[4];
+        ring_read<YT>(at + i * iter_bytes + (kR + kY) * pitch, pitch, l, g);
+        apply_gate(a, z[i], g);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        u[i][j] *= a.alpha;
-        if (branch) u[i][j] = fmaf(cz[i][j], f * z[i][j], u[i][j]);
-        ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+      for (int j = 0; j < 4; ++j) {
+        u[i][j] = mul2(u[i][j], f2(a.alpha));
+        if (branch) u[i][j] = fma2(cz[i][j], mul2(f2(f), z[i][j]), u[i][j]);
       }
-      if (a.residual_out.p) store8(reinterpret_cast<RT*>(a.residual_out.at(t, vec[i] * kR)), u[i]);
+      ss[0] += squares(u[i]);
+      if (a.residual_out.p) row_store<RT>(a.residual_out, t, l, u[i]);
     }
     if (!pre) continue;
     group_sums<1>(ss, red[threadIdx.y][buf + 1]);
@@ -210,10 +225,11 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
     if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = ru;
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
-      if (vec[i] * 8 >= a.H) continue;
+      const Lane<Q> l(i, a.H);
+      if (!l.ok0) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] *= ru * wx[i][j];
-      store8(reinterpret_cast<uint16_t*>(a.x_out.at(t, vec[i])), u[i]);
+      for (int j = 0; j < 4; ++j) u[i][j] = mul2(u[i][j], mul2(f2(ru), wx[i][j]));
+      row_store<uint16_t>(a.x_out, t, l, u[i]);
     }
   }
 }

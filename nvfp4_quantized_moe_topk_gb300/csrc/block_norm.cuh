@@ -66,7 +66,7 @@ inline NormParams norm_params(const moe_block_norm_args& a) {
   return p;
 }
 
-// Threads of a row: every thread owns ITERS groups of 8 channels.
+// Threads of a row: every thread owns ITERS times 8 channels.
 inline int norm_iters(int32_t hidden) { return hidden / 8 > kNormMaxThreads ? 2 : 1; }
 inline int norm_threads(int32_t hidden) {
   const int it = norm_iters(hidden), vecs = hidden / 8;
@@ -95,32 +95,141 @@ __device__ __forceinline__ void cp_async_wait(int depth) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// A thread's 8 values of type T in its ring: vectors `pitch` bytes apart.
-template <typename T>
-__device__ __forceinline__ void ring_copy(uint32_t dst, uint32_t pitch, const char* src) {
-#pragma unroll
-  for (int i = 0; i < Vec8<T>::kVecs; ++i) cp_async16(dst + i * pitch, src + 16 * i);
+// Two fp32 values that one instruction works on.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 f2(float v) { return {v, v}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
-template <typename T>
-__device__ __forceinline__ void ring_read(uint32_t at, uint32_t pitch, float (&v)[8]) {
-  uint4 d[Vec8<T>::kVecs];
-#pragma unroll
-  for (int i = 0; i < Vec8<T>::kVecs; ++i)
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(d[i].x), "=r"(d[i].y), "=r"(d[i].z), "=r"(d[i].w)
-                 : "r"(at + i * pitch)
-                 : "memory");
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Which 8 channels of a warp's 256 a lane owns.  QUADS false (all matrices
+// bf16): 8 neighbouring ones, 16 bytes.  QUADS true (some matrix is fp32): 4
+// at 4 lane and 4 at 128 + 4 lane, so that an fp32 access of the warp is two
+// runs of 512 contiguous bytes (8 neighbouring fp32 channels a lane would
+// touch every memory sector twice) and a bf16 one two runs of 256.
+template <bool QUADS>
+struct Lane {
+  int32_t c0;  // first channel; the second four are at c0 + kNext
+  bool ok0, ok1;
+  static constexpr int32_t kNext = QUADS ? 128 : 4;
+  __device__ __forceinline__ Lane(int32_t i, int32_t hidden) {
+    const int32_t lane = threadIdx.x & 31;
+    c0 = (int32_t)(threadIdx.x - lane + i * blockDim.x) * 8 + lane * (QUADS ? 4 : 8);
+    ok0 = c0 < hidden;
+    ok1 = c0 + kNext < hidden;
+  }
+};
+
+// The ring: for every matrix of a row, each warp's 256 channels lie contiguous
+// in shared memory (fp32: in two parts, `pitch` apart); `at` is the lane's 16
+// bytes there.  A lane copies 16 contiguous bytes an instruction, in order; in
+// QUADS form it reads bytes that its warp copied (__syncwarp in between).
+template <typename T, bool QUADS>
+__device__ __forceinline__ void ring_copy(uint32_t at, uint32_t pitch, const char* row, int32_t i, int32_t hidden) {
+  const int32_t lane = threadIdx.x & 31, base = (int32_t)(threadIdx.x - lane + i * blockDim.x) * 8;
   if constexpr (Vec8<T>::kVecs == 1) {
-    unpack8(d[0], v);
+    const int32_t c = base + lane * 8;
+    if (c < hidden) cp_async16(at, row + (uint32_t)c * 2u);
+  } else {
+    static_assert(QUADS, "fp32 rows are dealt in quads");
+    const int32_t c = base + lane * 4;
+    if (c < hidden) cp_async16(at, row + (uint32_t)c * 4u);
+    if (c + 128 < hidden) cp_async16(at + pitch, row + (uint32_t)c * 4u + 512);
+  }
+}
+// 0 where the lane has no channel.
+template <typename T, bool QUADS>
+__device__ __forceinline__ void ring_read(uint32_t at, uint32_t pitch, const Lane<QUADS>& l, F2 (&v)[4]) {
+  const uint32_t lane = threadIdx.x & 31;
+  if constexpr (Vec8<T>::kVecs == 1 && !QUADS) {
+    uint4 d;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(d.x), "=r"(d.y), "=r"(d.z), "=r"(d.w) : "r"(at) : "memory");
+    v[0] = {bf16lo(d.x), bf16hi(d.x)};
+    v[1] = {bf16lo(d.y), bf16hi(d.y)};
+    v[2] = {bf16lo(d.z), bf16hi(d.z)};
+    v[3] = {bf16lo(d.w), bf16hi(d.w)};
+  } else if constexpr (Vec8<T>::kVecs == 1) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint2 d;
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(d.x), "=r"(d.y) : "r"(at - lane * 8 + h * 256) : "memory");
+      v[2 * h] = {bf16lo(d.x), bf16hi(d.x)};
+      v[2 * h + 1] = {bf16lo(d.y), bf16hi(d.y)};
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      v[4 * i] = __uint_as_float(d[i].x);
-      v[4 * i + 1] = __uint_as_float(d[i].y);
-      v[4 * i + 2] = __uint_as_float(d[i].z);
-      v[4 * i + 3] = __uint_as_float(d[i].w);
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(v[2 * h].x), "=f"(v[2 * h].y), "=f"(v[2 * h + 1].x), "=f"(v[2 * h + 1].y)
+                   : "r"(at + h * pitch)
+                   : "memory");
+  }
+  if (QUADS && !l.ok1) v[2] = v[3] = f2(0.f);
+}
+template <typename T, bool QUADS>
+__device__ __forceinline__ void row_store(const NormRows& r, int32_t t, const Lane<QUADS>& l, const F2 (&v)[4]) {
+  char* row = r.at(t, 0);
+  if constexpr (Vec8<T>::kVecs == 1 && !QUADS) {
+    *reinterpret_cast<uint4*>(row + (uint32_t)l.c0 * 2u) =
+        make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                   pack_bf16x2(v[3].x, v[3].y));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h && !l.ok1) break;
+      const uint32_t c = (uint32_t)(l.c0 + h * Lane<QUADS>::kNext);
+      if constexpr (Vec8<T>::kVecs == 1)
+        *reinterpret_cast<uint2*>(row + c * 2u) =
+            make_uint2(pack_bf16x2(v[2 * h].x, v[2 * h].y), pack_bf16x2(v[2 * h + 1].x, v[2 * h + 1].y));
+      else
+        *reinterpret_cast<float4*>(row + c * 4u) = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
     }
   }
+}
+template <bool QUADS>
+__device__ __forceinline__ void load_param(const void* p, int32_t dtype, const Lane<QUADS>& l, F2 (&v)[4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    v[2 * h] = v[2 * h + 1] = f2(0.f);
+    if (h && !l.ok1) continue;
+    const int32_t c = l.c0 + h * Lane<QUADS>::kNext;
+    if (dtype == MOE_DTYPE_BF16) {
+      const uint2 d = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c);
+      v[2 * h] = {bf16lo(d.x), bf16hi(d.x)};
+      v[2 * h + 1] = {bf16lo(d.y), bf16hi(d.y)};
+    } else {
+      const float4 d = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+      v[2 * h] = {d.x, d.y};
+      v[2 * h + 1] = {d.z, d.w};
+    }
+  }
+}
+__device__ __forceinline__ void sigmoid2(F2 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = {sigmoid(v[j].x), sigmoid(v[j].y)};
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -147,7 +256,11 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float* red) {
   else
     asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? red[i * warps + lane] : 0.f);
+  for (int i = 0; i < N; ++i) {  // at most 16 warps: four steps join them
+    v[i] = (lane & 15) < warps ? red[i * warps + (lane & 15)] : 0.f;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+  }
 }
 
 inline int norm_sms() {

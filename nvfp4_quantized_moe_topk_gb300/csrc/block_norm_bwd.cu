@@ -43,37 +43,34 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
   const uint32_t mine = smem_u32(ring) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
   const uint32_t iter_bytes = stage_vecs / ITERS * pitch, stage_bytes = stage_vecs * pitch;
   const int32_t step = gridDim.x * blockDim.y, t0 = blockIdx.x * blockDim.y + threadIdx.y;
-  float acc_pre[ITERS][8] = {}, acc_post[ITERS][8] = {};
-  float wx[ITERS][8], c[ITERS][8];  // o + w_pre; beta g (o + w_post), without a full gate
-  int32_t vec[ITERS];
+  constexpr bool Q = Vec8<RT>::kVecs + Vec8<YT>::kVecs > 2;
+  F2 acc_pre[ITERS][4] = {}, acc_post[ITERS][4] = {};
+  F2 wx[ITERS][4], c[ITERS][4];  // o + w_pre; beta g (o + w_post), without a full gate
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    vec[i] = threadIdx.x + i * blockDim.x;
+    const Lane<Q> l(i, a.H);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      wx[i][j] = 0.f;
-      c[i][j] = a.beta;
+    for (int j = 0; j < 4; ++j) {
+      wx[i][j] = f2(0.f);
+      c[i][j] = f2(a.beta);
     }
-    if (vec[i] * 8 >= a.H) continue;
-    float w[8];
+    if (!l.ok0) continue;
+    F2 w[4];
     if (pre) {
-      load8_param(a.pre, a.param_dtype, vec[i] * 8, wx[i]);
+      load_param(a.pre, a.param_dtype, l, wx[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wx[i][j] += a.offset;
+      for (int j = 0; j < 4; ++j) wx[i][j] = add2(wx[i][j], f2(a.offset));
     }
     if (post) {
-      load8_param(a.post, a.param_dtype, vec[i] * 8, w);
+      load_param(a.post, a.param_dtype, l, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c[i][j] *= a.offset + w[j];
+      for (int j = 0; j < 4; ++j) c[i][j] = mul2(c[i][j], add2(f2(a.offset), w[j]));
     }
     if (channel) {
-      load8_param(a.gate.p, a.param_dtype, vec[i] * 8, w);
-      if (a.gate_sigmoid) {
+      load_param(a.gate.p, a.param_dtype, l, w);
+      if (a.gate_sigmoid) sigmoid2(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = sigmoid(w[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[i][j] *= w[j];
+      for (int j = 0; j < 4; ++j) c[i][j] = mul2(c[i][j], w[j]);
     }
   }
   // ring order: d_residual_out, residual_out, d_x, branch, full gate
@@ -84,69 +81,81 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
       const int32_t t = (int32_t)t64;
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
-        if (vec[i] * 8 >= a.H) continue;
         const uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
-        if (d.dr.p) ring_copy<RT>(at, pitch, d.dr.at(t, vec[i] * kR));
+        if (d.dr.p) ring_copy<RT, Q>(at, pitch, d.dr.at(t, 0), i, a.H);
         if (pre) {
-          ring_copy<RT>(at + kU * pitch, pitch, a.residual_out.at(t, vec[i] * kR));
-          ring_copy<uint16_t>(at + kDx * pitch, pitch, d.dx.at(t, vec[i]));
+          ring_copy<RT, Q>(at + kU * pitch, pitch, a.residual_out.at(t, 0), i, a.H);
+          ring_copy<uint16_t, Q>(at + kDx * pitch, pitch, d.dx.at(t, 0), i, a.H);
         }
-        if (branch) ring_copy<YT>(at + kB * pitch, pitch, a.branch.at(t, vec[i] * kY));
-        if (full) ring_copy<YT>(at + kG * pitch, pitch, a.gate.at(t, vec[i] * kY));
+        if (branch) ring_copy<YT, Q>(at + kB * pitch, pitch, a.branch.at(t, 0), i, a.H);
+        if (full) ring_copy<YT, Q>(at + kG * pitch, pitch, a.gate.at(t, 0), i, a.H);
       }
     }
     cp_async_commit();
   };
+  // the row's scalars are loaded one row ahead
+  float next_ru = 0.f, next_rp = 1.f, next_gate = 1.f;
+  auto scalars = [&](int64_t t64) {
+    if (t64 >= a.n) return;
+    if (pre) next_ru = a.rstd_pre[t64];
+    if (post) next_rp = a.rstd_post[t64];
+    if (token) next_gate = reinterpret_cast<const float*>(a.gate.p)[t64];
+  };
   for (int s = 0; s + 1 < stages; ++s) fetch((int64_t)t0 + (int64_t)s * step, s);
+  scalars(t0);
   int stage = 0, buf = 0;
   for (int64_t t64 = t0; t64 < a.n; t64 += step, stage = stage + 1 == stages ? 0 : stage + 1, buf ^= 1) {
     const int32_t t = (int32_t)t64;
+    __syncwarp();  // the warp has read the slot that is filled next
     fetch(t64 + (int64_t)(stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
-    const float ru = pre ? a.rstd_pre[t] : 0.f;
-    const float rp = post ? a.rstd_post[t] : 1.f;
-    float gt = 1.f;
-    if (token) {
-      gt = reinterpret_cast<const float*>(a.gate.p)[t];
-      if (a.gate_sigmoid) gt = sigmoid(gt);
-    }
+    const float ru = next_ru, rp = next_rp;
+    const float gt = token && a.gate_sigmoid ? sigmoid(next_gate) : next_gate;
+    scalars(t64 + step);
     cp_async_wait(stages - 1);
+    __syncwarp();
     const uint32_t at = mine + stage * stage_bytes;
-    float q[8], u[8], dx[8], y[8], g[8];
-    auto read = [&](int i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        q[j] = u[j] = dx[j] = y[j] = 0.f;
-        g[j] = 1.f;
-      }
+    F2 q[4], u[4], dx[4], y[4], g[4];
+    auto read = [&](int i, const Lane<Q>& l) {
       const uint32_t v = at + i * iter_bytes;
-      if (d.dr.p) ring_read<RT>(v, pitch, q);
-      if (pre) {
-        ring_read<RT>(v + kU * pitch, pitch, u);
-        ring_read<uint16_t>(v + kDx * pitch, pitch, dx);
-      }
-      if (branch) ring_read<YT>(v + kB * pitch, pitch, y);
-      if (full) {
-        ring_read<YT>(v + kG * pitch, pitch, g);
-        if (a.gate_sigmoid) {
+      if (MODE == kNormAny || !full) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = sigmoid(g[j]);
+        for (int j = 0; j < 4; ++j) {
+          if (MODE == kNormAny) q[j] = u[j] = dx[j] = y[j] = f2(0.f);
+          g[j] = f2(1.f);
         }
       }
+      if (d.dr.p) {
+        ring_read<RT>(v, pitch, l, q);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = f2(0.f);
+      }
+      if (pre) {
+        ring_read<RT>(v + kU * pitch, pitch, l, u);
+        ring_read<uint16_t>(v + kDx * pitch, pitch, l, dx);
+      }
+      if (branch) ring_read<YT>(v + kB * pitch, pitch, l, y);
+      if (full) {
+        ring_read<YT>(v + kG * pitch, pitch, l, g);
+        if (a.gate_sigmoid) sigmoid2(g);
+      }
     };
-    float s[3] = {0.f, 0.f, 0.f};
+    F2 s2[3] = {};
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
-      if (vec[i] * 8 >= a.H) continue;
-      read(i);
+      const Lane<Q> l(i, a.H);
+      if (!l.ok0) continue;
+      read(i, l);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float p = dx[j] * wx[i][j];
-        const float e = full ? c[i][j] * g[j] * y[j] : c[i][j] * y[j];
-        s[0] = fmaf(p, u[j], s[0]);
-        s[1] = fmaf(e, fmaf(ru, p, q[j]), s[1]);
-        s[2] = fmaf(e, u[j], s[2]);
+      for (int j = 0; j < 4; ++j) {
+        const F2 p = mul2(dx[j], wx[i][j]);
+        const F2 e = mul2(full ? mul2(c[i][j], g[j]) : c[i][j], y[j]);
+        s2[0] = fma2(p, u[j], s2[0]);
+        s2[1] = fma2(e, fma2(f2(ru), p, q[j]), s2[1]);
+        s2[2] = fma2(e, u[j], s2[2]);
       }
     }
+    float s[3] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y};
     group_sums<3>(s, red[threadIdx.y][buf]);
     const float m1 = ru * ru * ru * (s[0] * a.inv_h);
     const float T = rp * (s[1] - s[2] * m1);  // sum(c y rp G)
@@ -155,37 +164,41 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
     const float kc = rp * gt, ky = post ? rp * rp * gt * T * a.inv_h : 0.f;
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
-      if (vec[i] * 8 >= a.H) continue;
-      read(i);
+      const Lane<Q> l(i, a.H);
+      if (!l.ok0) continue;
+      read(i, l);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        q[j] = fmaf(-m1, u[j], fmaf(ru, dx[j] * wx[i][j], q[j]));  // G
-        acc_pre[i][j] = fmaf(ru * dx[j], u[j], acc_pre[i][j]);
-        dx[j] = a.alpha * q[j];
+      for (int j = 0; j < 4; ++j) {
+        const F2 rdx = mul2(f2(ru), dx[j]);
+        q[j] = fma2(f2(-m1), u[j], fma2(rdx, wx[i][j], q[j]));  // G
+        acc_pre[i][j] = fma2(rdx, u[j], acc_pre[i][j]);
+        dx[j] = mul2(f2(a.alpha), q[j]);
       }
-      if (d.d_residual.p) store8(reinterpret_cast<RT*>(d.d_residual.at(t, vec[i] * kR)), dx);
+      if (d.d_residual.p) row_store<RT>(d.d_residual, t, l, dx);
       if (!branch) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float yG = kc * y[j] * q[j];
-        acc_post[i][j] = full ? fmaf(g[j], yG, acc_post[i][j]) : acc_post[i][j] + yG;
-        u[j] = c[i][j] * yG;  // d_gate of this element (full)
-        q[j] *= kc * c[i][j];
-        if (full) q[j] *= g[j];
-        q[j] = fmaf(-ky, y[j], q[j]);
-        if (full && a.gate_sigmoid) u[j] *= g[j] * (1.f - g[j]);
+      for (int j = 0; j < 4; ++j) {
+        const F2 kq = mul2(f2(kc), q[j]);
+        const F2 yG = mul2(y[j], kq);
+        acc_post[i][j] = full ? fma2(g[j], yG, acc_post[i][j]) : add2(acc_post[i][j], yG);
+        if (full) {
+          u[j] = mul2(c[i][j], yG);  // d_gate of this element
+          if (a.gate_sigmoid) u[j] = mul2(u[j], fma2(mul2(f2(-1.f), g[j]), g[j], g[j]));
+        }
+        q[j] = fma2(f2(-ky), y[j], mul2(full ? mul2(c[i][j], g[j]) : c[i][j], kq));
       }
-      if (d.d_branch.p) store8(reinterpret_cast<YT*>(d.d_branch.at(t, vec[i] * kY)), q);
-      if (full && d.d_gate.p) store8(reinterpret_cast<YT*>(d.d_gate.at(t, vec[i] * kY)), u);
+      if (d.d_branch.p) row_store<YT>(d.d_branch, t, l, q);
+      if (full && d.d_gate.p) row_store<YT>(d.d_gate, t, l, u);
     }
   }
   // part[group][0..1][H]
-  float* own = part + (size_t)t0 * 2 * a.H;
+  const NormRows own = {reinterpret_cast<char*>(part), a.H / 4};
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    if (vec[i] * 8 >= a.H) continue;
-    if (d.d_pre) store8(own + vec[i] * 8, acc_pre[i]);
-    if (d.d_post || channel) store8(own + a.H + vec[i] * 8, acc_post[i]);
+    const Lane<Q> l(i, a.H);
+    if (!l.ok0) continue;
+    if (d.d_pre) row_store<float>(own, 2 * t0, l, acc_pre[i]);
+    if (d.d_post || channel) row_store<float>(own, 2 * t0 + 1, l, acc_post[i]);
   }
 }
 
