@@ -3,24 +3,27 @@
 //
 //   v = A[l] x (over the adapter's rank),  out = y + B[l] (scale[l] v)
 //
-// Tokens are grouped by adapter into tiles of 16, 32 or 64, and one CTA (or a
+// Tokens are grouped by adapter into tiles of 16 or 32, and one CTA (or a
 // cluster of CTAs, where there are few tiles) takes a tile through both
 // products: v never leaves the SM.  Both are bf16 warp matrix instructions
 // with tokens as rows.  At ranks up to 128 they are far below the tensor
-// cores' rate; what bounds the call is moving x, y and out, so the operands go
-// straight from global memory to registers: a lane's 16 bytes of a row are
-// the k elements of two matrix instructions (the order of k inside a window
-// of 32 is free as long as both operands use it), every byte of x is loaded
-// by one warp, and no shared-memory stage or barrier stands in the loops.
+// cores' rate; what bounds the call is moving x, y and out, so every thread
+// copies the 16-byte pieces of the operands that its own fragments are made of
+// into its own slots of a shared-memory ring, some steps ahead, by
+// asynchronous copies, and reads back only those: no barrier stands in the
+// loops.  A lane's 16 bytes of a row are the k elements of two matrix
+// instructions (the order of k inside a window of 32 is free as long as both
+// operands use it).
 //
 //   first product:  the warps (and the cluster's CTAs) split in_features in
 //     windows of 32; their partial sums meet in shared memory (and in the
 //     cluster's shared memories), added in a fixed order.
 //   second product: the warps split out_features in blocks of 32 columns.  The
 //     columns of a block are dealt to the four 8-column instructions so that
-//     a lane ends up with 8 neighbouring columns of a token: y comes in and
-//     out goes out as 16-byte vectors.  v enters as the sum of two bf16 terms
-//     (16 bits of mantissa), three for an fp32 out (24 bits).
+//     a lane ends up with 8 neighbouring columns of a token (two runs of 4
+//     where y or out is fp32): y comes in and out goes out in whole memory
+//     sectors.  v enters as the sum of two bf16 terms (16 bits of mantissa),
+//     three for an fp32 out (24 bits).
 //
 // Grouping: up to kFusedTokens tokens every CTA ranks the ids itself; beyond,
 // a one-CTA kernel (two kernels past kPlanSlice tokens) sorts the tokens by
@@ -278,23 +281,48 @@ __device__ __forceinline__ bool find_tile(const moe_lora_args& a, const LoraPlan
   return true;
 }
 
-// MW 16-token groups a warp, MSPLIT such warps side by side (the other warps
-// split in_features), NT groups of 8 ranks a pass of the first product.
-template <int MW, int MSPLIT, int NT>
+// 16 (or 8) bytes into a ring slot, zeros where `ok` is false (src is then not read).
+__device__ __forceinline__ void ring16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ring8(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 slot16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `ahead` (0..3) of the thread's newest groups are unfinished.
+__device__ __forceinline__ void ring_wait(int ahead) {
+  switch (ahead) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory");
+  }
+}
+
+constexpr uint32_t kSlotVec = kLoraThreads * 16;  // one 16-byte vector of every thread
+
+// MW 16-token groups a tile, NT groups of 8 ranks a pass of the first product.
+template <int MW, int NT>
 __global__ void __launch_bounds__(kLoraThreads, 2)
-    lora_kernel(const moe_lora_args a, const LoraPlan plan, int32_t fused, int32_t terms) {
-  constexpr int MT = 16 * MW * MSPLIT, KG = kLoraWarps / MSPLIT;
+    lora_kernel(const moe_lora_args a, const LoraPlan plan, int32_t fused, int32_t terms, uint32_t ring_bytes) {
+  constexpr int MT = 16 * MW, KG = kLoraWarps;
   constexpr int RPASS = 8 * NT, RP = RPASS + 8;  // ranks of a pass; row pitch of the partial sums
-  extern __shared__ __align__(16) float sm[];
+  extern __shared__ __align__(16) char sm[];
   __shared__ int32_t row[MT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const uint32_t C = cluster_size(), cr = cluster_rank();
   Tile t;
-  // [KG][MT][RP] partial sums; [MT][RP] the CTA's sum; then v, [terms][MT][VP] bf16
-  float* part = sm;
-  float* sum = sm + KG * MT * RP;
-  uint16_t* v = reinterpret_cast<uint16_t*>(sum + MT * RP);
+  // the ring, between the loops [KG][MT][RP] partial sums; in a cluster [MT][RP] the CTA's sum; v, [terms][MT][VP] bf16
+  float* part = reinterpret_cast<float*>(sm);
+  float* sum = reinterpret_cast<float*>(sm + ring_bytes);
+  uint16_t* v = reinterpret_cast<uint16_t*>(sum + (C > 1 ? MT * RP : 0));
   if (!find_tile<MT>(a, plan, fused != 0, (int32_t)(blockIdx.x / C), row, reinterpret_cast<int32_t*>(sm), t)) return;
+  const uint32_t slot = smem_u32(sm) + tid * 16;
   int32_t rank = 0;
   float scale = 0.f;
   if (t.adapter < a.n_adapters) {
@@ -303,74 +331,97 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   }
   const int32_t R32 = (rank + 31) & ~31;
   const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;  // pitch of v: rows 64 bytes apart mod 128
-  const int mg = warp % MSPLIT, kg = warp / MSPLIT;
+  __syncthreads();  // the tile's scratch, in the ring, has been read
 
   if (rank > 0) {
     const uint16_t* A = a.a + (int64_t)t.adapter * a.max_rank * a.in_features;
     const uint16_t* xr[MW][2];
+    bool live[MW][2];
 #pragma unroll
     for (int m = 0; m < MW; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int32_t tok = row[(mg * MW + m) * 16 + h * 8 + g];
-        xr[m][h] = tok >= 0 ? row_ptr<const uint16_t>(a.x, tok, a.in_features) : nullptr;
+        const int32_t tok = row[m * 16 + h * 8 + g];
+        live[m][h] = tok >= 0;
+        xr[m][h] = row_ptr<const uint16_t>(a.x, max(tok, 0), a.in_features);
       }
+    const int32_t w0 = (int32_t)cr * KG + warp, wstep = (int32_t)C * KG, wins = (a.in_features + 31) / 32;
     for (int32_t r0 = 0; r0 < rank; r0 += RPASS) {
+      const int32_t nt = min(NT, (rank - r0 + 7) / 8);
+      const uint32_t stage_bytes = (2 * MW + nt) * kSlotVec;
+      const int stages = min(4u, ring_bytes / stage_bytes);
+      auto fetch = [&](int32_t w, int stage) {
+        if (w < wins) {
+          const int32_t c = w * 32 + 8 * q;
+          const bool in = c < a.in_features;
+          const int32_t cc = in ? c : 0;
+          uint32_t at = slot + stage * stage_bytes;
+#pragma unroll
+          for (int m = 0; m < MW; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h, at += kSlotVec) ring16(at, xr[m][h] + cc, in && live[m][h]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j, at += kSlotVec) {
+            if (j >= nt) break;
+            const int32_t i = r0 + 8 * j + g;
+            const bool ok = in && i < rank;
+            ring16(at, A + (int64_t)(ok ? i : 0) * a.in_features + cc, ok);
+          }
+        }
+        ring_commit();
+      };
+      for (int s = 0; s + 1 < stages; ++s) fetch(w0 + s * wstep, s);
       float acc[MW][NT][4] = {};
-      for (int32_t c = ((int32_t)(cr * KG) + kg) * 32 + 8 * q; c - 8 * q < a.in_features; c += (int32_t)C * KG * 32) {
-        const bool in = c < a.in_features;
-        uint4 xa[MW][2], av[NT];
+      int stage = 0;
+      for (int32_t w = w0; w < wins; w += wstep, stage = stage + 1 == stages ? 0 : stage + 1) {
+        fetch(w + (stages - 1) * wstep, stage == 0 ? stages - 1 : stage - 1);
+        ring_wait(stages - 1);
+        uint32_t at = slot + stage * stage_bytes;
+        uint4 xa[MW][2];
 #pragma unroll
         for (int m = 0; m < MW; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            xa[m][h] = make_uint4(0, 0, 0, 0);
-            if (in && xr[m][h]) xa[m][h] = *reinterpret_cast<const uint4*>(xr[m][h] + c);
-          }
+          for (int h = 0; h < 2; ++h, at += kSlotVec) xa[m][h] = slot16(at);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          av[j] = make_uint4(0, 0, 0, 0);
-          const int32_t i = r0 + 8 * j + g;
-          if (in && i < rank) av[j] = __ldg(reinterpret_cast<const uint4*>(A + (int64_t)i * a.in_features + c));
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (r0 + 8 * j >= rank) break;
+        for (int j = 0; j < NT; ++j, at += kSlotVec) {
+          if (j >= nt) break;
+          const uint4 av = slot16(at);
 #pragma unroll
           for (int m = 0; m < MW; ++m) {
-            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, av[j].x, av[j].y);
-            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, av[j].z, av[j].w);
+            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, av.x, av.y);
+            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, av.z, av.w);
           }
         }
       }
-      if (r0 > 0) __syncthreads();  // the last pass's sums have been read
+      ring_wait(0);
+      __syncthreads();  // the ring becomes the partial sums
 #pragma unroll
       for (int m = 0; m < MW; ++m)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(part + (kg * MT + (mg * MW + m) * 16 + h * 8 + g) * RP + 8 * j + 2 * q) =
+            *reinterpret_cast<float2*>(part + (warp * MT + m * 16 + h * 8 + g) * RP + 8 * j + 2 * q) =
                 make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
       __syncthreads();
-      for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
-        const int m = i / RPASS, r = i % RPASS;
+      auto own_sum = [&](int m, int r) {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < KG; ++k) s += part[(k * MT + m) * RP + r];
-        sum[m * RP + r] = s;
-      }
-      if (C > 1)
+        return s;
+      };
+      if (C > 1) {
+        for (int i = tid; i < MT * RPASS; i += kLoraThreads)
+          sum[i / RPASS * RP + i % RPASS] = own_sum(i / RPASS, i % RPASS);
         cluster_sync();
-      else
-        __syncthreads();
+      }
       for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
         const int m = i / RPASS, r = i % RPASS;
         float s = 0.f;
         if (C > 1) {
           for (uint32_t k = 0; k < C; ++k) s += peer_float(sum + m * RP + r, k);
         } else {
-          s = sum[m * RP + r];
+          s = own_sum(m, r);
         }
         s = r0 + r < rank ? s * scale : 0.f;
         if (r0 + r < R32)
@@ -394,88 +445,158 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
     }
   }
 
-  // out = y + B v
+  // out = y + B v.  A lane's columns of a block: 4 at c0 and 4 at c0 + next.
+  const bool quads = a.y_dtype == MOE_DTYPE_F32 || a.out_dtype == MOE_DTYPE_F32;
+  const bool yf = a.y_dtype == MOE_DTYPE_F32, has_y = a.y.data != nullptr;
+  const int32_t lc = quads ? 4 : 8, next = quads ? 16 : 4;
   const uint16_t* B = a.b + (rank > 0 ? (int64_t)t.adapter * a.out_features * a.max_rank : 0);
-  const int32_t blocks = (a.out_features + 31) / 32;
-  for (int32_t ob = (int32_t)cr * kLoraWarps + warp; ob < blocks; ob += (int32_t)C * kLoraWarps) {
-    const int32_t o0 = ob * 32;
-    const bool mine = o0 + 8 * q < a.out_features;  // the lane's 8 columns
+  const int32_t blocks = (a.out_features + 31) / 32, kwins = R32 / 32;
+  const uint32_t y_vecs = !has_y ? 0 : yf ? 2 : 1;
+  const uint32_t stage_bytes = max(1u, 4 * kwins + 2 * MW * y_vecs) * kSlotVec;
+  const int stages = min(4u, ring_bytes / stage_bytes);
+  int32_t tok[MW][2];
 #pragma unroll
-    for (int mh = 0; mh < MSPLIT; ++mh) {
-      __syncwarp();
-      float acc[MW][4][4] = {};
-      for (int32_t k0 = 0; k0 < R32; k0 += 32) {
-        uint4 bv[4];
+  for (int m = 0; m < MW; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int32_t o = o0 + 8 * (g >> 1) + 2 * j + (g & 1), i = k0 + 8 * q;
-          bv[j] = make_uint4(0, 0, 0, 0);
-          if (o < a.out_features && i < rank) {
-            bv[j] = __ldg(reinterpret_cast<const uint4*>(B + (int64_t)o * a.max_rank + i));
-            const int32_t left = rank - i;
-            if (left < 8) {  // what lies beyond the rank may hold anything
-              bv[j].x &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-              bv[j].y &= left >= 4 ? 0xffffffffu : left == 3 ? 0xffffu : 0u;
-              bv[j].z &= left >= 6 ? 0xffffffffu : left == 5 ? 0xffffu : 0u;
-              bv[j].w &= left == 7 ? 0xffffu : 0u;
-            }
-          }
-        }
-        for (int k = 0; k < terms; ++k)
+    for (int h = 0; h < 2; ++h) tok[m][h] = row[m * 16 + h * 8 + g];
+  const int32_t b0 = (int32_t)cr * kLoraWarps + warp, bstep = (int32_t)C * kLoraWarps;
+  auto fetch = [&](int32_t ob, int stage) {
+    if (ob < blocks) {
+      uint32_t at = slot + stage * stage_bytes;
+      if (has_y) {
+        const int32_t c = ob * 32 + lc * q;
+        const bool in0 = c < a.out_features, in1 = c + next < a.out_features;
 #pragma unroll
-          for (int m = 0; m < MW; ++m) {
-            const uint16_t* vr = v + (k * MT + (mh * MW + m) * 16 + g) * VP + k0 + 8 * q;
-            const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * VP);
+        for (int m = 0; m < MW; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, bv[j].x, bv[j].y);
-              mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, bv[j].z, bv[j].w);
+          for (int h = 0; h < 2; ++h, at += y_vecs * kSlotVec) {
+            const bool ok = tok[m][h] >= 0;
+            const char* p = static_cast<const char*>(a.y.data);
+            const int64_t e = (int64_t)max(tok[m][h], 0) * (a.y.stride ? a.y.stride : a.out_features);
+            if (yf) {
+              ring16(at, p + 4 * (e + (in0 ? c : 0)), ok && in0);
+              ring16(at + kSlotVec, p + 4 * (e + (in1 ? c + next : 0)), ok && in1);
+            } else if (quads) {
+              ring8(at, p + 2 * (e + (in0 ? c : 0)), ok && in0);
+              ring8(at + 8, p + 2 * (e + (in1 ? c + next : 0)), ok && in1);
+            } else {
+              ring16(at, p + 2 * (e + (in0 ? c : 0)), ok && in0);
             }
           }
       }
-      if (!mine) continue;
+      for (int32_t k = 0; k < kwins; ++k)
 #pragma unroll
-      for (int m = 0; m < MW; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int32_t tok = row[(mh * MW + m) * 16 + h * 8 + g];
-          if (tok < 0) continue;
-          float r[8] = {};
-          if (a.y.data) {
-            if (a.y_dtype == MOE_DTYPE_BF16)
-              load8(row_ptr<const uint16_t>(a.y, tok, a.out_features) + o0 + 8 * q, r);
-            else
-              load8(row_ptr<const float>(a.y, tok, a.out_features) + o0 + 8 * q, r);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            r[2 * j] += acc[m][j][2 * h];
-            r[2 * j + 1] += acc[m][j][2 * h + 1];
-          }
-          if (a.out_dtype == MOE_DTYPE_BF16)
-            store8(row_ptr<uint16_t>(a.out, tok, a.out_features) + o0 + 8 * q, r);
-          else
-            store8(row_ptr<float>(a.out, tok, a.out_features) + o0 + 8 * q, r);
+        for (int j = 0; j < 4; ++j, at += kSlotVec) {
+          const int32_t o = ob * 32 + (j >> 1) * next + (g >> 1) * lc + 2 * (j & 1) + (g & 1), i = k * 32 + 8 * q;
+          const bool ok = o < a.out_features && i < rank;
+          ring16(at, B + (ok ? (int64_t)o * a.max_rank + i : 0), ok);
         }
     }
+    ring_commit();
+  };
+  for (int s = 0; s + 1 < stages; ++s) fetch(b0 + s * bstep, s);
+  int stage = 0;
+  for (int32_t ob = b0; ob < blocks; ob += bstep, stage = stage + 1 == stages ? 0 : stage + 1) {
+    __syncwarp();
+    fetch(ob + (stages - 1) * bstep, stage == 0 ? stages - 1 : stage - 1);
+    ring_wait(stages - 1);
+    const uint32_t y_at = slot + stage * stage_bytes;
+    uint32_t at = y_at + 2 * MW * y_vecs * kSlotVec;
+    float acc[MW][4][4] = {};
+    for (int32_t k0 = 0; k0 < R32; k0 += 32) {
+      uint4 bv[4];
+      const int32_t left = rank - (k0 + 8 * q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j, at += kSlotVec) {
+        bv[j] = slot16(at);
+        if (left < 8 && left > 0) {  // what lies beyond the rank may hold anything
+          bv[j].x &= left >= 2 ? 0xffffffffu : 0xffffu;
+          bv[j].y &= left >= 4 ? 0xffffffffu : left == 3 ? 0xffffu : 0u;
+          bv[j].z &= left >= 6 ? 0xffffffffu : left == 5 ? 0xffffu : 0u;
+          bv[j].w &= left == 7 ? 0xffffu : 0u;
+        }
+      }
+      for (int k = 0; k < terms; ++k)
+#pragma unroll
+        for (int m = 0; m < MW; ++m) {
+          const uint16_t* vr = v + (k * MT + m * 16 + g) * VP + k0 + 8 * q;
+          const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * VP);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, bv[j].x, bv[j].y);
+            mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, bv[j].z, bv[j].w);
+          }
+        }
+    }
+    const int32_t c = ob * 32 + lc * q;
+    const bool in0 = c < a.out_features, in1 = c + next < a.out_features;
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (tok[m][h] < 0 || !in0) continue;
+        float r[8] = {};
+        if (has_y) {
+          const uint32_t ya = y_at + (2 * m + h) * y_vecs * kSlotVec;
+          const uint4 d = slot16(ya);
+          if (yf) {
+            const uint4 e = slot16(ya + kSlotVec);
+            r[0] = __uint_as_float(d.x);
+            r[1] = __uint_as_float(d.y);
+            r[2] = __uint_as_float(d.z);
+            r[3] = __uint_as_float(d.w);
+            r[4] = __uint_as_float(e.x);
+            r[5] = __uint_as_float(e.y);
+            r[6] = __uint_as_float(e.z);
+            r[7] = __uint_as_float(e.w);
+          } else {
+            unpack8(d, r);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          r[2 * j] += acc[m][j][2 * h];
+          r[2 * j + 1] += acc[m][j][2 * h + 1];
+        }
+        if (a.out_dtype == MOE_DTYPE_F32) {
+          float* p = row_ptr<float>(a.out, tok[m][h], a.out_features) + c;
+          *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
+          if (in1) *reinterpret_cast<float4*>(p + next) = make_float4(r[4], r[5], r[6], r[7]);
+        } else {
+          uint16_t* p = row_ptr<uint16_t>(a.out, tok[m][h], a.out_features) + c;
+          if (!quads) {
+            store8(p, r);
+          } else {
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+            if (in1) *reinterpret_cast<uint2*>(p + next) = make_uint2(pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+          }
+        }
+      }
   }
 }
 
-template <int MW, int MSPLIT, int NT>
+template <int MW, int NT>
 cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tiles, int32_t cluster,
                         cudaStream_t s) {
-  constexpr int MT = 16 * MW * MSPLIT, KG = kLoraWarps / MSPLIT, RP = 8 * NT + 8;
+  constexpr int MT = 16 * MW, KG = kLoraWarps, RP = 8 * NT + 8;
   const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;
-  const size_t smem = std::max<size_t>((size_t)(KG + 1) * MT * RP * 4 + (size_t)terms * MT * VP * 2,
-                                       (kFusedTokens + kLoraWarps) * 4);
+  // ring: four steps where two CTAs fit an SM with them, else as many as do
+  // (two at least), else one CTA an SM
+  const uint32_t y_vecs = !a.y.data ? 0 : a.y_dtype == MOE_DTYPE_F32 ? 2 : 1;
+  const uint32_t step = std::max<uint32_t>(2 * MW + NT, 4 * ((a.max_rank + 31) / 32) + 2 * MW * y_vecs) * kSlotVec;
+  const uint32_t rest = (cluster > 1 ? MT * RP * 4 : 0) + terms * MT * VP * 2;
+  const uint32_t two = 112 * 1024 - rest;
+  uint32_t ring = std::min(4 * step, 2 * step <= two ? two / step * step : 4 * step);
+  ring = std::min(ring, (200 * 1024 - rest) / step * step);
+  ring = std::max<uint32_t>({ring, (uint32_t)(KG * MT * RP * 4), (uint32_t)((kFusedTokens + kLoraWarps) * 4)});
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = raise_smem_limit(lora_kernel<MW, MSPLIT, NT>, 200 * 1024, configured);
+  cudaError_t e = raise_smem_limit(lora_kernel<MW, NT>, 220 * 1024, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * cluster));
   cfg.blockDim = dim3(kLoraThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = ring + rest;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -485,15 +606,15 @@ cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, i
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = fused ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<MW, MSPLIT, NT>, a, p, (int32_t)fused, terms);
+  return cudaLaunchKernelEx(&cfg, lora_kernel<MW, NT>, a, p, (int32_t)fused, terms, ring);
 }
 
-template <int MW, int MSPLIT>
+template <int MW>
 cudaError_t lora_rank(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tiles, int32_t cluster,
                       cudaStream_t s) {
-  if (a.max_rank <= 16) return lora_launch<MW, MSPLIT, 2>(a, p, fused, tiles, cluster, s);
-  if (a.max_rank <= 32) return lora_launch<MW, MSPLIT, 4>(a, p, fused, tiles, cluster, s);
-  return lora_launch<MW, MSPLIT, 8>(a, p, fused, tiles, cluster, s);
+  if (a.max_rank <= 16) return lora_launch<MW, 2>(a, p, fused, tiles, cluster, s);
+  if (a.max_rank <= 32) return lora_launch<MW, 4>(a, p, fused, tiles, cluster, s);
+  return lora_launch<MW, 8>(a, p, fused, tiles, cluster, s);
 }
 
 }  // namespace
@@ -508,7 +629,7 @@ size_t lora_workspace(int32_t n, int32_t n_adapters) {
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s) {
   const int32_t n = a.n, L = a.n_adapters;
   const bool fused = n <= kFusedTokens;
-  const int32_t mt = n <= 1024 ? 16 : n <= 8192 ? 32 : 64;
+  const int32_t mt = n <= 1024 ? 16 : 32;
   const LoraPlan p = fused ? LoraPlan{} : lora_plan(workspace, n, L);
   if (!fused) {
     const int32_t slices = plan_slices(n);
@@ -526,9 +647,7 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
   const int32_t tiles = n / mt + std::min(n, L + 1);
   int32_t cluster = 1;
   while (cluster < 8 && tiles * cluster * 2 <= 608) cluster *= 2;
-  if (mt == 16) return lora_rank<1, 1>(a, p, fused, tiles, cluster, s);
-  if (mt == 32) return lora_rank<2, 1>(a, p, fused, tiles, cluster, s);
-  return lora_rank<2, 2>(a, p, fused, tiles, cluster, s);
+  return mt == 16 ? lora_rank<1>(a, p, fused, tiles, cluster, s) : lora_rank<2>(a, p, fused, tiles, cluster, s);
 }
 
 }  // namespace moe
