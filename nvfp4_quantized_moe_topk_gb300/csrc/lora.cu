@@ -281,12 +281,12 @@ __device__ __forceinline__ bool find_tile(const moe_lora_args& a, const LoraPlan
   return true;
 }
 
-// 16 (or 8) bytes into a ring slot, zeros where `ok` is false (src is then not read).
-__device__ __forceinline__ void ring16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+// 16 (or 8) bytes into a ring slot.
+__device__ __forceinline__ void ring16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void ring8(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+__device__ __forceinline__ void ring8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 slot16(uint32_t at) {
   uint4 v;
@@ -334,63 +334,79 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   __syncthreads();  // the tile's scratch, in the ring, has been read
 
   if (rank > 0) {
-    const uint16_t* A = a.a + (int64_t)t.adapter * a.max_rank * a.in_features;
-    const uint16_t* xr[MW][2];
-    bool live[MW][2];
+    const char* A = reinterpret_cast<const char*>(a.a + (int64_t)t.adapter * a.max_rank * a.in_features);
+    const uint32_t row_bytes = (uint32_t)a.in_features * 2;
+    // places past the tile's count take its first token: their rows of the
+    // products are never looked at
+    const char* xr[MW][2];
 #pragma unroll
     for (int m = 0; m < MW; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int32_t tok = row[m * 16 + h * 8 + g];
-        live[m][h] = tok >= 0;
-        xr[m][h] = row_ptr<const uint16_t>(a.x, max(tok, 0), a.in_features);
+        xr[m][h] = static_cast<const char*>(a.x.data) + 16 * q +
+                   (int64_t)(tok >= 0 ? tok : row[0]) * (a.x.stride ? a.x.stride : a.in_features) * 2;
       }
-    const int32_t w0 = (int32_t)cr * KG + warp, wstep = (int32_t)C * KG, wins = (a.in_features + 31) / 32;
+    // a warp takes pairs of windows, 128 bytes of a row: first the even, then the odd one
+    const uint32_t pair0 = ((uint32_t)cr * KG + warp) * 128, jump = (uint32_t)C * KG * 128 - 64;
     for (int32_t r0 = 0; r0 < rank; r0 += RPASS) {
       const int32_t nt = min(NT, (rank - r0 + 7) / 8);
       const uint32_t stage_bytes = (2 * MW + nt) * kSlotVec;
       const int stages = min(4u, ring_bytes / stage_bytes);
-      auto fetch = [&](int32_t w, int stage) {
-        if (w < wins) {
-          const int32_t c = w * 32 + 8 * q;
-          const bool in = c < a.in_features;
-          const int32_t cc = in ? c : 0;
-          uint32_t at = slot + stage * stage_bytes;
+      const char* Ar = A + (uint64_t)r0 * row_bytes;
+      const uint32_t lane_a = g * row_bytes + 16 * q;
+      uint32_t fetch_off = pair0;  // byte offset in a row of the window to fetch next
+      bool fetch_odd = false;
+      auto fetch = [&](int stage) {
+        if (fetch_off < row_bytes) {
+          if (fetch_off + 16 * q < row_bytes) {  // else the lane's part lies past the row's end, and is read as 0
+            const uint32_t at = slot + stage * stage_bytes;
 #pragma unroll
-          for (int m = 0; m < MW; ++m)
+            for (int m = 0; m < MW; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h, at += kSlotVec) ring16(at, xr[m][h] + cc, in && live[m][h]);
+              for (int h = 0; h < 2; ++h) ring16(at + (2 * m + h) * kSlotVec, xr[m][h] + fetch_off);
+            // rows between the rank and the next multiple of 8 are in the bank
+            // and reach only entries of v that are set to zero
 #pragma unroll
-          for (int j = 0; j < NT; ++j, at += kSlotVec) {
-            if (j >= nt) break;
-            const int32_t i = r0 + 8 * j + g;
-            const bool ok = in && i < rank;
-            ring16(at, A + (int64_t)(ok ? i : 0) * a.in_features + cc, ok);
+            for (int j = 0; j < NT; ++j) {
+              if (j >= nt) break;
+              ring16(at + (2 * MW + j) * kSlotVec, Ar + ((uint64_t)(8 * j) * row_bytes + fetch_off) + lane_a);
+            }
           }
         }
+        fetch_off += fetch_odd ? jump : 64;
+        fetch_odd = !fetch_odd;
         ring_commit();
       };
-      for (int s = 0; s + 1 < stages; ++s) fetch(w0 + s * wstep, s);
+      for (int s = 0; s + 1 < stages; ++s) fetch(s);
       float acc[MW][NT][4] = {};
       int stage = 0;
-      for (int32_t w = w0; w < wins; w += wstep, stage = stage + 1 == stages ? 0 : stage + 1) {
-        fetch(w + (stages - 1) * wstep, stage == 0 ? stages - 1 : stage - 1);
+      bool odd = false;
+      for (uint32_t off = pair0; off < row_bytes;
+           off += odd ? jump : 64, odd = !odd, stage = stage + 1 == stages ? 0 : stage + 1) {
+        fetch(stage == 0 ? stages - 1 : stage - 1);
         ring_wait(stages - 1);
-        uint32_t at = slot + stage * stage_bytes;
+        const uint32_t at = slot + stage * stage_bytes;
+        const bool past = off + 16 * q >= row_bytes;
         uint4 xa[MW][2];
 #pragma unroll
         for (int m = 0; m < MW; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h, at += kSlotVec) xa[m][h] = slot16(at);
-#pragma unroll
-        for (int j = 0; j < NT; ++j, at += kSlotVec) {
-          if (j >= nt) break;
-          const uint4 av = slot16(at);
-#pragma unroll
-          for (int m = 0; m < MW; ++m) {
-            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, av.x, av.y);
-            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, av.z, av.w);
+          for (int h = 0; h < 2; ++h) {
+            xa[m][h] = slot16(at + (2 * m + h) * kSlotVec);
+            if (past) xa[m][h] = make_uint4(0, 0, 0, 0);
           }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (j >= nt) break;
+          uint4 av = slot16(at + (2 * MW + j) * kSlotVec);
+          if (past) av = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int m = 0; m < MW; ++m)
+            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, av.x, av.y);
+#pragma unroll
+          for (int m = 0; m < MW; ++m)
+            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, av.z, av.w);
         }
       }
       ring_wait(0);
@@ -449,48 +465,62 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   const bool quads = a.y_dtype == MOE_DTYPE_F32 || a.out_dtype == MOE_DTYPE_F32;
   const bool yf = a.y_dtype == MOE_DTYPE_F32, has_y = a.y.data != nullptr;
   const int32_t lc = quads ? 4 : 8, next = quads ? 16 : 4;
-  const uint16_t* B = a.b + (rank > 0 ? (int64_t)t.adapter * a.out_features * a.max_rank : 0);
+  const char* B = reinterpret_cast<const char*>(a.b) +
+                  (rank > 0 ? (int64_t)t.adapter * a.out_features * a.max_rank * 2 : 0);
   const int32_t blocks = (a.out_features + 31) / 32, kwins = R32 / 32;
-  const uint32_t y_vecs = !has_y ? 0 : yf ? 2 : 1;
+  const uint32_t y_vecs = !has_y ? 0 : yf ? 2 : 1, y_size = yf ? 4 : 2;
   const uint32_t stage_bytes = max(1u, 4 * kwins + 2 * MW * y_vecs) * kSlotVec;
   const int stages = min(4u, ring_bytes / stage_bytes);
   int32_t tok[MW][2];
+  const char* yr[MW][2];  // (places past the tile's count: its first token, and nothing is stored)
 #pragma unroll
   for (int m = 0; m < MW; ++m)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) tok[m][h] = row[m * 16 + h * 8 + g];
+    for (int h = 0; h < 2; ++h) {
+      tok[m][h] = row[m * 16 + h * 8 + g];
+      yr[m][h] = static_cast<const char*>(a.y.data) +
+                 ((int64_t)(tok[m][h] >= 0 ? tok[m][h] : row[0]) * (a.y.stride ? a.y.stride : a.out_features) + lc * q) *
+                     y_size;
+    }
   const int32_t b0 = (int32_t)cr * kLoraWarps + warp, bstep = (int32_t)C * kLoraWarps;
+  const int32_t lane_o = (g >> 1) * lc + (g & 1);    // the lane's row of B in a block, without j's part
+  const uint32_t b_bytes = (uint32_t)a.max_rank * 2;  // of a row of B
+  const uint32_t lane_b = (uint32_t)lane_o * b_bytes + 16 * q;
   auto fetch = [&](int32_t ob, int stage) {
     if (ob < blocks) {
       uint32_t at = slot + stage * stage_bytes;
       if (has_y) {
-        const int32_t c = ob * 32 + lc * q;
-        const bool in0 = c < a.out_features, in1 = c + next < a.out_features;
+        const bool in0 = ob * 32 + lc * q < a.out_features, in1 = ob * 32 + lc * q + next < a.out_features;
+        const uint32_t e = (uint32_t)ob * 32 * y_size;
 #pragma unroll
         for (int m = 0; m < MW; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h, at += y_vecs * kSlotVec) {
-            const bool ok = tok[m][h] >= 0;
-            const char* p = static_cast<const char*>(a.y.data);
-            const int64_t e = (int64_t)max(tok[m][h], 0) * (a.y.stride ? a.y.stride : a.out_features);
+          for (int h = 0; h < 2; ++h) {
             if (yf) {
-              ring16(at, p + 4 * (e + (in0 ? c : 0)), ok && in0);
-              ring16(at + kSlotVec, p + 4 * (e + (in1 ? c + next : 0)), ok && in1);
-            } else if (quads) {
-              ring8(at, p + 2 * (e + (in0 ? c : 0)), ok && in0);
-              ring8(at + 8, p + 2 * (e + (in1 ? c + next : 0)), ok && in1);
+              if (in0) ring16(at, yr[m][h] + e);
+              if (in1) ring16(at + kSlotVec, yr[m][h] + e + 64);
+              at += 2 * kSlotVec;
             } else {
-              ring16(at, p + 2 * (e + (in0 ? c : 0)), ok && in0);
+              if (quads) {
+                if (in0) ring8(at, yr[m][h] + e);
+                if (in1) ring8(at + 8, yr[m][h] + e + 32);
+              } else if (in0) {
+                ring16(at, yr[m][h] + e);
+              }
+              at += kSlotVec;
             }
           }
       }
-      for (int32_t k = 0; k < kwins; ++k)
+      const char* Bo = B + (uint64_t)((uint32_t)ob * 32) * b_bytes;
+      const int32_t left_o = a.out_features - ob * 32 - lane_o;
+      for (int32_t k = 0; k < kwins; ++k) {
+        const bool in = k * 32 + 8 * q < rank;
 #pragma unroll
         for (int j = 0; j < 4; ++j, at += kSlotVec) {
-          const int32_t o = ob * 32 + (j >> 1) * next + (g >> 1) * lc + 2 * (j & 1) + (g & 1), i = k * 32 + 8 * q;
-          const bool ok = o < a.out_features && i < rank;
-          ring16(at, B + (ok ? (int64_t)o * a.max_rank + i : 0), ok);
+          const int32_t jo = (j >> 1) * next + 2 * (j & 1);
+          if (in && jo < left_o) ring16(at, Bo + ((uint64_t)(uint32_t)jo * b_bytes + k * 64) + lane_b);
         }
+      }
     }
     ring_commit();
   };
@@ -509,8 +539,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
 #pragma unroll
       for (int j = 0; j < 4; ++j, at += kSlotVec) {
         bv[j] = slot16(at);
-        if (left < 8 && left > 0) {  // what lies beyond the rank may hold anything
-          bv[j].x &= left >= 2 ? 0xffffffffu : 0xffffu;
+        if (left < 8) {  // what lies beyond the rank may hold anything
+          bv[j].x &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
           bv[j].y &= left >= 4 ? 0xffffffffu : left == 3 ? 0xffffu : 0u;
           bv[j].z &= left >= 6 ? 0xffffffffu : left == 5 ? 0xffffu : 0u;
           bv[j].w &= left == 7 ? 0xffffu : 0u;
@@ -522,10 +552,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           const uint16_t* vr = v + (k * MT + m * 16 + g) * VP + k0 + 8 * q;
           const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * VP);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, bv[j].x, bv[j].y);
-            mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, bv[j].z, bv[j].w);
-          }
+          for (int j = 0; j < 4; ++j) mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, bv[j].x, bv[j].y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, bv[j].z, bv[j].w);
         }
     }
     const int32_t c = ob * 32 + lc * q;
