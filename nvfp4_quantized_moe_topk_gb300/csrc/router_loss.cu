@@ -6,13 +6,17 @@
 //   loss = coef E / (N k) sum_s (1 / N_s) sum_e c[s][e] P[s][e]
 //   d_logits = p (g - sum g p) + the top-k weights' own softmax gradient
 //
-// One warp takes one token, its logits in registers.  A block owns a
+// One warp takes one token, its logits in registers (for few experts several
+// tokens at a time, so that enough loads are in flight).  A block owns a
 // contiguous range of tokens and walks the sequences that meet it; the column
 // sums of its tokens stay in registers until the sequence or the range ends
 // and are then written to slot block + sequence of the workspace (both only
 // grow along the walk, so each pair has a slot of its own).  The join adds the
 // slots of a sequence in block order: no atomics on floats, the same bits on
-// every run.
+// every run.  Batches that one block holds need no join: one launch.
+//
+// The top-k weights' gradient touches k of a row's experts: each warp adds it
+// to its row through its own row of shared memory, zero but for those.
 #include <algorithm>
 
 #include "block.cuh"
@@ -23,14 +27,16 @@ namespace moe {
 
 namespace {
 
-constexpr int kLossWarps = 8;
+constexpr int kLossThreads = 512, kLossWarps = kLossThreads / 32;
+constexpr int32_t kLossOneBlock = 4 * kLossWarps;  // tokens that one block takes alone
 
 // The workspace of both calls.
 struct LossSpace {
-  float* sums;     // [blocks + n_seqs][E]
-  int32_t* picks;  // [blocks + n_seqs][E]
-  int32_t* toks;   // [blocks + n_seqs]
-  float* dots;     // [n_seqs]: (1 / N_s) sum_e c P
+  float* sums;      // [blocks + n_seqs][E]
+  int32_t* picks;   // [blocks + n_seqs][E]
+  int32_t* toks;    // [blocks + n_seqs]
+  float* dots;      // [n_seqs]: (1 / N_s) sum_e c P
+  int32_t* ticket;  // blocks of the join that are done
 };
 
 __host__ __device__ inline int64_t round4(int64_t v) { return (v + 3) & ~int64_t(3); }
@@ -42,6 +48,7 @@ LossSpace loss_space(void* ws, int32_t n, int32_t E, int32_t S) {
   p.picks = reinterpret_cast<int32_t*>(p.sums + round4(slots * E));
   p.toks = p.picks + round4(slots * E);
   p.dots = reinterpret_cast<float*>(p.toks + round4(slots));
+  p.ticket = reinterpret_cast<int32_t*>(p.dots + round4(S));
   return p;
 }
 
@@ -75,224 +82,392 @@ __device__ __forceinline__ int32_t first_seq(const moe_router_args& a, int32_t t
   return lo;
 }
 
-// A token's softmax: lane l holds experts l + 32 i.  A row without any logit
-// above -inf gives p = 0.
-template <int SLOTS>
-__device__ __forceinline__ void token_softmax(const moe_router_args& a, int64_t t, int lane, float (&p)[SLOTS]) {
-  const float* row = a.logits + t * a.n_experts;
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < SLOTS; ++i) {
-    const int32_t e = lane + 32 * i;
-    p[i] = -INFINITY;
-    if (e < a.n_experts) p[i] = a.bias ? row[e] + __ldg(a.bias + e) : row[e];
-    m = fmaxf(m, p[i]);
+// A lane's N experts of a row.  VEC: groups of 4 (rows aligned to 16 bytes),
+// else one by one.
+template <bool VEC, int N>
+struct Row {
+  static_assert(N % 4 == 0, "");
+  static __device__ __forceinline__ int32_t expert(int i, int lane) {
+    return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : 32 * i + lane;
   }
+  static __device__ __forceinline__ void load(const float* row, int32_t E, int lane, float (&v)[N], float fill) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        float4 d = make_float4(fill, fill, fill, fill);
+        if (expert(i, lane) < E) d = *reinterpret_cast<const float4*>(row + expert(i, lane));
+        v[i] = d.x;
+        v[i + 1] = d.y;
+        v[i + 2] = d.z;
+        v[i + 3] = d.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = expert(i, lane) < E ? row[expert(i, lane)] : fill;
+    }
+  }
+  static __device__ __forceinline__ void store(float* row, int32_t E, int lane, const float (&v)[N]) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        if (expert(i, lane) < E)
+          *reinterpret_cast<float4*>(row + expert(i, lane)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (expert(i, lane) < E) row[expert(i, lane)] = v[i];
+    }
+  }
+};
+
+// A token's softmax from its logits (-inf past the last expert), in place; a
+// row without any logit above -inf gives p = 0.  s_bias: the bias in shared
+// memory, or nullptr.
+template <bool VEC, int N>
+__device__ __forceinline__ void softmax_row(const float* s_bias, int32_t E, int lane, float (&z)[N]) {
+  if (s_bias) {
+    float b[N];
+    Row<VEC, N>::load(s_bias, E, lane, b, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] += b[i];
+  }
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, z[i]);
   m = warp_max(m);
   if (m == -INFINITY) m = 0.f;
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) {
-    p[i] = expf(p[i] - m);
-    sum += p[i];
+  for (int i = 0; i < N; ++i) {
+    z[i] = expf(z[i] - m);
+    sum += z[i];
   }
   sum = warp_add(sum);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) p[i] *= inv;
+  for (int i = 0; i < N; ++i) z[i] *= inv;
 }
 
-template <int SLOTS>
-__global__ void __launch_bounds__(kLossWarps * 32)
-    balance_partial_kernel(const moe_router_args a, const LossSpace ws, int32_t per_block) {
-  extern __shared__ float sm[];  // [kLossWarps][E] sums, then [E] picks
+// The block's sum over its warps of a column of s_acc [kLossWarps][pitch].
+__device__ __forceinline__ float column(const float* s_acc, int32_t pitch, int32_t e) {
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kLossWarps; ++w) v += s_acc[w * pitch + e];
+  return v;
+}
+
+// Floats of a row in shared memory: the last lanes' groups of 4 included.
+__host__ __device__ inline int32_t row_pitch(int32_t E) { return (E + 3) & ~3; }
+
+__device__ __forceinline__ float block_sum(float v, float* s_warp) {
+  v = warp_add(v);
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) v += s_warp[w];
+  __syncthreads();
+  return v;
+}
+
+template <bool VEC, int N>
+__global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
+    balance_kernel(const moe_router_args a, const LossSpace ws, int32_t per_block, float* __restrict__ prob_sums,
+                   float* __restrict__ loss) {
+  constexpr int TOK = N >= 16 ? 1 : 16 / N;  // tokens of a warp at a time
+  extern __shared__ __align__(16) float sm[];  // [kLossWarps][pitch] sums, bias, picks
   __shared__ int32_t s_toks;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.n_experts;
-  int32_t* s_picks = reinterpret_cast<int32_t*>(sm + kLossWarps * E);
+  __shared__ float s_warp[kLossWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.n_experts, k = a.top_k;
+  const int32_t pitch = row_pitch(E);
+  float* s_bias = sm + kLossWarps * pitch;
+  int32_t* s_picks = reinterpret_cast<int32_t*>(s_bias + pitch);
+  const bool alone = gridDim.x == 1;
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !alone) *ws.ticket = 0;
+  for (int32_t e = threadIdx.x; e < E; e += kLossThreads) {
+    if (a.bias) s_bias[e] = a.bias[e];
+    s_picks[e] = 0;
+  }
+  if (threadIdx.x == 0) s_toks = 0;
+  __syncthreads();
   const int32_t lo = (int32_t)min((int64_t)blockIdx.x * per_block, (int64_t)a.n);
   const int32_t hi = (int32_t)min((int64_t)lo + per_block, (int64_t)a.n);
-  for (int32_t s = first_seq(a, lo); s < a.n_seqs; ++s) {
-    const int32_t beg = max(lo, seq_bound(a, s)), end = min(hi, seq_bound(a, s + 1));
-    if (seq_bound(a, s) >= hi) break;
-    if (beg >= end) continue;
-    for (int32_t e = threadIdx.x; e < E; e += blockDim.x) s_picks[e] = 0;
-    if (threadIdx.x == 0) s_toks = 0;
-    __syncthreads();
-    float acc[SLOTS] = {};
+  float total_dot = 0.f;
+  int32_t total = 0;
+  for (int32_t s = alone ? 0 : first_seq(a, lo); s < a.n_seqs; ++s) {
+    const int32_t at = seq_bound(a, s);
+    if (!alone && at >= hi) break;
+    const int32_t beg = max(lo, at), end = min(hi, seq_bound(a, s + 1));
+    if (!alone && beg >= end) continue;
+    float acc[N] = {};
     int32_t toks = 0;
-    for (int64_t t = (int64_t)beg + warp; t < end; t += kLossWarps) {
-      if (a.token_mask && !a.token_mask[t]) continue;
-      ++toks;
-      float p[SLOTS];
-      token_softmax<SLOTS>(a, t, lane, p);
+    for (int64_t t = (int64_t)beg + warp; t < end; t += kLossWarps * TOK) {
+      float z[TOK][N];
+      bool on[TOK];
 #pragma unroll
-      for (int i = 0; i < SLOTS; ++i) acc[i] += p[i];
-      if (lane < a.top_k) {
-        const int32_t e = a.topk_ids[t * a.top_k + lane];
+      for (int u = 0; u < TOK; ++u) {
+        const int64_t tu = t + u * kLossWarps;
+        on[u] = tu < end && (!a.token_mask || a.token_mask[tu]);
+        if (on[u]) Row<VEC, N>::load(a.logits + tu * E, E, lane, z[u], -INFINITY);
+        const int32_t e = on[u] && lane < k ? a.topk_ids[tu * k + lane] : -1;
         if (e >= 0 && e < E) atomicAdd(&s_picks[e], 1);
       }
-    }
+      __syncwarp();
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i)
-      if (lane + 32 * i < E) sm[warp * E + lane + 32 * i] = acc[i];
-    if (lane == 0) atomicAdd(&s_toks, toks);
-    __syncthreads();
-    const int64_t slot = (int64_t)blockIdx.x + s;
-    for (int32_t e = threadIdx.x; e < E; e += blockDim.x) {
-      float v = 0.f;
+      for (int u = 0; u < TOK; ++u) {
+        if (!on[u]) continue;
+        ++toks;
+        softmax_row<VEC, N>(a.bias ? s_bias : nullptr, E, lane, z[u]);
 #pragma unroll
-      for (int w = 0; w < kLossWarps; ++w) v += sm[w * E + e];
-      ws.sums[slot * E + e] = v;
-      ws.picks[slot * E + e] = s_picks[e];
+        for (int i = 0; i < N; ++i) acc[i] += z[u][i];
+      }
     }
-    if (threadIdx.x == 0) ws.toks[slot] = s_toks;
+    Row<VEC, N>::store(sm + warp * pitch, E, lane, acc);
+    if (lane == 0 && toks) atomicAdd(&s_toks, toks);
     __syncthreads();
+    const int32_t all = s_toks;
+    if (alone) {
+      float dot = 0.f;
+      for (int32_t e = threadIdx.x; e < E; e += kLossThreads) {
+        const float v = column(sm, pitch, e);
+        const int32_t c = s_picks[e];
+        prob_sums[(int64_t)s * E + e] = v;
+        a.counts[(int64_t)s * E + e] = c;
+        s_picks[e] = 0;
+        dot = fmaf((float)c, v, dot);
+      }
+      dot = block_sum(dot, s_warp);
+      if (threadIdx.x == 0) a.tokens[s] = all;
+      if (all > 0) total_dot += dot / (float)all;
+      total += all;
+    } else {
+      const int64_t slot = (int64_t)blockIdx.x + s;
+      for (int32_t e = threadIdx.x; e < E; e += kLossThreads) {
+        ws.sums[slot * E + e] = column(sm, pitch, e);
+        ws.picks[slot * E + e] = s_picks[e];
+        s_picks[e] = 0;
+      }
+      if (threadIdx.x == 0) ws.toks[slot] = all;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s_toks = 0;
+    __syncthreads();
+  }
+  if (alone && threadIdx.x == 0) {
+    a.tokens[a.n_seqs] = total;
+    loss[0] = total > 0 ? a.coef * ((float)E / ((float)total * (float)k)) * total_dot : 0.f;
   }
 }
 
-// One block per sequence: joins its slots in block order.
-constexpr int kJoinThreads = 256;
+// One block per sequence joins its slots in block order: thread (column, part
+// of the slots); the parts meet in shared memory in order.  The last block to
+// finish adds up the loss over the sequences, in their order.
+constexpr int kJoinThreads = 1024;
 __global__ void __launch_bounds__(kJoinThreads)
-    balance_join_kernel(const moe_router_args a, const LossSpace ws, int32_t per_block, float* __restrict__ prob_sums) {
-  __shared__ float s_dot[kJoinThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.n_experts;
+    balance_join_kernel(const moe_router_args a, const LossSpace ws, int32_t per_block, int32_t cols,
+                        float* __restrict__ prob_sums, float* __restrict__ loss) {
+  __shared__ float s_sum[kJoinThreads];
+  __shared__ int32_t s_pick[kJoinThreads];
+  __shared__ float s_warp[kJoinThreads / 32];
+  __shared__ int32_t s_last;
+  const int E = a.n_experts, tid = threadIdx.x;
   const int32_t s = blockIdx.x, beg = seq_bound(a, s), end = seq_bound(a, s + 1);
   const int32_t b0 = beg / per_block, b1 = end > beg ? (end - 1) / per_block : b0 - 1;
-  int32_t toks = 0;
-  for (int32_t b = b0; b <= b1; ++b) toks += ws.toks[(int64_t)b + s];
+  const int32_t parts = kJoinThreads / cols, part = tid / cols, col = tid % cols;  // cols: a power of two
+  pdl_wait();
   float dot = 0.f;
-  for (int32_t e = threadIdx.x; e < E; e += kJoinThreads) {
+  for (int32_t e0 = 0; e0 < E; e0 += cols) {
+    const int32_t e = e0 + col;
     float v = 0.f;
     int32_t c = 0;
-    for (int32_t b = b0; b <= b1; ++b) {
-      v += ws.sums[((int64_t)b + s) * E + e];
-      c += ws.picks[((int64_t)b + s) * E + e];
+    if (e < E) {
+#pragma unroll 4
+      for (int32_t b = b0 + part; b <= b1; b += parts) {
+        v += ws.sums[((int64_t)b + s) * E + e];
+        c += ws.picks[((int64_t)b + s) * E + e];
+      }
     }
-    prob_sums[(int64_t)s * E + e] = v;
-    a.counts[(int64_t)s * E + e] = c;
-    dot = fmaf((float)c, v, dot);
+    s_sum[tid] = v;
+    s_pick[tid] = c;
+    __syncthreads();
+    if (part == 0 && e < E) {
+      for (int32_t i = 1; i < parts; ++i) {
+        v += s_sum[i * cols + col];
+        c += s_pick[i * cols + col];
+      }
+      prob_sums[(int64_t)s * E + e] = v;
+      a.counts[(int64_t)s * E + e] = c;
+      dot = fmaf((float)c, v, dot);
+    }
+    __syncthreads();
   }
-  dot = warp_add(dot);
-  if (lane == 0) s_dot[warp] = dot;
+  int32_t toks = 0;
+  for (int32_t b = b0 + tid; b <= b1; b += kJoinThreads) toks += ws.toks[(int64_t)b + s];
+  s_pick[tid] = toks;
+  dot = block_sum(dot, s_warp);
+  if (tid < 32) {
+    toks = 0;
+    for (int i = tid; i < kJoinThreads; i += 32) toks += s_pick[i];
+    toks = __reduce_add_sync(0xffffffffu, toks);
+  }
+  if (tid == 0) {
+    a.tokens[s] = toks;
+    ws.dots[s] = toks > 0 ? dot / (float)toks : 0.f;
+    __threadfence();
+    s_last = atomicAdd(ws.ticket, 1) == (int32_t)gridDim.x - 1;
+  }
   __syncthreads();
-  if (threadIdx.x) return;
-  dot = 0.f;
-  for (int w = 0; w < kJoinThreads / 32; ++w) dot += s_dot[w];
-  a.tokens[s] = toks;
-  ws.dots[s] = toks > 0 ? dot / (float)toks : 0.f;
-}
-
-// One warp: the loss over the sequences.
-__global__ void balance_loss_kernel(const moe_router_args a, const LossSpace ws, float* __restrict__ loss) {
+  if (!s_last || tid >= 32) return;
+  __threadfence();
   float v = 0.f;
   int32_t n = 0;
-  for (int32_t s = threadIdx.x; s < a.n_seqs; s += 32) {
-    v += ws.dots[s];
-    n += a.tokens[s];
+  for (int32_t i = tid; i < a.n_seqs; i += 32) {
+    v += __ldcg(ws.dots + i);
+    n += __ldcg(a.tokens + i);
   }
   v = warp_add(v);
   n = __reduce_add_sync(0xffffffffu, n);
-  if (threadIdx.x) return;
+  if (tid) return;
   a.tokens[a.n_seqs] = n;
-  loss[0] = n > 0 ? a.coef * ((float)a.n_experts / ((float)n * (float)a.top_k)) * v : 0.f;
+  loss[0] = n > 0 ? a.coef * ((float)E / ((float)n * (float)a.top_k)) * v : 0.f;
 }
 
 // d_logits of a block's tokens and, where d_bias is wanted, their column sums
-// (slot = block).
-template <int SLOTS>
-__global__ void __launch_bounds__(kLossWarps * 32)
+// (slot = block; straight into d_bias where there is one block).
+template <bool VEC, int N>
+__global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
     router_backward_kernel(const moe_router_args a, const float* __restrict__ w, const float* __restrict__ dw,
                            const float* __restrict__ d_loss, float* __restrict__ d_logits, float* __restrict__ sums,
                            int32_t per_block) {
-  extern __shared__ float sm[];  // [kLossWarps][E] where sums are wanted
+  constexpr int TOK = N >= 16 ? 1 : 16 / N;
+  extern __shared__ __align__(16) float sm[];  // [kLossWarps][pitch] the warps' rows, bias, g
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.n_experts, k = a.top_k;
+  const int32_t pitch = row_pitch(E);
+  float* pick = sm + warp * pitch;  // zero between tokens
+  float* s_bias = sm + kLossWarps * pitch;
+  float* s_g = s_bias + pitch;
+  pdl_launch_dependents();
+  for (int32_t i = threadIdx.x; i < kLossWarps * pitch; i += kLossThreads) sm[i] = 0.f;
+  if (a.bias)
+    for (int32_t e = threadIdx.x; e < E; e += kLossThreads) s_bias[e] = a.bias[e];
   const int32_t lo = (int32_t)min((int64_t)blockIdx.x * per_block, (int64_t)a.n);
   const int32_t hi = (int32_t)min((int64_t)lo + per_block, (int64_t)a.n);
-  float acc[SLOTS] = {}, g[SLOTS] = {};
+  float acc[N] = {};
   float scale = 0.f;
   if (a.counts) {
     const int32_t total = a.tokens[a.n_seqs];
     if (total > 0) scale = a.coef * (d_loss ? d_loss[0] : 1.f) * ((float)E / ((float)total * (float)k));
   }
-  int32_t s = a.counts ? first_seq(a, lo) : 0, s_end = -1;  // g holds sequence s once s_end is its end
-  for (int64_t t = (int64_t)lo + warp; t < hi; t += kLossWarps) {
-    float d[SLOTS] = {};
-    if (a.counts && (!a.token_mask || a.token_mask[t])) {
-      if (t >= s_end) {
-        while (s < a.n_seqs && seq_bound(a, s + 1) <= t) ++s;
-        s_end = a.n;
-        float f = 0.f;
-        if (s < a.n_seqs && seq_bound(a, s) <= t) {
-          s_end = seq_bound(a, s + 1);
-          const int32_t mine = a.tokens[s];
-          if (mine > 0) f = scale / (float)mine;
+  // the sequences that meet the block (without a loss term: all its tokens at once)
+  for (int32_t s = a.counts ? first_seq(a, lo) : 0, at = lo; at < hi;) {
+    int32_t end = hi;
+    bool lossy = false;
+    if (a.counts && s < a.n_seqs) {
+      const int32_t beg = seq_bound(a, s);
+      if (beg > at) {
+        end = min(hi, beg);  // tokens of no sequence
+      } else {
+        end = max(at, min(hi, seq_bound(a, s + 1)));
+        lossy = true;
+        __syncthreads();  // the last sequence's g has been read
+        const int32_t mine = a.tokens[s];
+        const float f = mine > 0 ? scale / (float)mine : 0.f;
+        for (int32_t e = threadIdx.x; e < E; e += kLossThreads) s_g[e] = f * (float)a.counts[(int64_t)s * E + e];
+        ++s;
+      }
+    }
+    __syncthreads();
+    for (int64_t t = (int64_t)at + warp; t < end; t += kLossWarps * TOK) {
+      float d[TOK][N];
+      bool on[TOK];
+      int32_t id[TOK];
+      float wj[TOK], dj[TOK];
+#pragma unroll
+      for (int u = 0; u < TOK; ++u) {
+        const int64_t tu = t + u * kLossWarps;
+        const bool there = tu < end;
+        on[u] = there && lossy && (!a.token_mask || a.token_mask[tu]);
+        if (on[u]) Row<VEC, N>::load(a.logits + tu * E, E, lane, d[u], -INFINITY);
+        id[u] = -1;
+        wj[u] = dj[u] = 0.f;
+        if (w && there && lane < k) {
+          id[u] = a.topk_ids[tu * k + lane];
+          wj[u] = w[tu * k + lane];
+          dj[u] = dw[tu * k + lane];
         }
+      }
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-          const int32_t e = lane + 32 * i;
-          g[i] = e < E && f != 0.f ? f * (float)a.counts[(int64_t)s * E + e] : 0.f;
+      for (int u = 0; u < TOK; ++u) {
+        const int64_t tu = t + u * kLossWarps;
+        if (tu >= end) break;
+        if (on[u]) {
+          float g[N];
+          softmax_row<VEC, N>(a.bias ? s_bias : nullptr, E, lane, d[u]);
+          Row<VEC, N>::load(s_g, E, lane, g, 0.f);
+          float mean = 0.f;
+#pragma unroll
+          for (int i = 0; i < N; ++i) mean = fmaf(g[i], d[u][i], mean);
+          mean = warp_add(mean);
+#pragma unroll
+          for (int i = 0; i < N; ++i) d[u][i] *= g[i] - mean;
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) d[u][i] = 0.f;
         }
+        if (w) {
+          const float dz = wj[u] * (dj[u] - warp_add(wj[u] * dj[u]));
+          const bool in = id[u] >= 0 && id[u] < E;
+          const uint32_t same = __match_any_sync(0xffffffffu, in ? id[u] : -1 - lane);
+          if (__any_sync(0xffffffffu, __popc(same) > 1)) {  // an expert picked twice: one lane after the other
+            for (int j = 0; j < k; ++j) {
+              if (lane == j && in) pick[id[u]] += dz;
+              __syncwarp();
+            }
+          } else if (in) {
+            pick[id[u]] = dz;
+          }
+          __syncwarp();
+          float v[N];
+          Row<VEC, N>::load(pick, E, lane, v, 0.f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) d[u][i] += v[i];
+          __syncwarp();
+          if (in) pick[id[u]] = 0.f;
+          __syncwarp();
+        }
+        Row<VEC, N>::store(d_logits + tu * E, E, lane, d[u]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += d[u][i];
       }
-      token_softmax<SLOTS>(a, t, lane, d);
-      float mean = 0.f;
-#pragma unroll
-      for (int i = 0; i < SLOTS; ++i) mean = fmaf(g[i], d[i], mean);
-      mean = warp_add(mean);
-#pragma unroll
-      for (int i = 0; i < SLOTS; ++i) d[i] *= g[i] - mean;
     }
-    if (w) {
-      int32_t id = -1;
-      float dz = 0.f, wj = 0.f, dj = 0.f;
-      if (lane < k) {
-        id = a.topk_ids[t * k + lane];
-        wj = w[t * k + lane];
-        dj = dw[t * k + lane];
-      }
-      dz = wj * (dj - warp_add(wj * dj));
-      for (int j = 0; j < k; ++j) {
-        const int32_t e = __shfl_sync(0xffffffffu, id, j);
-        const float z = __shfl_sync(0xffffffffu, dz, j);
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i)
-          if (e == lane + 32 * i) d[i] += z;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-      const int32_t e = lane + 32 * i;
-      if (e < E) d_logits[t * E + e] = d[i];
-      acc[i] += d[i];
-    }
+    at = end;
   }
   if (!sums) return;
-#pragma unroll
-  for (int i = 0; i < SLOTS; ++i)
-    if (lane + 32 * i < E) sm[warp * E + lane + 32 * i] = acc[i];
   __syncthreads();
-  for (int32_t e = threadIdx.x; e < E; e += blockDim.x) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kLossWarps; ++i) v += sm[i * E + e];
-    sums[(int64_t)blockIdx.x * E + e] = v;
-  }
+  Row<VEC, N>::store(pick, E, lane, acc);
+  __syncthreads();
+  for (int32_t e = threadIdx.x; e < E; e += kLossThreads) sums[(int64_t)blockIdx.x * E + e] = column(sm, pitch, e);
 }
 
-// out[e] = sum of sums[b][e], b in order within each of 8 warps, warps in order.
-__global__ void __launch_bounds__(256)
+// out[e] = sum of sums[b][e], b in order within each of 32 warps, warps in order.
+constexpr int kBiasWarps = 32;
+__global__ void __launch_bounds__(32 * kBiasWarps)
     router_bias_kernel(const float* __restrict__ sums, int32_t blocks, int32_t E, float* __restrict__ out) {
-  __shared__ float part[8][32];
+  __shared__ float part[kBiasWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t e = blockIdx.x * 32 + lane;
+  pdl_wait();
   float v = 0.f;
-  if (e < E)
-    for (int32_t b = warp; b < blocks; b += 8) v += sums[(int64_t)b * E + e];
+  if (e < E) {
+#pragma unroll 8
+    for (int32_t b = warp; b < blocks; b += kBiasWarps) v += sums[(int64_t)b * E + e];
+  }
   part[warp][lane] = v;
   __syncthreads();
   if (warp || e >= E) return;
   v = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v += part[i][lane];
+  for (int i = 0; i < kBiasWarps; ++i) v += part[i][lane];
   out[e] = v;
 }
 
@@ -302,83 +477,85 @@ int32_t loss_per_block(int32_t n) {
   return std::max(1, (int32_t)(((int64_t)n + blocks - 1) / blocks));
 }
 
-template <int SLOTS>
-cudaError_t balance_t(const moe_router_args& a, const LossSpace& ws, cudaStream_t s) {
-  const size_t smem = (size_t)(kLossWarps + 1) * a.n_experts * sizeof(float);
-  balance_partial_kernel<SLOTS><<<router_loss_blocks(a.n), kLossWarps * 32, smem, s>>>(a, ws, loss_per_block(a.n));
+size_t loss_smem(int32_t E) { return (size_t)(kLossWarps + 2) * row_pitch(E) * sizeof(float); }
+
+template <bool VEC, int N>
+cudaError_t balance_t(const moe_router_args& a, const LossSpace& ws, float* prob_sums, float* loss, cudaStream_t s) {
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = raise_smem_limit(balance_kernel<VEC, N>, 80 * 1024, configured);
+  if (e != cudaSuccess) return e;
+  balance_kernel<VEC, N><<<router_loss_blocks(a.n), kLossThreads, loss_smem(a.n_experts), s>>>(
+      a, ws, loss_per_block(a.n), prob_sums, loss);
   return cudaGetLastError();
 }
 
-template <int SLOTS>
+template <bool VEC, int N>
 cudaError_t router_backward_t(const moe_router_args& a, const float* w, const float* dw, const float* d_loss,
                               float* d_logits, float* sums, cudaStream_t s) {
-  const size_t smem = sums ? (size_t)kLossWarps * a.n_experts * sizeof(float) : 0;
-  router_backward_kernel<SLOTS><<<router_loss_blocks(a.n), kLossWarps * 32, smem, s>>>(a, w, dw, d_loss, d_logits, sums,
-                                                                                       loss_per_block(a.n));
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = raise_smem_limit(router_backward_kernel<VEC, N>, 80 * 1024, configured);
+  if (e != cudaSuccess) return e;
+  router_backward_kernel<VEC, N><<<router_loss_blocks(a.n), kLossThreads, loss_smem(a.n_experts), s>>>(
+      a, w, dw, d_loss, d_logits, sums, loss_per_block(a.n));
   return cudaGetLastError();
 }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
 int32_t router_loss_blocks(int32_t n) {
-  return std::max(1, (int32_t)std::min<int64_t>(kRouterLossBlocks, ((int64_t)n + kLossWarps - 1) / kLossWarps));
+  if (n <= kLossOneBlock) return 1;
+  return (int32_t)std::min<int64_t>(kRouterLossBlocks, ((int64_t)n + kLossWarps - 1) / kLossWarps);
 }
 
 size_t router_loss_workspace(int32_t n, int32_t E, int32_t S) {
   const int64_t slots = router_loss_blocks(n) + (int64_t)S;
-  return (size_t)(2 * round4(slots * E) + round4(slots) + round4(S)) * 4;
+  return (size_t)(2 * round4(slots * E) + round4(slots) + round4(S) + 4) * 4;
 }
 
 cudaError_t launch_balance_loss(const moe_router_args& a, float* prob_sums, float* loss, void* workspace,
                                 cudaStream_t s) {
   const LossSpace ws = loss_space(workspace, a.n, a.n_experts, a.n_seqs);
   const int32_t E = a.n_experts;
-  if (a.n > 0) {
-    cudaError_t e;
-    if (E <= 32)
-      e = balance_t<1>(a, ws, s);
-    else if (E <= 64)
-      e = balance_t<2>(a, ws, s);
-    else if (E <= 128)
-      e = balance_t<4>(a, ws, s);
-    else if (E <= 256)
-      e = balance_t<8>(a, ws, s);
-    else if (E <= 512)
-      e = balance_t<16>(a, ws, s);
-    else
-      e = balance_t<32>(a, ws, s);
-    if (e != cudaSuccess) return e;
-  }
-  balance_join_kernel<<<(unsigned)a.n_seqs, kJoinThreads, 0, s>>>(a, ws, loss_per_block(a.n), prob_sums);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  balance_loss_kernel<<<1, 32, 0, s>>>(a, ws, loss);
-  return cudaGetLastError();
+  const bool vec = E % 4 == 0 && aligned16(a.logits);
+  cudaError_t e;
+  if (E <= 128)
+    e = vec ? balance_t<true, 4>(a, ws, prob_sums, loss, s) : balance_t<false, 4>(a, ws, prob_sums, loss, s);
+  else if (E <= 256)
+    e = vec ? balance_t<true, 8>(a, ws, prob_sums, loss, s) : balance_t<false, 8>(a, ws, prob_sums, loss, s);
+  else if (E <= 512)
+    e = vec ? balance_t<true, 16>(a, ws, prob_sums, loss, s) : balance_t<false, 16>(a, ws, prob_sums, loss, s);
+  else
+    e = vec ? balance_t<true, 32>(a, ws, prob_sums, loss, s) : balance_t<false, 32>(a, ws, prob_sums, loss, s);
+  if (e != cudaSuccess || router_loss_blocks(a.n) == 1) return e;
+  int32_t cols = 32;
+  while (cols < E && cols < kJoinThreads) cols *= 2;
+  return launch_ex(balance_join_kernel, dim3((unsigned)a.n_seqs), dim3(kJoinThreads), 0, s, true, a, ws,
+                   loss_per_block(a.n), cols, prob_sums, loss);
 }
 
 cudaError_t launch_router_backward(const moe_router_args& a, const float* w, const float* dw, const float* d_loss,
                                    float* d_logits, float* d_bias, void* workspace, cudaStream_t s) {
-  float* sums = d_bias ? static_cast<float*>(workspace) : nullptr;
-  const int32_t E = a.n_experts;
-  if (a.n > 0) {
-    cudaError_t e;
-    if (E <= 32)
-      e = router_backward_t<1>(a, w, dw, d_loss, d_logits, sums, s);
-    else if (E <= 64)
-      e = router_backward_t<2>(a, w, dw, d_loss, d_logits, sums, s);
-    else if (E <= 128)
-      e = router_backward_t<4>(a, w, dw, d_loss, d_logits, sums, s);
-    else if (E <= 256)
-      e = router_backward_t<8>(a, w, dw, d_loss, d_logits, sums, s);
-    else if (E <= 512)
-      e = router_backward_t<16>(a, w, dw, d_loss, d_logits, sums, s);
-    else
-      e = router_backward_t<32>(a, w, dw, d_loss, d_logits, sums, s);
-    if (e != cudaSuccess) return e;
-  }
-  if (!d_bias) return cudaSuccess;
-  router_bias_kernel<<<(unsigned)((E + 31) / 32), 256, 0, s>>>(sums, a.n > 0 ? router_loss_blocks(a.n) : 0, E, d_bias);
-  return cudaGetLastError();
+  const int32_t E = a.n_experts, blocks = router_loss_blocks(a.n);
+  float* sums = !d_bias ? nullptr : blocks == 1 ? d_bias : static_cast<float*>(workspace);
+  const bool vec = E % 4 == 0 && aligned16(a.logits) && aligned16(d_logits);
+  cudaError_t e;
+  if (E <= 128)
+    e = vec ? router_backward_t<true, 4>(a, w, dw, d_loss, d_logits, sums, s)
+            : router_backward_t<false, 4>(a, w, dw, d_loss, d_logits, sums, s);
+  else if (E <= 256)
+    e = vec ? router_backward_t<true, 8>(a, w, dw, d_loss, d_logits, sums, s)
+            : router_backward_t<false, 8>(a, w, dw, d_loss, d_logits, sums, s);
+  else if (E <= 512)
+    e = vec ? router_backward_t<true, 16>(a, w, dw, d_loss, d_logits, sums, s)
+            : router_backward_t<false, 16>(a, w, dw, d_loss, d_logits, sums, s);
+  else
+    e = vec ? router_backward_t<true, 32>(a, w, dw, d_loss, d_logits, sums, s)
+            : router_backward_t<false, 32>(a, w, dw, d_loss, d_logits, sums, s);
+  if (e != cudaSuccess || !d_bias || blocks == 1) return e;
+  return launch_ex(router_bias_kernel, dim3((unsigned)((E + 31) / 32)), dim3(32 * kBiasWarps), 0, s, true,
+                   (const float*)sums, blocks, E, d_bias);
 }
 
 }  // namespace moe
