@@ -279,18 +279,18 @@ GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 MAX_HIDDEN, MAX_EXPERTS, MAX_TOP_K = 8192, 1024, 32
 
 
-_torch = _BF16 = _F32 = _I32 = _U8 = _KINDS = _raw_stream = _current_device = None
+_torch = _BF16 = _F32 = _I32 = _U8 = _BOOL = _KINDS = _raw_stream = _current_device = None
 
 
 def _ready():
     """The loaded library; on first use also binds what the calls below take from torch (a call checks and packs in a
     few microseconds, so it looks nothing up by name)."""
-    global _torch, _BF16, _F32, _I32, _U8, _KINDS, _raw_stream, _current_device
+    global _torch, _BF16, _F32, _I32, _U8, _BOOL, _KINDS, _raw_stream, _current_device
     if _torch is None:
         import torch
 
         load()
-        _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        _BF16, _F32, _I32, _U8, _BOOL = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.bool
         _KINDS = (_BF16, _F32)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -500,12 +500,10 @@ def _router_pack(where, logits, bias, topk_ids, counts, tokens, coef, mask, seq_
         S = seq_offsets.shape[0] - 1 if seq_offsets.dim() == 1 else 0
         if S < 1:
             _refuse(where, "seq_offsets holds no sequence")
-    if mask is not None and mask.dtype is _torch.bool:
-        mask = mask.view(_U8)
     args = _ROUTER_ARGS.pack(
         n, E, k, S, coef, _array(logits, where, "logits", _F32, device, shape),
         _array(bias, where, "bias", _F32, device, (E,)), _array(topk_ids, where, "topk_ids", _I32, device, (n, k)),
-        _array(mask, where, "mask", _U8, device, (n,)),
+        0 if mask is None else _array(mask, where, "mask", _BOOL if mask.dtype is _BOOL else _U8, device, (n,)),
         _array(seq_offsets, where, "seq_offsets", _I32, device, (S + 1,)),
         _array(counts, where, "counts", _I32, device, (S, E)), _array(tokens, where, "tokens", _I32, device, (S + 1,)))
     return n, E, k, S, device, args

@@ -78,7 +78,8 @@ moe_status moe_block_norm(const moe_block_norm_args* args, moe_stream_t stream) 
 
 size_t moe_block_norm_workspace_bytes(int32_t n, int32_t hidden) {
   if (n < 0 || hidden <= 0) return 0;
-  return (size_t)block_norm_backward_groups(n) * 2 * (size_t)hidden * sizeof(float);
+  if (hidden > kNormMaxHidden) return 0;
+  return (size_t)block_norm_backward_slots(n, hidden) * 2 * (size_t)hidden * sizeof(float);
 }
 
 moe_status moe_block_norm_backward(const moe_block_norm_args* args, const moe_block_norm_grads* grads, void* workspace,

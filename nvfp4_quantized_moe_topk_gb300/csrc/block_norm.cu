@@ -5,16 +5,16 @@
 //   u = alpha r + beta g z
 //   x = u ru (o + w_pre)      ru = (mean u^2 + eps)^-1/2
 //
-// Each row is read once: a group of threads holds one row in registers (8
+// Each row is read once: a CTA holds one row in registers (8
 // consecutive channels a thread, one or two such vectors), so the second
 // norm's statistics come from the values that the first one left there.
 // Memory bounds it: per element the residual in and out, the branch and x.
 //
-// Batches of several rows per CTA run persistent groups, each over rows
-// b, b + groups, ...: a thread copies its own vectors of the next rows into
-// shared memory by asynchronous copies while it works on the current one and
-// reads back only what it copied itself, so the copies need no barrier and no
-// registers; the weights stay in registers over all rows.
+// Batches of several rows per CTA run persistent CTAs, each over rows b, b +
+// CTAs, ...: a thread copies its part of the next rows into shared memory by
+// asynchronous copies while it works on the current one and reads back only
+// what its warp copied, so the copies need no barrier and no registers; the
+// weights stay in registers over all rows.
 #include "block_norm.cuh"
 
 namespace moe {
@@ -69,15 +69,15 @@ __device__ __forceinline__ float squares(const F2 (&v)[4]) {
   return s.x + s.y;
 }
 
-// One row per CTA: batches too small for the persistent groups.
+// One row per CTA: batches too small for persistent ones.
 template <typename RT, typename YT, int ITERS>
 __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormParams a) {
-  __shared__ float red[2][kNormMaxThreads / 32];
+  __shared__ float red[2][16];
   constexpr bool Q = Vec8<RT>::kVecs + Vec8<YT>::kVecs > 2;
   const int32_t t = blockIdx.x;
   const bool branch = a.branch.p != nullptr;
   F2 u[ITERS][4], z[ITERS][4], cz[ITERS][4], wx[ITERS][4];
-  float ss[1] = {0.f};
+  float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const Lane<Q> l(i, a.H);
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
     row_load<RT>(a.residual, t, l, u[i]);
     if (branch) row_load<YT>(a.branch, t, l, z[i]);
     channel_factors<kNormAny>(a, l, cz[i], wx[i]);
-    if (a.post) ss[0] += squares(z[i]);
+    if (a.post) ss += squares(z[i]);
     if (a.gate_kind == MOE_GATE_FULL) {
       F2 g[4];
       row_load<YT>(a.gate, t, l, g);
@@ -98,12 +98,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
     if (a.gate_sigmoid) f = sigmoid(f);
   }
   if (a.post) {
-    group_sums<1>(ss, red[0]);
-    const float rp = rsqrtf(fmaf(ss[0], a.inv_h, a.eps));
+    ss = cta_sum(ss, red[0]);
+    const float rp = rsqrtf(fmaf(ss, a.inv_h, a.eps));
     if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rp;
     f *= rp;
   }
-  ss[0] = 0.f;
+  ss = 0.f;
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const Lane<Q> l(i, a.H);
@@ -113,12 +113,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
       u[i][j] = mul2(u[i][j], f2(a.alpha));
       if (branch) u[i][j] = fma2(cz[i][j], mul2(f2(f), z[i][j]), u[i][j]);
     }
-    ss[0] += squares(u[i]);
+    ss += squares(u[i]);
     if (a.residual_out.p) row_store<RT>(a.residual_out, t, l, u[i]);
   }
   if (!a.pre) return;
-  group_sums<1>(ss, red[1]);
-  const float ru = rsqrtf(fmaf(ss[0], a.inv_h, a.eps));
+  ss = cta_sum(ss, red[1]);
+  const float ru = rsqrtf(fmaf(ss, a.inv_h, a.eps));
   if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = ru;
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
@@ -130,32 +130,29 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
   }
 }
 
-// The same for a persistent group of blockDim.x threads (threadIdx.y: which of
-// the CTA's groups) over rows blockIdx.x * groups + threadIdx.y, + all groups, ...
+// The same for persistent CTAs over rows blockIdx.x, + gridDim.x, ...
 template <typename RT, typename YT, int ITERS, int MODE>
 __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
     block_norm_rows_kernel(const NormParams a, int32_t stages, int32_t stage_vecs) {
   extern __shared__ __align__(16) char ring[];
-  __shared__ float red[kNormMaxGroups][4][kNormMaxThreads / 32];
+  __shared__ float red[4][16];
   constexpr int kR = Vec8<RT>::kVecs, kY = Vec8<YT>::kVecs;
   constexpr bool Q = kR + kY > 2;
   const bool branch = MODE != kNormAny || a.branch.p != nullptr;
   const bool post = MODE != kNormAny || a.post != nullptr, pre = MODE != kNormAny || a.pre != nullptr;
   const bool full = MODE == kNormAny ? a.gate_kind == MOE_GATE_FULL : MODE == kNormFull;
   const bool token = (MODE == kNormAny || MODE == kNormScalar) && a.gate_kind == MOE_GATE_TOKEN;
-  const uint32_t pitch = blockDim.x * blockDim.y * 16;
-  const uint32_t mine = smem_u32(ring) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+  const uint32_t pitch = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
   const uint32_t iter_bytes = stage_vecs / ITERS * pitch, stage_bytes = stage_vecs * pitch;
-  const int32_t step = gridDim.x * blockDim.y, t0 = blockIdx.x * blockDim.y + threadIdx.y;
+  const uint32_t n = a.n, step = gridDim.x;
   F2 cz[ITERS][4], wx[ITERS][4];
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const Lane<Q> l(i, a.H);
     if (l.ok0) channel_factors<MODE>(a, l, cz[i], wx[i]);
   }
-  auto fetch = [&](int64_t t64, int stage) {
-    if (t64 < a.n) {
-      const int32_t t = (int32_t)t64;
+  auto fetch = [&](uint32_t t, int stage) {
+    if (t < n) {
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
@@ -167,40 +164,39 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
     cp_async_commit();  // one group a row, empty past the end
   };
   // a token's gate is loaded one row ahead
-  auto token_gate = [&](int64_t t64) {
-    return token && t64 < a.n ? reinterpret_cast<const float*>(a.gate.p)[t64] : 1.f;
+  auto token_gate = [&](uint32_t t) {
+    return token && t < n ? reinterpret_cast<const float*>(a.gate.p)[t] : 1.f;
   };
-  for (int s = 0; s + 1 < stages; ++s) fetch((int64_t)t0 + (int64_t)s * step, s);
-  float next_gate = token_gate(t0);
+  for (int s = 0; s + 1 < stages; ++s) fetch(blockIdx.x + s * step, s);
+  float next_gate = token_gate(blockIdx.x);
   int stage = 0, buf = 0;
-  for (int64_t t64 = t0; t64 < a.n; t64 += step, stage = stage + 1 == stages ? 0 : stage + 1, buf ^= 2) {
-    const int32_t t = (int32_t)t64;
+  for (uint32_t t = blockIdx.x; t < n; t += step, stage = stage + 1 == stages ? 0 : stage + 1, buf ^= 2) {
     __syncwarp();  // the warp has read the slot that is filled next
-    fetch(t64 + (int64_t)(stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    fetch(t + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
     float f = next_gate;
-    next_gate = token_gate(t64 + step);
+    next_gate = token_gate(t + step);
     if (token && a.gate_sigmoid) f = sigmoid(f);
     cp_async_wait(stages - 1);
     __syncwarp();
     const uint32_t at = mine + stage * stage_bytes;
     F2 u[ITERS][4], z[ITERS][4];
-    float ss[1] = {0.f};
+    float ss = 0.f;
     if (branch) {
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const Lane<Q> l(i, a.H);
         if (!l.ok0) continue;
         ring_read<YT>(at + i * iter_bytes + kR * pitch, pitch, l, z[i]);
-        ss[0] += squares(z[i]);
+        ss += squares(z[i]);
       }
     }
     if (post) {
-      group_sums<1>(ss, red[threadIdx.y][buf]);
-      const float rp = rsqrtf(fmaf(ss[0], a.inv_h, a.eps));
+      ss = cta_sum(ss, red[buf]);
+      const float rp = rsqrtf(fmaf(ss, a.inv_h, a.eps));
       if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rp;
       f *= rp;
     }
-    ss[0] = 0.f;
+    ss = 0.f;
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
       const Lane<Q> l(i, a.H);
@@ -216,12 +212,12 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
         u[i][j] = mul2(u[i][j], f2(a.alpha));
         if (branch) u[i][j] = fma2(cz[i][j], mul2(f2(f), z[i][j]), u[i][j]);
       }
-      ss[0] += squares(u[i]);
+      ss += squares(u[i]);
       if (a.residual_out.p) row_store<RT>(a.residual_out, t, l, u[i]);
     }
     if (!pre) continue;
-    group_sums<1>(ss, red[threadIdx.y][buf + 1]);
-    const float ru = rsqrtf(fmaf(ss[0], a.inv_h, a.eps));
+    ss = cta_sum(ss, red[buf + 1]);
+    const float ru = rsqrtf(fmaf(ss, a.inv_h, a.eps));
     if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = ru;
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
@@ -242,7 +238,7 @@ cudaError_t norm_rows(const NormParams& a, cudaStream_t s) {
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = raise_smem_limit(block_norm_rows_kernel<RT, YT, ITERS, MODE>, kNormSmem, configured);
   if (e != cudaSuccess) return e;
-  block_norm_rows_kernel<RT, YT, ITERS, MODE><<<p.ctas, p.block, p.smem, s>>>(a, p.stages, vecs);
+  block_norm_rows_kernel<RT, YT, ITERS, MODE><<<p.ctas, p.threads, p.smem, s>>>(a, p.stages, vecs);
   return cudaGetLastError();
 }
 

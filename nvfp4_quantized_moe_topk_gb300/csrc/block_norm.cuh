@@ -13,7 +13,6 @@
 namespace moe {
 
 constexpr int kNormMaxThreads = 512;
-constexpr int kNormMaxGroups = 8;  // rows side by side in a CTA
 constexpr int kNormSmem = 220 * 1024;
 
 // What a kernel knows at compile time.  kNormAny: nothing.  The others: branch,
@@ -194,8 +193,8 @@ __device__ __forceinline__ void row_store(const NormRows& r, int32_t t, const La
   char* row = r.at(t, 0);
   if constexpr (Vec8<T>::kVecs == 1 && !QUADS) {
     *reinterpret_cast<uint4*>(row + (uint32_t)l.c0 * 2u) =
-        make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
-                   pack_bf16x2(v[3].x, v[3].y));
+        make_uint4(pack2(v[0].x, v[0].y), pack2(v[1].x, v[1].y), pack2(v[2].x, v[2].y),
+                   pack2(v[3].x, v[3].y));
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -203,7 +202,7 @@ __device__ __forceinline__ void row_store(const NormRows& r, int32_t t, const La
       const uint32_t c = (uint32_t)(l.c0 + h * Lane<QUADS>::kNext);
       if constexpr (Vec8<T>::kVecs == 1)
         *reinterpret_cast<uint2*>(row + c * 2u) =
-            make_uint2(pack_bf16x2(v[2 * h].x, v[2 * h].y), pack_bf16x2(v[2 * h + 1].x, v[2 * h + 1].y));
+            make_uint2(pack2(v[2 * h].x, v[2 * h].y), pack2(v[2 * h + 1].x, v[2 * h + 1].y));
       else
         *reinterpret_cast<float4*>(row + c * 4u) = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
     }
@@ -232,35 +231,46 @@ __device__ __forceinline__ void sigmoid2(F2 (&v)[4]) {
   for (int j = 0; j < 4; ++j) v[j] = {sigmoid(v[j].x), sigmoid(v[j].y)};
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+__device__ __forceinline__ float shfl_xor(float v, int lanes) { return __shfl_xor_sync(0xffffffffu, v, lanes); }
+
+// Sum of a value over the CTA, in a fixed order, by one barrier; red is this
+// reduction's own 16 floats of shared memory.
+__device__ __forceinline__ float cta_sum(float v, float* red) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  for (int off = 16; off > 0; off >>= 1) v += shfl_xor(v, off);
+  if (warps == 1) return v;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = (lane & 15) < warps ? red[lane & 15] : 0.f;
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) v += shfl_xor(v, off);
   return v;
 }
-
-// Sums of N values over a group of blockDim.x threads (threadIdx.y: which), in
-// a fixed order, by one barrier; red is this reduction's own [N][warps] floats
-// of shared memory.
-template <int N>
-__device__ __forceinline__ void group_sums(float (&v)[N], float* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+// Of three values at once: the first two steps halve what a lane carries (the
+// quarters of the warp end up with one value each), red has 64 floats.
+__device__ __forceinline__ void cta_sums3(float& a, float& b, float& c, float* red) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const bool upper = lane & 16, odd = lane & 8;
+  float x = upper ? b : a, y = upper ? 0.f : c;  // kept: (a, c) below, (b, -) above
+  x += shfl_xor(upper ? a : b, 16);
+  y += shfl_xor(upper ? c : 0.f, 16);
+  float v = odd ? y : x;  // quarters: a, c, b, -
+  v += shfl_xor(odd ? x : y, 8);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[i * warps + warp] = v[i];
-  }
-  if (blockDim.y == 1)
+  for (int off = 4; off > 0; off >>= 1) v += shfl_xor(v, off);
+  if (warps > 1) {
+    if ((lane & 7) == 0) red[(lane >> 3) * 16 + (threadIdx.x >> 5)] = v;
     __syncthreads();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+    const int w = lane & 7;
+    const float* mine = red + (lane >> 3) * 16;
+    v = (w < warps ? mine[w] : 0.f) + (w + 8 < warps ? mine[w + 8] : 0.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {  // at most 16 warps: four steps join them
-    v[i] = (lane & 15) < warps ? red[i * warps + (lane & 15)] : 0.f;
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    for (int off = 4; off > 0; off >>= 1) v += shfl_xor(v, off);
   }
+  a = __shfl_sync(0xffffffffu, v, 0);
+  c = __shfl_sync(0xffffffffu, v, 8);
+  b = __shfl_sync(0xffffffffu, v, 16);
 }
 
 inline int norm_sms() {
@@ -270,23 +280,21 @@ inline int norm_sms() {
   return sms > 0 ? sms : 1;
 }
 
-// Shape of a persistent launch: threads x groups a CTA, ring stages (4, or 2
-// where two CTAs of 4 stages do not fit an SM, or 1 where two do not), CTAs of
-// about `sm_threads` threads an SM.
+// Shape of a persistent launch: ring stages (4, or 2 where two CTAs of 4
+// stages do not fit an SM, or 1 where two do not), CTAs of about `sm_threads`
+// threads an SM.
 struct NormPlan {
-  dim3 block;
-  int stages, smem, ctas;
+  int threads, stages, smem, ctas;
 };
+constexpr int kNormMaxPerSm = 24;
 inline NormPlan norm_plan(int32_t n, int32_t hidden, int stage_vecs, int sm_threads) {
   NormPlan p;
-  const int threads = norm_threads(hidden);
-  const int groups = std::max(1, std::min(kNormMaxGroups, 256 / threads));
-  p.block = dim3(threads, groups);
-  const int stage = stage_vecs * threads * groups * 16;
+  p.threads = norm_threads(hidden);
+  const int stage = stage_vecs * p.threads * 16;
   p.stages = 2 * 4 * stage <= kNormSmem ? 4 : 2 * stage <= kNormSmem ? 2 : 1;
   p.smem = p.stages * stage;
-  const int per_sm = std::max(1, std::min({sm_threads / (threads * groups), kNormSmem / p.smem, 8}));
-  p.ctas = (int)std::min<int64_t>(((int64_t)n + groups - 1) / groups, (int64_t)norm_sms() * per_sm);
+  const int per_sm = std::max(1, std::min({sm_threads / p.threads, kNormSmem / (p.smem + 1024), kNormMaxPerSm}));
+  p.ctas = (int)std::min<int64_t>(n, (int64_t)norm_sms() * per_sm);
   return p;
 }
 

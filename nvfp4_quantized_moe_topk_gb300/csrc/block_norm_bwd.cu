@@ -13,10 +13,10 @@
 //   d_pre_weight is the first, d_post_weight = beta g S, d_gate = beta w' S.
 //
 // Memory bounds it: two gradients, u and y in, two gradients out.  Persistent
-// groups of threads and rings in shared memory as in the forward pass.  A
+// CTAs and rings in shared memory as in the forward pass.  A
 // row's vectors are read twice from the ring, before and after the reduction,
 // which is cheaper than holding them in registers beside the channels' sums.
-// Each group writes its sums, and column_sum_kernel joins them in a fixed order.
+// Each CTA writes its sums, and column_sum_kernel joins them in a fixed order.
 #include "block_norm.cuh"
 
 namespace moe {
@@ -33,17 +33,17 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
     block_norm_backward_kernel(const NormParams a, const NormGrads d, float* __restrict__ part, int32_t stages,
                                int32_t stage_vecs) {
   extern __shared__ __align__(16) char ring[];
-  __shared__ float red[kNormMaxGroups][2][3 * (kNormMaxThreads / 32)];
+  __shared__ float red[2][64];
   const bool branch = MODE != kNormAny || a.branch.p != nullptr;
   const bool post = MODE != kNormAny || a.post != nullptr, pre = MODE != kNormAny || (a.pre && d.dx.p);
   const bool full = MODE == kNormAny ? a.gate_kind == MOE_GATE_FULL : MODE == kNormFull;
   const bool channel = MODE == kNormAny ? a.gate_kind == MOE_GATE_CHANNEL : MODE == kNormChannel;
   const bool token = (MODE == kNormAny || MODE == kNormScalar) && a.gate_kind == MOE_GATE_TOKEN;
-  const uint32_t pitch = blockDim.x * blockDim.y * 16;
-  const uint32_t mine = smem_u32(ring) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+  const uint32_t pitch = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
   const uint32_t iter_bytes = stage_vecs / ITERS * pitch, stage_bytes = stage_vecs * pitch;
-  const int32_t step = gridDim.x * blockDim.y, t0 = blockIdx.x * blockDim.y + threadIdx.y;
+  const uint32_t n = a.n, step = gridDim.x;
   constexpr bool Q = Vec8<RT>::kVecs + Vec8<YT>::kVecs > 2;
+  pdl_launch_dependents();
   F2 acc_pre[ITERS][4] = {}, acc_post[ITERS][4] = {};
   F2 wx[ITERS][4], c[ITERS][4];  // o + w_pre; beta g (o + w_post), without a full gate
 #pragma unroll
@@ -76,9 +76,8 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
   // ring order: d_residual_out, residual_out, d_x, branch, full gate
   constexpr int kR = Vec8<RT>::kVecs, kY = Vec8<YT>::kVecs;
   constexpr uint32_t kU = kR, kDx = 2 * kR, kB = kDx + 1, kG = kB + kY;
-  auto fetch = [&](int64_t t64, int stage) {
-    if (t64 < a.n) {
-      const int32_t t = (int32_t)t64;
+  auto fetch = [&](uint32_t t, int stage) {
+    if (t < n) {
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
@@ -95,22 +94,21 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
   };
   // the row's scalars are loaded one row ahead
   float next_ru = 0.f, next_rp = 1.f, next_gate = 1.f;
-  auto scalars = [&](int64_t t64) {
-    if (t64 >= a.n) return;
-    if (pre) next_ru = a.rstd_pre[t64];
-    if (post) next_rp = a.rstd_post[t64];
-    if (token) next_gate = reinterpret_cast<const float*>(a.gate.p)[t64];
+  auto scalars = [&](uint32_t t) {
+    if (t >= n) return;
+    if (pre) next_ru = a.rstd_pre[t];
+    if (post) next_rp = a.rstd_post[t];
+    if (token) next_gate = reinterpret_cast<const float*>(a.gate.p)[t];
   };
-  for (int s = 0; s + 1 < stages; ++s) fetch((int64_t)t0 + (int64_t)s * step, s);
-  scalars(t0);
+  for (int s = 0; s + 1 < stages; ++s) fetch(blockIdx.x + s * step, s);
+  scalars(blockIdx.x);
   int stage = 0, buf = 0;
-  for (int64_t t64 = t0; t64 < a.n; t64 += step, stage = stage + 1 == stages ? 0 : stage + 1, buf ^= 1) {
-    const int32_t t = (int32_t)t64;
+  for (uint32_t t = blockIdx.x; t < n; t += step, stage = stage + 1 == stages ? 0 : stage + 1, buf ^= 1) {
     __syncwarp();  // the warp has read the slot that is filled next
-    fetch(t64 + (int64_t)(stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    fetch(t + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
     const float ru = next_ru, rp = next_rp;
     const float gt = token && a.gate_sigmoid ? sigmoid(next_gate) : next_gate;
-    scalars(t64 + step);
+    scalars(t + step);
     cp_async_wait(stages - 1);
     __syncwarp();
     const uint32_t at = mine + stage * stage_bytes;
@@ -156,7 +154,7 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
       }
     }
     float s[3] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y};
-    group_sums<3>(s, red[threadIdx.y][buf]);
+    cta_sums3(s[0], s[1], s[2], red[buf]);
     const float m1 = ru * ru * ru * (s[0] * a.inv_h);
     const float T = rp * (s[1] - s[2] * m1);  // sum(c y rp G)
     if (token && d.d_gate.p && threadIdx.x == 0)
@@ -191,22 +189,22 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
       if (full && d.d_gate.p) row_store<YT>(d.d_gate, t, l, u);
     }
   }
-  // part[group][0..1][H]
+  // part[CTA][0..1][H]
   const NormRows own = {reinterpret_cast<char*>(part), a.H / 4};
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const Lane<Q> l(i, a.H);
     if (!l.ok0) continue;
-    if (d.d_pre) row_store<float>(own, 2 * t0, l, acc_pre[i]);
-    if (d.d_post || channel) row_store<float>(own, 2 * t0 + 1, l, acc_post[i]);
+    if (d.d_pre) row_store<float>(own, 2 * blockIdx.x, l, acc_pre[i]);
+    if (d.d_post || channel) row_store<float>(own, 2 * blockIdx.x + 1, l, acc_post[i]);
   }
 }
 
-// Joins the groups' sums: warp w of a 32-column CTA adds groups w, w + warps,
+// Joins the CTAs' sums: warp w of a 32-column CTA adds CTAs w, w + warps,
 // ... and warp 0 the warps in order.
 constexpr int kColWarps = 16;
 __global__ void __launch_bounds__(32 * kColWarps)
-    column_sum_kernel(const NormParams a, const NormGrads d, const float* __restrict__ part, int32_t groups) {
+    column_sum_kernel(const NormParams a, const NormGrads d, const float* __restrict__ part, int32_t ctas) {
   __shared__ float sum[kColWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, H = a.H;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
@@ -214,8 +212,11 @@ __global__ void __launch_bounds__(32 * kColWarps)
   if (which == 0 ? !d.d_pre : !d.d_post && !d_gate) return;
   const int32_t c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < H)
-    for (int32_t b = warp; b < groups; b += kColWarps) v += part[((size_t)b * 2 + which) * H + c];
+  pdl_wait();
+  if (c < H) {
+#pragma unroll 8
+    for (int32_t b = warp; b < ctas; b += kColWarps) v += part[((size_t)b * 2 + which) * H + c];
+  }
   sum[warp][lane] = v;
   __syncthreads();
   if (warp || c >= H) return;
@@ -245,39 +246,40 @@ __global__ void __launch_bounds__(32 * kColWarps)
 }
 
 template <typename RT, typename YT, int ITERS, int MAXT, int MODE>
-cudaError_t norm_backward_m(const NormParams& a, const NormGrads& d, float* part, int* groups, cudaStream_t s) {
+cudaError_t norm_backward_m(const NormParams& a, const NormGrads& d, float* part, int* ctas, cudaStream_t s) {
   const int vecs = ITERS * (2 * Vec8<RT>::kVecs + 1 + Vec8<YT>::kVecs * (a.gate_kind == MOE_GATE_FULL ? 2 : 1));
   NormPlan p = norm_plan(a.n, a.H, vecs, 768);
-  const int slots = block_norm_backward_groups(a.n);  // of the workspace
-  if ((int)p.block.y > slots) p.block.y = slots;
-  p.ctas = std::min(p.ctas, slots / (int)p.block.y);
-  *groups = p.ctas * (int)p.block.y;
+  p.ctas = std::min(p.ctas, block_norm_backward_slots(a.n, a.H));
+  *ctas = p.ctas;
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = raise_smem_limit(block_norm_backward_kernel<RT, YT, ITERS, MAXT, MODE>, kNormSmem, configured);
   if (e != cudaSuccess) return e;
-  block_norm_backward_kernel<RT, YT, ITERS, MAXT, MODE><<<p.ctas, p.block, p.smem, s>>>(a, d, part, p.stages, vecs);
+  block_norm_backward_kernel<RT, YT, ITERS, MAXT, MODE><<<p.ctas, p.threads, p.smem, s>>>(a, d, part, p.stages, vecs);
   return cudaGetLastError();
 }
 
 template <typename RT, typename YT, int ITERS, int MAXT>
-cudaError_t norm_backward_i(const NormParams& a, const NormGrads& d, float* part, int* groups, cudaStream_t s) {
+cudaError_t norm_backward_i(const NormParams& a, const NormGrads& d, float* part, int* ctas, cudaStream_t s) {
   if (!a.branch.p || !a.post || !a.pre || !d.dx.p)
-    return norm_backward_m<RT, YT, ITERS, MAXT, kNormAny>(a, d, part, groups, s);
-  if (a.gate_kind == MOE_GATE_CHANNEL) return norm_backward_m<RT, YT, ITERS, MAXT, kNormChannel>(a, d, part, groups, s);
-  if (a.gate_kind == MOE_GATE_FULL) return norm_backward_m<RT, YT, ITERS, MAXT, kNormFull>(a, d, part, groups, s);
-  return norm_backward_m<RT, YT, ITERS, MAXT, kNormScalar>(a, d, part, groups, s);
+    return norm_backward_m<RT, YT, ITERS, MAXT, kNormAny>(a, d, part, ctas, s);
+  if (a.gate_kind == MOE_GATE_CHANNEL) return norm_backward_m<RT, YT, ITERS, MAXT, kNormChannel>(a, d, part, ctas, s);
+  if (a.gate_kind == MOE_GATE_FULL) return norm_backward_m<RT, YT, ITERS, MAXT, kNormFull>(a, d, part, ctas, s);
+  return norm_backward_m<RT, YT, ITERS, MAXT, kNormScalar>(a, d, part, ctas, s);
 }
 
 template <typename RT, typename YT>
-cudaError_t norm_backward_t(const NormParams& a, const NormGrads& d, float* part, int* groups, cudaStream_t s) {
-  if (norm_iters(a.H) == 2) return norm_backward_i<RT, YT, 2, 512>(a, d, part, groups, s);
-  if (norm_threads(a.H) <= 384) return norm_backward_i<RT, YT, 1, 384>(a, d, part, groups, s);
-  return norm_backward_i<RT, YT, 1, 512>(a, d, part, groups, s);
+cudaError_t norm_backward_t(const NormParams& a, const NormGrads& d, float* part, int* ctas, cudaStream_t s) {
+  if (norm_iters(a.H) == 2) return norm_backward_i<RT, YT, 2, 512>(a, d, part, ctas, s);
+  if (norm_threads(a.H) <= 384) return norm_backward_i<RT, YT, 1, 384>(a, d, part, ctas, s);
+  return norm_backward_i<RT, YT, 1, 512>(a, d, part, ctas, s);
 }
 
 }  // namespace
 
-int block_norm_backward_groups(int32_t n) { return std::max(1, std::min<int32_t>(n, kNormBackwardGroups)); }
+// CTAs that the workspace has room for: those of a GPU with up to 160 SMs.
+int block_norm_backward_slots(int32_t n, int32_t hidden) {
+  return std::max(1, std::min<int32_t>(n, 160 * std::max(1, std::min(768 / norm_threads(hidden), kNormMaxPerSm))));
+}
 
 cudaError_t launch_block_norm_backward(const moe_block_norm_args& args, const moe_block_norm_grads& grads, float* part,
                                        cudaStream_t s) {
@@ -291,20 +293,20 @@ cudaError_t launch_block_norm_backward(const moe_block_norm_args& args, const mo
   d.d_gate = norm_rows(grads.d_gate, a.H, yb ? 2 : 4);
   d.d_post = grads.d_post_weight;
   d.d_pre = grads.d_pre_weight;
-  int groups = 0;
+  int ctas = 0;
   if (a.n > 0) {
     cudaError_t e;
     if (rb)
-      e = yb ? norm_backward_t<uint16_t, uint16_t>(a, d, part, &groups, s)
-             : norm_backward_t<uint16_t, float>(a, d, part, &groups, s);
+      e = yb ? norm_backward_t<uint16_t, uint16_t>(a, d, part, &ctas, s)
+             : norm_backward_t<uint16_t, float>(a, d, part, &ctas, s);
     else
-      e = yb ? norm_backward_t<float, uint16_t>(a, d, part, &groups, s)
-             : norm_backward_t<float, float>(a, d, part, &groups, s);
+      e = yb ? norm_backward_t<float, uint16_t>(a, d, part, &ctas, s)
+             : norm_backward_t<float, float>(a, d, part, &ctas, s);
     if (e != cudaSuccess) return e;
   }
   if (!d.d_pre && !d.d_post && !(a.gate_kind == MOE_GATE_CHANNEL && d.d_gate.p)) return cudaSuccess;
-  column_sum_kernel<<<dim3((a.H + 31) / 32, 2), 32 * kColWarps, 0, s>>>(a, d, part, groups);
-  return cudaGetLastError();
+  return launch_ex(column_sum_kernel, dim3((a.H + 31) / 32, 2), dim3(32 * kColWarps), 0, s, a.n > 0, a, d,
+                   (const float*)part, ctas);
 }
 
 }  // namespace moe

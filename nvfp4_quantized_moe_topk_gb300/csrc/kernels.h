@@ -224,10 +224,9 @@ cudaError_t launch_decode(const DecodeArgs& args, int num_sms, cudaStream_t s);
 // ------------------------------------------------- operators around the layer
 constexpr int kNormMaxHidden = 8192;
 constexpr int kNormDirectRows = 304;       // batches of at most this many rows take a CTA a row
-constexpr int kNormBackwardGroups = 1216;  // thread groups of the norms' backward pass, each with a slot of column sums
-int block_norm_backward_groups(int32_t n);
+int block_norm_backward_slots(int32_t n, int32_t hidden);  // CTAs of the backward pass, each with column sums of its own
 cudaError_t launch_block_norm(const moe_block_norm_args& a, cudaStream_t s);
-// part: [block_norm_backward_groups(n)][2][hidden] floats.
+// part: [block_norm_backward_slots(n, hidden)][2][hidden] floats.
 cudaError_t launch_block_norm_backward(const moe_block_norm_args& a, const moe_block_norm_grads& d, float* part,
                                        cudaStream_t s);
 

@@ -440,8 +440,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           if (!quads) {
             store8(p, r);
           } else {
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
-            if (in1) *reinterpret_cast<uint2*>(p + next) = make_uint2(pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
+            if (in1) *reinterpret_cast<uint2*>(p + next) = make_uint2(pack2(r[4], r[5]), pack2(r[6], r[7]));
           }
         }
       }

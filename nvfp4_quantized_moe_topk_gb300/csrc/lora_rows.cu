@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
         char* to = v_base + m * v_pitch + (uint32_t)(r0 / kPass) * 128 + (((lane >> 2) ^ ((m & 1) << 2)) * 16) +
                    (lane & 3) * 4;
         for (int k = 0; k < terms; ++k, to += kRowsTile * v_pitch) {  // a sum of bf16 terms, each the rounding of the rest
-          const uint32_t b = pack_bf16x2(s0, s1);
+          const uint32_t b = pack2(s0, s1);
           *reinterpret_cast<uint32_t*>(to) = b;
           s0 -= bf16lo(b);
           s1 -= bf16hi(b);
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           if (!quads) {
             store8(p, r);
           } else {
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
-            if (in1) *reinterpret_cast<uint2*>(p + next) = make_uint2(pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
+            if (in1) *reinterpret_cast<uint2*>(p + next) = make_uint2(pack2(r[4], r[5]), pack2(r[6], r[7]));
           }
         }
       }
