@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 from . import build as _build
@@ -269,155 +268,43 @@ def forward_noalloc(hidden, inter, n_experts, top_k, up_codes, up_scales, down_c
 
 
 # ---------------------------------------------------------------- operators around the layer
-# The argument structs of the C header, packed in one step (their layouts are
-# checked against the header's by a test).
-_NORM_ARGS = struct.Struct("@7i4f4xPqPqPqPPPqPqPP")
-_NORM_GRADS = struct.Struct("@PqPqPqPqPqPP")
-_ROUTER_ARGS = struct.Struct("@4if4xPPPPPPP")
-_LORA_ARGS = struct.Struct("@7i4xPPPPPPqPqPq")
-GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
-MAX_HIDDEN, MAX_EXPERTS, MAX_TOP_K = 8192, 1024, 32
+# Checked and called by the native module moe_binding (csrc/binding.cpp): the
+# smallest of these calls take a few microseconds.  Every refusal is a MoeError,
+# raised before anything is enqueued.
+_native = None
 
 
-_torch = _BF16 = _F32 = _I32 = _U8 = _BOOL = _KINDS = _raw_stream = _current_device = None
+def _binding():
+    """The native module; raises if it is not built (no fallback)."""
+    global _native
+    if _native is None:
+        import importlib.machinery
+        import importlib.util
 
-
-def _ready():
-    """The loaded library; on first use also binds what the calls below take from torch (a call checks and packs in a
-    few microseconds, so it looks nothing up by name)."""
-    global _torch, _BF16, _F32, _I32, _U8, _BOOL, _KINDS, _raw_stream, _current_device
-    if _torch is None:
-        import torch
+        import torch  # noqa: F401  (its libraries have to be loaded first)
 
         load()
-        _BF16, _F32, _I32, _U8, _BOOL = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.bool
-        _KINDS = (_BF16, _F32)
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda device: torch.cuda.current_stream(device).cuda_stream)
-        _current_device = torch.cuda.current_device
-        _torch = torch
-    return _lib
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"the binding is not built ({_build.BINDING}); run __graft_entry__.build() or "
+                               "python -m nvfp4_quantized_moe_topk_gb300.build")
+        loader = importlib.machinery.ExtensionFileLoader("moe_binding", _build.BINDING)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("moe_binding", loader))
+        loader.exec_module(module)
+        module.set_error(MoeError)
+        _native = module
+    return _native
 
 
-def _refuse(where: str, why: str):
-    raise MoeError(1, where, why)
+def _new_workspace(size: int, like=None, stream=None):
+    """size bytes on the current device; for a call on another stream than the current one, allocated on that."""
+    import torch
 
-
-def _dtype_code(t, where, name):
-    """MOE_DTYPE_ of a tensor that may be bf16 or fp32."""
-    d = t.dtype
-    if d is _F32:
-        return 1
-    if d is not _BF16:
-        _refuse(where, f"{name} is {d}; bfloat16 or float32 is supported")
-    return 0
-
-
-def _is(t, where, name, dtype, device):
-    if t.dtype is not dtype:
-        _refuse(where, f"{name} is {t.dtype}, not {dtype}")
-    if t.get_device() != device or device < 0:
-        _refuse(where, f"{name} is not on the call's CUDA device")
-
-
-def _rows(t, where, name, dtype, device, shape):
-    """(address, row stride in elements, 0: contiguous) of a matrix; (0, 0) for None."""
-    if t is None:
-        return 0, 0
-    if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
-        return t.data_ptr(), 0
-    _is(t, where, name, dtype, device)
-    if t.shape != shape:
-        _refuse(where, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    n, cols = shape
-    step, inner = t.stride()
-    if (cols > 1 and inner != 1) or (n > 1 and step < cols):
-        _refuse(where, f"{name} has strides {t.stride()}: rows must be contiguous and must not overlap")
-    return t.data_ptr(), step if n > 1 else 0
-
-
-def _array(t, where, name, dtype, device, shape):
-    """Address of a contiguous array; 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    _is(t, where, name, dtype, device)
-    if t.shape != shape:
-        _refuse(where, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    _refuse(where, f"{name} is not contiguous")
-
-
-def _on(device, where):
-    """The call's device is the current one (its kernels are launched there)."""
-    if device < 0 or device != _current_device():
-        _refuse(where, "the tensors are not on the current CUDA device")
-
-
-def _handle(stream, device):
-    """cudaStream_t of a stream argument (None: the current stream) as an integer."""
+    device = "cuda" if like is None else like.device
     if stream is None:
-        return _raw_stream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _workspace(workspace, need, args, where, device, stream):
-    """(tensor, address, bytes): the caller's, or need(*args) bytes allocated on the call's stream."""
-    if workspace is None:
-        size = max(16, need(*args))
-        if stream is None:
-            workspace = _torch.empty(size, dtype=_U8, device=f"cuda:{device}")
-        else:
-            s = _torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-            with _torch.cuda.stream(s):
-                workspace = _torch.empty(size, dtype=_U8, device=f"cuda:{device}")
-        return workspace, workspace.data_ptr(), size
-    _is(workspace, where, "workspace", _U8, device)
-    if not workspace.is_contiguous():
-        _refuse(where, "workspace is not contiguous")
-    return workspace, workspace.data_ptr(), workspace.numel()
-
-
-def _new_workspace(size):
-    return _torch.empty(max(16, size), dtype=_U8, device="cuda")
-
-
-def _norm_gate(gate, shape, act, par, device, where, name="gate"):
-    """(kind, address, stride) of a gate [hidden], [n, 1] or [n, hidden] of type par, fp32 or act."""
-    if gate is None:
-        return GATE_NONE, 0, 0
-    n, hidden = shape
-    if gate.dim() == 1:
-        return GATE_CHANNEL, _array(gate, where, name, par, device, (hidden,)), 0
-    if gate.shape == (n, 1):
-        return GATE_TOKEN, _array(gate, where, name, _F32, device, (n, 1)), 0
-    if gate.shape != shape:
-        _refuse(where, f"{name} is {tuple(gate.shape)}; {(hidden,)}, {(n, 1)} or {(n, hidden)} is supported")
-    p, step = _rows(gate, where, name, act, device, shape)
-    return GATE_FULL, p, step
-
-
-def _norm_pack(where, shape, device, res, branch, residual, gate, post_weight, pre_weight, residual_out, x_out,
-               rstd_post, rstd_pre, eps, residual_scale, branch_scale, weight_offset, gate_sigmoid):
-    """(kind of gate, type of branch, type of the parameters, packed struct)."""
-    n, hidden = shape
-    act = res if branch is None else _dtype_code(branch, where, "branch")
-    lead = post_weight if post_weight is not None else pre_weight
-    if lead is None and gate is not None and gate.dim() == 1:
-        lead = gate
-    par = 1 if lead is None else _dtype_code(lead, where, "the weights")
-    act_t, par_t, res_t, vec = _KINDS[act], _KINDS[par], _KINDS[res], (hidden,)
-    kind, gp, gs = _norm_gate(gate, shape, act_t, par_t, device, where)
-    rp, rs = _rows(residual, where, "residual", res_t, device, shape)
-    bp, bs = _rows(branch, where, "branch", act_t, device, shape)
-    op, os_ = _rows(residual_out, where, "residual_out", res_t, device, shape)
-    xp, xs = _rows(x_out, where, "x_out", _BF16, device, shape)
-    return kind, act_t, _NORM_ARGS.pack(
-        n, hidden, res, act, par, kind, 1 if gate_sigmoid and kind else 0, eps, residual_scale, branch_scale,
-        weight_offset, rp, rs, bp, bs, gp, gs, _array(post_weight, where, "post_weight", par_t, device, vec),
-        _array(pre_weight, where, "pre_weight", par_t, device, vec), op, os_, xp, xs,
-        _array(rstd_post, where, "rstd_post", _F32, device, (n,)),
-        _array(rstd_pre, where, "rstd_pre", _F32, device, (n,)))
+        return torch.empty(max(16, size), dtype=torch.uint8, device=device)
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(max(16, size), dtype=torch.uint8, device=device)
 
 
 def block_norm(residual, branch=None, gate=None, post_weight=None, pre_weight=None, residual_out=None, x_out=None,
@@ -427,25 +314,16 @@ def block_norm(residual, branch=None, gate=None, post_weight=None, pre_weight=No
 
     residual_out = residual_scale * residual + branch_scale * gate * norm(branch, post_weight) and
     x_out = norm(residual_out, pre_weight).  Tensors are [n, hidden]; the gate is [hidden], [n, 1] (fp32) or
-    [n, hidden]; without ``branch`` it is the norm before a block, without ``pre_weight`` the norm after one."""
-    L = _lib if _torch is not None else _ready()
-    where = "moe_block_norm"
-    if residual is None or residual.dim() != 2:
-        _refuse(where, "residual is not an [n, hidden] tensor")
-    device = residual.get_device()
-    _on(device, where)
-    args = _norm_pack(where, residual.shape, device, _dtype_code(residual, where, "residual"), branch, residual, gate,
-                      post_weight, pre_weight, residual_out, x_out, rstd_post, rstd_pre, eps, residual_scale,
-                      branch_scale, weight_offset, gate_sigmoid)[2]
-    status = L.moe_block_norm(args, _handle(stream, device))
-    if status:
-        raise MoeError(status, where)
+    [n, hidden]; without ``branch`` it is the norm before a block, without ``pre_weight`` the norm after one.
+    ``rstd_post`` and ``rstd_pre`` [n] receive the row statistics that the backward pass needs."""
+    (_native or _binding()).block_norm(residual, branch, gate, post_weight, pre_weight, residual_out, x_out, rstd_post,
+                                       rstd_pre, eps, residual_scale, branch_scale, weight_offset, gate_sigmoid, stream)
     return residual_out, x_out
 
 
 def block_norm_workspace(n: int, hidden: int):
     """A workspace for block_norm_backward of up to n tokens."""
-    return _new_workspace(_ready().moe_block_norm_workspace_bytes(n, hidden))
+    return _new_workspace(load().moe_block_norm_workspace_bytes(n, hidden))
 
 
 def block_norm_backward(d_residual_out, d_x, residual_out, branch=None, gate=None, post_weight=None, pre_weight=None,
@@ -455,58 +333,27 @@ def block_norm_backward(d_residual_out, d_x, residual_out, branch=None, gate=Non
                         workspace=None, stream=None):
     """``moe_block_norm_backward``: fills the given gradients from those of residual_out and x_out (either may be
     None: zero).  residual_out, rstd_post and rstd_pre are what block_norm left."""
-    L = _lib if _torch is not None else _ready()
-    where = "moe_block_norm_backward"
-    lead = d_residual_out if d_residual_out is not None else residual_out if residual_out is not None else branch
-    if lead is None or lead.dim() != 2:
-        _refuse(where, "no [n, hidden] gradient is given")
-    shape, device = lead.shape, lead.get_device()
-    _on(device, where)
-    n, hidden = shape
-    kind, act_t, args = _norm_pack(
-        where, shape, device, _dtype_code(lead, where, "the residual"), branch, None, gate, post_weight, pre_weight,
-        residual_out, None, rstd_post, rstd_pre, eps, residual_scale, branch_scale, weight_offset, gate_sigmoid)
-    dk, dgp, dgs = _norm_gate(d_gate, shape, act_t, _F32, device, where, "d_gate")
-    if dk and dk != kind:
-        _refuse(where, f"d_gate is {tuple(d_gate.shape)}, the gate another shape")
-    res_t = lead.dtype
-    a, ast = _rows(d_residual_out, where, "d_residual_out", res_t, device, shape)
-    b, bst = _rows(d_x, where, "d_x", _BF16, device, shape)
-    c, cst = _rows(d_residual, where, "d_residual", res_t, device, shape)
-    d, dst = _rows(d_branch, where, "d_branch", act_t, device, shape)
-    grads = _NORM_GRADS.pack(a, ast, b, bst, c, cst, d, dst, dgp, dgs,
-                             _array(d_post_weight, where, "d_post_weight", _F32, device, (hidden,)),
-                             _array(d_pre_weight, where, "d_pre_weight", _F32, device, (hidden,)))
-    keep, wp, wb = _workspace(workspace, L.moe_block_norm_workspace_bytes, (n, hidden), where, device, stream)
-    status = L.moe_block_norm_backward(args, grads, wp, wb, _handle(stream, device))
-    if status:
-        raise MoeError(status, where)
+    native = _native or _binding()
+    if workspace is None:
+        lead = next((t for t in (d_residual_out, residual_out, branch) if t is not None and t.dim() == 2), None)
+        if lead is not None and lead.is_cuda:
+            workspace = _new_workspace(_lib.moe_block_norm_workspace_bytes(*lead.shape), lead, stream)
+    native.block_norm_backward(d_residual_out, d_x, residual_out, branch, gate, post_weight, pre_weight, rstd_post,
+                               rstd_pre, d_residual, d_branch, d_gate, d_post_weight, d_pre_weight, eps,
+                               residual_scale, branch_scale, weight_offset, gate_sigmoid, workspace, stream)
     return d_residual, d_branch
 
 
 def router_workspace(n: int, n_experts: int, n_seqs: int = 1):
     """A workspace for balance_loss and router_backward of up to n tokens in n_seqs sequences."""
-    return _new_workspace(_ready().moe_router_workspace_bytes(n, n_experts, n_seqs))
+    return _new_workspace(load().moe_router_workspace_bytes(n, n_experts, n_seqs))
 
 
-def _router_pack(where, logits, bias, topk_ids, counts, tokens, coef, mask, seq_offsets):
-    if logits is None or logits.dim() != 2 or topk_ids is None or topk_ids.dim() != 2:
-        _refuse(where, "logits are not [n, n_experts] or topk_ids not [n, top_k]")
-    shape, k, device = logits.shape, topk_ids.shape[1], logits.get_device()
-    n, E = shape
-    _on(device, where)
-    S = 1
-    if seq_offsets is not None:
-        S = seq_offsets.shape[0] - 1 if seq_offsets.dim() == 1 else 0
-        if S < 1:
-            _refuse(where, "seq_offsets holds no sequence")
-    args = _ROUTER_ARGS.pack(
-        n, E, k, S, coef, _array(logits, where, "logits", _F32, device, shape),
-        _array(bias, where, "bias", _F32, device, (E,)), _array(topk_ids, where, "topk_ids", _I32, device, (n, k)),
-        0 if mask is None else _array(mask, where, "mask", _BOOL if mask.dtype is _BOOL else _U8, device, (n,)),
-        _array(seq_offsets, where, "seq_offsets", _I32, device, (S + 1,)),
-        _array(counts, where, "counts", _I32, device, (S, E)), _array(tokens, where, "tokens", _I32, device, (S + 1,)))
-    return n, E, k, S, device, args
+def _router_workspace_for(logits, seq_offsets, stream):
+    if logits is None or logits.dim() != 2 or not logits.is_cuda:
+        return None  # refused by the call
+    seqs = 1 if seq_offsets is None else max(1, seq_offsets.numel() - 1)
+    return _new_workspace(load().moe_router_workspace_bytes(*logits.shape, seqs), logits, stream)
 
 
 def balance_loss(logits, bias, topk_ids, loss, counts, prob_sums, tokens, *, coef: float, mask=None,
@@ -514,14 +361,11 @@ def balance_loss(logits, bias, topk_ids, loss, counts, prob_sums, tokens, *, coe
     """``moe_balance_loss``: fills loss [1], counts [S, E] int32, prob_sums [S, E] and tokens [S + 1] int32 (each
     sequence's tokens, then all) from logits [n, E] (+ bias [E]) and topk_ids [n, k].  ``mask`` [n] (bool or uint8)
     leaves tokens out; ``seq_offsets`` [S + 1] int32 cuts the batch into sequences (None: one)."""
-    L = _lib if _torch is not None else _ready()
-    where = "moe_balance_loss"
-    n, E, _, S, device, args = _router_pack(where, logits, bias, topk_ids, counts, tokens, coef, mask, seq_offsets)
-    keep, wp, wb = _workspace(workspace, L.moe_router_workspace_bytes, (n, E, S), where, device, stream)
-    status = L.moe_balance_loss(args, _array(prob_sums, where, "prob_sums", _F32, device, (S, E)),
-                                _array(loss, where, "loss", _F32, device, (1,)), wp, wb, _handle(stream, device))
-    if status:
-        raise MoeError(status, where)
+    native = _native or _binding()
+    if workspace is None:
+        workspace = _router_workspace_for(logits, seq_offsets, stream)
+    native.balance_loss(logits, bias, topk_ids, loss, counts, prob_sums, tokens, coef, mask, seq_offsets, workspace,
+                        stream)
     return loss
 
 
@@ -529,51 +373,25 @@ def router_backward(logits, bias, topk_ids, topk_weights, d_weights, counts, tok
                     d_loss=None, coef: float, mask=None, seq_offsets=None, workspace=None, stream=None):
     """``moe_router_backward``: d_logits [n, E] (and d_bias [E]) of d_loss [1] times the balance loss (counts and
     tokens as balance_loss left them; None: no loss) and of the top-k weights (d_weights [n, k]; None: none)."""
-    L = _lib if _torch is not None else _ready()
-    where = "moe_router_backward"
-    n, E, k, S, device, args = _router_pack(where, logits, bias, topk_ids, counts, tokens, coef, mask, seq_offsets)
-    keep, wp, wb = _workspace(workspace, L.moe_router_workspace_bytes, (n, E, S), where, device, stream)
-    status = L.moe_router_backward(args, _array(topk_weights, where, "topk_weights", _F32, device, (n, k)),
-                                   _array(d_weights, where, "d_weights", _F32, device, (n, k)),
-                                   _array(d_loss, where, "d_loss", _F32, device, (1,)),
-                                   _array(d_logits, where, "d_logits", _F32, device, (n, E)),
-                                   _array(d_bias, where, "d_bias", _F32, device, (E,)), wp, wb,
-                                   _handle(stream, device))
-    if status:
-        raise MoeError(status, where)
+    native = _native or _binding()
+    if workspace is None:
+        workspace = _router_workspace_for(logits, seq_offsets, stream)
+    native.router_backward(logits, bias, topk_ids, topk_weights, d_weights, counts, tokens, d_logits, d_bias, d_loss,
+                           coef, mask, seq_offsets, workspace, stream)
     return d_logits
 
 
 def lora_workspace(n: int, n_adapters: int):
     """A workspace for lora_apply of up to n tokens over n_adapters adapters."""
-    return _new_workspace(_ready().moe_lora_workspace_bytes(n, n_adapters))
+    return _new_workspace(load().moe_lora_workspace_bytes(n, n_adapters))
 
 
 def lora_apply(x, adapter_ids, a, b, y, out, *, scale=None, ranks=None, workspace=None, stream=None):
     """``moe_lora_apply``: out[t] = y[t] + scale[l] * B[l] (A[l] x[t]) with l = adapter_ids[t] (an id outside the
     bank, such as -1: out[t] = y[t]).  x [n, in] bf16, a [L, R, in] and b [L, out, R] bf16, y [n, out] (None: zero)
     and out [n, out] bf16 or fp32 (out may be y), scale [L] fp32, ranks [L] int32."""
-    L = _lib if _torch is not None else _ready()
-    where = "moe_lora_apply"
-    if x is None or x.dim() != 2 or a is None or a.dim() != 3 or b is None or b.dim() != 3 or out is None:
-        _refuse(where, "x is not [n, in], a not [L, R, in], b not [L, out, R], or out is missing")
-    n, inp = shape = x.shape
-    adapters, R, _ = a.shape
-    o = b.shape[1]
-    device = x.get_device()
-    _on(device, where)
-    yd = 0 if y is None else _dtype_code(y, where, "y")
-    od = _dtype_code(out, where, "out")
-    xp, xs = _rows(x, where, "x", _BF16, device, shape)
-    yp, ys = _rows(y, where, "y", _KINDS[yd], device, (n, o))
-    op, os_ = _rows(out, where, "out", _KINDS[od], device, (n, o))
-    args = _LORA_ARGS.pack(
-        n, inp, o, adapters, R, yd, od, _array(a, where, "a", _BF16, device, (adapters, R, inp)),
-        _array(b, where, "b", _BF16, device, (adapters, o, R)), _array(scale, where, "scale", _F32, device, (adapters,)),
-        _array(ranks, where, "ranks", _I32, device, (adapters,)),
-        _array(adapter_ids, where, "adapter_ids", _I32, device, (n,)), xp, xs, yp, ys, op, os_)
-    keep, wp, wb = _workspace(workspace, L.moe_lora_workspace_bytes, (n, adapters), where, device, stream)
-    status = L.moe_lora_apply(args, wp, wb, _handle(stream, device))
-    if status:
-        raise MoeError(status, where)
+    native = _native or _binding()
+    if workspace is None and x is not None and x.dim() == 2 and x.is_cuda and a is not None:
+        workspace = _new_workspace(_lib.moe_lora_workspace_bytes(x.shape[0], a.shape[0]), x, stream)
+    native.lora_apply(x, adapter_ids, a, b, y, out, scale, ranks, workspace, stream)
     return out

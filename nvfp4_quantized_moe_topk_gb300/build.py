@@ -3,7 +3,10 @@
 Each translation unit is compiled by nvcc in parallel, then linked into one
 shared library with the CUDA runtime linked statically.  The driver API entry
 point needed for tensor maps is resolved at run time, so the library does not
-link libcuda.  Usage: ``python -m nvfp4_quantized_moe_topk_gb300.build``.
+link libcuda.  ``csrc/binding.cpp``, the Python module with the argument checks
+of the operators around the layer, is compiled beside it by g++ against the
+installed torch and linked to the library.
+Usage: ``python -m nvfp4_quantized_moe_topk_gb300.build``.
 """
 from __future__ import annotations
 
@@ -19,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe_nvfp4.so")
+BINDING = os.path.join(BUILD, "moe_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -36,15 +40,47 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _torch_dir() -> str:
+    import importlib.util
+
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_binding() -> str:
+    """The object file of csrc/binding.cpp."""
+    import sysconfig
+
+    torch, obj = _torch_dir(), os.path.join(BUILD, "binding.cpp.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-I", os.path.join(torch, "include"),
+           "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    tmp = BINDING + f".tmp{os.getpid()}"
+    libs = os.path.join(_torch_dir(), "lib")
+    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-l:libmoe_nvfp4.so", "-Wl,-rpath,$ORIGIN",
+                        "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -64,13 +100,16 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(sources()))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(sources()) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 

@@ -2,6 +2,7 @@
 CUDA call (no accepted call is made here: the addresses are not memory)."""
 import os
 import shutil
+import struct
 import subprocess
 
 import pytest
@@ -9,6 +10,11 @@ import pytest
 from nvfp4_quantized_moe_topk_gb300 import api
 from nvfp4_quantized_moe_topk_gb300 import build as B
 
+# the argument structs of the header, packed
+NORM_ARGS = struct.Struct("@7i4f4xPqPqPqPPPqPqPP")
+NORM_GRADS = struct.Struct("@PqPqPqPqPqPP")
+ROUTER_ARGS = struct.Struct("@4if4xPPPPPPP")
+LORA_ARGS = struct.Struct("@7i4xPPPPPPqPqPq")
 A = 4096  # an aligned address that is never looked at
 
 
@@ -42,8 +48,8 @@ def test_struct_layouts_match_the_header(tmp_path):
     subprocess.run([gcc, "-std=c99", f"-I{inc}", str(src), "-o", str(exe)], check=True)
     got = [[int(v) for v in l.split()] for l in subprocess.run([str(exe)], capture_output=True,
                                                                text=True).stdout.splitlines()]
-    assert [g[0] for g in got] == [api._NORM_ARGS.size, api._NORM_GRADS.size, api._ROUTER_ARGS.size,
-                                   api._LORA_ARGS.size]
+    assert [g[0] for g in got] == [NORM_ARGS.size, NORM_GRADS.size, ROUTER_ARGS.size,
+                                   LORA_ARGS.size]
     assert got[0][1:] == [0, 40, 48, 64, 80, 96, 104, 112, 128, 144, 152]
     assert got[1][1:] == [0, 16, 32, 48, 64, 80, 88]
     assert got[2][1:] == [0, 12, 16, 24, 32, 40, 48, 56, 64, 72]
@@ -59,19 +65,19 @@ LORA = dict(n=4, inp=64, out_=64, L=2, R=16, yd=0, od=0, a=A, b=A, scale=A, rank
 
 
 def norm(**kw):
-    return api._NORM_ARGS.pack(*dict(NORM, **kw).values())
+    return NORM_ARGS.pack(*dict(NORM, **kw).values())
 
 
 def grad(**kw):
-    return api._NORM_GRADS.pack(*dict(GRAD, **kw).values())
+    return NORM_GRADS.pack(*dict(GRAD, **kw).values())
 
 
 def router(**kw):
-    return api._ROUTER_ARGS.pack(*dict(ROUTER, **kw).values())
+    return ROUTER_ARGS.pack(*dict(ROUTER, **kw).values())
 
 
 def lora(**kw):
-    return api._LORA_ARGS.pack(*dict(LORA, **kw).values())
+    return LORA_ARGS.pack(*dict(LORA, **kw).values())
 
 
 @pytest.mark.parametrize("want,kw", [
