@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
   const bool post = MODE != kNormAny || a.post != nullptr, pre = MODE != kNormAny || a.pre != nullptr;
   const bool full = MODE == kNormAny ? a.gate_kind == MOE_GATE_FULL : MODE == kNormFull;
   const bool token = (MODE == kNormAny || MODE == kNormScalar) && a.gate_kind == MOE_GATE_TOKEN;
-  const uint32_t pitch = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t pitch = blockDim.x * 16, mine = threadIdx.x * 16, ring_u32 = smem_u32(ring);
   const uint32_t iter_bytes = stage_vecs / ITERS * pitch, stage_bytes = stage_vecs * pitch;
   const uint32_t n = a.n, step = gridDim.x;
   F2 cz[ITERS][4], wx[ITERS][4];
@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
-        ring_copy<RT, Q>(at, pitch, a.residual.at(t, 0), i, a.H);
-        if (branch) ring_copy<YT, Q>(at + kR * pitch, pitch, a.branch.at(t, 0), i, a.H);
-        if (full) ring_copy<YT, Q>(at + (kR + kY) * pitch, pitch, a.gate.at(t, 0), i, a.H);
+        ring_copy<RT, Q>(ring_u32 + at, pitch, a.residual.at(t, 0), i, a.H);
+        if (branch) ring_copy<YT, Q>(ring_u32 + at + kR * pitch, pitch, a.branch.at(t, 0), i, a.H);
+        if (full) ring_copy<YT, Q>(ring_u32 + at + (kR + kY) * pitch, pitch, a.gate.at(t, 0), i, a.H);
       }
     }
     cp_async_commit();  // one group a row, empty past the end
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
       for (int i = 0; i < ITERS; ++i) {
         const Lane<Q> l(i, a.H);
         if (!l.ok0) continue;
-        ring_read<YT>(at + i * iter_bytes + kR * pitch, pitch, l, z[i]);
+        ring_read<YT>(ring, at + i * iter_bytes + kR * pitch, pitch, l, z[i]);
         ss += squares(z[i]);
       }
     }
@@ -201,10 +201,10 @@ __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
     for (int i = 0; i < ITERS; ++i) {
       const Lane<Q> l(i, a.H);
       if (!l.ok0) continue;
-      ring_read<RT>(at + i * iter_bytes, pitch, l, u[i]);
+      ring_read<RT>(ring, at + i * iter_bytes, pitch, l, u[i]);
       if (full) {
         F2 g[4];
-        ring_read<YT>(at + i * iter_bytes + (kR + kY) * pitch, pitch, l, g);
+        ring_read<YT>(ring, at + i * iter_bytes + (kR + kY) * pitch, pitch, l, g);
         apply_gate(a, z[i], g);
       }
 #pragma unroll

@@ -159,13 +159,13 @@ __device__ __forceinline__ void ring_copy(uint32_t at, uint32_t pitch, const cha
     if (c + 128 < hidden) cp_async16(at + pitch, row + (uint32_t)c * 4u + 512);
   }
 }
-// 0 where the lane has no channel.
+// The lane's values from the ring (`at`: offset of its 16 bytes in the CTA's
+// dynamic shared memory), 0 where it has no channel.
 template <typename T, bool QUADS>
-__device__ __forceinline__ void ring_read(uint32_t at, uint32_t pitch, const Lane<QUADS>& l, F2 (&v)[4]) {
-  const uint32_t lane = threadIdx.x & 31;
+__device__ __forceinline__ void ring_read(const char* ring, uint32_t at, uint32_t pitch, const Lane<QUADS>& l,
+                                          F2 (&v)[4]) {
   if constexpr (Vec8<T>::kVecs == 1 && !QUADS) {
-    uint4 d;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(d.x), "=r"(d.y), "=r"(d.z), "=r"(d.w) : "r"(at) : "memory");
+    const uint4 d = *reinterpret_cast<const uint4*>(ring + at);
     v[0] = {bf16lo(d.x), bf16hi(d.x)};
     v[1] = {bf16lo(d.y), bf16hi(d.y)};
     v[2] = {bf16lo(d.z), bf16hi(d.z)};
@@ -173,18 +173,17 @@ __device__ __forceinline__ void ring_read(uint32_t at, uint32_t pitch, const Lan
   } else if constexpr (Vec8<T>::kVecs == 1) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint2 d;
-      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(d.x), "=r"(d.y) : "r"(at - lane * 8 + h * 256) : "memory");
+      const uint2 d = *reinterpret_cast<const uint2*>(ring + at - (threadIdx.x & 31) * 8 + h * 256);
       v[2 * h] = {bf16lo(d.x), bf16hi(d.x)};
       v[2 * h + 1] = {bf16lo(d.y), bf16hi(d.y)};
     }
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(v[2 * h].x), "=f"(v[2 * h].y), "=f"(v[2 * h + 1].x), "=f"(v[2 * h + 1].y)
-                   : "r"(at + h * pitch)
-                   : "memory");
+    for (int h = 0; h < 2; ++h) {
+      const float4 d = *reinterpret_cast<const float4*>(ring + at + h * pitch);
+      v[2 * h] = {d.x, d.y};
+      v[2 * h + 1] = {d.z, d.w};
+    }
   }
   if (QUADS && !l.ok1) v[2] = v[3] = f2(0.f);
 }

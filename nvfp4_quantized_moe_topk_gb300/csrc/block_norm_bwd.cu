@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
   const bool full = MODE == kNormAny ? a.gate_kind == MOE_GATE_FULL : MODE == kNormFull;
   const bool channel = MODE == kNormAny ? a.gate_kind == MOE_GATE_CHANNEL : MODE == kNormChannel;
   const bool token = (MODE == kNormAny || MODE == kNormScalar) && a.gate_kind == MOE_GATE_TOKEN;
-  const uint32_t pitch = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t pitch = blockDim.x * 16, mine = threadIdx.x * 16, ring_u32 = smem_u32(ring);
   const uint32_t iter_bytes = stage_vecs / ITERS * pitch, stage_bytes = stage_vecs * pitch;
   const uint32_t n = a.n, step = gridDim.x;
   constexpr bool Q = Vec8<RT>::kVecs + Vec8<YT>::kVecs > 2;
@@ -81,13 +81,13 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const uint32_t at = mine + stage * stage_bytes + i * iter_bytes;
-        if (d.dr.p) ring_copy<RT, Q>(at, pitch, d.dr.at(t, 0), i, a.H);
+        if (d.dr.p) ring_copy<RT, Q>(ring_u32 + at, pitch, d.dr.at(t, 0), i, a.H);
         if (pre) {
-          ring_copy<RT, Q>(at + kU * pitch, pitch, a.residual_out.at(t, 0), i, a.H);
-          ring_copy<uint16_t, Q>(at + kDx * pitch, pitch, d.dx.at(t, 0), i, a.H);
+          ring_copy<RT, Q>(ring_u32 + at + kU * pitch, pitch, a.residual_out.at(t, 0), i, a.H);
+          ring_copy<uint16_t, Q>(ring_u32 + at + kDx * pitch, pitch, d.dx.at(t, 0), i, a.H);
         }
-        if (branch) ring_copy<YT, Q>(at + kB * pitch, pitch, a.branch.at(t, 0), i, a.H);
-        if (full) ring_copy<YT, Q>(at + kG * pitch, pitch, a.gate.at(t, 0), i, a.H);
+        if (branch) ring_copy<YT, Q>(ring_u32 + at + kB * pitch, pitch, a.branch.at(t, 0), i, a.H);
+        if (full) ring_copy<YT, Q>(ring_u32 + at + kG * pitch, pitch, a.gate.at(t, 0), i, a.H);
       }
     }
     cp_async_commit();
@@ -123,18 +123,18 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
         }
       }
       if (d.dr.p) {
-        ring_read<RT>(v, pitch, l, q);
+        ring_read<RT>(ring, v, pitch, l, q);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) q[j] = f2(0.f);
       }
       if (pre) {
-        ring_read<RT>(v + kU * pitch, pitch, l, u);
-        ring_read<uint16_t>(v + kDx * pitch, pitch, l, dx);
+        ring_read<RT>(ring, v + kU * pitch, pitch, l, u);
+        ring_read<uint16_t>(ring, v + kDx * pitch, pitch, l, dx);
       }
-      if (branch) ring_read<YT>(v + kB * pitch, pitch, l, y);
+      if (branch) ring_read<YT>(ring, v + kB * pitch, pitch, l, y);
       if (full) {
-        ring_read<YT>(v + kG * pitch, pitch, l, g);
+        ring_read<YT>(ring, v + kG * pitch, pitch, l, g);
         if (a.gate_sigmoid) sigmoid2(g);
       }
     };

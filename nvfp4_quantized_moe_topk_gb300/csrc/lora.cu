@@ -154,206 +154,76 @@ constexpr int kSmallTokens = 1024;  // more than these take lora_rows.cu
 template <int NT>
 __global__ void __launch_bounds__(kLoraThreads, 2)
     lora_kernel(const moe_lora_args a, const LoraPlan plan, int32_t fused, int32_t terms, uint32_t ring_bytes) {
-  constexpr int MW = 1, MT = 16, KG = kLoraWarps;
+  constexpr int MT = 16, KG = kLoraWarps;
   constexpr int RPASS = 8 * NT, RP = RPASS + 8;  // ranks of a pass; row pitch of the partial sums
   extern __shared__ __align__(16) char sm[];
   __shared__ int32_t row[MT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const uint32_t C = cluster_size(), cr = cluster_rank();
   Tile t;
-  // the ring, between the loops [KG][MT][RP] partial sums; in a cluster [MT][RP] the CTA's sum; v, [terms][MT][VP] bf16
-  float* part = reinterpret_cast<float*>(sm);
-  float* sum = reinterpret_cast<float*>(sm + ring_bytes);
-  uint16_t* v = reinterpret_cast<uint16_t*>(sum + (C > 1 ? MT * RP : 0));
-  if (!find_tile<MT>(a, plan, fused != 0, (int32_t)(blockIdx.x / C), row, reinterpret_cast<int32_t*>(sm), t)) return;
-  const uint32_t slot = smem_u32(sm) + tid * 16;
-  int32_t rank = 0;
-  float scale = 0.f;
-  if (t.adapter < a.n_adapters) {
-    rank = a.ranks ? min(max(a.ranks[t.adapter], 0), a.max_rank) : a.max_rank;
-    scale = a.scale ? a.scale[t.adapter] : 1.f;
-  }
+  // ring; the warps' sums [KG][MT][RP]; in a cluster the CTAs' sums [C][MT][RP]; v [terms][MT][VP] bf16
+  float* part = reinterpret_cast<float*>(sm + ring_bytes);
+  float* recv = part + KG * MT * RP;
+  uint16_t* v = reinterpret_cast<uint16_t*>(recv + (C > 1 ? C * MT * RP : 0));
+  const int32_t tile = (int32_t)(blockIdx.x / C);
+  if (!(fused ? ranked_tile<MT>(a, tile, row, reinterpret_cast<int32_t*>(part), t)
+              : planned_tile<MT>(a, plan, tile, row, t)))
+    return;
+  if (C > 1) cluster_arrive();  // (waited for before the first store into a peer: it has started by then)
+  const uint32_t slot = tid * 16, sm_u32 = smem_u32(sm);  // offsets in sm; cp.async takes addresses
+  const int32_t rank = t.rank;
   const int32_t R32 = (rank + 31) & ~31;
   const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;  // pitch of v: rows 64 bytes apart mod 128
-  __syncthreads();  // the tile's scratch, in the ring, has been read
-
-  if (rank > 0) {
-    const char* A = reinterpret_cast<const char*>(a.a + (int64_t)t.adapter * a.max_rank * a.in_features);
-    const uint32_t row_bytes = (uint32_t)a.in_features * 2;
-    // places past the tile's count take its first token: their rows of the
-    // products are never looked at
-    const char* xr[MW][2];
+  // places past the tile's count take its first token: their rows of the products are never looked at
+  int32_t tok[2];
+  int64_t at_tok[2];
 #pragma unroll
-    for (int m = 0; m < MW; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int32_t tok = row[m * 16 + h * 8 + g];
-        xr[m][h] = static_cast<const char*>(a.x.data) + 16 * q +
-                   (int64_t)(tok >= 0 ? tok : row[0]) * (a.x.stride ? a.x.stride : a.in_features) * 2;
-      }
-    // a warp takes pairs of windows, 128 bytes of a row: first the even, then the odd one
-    const uint32_t pair0 = ((uint32_t)cr * KG + warp) * 128, jump = (uint32_t)C * KG * 128 - 64;
-    for (int32_t r0 = 0; r0 < rank; r0 += RPASS) {
-      const int32_t nt = min(NT, (rank - r0 + 7) / 8);
-      const uint32_t stage_bytes = (2 * MW + nt) * kSlotVec;
-      const int stages = min(4u, ring_bytes / stage_bytes);
-      const char* Ar = A + (uint64_t)r0 * row_bytes;
-      const uint32_t lane_a = g * row_bytes + 16 * q;
-      uint32_t fetch_off = pair0;  // byte offset in a row of the window to fetch next
-      bool fetch_odd = false;
-      auto fetch = [&](int stage) {
-        if (fetch_off < row_bytes) {
-          if (fetch_off + 16 * q < row_bytes) {  // else the lane's part lies past the row's end, and is read as 0
-            const uint32_t at = slot + stage * stage_bytes;
-#pragma unroll
-            for (int m = 0; m < MW; ++m)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) ring16(at + (2 * m + h) * kSlotVec, xr[m][h] + fetch_off);
-            // rows between the rank and the next multiple of 8 are in the bank
-            // and reach only entries of v that are set to zero
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              if (j >= nt) break;
-              ring16(at + (2 * MW + j) * kSlotVec, Ar + ((uint64_t)(8 * j) * row_bytes + fetch_off) + lane_a);
-            }
-          }
-        }
-        fetch_off += fetch_odd ? jump : 64;
-        fetch_odd = !fetch_odd;
-        ring_commit();
-      };
-      for (int s = 0; s + 1 < stages; ++s) fetch(s);
-      float acc[MW][NT][4] = {};
-      int stage = 0;
-      bool odd = false;
-      for (uint32_t off = pair0; off < row_bytes;
-           off += odd ? jump : 64, odd = !odd, stage = stage + 1 == stages ? 0 : stage + 1) {
-        fetch(stage == 0 ? stages - 1 : stage - 1);
-        ring_wait(stages - 1);
-        const uint32_t at = slot + stage * stage_bytes;
-        const bool past = off + 16 * q >= row_bytes;
-        uint4 xa[MW][2];
-#pragma unroll
-        for (int m = 0; m < MW; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            xa[m][h] = slot16(at + (2 * m + h) * kSlotVec);
-            if (past) xa[m][h] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (j >= nt) break;
-          uint4 av = slot16(at + (2 * MW + j) * kSlotVec);
-          if (past) av = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int m = 0; m < MW; ++m)
-            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, av.x, av.y);
-#pragma unroll
-          for (int m = 0; m < MW; ++m)
-            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, av.z, av.w);
-        }
-      }
-      ring_wait(0);
-      __syncthreads();  // the ring becomes the partial sums
-#pragma unroll
-      for (int m = 0; m < MW; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(part + (warp * MT + m * 16 + h * 8 + g) * RP + 8 * j + 2 * q) =
-                make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-      __syncthreads();
-      auto own_sum = [&](int m, int r) {
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < KG; ++k) s += part[(k * MT + m) * RP + r];
-        return s;
-      };
-      if (C > 1) {
-        for (int i = tid; i < MT * RPASS; i += kLoraThreads)
-          sum[i / RPASS * RP + i % RPASS] = own_sum(i / RPASS, i % RPASS);
-        cluster_sync();
-      }
-      for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
-        const int m = i / RPASS, r = i % RPASS;
-        float s = 0.f;
-        if (C > 1) {
-          for (uint32_t k = 0; k < C; ++k) s += peer_float(sum + m * RP + r, k);
-        } else {
-          s = own_sum(m, r);
-        }
-        s = r0 + r < rank ? s * scale : 0.f;
-        if (r0 + r < R32)
-          for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
-            const uint16_t b = f2bf_rn(s);
-            v[(k * MT + m) * VP + r0 + r] = b;
-            s -= bf16lo(b);
-          }
-      }
-      if (C > 1)
-        cluster_sync();  // the peers have read this CTA's sums
-      else
-        __syncthreads();
-    }
-    // what the last pass does not reach up to the next window of 32
-    const int32_t done = (rank + RPASS - 1) / RPASS * RPASS;
-    if (done < R32) {
-      for (int i = tid; i < terms * MT * (R32 - done); i += kLoraThreads)
-        v[i / (R32 - done) * VP + done + i % (R32 - done)] = 0;
-      __syncthreads();
-    }
+  for (int h = 0; h < 2; ++h) {
+    tok[h] = row[h * 8 + g];
+    at_tok[h] = tok[h] >= 0 ? tok[h] : row[0];
   }
 
-  // out = y + B v.  A lane's columns of a block: 4 at c0 and 4 at c0 + next.
+  // The second product's steps: a block of 32 columns of y and B.  A lane's columns: 4 at c0 and 4 at c0 + next.
   const bool quads = a.y_dtype == MOE_DTYPE_F32 || a.out_dtype == MOE_DTYPE_F32;
   const bool yf = a.y_dtype == MOE_DTYPE_F32, has_y = a.y.data != nullptr;
   const int32_t lc = quads ? 4 : 8, next = quads ? 16 : 4;
+  const uint32_t y_vecs = !has_y ? 0 : yf ? 2 : 1, y_size = yf ? 4 : 2;
   const char* B = reinterpret_cast<const char*>(a.b) +
                   (rank > 0 ? (int64_t)t.adapter * a.out_features * a.max_rank * 2 : 0);
   const int32_t blocks = (a.out_features + 31) / 32, kwins = R32 / 32;
-  const uint32_t y_vecs = !has_y ? 0 : yf ? 2 : 1, y_size = yf ? 4 : 2;
-  const uint32_t stage_bytes = max(1u, 4 * kwins + 2 * MW * y_vecs) * kSlotVec;
-  const int stages = min(4u, ring_bytes / stage_bytes);
-  int32_t tok[MW][2];
-  const char* yr[MW][2];  // (places past the tile's count: its first token, and nothing is stored)
+  const uint32_t y_step = max(1u, 4 * kwins + 2 * y_vecs) * kSlotVec;
+  const int y_stages = ring_stages(ring_bytes, y_step);
+  const char* yr[2];
 #pragma unroll
-  for (int m = 0; m < MW; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      tok[m][h] = row[m * 16 + h * 8 + g];
-      yr[m][h] = static_cast<const char*>(a.y.data) +
-                 ((int64_t)(tok[m][h] >= 0 ? tok[m][h] : row[0]) * (a.y.stride ? a.y.stride : a.out_features) + lc * q) *
-                     y_size;
-    }
+  for (int h = 0; h < 2; ++h)
+    yr[h] = static_cast<const char*>(a.y.data) +
+            (at_tok[h] * (a.y.stride ? a.y.stride : a.out_features) + lc * q) * y_size;
   const int32_t b0 = (int32_t)cr * kLoraWarps + warp, bstep = (int32_t)C * kLoraWarps;
   const int32_t lane_o = (g >> 1) * lc + (g & 1);    // the lane's row of B in a block, without j's part
   const uint32_t b_bytes = (uint32_t)a.max_rank * 2;  // of a row of B
   const uint32_t lane_b = (uint32_t)lane_o * b_bytes + 16 * q;
-  auto fetch = [&](int32_t ob, int stage) {
+  auto fetch_y = [&](int32_t ob, int stage) {
     if (ob < blocks) {
-      uint32_t at = slot + stage * stage_bytes;
+      uint32_t at = slot + stage * y_step;
       if (has_y) {
         const bool in0 = ob * 32 + lc * q < a.out_features, in1 = ob * 32 + lc * q + next < a.out_features;
         const uint32_t e = (uint32_t)ob * 32 * y_size;
 #pragma unroll
-        for (int m = 0; m < MW; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (yf) {
-              if (in0) ring16(at, yr[m][h] + e);
-              if (in1) ring16(at + kSlotVec, yr[m][h] + e + 64);
-              at += 2 * kSlotVec;
-            } else {
-              if (quads) {
-                if (in0) ring8(at, yr[m][h] + e);
-                if (in1) ring8(at + 8, yr[m][h] + e + 32);
-              } else if (in0) {
-                ring16(at, yr[m][h] + e);
-              }
-              at += kSlotVec;
+        for (int h = 0; h < 2; ++h) {
+          if (yf) {
+            if (in0) ring16(sm_u32 + at, yr[h] + e);
+            if (in1) ring16(sm_u32 + at + kSlotVec, yr[h] + e + 64);
+            at += 2 * kSlotVec;
+          } else {
+            if (quads) {
+              if (in0) ring8(sm_u32 + at, yr[h] + e);
+              if (in1) ring8(sm_u32 + at + 8, yr[h] + e + 32);
+            } else if (in0) {
+              ring16(sm_u32 + at, yr[h] + e);
             }
+            at += kSlotVec;
           }
+        }
       }
       const char* Bo = B + (uint64_t)((uint32_t)ob * 32) * b_bytes;
       const int32_t left_o = a.out_features - ob * 32 - lane_o;
@@ -362,27 +232,140 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j, at += kSlotVec) {
           const int32_t jo = (j >> 1) * next + 2 * (j & 1);
-          if (in && jo < left_o) ring16(at, Bo + ((uint64_t)(uint32_t)jo * b_bytes + k * 64) + lane_b);
+          if (in && jo < left_o) ring16(sm_u32 + at, Bo + ((uint64_t)(uint32_t)jo * b_bytes + k * 64) + lane_b);
         }
       }
     }
     ring_commit();
   };
-  for (int s = 0; s + 1 < stages; ++s) fetch(b0 + s * bstep, s);
+  auto fetch_first_y = [&] {
+    for (int s = 0; s + 1 < y_stages; ++s) fetch_y(b0 + s * bstep, s);
+  };
+
+  if (rank == 0) fetch_first_y();
+  if (rank > 0) {
+    const uint32_t row_bytes = (uint32_t)a.in_features * 2;
+    const char* xr[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      xr[h] = static_cast<const char*>(a.x.data) + 16 * q + at_tok[h] * (a.x.stride ? a.x.stride : a.in_features) * 2;
+    // a warp takes pairs of windows, 128 bytes of a row: first the even, then the odd one
+    const uint32_t pair0 = ((uint32_t)cr * KG + warp) * 128, jump = (uint32_t)C * KG * 128 - 64;
+    for (int32_t r0 = 0; r0 < rank; r0 += RPASS) {
+      const int32_t nt = min(NT, (rank - r0 + 7) / 8);
+      const uint32_t step = (2 + nt) * kSlotVec;
+      const int stages = ring_stages(ring_bytes, step);
+      const char* A = reinterpret_cast<const char*>(a.a) +
+                      ((int64_t)t.adapter * a.max_rank + r0) * (int64_t)row_bytes;
+      const uint32_t lane_a = g * row_bytes + 16 * q;
+      uint32_t fetch_off = pair0;  // byte offset in a row of the window to fetch next
+      bool fetch_odd = false;
+      auto fetch = [&](int stage) {
+        if (fetch_off < row_bytes && fetch_off + 16 * q < row_bytes) {  // else past the row's end, and read as 0
+          const uint32_t at = slot + stage * step;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) ring16(sm_u32 + at + h * kSlotVec, xr[h] + fetch_off);
+          // rows between the rank and the next multiple of 8 are in the bank and reach only entries of v that are
+          // set to zero
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (j >= nt) break;
+            ring16(sm_u32 + at + (2 + j) * kSlotVec, A + ((uint64_t)(8 * j) * row_bytes + fetch_off) + lane_a);
+          }
+        }
+        fetch_off += fetch_odd ? jump : 64;
+        fetch_odd = !fetch_odd;
+        ring_commit();
+      };
+      for (int s = 0; s + 1 < stages; ++s) fetch(s);
+      float acc[NT][4] = {};
+      int stage = 0;
+      bool odd = false;
+      for (uint32_t off = pair0; off < row_bytes;
+           off += odd ? jump : 64, odd = !odd, stage = stage + 1 == stages ? 0 : stage + 1) {
+        fetch(stage == 0 ? stages - 1 : stage - 1);
+        ring_wait(stages - 1);
+        __syncwarp();
+        const uint32_t at = slot + stage * step;
+        const bool past = off + 16 * q >= row_bytes;
+        uint4 xa[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          xa[h] = slot16(sm, at + h * kSlotVec);
+          if (past) xa[h] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (j >= nt) break;
+          uint4 av = slot16(sm, at + (2 + j) * kSlotVec);
+          if (past) av = make_uint4(0, 0, 0, 0);
+          mma_bf16(acc[j], xa[0].x, xa[1].x, xa[0].y, xa[1].y, av.x, av.y);
+          mma_bf16(acc[j], xa[0].z, xa[1].z, xa[0].w, xa[1].w, av.z, av.w);
+        }
+      }
+      // the thread's slots are free: the second product's first steps, while the sums meet
+      if (r0 + RPASS >= rank) fetch_first_y();
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(part + (warp * MT + h * 8 + g) * RP + 8 * j + 2 * q) =
+              make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+      __syncthreads();
+      auto own_sum = [&](int m, int r) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) s += part[(k * MT + m) * RP + r];
+        return s;
+      };
+      if (C > 1) {
+        // every CTA of the cluster gets all CTAs' sums (and has read the last pass's)
+        cluster_wait();
+        for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
+          const int m = i / RPASS, r = i % RPASS;
+          const float s = own_sum(m, r);
+          for (uint32_t k = 0; k < C; ++k) push_float(recv + (cr * MT + m) * RP + r, k, s);
+        }
+        cluster_sync();
+      }
+      for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
+        const int m = i / RPASS, r = i % RPASS;
+        float s = 0.f;
+        if (C > 1) {
+          for (uint32_t k = 0; k < C; ++k) s += recv[(k * MT + m) * RP + r];
+        } else {
+          s = own_sum(m, r);
+        }
+        s = r0 + r < rank ? s * t.scale : 0.f;
+        if (r0 + r < R32)
+          for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
+            const uint16_t b = f2bf_rn(s);
+            v[(k * MT + m) * VP + r0 + r] = b;
+            s -= bf16lo(b);
+          }
+      }
+      if (NT == 2)  // the second half of the window of 32
+        for (int k = 0; k < terms; ++k) v[(k * MT + (tid >> 4)) * VP + 16 + (tid & 15)] = 0;
+      if (C > 1 && r0 + RPASS < rank) cluster_arrive();
+      __syncthreads();
+    }
+  }
+
+  // out = y + B v
   int stage = 0;
-  for (int32_t ob = b0; ob < blocks; ob += bstep, stage = stage + 1 == stages ? 0 : stage + 1) {
+  for (int32_t ob = b0; ob < blocks; ob += bstep, stage = stage + 1 == y_stages ? 0 : stage + 1) {
+    fetch_y(ob + (y_stages - 1) * bstep, stage == 0 ? y_stages - 1 : stage - 1);
+    ring_wait(y_stages - 1);
     __syncwarp();
-    fetch(ob + (stages - 1) * bstep, stage == 0 ? stages - 1 : stage - 1);
-    ring_wait(stages - 1);
-    const uint32_t y_at = slot + stage * stage_bytes;
-    uint32_t at = y_at + 2 * MW * y_vecs * kSlotVec;
-    float acc[MW][4][4] = {};
+    const uint32_t y_at = slot + stage * y_step;
+    uint32_t at = y_at + 2 * y_vecs * kSlotVec;
+    float acc[4][4] = {};
     for (int32_t k0 = 0; k0 < R32; k0 += 32) {
       uint4 bv[4];
       const int32_t left = rank - (k0 + 8 * q);
 #pragma unroll
       for (int j = 0; j < 4; ++j, at += kSlotVec) {
-        bv[j] = slot16(at);
+        bv[j] = slot16(sm, at);
         if (left < 8) {  // what lies beyond the rank may hold anything
           bv[j].x &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
           bv[j].y &= left >= 4 ? 0xffffffffu : left == 3 ? 0xffffu : 0u;
@@ -390,79 +373,74 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           bv[j].w &= left == 7 ? 0xffffu : 0u;
         }
       }
-      for (int k = 0; k < terms; ++k)
+      for (int k = 0; k < terms; ++k) {
+        const uint16_t* vr = v + (k * MT + g) * VP + k0 + 8 * q;
+        const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * VP);
+        __syncwarp();
 #pragma unroll
-        for (int m = 0; m < MW; ++m) {
-          const uint16_t* vr = v + (k * MT + m * 16 + g) * VP + k0 + 8 * q;
-          const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * VP);
+        for (int j = 0; j < 4; ++j) mma_bf16(acc[j], lo.x, hi.x, lo.y, hi.y, bv[j].x, bv[j].y);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, bv[j].x, bv[j].y);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, bv[j].z, bv[j].w);
-        }
+        for (int j = 0; j < 4; ++j) mma_bf16(acc[j], lo.z, hi.z, lo.w, hi.w, bv[j].z, bv[j].w);
+      }
     }
     const int32_t c = ob * 32 + lc * q;
     const bool in0 = c < a.out_features, in1 = c + next < a.out_features;
 #pragma unroll
-    for (int m = 0; m < MW; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (tok[m][h] < 0 || !in0) continue;
-        float r[8] = {};
-        if (has_y) {
-          const uint32_t ya = y_at + (2 * m + h) * y_vecs * kSlotVec;
-          const uint4 d = slot16(ya);
-          if (yf) {
-            const uint4 e = slot16(ya + kSlotVec);
-            r[0] = __uint_as_float(d.x);
-            r[1] = __uint_as_float(d.y);
-            r[2] = __uint_as_float(d.z);
-            r[3] = __uint_as_float(d.w);
-            r[4] = __uint_as_float(e.x);
-            r[5] = __uint_as_float(e.y);
-            r[6] = __uint_as_float(e.z);
-            r[7] = __uint_as_float(e.w);
-          } else {
-            unpack8(d, r);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          r[2 * j] += acc[m][j][2 * h];
-          r[2 * j + 1] += acc[m][j][2 * h + 1];
-        }
-        if (a.out_dtype == MOE_DTYPE_F32) {
-          float* p = row_ptr<float>(a.out, tok[m][h], a.out_features) + c;
-          *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
-          if (in1) *reinterpret_cast<float4*>(p + next) = make_float4(r[4], r[5], r[6], r[7]);
+    for (int h = 0; h < 2; ++h) {
+      if (tok[h] < 0 || !in0) continue;
+      float r[8] = {};
+      if (has_y) {
+        const uint32_t ya = y_at + h * y_vecs * kSlotVec;
+        const uint4 d = slot16(sm, ya);
+        if (yf) {
+          const uint4 e = slot16(sm, ya + kSlotVec);
+          r[0] = __uint_as_float(d.x);
+          r[1] = __uint_as_float(d.y);
+          r[2] = __uint_as_float(d.z);
+          r[3] = __uint_as_float(d.w);
+          r[4] = __uint_as_float(e.x);
+          r[5] = __uint_as_float(e.y);
+          r[6] = __uint_as_float(e.z);
+          r[7] = __uint_as_float(e.w);
         } else {
-          uint16_t* p = row_ptr<uint16_t>(a.out, tok[m][h], a.out_features) + c;
-          if (!quads) {
-            store8(p, r);
-          } else {
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
-            if (in1) *reinterpret_cast<uint2*>(p + next) = make_uint2(pack2(r[4], r[5]), pack2(r[6], r[7]));
-          }
+          unpack8(d, r);
         }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[2 * j] += acc[j][2 * h];
+        r[2 * j + 1] += acc[j][2 * h + 1];
+      }
+      if (a.out_dtype == MOE_DTYPE_F32) {
+        float* p = row_ptr<float>(a.out, tok[h], a.out_features) + c;
+        *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
+        if (in1) *reinterpret_cast<float4*>(p + next) = make_float4(r[4], r[5], r[6], r[7]);
+      } else {
+        uint16_t* p = row_ptr<uint16_t>(a.out, tok[h], a.out_features) + c;
+        if (!quads) {
+          store8(p, r);
+        } else {
+          *reinterpret_cast<uint2*>(p) = make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
+          if (in1) *reinterpret_cast<uint2*>(p + next) = make_uint2(pack2(r[4], r[5]), pack2(r[6], r[7]));
+        }
+      }
+    }
   }
+  if (C > 1 && rank == 0) cluster_wait();  // (the arrival at the start)
 }
 
 template <int NT>
 cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tiles, int32_t cluster,
                         cudaStream_t s) {
-  constexpr int MW = 1, MT = 16, KG = kLoraWarps, RP = 8 * NT + 8;
+  constexpr int MT = 16, RP = 8 * NT + 8;
   const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;
-  // ring: four steps where two CTAs fit an SM with them, else as many as do
-  // (two at least), else one CTA an SM
+  // up to four ring steps, as many as let two CTAs share an SM if those are two or more, else as fit one
   const uint32_t y_vecs = !a.y.data ? 0 : a.y_dtype == MOE_DTYPE_F32 ? 2 : 1;
-  const uint32_t step = std::max<uint32_t>(2 * MW + NT, 4 * ((a.max_rank + 31) / 32) + 2 * MW * y_vecs) * kSlotVec;
-  const uint32_t rest = (cluster > 1 ? MT * RP * 4 : 0) + terms * MT * VP * 2;
-  const uint32_t two = 112 * 1024 - rest;
-  uint32_t ring = std::min(4 * step, 2 * step <= two ? two / step * step : 4 * step);
-  ring = std::min(ring, (200 * 1024 - rest) / step * step);
-  ring = std::max<uint32_t>({ring, (uint32_t)(KG * MT * RP * 4), (uint32_t)((kFusedTokens + kLoraWarps) * 4)});
+  const uint32_t step = std::max<uint32_t>(2 + NT, 4 * ((a.max_rank + 31) / 32) + 2 * y_vecs) * kSlotVec;
+  const uint32_t rest = (kLoraWarps + (cluster > 1 ? cluster : 0)) * MT * RP * 4 + terms * MT * VP * 2;
+  const uint32_t room = (rest + 2 * step <= 112 * 1024 ? 112 * 1024 : 220 * 1024) - rest;
+  const uint32_t ring = std::min(4u, room / step) * step;
   static std::atomic<bool> configured[kMaxDevices];
   cudaError_t e = raise_smem_limit(lora_kernel<NT>, 220 * 1024, configured);
   if (e != cudaSuccess) return e;

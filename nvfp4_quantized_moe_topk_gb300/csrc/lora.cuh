@@ -43,8 +43,7 @@ __device__ __forceinline__ int32_t bucket_of(int32_t id, int32_t L) { return id 
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -62,6 +61,14 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores v at this CTA's shared address `p`, in CTA `rank` of the cluster.
+__device__ __forceinline__ void push_float(float* p, uint32_t rank, float v) {
+  uint32_t addr;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 // The float at this CTA's shared address `p`, in CTA `rank` of the cluster.
 __device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
   uint32_t addr;
@@ -71,67 +78,99 @@ __device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
   return v;
 }
 
-// What a CTA works on.
+// What a CTA works on: up to MT tokens of an adapter (n_adapters: tokens
+// without one, rank 0).
 struct Tile {
-  int32_t adapter, count;
+  int32_t adapter, count, rank;
+  float scale;
 };
+__device__ __forceinline__ int32_t adapter_rank(const moe_lora_args& a, int32_t l) {
+  if (l >= a.n_adapters) return 0;
+  return a.ranks ? min(max(a.ranks[l], 0), a.max_rank) : a.max_rank;
+}
+__device__ __forceinline__ float adapter_scale(const moe_lora_args& a, int32_t l) {
+  return l < a.n_adapters && a.scale ? a.scale[l] : 1.f;
+}
 
-// Finds this CTA's tile and its tokens (row[i], -1 past the count).  Returns
-// false, for the whole cluster alike, where there is none left.
+// Finds this CTA's tile in the plan and its tokens (row[i], -1 past the
+// count).  Returns false, for the whole cluster alike, where there is none left.
 template <int MT>
-__device__ __forceinline__ bool find_tile(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tile,
-                                          int32_t* row, int32_t* scratch, Tile& t) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, L = a.n_adapters;
+__device__ __forceinline__ bool planned_tile(const moe_lora_args& a, const LoraPlan& p, int32_t tile, int32_t* row,
+                                             Tile& t) {
+  const int tid = threadIdx.x, L = a.n_adapters;
   __shared__ int32_t found[3];
   if (tid == 0) found[0] = -1;
   if (tid < MT) row[tid] = -1;
-  if (!fused) {
-    pdl_wait();
-    __syncthreads();
-    for (int32_t l = tid; l <= L; l += kLoraThreads) {
-      const int32_t b0 = p.tile_base[l], b1 = p.tile_base[l + 1];
-      if (tile >= b0 && tile < b1) {
-        const int32_t first = p.starts[l] + (tile - b0) * MT;
-        found[0] = l;
-        found[1] = first;
-        found[2] = min(MT, p.starts[l + 1] - first);
-      }
+  pdl_wait();
+  __syncthreads();
+  for (int32_t l = tid; l <= L; l += kLoraThreads) {
+    const int32_t b0 = p.tile_base[l], b1 = p.tile_base[l + 1];
+    if (tile >= b0 && tile < b1) {
+      const int32_t first = p.starts[l] + (tile - b0) * MT;
+      found[0] = l;
+      found[1] = first;
+      found[2] = min(MT, p.starts[l + 1] - first);
     }
-    __syncthreads();
-    t.adapter = found[0];
-    if (t.adapter < 0) return false;
-    t.count = found[2];
-    if (tid < t.count) row[tid] = p.order[found[1] + tid];
-    __syncthreads();
-    return true;
   }
-  // ids in shared memory; a token whose rank among its adapter's is a multiple
-  // of MT leads a tile, tiles in the order of their leaders
-  const int32_t n = a.n;
+  __syncthreads();
+  t.adapter = found[0];
+  if (t.adapter < 0) return false;
+  t.count = found[2];
+  t.rank = adapter_rank(a, t.adapter);
+  t.scale = adapter_scale(a, t.adapter);
+  if (tid < t.count) row[tid] = p.order[found[1] + tid];
+  __syncthreads();
+  return true;
+}
+
+// The same without a plan, for at most one token a thread: every CTA ranks the
+// ids itself.  A token whose rank among its adapter's is a multiple of MT leads
+// a tile, tiles in the order of their leaders.
+template <int MT>
+__device__ __forceinline__ bool ranked_tile(const moe_lora_args& a, int32_t tile, int32_t* row, int32_t* scratch,
+                                            Tile& t) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, L = a.n_adapters, n = a.n;
+  __shared__ int32_t found[4];
   int32_t* leaders = scratch + kFusedTokens;  // per warp
   const int32_t mine = tid < n ? bucket_of(a.adapter_ids[tid], L) : -1;
+  if (tid == 0) found[0] = -1;
+  if (tid < MT) row[tid] = -1;
   scratch[tid] = mine;
-  __syncthreads();
-  int32_t rank = 0;
-  const int4* ids4 = reinterpret_cast<const int4*>(scratch);
-  for (int32_t i = 0; i < (tid & ~31); i += 4) {  // the warps before this one
-    const int4 v = ids4[i >> 2];
-    rank += (v.x == mine) + (v.y == mine) + (v.z == mine) + (v.w == mine);
+  int32_t my_rank = 0;
+  float my_scale = 0.f;
+  if (mine >= 0) {  // (on their way while the ranks are found)
+    my_rank = adapter_rank(a, mine);
+    my_scale = adapter_scale(a, mine);
   }
-  rank += __popc(__match_any_sync(0xffffffffu, mine) & ((1u << lane) - 1u));
+  int32_t rank = __popc(__match_any_sync(0xffffffffu, mine) & ((1u << lane) - 1u));
+  if (n > 32) {
+    __syncthreads();
+    const int4* ids4 = reinterpret_cast<const int4*>(scratch);
+    const int32_t before = warp * 32 < n ? warp * 32 : 0;  // the warps before this one
+#pragma unroll 8
+    for (int32_t i = 0; i < before; i += 4) {
+      const int4 v = ids4[i >> 2];
+      rank += (v.x == mine) + (v.y == mine) + (v.z == mine) + (v.w == mine);
+    }
+  }
   const bool leads = mine >= 0 && rank % MT == 0;
   const uint32_t lead = __ballot_sync(0xffffffffu, leads);
   if (lane == 0) leaders[warp] = __popc(lead);
   __syncthreads();
   int32_t at = __popc(lead & ((1u << lane) - 1u));
-  for (int w = 0; w < warp; ++w) at += leaders[w];
+#pragma unroll
+  for (int w = 0; w < kLoraWarps; ++w) at += w < warp ? leaders[w] : 0;
   if (leads && at == tile) {
     found[0] = mine;
     found[1] = rank / MT;
+    found[2] = my_rank;
+    found[3] = __float_as_int(my_scale);
   }
   __syncthreads();
   t.adapter = found[0];
   if (t.adapter < 0) return false;
+  t.rank = found[2];
+  t.scale = __int_as_float(found[3]);
   const bool in = mine == t.adapter && rank / MT == found[1];
   if (in) row[rank % MT] = tid;
   t.count = __syncthreads_count(in);
@@ -145,11 +184,10 @@ __device__ __forceinline__ void ring16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void ring8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint4 slot16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
+// 16 bytes of shared memory at offset `at` of the CTA's dynamic part.  (A plain
+// load: what orders it after the copies is ring_wait, and in between the
+// compiler may move it ahead of matrix instructions.)
+__device__ __forceinline__ uint4 slot16(const char* sm, uint32_t at) { return *reinterpret_cast<const uint4*>(sm + at); }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most `ahead` (0..3) of the thread's newest groups are unfinished.
 __device__ __forceinline__ void ring_wait(int ahead) {
@@ -159,6 +197,11 @@ __device__ __forceinline__ void ring_wait(int ahead) {
     case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
     default: asm volatile("cp.async.wait_group 3;" ::: "memory");
   }
+}
+
+// Ring stages of `step` bytes that fit, at most four.
+__device__ __forceinline__ int ring_stages(uint32_t bytes, uint32_t step) {
+  return 1 + (bytes >= 2 * step) + (bytes >= 3 * step) + (bytes >= 4 * step);
 }
 
 constexpr uint32_t kSlotVec = kLoraThreads * 16;  // one 16-byte vector of every thread

@@ -42,18 +42,14 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   const int group = warp & 3, half = warp >> 2, htid = tid & (kHalf - 1);
   const uint32_t C = cluster_size(), cr = cluster_rank();
   Tile t;
-  if (!find_tile<kRowsTile>(a, plan, false, (int32_t)(blockIdx.x / C), row, nullptr, t)) return;
-  int32_t rank = 0;
-  float scale = 0.f;
-  if (t.adapter < a.n_adapters) {
-    rank = a.ranks ? min(max(a.ranks[t.adapter], 0), a.max_rank) : a.max_rank;
-    scale = a.scale ? a.scale[t.adapter] : 1.f;
-  }
+  if (!planned_tile<kRowsTile>(a, plan, (int32_t)(blockIdx.x / C), row, t)) return;
+  const int32_t rank = t.rank;
+  const float scale = t.scale;
   // ring; v [terms][64][VP] bf16; in a cluster the CTA's sums [64][kPartPitch].  Between the loops the ring holds
   // the halves' sums [2][64][kPartPitch].
   const int32_t kwins = (rank + 31) / 32;
   const uint32_t v_pitch = (uint32_t)((a.max_rank + 63) / 64) * 128;  // bytes
-  const uint32_t ring = smem_u32(sm), v_at = ring + ring_bytes;
+  const uint32_t sm_u32 = smem_u32(sm), v_at = ring_bytes;  // (offsets in sm; cp.async takes addresses)
   char* v_base = sm + ring_bytes;
   float* part = reinterpret_cast<float*>(sm);
   float* sum = reinterpret_cast<float*>(v_base + terms * kRowsTile * v_pitch);
@@ -73,7 +69,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
       const int32_t nt = min(kPass / 8, (rank - r0 + 15) / 16 * 2);  // groups of 8 ranks, in pairs
       const int32_t a_rows = min(8 * nt, a.max_rank - r0);  // rows past the rank reach only entries of v that are set to zero
       const uint32_t step = shrink_step(nt);
-      const int stages = (int)min(4u, ring_bytes / step);
+      const int stages = ring_stages(ring_bytes, step);
       const uint32_t a_at = 4 * kHalfVec;  // of the half's part of a step: x, then A
       // this thread's 16-byte piece of A: row ar + 16 i, piece ap
       const int32_t ar = htid >> 3, ap = htid & 7;
@@ -81,21 +77,21 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
       const uint32_t a_to = a_at + ar * 128 + ((ap ^ ((ar & 1) << 2)) * 16);
       auto fetch = [&](uint32_t off, int stage) {
         if (off < row_bytes) {
-          const uint32_t at = ring + stage * step + half * (step / 2);
+          const uint32_t at = stage * step + half * (step / 2);
           const uint32_t slot = at + htid * 16;
           if (off + 16 * q < row_bytes) {
-            ring16(slot, x0 + off);
-            ring16(slot + kHalfVec, x1 + off);
+            ring16(sm_u32 + slot, x0 + off);
+            ring16(sm_u32 + slot + kHalfVec, x1 + off);
           }
           if (off + 64 + 16 * q < row_bytes) {
-            ring16(slot + 2 * kHalfVec, x0 + off + 64);
-            ring16(slot + 3 * kHalfVec, x1 + off + 64);
+            ring16(sm_u32 + slot + 2 * kHalfVec, x0 + off + 64);
+            ring16(sm_u32 + slot + 3 * kHalfVec, x1 + off + 64);
           }
           if (off + 16 * ap < row_bytes) {
             const char* src = Ap + off;
 #pragma unroll
             for (int i = 0; i < kPass / 16; ++i)
-              if (ar + 16 * i < a_rows) ring16(at + a_to + i * 16 * 128, src + (uint64_t)(16 * i) * row_bytes);
+              if (ar + 16 * i < a_rows) ring16(sm_u32 + at + a_to + i * 16 * 128, src + (uint64_t)(16 * i) * row_bytes);
           }
         }
         ring_commit();
@@ -108,18 +104,18 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
         half_barrier(half);  // the step is there for all, and the one before has been read
         fetch(off + (stages - 1) * jump, stage == 0 ? stages - 1 : stage - 1);
         __syncwarp();
-        const uint32_t at = ring + stage * step + half * (step / 2);
+        const uint32_t at = stage * step + half * (step / 2);
         const bool tail = off + 128 > row_bytes;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          uint4 xa0 = slot16(at + htid * 16 + (2 * w) * kHalfVec), xa1 = slot16(at + htid * 16 + (2 * w + 1) * kHalfVec);
+          uint4 xa0 = slot16(sm, at + htid * 16 + (2 * w) * kHalfVec), xa1 = slot16(sm, at + htid * 16 + (2 * w + 1) * kHalfVec);
           const bool past = tail && off + 64 * w + 16 * q >= row_bytes;
           if (past) xa0 = xa1 = make_uint4(0, 0, 0, 0);
           const uint32_t from = at + a_at + g * 128 + (((w * 4 + q) ^ ((g & 1) << 2)) * 16);
 #pragma unroll
           for (int j = 0; j < kPass / 8; j += 2) {
             if (j >= nt) break;
-            uint4 b0 = slot16(from + j * 1024), b1 = slot16(from + (j + 1) * 1024);
+            uint4 b0 = slot16(sm, from + j * 1024), b1 = slot16(sm, from + (j + 1) * 1024);
             if (past) b0 = b1 = make_uint4(0, 0, 0, 0);
             mma_bf16(acc[j], xa0.x, xa1.x, xa0.y, xa1.y, b0.x, b0.y);
             mma_bf16(acc[j + 1], xa0.x, xa1.x, xa0.y, xa1.y, b1.x, b1.y);
@@ -191,11 +187,12 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   const char* y0 = static_cast<const char*>(a.y.data) + t0 * ys + lc * q * y_size;
   const char* y1 = static_cast<const char*>(a.y.data) + t1 * ys + lc * q * y_size;
   const uint32_t step = max(expand_step(kwins, y_vecs), 32u);
-  const int stages = (int)min(4u, ring_bytes / step);
+  const int stages = ring_stages(ring_bytes, step);
+  const bool odd_rank = rank & 7;  // its last 16-byte piece of B is masked where it is read
   const int32_t blocks = (a.out_features + 63) / 64, b0 = (int32_t)cr * 2 + half, bstep = (int32_t)C * 2;
   auto fetch = [&](int32_t ob, int stage) {
     if (ob < blocks) {
-      const uint32_t at = ring + stage * step + half * (step / 2);
+      const uint32_t at = stage * step + half * (step / 2);
       const int32_t left = a.out_features - ob * 64;
       if (has_y) {
         uint32_t slot = at + htid * 16;
@@ -206,25 +203,25 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           const uint32_t ew = e + w * 32 * y_size;
           if (yf) {
             if (in0) {
-              ring16(slot, y0 + ew);
-              ring16(slot + 2 * kHalfVec, y1 + ew);
+              ring16(sm_u32 + slot, y0 + ew);
+              ring16(sm_u32 + slot + 2 * kHalfVec, y1 + ew);
             }
             if (in1) {
-              ring16(slot + kHalfVec, y0 + ew + 64);
-              ring16(slot + 3 * kHalfVec, y1 + ew + 64);
+              ring16(sm_u32 + slot + kHalfVec, y0 + ew + 64);
+              ring16(sm_u32 + slot + 3 * kHalfVec, y1 + ew + 64);
             }
           } else if (quads) {
             if (in0) {
-              ring8(slot, y0 + ew);
-              ring8(slot + kHalfVec, y1 + ew);
+              ring8(sm_u32 + slot, y0 + ew);
+              ring8(sm_u32 + slot + kHalfVec, y1 + ew);
             }
             if (in1) {
-              ring8(slot + 8, y0 + ew + 32);
-              ring8(slot + kHalfVec + 8, y1 + ew + 32);
+              ring8(sm_u32 + slot + 8, y0 + ew + 32);
+              ring8(sm_u32 + slot + kHalfVec + 8, y1 + ew + 32);
             }
           } else if (in0) {
-            ring16(slot, y0 + ew);
-            ring16(slot + kHalfVec, y1 + ew);
+            ring16(sm_u32 + slot, y0 + ew);
+            ring16(sm_u32 + slot + kHalfVec, y1 + ew);
           }
           slot += 2 * y_vecs * kHalfVec;
         }
@@ -233,11 +230,14 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
       const char* src = B + (uint64_t)((uint32_t)ob * 64) * b_bytes;
       for (int32_t k = 0; k < kwins; ++k) {
         const int32_t p = k * 4 + (htid & 3);
-        if (8 * p >= rank) continue;  // read as 0
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int32_t o = (htid >> 2) + 32 * i;
-          if (o < left) ring16(b_at + o * b_pitch + ((p ^ ((o & 1) * swap)) * 16), src + o * b_bytes + 16 * p);
+          const uint32_t to = b_at + o * b_pitch + ((p ^ ((o & 1) * swap)) * 16);
+          if (8 * p >= rank)  // what lies beyond the rank may hold anything
+            *reinterpret_cast<uint4*>(sm + to) = make_uint4(0, 0, 0, 0);
+          else if (o < left)
+            ring16(sm_u32 + to, src + o * b_bytes + 16 * p);
         }
       }
     }
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
     ring_wait(stages - 2);
     half_barrier(half);
     fetch(ob + (stages - 1) * bstep, stage == 0 ? stages - 1 : stage - 1);
-    const uint32_t at = ring + stage * step + half * (step / 2);
+    const uint32_t at = stage * step + half * (step / 2);
     const uint32_t b_at = at + 4 * y_vecs * kHalfVec;
     float acc[2][4][4] = {};
     for (int32_t k = 0; k < kwins; ++k) {
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
       for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          bv[w][j] = slot16(from + (w * 32 + (j >> 1) * next + 2 * (j & 1)) * b_pitch);
-          if (left < 8) {  // what lies beyond the rank may hold anything
+          bv[w][j] = slot16(sm, from + (w * 32 + (j >> 1) * next + 2 * (j & 1)) * b_pitch);
+          if (odd_rank && left < 8) {
             bv[w][j].x &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
             bv[w][j].y &= left >= 4 ? 0xffffffffu : left == 3 ? 0xffffu : 0u;
             bv[w][j].z &= left >= 6 ? 0xffffffffu : left == 5 ? 0xffffu : 0u;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
         }
       const uint32_t vp = v_at + (group * 16 + g) * v_pitch + (k / 2) * 128 + ((((k & 1) * 4 + q) ^ ((g & 1) << 2)) * 16);
       for (int i = 0; i < terms; ++i) {
-        const uint4 lo = slot16(vp + i * kRowsTile * v_pitch), hi = slot16(vp + (i * kRowsTile + 8) * v_pitch);
+        const uint4 lo = slot16(sm, vp + i * kRowsTile * v_pitch), hi = slot16(sm, vp + (i * kRowsTile + 8) * v_pitch);
         __syncwarp();
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -292,9 +292,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
         float r[8] = {};
         if (has_y) {
           const uint32_t ya = at + htid * 16 + (2 * w + h) * y_vecs * kHalfVec;
-          const uint4 d = slot16(ya);
+          const uint4 d = slot16(sm, ya);
           if (yf) {
-            const uint4 e = slot16(ya + kHalfVec);
+            const uint4 e = slot16(sm, ya + kHalfVec);
             r[0] = __uint_as_float(d.x);
             r[1] = __uint_as_float(d.y);
             r[2] = __uint_as_float(d.z);
