@@ -82,6 +82,21 @@ __device__ __forceinline__ int32_t first_seq(const moe_router_args& a, int32_t t
   return lo;
 }
 
+// The same for a block, by all its threads at once where there are not too
+// many sequences (a binary search is a chain of dependent loads).
+__device__ __forceinline__ int32_t block_first_seq(const moe_router_args& a, int32_t t, int32_t* s_min) {
+  if (!a.seq_offsets || a.n_seqs > 4096) return first_seq(a, t);
+  if (threadIdx.x == 0) *s_min = a.n_seqs;
+  __syncthreads();
+  for (int32_t i = threadIdx.x; i < a.n_seqs; i += blockDim.x)
+    if (seq_bound(a, i + 1) > t) {
+      atomicMin(s_min, i);
+      break;
+    }
+  __syncthreads();
+  return *s_min;
+}
+
 // A lane's N experts of a row.  VEC: groups of 4 (rows aligned to 16 bytes),
 // else one by one.
 template <bool VEC, int N>
@@ -122,7 +137,9 @@ struct Row {
 
 // A token's softmax from its logits (-inf past the last expert), in place; a
 // row without any logit above -inf gives p = 0.  s_bias: the bias in shared
-// memory, or nullptr.
+// memory, or nullptr.  The exponential is that of 2 in hardware (2 units in the
+// last place, and the rounding of (z - max) log2 e: 1e-7 to 1e-6 of p); p below
+// 2^-126 counts as 0.
 template <bool VEC, int N>
 __device__ __forceinline__ void softmax_row(const float* s_bias, int32_t E, int lane, float (&z)[N]) {
   if (s_bias) {
@@ -139,7 +156,7 @@ __device__ __forceinline__ void softmax_row(const float* s_bias, int32_t E, int 
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    z[i] = expf(z[i] - m);
+    z[i] = __expf(z[i] - m);
     sum += z[i];
   }
   sum = warp_add(sum);
@@ -169,13 +186,45 @@ __device__ __forceinline__ float block_sum(float v, float* s_warp) {
   return v;
 }
 
+// A warp's tokens in a block's range [lo, hi): group j holds tokens lo + warp +
+// kLossWarps (TOK j + u), u < TOK.  A group's loads do not depend on the
+// sequences, so the first group is on its way while those are looked up.
+template <bool VEC, int N>
+struct Group {
+  static constexpr int TOK = N >= 16 ? 1 : 16 / N;
+  static constexpr int kSpan = kLossWarps * TOK;
+  int32_t j;  // which group is loaded (-1: none)
+  float z[TOK][N];
+  int32_t id[TOK];
+  bool on[TOK];  // the token takes part in the loss
+
+  static __device__ __forceinline__ int64_t token(int32_t lo, int32_t j, int u) {
+    return (int64_t)lo + (threadIdx.x >> 5) + kLossWarps * ((int64_t)TOK * j + u);
+  }
+  __device__ __forceinline__ void load(const moe_router_args& a, int32_t lo, int32_t hi, int32_t group, bool logits,
+                                       bool ids) {
+    const int lane = threadIdx.x & 31;
+    j = group;
+#pragma unroll
+    for (int u = 0; u < TOK; ++u) {
+      const int64_t t = token(lo, j, u);
+      id[u] = -1;
+      on[u] = t < hi;
+      if (t >= hi) continue;
+      if (logits) Row<VEC, N>::load(a.logits + t * a.n_experts, a.n_experts, lane, z[u], -INFINITY);
+      if (ids && lane < a.top_k) id[u] = a.topk_ids[t * a.top_k + lane];
+      if (a.token_mask) on[u] = a.token_mask[t];
+    }
+  }
+};
+
 template <bool VEC, int N>
 __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
     balance_kernel(const moe_router_args a, const LossSpace ws, int32_t per_block, float* __restrict__ prob_sums,
                    float* __restrict__ loss) {
-  constexpr int TOK = N >= 16 ? 1 : 16 / N;  // tokens of a warp at a time
+  constexpr int TOK = Group<VEC, N>::TOK, kSpan = Group<VEC, N>::kSpan;
   extern __shared__ __align__(16) float sm[];  // [kLossWarps][pitch] sums, bias, picks
-  __shared__ int32_t s_toks;
+  __shared__ int32_t s_toks, s_first;
   __shared__ float s_warp[kLossWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.n_experts, k = a.top_k;
   const int32_t pitch = row_pitch(E);
@@ -183,43 +232,40 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
   int32_t* s_picks = reinterpret_cast<int32_t*>(s_bias + pitch);
   const bool alone = gridDim.x == 1;
   pdl_launch_dependents();
+  const int32_t lo = (int32_t)min((int64_t)blockIdx.x * per_block, (int64_t)a.n);
+  const int32_t hi = (int32_t)min((int64_t)lo + per_block, (int64_t)a.n);
+  Group<VEC, N> gr;
+  gr.load(a, lo, hi, 0, true, true);
   if (blockIdx.x == 0 && threadIdx.x == 0 && !alone) *ws.ticket = 0;
   for (int32_t e = threadIdx.x; e < E; e += kLossThreads) {
     if (a.bias) s_bias[e] = a.bias[e];
     s_picks[e] = 0;
   }
   if (threadIdx.x == 0) s_toks = 0;
+  const int32_t s0 = alone ? 0 : block_first_seq(a, lo, &s_first);
   __syncthreads();
-  const int32_t lo = (int32_t)min((int64_t)blockIdx.x * per_block, (int64_t)a.n);
-  const int32_t hi = (int32_t)min((int64_t)lo + per_block, (int64_t)a.n);
   float total_dot = 0.f;
   int32_t total = 0;
-  for (int32_t s = alone ? 0 : first_seq(a, lo); s < a.n_seqs; ++s) {
+  for (int32_t s = s0; s < a.n_seqs; ++s) {
     const int32_t at = seq_bound(a, s);
     if (!alone && at >= hi) break;
     const int32_t beg = max(lo, at), end = min(hi, seq_bound(a, s + 1));
     if (!alone && beg >= end) continue;
     float acc[N] = {};
     int32_t toks = 0;
-    for (int64_t t = (int64_t)beg + warp; t < end; t += kLossWarps * TOK) {
-      float z[TOK][N];
-      bool on[TOK];
+    for (int32_t j = (beg - lo) / kSpan; beg < end && j <= (end - 1 - lo) / kSpan; ++j) {
+      if (gr.j != j) gr.load(a, lo, hi, j, true, true);
+      gr.j = -1;
 #pragma unroll
       for (int u = 0; u < TOK; ++u) {
-        const int64_t tu = t + u * kLossWarps;
-        on[u] = tu < end && (!a.token_mask || a.token_mask[tu]);
-        if (on[u]) Row<VEC, N>::load(a.logits + tu * E, E, lane, z[u], -INFINITY);
-        const int32_t e = on[u] && lane < k ? a.topk_ids[tu * k + lane] : -1;
-        if (e >= 0 && e < E) atomicAdd(&s_picks[e], 1);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int u = 0; u < TOK; ++u) {
-        if (!on[u]) continue;
+        const int64_t t = Group<VEC, N>::token(lo, j, u);
+        if (t < beg || t >= end || !gr.on[u]) continue;
         ++toks;
-        softmax_row<VEC, N>(a.bias ? s_bias : nullptr, E, lane, z[u]);
+        if (gr.id[u] >= 0 && gr.id[u] < E) atomicAdd(&s_picks[gr.id[u]], 1);
+        __syncwarp();
+        softmax_row<VEC, N>(a.bias ? s_bias : nullptr, E, lane, gr.z[u]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += z[u][i];
+        for (int i = 0; i < N; ++i) acc[i] += gr.z[u][i];
       }
     }
     Row<VEC, N>::store(sm + warp * pitch, E, lane, acc);
@@ -275,6 +321,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int32_t b0 = beg / per_block, b1 = end > beg ? (end - 1) / per_block : b0 - 1;
   const int32_t parts = kJoinThreads / cols, part = tid / cols, col = tid % cols;  // cols: a power of two
   pdl_wait();
+  int32_t toks = 0;
+  for (int32_t b = b0 + tid; b <= b1; b += kJoinThreads) toks += ws.toks[(int64_t)b + s];
   float dot = 0.f;
   for (int32_t e0 = 0; e0 < E; e0 += cols) {
     const int32_t e = e0 + col;
@@ -301,8 +349,6 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
     __syncthreads();
   }
-  int32_t toks = 0;
-  for (int32_t b = b0 + tid; b <= b1; b += kJoinThreads) toks += ws.toks[(int64_t)b + s];
   s_pick[tid] = toks;
   dot = block_sum(dot, s_warp);
   if (tid < 32) {
@@ -339,8 +385,9 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
     router_backward_kernel(const moe_router_args a, const float* __restrict__ w, const float* __restrict__ dw,
                            const float* __restrict__ d_loss, float* __restrict__ d_logits, float* __restrict__ sums,
                            int32_t per_block) {
-  constexpr int TOK = N >= 16 ? 1 : 16 / N;
+  constexpr int TOK = N >= 16 ? 1 : 8 / N;
   extern __shared__ __align__(16) float sm[];  // [kLossWarps][pitch] the warps' rows, bias, g
+  __shared__ int32_t s_first;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.n_experts, k = a.top_k;
   const int32_t pitch = row_pitch(E);
   float* pick = sm + warp * pitch;  // zero between tokens
@@ -353,13 +400,12 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
   const int32_t lo = (int32_t)min((int64_t)blockIdx.x * per_block, (int64_t)a.n);
   const int32_t hi = (int32_t)min((int64_t)lo + per_block, (int64_t)a.n);
   float acc[N] = {};
-  float scale = 0.f;
-  if (a.counts) {
-    const int32_t total = a.tokens[a.n_seqs];
-    if (total > 0) scale = a.coef * (d_loss ? d_loss[0] : 1.f) * ((float)E / ((float)total * (float)k));
-  }
+  const int32_t total = a.counts ? a.tokens[a.n_seqs] : 0;
+  const float up = d_loss ? d_loss[0] : 1.f;
+  int32_t s = a.counts ? block_first_seq(a, lo, &s_first) : 0;
+  const float scale = total > 0 ? a.coef * up * ((float)E / ((float)total * (float)k)) : 0.f;
   // the sequences that meet the block (without a loss term: all its tokens at once)
-  for (int32_t s = a.counts ? first_seq(a, lo) : 0, at = lo; at < hi;) {
+  for (int32_t at = lo; at < hi;) {
     int32_t end = hi;
     bool lossy = false;
     if (a.counts && s < a.n_seqs) {
