@@ -498,6 +498,12 @@ MOE_API moe_status moe_lora_apply(const moe_lora_args *args, void *workspace, si
                                   moe_stream_t stream);
 MOE_API size_t moe_lora_workspace_bytes(int32_t n, int32_t n_adapters);
 
+/* Reads and clears the current device's error flags of moe_lora_apply: 0, or
+ * MOE_DEVFLAG_TIMEOUT where a bounded wait inside the kernel for long batches
+ * ran out (that call's out is then undefined).  Synchronizes the device.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+MOE_API moe_status moe_lora_get_device_error(int32_t *flags);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,8 @@ ENTRY_POINTS = ("moe_nvfp4_status_string", "moe_nvfp4_create", "moe_nvfp4_destro
                 "nvfp4_matmul", "weighted_row_sum", "moe_nvfp4_forward_noalloc", "moe_router_topk",
                 "moe_nvfp4_shared_expert_forward", "moe_nvfp4_debug_offset_grid_barrier", "moe_block_norm",
                 "moe_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_balance_loss", "moe_router_backward",
-                "moe_router_workspace_bytes", "moe_lora_apply", "moe_lora_workspace_bytes")
+                "moe_router_workspace_bytes", "moe_lora_apply", "moe_lora_workspace_bytes",
+                "moe_lora_get_device_error")
 
 _lock = threading.Lock()
 _lib = None
@@ -100,6 +101,7 @@ def load(build_if_missing: bool = False):
         L.moe_router_workspace_bytes.argtypes = [i32, i32, i32]
         L.moe_lora_apply.argtypes = [vp, vp, sz, vp]
         L.moe_lora_workspace_bytes.argtypes = [i32, i32]
+        L.moe_lora_get_device_error.argtypes = [ctypes.POINTER(i32)]
         for name in ENTRY_POINTS:
             if name.endswith("_workspace_bytes"):
                 getattr(L, name).restype = sz
@@ -395,3 +397,10 @@ def lora_apply(x, adapter_ids, a, b, y, out, *, scale=None, ranks=None, workspac
         workspace = _new_workspace(_lib.moe_lora_workspace_bytes(x.shape[0], a.shape[0]), x, stream)
     native.lora_apply(x, adapter_ids, a, b, y, out, scale, ranks, workspace, stream)
     return out
+
+
+def lora_device_error() -> int:
+    """Reads and clears lora_apply's device error flags (DEVFLAG_TIMEOUT); synchronizes the device."""
+    f = ctypes.c_int32()
+    _check(load().moe_lora_get_device_error(ctypes.byref(f)), "moe_lora_get_device_error")
+    return f.value

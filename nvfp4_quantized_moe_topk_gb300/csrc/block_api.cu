@@ -172,4 +172,9 @@ moe_status moe_lora_apply(const moe_lora_args* args, void* workspace, size_t wor
   return status_of(launch_lora(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_lora_get_device_error(int32_t* flags) {
+  if (!flags) return MOE_ERR_INVALID_ARG;
+  return status_of(lora_device_flags(flags));
+}
+
 }  // extern "C"

@@ -241,6 +241,7 @@ cudaError_t launch_router_backward(const moe_router_args& a, const float* w, con
 constexpr int kLoraMaxRank = 128;
 size_t lora_workspace(int32_t n, int32_t n_adapters);  // bytes
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s);
+cudaError_t lora_device_flags(int32_t* flags);  // synchronizes the device; reads and clears
 
 // Host helpers for tensor maps (driver entry point resolved at run time).
 cudaError_t make_tmap_act(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K);

@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 constexpr int kSmallTokens = 1024;  // more than these take lora_rows.cu
+constexpr int kMmaTiles = 96;       // from this many full tiles of 128 on, lora_mma.cu
 
 // Tiles of 16 tokens; NT groups of 8 ranks a pass of the first product.
 template <int NT>
@@ -471,8 +472,8 @@ size_t lora_workspace(int32_t n, int32_t n_adapters) {
 
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s) {
   const int32_t n = a.n, L = a.n_adapters;
-  const bool fused = n <= kFusedTokens, rows = n > kSmallTokens;
-  const int32_t mt = rows ? kRowsTile : 16;
+  const bool fused = n <= kFusedTokens, rows = n > kSmallTokens, mma = n >= kMmaTokens * kMmaTiles && lora_mma_fits(a);
+  const int32_t mt = mma ? kMmaTokens : rows ? kRowsTile : 16;
   const LoraPlan p = fused ? LoraPlan{} : lora_plan(workspace, n, L);
   if (!fused) {
     const int32_t slices = plan_slices(n);
@@ -488,6 +489,7 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
   }
   // every group has at most one tile that is not full
   const int32_t tiles = n / mt + std::min(n, L + 1);
+  if (mma) return launch_lora_mma(a, p, tiles, s);
   if (rows) return launch_lora_rows(a, p, tiles, s);
   int32_t cluster = 1;
   while (cluster < 8 && tiles * cluster * 2 <= 608) cluster *= 2;

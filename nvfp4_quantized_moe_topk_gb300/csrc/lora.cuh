@@ -189,13 +189,14 @@ __device__ __forceinline__ void ring8(uint32_t dst, const void* src) {
 // compiler may move it ahead of matrix instructions.)
 __device__ __forceinline__ uint4 slot16(const char* sm, uint32_t at) { return *reinterpret_cast<const uint4*>(sm + at); }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `ahead` (0..3) of the thread's newest groups are unfinished.
+// Waits until at most `ahead` (0..4) of the thread's newest groups are unfinished.
 __device__ __forceinline__ void ring_wait(int ahead) {
   switch (ahead) {
     case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
     case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
     case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 3;" ::: "memory");
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 4;" ::: "memory");
   }
 }
 
@@ -205,6 +206,11 @@ __device__ __forceinline__ int ring_stages(uint32_t bytes, uint32_t step) {
 }
 
 constexpr uint32_t kSlotVec = kLoraThreads * 16;  // one 16-byte vector of every thread
+
+// lora_mma.cu: at most `tiles` tiles of kMmaTokens tokens; whether a call's sizes fit its shared memory.
+constexpr int kMmaTokens = 128;
+cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, cudaStream_t s);
+bool lora_mma_fits(const moe_lora_args& a);
 
 // lora_rows.cu: at most `tiles` tiles of kRowsTile tokens.
 constexpr int kRowsTile = 64;

@@ -254,3 +254,107 @@ def test_refusals(dev):
         with pytest.raises(api.MoeError) as e:
             t.run()
         assert e.value.status == 2, (inp, o, R)
+
+
+# ------------------------------------------------------------------ batches that fill the GPU with tiles of 128 tokens
+
+LONG = 12400  # 96 full tiles of 128 and more
+
+
+@pytest.mark.parametrize("inp,out,R", [(8, 8, 8), (72, 136, 16), (264, 72, 24), (1000, 504, 64), (200, 264, 128),
+                                       (64, 64, 40), (456, 1032, 32)])
+@pytest.mark.parametrize("y,o", [("bf16", "bf16"), ("fp32", "bf16"), ("fp32", "fp32"), ("bf16", "fp32")])
+def test_long_sizes_and_types(dev, inp, out, R, y, o):
+    from nvfp4_quantized_moe_topk_gb300 import api
+
+    c = Case(dev, _ids(LONG, 5, inp, run=300), inp, out, 5, R, y, o, seed=R)
+    c.check(c.run())
+    assert api.lora_device_error() == 0
+
+
+@pytest.mark.parametrize("run", [1, 90, 3000])
+@pytest.mark.parametrize("R", [8, 16, 64, 128])
+def test_long_mixed_ranks(dev, run, R):
+    L = 9
+    ranks = [0, R, R // 2, 1, R - 1, 7, -3, R + 5, min(R, 13)]
+    c = Case(dev, _ids(LONG + 37, L, R, run), 328, 136, L, R, "fp32", "bf16", ranks, seed=R)
+    for l in range(L):
+        r = min(max(ranks[l], 0), R)
+        c.a[l, r:] = float("nan")
+        c.b[l, :, r:] = float("nan")
+    c.check(c.run())
+
+
+def test_long_one_adapter_none_and_many(dev):
+    import torch
+
+    from nvfp4_quantized_moe_topk_gb300 import api
+
+    c = Case(dev, [2] * LONG, 264, 136, 4, 16, "fp32", "fp32")
+    c.check(c.run())
+    c.ids.fill_(-1)
+    assert torch.equal(c.run(), c.y)
+    c = Case(dev, _ids(LONG, 700, 3, run=2), 136, 72, 700, 16)
+    c.check(c.run())
+    assert api.lora_device_error() == 0
+
+
+def test_long_without_y_in_place_strides_and_bad_tokens(dev):
+    import torch
+
+    n = LONG
+    ids = _ids(n, 4, 1, run=400)
+    c = Case(dev, ids, 264, 136, 4, 32, None, "fp32", scale=False)
+    c.check(c.run())
+    c = Case(dev, ids, 264, 136, 4, 32)
+    want = c.run()
+    c.check(want)
+    kept = c.y.clone()
+    assert torch.equal(c.run(out=c.y), want)
+    c.y = kept
+    wide = torch.full((n, 600), 3.0, dtype=torch.bfloat16, device=dev)
+    x, y, out = wide[:, 8:272], wide[:, 280:416], wide[:, 424:560]
+    x.copy_(c.x)
+    y.copy_(c.y)
+    c.x, c.y = x, y
+    assert torch.equal(c.run(out=out), want)
+    for part in (wide[:, :8], wide[:, 272:280], wide[:, 416:424], wide[:, 560:]):
+        assert bool((part == 3).all())
+    c.ids.fill_(1)
+    want = c.run()
+    c.x[3, 7] = float("nan")
+    c.x[n - 2, 9] = float("inf")
+    got = c.run()
+    rest = torch.ones(n, dtype=torch.bool, device=dev)
+    rest[[3, n - 2]] = False
+    assert torch.equal(got[rest], want[rest])
+    assert bool(torch.isnan(got[3]).all()) and not bool(torch.isfinite(got[n - 2]).any())
+
+
+def test_long_repeated_on_another_stream_and_in_a_graph(dev):
+    import torch
+
+    from nvfp4_quantized_moe_topk_gb300 import api
+
+    c = Case(dev, _ids(LONG, 6, 4, 50), 264, 136, 6, 16)
+    ws = api.lora_workspace(LONG, 6)
+    want = c.run(workspace=ws)
+    ws.fill_(0xFF)
+    assert torch.equal(c.run(workspace=ws), want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = c.run(stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    out = torch.empty_like(want)
+    c.run(out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(out=out, workspace=ws)
+    c.ids.copy_(torch.tensor(_ids(LONG, 6, 7, 20), dtype=torch.int32))
+    c.x.normal_()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(out)
