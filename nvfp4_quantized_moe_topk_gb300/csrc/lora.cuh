@@ -103,7 +103,7 @@ __device__ __forceinline__ bool planned_tile(const moe_lora_args& a, const LoraP
   if (tid < MT) row[tid] = -1;
   pdl_wait();
   __syncthreads();
-  for (int32_t l = tid; l <= L; l += kLoraThreads) {
+  for (int32_t l = tid; l <= L; l += blockDim.x) {
     const int32_t b0 = p.tile_base[l], b1 = p.tile_base[l + 1];
     if (tile >= b0 && tile < b1) {
       const int32_t first = p.starts[l] + (tile - b0) * MT;
@@ -189,14 +189,16 @@ __device__ __forceinline__ void ring8(uint32_t dst, const void* src) {
 // compiler may move it ahead of matrix instructions.)
 __device__ __forceinline__ uint4 slot16(const char* sm, uint32_t at) { return *reinterpret_cast<const uint4*>(sm + at); }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `ahead` (0..4) of the thread's newest groups are unfinished.
+// Waits until at most `ahead` (0..6) of the thread's newest groups are unfinished.
 __device__ __forceinline__ void ring_wait(int ahead) {
   switch (ahead) {
     case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
     case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
     case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
     case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 4;" ::: "memory");
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 6;" ::: "memory");
   }
 }
 
