@@ -70,15 +70,29 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int32_t l = tid; l <= L; l += kPlanThreads) sm_plan[l] = 0;
   __syncthreads();
   const int steps = (int)min((int64_t)kPlanPer, ((int64_t)n - beg + kPlanThreads - 1) / kPlanThreads);
+  // a token's place in its bucket: the lanes of a warp with the same bucket take theirs by one addition
+  constexpr int kBatch = 4;  // chains of match, add and shuffle side by side
 #pragma unroll
-  for (int j = 0; j < kPlanPer; ++j) {
-    if (j >= steps) break;
-    key[j] = beg + tid + j * kPlanThreads < n ? bucket_of(key[j], L) : -1;
-    const uint32_t peers = __match_any_sync(0xffffffffu, key[j]);
-    const int leader = __ffs(peers) - 1;
-    int32_t base = 0;
-    if (key[j] >= 0 && lane == leader) base = atomicAdd(&sm_plan[key[j]], __popc(peers));
-    rank[j] = __shfl_sync(0xffffffffu, base, leader) + __popc(peers & ((1u << lane) - 1u));
+  for (int j0 = 0; j0 < kPlanPer; j0 += kBatch) {
+    if (j0 >= steps) break;
+    uint32_t peers[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i;
+      key[j] = beg + tid + j * kPlanThreads < n ? bucket_of(key[j], L) : -1;
+      peers[i] = __match_any_sync(0xffffffffu, key[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i;
+      rank[j] = 0;
+      if (key[j] >= 0 && lane == __ffs(peers[i]) - 1) rank[j] = atomicAdd(&sm_plan[key[j]], __popc(peers[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i;
+      rank[j] = __shfl_sync(0xffffffffu, rank[j], __ffs(peers[i]) - 1) + __popc(peers[i] & ((1u << lane) - 1u));
+    }
   }
   __syncthreads();
   // adapter tid: its tokens in all slices and in those before this one

@@ -69,12 +69,12 @@ __device__ __forceinline__ void push_float(float* p, uint32_t rank, float v) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-// The float at this CTA's shared address `p`, in CTA `rank` of the cluster.
-__device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
+// Two floats at this CTA's shared address `p`, in CTA `rank` of the cluster.
+__device__ __forceinline__ float2 peer_float2(const float* p, uint32_t rank) {
   uint32_t addr;
-  float v;
+  float2 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 

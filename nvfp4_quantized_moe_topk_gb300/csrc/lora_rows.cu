@@ -134,31 +134,43 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           *reinterpret_cast<float2*>(part + (half * kRowsTile + group * 16 + h * 8 + g) * kPartPitch + 8 * j + 2 * q) =
               make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
       __syncthreads();
-      // thread: two ranks of rows tid / 32, + 8, ...
+      // thread: two ranks of rows warp, warp + 8, ...
+      constexpr int kRows = kRowsTile / kLoraWarps;
       const int32_t r = 2 * lane;
+      const bool used = r0 + r < rank;
+      float2 s[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float* p = part + (warp + i * kLoraWarps) * kPartPitch + r;
+        const float2 p0 = *reinterpret_cast<const float2*>(p);
+        const float2 p1 = *reinterpret_cast<const float2*>(p + kRowsTile * kPartPitch);
+        s[i] = make_float2(p0.x + p1.x, p0.y + p1.y);
+      }
       if (C > 1) {
-        for (int m = warp; m < kRowsTile; m += kLoraWarps) {
-          const float2 p0 = *reinterpret_cast<const float2*>(part + m * kPartPitch + r);
-          const float2 p1 = *reinterpret_cast<const float2*>(part + (kRowsTile + m) * kPartPitch + r);
-          *reinterpret_cast<float2*>(sum + m * kPartPitch + r) = make_float2(p0.x + p1.x, p0.y + p1.y);
+        if (used) {
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            *reinterpret_cast<float2*>(sum + (warp + i * kLoraWarps) * kPartPitch + r) = s[i];
         }
         cluster_sync();
-      }
-      for (int m = warp; m < kRowsTile; m += kLoraWarps) {
-        float s0 = 0.f, s1 = 0.f;
-        if (C > 1) {
-          for (uint32_t k = 0; k < C; ++k) {
-            s0 += peer_float(sum + m * kPartPitch + r, k);
-            s1 += peer_float(sum + m * kPartPitch + r + 1, k);
+        // added in the order of the cluster's CTAs, the same in each of them
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) s[i] = make_float2(0.f, 0.f);
+        for (uint32_t k = 0; used && k < C; ++k) {
+          float2 p[kRows];
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) p[i] = peer_float2(sum + (warp + i * kLoraWarps) * kPartPitch + r, k);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            s[i].x += p[i].x;
+            s[i].y += p[i].y;
           }
-        } else {
-          const float2 p0 = *reinterpret_cast<const float2*>(part + m * kPartPitch + r);
-          const float2 p1 = *reinterpret_cast<const float2*>(part + (kRowsTile + m) * kPartPitch + r);
-          s0 = p0.x + p1.x;
-          s1 = p0.y + p1.y;
         }
-        s0 = r0 + r < rank ? s0 * scale : 0.f;
-        s1 = r0 + r + 1 < rank ? s1 * scale : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int m = warp + i * kLoraWarps;
+        float s0 = used ? s[i].x * scale : 0.f, s1 = r0 + r + 1 < rank ? s[i].y * scale : 0.f;
         char* to = v_base + m * v_pitch + (uint32_t)(r0 / kPass) * 128 + (((lane >> 2) ^ ((m & 1) << 2)) * 16) +
                    (lane & 3) * 4;
         for (int k = 0; k < terms; ++k, to += kRowsTile * v_pitch) {  // a sum of bf16 terms, each the rounding of the rest
