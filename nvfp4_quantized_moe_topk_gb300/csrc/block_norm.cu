@@ -49,12 +49,6 @@ __device__ __forceinline__ void channel_factors(const NormParams& a, const Lane<
   }
 }
 
-// A lane's values of a row from global memory, 0 where it has no channel.
-template <typename T, bool QUADS>
-__device__ __forceinline__ void row_load(const NormRows& r, int32_t t, const Lane<QUADS>& l, F2 (&v)[4]) {
-  load_param(r.at(t, 0), Vec8<T>::kVecs == 1 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, l, v);
-}
-
 // z <- gate * z
 __device__ __forceinline__ void apply_gate(const NormParams& a, F2 (&z)[4], F2 (&g)[4]) {
   if (a.gate_sigmoid) sigmoid2(g);
@@ -69,68 +63,7 @@ __device__ __forceinline__ float squares(const F2 (&v)[4]) {
   return s.x + s.y;
 }
 
-// One row per CTA: batches too small for persistent ones.
-template <typename RT, typename YT, int ITERS>
-__global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormParams a) {
-  __shared__ float red[2][16];
-  constexpr bool Q = Vec8<RT>::kVecs + Vec8<YT>::kVecs > 2;
-  const int32_t t = blockIdx.x;
-  const bool branch = a.branch.p != nullptr;
-  F2 u[ITERS][4], z[ITERS][4], cz[ITERS][4], wx[ITERS][4];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < ITERS; ++i) {
-    const Lane<Q> l(i, a.H);
-    if (!l.ok0) continue;
-    row_load<RT>(a.residual, t, l, u[i]);
-    if (branch) row_load<YT>(a.branch, t, l, z[i]);
-    channel_factors<kNormAny>(a, l, cz[i], wx[i]);
-    if (a.post) ss += squares(z[i]);
-    if (a.gate_kind == MOE_GATE_FULL) {
-      F2 g[4];
-      row_load<YT>(a.gate, t, l, g);
-      apply_gate(a, z[i], g);
-    }
-  }
-  float f = 1.f;
-  if (a.gate_kind == MOE_GATE_TOKEN) {
-    f = reinterpret_cast<const float*>(a.gate.p)[t];
-    if (a.gate_sigmoid) f = sigmoid(f);
-  }
-  if (a.post) {
-    ss = cta_sum(ss, red[0]);
-    const float rp = rsqrtf(fmaf(ss, a.inv_h, a.eps));
-    if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rp;
-    f *= rp;
-  }
-  ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < ITERS; ++i) {
-    const Lane<Q> l(i, a.H);
-    if (!l.ok0) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u[i][j] = mul2(u[i][j], f2(a.alpha));
-      if (branch) u[i][j] = fma2(cz[i][j], mul2(f2(f), z[i][j]), u[i][j]);
-    }
-    ss += squares(u[i]);
-    if (a.residual_out.p) row_store<RT>(a.residual_out, t, l, u[i]);
-  }
-  if (!a.pre) return;
-  ss = cta_sum(ss, red[1]);
-  const float ru = rsqrtf(fmaf(ss, a.inv_h, a.eps));
-  if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = ru;
-#pragma unroll
-  for (int i = 0; i < ITERS; ++i) {
-    const Lane<Q> l(i, a.H);
-    if (!l.ok0) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[i][j] = mul2(u[i][j], mul2(f2(ru), wx[i][j]));
-    row_store<uint16_t>(a.x_out, t, l, u[i]);
-  }
-}
-
-// The same for persistent CTAs over rows blockIdx.x, + gridDim.x, ...
+// Persistent CTAs over rows blockIdx.x, + gridDim.x, ...
 template <typename RT, typename YT, int ITERS, int MODE>
 __global__ void __launch_bounds__(kNormMaxThreads, 3 - ITERS)
     block_norm_rows_kernel(const NormParams a, int32_t stages, int32_t stage_vecs) {
@@ -244,10 +177,6 @@ cudaError_t norm_rows(const NormParams& a, cudaStream_t s) {
 
 template <typename RT, typename YT, int ITERS>
 cudaError_t norm_forward_i(const NormParams& a, cudaStream_t s) {
-  if (a.n <= kNormDirectRows) {
-    block_norm_kernel<RT, YT, ITERS><<<(unsigned)a.n, norm_threads(a.H), 0, s>>>(a);
-    return cudaGetLastError();
-  }
   if (!a.branch.p || !a.post || !a.pre) return norm_rows<RT, YT, ITERS, kNormAny>(a, s);
   if (a.gate_kind == MOE_GATE_CHANNEL) return norm_rows<RT, YT, ITERS, kNormChannel>(a, s);
   if (a.gate_kind == MOE_GATE_FULL) return norm_rows<RT, YT, ITERS, kNormFull>(a, s);

@@ -223,7 +223,6 @@ cudaError_t launch_decode(const DecodeArgs& args, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------- operators around the layer
 constexpr int kNormMaxHidden = 8192;
-constexpr int kNormDirectRows = 304;       // batches of at most this many rows take a CTA a row
 int block_norm_backward_slots(int32_t n, int32_t hidden);  // CTAs of the backward pass, each with column sums of its own
 cudaError_t launch_block_norm(const moe_block_norm_args& a, cudaStream_t s);
 // part: [block_norm_backward_slots(n, hidden)][2][hidden] floats.
@@ -231,7 +230,6 @@ cudaError_t launch_block_norm_backward(const moe_block_norm_args& a, const moe_b
                                        cudaStream_t s);
 
 constexpr int kRouterLossBlocks = 304;  // blocks of the balance loss and the router's backward pass
-int32_t router_loss_blocks(int32_t n);
 size_t router_loss_workspace(int32_t n, int32_t E, int32_t S);  // bytes
 cudaError_t launch_balance_loss(const moe_router_args& a, float* prob_sums, float* loss, void* workspace,
                                 cudaStream_t s);

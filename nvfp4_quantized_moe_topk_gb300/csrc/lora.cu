@@ -162,8 +162,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-constexpr int kSmallTokens = 1024;  // more than these take lora_rows.cu
-constexpr int kMmaTiles = 96;       // from this many full tiles of 128 on, lora_mma.cu
+// More tokens than these take the larger tiles of lora_mma.cu (ranks up to
+// kMmaRank) or lora_rows.cu.  TODO figures
+inline int32_t small_tokens(int32_t max_rank) { return max_rank <= 32 ? 1280 : 512; }
 
 // Tiles of 16 tokens; NT groups of 8 ranks a pass of the first product.
 template <int NT>
@@ -459,20 +460,8 @@ cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, i
   static std::atomic<bool> configured[kMaxDevices];
   cudaError_t e = raise_smem_limit(lora_kernel<NT>, 220 * 1024, configured);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * cluster));
-  cfg.blockDim = dim3(kLoraThreads);
-  cfg.dynamicSmemBytes = ring + rest;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = fused ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<NT>, a, p, (int32_t)fused, terms, ring);
+  return lora_launch_cluster(lora_kernel<NT>, tiles, cluster, kLoraThreads, ring + rest, !fused, s, a, p, (int32_t)fused,
+                             terms, ring);
 }
 
 }  // namespace
@@ -486,8 +475,8 @@ size_t lora_workspace(int32_t n, int32_t n_adapters) {
 
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s) {
   const int32_t n = a.n, L = a.n_adapters;
-  const bool fused = n <= kFusedTokens, rows = n > kSmallTokens, mma = n >= kMmaTokens * kMmaTiles && lora_mma_fits(a);
-  const int32_t mt = mma ? kMmaTokens : rows ? kRowsTile : 16;
+  const bool fused = n <= kFusedTokens, small = n <= small_tokens(a.max_rank), mma = !small && a.max_rank <= kMmaRank;
+  const int32_t mt = mma ? kMmaTokens : small ? 16 : kRowsTile;
   const LoraPlan p = fused ? LoraPlan{} : lora_plan(workspace, n, L);
   if (!fused) {
     const int32_t slices = plan_slices(n);
@@ -501,10 +490,10 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // every group has at most one tile that is not full
-  const int32_t tiles = n / mt + std::min(n, L + 1);
-  if (mma) return launch_lora_mma(a, p, tiles, s);
-  if (rows) return launch_lora_rows(a, p, tiles, s);
+  // every group has at most one tile that is not full, half of one on average
+  const int32_t groups = std::min(n, L + 1), tiles = n / mt + groups, expected = n / mt + (groups + 1) / 2;
+  if (mma) return launch_lora_mma(a, p, tiles, expected, s);
+  if (!small) return launch_lora_rows(a, p, tiles, expected, s);
   int32_t cluster = 1;
   while (cluster < 8 && tiles * cluster * 2 <= 608) cluster *= 2;
   if (a.max_rank <= 16) return lora_launch<2>(a, p, fused, tiles, cluster, s);

@@ -77,6 +77,17 @@ __device__ __forceinline__ float2 peer_float2(const float* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
+// Four.
+__device__ __forceinline__ float4 peer_float4(const float* p, uint32_t rank) {
+  uint32_t addr;
+  float4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 // What a CTA works on: up to MT tokens of an adapter (n_adapters: tokens
 // without one, rank 0).
@@ -209,13 +220,69 @@ __device__ __forceinline__ int ring_stages(uint32_t bytes, uint32_t step) {
 
 constexpr uint32_t kSlotVec = kLoraThreads * 16;  // one 16-byte vector of every thread
 
-// lora_mma.cu: at most `tiles` tiles of kMmaTokens tokens; whether a call's sizes fit its shared memory.
+// Launches tiles x cluster CTAs in clusters of `cluster`; pdl: the kernel begins
+// with a wait for the kernel before it.
+template <typename... KArgs, typename... Args>
+cudaError_t lora_launch_cluster(void (*kernel)(KArgs...), int32_t tiles, int32_t cluster, int threads, size_t smem,
+                                bool pdl, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * cluster));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTAs that share a tile where one occupies an SM: as many (up to
+// kLoraMaxCluster) as leave all tiles on the GPU at once.  How many clusters of
+// a size that is depends on the SMs of its clusters of SMs and is asked for
+// once a device and size.  `tiles`: the tiles to expect, half a tile more for
+// every adapter than full tiles alone would be (where there are a few more, they
+// wait for the first to finish).
+constexpr int32_t kLoraMaxCluster = 8;
+template <typename... KArgs>
+cudaError_t lora_cluster(void (*kernel)(KArgs...), int threads, size_t smem, int32_t tiles,
+                         std::atomic<int32_t> (&held)[kMaxDevices][kLoraMaxCluster + 1], int32_t* cluster) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  for (*cluster = kLoraMaxCluster; *cluster > 1; --*cluster) {
+    int32_t most = dev < kMaxDevices ? held[dev][*cluster].load(std::memory_order_relaxed) : 0;
+    if (!most) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)*cluster);
+      cfg.blockDim = dim3((unsigned)threads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = (unsigned)*cluster;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (dev < kMaxDevices) held[dev][*cluster].store(std::max(most, 1), std::memory_order_relaxed);
+    }
+    if (tiles <= most) break;
+  }
+  return cudaSuccess;
+}
+
+// lora_mma.cu: at most `tiles` tiles of kMmaTokens tokens, ranks up to kMmaRank.
 constexpr int kMmaTokens = 128;
-cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, cudaStream_t s);
-bool lora_mma_fits(const moe_lora_args& a);
+constexpr int kMmaRank = 64;
+cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s);
 
 // lora_rows.cu: at most `tiles` tiles of kRowsTile tokens.
 constexpr int kRowsTile = 64;
-cudaError_t launch_lora_rows(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, cudaStream_t s);
+cudaError_t launch_lora_rows(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s);
 
 }  // namespace moe

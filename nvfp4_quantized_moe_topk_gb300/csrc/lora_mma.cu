@@ -28,7 +28,8 @@ namespace {
 constexpr int kMmaTile = kMmaTokens;
 constexpr int kMmaThreads = 512, kMmaHalf = kMmaThreads / 2;
 constexpr uint32_t kOperandTile = 128 * 128;  // 128 rows of 64 bf16
-constexpr int kMmaMaxStages = 8;
+constexpr uint32_t kMmaMaxStages = 8;
+constexpr uint32_t kMmaSmem = 224 * 1024;
 constexpr uint32_t kD2 = 256, kTmemCols = 512;  // tensor memory: the halves' D1 in 128 columns each, then their D2
 
 // Set where a bounded wait ran out; read by moe_lora_get_device_error.
@@ -51,8 +52,8 @@ __device__ __forceinline__ bool half_or(int half, bool any) {
 __host__ __device__ inline int32_t block_columns(bool y_f32, bool out_f32) { return y_f32 || out_f32 ? 32 : 64; }
 // Bytes of a half's ring steps: x and A; y and B.
 __host__ __device__ inline uint32_t mma_step1(int32_t ranks16) { return kOperandTile + (uint32_t)ranks16 * 16 * 128; }
-__host__ __device__ inline uint32_t mma_step2(bool has_y, int32_t rank_blocks, int32_t columns) {
-  return (has_y ? kOperandTile : 0) + (uint32_t)rank_blocks * columns * 128;
+__host__ __device__ inline uint32_t mma_step2(bool has_y, bool has_b, int32_t columns) {
+  return (has_y ? kOperandTile : 0) + (has_b ? columns * 128 : 0);
 }
 
 __global__ void __launch_bounds__(kMmaThreads, 1)
@@ -64,15 +65,17 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   char* sm = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int half = tid / kMmaHalf, htid = tid % kMmaHalf, hwarp = htid >> 5;
+  const uint32_t C = cluster_size(), cr = cluster_rank();
+  const int32_t mine = (int32_t)cr * 2 + half, jump = (int32_t)C * 2;  // this half's first step, and from one to the next
   if (tid == 0) {
     for (int h = 0; h < 2; ++h) {
-      for (int s = 0; s < kMmaMaxStages; ++s) mbar_init(&done1[h][s], 1);
+      for (uint32_t s = 0; s < kMmaMaxStages; ++s) mbar_init(&done1[h][s], 1);
       mbar_init(&done2[h], 1);
     }
     fence_mbar_init();
   }
   Tile t;
-  if (!planned_tile<kMmaTile>(a, plan, (int32_t)blockIdx.x, row, t)) return;
+  if (!planned_tile<kMmaTile>(a, plan, (int32_t)(blockIdx.x / C), row, t)) return;
   if (warp == 0) {
     tmem_alloc(&tmem_slot, kTmemCols);
     tmem_relinquish();
@@ -81,17 +84,69 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int32_t rank = t.rank, ranks16 = (rank + 15) / 16, rank_blocks = (a.max_rank + 63) / 64;
-  // the halves' rings; the halves' out blocks; v [terms][rank_blocks] operand tiles
+  const int32_t rank = t.rank, ranks16 = (rank + 15) / 16;
+  // the halves' rings; the halves' out blocks; v [terms] operand tiles
   const uint32_t sm_u32 = smem_u32(sm), ring = half * ring_bytes;
   char* obuf = sm + 2 * ring_bytes + half * kOperandTile;
   const uint32_t v_at = 2 * ring_bytes + 2 * kOperandTile;
+  static_assert(kMmaRank == 64, "a rank of v is one of 4 x 16, a row of A or B 128 bytes of one operand tile");
   const uint32_t quadrant = (uint32_t)(32 * (warp & 3)) << 16;  // this warp's lanes of tensor memory
   const int m = 32 * (warp & 3) + lane;                         // its thread's token
   const int p8 = htid & 7, r8 = htid >> 3;  // copies of 128-byte rows: piece, first row (the others 32, 64, 96 further)
   const uint32_t to8 = swizzled(r8, p8);    // (32 rows further: the same swizzle)
   bool dead = false;                        // a wait ran out
 
+  // out = y + B v (its first steps are fetched before v is made)
+  const bool yf = a.y_dtype == MOE_DTYPE_F32, of = a.out_dtype == MOE_DTYPE_F32, has_y = a.y.data != nullptr;
+  const int32_t columns = block_columns(yf, of), blocks = (a.out_features + columns - 1) / columns;
+  const uint32_t y_size = yf ? 4 : 2, o_size = of ? 4 : 2, out_idesc = idesc_bf16(128, (uint32_t)columns);
+  const uint32_t b_at = has_y ? kOperandTile : 0;
+  const uint32_t out_step = max(mma_step2(has_y, rank > 0, columns), 1024u);
+  const int out_stages = (int)min(kMmaMaxStages, ring_bytes / out_step);
+  // rows of y and out in vectors of 16 bytes: a product of two 32-bit numbers a row
+  const uint32_t y_stride = (uint32_t)((a.y.stride ? a.y.stride : a.out_features) * y_size / 16);
+  const uint32_t o_stride = (uint32_t)((a.out.stride ? a.out.stride : a.out_features) * o_size / 16);
+  const char* y_base = static_cast<const char*>(a.y.data);
+  char* o_base = static_cast<char*>(a.out.data);
+  const uint32_t y_pieces = columns * y_size / 16, o_pieces = columns * o_size / 16;  // of a block's row: 8 or 4
+  const uint32_t y_row = (uint32_t)a.out_features * y_size / 16, o_row = (uint32_t)a.out_features * o_size / 16;
+  const uint32_t b_bytes = (uint32_t)a.max_rank * 2;
+  const char* B = reinterpret_cast<const char*>(a.b) +
+                  (rank > 0 ? ((int64_t)t.adapter * a.out_features + r8) * (int64_t)b_bytes + 16 * p8 : 0);
+  auto fetch_out = [&](int32_t ob, int stage) {
+    if (ob < blocks) {
+      const uint32_t at = ring + stage * out_step + to8, vec = (uint32_t)ob * y_pieces + p8;
+      if (has_y && (uint32_t)p8 < y_pieces && vec < y_row) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t tok = row[r8 + 32 * i];
+          if (tok >= 0) ring16(sm_u32 + at + i * 32 * 128, y_base + (((uint64_t)(uint32_t)tok * y_stride + vec) << 4));
+        }
+      }
+      const int32_t left = min(a.out_features - ob * columns, columns);
+      const int32_t rest = rank - 8 * p8;  // ranks in this thread's piece and after it
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (p8 >= 2 * ranks16 || r8 + 32 * i >= left) break;
+        const uint32_t to = at + b_at + i * 32 * 128;
+        const char* from = B + (uint64_t)(uint32_t)(ob * columns + 32 * i) * b_bytes;
+        if (rest >= 8) {
+          ring16(sm_u32 + to, from);
+        } else {  // what lies beyond the rank may hold anything
+          uint4 b = make_uint4(0, 0, 0, 0);
+          if (rest > 0) {
+            b = __ldg(reinterpret_cast<const uint4*>(from));
+            b.x &= rest >= 2 ? 0xffffffffu : 0xffffu;
+            b.y &= rest >= 4 ? 0xffffffffu : rest == 3 ? 0xffffu : 0u;
+            b.z &= rest >= 6 ? 0xffffffffu : rest == 5 ? 0xffffu : 0u;
+            b.w &= rest == 7 ? 0xffffu : 0u;
+          }
+          *reinterpret_cast<uint4*>(sm + to) = b;
+        }
+      }
+    }
+    ring_commit();
+  };
   if (rank > 0) {
     const uint32_t row_bytes = (uint32_t)a.in_features * 2, idesc = idesc_bf16(128, (uint32_t)ranks16 * 16);
     const int32_t chunks = (a.in_features + 63) / 64;
@@ -107,7 +162,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const char* Ar = reinterpret_cast<const char*>(a.a) +
                      ((int64_t)t.adapter * a.max_rank + r8) * (int64_t)row_bytes + 16 * p8;
     const uint32_t step = mma_step1(ranks16);
-    const int stages = (int)min((uint32_t)kMmaMaxStages, ring_bytes / step);
+    const int stages = (int)min(kMmaMaxStages, ring_bytes / step);
     auto fetch = [&](int32_t c, int stage) {
       if (c < chunks) {
         const uint32_t off = (uint32_t)c * 128, at = ring + stage * step + to8;
@@ -115,7 +170,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) ring16(sm_u32 + at + i * 32 * 128, xr[i] + off);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
             if (r8 + 32 * i < a_rows)
               ring16(sm_u32 + at + kOperandTile + i * 32 * 128, Ar + ((uint64_t)(32 * i) * row_bytes + off));
         } else {  // past the row's end
@@ -129,10 +184,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       }
       ring_commit();
     };
-    for (int s = 0; s + 1 < stages; ++s) fetch(half + 2 * s, s);
+    for (int s = 0; s + 1 < stages; ++s) fetch(mine + jump * s, s);
     int stage = 0, last = 0;
     uint32_t parity = 0, last_parity = 0;
-    for (int32_t c = half; c < chunks; c += 2) {
+    for (int32_t c = mine; c < chunks; c += jump) {
       ring_wait(stages - 2);
       fence_proxy_async_smem();
       dead = half_or(half, dead);
@@ -143,14 +198,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma_bf16(tmem + half * 128, smem_desc_k128(x_at + 32 * k), smem_desc_k128(a_at + 32 * k), idesc,
-                        c != half || k != 0);
+                        c != mine || k != 0);
           tc_commit(&done1[half][stage]);
         }
         __syncwarp();
       }
       // the step before this one has been read: its slot takes the chunk `stages - 1` steps ahead
-      if (c != half && !mbar_wait(&done1[half][last], last_parity, &g_lora_flags)) dead = true;
-      fetch(c + 2 * (stages - 1), stage == 0 ? stages - 1 : stage - 1);
+      if (c != mine && !mbar_wait(&done1[half][last], last_parity, &g_lora_flags)) dead = true;
+      fetch(c + jump * (stages - 1), stage == 0 ? stages - 1 : stage - 1);
       last = stage;
       last_parity = parity;
       if (++stage == stages) {
@@ -158,24 +213,56 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         parity ^= 1;
       }
     }
-    if (half < chunks && !dead && !mbar_wait(&done1[half][last], last_parity, &g_lora_flags)) dead = true;
+    if (mine < chunks && !dead && !mbar_wait(&done1[half][last], last_parity, &g_lora_flags)) dead = true;
     ring_wait(0);
+    if (!dead)
+      for (int s = 0; s + 1 < out_stages; ++s) fetch_out(mine + jump * s, s);
     dead = __syncthreads_or(dead);
     tc_fence_after();
-    // D1 -> v: a thread its token's 16 ranks at a time
-    for (int32_t j = warp >> 2; j < ranks16 && !dead; j += kMmaThreads / 128) {
-      uint32_t d0[16], d1[16];
-      tmem_ld16(tmem + quadrant + 16 * j, d0);
-      if (chunks > 1) tmem_ld16(tmem + quadrant + 128 + 16 * j, d1);
+    // D1 -> v: a thread its token's 16 ranks from 16 j on.  In a cluster the CTAs' sums meet in the (still unused) out
+    // blocks, [4 ranks][128 tokens], and are added in the order of the CTAs, the same in each of them.
+    const int32_t j = warp >> 2;
+    const bool has = j < ranks16 && !dead;
+    float s[16];
+    if (has) {
+      uint32_t d0[16] = {}, d1[16] = {};
+      if ((int32_t)cr * 2 < chunks) tmem_ld16(tmem + quadrant + 16 * j, d0);  // (a half without a step has no sum)
+      if ((int32_t)cr * 2 + 1 < chunks) tmem_ld16(tmem + quadrant + 128 + 16 * j, d1);
       tmem_ld_wait();
-      float s[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float sum = chunks > 1 ? __uint_as_float(d0[i]) + __uint_as_float(d1[i]) : __uint_as_float(d0[i]);
-        s[i] = 16 * j + i < rank ? sum * t.scale : 0.f;
+      for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(d0[i]) + __uint_as_float(d1[i]);
+    }
+    if (C > 1) {
+      float* meet = reinterpret_cast<float*>(sm + 2 * ring_bytes) + (4 * j * kMmaTile + m) * 4;
+      if (has) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(meet + i * kMmaTile * 4) =
+              make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
       }
+      cluster_sync();
+      if (has) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 0.f;
+        for (uint32_t r = 0; r < C; ++r) {
+          float4 p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = peer_float4(meet + i * kMmaTile * 4, r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[4 * i] += p[i].x;
+            s[4 * i + 1] += p[i].y;
+            s[4 * i + 2] += p[i].z;
+            s[4 * i + 3] += p[i].w;
+          }
+        }
+      }
+      cluster_arrive();  // (waited for before the first write to the out blocks)
+    }
+    if (has) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 16 * j + i < rank ? s[i] * t.scale : 0.f;
       for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
-        const uint32_t tile = v_at + (uint32_t)(k * rank_blocks + j / 4) * kOperandTile;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t o[4];
@@ -186,69 +273,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             lo -= bf16lo(o[i]);
             hi -= bf16hi(o[i]);
           }
-          *reinterpret_cast<uint4*>(sm + tile + swizzled(m, (j % 4) * 2 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(sm + v_at + (uint32_t)k * kOperandTile + swizzled(m, j * 2 + h)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
     }
     tc_fence_before();
     fence_proxy_async_smem();
+    if (C > 1) cluster_wait();
     __syncthreads();
     tc_fence_after();
+  } else {
+    for (int s = 0; s + 1 < out_stages; ++s) fetch_out(mine + jump * s, s);
   }
 
-  // out = y + B v
-  const bool yf = a.y_dtype == MOE_DTYPE_F32, of = a.out_dtype == MOE_DTYPE_F32, has_y = a.y.data != nullptr;
-  const int32_t columns = block_columns(yf, of), blocks = (a.out_features + columns - 1) / columns;
-  const uint32_t y_size = yf ? 4 : 2, o_size = of ? 4 : 2, idesc = idesc_bf16(128, (uint32_t)columns);
-  const uint32_t b_at = has_y ? kOperandTile : 0, b_tile = columns * 128;
-  const uint32_t step = max(mma_step2(has_y, rank > 0 ? rank_blocks : 0, columns), 1024u);
-  const int stages = (int)min((uint32_t)kMmaMaxStages, ring_bytes / step);
-  // rows of y and out in vectors of 16 bytes: a product of two 32-bit numbers a row
-  const uint32_t y_stride = (uint32_t)((a.y.stride ? a.y.stride : a.out_features) * y_size / 16);
-  const uint32_t o_stride = (uint32_t)((a.out.stride ? a.out.stride : a.out_features) * o_size / 16);
-  const char* y_base = static_cast<const char*>(a.y.data);
-  char* o_base = static_cast<char*>(a.out.data);
-  const uint32_t y_pieces = columns * y_size / 16, o_pieces = columns * o_size / 16;  // of a block's row: 8 or 4
-  const uint32_t y_row = (uint32_t)a.out_features * y_size / 16, o_row = (uint32_t)a.out_features * o_size / 16;
-  const uint32_t b_bytes = (uint32_t)a.max_rank * 2;
-  const char* B = reinterpret_cast<const char*>(a.b) +
-                  (rank > 0 ? ((int64_t)t.adapter * a.out_features + r8) * (int64_t)b_bytes + 16 * p8 : 0);
-  auto fetch = [&](int32_t ob, int stage) {
-    if (ob < blocks) {
-      const uint32_t at = ring + stage * step + to8, vec = (uint32_t)ob * y_pieces + p8;
-      if (has_y && (uint32_t)p8 < y_pieces && vec < y_row) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t tok = row[r8 + 32 * i];
-          if (tok >= 0) ring16(sm_u32 + at + i * 32 * 128, y_base + (((uint64_t)(uint32_t)tok * y_stride + vec) << 4));
-        }
-      }
-      const int32_t left = min(a.out_features - ob * columns, columns);
-      for (int32_t k = 0; 64 * k < 16 * ranks16; ++k) {
-        const int32_t rest = rank - (64 * k + 8 * p8);  // ranks in this thread's piece and after it
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (r8 + 32 * i >= left) break;
-          const uint32_t to = at + b_at + k * b_tile + i * 32 * 128;
-          const char* from = B + ((uint64_t)(uint32_t)(ob * columns + 32 * i) * b_bytes + 128 * k);
-          if (rest >= 8) {
-            ring16(sm_u32 + to, from);
-          } else {  // what lies beyond the rank may hold anything
-            uint4 b = make_uint4(0, 0, 0, 0);
-            if (rest > 0) {
-              b = __ldg(reinterpret_cast<const uint4*>(from));
-              b.x &= rest >= 2 ? 0xffffffffu : 0xffffu;
-              b.y &= rest >= 4 ? 0xffffffffu : rest == 3 ? 0xffffu : 0u;
-              b.z &= rest >= 6 ? 0xffffffffu : rest == 5 ? 0xffffu : 0u;
-              b.w &= rest == 7 ? 0xffffu : 0u;
-            }
-            *reinterpret_cast<uint4*>(sm + to) = b;
-          }
-        }
-      }
-    }
-    ring_commit();
-  };
   // adds y (in ring step `stage`) to the half's D2, 16 of a thread's columns from `first` on, into the out block
   auto finish = [&](uint32_t first, int stage) {
     uint32_t d[16];
@@ -262,7 +300,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (has_y && yf) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 y = slot16(sm, ring + stage * step + swizzled(m, first / 4 + i));
+        const uint4 y = slot16(sm, ring + stage * out_step + swizzled(m, first / 4 + i));
         r[4 * i] += __uint_as_float(y.x);
         r[4 * i + 1] += __uint_as_float(y.y);
         r[4 * i + 2] += __uint_as_float(y.z);
@@ -272,7 +310,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float y[8];
-        unpack8(slot16(sm, ring + stage * step + swizzled(m, first / 8 + i)), y);
+        unpack8(slot16(sm, ring + stage * out_step + swizzled(m, first / 8 + i)), y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[8 * i + j] += y[j];
       }
@@ -290,12 +328,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                        pack2(r[8 * i + 4], r[8 * i + 5]), pack2(r[8 * i + 6], r[8 * i + 7]));
     }
   };
-  if (!dead)
-    for (int s = 0; s + 1 < stages; ++s) fetch(half + 2 * s, s);
   int stage = 0;
   uint32_t parity = 0;
-  for (int32_t ob = half; ob < blocks && !dead; ob += 2) {
-    ring_wait(stages - 2);
+  for (int32_t ob = mine; ob < blocks && !dead; ob += jump) {
+    ring_wait(out_stages - 2);
     fence_proxy_async_smem();
     dead = half_or(half, dead);  // block ob has landed, and the out block before it has been written out
     if (dead) break;
@@ -303,19 +339,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       if (hwarp == 0) {
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t b = sm_u32 + ring + stage * step + b_at;
+          const uint32_t b = sm_u32 + ring + stage * out_step + b_at;
           for (int k = 0; k < terms; ++k)
             for (int32_t j = 0; j < ranks16; ++j)
-              tc_mma_bf16(tmem + kD2 + half * 64,
-                          smem_desc_k128(sm_u32 + v_at + (uint32_t)(k * rank_blocks + j / 4) * kOperandTile + (j % 4) * 32),
-                          smem_desc_k128(b + (uint32_t)(j / 4) * b_tile + (j % 4) * 32), idesc, (k | j) != 0);
+              tc_mma_bf16(tmem + kD2 + half * 64, smem_desc_k128(sm_u32 + v_at + (uint32_t)k * kOperandTile + j * 32),
+                          smem_desc_k128(b + j * 32), out_idesc, (k | j) != 0);
           tc_commit(&done2[half]);
         }
         __syncwarp();
       }
     }
-    // the step before this one has been read: its slot takes the block `stages - 1` steps ahead
-    fetch(ob + 2 * (stages - 1), stage == 0 ? stages - 1 : stage - 1);
+    // the step before this one has been read: its slot takes the block `out_stages - 1` steps ahead
+    fetch_out(ob + jump * (out_stages - 1), stage == 0 ? out_stages - 1 : stage - 1);
     if (rank > 0) {
       if (!mbar_wait(&done2[half], parity, &g_lora_flags)) dead = true;
       parity ^= 1;
@@ -339,7 +374,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
               *reinterpret_cast<const uint4*>(obuf + to8 + i * 32 * 128);
       }
     }
-    stage = stage + 1 == stages ? 0 : stage + 1;
+    stage = stage + 1 == out_stages ? 0 : stage + 1;
   }
   ring_wait(0);
   tc_fence_before();
@@ -347,34 +382,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Shared memory of a call: both rings (0 where they do not fit) and the rest.
-uint32_t mma_smem(const moe_lora_args& a, uint32_t* rest) {
-  const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3, rank_blocks = (a.max_rank + 63) / 64;
-  const uint32_t step1 = mma_step1((a.max_rank + 15) / 16);
-  const uint32_t step2 = std::max(mma_step2(a.y.data != nullptr, rank_blocks,
-                                            block_columns(a.y_dtype == MOE_DTYPE_F32, a.out_dtype == MOE_DTYPE_F32)),
-                                  1024u);
-  *rest = 1024 + 2 * kOperandTile + terms * rank_blocks * kOperandTile;
-  const uint32_t each = (224 * 1024 - *rest) / 2 / 1024 * 1024;
-  return each >= 2 * std::max(step1, step2) ? std::min(each, kMmaMaxStages * std::max(step1, step2)) : 0;
-}
-
 }  // namespace
 
-cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, cudaStream_t s) {
-  const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
-  uint32_t rest = 0;
-  const uint32_t ring = mma_smem(a, &rest);
+cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s) {
   static std::atomic<bool> configured[kMaxDevices];
-  const cudaError_t e = raise_smem_limit(lora_mma_kernel, 224 * 1024, configured);
+  cudaError_t e = raise_smem_limit(lora_mma_kernel, kMmaSmem, configured);
   if (e != cudaSuccess) return e;
-  return launch_ex(lora_mma_kernel, dim3((unsigned)tiles), dim3(kMmaThreads), 2 * ring + rest, s, true, a, p, terms,
-                   ring);
-}
-
-bool lora_mma_fits(const moe_lora_args& a) {
-  uint32_t rest = 0;
-  return mma_smem(a, &rest) > 0;
+  static std::atomic<int32_t> held[kMaxDevices][kLoraMaxCluster + 1];
+  int32_t cluster = 1;
+  e = lora_cluster(lora_mma_kernel, kMmaThreads, kMmaSmem, expected, held, &cluster);
+  if (e != cudaSuccess) return e;
+  const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
+  const uint32_t step = std::max(mma_step1((a.max_rank + 15) / 16),
+                                 mma_step2(a.y.data != nullptr, true, block_columns(a.y_dtype == MOE_DTYPE_F32,
+                                                                                 a.out_dtype == MOE_DTYPE_F32)));
+  const uint32_t rest = 1024 + 2 * kOperandTile + terms * kOperandTile;
+  const uint32_t ring = std::min((kMmaSmem - rest) / 2 / 1024 * 1024, kMmaMaxStages * step);  // two steps at least
+  return lora_launch_cluster(lora_mma_kernel, tiles, cluster, kMmaThreads, 2 * ring + rest, true, s, a, p, terms, ring);
 }
 
 cudaError_t lora_device_flags(int32_t* flags) {

@@ -345,40 +345,25 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
 
 }  // namespace
 
-cudaError_t launch_lora_rows(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // (tiles is a bound: one more for every adapter than full tiles alone would be)
+cudaError_t launch_lora_rows(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s) {
+  static std::atomic<bool> configured[kMaxDevices];
+  cudaError_t e = raise_smem_limit(lora_rows_kernel, 225 * 1024, configured);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int32_t> held[kMaxDevices][kLoraMaxCluster + 1];
   int32_t cluster = 1;
-  while (cluster < 4 && tiles * cluster * 2 <= sms + sms / 8) cluster *= 2;
+  e = lora_cluster(lora_rows_kernel, kLoraThreads, 225 * 1024, expected, held, &cluster);
+  if (e != cudaSuccess) return e;
   const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const uint32_t y_vecs = !a.y.data ? 0 : a.y_dtype == MOE_DTYPE_F32 ? 2 : 1;
   const uint32_t rest = terms * kRowsTile * ((a.max_rank + 63) / 64) * 128 +
                         (cluster > 1 ? kRowsTile * kPartPitch * 4 : 0);
-  // up to four ring steps, at least two: where the grid has more CTAs than the GPU SMs, as many as let two CTAs share
-  // an SM if those are two or more; else as many as fit one
+  // up to four ring steps, at least two: without a cluster as many as let two CTAs share an SM if those are two or
+  // more, else as many as fit one
   const uint32_t step = std::max(shrink_step(std::min(a.max_rank, kPass) / 8), expand_step((a.max_rank + 31) / 32, y_vecs));
   const uint32_t two = 112 * 1024, one = 224 * 1024;
-  uint32_t ring = std::min(4 * step, (tiles * cluster > sms && rest + 2 * step <= two ? two : one) - rest);
+  uint32_t ring = std::min(4 * step, (cluster == 1 && rest + 2 * step <= two ? two : one) - rest);
   ring = std::max<uint32_t>(ring, 2 * kRowsTile * kPartPitch * 4) / 128 * 128;
-  static std::atomic<bool> configured[kMaxDevices];
-  const cudaError_t e = raise_smem_limit(lora_rows_kernel, 225 * 1024, configured);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * cluster));
-  cfg.blockDim = dim3(kLoraThreads);
-  cfg.dynamicSmemBytes = ring + rest;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, lora_rows_kernel, a, p, terms, ring);
+  return lora_launch_cluster(lora_rows_kernel, tiles, cluster, kLoraThreads, ring + rest, true, s, a, p, terms, ring);
 }
 
 }  // namespace moe

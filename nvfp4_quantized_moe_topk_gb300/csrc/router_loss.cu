@@ -28,7 +28,22 @@ namespace moe {
 namespace {
 
 constexpr int kLossThreads = 512, kLossWarps = kLossThreads / 32;
-constexpr int32_t kLossOneBlock = 4 * kLossWarps;  // tokens that one block takes alone
+
+// Blocks of a call.  One block alone needs no join, so it takes what it can
+// walk in the time of one: up to `alone` tokens of a few sequences (each
+// sequence costs a walk of the block 1.5 us).  Else 16 tokens a block, one a
+// warp, or fewer where that leaves a block several sequences, up to two blocks
+// an SM.  Measured on a GB300, one block against several: balance loss, 64
+// experts, 64 tokens 4.6 / 7.1 us, 96 5.8 / 7.2, 128 6.5 / 7.2, with 256
+// experts 96 6.3 / 7.5 and 128 7.5 / 7.4; backward 16 tokens 3.9 / TODO, 32
+// 5.0 / 4.8, 64 7.3 / 4.8 (its join is needed by d_bias only).
+constexpr int32_t kBalanceAlone = 6 * kLossWarps, kBackwardAlone = kLossWarps, kAloneSeqs = 2;
+int32_t loss_blocks(int32_t n, int32_t S, int32_t alone) {
+  if (n <= 1 || (n <= alone && S <= kAloneSeqs)) return 1;
+  return std::min(kRouterLossBlocks, std::max((int32_t)(((int64_t)n + kLossWarps - 1) / kLossWarps), std::min(n, S)));
+}
+int32_t balance_blocks(int32_t n, int32_t S) { return loss_blocks(n, S, kBalanceAlone); }
+int32_t backward_blocks(int32_t n, int32_t S) { return loss_blocks(n, S, kBackwardAlone); }  // (never fewer)
 
 // The workspace of both calls.
 struct LossSpace {
@@ -42,7 +57,7 @@ struct LossSpace {
 __host__ __device__ inline int64_t round4(int64_t v) { return (v + 3) & ~int64_t(3); }
 
 LossSpace loss_space(void* ws, int32_t n, int32_t E, int32_t S) {
-  const int64_t slots = router_loss_blocks(n) + (int64_t)S;
+  const int64_t slots = backward_blocks(n, S) + (int64_t)S;
   LossSpace p;
   p.sums = static_cast<float*>(ws);
   p.picks = reinterpret_cast<int32_t*>(p.sums + round4(slots * E));
@@ -250,10 +265,19 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
     const int32_t at = seq_bound(a, s);
     if (!alone && at >= hi) break;
     const int32_t beg = max(lo, at), end = min(hi, seq_bound(a, s + 1));
-    if (!alone && beg >= end) continue;
+    if (beg >= end) {
+      if (alone) {
+        for (int32_t e = threadIdx.x; e < E; e += kLossThreads) {
+          prob_sums[(int64_t)s * E + e] = 0.f;
+          a.counts[(int64_t)s * E + e] = 0;
+        }
+        if (threadIdx.x == 0) a.tokens[s] = 0;
+      }
+      continue;
+    }
     float acc[N] = {};
     int32_t toks = 0;
-    for (int32_t j = (beg - lo) / kSpan; beg < end && j <= (end - 1 - lo) / kSpan; ++j) {
+    for (int32_t j = (beg - lo) / kSpan; j <= (end - 1 - lo) / kSpan; ++j) {
       if (gr.j != j) gr.load(a, lo, hi, j, true, true);
       gr.j = -1;
 #pragma unroll
@@ -518,8 +542,7 @@ __global__ void __launch_bounds__(32 * kBiasWarps)
 }
 
 // Tokens of a block.
-int32_t loss_per_block(int32_t n) {
-  const int32_t blocks = router_loss_blocks(n);
+int32_t loss_per_block(int32_t n, int32_t blocks) {
   return std::max(1, (int32_t)(((int64_t)n + blocks - 1) / blocks));
 }
 
@@ -530,8 +553,9 @@ cudaError_t balance_t(const moe_router_args& a, const LossSpace& ws, float* prob
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = raise_smem_limit(balance_kernel<VEC, N>, 80 * 1024, configured);
   if (e != cudaSuccess) return e;
-  balance_kernel<VEC, N><<<router_loss_blocks(a.n), kLossThreads, loss_smem(a.n_experts), s>>>(
-      a, ws, loss_per_block(a.n), prob_sums, loss);
+  const int32_t blocks = balance_blocks(a.n, a.n_seqs);
+  balance_kernel<VEC, N><<<blocks, kLossThreads, loss_smem(a.n_experts), s>>>(
+      a, ws, loss_per_block(a.n, blocks), prob_sums, loss);
   return cudaGetLastError();
 }
 
@@ -541,8 +565,9 @@ cudaError_t router_backward_t(const moe_router_args& a, const float* w, const fl
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = raise_smem_limit(router_backward_kernel<VEC, N>, 80 * 1024, configured);
   if (e != cudaSuccess) return e;
-  router_backward_kernel<VEC, N><<<router_loss_blocks(a.n), kLossThreads, loss_smem(a.n_experts), s>>>(
-      a, w, dw, d_loss, d_logits, sums, loss_per_block(a.n));
+  const int32_t blocks = backward_blocks(a.n, a.n_seqs);
+  router_backward_kernel<VEC, N><<<blocks, kLossThreads, loss_smem(a.n_experts), s>>>(
+      a, w, dw, d_loss, d_logits, sums, loss_per_block(a.n, blocks));
   return cudaGetLastError();
 }
 
@@ -550,13 +575,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 }  // namespace
 
-int32_t router_loss_blocks(int32_t n) {
-  if (n <= kLossOneBlock) return 1;
-  return (int32_t)std::min<int64_t>(kRouterLossBlocks, ((int64_t)n + kLossWarps - 1) / kLossWarps);
-}
-
 size_t router_loss_workspace(int32_t n, int32_t E, int32_t S) {
-  const int64_t slots = router_loss_blocks(n) + (int64_t)S;
+  const int64_t slots = backward_blocks(n, S) + (int64_t)S;
   return (size_t)(2 * round4(slots * E) + round4(slots) + round4(S) + 4) * 4;
 }
 
@@ -574,16 +594,17 @@ cudaError_t launch_balance_loss(const moe_router_args& a, float* prob_sums, floa
     e = vec ? balance_t<true, 16>(a, ws, prob_sums, loss, s) : balance_t<false, 16>(a, ws, prob_sums, loss, s);
   else
     e = vec ? balance_t<true, 32>(a, ws, prob_sums, loss, s) : balance_t<false, 32>(a, ws, prob_sums, loss, s);
-  if (e != cudaSuccess || router_loss_blocks(a.n) == 1) return e;
+  const int32_t blocks = balance_blocks(a.n, a.n_seqs);
+  if (e != cudaSuccess || blocks == 1) return e;
   int32_t cols = 32;
   while (cols < E && cols < kJoinThreads) cols *= 2;
   return launch_ex(balance_join_kernel, dim3((unsigned)a.n_seqs), dim3(kJoinThreads), 0, s, true, a, ws,
-                   loss_per_block(a.n), cols, prob_sums, loss);
+                   loss_per_block(a.n, blocks), cols, prob_sums, loss);
 }
 
 cudaError_t launch_router_backward(const moe_router_args& a, const float* w, const float* dw, const float* d_loss,
                                    float* d_logits, float* d_bias, void* workspace, cudaStream_t s) {
-  const int32_t E = a.n_experts, blocks = router_loss_blocks(a.n);
+  const int32_t E = a.n_experts, blocks = backward_blocks(a.n, a.n_seqs);
   float* sums = !d_bias ? nullptr : blocks == 1 ? d_bias : static_cast<float*>(workspace);
   const bool vec = E % 4 == 0 && aligned16(a.logits) && aligned16(d_logits);
   cudaError_t e;

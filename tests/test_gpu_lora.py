@@ -358,3 +358,26 @@ def test_long_repeated_on_another_stream_and_in_a_graph(dev):
     g.replay()
     torch.cuda.synchronize()
     c.check(out)
+
+
+# ------------------------------------------------------------------ tiles that a cluster shares
+
+@pytest.mark.parametrize("n,L", [(520, 3), (1300, 5), (2600, 2), (4400, 16), (7000, 6)])
+@pytest.mark.parametrize("inp,out", [(8, 1040), (328, 8), (2056, 520)])
+@pytest.mark.parametrize("R", [8, 48, 64, 96, 128])
+def test_clusters(dev, n, L, inp, out, R):
+    """Few tiles of many tokens: CTAs of a cluster split both products, some of them with nothing to do in one."""
+    from nvfp4_quantized_moe_topk_gb300 import api
+
+    y, o = [("bf16", "bf16"), ("fp32", "bf16"), ("fp32", "fp32"), ("bf16", "fp32")][(n // 20 + R // 8) % 4]
+    ranks = [max(R - 3 * l, 0) for l in range(L)]
+    c = Case(dev, _ids(n, L, n + R, run=150), inp, out, L, R, y, o, ranks, seed=R)
+    for l in range(L):
+        c.a[l, ranks[l]:] = float("nan")
+        c.b[l, :, ranks[l]:] = float("nan")
+    got = c.run()
+    c.check(got)
+    import torch
+
+    assert torch.equal(c.run(), got)
+    assert api.lora_device_error() == 0

@@ -139,6 +139,13 @@ def test_many_short_sequences(dev):
     _check(Batch(dev, 3000, 64, 4, list(range(0, 3001, 3)), 0.2))
 
 
+@pytest.mark.parametrize("n,ends", [
+    (1, [0] * 40 + [1] * 24), (3, [0, 1, 1, 2, 3]), (16, list(range(17))), (33, sorted(list(range(34)) + [5, 5, 9, 33])),
+    (64, [0, 10, 20, 20, 50, 64]), (96, [0, 0, 96]), (97, [0, 40, 97]), (300, list(range(301)))])
+def test_few_tokens_of_several_sequences(dev, n, ends):
+    _check(Batch(dev, n, 72, 3, ends, 0.1, seed=n))
+
+
 def test_sequences_wholly_masked_and_all_masked(dev):
     import torch
 
