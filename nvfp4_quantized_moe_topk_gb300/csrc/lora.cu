@@ -490,8 +490,8 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // every group has at most one tile that is not full, half of one on average
-  const int32_t groups = std::min(n, L + 1), tiles = n / mt + groups, expected = n / mt + (groups + 1) / 2;
+  // every group has at most one tile that is not full; an adapter has half of one on average
+  const int32_t tiles = n / mt + std::min(n, L + 1), expected = n / mt + std::min(n, L) / 2;
   if (mma) return launch_lora_mma(a, p, tiles, expected, s);
   if (!small) return launch_lora_rows(a, p, tiles, expected, s);
   int32_t cluster = 1;
