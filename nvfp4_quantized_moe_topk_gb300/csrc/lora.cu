@@ -475,7 +475,7 @@ size_t lora_workspace(int32_t n, int32_t n_adapters) {
 
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s) {
   const int32_t n = a.n, L = a.n_adapters;
-  const bool fused = n <= kFusedTokens, small = n <= small_tokens(a.max_rank), mma = !small && a.max_rank <= kMmaRank;
+  const bool fused = n <= kFusedTokens, small = n <= small_tokens(a.max_rank), mma = !small && lora_mma_fits(a);
   const int32_t mt = mma ? kMmaTokens : small ? 16 : kRowsTile;
   const LoraPlan p = fused ? LoraPlan{} : lora_plan(workspace, n, L);
   if (!fused) {

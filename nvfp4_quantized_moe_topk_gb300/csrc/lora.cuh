@@ -276,9 +276,9 @@ cudaError_t lora_cluster(void (*kernel)(KArgs...), int threads, size_t smem, int
   return cudaSuccess;
 }
 
-// lora_mma.cu: at most `tiles` tiles of kMmaTokens tokens, ranks up to kMmaRank.
+// lora_mma.cu: at most `tiles` tiles of kMmaTokens tokens; whether a call's sizes fit its shared memory.
 constexpr int kMmaTokens = 128;
-constexpr int kMmaRank = 64;
+bool lora_mma_fits(const moe_lora_args& a);
 cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s);
 
 // lora_rows.cu: at most `tiles` tiles of kRowsTile tokens.

@@ -29,7 +29,7 @@ constexpr int kMmaTile = kMmaTokens;
 constexpr int kMmaThreads = 512, kMmaHalf = kMmaThreads / 2;
 constexpr uint32_t kOperandTile = 128 * 128;  // 128 rows of 64 bf16
 constexpr uint32_t kMmaMaxStages = 8;
-constexpr uint32_t kMmaSmem = 224 * 1024;
+constexpr uint32_t kMmaSmem = 226 * 1024;
 constexpr uint32_t kD2 = 256, kTmemCols = 512;  // tensor memory: the halves' D1 in 128 columns each, then their D2
 
 // Set where a bounded wait ran out; read by moe_lora_get_device_error.
@@ -56,10 +56,12 @@ __device__ __forceinline__ bool half_or(int half, bool any) {
 __host__ __device__ inline int32_t block_columns(bool y_f32, bool out_f32) { return y_f32 || out_f32 ? 32 : 64; }
 // Bytes of a half's ring steps: x and A; y and B.
 __host__ __device__ inline uint32_t mma_step1(int32_t ranks16) { return kOperandTile + (uint32_t)ranks16 * 16 * 128; }
-__host__ __device__ inline uint32_t mma_step2(bool has_y, bool has_b, int32_t columns) {
-  return (has_y ? kOperandTile : 0) + (has_b ? columns * 128 : 0);
+__host__ __device__ inline uint32_t mma_step2(bool has_y, int32_t rank_blocks, int32_t columns) {
+  return (has_y ? kOperandTile : 0) + (uint32_t)rank_blocks * columns * 128;
 }
 
+// RB: blocks of 64 ranks (1 or 2).
+template <int RB>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     lora_mma_kernel(const moe_lora_args a, const LoraPlan plan, int32_t terms, uint32_t ring_bytes) {
   extern __shared__ __align__(16) char sm_raw[];
@@ -96,11 +98,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int32_t rank = t.rank, ranks16 = (rank + 15) / 16;
-  // the halves' rings; the halves' out blocks; v [terms] operand tiles
+  // the halves' rings; the halves' out blocks; v [terms][RB] operand tiles
   const uint32_t sm_u32 = smem_u32(sm), ring = half * ring_bytes;
   char* obuf = sm + 2 * ring_bytes + half * kOperandTile;
   const uint32_t v_at = 2 * ring_bytes + 2 * kOperandTile;
-  static_assert(kMmaRank == 64, "a rank of v is one of 4 x 16, a row of A or B 128 bytes of one operand tile");
   const uint32_t quadrant = (uint32_t)(32 * (warp & 3)) << 16;  // this warp's lanes of tensor memory
   const int m = 32 * (warp & 3) + lane;                         // its thread's token
   const int p8 = htid & 7, r8 = htid >> 3;  // copies of 128-byte rows: piece, first row (the others 32, 64, 96 further)
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const bool yf = a.y_dtype == MOE_DTYPE_F32, of = a.out_dtype == MOE_DTYPE_F32, has_y = a.y.data != nullptr;
   const int32_t columns = block_columns(yf, of), blocks = (a.out_features + columns - 1) / columns;
   const uint32_t y_size = yf ? 4 : 2, o_size = of ? 4 : 2, out_idesc = idesc_bf16(128, (uint32_t)columns);
-  const uint32_t b_at = has_y ? kOperandTile : 0;
-  const uint32_t out_step = max(mma_step2(has_y, rank > 0, columns), 1024u);
+  const uint32_t b_at = has_y ? kOperandTile : 0, b_tile = columns * 128;
+  const uint32_t out_step = max(mma_step2(has_y, rank > 0 ? RB : 0, columns), 1024u);
   const int out_stages = (int)min(kMmaMaxStages, ring_bytes / out_step);
   // rows of y and out in vectors of 16 bytes: a product of two 32-bit numbers a row
   const uint32_t y_stride = (uint32_t)((a.y.stride ? a.y.stride : a.out_features) * y_size / 16);
@@ -135,24 +136,27 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
       }
       const int32_t left = min(a.out_features - ob * columns, columns);
-      const int32_t rest = rank - 8 * p8;  // ranks in this thread's piece and after it
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (p8 >= 2 * ranks16 || r8 + 32 * i >= left) break;
-        const uint32_t to = at + b_at + i * 32 * 128;
-        const char* from = B + (uint64_t)(uint32_t)(ob * columns + 32 * i) * b_bytes;
-        if (rest >= 8) {
-          ring16(sm_u32 + to, from);
-        } else {  // what lies beyond the rank may hold anything
-          uint4 b = make_uint4(0, 0, 0, 0);
-          if (rest > 0) {
-            b = __ldg(reinterpret_cast<const uint4*>(from));
-            b.x &= rest >= 2 ? 0xffffffffu : 0xffffu;
-            b.y &= rest >= 4 ? 0xffffffffu : rest == 3 ? 0xffffu : 0u;
-            b.z &= rest >= 6 ? 0xffffffffu : rest == 5 ? 0xffffu : 0u;
-            b.w &= rest == 7 ? 0xffffu : 0u;
+      for (int k = 0; k < RB; ++k) {
+        const int32_t rest = rank - 64 * k - 8 * p8;  // ranks in this thread's piece and after it
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (p8 + 8 * k >= 2 * ranks16 || r8 + 32 * i >= left) break;
+          const uint32_t to = at + b_at + k * b_tile + i * 32 * 128;
+          const char* from = B + ((uint64_t)(uint32_t)(ob * columns + 32 * i) * b_bytes + 128 * k);
+          if (rest >= 8) {
+            ring16(sm_u32 + to, from);
+          } else {  // what lies beyond the rank may hold anything
+            uint4 b = make_uint4(0, 0, 0, 0);
+            if (rest > 0) {
+              b = __ldg(reinterpret_cast<const uint4*>(from));
+              b.x &= rest >= 2 ? 0xffffffffu : 0xffffu;
+              b.y &= rest >= 4 ? 0xffffffffu : rest == 3 ? 0xffffu : 0u;
+              b.z &= rest >= 6 ? 0xffffffffu : rest == 5 ? 0xffffu : 0u;
+              b.w &= rest == 7 ? 0xffffu : 0u;
+            }
+            *reinterpret_cast<uint4*>(sm + to) = b;
           }
-          *reinterpret_cast<uint4*>(sm + to) = b;
         }
       }
     }
@@ -181,14 +185,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) ring16(sm_u32 + at + i * 32 * 128, xr[i] + off);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2 * RB; ++i)
             if (r8 + 32 * i < a_rows)
               ring16(sm_u32 + at + kOperandTile + i * 32 * 128, Ar + ((uint64_t)(32 * i) * row_bytes + off));
         } else {  // past the row's end
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             *reinterpret_cast<uint4*>(sm + at + i * 32 * 128) = make_uint4(0, 0, 0, 0);
-            if (r8 + 32 * i < a_rows)
+            if (i < 2 * RB && r8 + 32 * i < a_rows)
               *reinterpret_cast<uint4*>(sm + at + kOperandTile + i * 32 * 128) = make_uint4(0, 0, 0, 0);
           }
         }
@@ -226,65 +230,74 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     if (mine < chunks && !dead && !mbar_wait(&done1[half][last], last_parity, &g_lora_flags)) dead = true;
     ring_wait(0);
-    if (!dead)
+    // the CTAs' sums of a cluster meet in the (still unused) out blocks, those of two blocks of ranks in the rings
+    const bool ring_meets = RB > 1 && C > 1;
+    if (!dead && !ring_meets)
       for (int s = 0; s + 1 < out_stages; ++s) fetch_out(mine + jump * s, s);
     dead = __syncthreads_or(dead);
     tc_fence_after();
-    // D1 -> v: a thread its token's 16 ranks from 16 j on.  In a cluster the CTAs' sums meet in the (still unused) out
-    // blocks, [4 ranks][128 tokens], and are added in the order of the CTAs, the same in each of them.
-    const int32_t j = warp >> 2;
-    const bool has = j < ranks16 && !dead;
-    float s[16];
-    if (has) {
+    // D1 -> v: a thread its token's 16 ranks from 16 j on, j = j0, j0 + 4
+    const int32_t j0 = warp >> 2;
+    float s[RB][16];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int32_t j = j0 + 4 * b;
+      if (j >= ranks16 || dead) continue;
       uint32_t d0[16] = {}, d1[16] = {};
       if ((int32_t)cr * 2 < chunks) tmem_ld16(tmem + quadrant + 16 * j, d0);  // (a half without a step has no sum)
       if ((int32_t)cr * 2 + 1 < chunks) tmem_ld16(tmem + quadrant + 128 + 16 * j, d1);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(d0[i]) + __uint_as_float(d1[i]);
+      for (int i = 0; i < 16; ++i) s[b][i] = __uint_as_float(d0[i]) + __uint_as_float(d1[i]);
     }
-    if (C > 1) {
-      float* meet = reinterpret_cast<float*>(sm + 2 * ring_bytes) + (4 * j * kMmaTile + m) * 4;
-      if (has) {
+    if (C > 1) {  // [4 ranks][128 tokens], added in the order of the CTAs, the same in each of them
+      float* meet = reinterpret_cast<float*>(ring_meets ? sm : sm + 2 * ring_bytes) + m * 4;
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(meet + i * kMmaTile * 4) =
-              make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
-      }
+          if (j0 + 4 * b < ranks16 && !dead)
+            *reinterpret_cast<float4*>(meet + (4 * (j0 + 4 * b) + i) * kMmaTile * 4) =
+                make_float4(s[b][4 * i], s[b][4 * i + 1], s[b][4 * i + 2], s[b][4 * i + 3]);
       cluster_sync();
-      if (has) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 0.f;
+      for (int b = 0; b < RB; ++b) {
+        if (j0 + 4 * b >= ranks16 || dead) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
         for (uint32_t r = 0; r < C; ++r) {
           float4 p[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = peer_float4(meet + i * kMmaTile * 4, r);
+          for (int i = 0; i < 4; ++i) p[i] = peer_float4(meet + (4 * (j0 + 4 * b) + i) * kMmaTile * 4, r);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s[4 * i] += p[i].x;
-            s[4 * i + 1] += p[i].y;
-            s[4 * i + 2] += p[i].z;
-            s[4 * i + 3] += p[i].w;
+            s[b][4 * i] += p[i].x;
+            s[b][4 * i + 1] += p[i].y;
+            s[b][4 * i + 2] += p[i].z;
+            s[b][4 * i + 3] += p[i].w;
           }
         }
       }
-      cluster_arrive();  // (waited for before the first write to the out blocks)
+      cluster_arrive();  // (waited for before the first write to where they met)
     }
-    if (has) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = 16 * j + i < rank ? s[i] * t.scale : 0.f;
+    for (int b = 0; b < RB; ++b) {
+      const int32_t j = j0 + 4 * b;
+      if (j >= ranks16 || dead) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = 16 * j + i < rank ? s[b][i] * t.scale : 0.f;
       for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t o[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float &lo = s[8 * h + 2 * i], &hi = s[8 * h + 2 * i + 1];
+            float &lo = s[b][8 * h + 2 * i], &hi = s[b][8 * h + 2 * i + 1];
             o[i] = pack2(lo, hi);
             lo -= bf16lo(o[i]);
             hi -= bf16hi(o[i]);
           }
-          *reinterpret_cast<uint4*>(sm + v_at + (uint32_t)k * kOperandTile + swizzled(m, j * 2 + h)) =
+          *reinterpret_cast<uint4*>(sm + v_at + (uint32_t)(k * RB + b) * kOperandTile + swizzled(m, j0 * 2 + h)) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
@@ -292,6 +305,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     tc_fence_before();
     fence_proxy_async_smem();
     if (C > 1) cluster_wait();
+    if (ring_meets && !dead)
+      for (int s = 0; s + 1 < out_stages; ++s) fetch_out(mine + jump * s, s);
     __syncthreads();
     tc_fence_after();
   } else {
@@ -353,8 +368,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           const uint32_t b = sm_u32 + ring + stage * out_step + b_at;
           for (int k = 0; k < terms; ++k)
             for (int32_t j = 0; j < ranks16; ++j)
-              tc_mma_bf16(tmem + kD2 + half * 64, smem_desc_k128(sm_u32 + v_at + (uint32_t)k * kOperandTile + j * 32),
-                          smem_desc_k128(b + j * 32), out_idesc, (k | j) != 0);
+              tc_mma_bf16(tmem + kD2 + half * 64, smem_desc_k128(sm_u32 + v_at + (uint32_t)(k * RB + j / 4) * kOperandTile + (j % 4) * 32),
+                          smem_desc_k128(b + (uint32_t)(j / 4) * b_tile + (j % 4) * 32), out_idesc, (k | j) != 0);
           tc_commit(&done2[half]);
         }
         __syncwarp();
@@ -393,23 +408,32 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-}  // namespace
-
-cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s) {
+template <int RB>
+cudaError_t lora_mma_launch(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s) {
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = raise_smem_limit(lora_mma_kernel, kMmaSmem, configured);
+  cudaError_t e = raise_smem_limit(lora_mma_kernel<RB>, kMmaSmem, configured);
   if (e != cudaSuccess) return e;
   static std::atomic<int32_t> held[kMaxDevices][kLoraMaxCluster + 1];
   int32_t cluster = 1;
-  e = lora_cluster(lora_mma_kernel, kMmaThreads, kMmaSmem, expected, held, &cluster);
+  e = lora_cluster(lora_mma_kernel<RB>, kMmaThreads, kMmaSmem, expected, held, &cluster);
   if (e != cudaSuccess) return e;
   const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const uint32_t step = std::max(mma_step1((a.max_rank + 15) / 16),
-                                 mma_step2(a.y.data != nullptr, true, block_columns(a.y_dtype == MOE_DTYPE_F32,
-                                                                                 a.out_dtype == MOE_DTYPE_F32)));
-  const uint32_t rest = 1024 + 2 * kOperandTile + terms * kOperandTile;
-  const uint32_t ring = std::min((kMmaSmem - rest) / 2 / 1024 * 1024, kMmaMaxStages * step);  // two steps at least
-  return lora_launch_cluster(lora_mma_kernel, tiles, cluster, kMmaThreads, 2 * ring + rest, true, s, a, p, terms, ring);
+                                 mma_step2(a.y.data != nullptr, RB, block_columns(a.y_dtype == MOE_DTYPE_F32,
+                                                                                  a.out_dtype == MOE_DTYPE_F32)));
+  const uint32_t rest = 1024 + 2 * kOperandTile + terms * RB * kOperandTile;
+  // (two steps at least: 2 x 24 KB of 72, or with RB 2 and two terms 2 x 32 of 64)
+  const uint32_t ring = std::min((kMmaSmem - rest) / 2 / 1024 * 1024, kMmaMaxStages * step);
+  return lora_launch_cluster(lora_mma_kernel<RB>, tiles, cluster, kMmaThreads, 2 * ring + rest, true, s, a, p, terms,
+                             ring);
+}
+
+}  // namespace
+
+bool lora_mma_fits(const moe_lora_args& a) { return a.max_rank <= 64 || a.out_dtype == MOE_DTYPE_BF16; }
+
+cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s) {
+  return a.max_rank <= 64 ? lora_mma_launch<1>(a, p, tiles, expected, s) : lora_mma_launch<2>(a, p, tiles, expected, s);
 }
 
 cudaError_t lora_device_flags(int32_t* flags) {
