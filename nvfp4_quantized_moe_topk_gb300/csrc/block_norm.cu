@@ -10,11 +10,16 @@
 // norm's statistics come from the values that the first one left there.
 // Memory bounds it: per element the residual in and out, the branch and x.
 //
-// Batches of several rows per CTA run persistent CTAs, each over rows b, b +
+// Persistent CTAs (one for every row of a small batch), each over rows b, b +
 // CTAs, ...: a thread copies its part of the next rows into shared memory by
 // asynchronous copies while it works on the current one and reads back only
 // what its warp copied, so the copies need no barrier and no registers; the
-// weights stay in registers over all rows.
+// weights stay in registers over all rows.  Measured on a GB300: 16384 rows of
+// 4096, fp32 residual, bf16 branch: 136 us, 5.9 TB/s (87 % of a copy's rate); 1536
+// threads an SM or two vectors a thread gain nothing.  One row of 2688: 2.9 us,
+// latency of a launch, one load and two sums over the CTA (a kernel without
+// the ring, a CTA a row, takes as long, and with 304 rows of 8192 9.7 us
+// instead of 7.6, so there is none).
 #include "block_norm.cuh"
 
 namespace moe {

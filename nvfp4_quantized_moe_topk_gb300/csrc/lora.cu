@@ -3,11 +3,15 @@
 //
 //   v = A[l] x (over the adapter's rank),  out = y + B[l] (scale[l] v)
 //
-// Tokens are grouped by adapter into tiles of 16 or 32, and one CTA (or a
-// cluster of CTAs, where there are few tiles) takes a tile through both
-// products: v never leaves the SM.  Both are bf16 warp matrix instructions
-// with tokens as rows.  At ranks up to 128 they are far below the tensor
-// cores' rate; what bounds the call is moving x, y and out, so every thread
+// Tokens are grouped by adapter into tiles, and one CTA (or a cluster of CTAs,
+// where there are few tiles) takes a tile through both products: v never
+// leaves the SM.  Larger batches take tiles of 128 (lora_mma.cu) or 64
+// (lora_rows.cu); here tiles are 16 tokens.  Both products are bf16 warp matrix
+// instructions with tokens as rows.  What bounds a call of few tokens is
+// latency: finding the tile, two chains of copies and a meeting of the cluster
+// between them (32 tokens, 2688 to 1856, rank 16: 7.4 us on a GB300, of which
+// the bytes are 0.5), so what counts is how many bytes are in flight at once.
+// Every thread
 // copies the 16-byte pieces of the operands that its own fragments are made of
 // into its own slots of a shared-memory ring, some steps ahead, by
 // asynchronous copies, and reads back only those: no barrier stands in the
@@ -25,7 +29,8 @@
 //     sectors.  v enters as the sum of two bf16 terms (16 bits of mantissa),
 //     three for an fp32 out (24 bits).
 //
-// Grouping: up to kFusedTokens tokens every CTA ranks the ids itself; beyond,
+// Grouping: up to kFusedTokens tokens every CTA ranks the ids itself (one id a
+// thread, one launch: 100 tokens 8.6 us against 10.8, 256 10.8 / 11.6); beyond,
 // a one-CTA kernel (two kernels past kPlanSlice tokens) sorts the tokens by
 // adapter into the workspace.  A token's row of the products depends on no
 // other token, so the order inside a group does not matter to the result.
@@ -162,9 +167,17 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// More tokens than these take the larger tiles of lora_mma.cu (ranks up to
-// kMmaRank) or lora_rows.cu.  TODO figures
-inline int32_t small_tokens(int32_t max_rank) { return max_rank <= 32 ? 1280 : 512; }
+// More tokens than these take the larger tiles of lora_mma.cu or lora_rows.cu:
+// there the adapter's matrices are read less often, which counts the more the
+// larger the rank, but fewer CTAs share a small batch.  Tiles of 16 against
+// 128, us on a GB300:
+//   4096 to 4096, rank 16: 1024 tokens 16.1 / 22.2, 1536 27.4 / 25.7, 3000 37.8 / 29.7
+//   4096 to 1024, rank 32: 1024 13.0 / 19.9, 1536 16.0 / 20.1, 2048 21.4 / 20.0, 3000 29.5 / 21.5
+//   4096 to 4096, rank 64: 300 23.7 / 23.8, 640 34.4 / 32.4, 1024 51.0 / 33.9, 2048 59.6 / 36.4
+//   rank 128: 512 40.2, 768 64.2 / 44.4, 1024 77.8 / 46.7; against 64 (lora_rows.cu): 512 40.2 / 46.3, 768 64.2 / 52.1
+constexpr int32_t kSmallTokens = 1280, kSmallTokensWide = 512;  // max_rank up to 32, above
+static_assert(kSmallTokens >= kFusedTokens && kSmallTokensWide >= kFusedTokens, "the other kernels need the plan");
+inline int32_t small_tokens(int32_t max_rank) { return max_rank <= 32 ? kSmallTokens : kSmallTokensWide; }
 
 // Tiles of 16 tokens; NT groups of 8 ranks a pass of the first product.
 template <int NT>
@@ -494,8 +507,11 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
   const int32_t tiles = n / mt + std::min(n, L + 1), expected = n / mt + std::min(n, L) / 2;
   if (mma) return launch_lora_mma(a, p, tiles, expected, s);
   if (!small) return launch_lora_rows(a, p, tiles, expected, s);
+  // Up to 400 CTAs, of which two share an SM (`tiles` is a bound, so some have nothing to do).  With 608 a call of 768
+  // tokens takes 20 us instead of 15, with 304 one of 1024 18 instead of 15.5; clusters of 4 or 2 for a single token
+  // 7.1 and 9.6 us instead of 6.0.
   int32_t cluster = 1;
-  while (cluster < 8 && tiles * cluster * 2 <= 608) cluster *= 2;
+  while (cluster < 8 && tiles * cluster * 2 <= 400) cluster *= 2;
   if (a.max_rank <= 16) return lora_launch<2>(a, p, fused, tiles, cluster, s);
   if (a.max_rank <= 32) return lora_launch<4>(a, p, fused, tiles, cluster, s);
   return lora_launch<8>(a, p, fused, tiles, cluster, s);

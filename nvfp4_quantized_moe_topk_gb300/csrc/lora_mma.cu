@@ -1,5 +1,5 @@
-// lora_mma.cu -- the adapters for batches that fill the GPU with tiles of 128
-// tokens: one CTA takes a tile through both products on the tensor cores'
+// lora_mma.cu -- the adapters for many tokens: a CTA, or a cluster of CTAs,
+// takes 128 tokens of one adapter through both products on the tensor cores'
 // asynchronous path (tcgen05, accumulators in tensor memory).
 //
 // Moving x, y and out bounds it.  Warp-level matrix instructions reread the
@@ -9,7 +9,12 @@
 // What a step then costs is issuing its copies, one barrier and a few waits,
 // one after the other; so two halves of the CTA (8 warps each) take alternate
 // steps with barriers, rings and accumulators of their own, and one half's
-// copies run beside the other's waits.
+// copies run beside the other's waits (16384 tokens, 4096 to 2048, rank 64,
+// bf16: 92 us with one half of 512 threads, 77 with two, of which the bytes are
+// 40; 3.6 TB/s).  Where there are fewer tiles than SMs, the CTAs of a cluster
+// take turns with the steps of both products and add their D1 through each
+// other's shared memory (4096 tokens, 4096 to 4096, rank 64: 94 us with a CTA a
+// tile, 39 with four).
 //
 //   first product:  D1[128 tokens][ranks] += x chunk . A chunk^T, 64 columns of
 //     in_features a step (the tokens' rows are gathered: 8 lanes copy 128 bytes

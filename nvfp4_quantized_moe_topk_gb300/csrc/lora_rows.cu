@@ -1,15 +1,17 @@
-// lora_rows.cu -- the adapters for many tokens: a CTA (or a cluster of up to
-// four) takes 64 tokens of one adapter through both products.
+// lora_rows.cu -- the adapters for many tokens where lora_mma.cu's operands do
+// not fit its shared memory (ranks above 64 with an fp32 out: three terms of v):
+// a CTA, or a cluster of CTAs, takes 64 tokens of one adapter through both
+// products with warp matrix instructions.
 //
-// Moving x, y and out bounds it, so what counts is how much of them is in
-// flight and that the adapter's matrices, which every tile of the adapter
-// reads again from L2, take little of the rings: with 64 tokens a tile A and B
-// are read once per 64 rows of x and y.  Warps are 4 groups of 16 tokens x 2
-// halves.  In the first product the halves take alternate 64-column chunks of
-// in_features, in the second alternate 64-column blocks of out_features.  The
-// four warps of a half share its chunk of A (or B) in shared memory, copied by
-// all of them and met at one barrier a step; their own tokens' 16-byte pieces
-// of x (or y) go through thread-private slots of the same ring steps.
+// With 64 tokens a tile A and B are read once per 64 rows of x and y.  Warps
+// are 4 groups of 16 tokens x 2 halves.  In the first product the halves take
+// alternate 64-column chunks of in_features, in the second alternate 64-column
+// blocks of out_features.  The four warps of a half share its chunk of A (or B)
+// in shared memory, copied by all of them and met at one barrier a step; their
+// own tokens' 16-byte pieces of x (or y) go through thread-private slots of the
+// same ring steps.  Every 16 tokens reread A and B from shared memory, which at
+// these ranks is what bounds it: 4096 tokens, 4096 to 4096, rank 128 99 us with
+// a bf16 out, 16384 349 (lora_mma.cu: 50 and 135; the bytes are 15 and 60).
 //
 // Shared rows of A, B and v are read as 16 bytes by lane (row g, piece q); rows
 // whose pitch is a multiple of 128 bytes are stored with pieces 0-3 and 4-7

@@ -15,6 +15,12 @@
 // slots of a sequence in block order: no atomics on floats, the same bits on
 // every run.  Batches that one block holds need no join: one launch.
 //
+// Measured on a GB300: loss of 16384 tokens, 128 experts, 7 sequences, two
+// launches 13.8 us (what it reads takes 1.3 at a copy's rate: a warp's chain of
+// maximum, exponentials, sum, and then the join; 4.2 to 4.5 us for 33 tokens in one
+// launch); backward of 16384 tokens, 512 experts 22.4 us, 3 TB/s, of 4314 tokens,
+// 128 experts 8.5.
+//
 // The top-k weights' gradient touches k of a row's experts: each warp adds it
 // to its row through its own row of shared memory, zero but for those.
 #include <algorithm>
@@ -29,21 +35,20 @@ namespace {
 
 constexpr int kLossThreads = 512, kLossWarps = kLossThreads / 32;
 
-// Blocks of a call.  One block alone needs no join, so it takes what it can
-// walk in the time of one: up to `alone` tokens of a few sequences (each
-// sequence costs a walk of the block 1.5 us).  Else 16 tokens a block, one a
-// warp, or fewer where that leaves a block several sequences, up to two blocks
-// an SM.  Measured on a GB300, one block against several: balance loss, 64
-// experts, 64 tokens 4.6 / 7.1 us, 96 5.8 / 7.2, 128 6.5 / 7.2, with 256
-// experts 96 6.3 / 7.5 and 128 7.5 / 7.4; backward 16 tokens 3.9 / TODO, 32
-// 5.0 / 4.8, 64 7.3 / 4.8 (its join is needed by d_bias only).
-constexpr int32_t kBalanceAlone = 6 * kLossWarps, kBackwardAlone = kLossWarps, kAloneSeqs = 2;
-int32_t loss_blocks(int32_t n, int32_t S, int32_t alone) {
-  if (n <= 1 || (n <= alone && S <= kAloneSeqs)) return 1;
-  return std::min(kRouterLossBlocks, std::max((int32_t)(((int64_t)n + kLossWarps - 1) / kLossWarps), std::min(n, S)));
+// Blocks of a call: 16 tokens a block, one a warp, or fewer where there are
+// more sequences than that (each costs a walk of the block some 1.5 us), up to
+// two blocks an SM (with four, 16384 tokens of 64 experts take 17.6 instead of
+// 13.7 us in the loss, 27 instead of 23 in the backward pass).  The loss of one
+// block needs no join, so there one block takes up to 96 tokens of up to 4
+// sequences.  One block against several, measured on a GB300, loss with 64
+// experts: 64 tokens 4.6 / 7.1 us, 96 6.0 / 7.2, 128 6.5 / 7.2, with 256 experts
+// 128 7.5 / 7.4; 64 tokens of 4 sequences 9.9 / 10.8, of 16 30 / 11.4.  (Backward,
+// whose join only adds d_bias up: 32 tokens 5.0 / 4.8, 64 7.3 / 4.8.)
+int32_t loss_blocks(int32_t n, int32_t S) {
+  const int32_t by_tokens = (int32_t)(((int64_t)n + kLossWarps - 1) / kLossWarps);
+  return std::max(1, std::min(kRouterLossBlocks, std::max(by_tokens, std::min(n, S))));
 }
-int32_t balance_blocks(int32_t n, int32_t S) { return loss_blocks(n, S, kBalanceAlone); }
-int32_t backward_blocks(int32_t n, int32_t S) { return loss_blocks(n, S, kBackwardAlone); }  // (never fewer)
+int32_t balance_blocks(int32_t n, int32_t S) { return n <= 6 * kLossWarps && S <= 4 ? 1 : loss_blocks(n, S); }
 
 // The workspace of both calls.
 struct LossSpace {
@@ -57,7 +62,7 @@ struct LossSpace {
 __host__ __device__ inline int64_t round4(int64_t v) { return (v + 3) & ~int64_t(3); }
 
 LossSpace loss_space(void* ws, int32_t n, int32_t E, int32_t S) {
-  const int64_t slots = backward_blocks(n, S) + (int64_t)S;
+  const int64_t slots = loss_blocks(n, S) + (int64_t)S;
   LossSpace p;
   p.sums = static_cast<float*>(ws);
   p.picks = reinterpret_cast<int32_t*>(p.sums + round4(slots * E));
@@ -565,7 +570,7 @@ cudaError_t router_backward_t(const moe_router_args& a, const float* w, const fl
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = raise_smem_limit(router_backward_kernel<VEC, N>, 80 * 1024, configured);
   if (e != cudaSuccess) return e;
-  const int32_t blocks = backward_blocks(a.n, a.n_seqs);
+  const int32_t blocks = loss_blocks(a.n, a.n_seqs);
   router_backward_kernel<VEC, N><<<blocks, kLossThreads, loss_smem(a.n_experts), s>>>(
       a, w, dw, d_loss, d_logits, sums, loss_per_block(a.n, blocks));
   return cudaGetLastError();
@@ -576,7 +581,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 }  // namespace
 
 size_t router_loss_workspace(int32_t n, int32_t E, int32_t S) {
-  const int64_t slots = backward_blocks(n, S) + (int64_t)S;
+  const int64_t slots = loss_blocks(n, S) + (int64_t)S;
   return (size_t)(2 * round4(slots * E) + round4(slots) + round4(S) + 4) * 4;
 }
 
@@ -604,7 +609,7 @@ cudaError_t launch_balance_loss(const moe_router_args& a, float* prob_sums, floa
 
 cudaError_t launch_router_backward(const moe_router_args& a, const float* w, const float* dw, const float* d_loss,
                                    float* d_logits, float* d_bias, void* workspace, cudaStream_t s) {
-  const int32_t E = a.n_experts, blocks = backward_blocks(a.n, a.n_seqs);
+  const int32_t E = a.n_experts, blocks = loss_blocks(a.n, a.n_seqs);
   float* sums = !d_bias ? nullptr : blocks == 1 ? d_bias : static_cast<float*>(workspace);
   const bool vec = E % 4 == 0 && aligned16(a.logits) && aligned16(d_logits);
   cudaError_t e;
