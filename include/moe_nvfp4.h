@@ -419,8 +419,8 @@ MOE_API size_t moe_block_norm_workspace_bytes(int32_t n, int32_t hidden);
  * that is, coef times the token-weighted mean over the sequences of
  * n_experts * sum_e f_e P_e with f the share of picks and P the mean
  * probability; 0 when no token takes part.  A logit of -inf gives its expert
- * probability 0, a row of nothing else adds no probability; the logits of
- * masked tokens are not looked at.  Other infinities and NaN are outside the
+ * probability 0, a row of nothing else adds no probability, probabilities
+ * below 2^-126 count as 0; the logits of masked tokens are not looked at.  Other infinities and NaN are outside the
  * contract. */
 typedef struct moe_router_args {
   int32_t n;                  /* tokens */
