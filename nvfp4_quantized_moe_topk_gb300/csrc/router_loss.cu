@@ -55,7 +55,7 @@ struct LossSpace {
   float* sums;      // [blocks + n_seqs][E]
   int32_t* picks;   // [blocks + n_seqs][E]
   int32_t* toks;    // [blocks + n_seqs]
-  float* dots;      // [n_seqs]: (1 / N_s) sum_e c P
+  float* dots;      // [n_seqs][ceil(E / 32)]: (1 / N_s) sum of c P over 32 experts
   int32_t* ticket;  // blocks of the join that are done
 };
 
@@ -68,15 +68,10 @@ LossSpace loss_space(void* ws, int32_t n, int32_t E, int32_t S) {
   p.picks = reinterpret_cast<int32_t*>(p.sums + round4(slots * E));
   p.toks = p.picks + round4(slots * E);
   p.dots = reinterpret_cast<float*>(p.toks + round4(slots));
-  p.ticket = reinterpret_cast<int32_t*>(p.dots + round4(S));
+  p.ticket = reinterpret_cast<int32_t*>(p.dots + round4((int64_t)S * ((E + 31) / 32)));
   return p;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
 __device__ __forceinline__ float warp_add(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -125,65 +120,109 @@ struct Row {
   static __device__ __forceinline__ int32_t expert(int i, int lane) {
     return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : 32 * i + lane;
   }
-  static __device__ __forceinline__ void load(const float* row, int32_t E, int lane, float (&v)[N], float fill) {
+  // Experts expert(i), expert(i + 1) of a row, i even.
+  static __device__ __forceinline__ void load4(const float* row, int32_t E, int lane, int i, F2 (&v)[2], float fill) {
+    v[0] = v[1] = f2(fill);
     if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        float4 d = make_float4(fill, fill, fill, fill);
-        if (expert(i, lane) < E) d = *reinterpret_cast<const float4*>(row + expert(i, lane));
-        v[i] = d.x;
-        v[i + 1] = d.y;
-        v[i + 2] = d.z;
-        v[i + 3] = d.w;
+      if (expert(i, lane) < E) {
+        const float4 d = *reinterpret_cast<const float4*>(row + expert(i, lane));
+        v[0] = {d.x, d.y};
+        v[1] = {d.z, d.w};
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = expert(i, lane) < E ? row[expert(i, lane)] : fill;
+      if (expert(i, lane) < E) v[0].x = row[expert(i, lane)];
+      if (expert(i + 1, lane) < E) v[0].y = row[expert(i + 1, lane)];
+      if (expert(i + 2, lane) < E) v[1].x = row[expert(i + 2, lane)];
+      if (expert(i + 3, lane) < E) v[1].y = row[expert(i + 3, lane)];
     }
   }
-  static __device__ __forceinline__ void store(float* row, int32_t E, int lane, const float (&v)[N]) {
-    if constexpr (VEC) {
+  static __device__ __forceinline__ void load(const float* row, int32_t E, int lane, F2 (&v)[N / 2], float fill) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4)
-        if (expert(i, lane) < E)
-          *reinterpret_cast<float4*>(row + expert(i, lane)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
+    for (int i = 0; i < N; i += 4) {
+      F2 d[2];
+      load4(row, E, lane, i, d, fill);
+      v[i / 2] = d[0];
+      v[i / 2 + 1] = d[1];
+    }
+  }
+  static __device__ __forceinline__ void store(float* row, int32_t E, int lane, const F2 (&v)[N / 2]) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (expert(i, lane) < E) row[expert(i, lane)] = v[i];
+    for (int i = 0; i < N; i += 4) {
+      const F2 p = v[i / 2], q = v[i / 2 + 1];
+      if constexpr (VEC) {
+        if (expert(i, lane) < E) *reinterpret_cast<float4*>(row + expert(i, lane)) = make_float4(p.x, p.y, q.x, q.y);
+      } else {
+        if (expert(i, lane) < E) row[expert(i, lane)] = p.x;
+        if (expert(i + 1, lane) < E) row[expert(i + 1, lane)] = p.y;
+        if (expert(i + 2, lane) < E) row[expert(i + 2, lane)] = q.x;
+        if (expert(i + 3, lane) < E) row[expert(i + 3, lane)] = q.y;
+      }
     }
   }
 };
 
-// A token's softmax from its logits (-inf past the last expert), in place; a
-// row without any logit above -inf gives p = 0.  s_bias: the bias in shared
-// memory, or nullptr.  The exponential is that of 2 in hardware (2 units in the
-// last place, and the rounding of (z - max) log2 e: 1e-7 to 1e-6 of p); p below
-// 2^-126 counts as 0.
-template <bool VEC, int N>
-__device__ __forceinline__ void softmax_row(const float* s_bias, int32_t E, int lane, float (&z)[N]) {
-  if (s_bias) {
-    float b[N];
-    Row<VEC, N>::load(s_bias, E, lane, b, 0.f);
+// Warp sums of M values, side by side.
+template <int M>
+__device__ __forceinline__ void warp_sums(float (&v)[M]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] += b[i];
-  }
-  float m = z[0];
+  for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, z[i]);
-  m = warp_max(m);
-  if (m == -INFINITY) m = 0.f;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    z[i] = __expf(z[i] - m);
-    sum += z[i];
-  }
-  sum = warp_add(sum);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) z[i] *= inv;
+    for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
 }
+
+// 2^x in hardware (2 units in the last place; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// From the logits of TOK tokens (-inf past the last expert) the numerators of
+// their softmax, z <- e^(z - max) in place, and the lane's part of their sums; a
+// row without any logit above -inf gives 0.  s_bias: the bias in shared memory,
+// or nullptr.  e^(z - max) is 2^(z log2 e - c) with c = max log2 e rounded: one
+// fma, and c's rounding cancels in the quotient.  p is good to 1e-6.
+template <bool VEC, int N, int TOK>
+__device__ __forceinline__ void softmax_parts(const float* s_bias, int32_t E, int lane, F2 (&z)[TOK][N / 2],
+                                              float (&sum)[TOK]) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  if (s_bias) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      F2 b[2];
+      Row<VEC, N>::load4(s_bias, E, lane, i, b, 0.f);
+#pragma unroll
+      for (int u = 0; u < TOK; ++u) {
+        z[u][i / 2] = add2(z[u][i / 2], b[0]);
+        z[u][i / 2 + 1] = add2(z[u][i / 2 + 1], b[1]);
+      }
+    }
+  }
+  float m[TOK];
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) {
+    m[u] = fmaxf(z[u][0].x, z[u][0].y);
+#pragma unroll
+    for (int i = 1; i < N / 2; ++i) m[u] = fmaxf(m[u], fmaxf(z[u][i].x, z[u][i].y));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int u = 0; u < TOK; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) {
+    const F2 c = f2(m[u] == -INFINITY ? 0.f : -m[u] * kLog2e);
+    F2 s = f2(0.f);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const F2 x = fma2(z[u][i], f2(kLog2e), c);
+      z[u][i] = {exp2_fast(x.x), exp2_fast(x.y)};
+      s = add2(s, z[u][i]);
+    }
+    sum[u] = s.x + s.y;
+  }
+}
+__device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : 0.f; }
 
 // The block's sum over its warps of a column of s_acc [kLossWarps][pitch].
 __device__ __forceinline__ float column(const float* s_acc, int32_t pitch, int32_t e) {
@@ -207,22 +246,23 @@ __device__ __forceinline__ float block_sum(float v, float* s_warp) {
 }
 
 // A warp's tokens in a block's range [lo, hi): group j holds tokens lo + warp +
-// kLossWarps (TOK j + u), u < TOK.  A group's loads do not depend on the
-// sequences, so the first group is on its way while those are looked up.
+// kLossWarps (TOK j + u), u < TOK.  A group's loads and softmax do not depend on
+// the sequences, so the first group is on its way while those are looked up.
 template <bool VEC, int N>
 struct Group {
   static constexpr int TOK = N >= 16 ? 1 : 16 / N;
+  static constexpr int kBackward = N >= 8 ? 1 : 2;  // of the backward pass
   static constexpr int kSpan = kLossWarps * TOK;
-  int32_t j;  // which group is loaded (-1: none)
-  float z[TOK][N];
+  int32_t j;            // which group this is
+  F2 z[TOK][N / 2];     // the logits, then the numerators of their softmax
+  float inv[TOK];       // 1 / the sum of those
   int32_t id[TOK];
-  bool on[TOK];  // the token takes part in the loss
+  bool on[TOK];         // the token takes part in the loss
 
   static __device__ __forceinline__ int64_t token(int32_t lo, int32_t j, int u) {
     return (int64_t)lo + (threadIdx.x >> 5) + kLossWarps * ((int64_t)TOK * j + u);
   }
-  __device__ __forceinline__ void load(const moe_router_args& a, int32_t lo, int32_t hi, int32_t group, bool logits,
-                                       bool ids) {
+  __device__ __forceinline__ void load(const moe_router_args& a, int32_t lo, int32_t hi, int32_t group) {
     const int lane = threadIdx.x & 31;
     j = group;
 #pragma unroll
@@ -230,11 +270,26 @@ struct Group {
       const int64_t t = token(lo, j, u);
       id[u] = -1;
       on[u] = t < hi;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) z[u][i] = f2(-INFINITY);
       if (t >= hi) continue;
-      if (logits) Row<VEC, N>::load(a.logits + t * a.n_experts, a.n_experts, lane, z[u], -INFINITY);
-      if (ids && lane < a.top_k) id[u] = a.topk_ids[t * a.top_k + lane];
+      Row<VEC, N>::load(a.logits + t * a.n_experts, a.n_experts, lane, z[u], -INFINITY);
+      if (lane < a.top_k) id[u] = a.topk_ids[t * a.top_k + lane];
       if (a.token_mask) on[u] = a.token_mask[t];
     }
+  }
+  // (a masked token's logits may be anything: its numerators become 0)
+  __device__ __forceinline__ void softmax(const float* s_bias, int32_t E) {
+#pragma unroll
+    for (int u = 0; u < TOK; ++u)
+      if (!on[u]) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) z[u][i] = f2(-INFINITY);
+      }
+    softmax_parts<VEC, N, TOK>(s_bias, E, threadIdx.x & 31, z, inv);
+    warp_sums(inv);
+#pragma unroll
+    for (int u = 0; u < TOK; ++u) inv[u] = inverse(inv[u]);
   }
 };
 
@@ -255,7 +310,7 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
   const int32_t lo = (int32_t)min((int64_t)blockIdx.x * per_block, (int64_t)a.n);
   const int32_t hi = (int32_t)min((int64_t)lo + per_block, (int64_t)a.n);
   Group<VEC, N> gr;
-  gr.load(a, lo, hi, 0, true, true);
+  gr.load(a, lo, hi, 0);
   if (blockIdx.x == 0 && threadIdx.x == 0 && !alone) *ws.ticket = 0;
   for (int32_t e = threadIdx.x; e < E; e += kLossThreads) {
     if (a.bias) s_bias[e] = a.bias[e];
@@ -264,6 +319,7 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
   if (threadIdx.x == 0) s_toks = 0;
   const int32_t s0 = alone ? 0 : block_first_seq(a, lo, &s_first);
   __syncthreads();
+  gr.softmax(a.bias ? s_bias : nullptr, E);
   float total_dot = 0.f;
   int32_t total = 0;
   for (int32_t s = s0; s < a.n_seqs; ++s) {
@@ -280,21 +336,22 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
       }
       continue;
     }
-    float acc[N] = {};
+    F2 acc[N / 2] = {};
     int32_t toks = 0;
     for (int32_t j = (beg - lo) / kSpan; j <= (end - 1 - lo) / kSpan; ++j) {
-      if (gr.j != j) gr.load(a, lo, hi, j, true, true);
-      gr.j = -1;
+      if (gr.j != j) {  // (a group that meets two sequences is not loaded again)
+        gr.load(a, lo, hi, j);
+        gr.softmax(a.bias ? s_bias : nullptr, E);
+      }
 #pragma unroll
       for (int u = 0; u < TOK; ++u) {
         const int64_t t = Group<VEC, N>::token(lo, j, u);
-        if (t < beg || t >= end || !gr.on[u]) continue;
-        ++toks;
-        if (gr.id[u] >= 0 && gr.id[u] < E) atomicAdd(&s_picks[gr.id[u]], 1);
-        __syncwarp();
-        softmax_row<VEC, N>(a.bias ? s_bias : nullptr, E, lane, gr.z[u]);
+        const bool in = t >= beg && t < end && gr.on[u];
+        toks += in;
+        if (in && gr.id[u] >= 0 && gr.id[u] < E) atomicAdd(&s_picks[gr.id[u]], 1);
+        const F2 inv = f2(in ? gr.inv[u] : 0.f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += gr.z[u][i];
+        for (int i = 0; i < N / 2; ++i) acc[i] = fma2(gr.z[u][i], inv, acc[i]);
       }
     }
     Row<VEC, N>::store(sm + warp * pitch, E, lane, acc);
@@ -334,77 +391,85 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
   }
 }
 
-// One block per sequence joins its slots in block order: thread (column, part
-// of the slots); the parts meet in shared memory in order.  The last block to
-// finish adds up the loss over the sequences, in their order.
-constexpr int kJoinThreads = 1024;
+// A block's sum over rows [b0, b1] of 32 columns (col: this lane's is there) of
+// a matrix of E: warp w adds rows b0 + w, + kJoinWarps, ... in order, kBatch
+// loads at a time; then lane l of warp c holds column c's sum of warp l, and a
+// butterfly adds those.  Every thread of warp c gets column c's sum.
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
+template <typename T, int kBatch>
+__device__ __forceinline__ T join_columns(const T* __restrict__ m, int32_t b0, int32_t b1, int32_t E, int32_t e, bool col,
+                                          T (*s)[33]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T v = 0;
+  for (int32_t b = b0 + warp; b <= b1; b += kBatch * kJoinWarps) {
+    T x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int32_t r = b + i * kJoinWarps;
+      x[i] = col && r <= b1 ? m[(int64_t)r * E + e] : T(0);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) v += x[i];
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  v = s[lane][warp];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// Block (s, y) joins 32 columns of the slots of sequence s; the last block to
+// finish adds up the loss over the sequences' parts, in a fixed order.
 __global__ void __launch_bounds__(kJoinThreads)
-    balance_join_kernel(const moe_router_args a, const LossSpace ws, int32_t per_block, int32_t cols,
-                        float* __restrict__ prob_sums, float* __restrict__ loss) {
-  __shared__ float s_sum[kJoinThreads];
-  __shared__ int32_t s_pick[kJoinThreads];
-  __shared__ float s_warp[kJoinThreads / 32];
-  __shared__ int32_t s_last;
-  const int E = a.n_experts, tid = threadIdx.x;
+    balance_join_kernel(const moe_router_args a, const LossSpace ws, int32_t per_block, float* __restrict__ prob_sums,
+                        float* __restrict__ loss) {
+  __shared__ float s_sum[32][33];
+  __shared__ int32_t s_pick[32][33];
+  __shared__ float s_dot[32];
+  __shared__ int32_t s_toks[32], s_last;
+  const int E = a.n_experts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t s = blockIdx.x, beg = seq_bound(a, s), end = seq_bound(a, s + 1);
   const int32_t b0 = beg / per_block, b1 = end > beg ? (end - 1) / per_block : b0 - 1;
-  const int32_t parts = kJoinThreads / cols, part = tid / cols, col = tid % cols;  // cols: a power of two
+  const int32_t e = blockIdx.y * 32 + lane, mine = blockIdx.y * 32 + warp;
   pdl_wait();
   int32_t toks = 0;
   for (int32_t b = b0 + tid; b <= b1; b += kJoinThreads) toks += ws.toks[(int64_t)b + s];
-  float dot = 0.f;
-  for (int32_t e0 = 0; e0 < E; e0 += cols) {
-    const int32_t e = e0 + col;
-    float v = 0.f;
-    int32_t c = 0;
-    if (e < E) {
-#pragma unroll 4
-      for (int32_t b = b0 + part; b <= b1; b += parts) {
-        v += ws.sums[((int64_t)b + s) * E + e];
-        c += ws.picks[((int64_t)b + s) * E + e];
-      }
+  const float v = join_columns<float, 6>(ws.sums + (int64_t)s * E, b0, b1, E, e, e < E, s_sum);
+  const int32_t c = join_columns<int32_t, 6>(ws.picks + (int64_t)s * E, b0, b1, E, e, e < E, s_pick);
+  toks = __reduce_add_sync(0xffffffffu, toks);
+  if (lane == 0) {
+    if (mine < E) {
+      prob_sums[(int64_t)s * E + mine] = v;
+      a.counts[(int64_t)s * E + mine] = c;
     }
-    s_sum[tid] = v;
-    s_pick[tid] = c;
-    __syncthreads();
-    if (part == 0 && e < E) {
-      for (int32_t i = 1; i < parts; ++i) {
-        v += s_sum[i * cols + col];
-        c += s_pick[i * cols + col];
-      }
-      prob_sums[(int64_t)s * E + e] = v;
-      a.counts[(int64_t)s * E + e] = c;
-      dot = fmaf((float)c, v, dot);
-    }
-    __syncthreads();
-  }
-  s_pick[tid] = toks;
-  dot = block_sum(dot, s_warp);
-  if (tid < 32) {
-    toks = 0;
-    for (int i = tid; i < kJoinThreads; i += 32) toks += s_pick[i];
-    toks = __reduce_add_sync(0xffffffffu, toks);
-  }
-  if (tid == 0) {
-    a.tokens[s] = toks;
-    ws.dots[s] = toks > 0 ? dot / (float)toks : 0.f;
-    __threadfence();
-    s_last = atomicAdd(ws.ticket, 1) == (int32_t)gridDim.x - 1;
+    s_dot[warp] = (float)c * v;  // (0 past the last expert)
+    s_toks[warp] = toks;
   }
   __syncthreads();
-  if (!s_last || tid >= 32) return;
-  __threadfence();
-  float v = 0.f;
-  int32_t n = 0;
-  for (int32_t i = tid; i < a.n_seqs; i += 32) {
-    v += __ldcg(ws.dots + i);
-    n += __ldcg(a.tokens + i);
+  if (warp) return;
+  const float dot = warp_add(s_dot[lane]);
+  toks = __reduce_add_sync(0xffffffffu, s_toks[lane]);
+  if (lane == 0) {
+    if (blockIdx.y == 0) a.tokens[s] = toks;
+    ws.dots[(int64_t)s * gridDim.y + blockIdx.y] = toks > 0 ? dot / (float)toks : 0.f;
+    __threadfence();
+    s_last = atomicAdd(ws.ticket, 1) == (int32_t)(gridDim.x * gridDim.y) - 1;
   }
-  v = warp_add(v);
+  __syncwarp();
+  if (!s_last) return;
+  __threadfence();
+  float sum = 0.f;
+  int32_t n = 0;
+  const int64_t parts = (int64_t)a.n_seqs * gridDim.y;
+#pragma unroll 4
+  for (int64_t i = lane; i < parts; i += 32) sum += __ldcg(ws.dots + i);
+  for (int32_t i = lane; i < a.n_seqs; i += 32) n += __ldcg(a.tokens + i);
+  sum = warp_add(sum);
   n = __reduce_add_sync(0xffffffffu, n);
-  if (tid) return;
+  if (lane) return;
   a.tokens[a.n_seqs] = n;
-  loss[0] = n > 0 ? a.coef * ((float)E / ((float)n * (float)a.top_k)) * v : 0.f;
+  loss[0] = n > 0 ? a.coef * ((float)E / ((float)n * (float)a.top_k)) * sum : 0.f;
 }
 
 // d_logits of a block's tokens and, where d_bias is wanted, their column sums
@@ -414,21 +479,21 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
     router_backward_kernel(const moe_router_args a, const float* __restrict__ w, const float* __restrict__ dw,
                            const float* __restrict__ d_loss, float* __restrict__ d_logits, float* __restrict__ sums,
                            int32_t per_block) {
-  constexpr int TOK = N >= 16 ? 1 : 8 / N;
-  extern __shared__ __align__(16) float sm[];  // [kLossWarps][pitch] the warps' rows, bias, g
+  constexpr int TOK = Group<VEC, N>::kBackward;
+  extern __shared__ __align__(16) float sm[];  // [TOK][kLossWarps][pitch] the warps' rows, bias, g
   __shared__ int32_t s_first;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.n_experts, k = a.top_k;
   const int32_t pitch = row_pitch(E);
-  float* pick = sm + warp * pitch;  // zero between tokens
-  float* s_bias = sm + kLossWarps * pitch;
+  float* pick = sm + warp * pitch;  // zero between tokens; the next row of the warp kLossWarps rows further
+  float* s_bias = sm + TOK * kLossWarps * pitch;
   float* s_g = s_bias + pitch;
   pdl_launch_dependents();
-  for (int32_t i = threadIdx.x; i < kLossWarps * pitch; i += kLossThreads) sm[i] = 0.f;
+  for (int32_t i = threadIdx.x; i < TOK * kLossWarps * pitch; i += kLossThreads) sm[i] = 0.f;
   if (a.bias)
     for (int32_t e = threadIdx.x; e < E; e += kLossThreads) s_bias[e] = a.bias[e];
   const int32_t lo = (int32_t)min((int64_t)blockIdx.x * per_block, (int64_t)a.n);
   const int32_t hi = (int32_t)min((int64_t)lo + per_block, (int64_t)a.n);
-  float acc[N] = {};
+  F2 acc[N / 2] = {};
   const int32_t total = a.counts ? a.tokens[a.n_seqs] : 0;
   const float up = d_loss ? d_loss[0] : 1.f;
   int32_t s = a.counts ? block_first_seq(a, lo, &s_first) : 0;
@@ -453,16 +518,21 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
     }
     __syncthreads();
     for (int64_t t = (int64_t)at + warp; t < end; t += kLossWarps * TOK) {
-      float d[TOK][N];
-      bool on[TOK];
+      F2 d[TOK][N / 2];
       int32_t id[TOK];
       float wj[TOK], dj[TOK];
+      bool any = false;
 #pragma unroll
       for (int u = 0; u < TOK; ++u) {
         const int64_t tu = t + u * kLossWarps;
-        const bool there = tu < end;
-        on[u] = there && lossy && (!a.token_mask || a.token_mask[tu]);
-        if (on[u]) Row<VEC, N>::load(a.logits + tu * E, E, lane, d[u], -INFINITY);
+        const bool there = tu < end, on = there && lossy && (!a.token_mask || a.token_mask[tu]);
+        any = any || on;
+        if (on) {
+          Row<VEC, N>::load(a.logits + tu * E, E, lane, d[u], -INFINITY);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) d[u][i] = f2(-INFINITY);
+        }
         id[u] = -1;
         wj[u] = dj[u] = 0.f;
         if (w && there && lane < k) {
@@ -471,48 +541,73 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
           dj[u] = dw[tu * k + lane];
         }
       }
+      // sums over the experts of e^z and g e^z, over the picks of w dw
+      float part[3][TOK] = {};
+      if (any) {
+        softmax_parts<VEC, N, TOK>(a.bias ? s_bias : nullptr, E, lane, d, part[0]);
+        F2 m[TOK] = {};
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          F2 g[2];
+          Row<VEC, N>::load4(s_g, E, lane, i, g, 0.f);
+#pragma unroll
+          for (int u = 0; u < TOK; ++u) m[u] = fma2(g[1], d[u][i / 2 + 1], fma2(g[0], d[u][i / 2], m[u]));
+        }
+#pragma unroll
+        for (int u = 0; u < TOK; ++u) part[1][u] = m[u].x + m[u].y;
+      }
+#pragma unroll
+      for (int u = 0; u < TOK; ++u) part[2][u] = wj[u] * dj[u];
+      warp_sums(reinterpret_cast<float(&)[3 * TOK]>(part));
+      if (w) {
+#pragma unroll
+        for (int u = 0; u < TOK; ++u) {
+          float* p = pick + u * kLossWarps * pitch;
+          const float dz = wj[u] * (dj[u] - part[2][u]);
+          if (id[u] >= E) id[u] = -1;
+          // each lane leaves its number at its expert: where another is found, an expert was picked twice
+          int32_t* tag = reinterpret_cast<int32_t*>(p);
+          if (id[u] >= 0) tag[id[u]] = lane;
+          __syncwarp();
+          if (__any_sync(0xffffffffu, id[u] >= 0 && tag[id[u]] != lane)) {
+            if (id[u] >= 0) p[id[u]] = 0.f;
+            __syncwarp();
+            for (int j = 0; j < k; ++j) {  // one lane after the other
+              if (lane == j && id[u] >= 0) p[id[u]] += dz;
+              __syncwarp();
+            }
+          } else if (id[u] >= 0) {
+            p[id[u]] = dz;
+          }
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int u = 0; u < TOK; ++u) {
         const int64_t tu = t + u * kLossWarps;
         if (tu >= end) break;
-        if (on[u]) {
-          float g[N];
-          softmax_row<VEC, N>(a.bias ? s_bias : nullptr, E, lane, d[u]);
-          Row<VEC, N>::load(s_g, E, lane, g, 0.f);
-          float mean = 0.f;
+        const float inv = inverse(part[0][u]);
+        const F2 mean = f2(-part[1][u] * inv);
 #pragma unroll
-          for (int i = 0; i < N; ++i) mean = fmaf(g[i], d[u][i], mean);
-          mean = warp_add(mean);
+        for (int i = 0; i < N; i += 4) {
+          F2 g[2], v[2] = {f2(0.f), f2(0.f)};
+          if (any) Row<VEC, N>::load4(s_g, E, lane, i, g, 0.f);
+          if (w) Row<VEC, N>::load4(pick + u * kLossWarps * pitch, E, lane, i, v, 0.f);
 #pragma unroll
-          for (int i = 0; i < N; ++i) d[u][i] *= g[i] - mean;
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) d[u][i] = 0.f;
-        }
-        if (w) {
-          const float dz = wj[u] * (dj[u] - warp_add(wj[u] * dj[u]));
-          const bool in = id[u] >= 0 && id[u] < E;
-          const uint32_t same = __match_any_sync(0xffffffffu, in ? id[u] : -1 - lane);
-          if (__any_sync(0xffffffffu, __popc(same) > 1)) {  // an expert picked twice: one lane after the other
-            for (int j = 0; j < k; ++j) {
-              if (lane == j && in) pick[id[u]] += dz;
-              __syncwarp();
-            }
-          } else if (in) {
-            pick[id[u]] = dz;
+          for (int q = 0; q < 2; ++q) {
+            F2& e = d[u][i / 2 + q];
+            e = any ? fma2(mul2(e, f2(inv)), add2(g[q], mean), v[q]) : v[q];
+            acc[i / 2 + q] = add2(acc[i / 2 + q], e);
           }
-          __syncwarp();
-          float v[N];
-          Row<VEC, N>::load(pick, E, lane, v, 0.f);
-#pragma unroll
-          for (int i = 0; i < N; ++i) d[u][i] += v[i];
-          __syncwarp();
-          if (in) pick[id[u]] = 0.f;
-          __syncwarp();
         }
         Row<VEC, N>::store(d_logits + tu * E, E, lane, d[u]);
+      }
+      if (w) {
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += d[u][i];
+        for (int u = 0; u < TOK; ++u)
+          if (id[u] >= 0) pick[u * kLossWarps * pitch + id[u]] = 0.f;
+        __syncwarp();
       }
     }
     at = end;
@@ -524,26 +619,15 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
   for (int32_t e = threadIdx.x; e < E; e += kLossThreads) sums[(int64_t)blockIdx.x * E + e] = column(sm, pitch, e);
 }
 
-// out[e] = sum of sums[b][e], b in order within each of 32 warps, warps in order.
-constexpr int kBiasWarps = 32;
-__global__ void __launch_bounds__(32 * kBiasWarps)
+// out[e] = sum of sums[b][e] over the blocks.
+__global__ void __launch_bounds__(kJoinThreads)
     router_bias_kernel(const float* __restrict__ sums, int32_t blocks, int32_t E, float* __restrict__ out) {
-  __shared__ float part[kBiasWarps][32];
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t e = blockIdx.x * 32 + lane;
+  const int32_t e = blockIdx.x * 32 + lane, mine = blockIdx.x * 32 + warp;
   pdl_wait();
-  float v = 0.f;
-  if (e < E) {
-#pragma unroll 8
-    for (int32_t b = warp; b < blocks; b += kBiasWarps) v += sums[(int64_t)b * E + e];
-  }
-  part[warp][lane] = v;
-  __syncthreads();
-  if (warp || e >= E) return;
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < kBiasWarps; ++i) v += part[i][lane];
-  out[e] = v;
+  const float v = join_columns<float, 10>(sums, 0, blocks - 1, E, e, e < E, s);
+  if (lane == 0 && mine < E) out[mine] = v;
 }
 
 // Tokens of a block.
@@ -551,7 +635,7 @@ int32_t loss_per_block(int32_t n, int32_t blocks) {
   return std::max(1, (int32_t)(((int64_t)n + blocks - 1) / blocks));
 }
 
-size_t loss_smem(int32_t E) { return (size_t)(kLossWarps + 2) * row_pitch(E) * sizeof(float); }
+size_t loss_smem(int32_t E, int rows) { return (size_t)(rows * kLossWarps + 2) * row_pitch(E) * sizeof(float); }
 
 template <bool VEC, int N>
 cudaError_t balance_t(const moe_router_args& a, const LossSpace& ws, float* prob_sums, float* loss, cudaStream_t s) {
@@ -559,7 +643,7 @@ cudaError_t balance_t(const moe_router_args& a, const LossSpace& ws, float* prob
   const cudaError_t e = raise_smem_limit(balance_kernel<VEC, N>, 80 * 1024, configured);
   if (e != cudaSuccess) return e;
   const int32_t blocks = balance_blocks(a.n, a.n_seqs);
-  balance_kernel<VEC, N><<<blocks, kLossThreads, loss_smem(a.n_experts), s>>>(
+  balance_kernel<VEC, N><<<blocks, kLossThreads, loss_smem(a.n_experts, 1), s>>>(
       a, ws, loss_per_block(a.n, blocks), prob_sums, loss);
   return cudaGetLastError();
 }
@@ -571,7 +655,7 @@ cudaError_t router_backward_t(const moe_router_args& a, const float* w, const fl
   const cudaError_t e = raise_smem_limit(router_backward_kernel<VEC, N>, 80 * 1024, configured);
   if (e != cudaSuccess) return e;
   const int32_t blocks = loss_blocks(a.n, a.n_seqs);
-  router_backward_kernel<VEC, N><<<blocks, kLossThreads, loss_smem(a.n_experts), s>>>(
+  router_backward_kernel<VEC, N><<<blocks, kLossThreads, loss_smem(a.n_experts, Group<VEC, N>::kBackward), s>>>(
       a, w, dw, d_loss, d_logits, sums, loss_per_block(a.n, blocks));
   return cudaGetLastError();
 }
@@ -582,7 +666,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 size_t router_loss_workspace(int32_t n, int32_t E, int32_t S) {
   const int64_t slots = loss_blocks(n, S) + (int64_t)S;
-  return (size_t)(2 * round4(slots * E) + round4(slots) + round4(S) + 4) * 4;
+  return (size_t)(2 * round4(slots * E) + round4(slots) + round4((int64_t)S * ((E + 31) / 32)) + 4) * 4;
 }
 
 cudaError_t launch_balance_loss(const moe_router_args& a, float* prob_sums, float* loss, void* workspace,
@@ -601,10 +685,8 @@ cudaError_t launch_balance_loss(const moe_router_args& a, float* prob_sums, floa
     e = vec ? balance_t<true, 32>(a, ws, prob_sums, loss, s) : balance_t<false, 32>(a, ws, prob_sums, loss, s);
   const int32_t blocks = balance_blocks(a.n, a.n_seqs);
   if (e != cudaSuccess || blocks == 1) return e;
-  int32_t cols = 32;
-  while (cols < E && cols < kJoinThreads) cols *= 2;
-  return launch_ex(balance_join_kernel, dim3((unsigned)a.n_seqs), dim3(kJoinThreads), 0, s, true, a, ws,
-                   loss_per_block(a.n, blocks), cols, prob_sums, loss);
+  return launch_ex(balance_join_kernel, dim3((unsigned)a.n_seqs, (unsigned)((E + 31) / 32)), dim3(kJoinThreads), 0, s,
+                   true, a, ws, loss_per_block(a.n, blocks), prob_sums, loss);
 }
 
 cudaError_t launch_router_backward(const moe_router_args& a, const float* w, const float* dw, const float* d_loss,
@@ -626,7 +708,7 @@ cudaError_t launch_router_backward(const moe_router_args& a, const float* w, con
     e = vec ? router_backward_t<true, 32>(a, w, dw, d_loss, d_logits, sums, s)
             : router_backward_t<false, 32>(a, w, dw, d_loss, d_logits, sums, s);
   if (e != cudaSuccess || !d_bias || blocks == 1) return e;
-  return launch_ex(router_bias_kernel, dim3((unsigned)((E + 31) / 32)), dim3(32 * kBiasWarps), 0, s, true,
+  return launch_ex(router_bias_kernel, dim3((unsigned)((E + 31) / 32)), dim3(kJoinThreads), 0, s, true,
                    (const float*)sums, blocks, E, d_bias);
 }
 
