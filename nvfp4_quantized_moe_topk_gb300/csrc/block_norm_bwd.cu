@@ -203,49 +203,35 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
   }
 }
 
-// Joins the CTAs' sums: warp w of a 32-column CTA adds CTAs w, w + warps,
-// ... and warp 0 the warps in order.
-constexpr int kColWarps = 16;
-__global__ void __launch_bounds__(32 * kColWarps)
+// Joins the CTAs' sums, 32 columns a CTA (blockIdx.y: which of the two sums).
+__global__ void __launch_bounds__(kJoinThreads)
     column_sum_kernel(const NormParams a, const NormGrads d, const float* __restrict__ part, int32_t ctas) {
-  __shared__ float sum[kColWarps][32];
+  __shared__ float sum[kJoinWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, H = a.H;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   float* d_gate = channel ? reinterpret_cast<float*>(d.d_gate.p) : nullptr;
   if (which == 0 ? !d.d_pre : !d.d_post && !d_gate) return;
-  const int32_t c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  pdl_wait();
-  if (c < H) {
-#pragma unroll 8
-    for (int32_t b = warp; b < ctas; b += kColWarps) v += part[((size_t)b * 2 + which) * H + c];
+  const int32_t c = blockIdx.x * 32 + lane, mine = blockIdx.x * 32 + warp;  // column loaded, column written
+  auto param = [&](const void* p) {
+    return a.param_dtype == MOE_DTYPE_BF16 ? bf16lo(static_cast<const uint16_t*>(p)[mine])
+                                           : static_cast<const float*>(p)[mine];
+  };
+  float g = 1.f, w = 1.f;  // (no results of the kernel before)
+  if (which && mine < H) {
+    if (channel) g = param(a.gate.p);
+    if (a.post) w = a.offset + param(a.post);
   }
-  sum[warp][lane] = v;
-  __syncthreads();
-  if (warp || c >= H) return;
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < kColWarps; ++i) v += sum[i][lane];
+  pdl_wait();
+  float v = join_columns<float, 10>(part + (size_t)which * H, 0, ctas - 1, 2 * H, c, c < H, sum);
+  if (lane || mine >= H) return;
   if (which == 0) {
-    d.d_pre[c] = v;
+    d.d_pre[mine] = v;
     return;
   }
-  auto param = [&](const void* p) {
-    return a.param_dtype == MOE_DTYPE_BF16 ? bf16lo(static_cast<const uint16_t*>(p)[c])
-                                           : static_cast<const float*>(p)[c];
-  };
   v *= a.beta;
-  float g = 1.f;
-  if (channel) {
-    g = param(a.gate.p);
-    if (a.gate_sigmoid) g = sigmoid(g);
-  }
-  if (d_gate) {
-    float o = a.post ? v * (a.offset + param(a.post)) : v;
-    if (a.gate_sigmoid) o *= g * (1.f - g);
-    d_gate[c] = o;
-  }
-  if (d.d_post) d.d_post[c] = v * g;
+  if (channel && a.gate_sigmoid) g = sigmoid(g);
+  if (d_gate) d_gate[mine] = v * w * (a.gate_sigmoid ? g * (1.f - g) : 1.f);
+  if (d.d_post) d.d_post[mine] = v * g;
 }
 
 template <typename RT, typename YT, int ITERS, int MAXT, int MODE>
@@ -310,7 +296,7 @@ cudaError_t launch_block_norm_backward(const moe_block_norm_args& args, const mo
     if (e != cudaSuccess) return e;
   }
   if (!d.d_pre && !d.d_post && !(a.gate_kind == MOE_GATE_CHANNEL && d.d_gate.p)) return cudaSuccess;
-  return launch_ex(column_sum_kernel, dim3((a.H + 31) / 32, 2), dim3(32 * kColWarps), 0, s, a.n > 0, a, d,
+  return launch_ex(column_sum_kernel, dim3((a.H + 31) / 32, 2), dim3(kJoinThreads), 0, s, a.n > 0, a, d,
                    (const float*)part, ctas);
 }
 

@@ -391,34 +391,6 @@ __global__ void __launch_bounds__(kLossThreads, N > 16 ? 1 : 2)
   }
 }
 
-// A block's sum over rows [b0, b1] of 32 columns (col: this lane's is there) of
-// a matrix of E: warp w adds rows b0 + w, + kJoinWarps, ... in order, kBatch
-// loads at a time; then lane l of warp c holds column c's sum of warp l, and a
-// butterfly adds those.  Every thread of warp c gets column c's sum.
-constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
-template <typename T, int kBatch>
-__device__ __forceinline__ T join_columns(const T* __restrict__ m, int32_t b0, int32_t b1, int32_t E, int32_t e, bool col,
-                                          T (*s)[33]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T v = 0;
-  for (int32_t b = b0 + warp; b <= b1; b += kBatch * kJoinWarps) {
-    T x[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int32_t r = b + i * kJoinWarps;
-      x[i] = col && r <= b1 ? m[(int64_t)r * E + e] : T(0);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) v += x[i];
-  }
-  s[warp][lane] = v;
-  __syncthreads();
-  v = s[lane][warp];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
 // Block (s, y) joins 32 columns of the slots of sequence s; the last block to
 // finish adds up the loss over the sequences' parts, in a fixed order.
 __global__ void __launch_bounds__(kJoinThreads)
