@@ -103,10 +103,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int32_t rank = t.rank, ranks16 = (rank + 15) / 16;
-  // the halves' rings; the halves' out blocks; v [terms][RB] operand tiles
-  const uint32_t sm_u32 = smem_u32(sm), ring = half * ring_bytes;
-  char* obuf = sm + 2 * ring_bytes + half * kOperandTile;
-  const uint32_t v_at = 2 * ring_bytes + 2 * kOperandTile;
+  // First product: each half's ring is half of the space.  Then: the first half's ring, the halves' out blocks, v
+  // [terms][RB] operand tiles, the second half's ring (which each half may fill when its own part of the first
+  // product is done).
+  const uint32_t sm_u32 = smem_u32(sm), space = 2 * ring_bytes + (2 + terms * RB) * kOperandTile;
+  const uint32_t ring1_bytes = space / 2 / 1024 * 1024, ring1 = half * ring1_bytes;
+  const uint32_t ring = half * (space - ring_bytes), out_at = ring_bytes, v_at = ring_bytes + 2 * kOperandTile;
+  char* obuf = sm + out_at + half * kOperandTile;
   const uint32_t quadrant = (uint32_t)(32 * (warp & 3)) << 16;  // this warp's lanes of tensor memory
   const int m = 32 * (warp & 3) + lane;                         // its thread's token
   const int p8 = htid & 7, r8 = htid >> 3;  // copies of 128-byte rows: piece, first row (the others 32, 64, 96 further)
@@ -182,10 +185,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const char* Ar = reinterpret_cast<const char*>(a.a) +
                      ((int64_t)t.adapter * a.max_rank + r8) * (int64_t)row_bytes + 16 * p8;
     const uint32_t step = mma_step1(ranks16);
-    const int stages = (int)min(kMmaMaxStages, ring_bytes / step);
+    const int stages = (int)min(kMmaMaxStages, ring1_bytes / step);
     auto fetch = [&](int32_t c, int stage) {
       if (c < chunks) {
-        const uint32_t off = (uint32_t)c * 128, at = ring + stage * step + to8;
+        const uint32_t off = (uint32_t)c * 128, at = ring1 + stage * step + to8;
         if (off + 16 * p8 < row_bytes) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) ring16(sm_u32 + at + i * 32 * 128, xr[i] + off);
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       if (dead) break;
       if (hwarp == 0) {
         if (elect_one()) {
-          const uint32_t x_at = sm_u32 + ring + stage * step, a_at = x_at + kOperandTile;
+          const uint32_t x_at = sm_u32 + ring1 + stage * step, a_at = x_at + kOperandTile;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma_bf16(tmem + half * 128, smem_desc_k128(x_at + 32 * k), smem_desc_k128(a_at + 32 * k), idesc,
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       for (int i = 0; i < 16; ++i) s[b][i] = __uint_as_float(d0[i]) + __uint_as_float(d1[i]);
     }
     if (C > 1) {  // [4 ranks][128 tokens], added in the order of the CTAs, the same in each of them
-      float* meet = reinterpret_cast<float*>(ring_meets ? sm : sm + 2 * ring_bytes) + m * 4;
+      float* meet = reinterpret_cast<float*>(sm + (ring_meets ? 0 : out_at)) + m * 4;
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
