@@ -242,11 +242,16 @@ __device__ __forceinline__ void cta_sums3(float& a, float& b, float& c, float* r
   b = __shfl_sync(0xffffffffu, v, 16);
 }
 
-inline int norm_sms() {
+inline int norm_sms() {  // (asked for once a device)
+  static std::atomic<int> held[kMaxDevices];
   int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+  sms = held[dev].load(std::memory_order_relaxed);
+  if (sms) return sms;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 0 ? sms : 1;
+  sms = std::max(sms, 1);
+  held[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 // Shape of a persistent launch: CTAs of about `sm_threads` threads an SM, and

@@ -17,9 +17,9 @@
 // row's vectors are read twice from the ring, before and after the reduction,
 // which is cheaper than holding them in registers beside the channels' sums.
 // Each CTA writes its sums, and column_sum_kernel joins them in a fixed order.
-// Measured on a GB300: 4314 rows of 2688, all bf16, gate per channel: 32 us with
-// the join, 4.4 TB/s (65 % of a copy's rate; 40 us with one CTA an SM).  61 rows of
-// 1000: 5.5 us, two launches' latency.
+// Measured on a GB300: 4314 rows of 2688, all bf16, gate per channel: 30.6 us with
+// the join, 4.6 TB/s (67 % of a copy's rate; 40 us with one CTA an SM).  61 rows of
+// 1000: 4.9 us, two launches' latency.
 #include "block_norm.cuh"
 
 namespace moe {
@@ -259,7 +259,7 @@ cudaError_t norm_backward_i(const NormParams& a, const NormGrads& d, float* part
 template <typename RT, typename YT>
 cudaError_t norm_backward_t(const NormParams& a, const NormGrads& d, float* part, int* ctas, cudaStream_t s) {
   if (norm_iters(a.H) == 2) return norm_backward_i<RT, YT, 2, 512>(a, d, part, ctas, s);
-  // rows of up to 384 threads: two CTAs an SM, at 85 registers a thread (2688 channels: 32 us, with one of 128 registers
+  // rows of up to 384 threads: two CTAs an SM, at 85 registers a thread (2688 channels: 31 us, with one of 128 registers
   // 40); wider rows fill an SM alone
   if (norm_threads(a.H) <= 384) return norm_backward_i<RT, YT, 1, 384>(a, d, part, ctas, s);
   return norm_backward_i<RT, YT, 1, 512>(a, d, part, ctas, s);

@@ -175,11 +175,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 // there the adapter's matrices are read less often, which counts the more the
 // larger the rank, but fewer CTAs share a small batch.  Tiles of 16 against
 // 128, us on a GB300:
-//   4096 to 4096, rank 16: 1024 tokens 16.1 / 22.2, 1536 27.4 / 25.7, 3000 37.8 / 29.7
-//   4096 to 1024, rank 32: 1024 13.0 / 19.9, 1536 16.0 / 20.1, 2048 21.4 / 20.0, 3000 29.5 / 21.5
-//   4096 to 4096, rank 64: 300 23.7 / 23.8, 640 34.4 / 32.4, 1024 51.0 / 33.9, 2048 59.6 / 36.4
-//   rank 128: 512 40.2, 768 64.2 / 44.4, 1024 77.8 / 46.7; against 64 (lora_rows.cu): 512 40.2 / 46.3, 768 64.2 / 52.1
-constexpr int32_t kSmallTokens = 1280, kSmallTokensWide = 512;  // max_rank up to 32, above
+//   4096 to 4096, rank 16: 1024 tokens 15.6 / 21.0, 2048 23.3 / 26.8, 3000 37.3 / 29.8
+//   4096 to 1024, rank 32: 1024 12.6 / 19.5, 2048 16.6 / 19.5, 3000 23.9 / 21.3
+//   4096 to 4096, rank 64: 300 23.3 / 30.3, 640 33.9 / 31.4, 1536 50.9 / 33.8
+//   the same, rank 128: 300 31.8 / 41.0, 512 39.9 / 41.6, 768 52.0 / 43.3, 2048 82.6 / 45.4
+constexpr int32_t kSmallTokens = 2048, kSmallTokensWide = 512;  // max_rank up to 32, above
 static_assert(kSmallTokens >= kFusedTokens && kSmallTokensWide >= kFusedTokens, "the other kernels need the plan");
 inline int32_t small_tokens(int32_t max_rank) { return max_rank <= 32 ? kSmallTokens : kSmallTokensWide; }
 

@@ -10,11 +10,11 @@
 // one after the other; so two halves of the CTA (8 warps each) take alternate
 // steps with barriers, rings and accumulators of their own, and one half's
 // copies run beside the other's waits (16384 tokens, 4096 to 2048, rank 64,
-// bf16: 92 us with one half of 512 threads, 77 with two, of which the bytes are
-// 40; 3.6 TB/s).  Where there are fewer tiles than SMs, the CTAs of a cluster
+// bf16: 92 us with one half of 512 threads, 75 with two, of which the bytes are
+// 40; 3.7 TB/s).  Where there are fewer tiles than SMs, the CTAs of a cluster
 // take turns with the steps of both products and add their D1 through each
 // other's shared memory (4096 tokens, 4096 to 4096, rank 64: 94 us with a CTA a
-// tile, 39 with four).
+// tile, 38 with four).
 //
 //   first product:  D1[128 tokens][ranks] += x chunk . A chunk^T, 64 columns of
 //     in_features a step (the tokens' rows are gathered: 8 lanes copy 128 bytes

@@ -11,7 +11,7 @@
 // own tokens' 16-byte pieces of x (or y) go through thread-private slots of the
 // same ring steps.  Every 16 tokens reread A and B from shared memory, which at
 // these ranks is what bounds it: 4096 tokens, 4096 to 4096, rank 128 99 us with
-// a bf16 out, 16384 349 (lora_mma.cu: 50 and 135; the bytes are 15 and 60).
+// a bf16 out, 16384 349 (lora_mma.cu: 47 and 121; the bytes are 15 and 60).
 //
 // Shared rows of A, B and v are read as 16 bytes by lane (row g, piece q); rows
 // whose pitch is a multiple of 128 bytes are stored with pieces 0-3 and 4-7

@@ -16,10 +16,11 @@
 // every run.  Batches that one block holds need no join: one launch.
 //
 // Measured on a GB300: loss of 16384 tokens, 128 experts, 7 sequences, two
-// launches 13.8 us (what it reads takes 1.3 at a copy's rate: a warp's chain of
-// maximum, exponentials, sum, and then the join; 4.2 to 4.5 us for 33 tokens in one
-// launch); backward of 16384 tokens, 512 experts 22.4 us, 3 TB/s, of 4314 tokens,
-// 128 experts 8.5.
+// launches 11.7 us (what it reads takes 1.3 at a copy's rate; latency: two
+// launches, sequence lookup, a group's loads and softmax, the join; 4.2 us for 33
+// tokens in one launch); backward of 16384 tokens, 512 experts 20.3 us, of which 11
+// at 5.9 TB/s and the rest before the first logits and after the last; of 4314
+// tokens, 128 experts 7.9.
 //
 // The top-k weights' gradient touches k of a row's experts: each warp adds it
 // to its row through its own row of shared memory, zero but for those.
@@ -36,19 +37,20 @@ namespace {
 constexpr int kLossThreads = 512, kLossWarps = kLossThreads / 32;
 
 // Blocks of a call: 16 tokens a block, one a warp, or fewer where there are
-// more sequences than that (each costs a walk of the block some 1.5 us), up to
-// two blocks an SM (with four, 16384 tokens of 64 experts take 17.6 instead of
-// 13.7 us in the loss, 27 instead of 23 in the backward pass).  The loss of one
-// block needs no join, so there one block takes up to 96 tokens of up to 4
-// sequences.  One block against several, measured on a GB300, loss with 64
-// experts: 64 tokens 4.6 / 7.1 us, 96 6.0 / 7.2, 128 6.5 / 7.2, with 256 experts
-// 128 7.5 / 7.4; 64 tokens of 4 sequences 9.9 / 10.8, of 16 30 / 11.4.  (Backward,
-// whose join only adds d_bias up: 32 tokens 5.0 / 4.8, 64 7.3 / 4.8.)
+// more sequences than that (each costs a walk of the block about a microsecond),
+// up to two blocks an SM (with four, 16384 tokens take 15.5 instead of 11.6 us in
+// the loss, 24 instead of 20 in the backward pass).  The loss of one block needs
+// no join, so there one block takes up to 128 tokens of up to 4 sequences.  One
+// block against several, measured on a GB300, us: 64 tokens, 64 experts 4.2 / 7.9,
+// 128 tokens 5.6 / 7.9, 256 8.5 / 8.1; 128 tokens, 256 experts 6.7 / 7.9, 256 10.8
+// / 8.0; 128 experts, 128 tokens of 4 sequences 9.2 / 9.8, of 16 22 / 11.5.
+// (Backward, whose join only adds d_bias up, one block: 32 tokens 5.0 / 4.8, 64
+// 7.3 / 4.8.)
 int32_t loss_blocks(int32_t n, int32_t S) {
   const int32_t by_tokens = (int32_t)(((int64_t)n + kLossWarps - 1) / kLossWarps);
   return std::max(1, std::min(kRouterLossBlocks, std::max(by_tokens, std::min(n, S))));
 }
-int32_t balance_blocks(int32_t n, int32_t S) { return n <= 6 * kLossWarps && S <= 4 ? 1 : loss_blocks(n, S); }
+int32_t balance_blocks(int32_t n, int32_t S) { return n <= 8 * kLossWarps && S <= 4 ? 1 : loss_blocks(n, S); }
 
 // The workspace of both calls.
 struct LossSpace {
