@@ -9,7 +9,7 @@
 // (lora_rows.cu); here tiles are 16 tokens.  Both products are bf16 warp matrix
 // instructions with tokens as rows.  What bounds a call of few tokens is
 // latency: finding the tile, two chains of copies and a meeting of the cluster
-// between them (32 tokens, 2688 to 1856, rank 16: 7.4 us on a GB300, of which
+// between them (32 tokens, 2688 to 1856, ranks to 32: 6.7 us on a GB300, of which
 // the bytes are 0.5), so what counts is how many bytes are in flight at once.
 // Every thread
 // copies the 16-byte pieces of the operands that its own fragments are made of
@@ -21,7 +21,9 @@
 //
 //   first product:  the warps (and the cluster's CTAs) split in_features in
 //     windows of 32; their partial sums meet in shared memory (and in the
-//     cluster's shared memories), added in a fixed order.
+//     cluster's shared memories, each store counted on the receiver's
+//     mbarrier: half a microsecond less than a barrier of the cluster after
+//     them), added in a fixed order.
 //   second product: the warps split out_features in blocks of 32 columns.  The
 //     columns of a block are dealt to the four 8-column instructions so that
 //     a lane ends up with 8 neighbouring columns of a token (two runs of 4
@@ -183,6 +185,9 @@ constexpr int32_t kSmallTokens = 2048, kSmallTokensWide = 512;  // max_rank up t
 static_assert(kSmallTokens >= kFusedTokens && kSmallTokensWide >= kFusedTokens, "the other kernels need the plan");
 inline int32_t small_tokens(int32_t max_rank) { return max_rank <= 32 ? kSmallTokens : kSmallTokensWide; }
 
+// Set where a bounded wait ran out.
+__device__ int32_t g_lora_small_flags;
+
 // Tiles of 16 tokens; NT groups of 8 ranks a pass of the first product.
 template <int NT>
 __global__ void __launch_bounds__(kLoraThreads, 2)
@@ -191,8 +196,13 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   constexpr int RPASS = 8 * NT, RP = RPASS + 8;  // ranks of a pass; row pitch of the partial sums
   extern __shared__ __align__(16) char sm[];
   __shared__ int32_t row[MT];
+  __shared__ __align__(8) uint64_t met;  // the CTAs' sums of a pass have arrived
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const uint32_t C = cluster_size(), cr = cluster_rank();
+  if (C > 1 && tid == 0) {
+    mbar_init(&met, 1);
+    fence_mbar_init();
+  }
   Tile t;
   // ring; the warps' sums [KG][MT][RP]; in a cluster the CTAs' sums [C][MT][RP]; v [terms][MT][VP] bf16
   float* part = reinterpret_cast<float*>(sm + ring_bytes);
@@ -202,10 +212,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   if (!(fused ? ranked_tile<MT>(a, tile, row, reinterpret_cast<int32_t*>(part), t)
               : planned_tile<MT>(a, plan, tile, row, t)))
     return;
-  if (C > 1) cluster_arrive();  // (waited for before the first store into a peer: it has started by then)
+  if (C > 1) cluster_arrive();  // (waited for before the first store into a peer: its mbarrier is ready by then)
   const uint32_t slot = tid * 16, sm_u32 = smem_u32(sm);  // offsets in sm; cp.async takes addresses
-  const int32_t rank = t.rank;
-  const int32_t R32 = (rank + 31) & ~31;
   const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;  // pitch of v: rows 64 bytes apart mod 128
   // places past the tile's count take its first token: their rows of the products are never looked at
   int32_t tok[2];
@@ -215,6 +223,42 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
     tok[h] = row[h * 8 + g];
     at_tok[h] = tok[h] >= 0 ? tok[h] : row[0];
   }
+
+  // The first product's steps: a window of 32 columns of x and A.  A warp takes pairs of windows, 128 bytes of a row:
+  // first the even, then the odd one.
+  const uint32_t row_bytes = (uint32_t)a.in_features * 2, lane_a = g * row_bytes + 16 * q;
+  const uint32_t pair0 = ((uint32_t)cr * KG + warp) * 128, jump = (uint32_t)C * KG * 128 - 64;
+  const char* xr[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    xr[h] = static_cast<const char*>(a.x.data) + 16 * q + at_tok[h] * (a.x.stride ? a.x.stride : a.in_features) * 2;
+  const char* A = reinterpret_cast<const char*>(a.a) + (int64_t)t.adapter * a.max_rank * (int64_t)row_bytes;
+  uint32_t fetch_off = pair0;  // byte offset in a row of the window to fetch next
+  bool fetch_odd = false;
+  auto fetch = [&](int stage, uint32_t step, int32_t nt) {
+    if (fetch_off < row_bytes && fetch_off + 16 * q < row_bytes) {  // else past the row's end, and read as 0
+      const uint32_t at = slot + stage * step;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ring16(sm_u32 + at + h * kSlotVec, xr[h] + fetch_off);
+      // rows from the rank on are in the bank and reach only entries of v that are set to zero
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (j >= nt) break;
+        ring16(sm_u32 + at + (2 + j) * kSlotVec, A + ((uint64_t)(8 * j) * row_bytes + fetch_off) + lane_a);
+      }
+    }
+    fetch_off += fetch_odd ? jump : 64;
+    fetch_odd = !fetch_odd;
+    ring_commit();
+  };
+  // (the first steps are on their way before the adapter's rank is here: as many rows as any has)
+  int32_t nt = min(NT, a.max_rank / 8);
+  uint32_t step = (2 + nt) * kSlotVec;
+  int stages = ring_stages(ring_bytes, step);
+  if (t.adapter < a.n_adapters)
+    for (int s = 0; s + 1 < stages; ++s) fetch(s, step, nt);
+  const int32_t rank = t.rank;
+  const int32_t R32 = (rank + 31) & ~31;
 
   // The second product's steps: a block of 32 columns of y and B.  A lane's columns: 4 at c0 and 4 at c0 + next.
   const bool quads = a.y_dtype == MOE_DTYPE_F32 || a.out_dtype == MOE_DTYPE_F32;
@@ -275,48 +319,27 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
     for (int s = 0; s + 1 < y_stages; ++s) fetch_y(b0 + s * bstep, s);
   };
 
-  if (rank == 0) fetch_first_y();
+  if (rank == 0) {
+    ring_wait(0);  // (what was fetched for the first product)
+    fetch_first_y();
+  }
   if (rank > 0) {
-    const uint32_t row_bytes = (uint32_t)a.in_features * 2;
-    const char* xr[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      xr[h] = static_cast<const char*>(a.x.data) + 16 * q + at_tok[h] * (a.x.stride ? a.x.stride : a.in_features) * 2;
-    // a warp takes pairs of windows, 128 bytes of a row: first the even, then the odd one
-    const uint32_t pair0 = ((uint32_t)cr * KG + warp) * 128, jump = (uint32_t)C * KG * 128 - 64;
     for (int32_t r0 = 0; r0 < rank; r0 += RPASS) {
-      const int32_t nt = min(NT, (rank - r0 + 7) / 8);
-      const uint32_t step = (2 + nt) * kSlotVec;
-      const int stages = ring_stages(ring_bytes, step);
-      const char* A = reinterpret_cast<const char*>(a.a) +
-                      ((int64_t)t.adapter * a.max_rank + r0) * (int64_t)row_bytes;
-      const uint32_t lane_a = g * row_bytes + 16 * q;
-      uint32_t fetch_off = pair0;  // byte offset in a row of the window to fetch next
-      bool fetch_odd = false;
-      auto fetch = [&](int stage) {
-        if (fetch_off < row_bytes && fetch_off + 16 * q < row_bytes) {  // else past the row's end, and read as 0
-          const uint32_t at = slot + stage * step;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) ring16(sm_u32 + at + h * kSlotVec, xr[h] + fetch_off);
-          // rows between the rank and the next multiple of 8 are in the bank and reach only entries of v that are
-          // set to zero
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if (j >= nt) break;
-            ring16(sm_u32 + at + (2 + j) * kSlotVec, A + ((uint64_t)(8 * j) * row_bytes + fetch_off) + lane_a);
-          }
-        }
-        fetch_off += fetch_odd ? jump : 64;
-        fetch_odd = !fetch_odd;
-        ring_commit();
-      };
-      for (int s = 0; s + 1 < stages; ++s) fetch(s);
+      nt = min(NT, (rank - r0 + 7) / 8);
+      if (r0 > 0) {
+        A += (uint64_t)RPASS * row_bytes;
+        step = (2 + nt) * kSlotVec;
+        stages = ring_stages(ring_bytes, step);
+        fetch_off = pair0;
+        fetch_odd = false;
+        for (int s = 0; s + 1 < stages; ++s) fetch(s, step, nt);
+      }
       float acc[NT][4] = {};
       int stage = 0;
       bool odd = false;
       for (uint32_t off = pair0; off < row_bytes;
            off += odd ? jump : 64, odd = !odd, stage = stage + 1 == stages ? 0 : stage + 1) {
-        fetch(stage == 0 ? stages - 1 : stage - 1);
+        fetch(stage == 0 ? stages - 1 : stage - 1, step, nt);
         ring_wait(stages - 1);
         __syncwarp();
         const uint32_t at = slot + stage * step;
@@ -345,35 +368,38 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           *reinterpret_cast<float2*>(part + (warp * MT + h * 8 + g) * RP + 8 * j + 2 * q) =
               make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
       __syncthreads();
-      auto own_sum = [&](int m, int r) {
-        float s = 0.f;
+      // a thread: M neighbouring ranks of a token
+      constexpr int M = MT * RPASS / kLoraThreads;
+      const int m = tid * M / RPASS, r = tid * M % RPASS;
+      float sum[M] = {};
 #pragma unroll
-        for (int k = 0; k < KG; ++k) s += part[(k * MT + m) * RP + r];
-        return s;
-      };
+      for (int k = 0; k < KG; ++k)
+#pragma unroll
+        for (int i = 0; i < M; ++i) sum[i] += part[(k * MT + m) * RP + r + i];
       if (C > 1) {
-        // every CTA of the cluster gets all CTAs' sums (and has read the last pass's)
+        // Every CTA of the cluster gets all CTAs' sums, of the tokens and ranks that there are; each counts the bytes
+        // that arrive (and the peers have read the last pass's).
+        const int32_t ranks = min(RPASS, (rank - r0 + M - 1) / M * M);
+        const bool used = m < t.count && r < ranks;
+        if (tid == 0) mbar_arrive_expect_tx(&met, C * t.count * ranks * 4);
         cluster_wait();
-        for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
-          const int m = i / RPASS, r = i % RPASS;
-          const float s = own_sum(m, r);
-          for (uint32_t k = 0; k < C; ++k) push_float(recv + (cr * MT + m) * RP + r, k, s);
-        }
-        cluster_sync();
+        if (used)
+          for (uint32_t k = 0; k < C; ++k) push_floats<M>(recv + (cr * MT + m) * RP + r, k, sum, &met);
+        mbar_wait(&met, (uint32_t)(r0 / RPASS) & 1, &g_lora_small_flags);
+#pragma unroll
+        for (int i = 0; i < M; ++i) sum[i] = 0.f;
+        if (used)
+          for (uint32_t k = 0; k < C; ++k)
+#pragma unroll
+            for (int i = 0; i < M; ++i) sum[i] += recv[(k * MT + m) * RP + r + i];
       }
-      for (int i = tid; i < MT * RPASS; i += kLoraThreads) {
-        const int m = i / RPASS, r = i % RPASS;
-        float s = 0.f;
-        if (C > 1) {
-          for (uint32_t k = 0; k < C; ++k) s += recv[(k * MT + m) * RP + r];
-        } else {
-          s = own_sum(m, r);
-        }
-        s = r0 + r < rank ? s * t.scale : 0.f;
-        if (r0 + r < R32)
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        float s = r0 + r + i < rank ? sum[i] * t.scale : 0.f;
+        if (r0 + r + i < R32)
           for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
             const uint16_t b = f2bf_rn(s);
-            v[(k * MT + m) * VP + r0 + r] = b;
+            v[(k * MT + m) * VP + r0 + r + i] = b;
             s -= bf16lo(b);
           }
       }
@@ -483,6 +509,13 @@ cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, i
 
 }  // namespace
 
+cudaError_t lora_small_flags(int32_t* flags) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_lora_small_flags, sizeof(int32_t));
+  const int32_t zero = 0;
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_lora_small_flags, &zero, sizeof(int32_t));
+  return e;
+}
+
 size_t lora_workspace(int32_t n, int32_t n_adapters) {
   const int64_t L = n_adapters;
   if (n <= kFusedTokens) return 0;
@@ -513,7 +546,7 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
   if (!small) return launch_lora_rows(a, p, tiles, expected, s);
   // Up to 400 CTAs, of which two share an SM (`tiles` is a bound, so some have nothing to do).  With 608 a call of 768
   // tokens takes 20 us instead of 15, with 304 one of 1024 18 instead of 15.5; clusters of 4 or 2 for a single token
-  // 7.1 and 9.6 us instead of 6.0.
+  // take 1.1 and 3.6 us more.
   int32_t cluster = 1;
   while (cluster < 8 && tiles * cluster * 2 <= 400) cluster *= 2;
   if (a.max_rank <= 16) return lora_launch<2>(a, p, fused, tiles, cluster, s);

@@ -63,11 +63,26 @@ __device__ __forceinline__ void cluster_sync() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Stores v at this CTA's shared address `p`, in CTA `rank` of the cluster.
-__device__ __forceinline__ void push_float(float* p, uint32_t rank, float v) {
-  uint32_t addr;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Stores M (1, 2 or 4) floats at this CTA's shared address `p`, in CTA `rank` of
+// the cluster, and counts their bytes on that CTA's mbarrier `bar`.
+template <int M>
+__device__ __forceinline__ void push_floats(const float* p, uint32_t rank, const float (&v)[M], uint64_t* bar) {
+  uint32_t to, on;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(p)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(on) : "r"(smem_u32(bar)), "r"(rank));
+  if constexpr (M == 1)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
+                 "r"(__float_as_uint(v[0])), "r"(on)
+                 : "memory");
+  else if constexpr (M == 2)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(on)
+                 : "memory");
+  else
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(on)
+                 : "memory");
 }
 // Two floats at this CTA's shared address `p`, in CTA `rank` of the cluster.
 __device__ __forceinline__ float2 peer_float2(const float* p, uint32_t rank) {
@@ -141,18 +156,12 @@ template <int MT>
 __device__ __forceinline__ bool ranked_tile(const moe_lora_args& a, int32_t tile, int32_t* row, int32_t* scratch,
                                             Tile& t) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, L = a.n_adapters, n = a.n;
-  __shared__ int32_t found[4];
+  __shared__ int32_t found[2];
   int32_t* leaders = scratch + kFusedTokens;  // per warp
   const int32_t mine = tid < n ? bucket_of(a.adapter_ids[tid], L) : -1;
   if (tid == 0) found[0] = -1;
   if (tid < MT) row[tid] = -1;
   scratch[tid] = mine;
-  int32_t my_rank = 0;
-  float my_scale = 0.f;
-  if (mine >= 0) {  // (on their way while the ranks are found)
-    my_rank = adapter_rank(a, mine);
-    my_scale = adapter_scale(a, mine);
-  }
   int32_t rank = __popc(__match_any_sync(0xffffffffu, mine) & ((1u << lane) - 1u));
   if (n > 32) {
     __syncthreads();
@@ -174,14 +183,12 @@ __device__ __forceinline__ bool ranked_tile(const moe_lora_args& a, int32_t tile
   if (leads && at == tile) {
     found[0] = mine;
     found[1] = rank / MT;
-    found[2] = my_rank;
-    found[3] = __float_as_int(my_scale);
   }
   __syncthreads();
   t.adapter = found[0];
   if (t.adapter < 0) return false;
-  t.rank = found[2];
-  t.scale = __int_as_float(found[3]);
+  t.rank = adapter_rank(a, t.adapter);
+  t.scale = adapter_scale(a, t.adapter);
   const bool in = mine == t.adapter && rank / MT == found[1];
   if (in) row[rank % MT] = tid;
   t.count = __syncthreads_count(in);
@@ -280,6 +287,9 @@ cudaError_t lora_cluster(void (*kernel)(KArgs...), int threads, size_t smem, int
 constexpr int kMmaTokens = 128;
 bool lora_mma_fits(const moe_lora_args& a);
 cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s);
+
+// Reads and clears the flags of lora.cu's bounded waits.
+cudaError_t lora_small_flags(int32_t* flags);
 
 // lora_rows.cu: at most `tiles` tiles of kRowsTile tokens.
 constexpr int kRowsTile = 64;

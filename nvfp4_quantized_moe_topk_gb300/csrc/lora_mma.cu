@@ -446,9 +446,12 @@ cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t t
 
 cudaError_t lora_device_flags(int32_t* flags) {
   cudaError_t e = cudaDeviceSynchronize();
-  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(flags, g_lora_flags, sizeof(int32_t));
+  int32_t mine = 0;
+  if (e == cudaSuccess) e = lora_small_flags(flags);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&mine, g_lora_flags, sizeof(int32_t));
   const int32_t zero = 0;
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_lora_flags, &zero, sizeof(int32_t));
+  if (e == cudaSuccess) *flags |= mine;
   return e;
 }
 
