@@ -97,14 +97,13 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 // A block's sum over rows [b0, b1] of 32 columns (col: this lane's is there) of
 // a matrix of E: warp w adds rows b0 + w, + kJoinWarps, ... in order, kBatch
 // loads at a time; then lane l of warp c holds column c's sum of warp l, and a
-// butterfly adds those.  Every thread of warp c gets column c's sum.
+// butterfly adds those.  join_part is the warps' own part, join_parts (after
+// s[warp][lane] = that and a barrier) gives every thread of warp c column c's sum.
 constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
-template <typename T, int kBatch>
-__device__ __forceinline__ T join_columns(const T* __restrict__ m, int32_t b0, int32_t b1, int32_t E, int32_t e, bool col,
-                                          T (*s)[33]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <int kBatch, typename T>
+__device__ __forceinline__ T join_part(const T* __restrict__ m, int32_t b0, int32_t b1, int32_t E, int32_t e, bool col) {
   T v = 0;
-  for (int32_t b = b0 + warp; b <= b1; b += kBatch * kJoinWarps) {
+  for (int32_t b = b0 + (int32_t)(threadIdx.x >> 5); b <= b1; b += kBatch * kJoinWarps) {
     T x[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -114,9 +113,11 @@ __device__ __forceinline__ T join_columns(const T* __restrict__ m, int32_t b0, i
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) v += x[i];
   }
-  s[warp][lane] = v;
-  __syncthreads();
-  v = s[lane][warp];
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T join_parts(const T (*s)[33]) {
+  T v = s[threadIdx.x & 31][threadIdx.x >> 5];
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;

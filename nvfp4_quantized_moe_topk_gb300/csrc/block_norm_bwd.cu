@@ -222,7 +222,9 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (a.post) w = a.offset + param(a.post);
   }
   pdl_wait();
-  float v = join_columns<float, 10>(part + (size_t)which * H, 0, ctas - 1, 2 * H, c, c < H, sum);
+  sum[warp][lane] = join_part<10>(part + (size_t)which * H, 0, ctas - 1, 2 * H, c, c < H);
+  __syncthreads();
+  float v = join_parts(sum);
   if (lane || mine >= H) return;
   if (which == 0) {
     d.d_pre[mine] = v;

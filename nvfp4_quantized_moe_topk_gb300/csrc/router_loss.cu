@@ -409,8 +409,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   pdl_wait();
   int32_t toks = 0;
   for (int32_t b = b0 + tid; b <= b1; b += kJoinThreads) toks += ws.toks[(int64_t)b + s];
-  const float v = join_columns<float, 6>(ws.sums + (int64_t)s * E, b0, b1, E, e, e < E, s_sum);
-  const int32_t c = join_columns<int32_t, 6>(ws.picks + (int64_t)s * E, b0, b1, E, e, e < E, s_pick);
+  const float part = join_part<6>(ws.sums + (int64_t)s * E, b0, b1, E, e, e < E);
+  const int32_t picks = join_part<6>(ws.picks + (int64_t)s * E, b0, b1, E, e, e < E);
+  s_sum[warp][lane] = part;
+  s_pick[warp][lane] = picks;
+  __syncthreads();
+  const float v = join_parts(s_sum);
+  const int32_t c = join_parts(s_pick);
   toks = __reduce_add_sync(0xffffffffu, toks);
   if (lane == 0) {
     if (mine < E) {
@@ -600,7 +605,9 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t e = blockIdx.x * 32 + lane, mine = blockIdx.x * 32 + warp;
   pdl_wait();
-  const float v = join_columns<float, 10>(sums, 0, blocks - 1, E, e, e < E, s);
+  s[warp][lane] = join_part<10>(sums, 0, blocks - 1, E, e, e < E);
+  __syncthreads();
+  const float v = join_parts(s);
   if (lane == 0 && mine < E) out[mine] = v;
 }
 
