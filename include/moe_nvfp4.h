@@ -474,8 +474,8 @@ MOE_API size_t moe_router_workspace_bytes(int32_t n, int32_t n_experts, int32_t 
  * result is rounded once. */
 typedef struct moe_lora_args {
   int32_t n;            /* tokens */
-  int32_t in_features;  /* multiple of 8 */
-  int32_t out_features; /* multiple of 8 */
+  int32_t in_features;  /* multiple of 8, at most 2^24 */
+  int32_t out_features; /* multiple of 8, at most 2^24 */
   int32_t n_adapters;   /* 1..1024 */
   int32_t max_rank;     /* multiple of 8, at most 128 */
   int32_t y_dtype;      /* MOE_DTYPE_ of y */
@@ -499,8 +499,8 @@ MOE_API moe_status moe_lora_apply(const moe_lora_args *args, void *workspace, si
 MOE_API size_t moe_lora_workspace_bytes(int32_t n, int32_t n_adapters);
 
 /* Reads and clears the current device's error flags of moe_lora_apply: 0, or
- * MOE_DEVFLAG_TIMEOUT where a bounded wait inside the kernel for long batches
- * ran out (that call's out is then undefined).  Synchronizes the device.
+ * MOE_DEVFLAG_TIMEOUT where a bounded wait inside its kernels ran out (that
+ * call's out is then undefined).  Synchronizes the device.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 MOE_API moe_status moe_lora_get_device_error(int32_t *flags);
 

@@ -156,7 +156,8 @@ moe_status moe_lora_apply(const moe_lora_args* args, void* workspace, size_t wor
   if (a.n < 0 || a.in_features <= 0 || a.out_features <= 0 || a.n_adapters <= 0 || a.max_rank <= 0)
     return MOE_ERR_INVALID_ARG;
   if (!is_dtype(a.y_dtype) || !is_dtype(a.out_dtype)) return MOE_ERR_INVALID_ARG;
-  if (a.in_features % 8 || a.out_features % 8 || a.max_rank % 8 || a.max_rank > kLoraMaxRank || a.n_adapters > 1024)
+  if (a.in_features % 8 || a.out_features % 8 || a.max_rank % 8 || a.max_rank > kLoraMaxRank || a.n_adapters > 1024 ||
+      a.in_features > kLoraMaxFeatures || a.out_features > kLoraMaxFeatures)
     return MOE_ERR_UNSUPPORTED;
   if (!rows_ok(a.x, a.in_features, MOE_DTYPE_BF16) || !rows_ok(a.y, a.out_features, a.y_dtype) ||
       !rows_ok(a.out, a.out_features, a.out_dtype) || !aligned(a.a, 16) || !aligned(a.b, 16) || !aligned(a.scale, 4) ||

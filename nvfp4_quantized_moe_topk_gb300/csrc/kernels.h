@@ -237,6 +237,7 @@ cudaError_t launch_router_backward(const moe_router_args& a, const float* w, con
                                    float* d_logits, float* d_bias, void* workspace, cudaStream_t s);
 
 constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxFeatures = 1 << 24;  // byte offsets within a few rows stay below 2^32
 size_t lora_workspace(int32_t n, int32_t n_adapters);  // bytes
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s);
 cudaError_t lora_device_flags(int32_t* flags);  // synchronizes the device; reads and clears

@@ -144,7 +144,7 @@ def test_router_other_refusals(lib):
 
 @pytest.mark.parametrize("want,kw", [
     (1, dict(n=-1)), (1, dict(inp=0)), (1, dict(out_=-8)), (1, dict(L=0)), (1, dict(R=0)), (2, dict(inp=60)),
-    (2, dict(out_=4)), (2, dict(R=12)), (2, dict(R=136)), (2, dict(L=1025)), (1, dict(yd=2)), (1, dict(od=-1)),
+    (2, dict(inp=(1 << 24) + 8)), (2, dict(out_=(1 << 24) + 8)), (2, dict(out_=4)), (2, dict(R=12)), (2, dict(R=136)), (2, dict(L=1025)), (1, dict(yd=2)), (1, dict(od=-1)),
     (1, dict(a=0)), (1, dict(b=0)), (1, dict(ids=0)), (1, dict(x=0)), (1, dict(out=0)), (1, dict(a=A + 8)),
     (1, dict(scale=A + 2)), (1, dict(xst=56)), (1, dict(xst=68)), (1, dict(out=A, od=1)), (1, dict(out=A, ost=72))])
 def test_lora_refusals(lib, want, kw):
