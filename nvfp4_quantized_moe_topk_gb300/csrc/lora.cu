@@ -31,10 +31,11 @@
 //     sectors.  v enters as the sum of two bf16 terms (16 bits of mantissa),
 //     three for an fp32 out (24 bits).
 //
-// Grouping: up to kFusedTokens tokens every CTA ranks the ids itself (one id a
-// thread, one launch: 100 tokens 8.6 us against 10.8, 256 10.8 / 11.6); beyond,
-// a one-CTA kernel (two kernels past kPlanSlice tokens) sorts the tokens by
-// adapter into the workspace.  A token's row of the products depends on no
+// Grouping: up to kRankedTokens tokens every CTA compares each id with those
+// before it (ranked_tile), up to small_tokens every CTA counts the adapters'
+// tokens (counted_tile); for larger batches a one-CTA kernel (two kernels past
+// kPlanSlice tokens) sorts the tokens by adapter into the workspace, which the
+// next launch's start overlaps.  A token's row of the products depends on no
 // other token, so the order inside a group does not matter to the result.
 #include "lora.cuh"
 
@@ -177,12 +178,16 @@ __global__ void __launch_bounds__(kPlanThreads)
 // there the adapter's matrices are read less often, which counts the more the
 // larger the rank, but fewer CTAs share a small batch.  Tiles of 16 against
 // 128, us on a GB300:
-//   4096 to 4096, rank 16: 1024 tokens 15.6 / 21.0, 2048 23.3 / 26.8, 3000 37.3 / 29.8
-//   4096 to 1024, rank 32: 1024 12.6 / 19.5, 2048 16.6 / 19.5, 3000 23.9 / 21.3
-//   4096 to 4096, rank 64: 300 23.3 / 30.3, 640 33.9 / 31.4, 1536 50.9 / 33.8
-//   the same, rank 128: 300 31.8 / 41.0, 512 39.9 / 41.6, 768 52.0 / 43.3, 2048 82.6 / 45.4
+//   4096 to 4096, rank 16: 1024 tokens 13.2 / 21.0, 2048 21.6 / 26.8, 3000 37.5 / 29.8
+//   4096 to 1024, rank 32: 1024 10.8 / 19.5, 2048 15.1 / 19.5, 3000 23.6 / 21.3
+//   4096 to 4096, rank 64: 300 23.2 / 30.3, 640 35.4 / 31.4, 1536 50.8 / 33.8
+//   the same, rank 128: 300 31.9 / 41.0, 512 42.3 / 41.6, 768 52.5 / 43.3
 constexpr int32_t kSmallTokens = 2048, kSmallTokensWide = 512;  // max_rank up to 32, above
-static_assert(kSmallTokens >= kFusedTokens && kSmallTokensWide >= kFusedTokens, "the other kernels need the plan");
+// Comparing against counting: 64 tokens 7.3 / 8.0 us, 128 8.1 / 8.1, 256 10.2 / 8.9; counting against a sorting
+// kernel before: 384 9.6 / 12.1, 1024 13.4 / 16.1 (4096 to 4096, rank 16, 16 adapters); in lora_mma.cu, with up to
+// 16384 tokens, counting gains nothing (4314 32.8 / 31.7, 16384 75.5 / 74.5).
+constexpr int32_t kRankedTokens = 128;
+static_assert(kRankedTokens <= kLoraThreads, "one token a thread");
 inline int32_t small_tokens(int32_t max_rank) { return max_rank <= 32 ? kSmallTokens : kSmallTokensWide; }
 
 // Set where a bounded wait ran out.
@@ -191,7 +196,7 @@ __device__ int32_t g_lora_small_flags;
 // Tiles of 16 tokens; NT groups of 8 ranks a pass of the first product.
 template <int NT>
 __global__ void __launch_bounds__(kLoraThreads, 2)
-    lora_kernel(const moe_lora_args a, const LoraPlan plan, int32_t fused, int32_t terms, uint32_t ring_bytes) {
+    lora_kernel(const moe_lora_args a, int32_t terms, uint32_t ring_bytes) {
   constexpr int MT = 16, KG = kLoraWarps;
   constexpr int RPASS = 8 * NT, RP = RPASS + 8;  // ranks of a pass; row pitch of the partial sums
   extern __shared__ __align__(16) char sm[];
@@ -209,8 +214,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   float* recv = part + KG * MT * RP;
   uint16_t* v = reinterpret_cast<uint16_t*>(recv + (C > 1 ? C * MT * RP : 0));
   const int32_t tile = (int32_t)(blockIdx.x / C);
-  if (!(fused ? ranked_tile<MT>(a, tile, row, reinterpret_cast<int32_t*>(part), t)
-              : planned_tile<MT>(a, plan, tile, row, t)))
+  if (!(a.n <= kRankedTokens ? ranked_tile<MT>(a, tile, row, reinterpret_cast<int32_t*>(part), t)
+                            : counted_tile<MT, kSmallTokens / kLoraThreads>(a, tile, row, reinterpret_cast<int32_t*>(sm), t)))
     return;
   if (C > 1) cluster_arrive();  // (waited for before the first store into a peer: its mbarrier is ready by then)
   const uint32_t slot = tid * 16, sm_u32 = smem_u32(sm);  // offsets in sm; cp.async takes addresses
@@ -489,8 +494,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
 }
 
 template <int NT>
-cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, int32_t tiles, int32_t cluster,
-                        cudaStream_t s) {
+cudaError_t lora_launch(const moe_lora_args& a, int32_t tiles, int32_t cluster, cudaStream_t s) {
   constexpr int MT = 16, RP = 8 * NT + 8;
   const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;
@@ -503,8 +507,7 @@ cudaError_t lora_launch(const moe_lora_args& a, const LoraPlan& p, bool fused, i
   static std::atomic<bool> configured[kMaxDevices];
   cudaError_t e = raise_smem_limit(lora_kernel<NT>, 220 * 1024, configured);
   if (e != cudaSuccess) return e;
-  return lora_launch_cluster(lora_kernel<NT>, tiles, cluster, kLoraThreads, ring + rest, !fused, s, a, p, (int32_t)fused,
-                             terms, ring);
+  return lora_launch_cluster(lora_kernel<NT>, tiles, cluster, kLoraThreads, ring + rest, false, s, a, terms, ring);
 }
 
 }  // namespace
@@ -518,17 +521,17 @@ cudaError_t lora_small_flags(int32_t* flags) {
 
 size_t lora_workspace(int32_t n, int32_t n_adapters) {
   const int64_t L = n_adapters;
-  if (n <= kFusedTokens) return 0;
+  if (n <= kSmallTokensWide) return 0;
   const int64_t slices = plan_slices(n);
   return (size_t)(up4(n) + 2 * up4(L + 2) + (slices > 1 ? slices * (L + 1) : 0)) * 4;
 }
 
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s) {
   const int32_t n = a.n, L = a.n_adapters;
-  const bool fused = n <= kFusedTokens, small = n <= small_tokens(a.max_rank), mma = !small && lora_mma_fits(a);
+  const bool small = n <= small_tokens(a.max_rank), mma = !small && lora_mma_fits(a);
   const int32_t mt = mma ? kMmaTokens : small ? 16 : kRowsTile;
-  const LoraPlan p = fused ? LoraPlan{} : lora_plan(workspace, n, L);
-  if (!fused) {
+  const LoraPlan p = small ? LoraPlan{} : lora_plan(workspace, n, L);
+  if (!small) {
     const int32_t slices = plan_slices(n);
     const size_t smem = (size_t)(L + 1) * 4;
     if (slices > 1) {
@@ -549,9 +552,9 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
   // take 1.1 and 3.6 us more.
   int32_t cluster = 1;
   while (cluster < 8 && tiles * cluster * 2 <= 400) cluster *= 2;
-  if (a.max_rank <= 16) return lora_launch<2>(a, p, fused, tiles, cluster, s);
-  if (a.max_rank <= 32) return lora_launch<4>(a, p, fused, tiles, cluster, s);
-  return lora_launch<8>(a, p, fused, tiles, cluster, s);
+  if (a.max_rank <= 16) return lora_launch<2>(a, tiles, cluster, s);
+  if (a.max_rank <= 32) return lora_launch<4>(a, tiles, cluster, s);
+  return lora_launch<8>(a, tiles, cluster, s);
 }
 
 }  // namespace moe

@@ -13,7 +13,6 @@ namespace moe {
 
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kFusedTokens = 256;         // at most one token a thread
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = 16;              // tokens a thread of the sorting kernel
 constexpr int kPlanSlice = kPlanThreads * kPlanPer;
@@ -157,7 +156,7 @@ __device__ __forceinline__ bool ranked_tile(const moe_lora_args& a, int32_t tile
                                             Tile& t) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, L = a.n_adapters, n = a.n;
   __shared__ int32_t found[2];
-  int32_t* leaders = scratch + kFusedTokens;  // per warp
+  int32_t* leaders = scratch + kLoraThreads;  // per warp
   const int32_t mine = tid < n ? bucket_of(a.adapter_ids[tid], L) : -1;
   if (tid == 0) found[0] = -1;
   if (tid < MT) row[tid] = -1;
@@ -192,6 +191,91 @@ __device__ __forceinline__ bool ranked_tile(const moe_lora_args& a, int32_t tile
   const bool in = mine == t.adapter && rank / MT == found[1];
   if (in) row[rank % MT] = tid;
   t.count = __syncthreads_count(in);
+  return true;
+}
+
+// The block's inclusive scan of v; sums: 32 entries of shared memory.
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  const int32_t before = lane < warp ? sums[lane] : 0;
+  return v + __reduce_add_sync(0xffffffffu, before);
+}
+
+// The same without a plan for up to PER tokens a thread: every CTA counts the
+// adapters' tokens and picks its tile's, an adapter's in the batch's order (which
+// all CTAs agree on).  scratch: n_adapters + 1 and PER x warps entries.
+template <int MT, int PER>
+__device__ __forceinline__ bool counted_tile(const moe_lora_args& a, int32_t tile, int32_t* row, int32_t* scratch,
+                                             Tile& t) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, W = T / 32;
+  const int32_t L = a.n_adapters, n = a.n;
+  __shared__ int32_t found[2], tile_sums[32], token_sums[32];
+  int32_t* count = scratch + PER * W;
+  const int steps = (n + T - 1) / T;
+  int32_t key[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) key[j] = tid + j * T < n ? a.adapter_ids[tid + j * T] : 0;
+  for (int32_t l = tid; l <= L; l += T) count[l] = 0;
+  if (tid == 0) found[0] = -1;
+  if (tid < MT) row[tid] = -1;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {  // (one addition for a warp whose tokens share their adapter)
+    if (j >= steps) break;
+    key[j] = tid + j * T < n ? bucket_of(key[j], L) : -1;
+    const bool one = __all_sync(0xffffffffu, key[j] == __shfl_sync(0xffffffffu, key[j], 0));
+    if (key[j] >= 0 && (!one || lane == 0)) atomicAdd(&count[key[j]], one ? 32 : 1);
+  }
+  __syncthreads();
+  // the adapter of this tile, adapters in order: each thread looks at a few
+  const int32_t each = (L + T) / T, l0 = tid * each, l1 = min(l0 + each, L + 1);
+  int32_t tiles = 0;
+  for (int32_t l = l0; l < l1; ++l) tiles += (count[l] + MT - 1) / MT;
+  int32_t at = block_scan(tiles, tile_sums) - tiles;
+  if (tile >= at && tile < at + tiles)
+    for (int32_t l = l0; l < l1; ++l) {
+      const int32_t mine = (count[l] + MT - 1) / MT;
+      if (tile < at + mine) {
+        found[0] = l;
+        found[1] = (tile - at) * MT;
+        break;
+      }
+      at += mine;
+    }
+  __syncthreads();
+  t.adapter = found[0];
+  if (t.adapter < 0) return false;
+  t.rank = adapter_rank(a, t.adapter);
+  t.scale = adapter_scale(a, t.adapter);
+  const int32_t first = found[1];
+  t.count = min(MT, count[t.adapter] - first);
+  // each of its tokens' place among them: tokens before it in its warp, and in the warps of lower tokens
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (j >= steps) break;
+    const uint32_t same = __ballot_sync(0xffffffffu, key[j] == t.adapter);
+    if (lane == 0) scratch[j * W + warp] = __popc(same);
+  }
+  __syncthreads();
+  const int32_t mine = tid < steps * W ? scratch[tid] : 0;
+  const int32_t before = block_scan(mine, token_sums) - mine;
+  if (tid < steps * W) scratch[tid] = before;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (j >= steps) break;
+    const uint32_t same = __ballot_sync(0xffffffffu, key[j] == t.adapter);
+    const int32_t place = scratch[j * W + warp] + __popc(same & ((1u << lane) - 1u)) - first;
+    if (key[j] == t.adapter && place >= 0 && place < MT) row[place] = tid + j * T;
+  }
+  __syncthreads();
   return true;
 }
 
