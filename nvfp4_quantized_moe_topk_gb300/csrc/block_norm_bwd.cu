@@ -26,6 +26,8 @@ namespace moe {
 
 namespace {
 
+constexpr int kNormBackwardPerSm = 8;
+
 struct NormGrads {
   NormRows dr, dx, d_residual, d_branch, d_gate;
   float *d_post, *d_pre;
@@ -240,7 +242,10 @@ template <typename RT, typename YT, int ITERS, int MAXT, int MODE>
 cudaError_t norm_backward_m(const NormParams& a, const NormGrads& d, float* part, int* ctas, cudaStream_t s) {
   const int vecs = ITERS * (2 * Vec8<RT>::kVecs + 1 + Vec8<YT>::kVecs * (a.gate_kind == MOE_GATE_FULL ? 2 : 1));
   NormPlan p = norm_plan(a.n, a.H, vecs, 768);
-  p.ctas = std::min(p.ctas, block_norm_backward_slots(a.n, a.H));
+  // Every CTA's sums cost the join a row: no more than eight CTAs an SM, and four rows a CTA where that leaves one an SM
+  // (4470 rows of 128: 15.7 us without, 10.3 so; 16384 19.5 / 16.8; 1000 rows of 2048 12.9 / 11.7).
+  const int sms = norm_sms();
+  p.ctas = std::min({p.ctas, kNormBackwardPerSm * sms, std::max(sms, (int)(a.n / 4)), block_norm_backward_slots(a.n, a.H)});
   *ctas = p.ctas;
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = raise_smem_limit(block_norm_backward_kernel<RT, YT, ITERS, MAXT, MODE>, kNormSmem, configured);
@@ -271,7 +276,7 @@ cudaError_t norm_backward_t(const NormParams& a, const NormGrads& d, float* part
 
 // CTAs that the workspace has room for: those of a GPU with up to 160 SMs.
 int block_norm_backward_slots(int32_t n, int32_t hidden) {
-  return std::max(1, std::min<int32_t>(n, 160 * std::max(1, std::min(768 / norm_threads(hidden), kNormMaxPerSm))));
+  return std::max(1, std::min<int32_t>(n, 160 * std::max(1, std::min(768 / norm_threads(hidden), kNormBackwardPerSm))));
 }
 
 cudaError_t launch_block_norm_backward(const moe_block_norm_args& args, const moe_block_norm_grads& grads, float* part,

@@ -543,8 +543,9 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // every group has at most one tile that is not full; an adapter has half of one on average
-  const int32_t tiles = n / mt + std::min(n, L + 1), expected = n / mt + std::min(n, L) / 2;
+  // Every group has at most one tile that is not full; an adapter has half of one on average, and three quarters are
+  // allowed for (a tile too many for the clusters that fit at once waits for the first to finish).
+  const int32_t tiles = n / mt + std::min(n, L + 1), expected = n / mt + (3 * std::min(n, L) + 3) / 4;
   if (mma) return launch_lora_mma(a, p, tiles, expected, s);
   if (!small) return launch_lora_rows(a, p, tiles, expected, s);
   // Up to 400 CTAs, of which two share an SM (`tiles` is a bound, so some have nothing to do).  With 608 a call of 768

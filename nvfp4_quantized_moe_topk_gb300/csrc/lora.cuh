@@ -335,9 +335,8 @@ cudaError_t lora_launch_cluster(void (*kernel)(KArgs...), int32_t tiles, int32_t
 // CTAs that share a tile where one occupies an SM: as many (up to
 // kLoraMaxCluster) as leave all tiles on the GPU at once.  How many clusters of
 // a size that is depends on the SMs of its clusters of SMs and is asked for
-// once a device and size.  `tiles`: the tiles to expect, half a tile more for
-// every adapter than full tiles alone would be (where there are a few more, they
-// wait for the first to finish).
+// once a device and size.  `tiles`: the tiles to expect (where there are a few
+// more, they wait for the first to finish).
 constexpr int32_t kLoraMaxCluster = 8;
 template <typename... KArgs>
 cudaError_t lora_cluster(void (*kernel)(KArgs...), int threads, size_t smem, int32_t tiles,

@@ -14,7 +14,7 @@
 // 40; 3.7 TB/s).  Where there are fewer tiles than SMs, the CTAs of a cluster
 // take turns with the steps of both products and add their D1 through each
 // other's shared memory (4096 tokens, 4096 to 4096, rank 64: 94 us with a CTA a
-// tile, 38 with four).
+// tile, 43 with three, 38 with four).
 //
 //   first product:  D1[128 tokens][ranks] += x chunk . A chunk^T, 64 columns of
 //     in_features a step (the tokens' rows are gathered: 8 lanes copy 128 bytes
