@@ -381,3 +381,11 @@ def test_clusters(dev, n, L, inp, out, R):
 
     assert torch.equal(c.run(), got)
     assert api.lora_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [128, 129, 256, 257, 2048, 2049])
+@pytest.mark.parametrize("L,run", [(1, 300), (1024, 1), (1024, 40), (255, 3), (256, 3)])
+def test_grouping(dev, n, L, run):
+    """Both sides of each way to group the tokens, few and many adapters, in runs and in random order."""
+    c = Case(dev, _ids(n, L, n + L, run), 72, 40, L, 8, "fp32", "fp32")
+    c.check(c.run())
