@@ -1,6 +1,6 @@
-// lora.cuh -- what the adapter kernels share (lora.cu: few tokens, lora_rows.cu:
-// many): the plan that groups tokens by adapter, matrix instructions, the
-// clusters' shared memory and asynchronous copies.
+// lora.cuh -- what the adapter kernels share (lora.cu: few tokens; lora_mma.cu
+// and lora_rows.cu: many): the ways to group tokens by adapter, matrix
+// instructions, the clusters' shared memory and asynchronous copies.
 #pragma once
 
 #include <algorithm>
