@@ -469,9 +469,8 @@ MOE_API size_t moe_router_workspace_bytes(int32_t n, int32_t n_experts, int32_t 
  *     v[i]      = sum_c a[l][i][c] * x[t][c]        i < ranks[l]
  *     out[t][o] = y[t][o] + scale[l] * sum_i b[l][o][i] * v[i]
  * for every token and out[t] = y[t] without an adapter.  Products of bf16 are
- * exact and summed in fp32; v is not rounded to fewer than 16 bits of
- * mantissa on the way to the second product (24 for an fp32 out), and the
- * result is rounded once. */
+ * exact and summed in fp32; scale * v keeps its 24 bits on the way to the
+ * second product, and the result is rounded once. */
 typedef struct moe_lora_args {
   int32_t n;            /* tokens */
   int32_t in_features;  /* multiple of 8, at most 2^24 */

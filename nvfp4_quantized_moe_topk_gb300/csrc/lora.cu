@@ -28,8 +28,7 @@
 //     columns of a block are dealt to the four 8-column instructions so that
 //     a lane ends up with 8 neighbouring columns of a token (two runs of 4
 //     where y or out is fp32): y comes in and out goes out in whole memory
-//     sectors.  v enters as the sum of two bf16 terms (16 bits of mantissa),
-//     three for an fp32 out (24 bits).
+//     sectors.  v enters as the sum of three bf16 terms (24 bits of mantissa).
 //
 // Grouping: up to kRankedTokens tokens every CTA compares each id with those
 // before it (ranked_tile), up to small_tokens every CTA counts the adapters'
@@ -196,7 +195,7 @@ __device__ int32_t g_lora_small_flags;
 // Tiles of 16 tokens; NT groups of 8 ranks a pass of the first product.
 template <int NT>
 __global__ void __launch_bounds__(kLoraThreads, 2)
-    lora_kernel(const moe_lora_args a, int32_t terms, uint32_t ring_bytes) {
+    lora_kernel(const moe_lora_args a, uint32_t ring_bytes) {
   constexpr int MT = 16, KG = kLoraWarps;
   constexpr int RPASS = 8 * NT, RP = RPASS + 8;  // ranks of a pass; row pitch of the partial sums
   extern __shared__ __align__(16) char sm[];
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
     fence_mbar_init();
   }
   Tile t;
-  // ring; the warps' sums [KG][MT][RP]; in a cluster the CTAs' sums [C][MT][RP]; v [terms][MT][VP] bf16
+  // ring; the warps' sums [KG][MT][RP]; in a cluster the CTAs' sums [C][MT][RP]; v [kLoraTerms][MT][VP] bf16
   float* part = reinterpret_cast<float*>(sm + ring_bytes);
   float* recv = part + KG * MT * RP;
   uint16_t* v = reinterpret_cast<uint16_t*>(recv + (C > 1 ? C * MT * RP : 0));
@@ -402,14 +401,14 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
       for (int i = 0; i < M; ++i) {
         float s = r0 + r + i < rank ? sum[i] * t.scale : 0.f;
         if (r0 + r + i < R32)
-          for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
+          for (int k = 0; k < kLoraTerms; ++k) {
             const uint16_t b = f2bf_rn(s);
             v[(k * MT + m) * VP + r0 + r + i] = b;
             s -= bf16lo(b);
           }
       }
       if (NT == 2)  // the second half of the window of 32
-        for (int k = 0; k < terms; ++k) v[(k * MT + (tid >> 4)) * VP + 16 + (tid & 15)] = 0;
+        for (int k = 0; k < kLoraTerms; ++k) v[(k * MT + (tid >> 4)) * VP + 16 + (tid & 15)] = 0;
       if (C > 1 && r0 + RPASS < rank) cluster_arrive();
       __syncthreads();
     }
@@ -437,7 +436,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           bv[j].w &= left == 7 ? 0xffffu : 0u;
         }
       }
-      for (int k = 0; k < terms; ++k) {
+      for (int k = 0; k < kLoraTerms; ++k) {
         const uint16_t* vr = v + (k * MT + g) * VP + k0 + 8 * q;
         const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * VP);
         __syncwarp();
@@ -496,18 +495,17 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
 template <int NT>
 cudaError_t lora_launch(const moe_lora_args& a, int32_t tiles, int32_t cluster, cudaStream_t s) {
   constexpr int MT = 16, RP = 8 * NT + 8;
-  const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const int32_t VP = a.max_rank <= 32 ? 32 : ((a.max_rank + 63) & ~63) + 32;
   // up to four ring steps, as many as let two CTAs share an SM if those are two or more, else as fit one
   const uint32_t y_vecs = !a.y.data ? 0 : a.y_dtype == MOE_DTYPE_F32 ? 2 : 1;
   const uint32_t step = std::max<uint32_t>(2 + NT, 4 * ((a.max_rank + 31) / 32) + 2 * y_vecs) * kSlotVec;
-  const uint32_t rest = (kLoraWarps + (cluster > 1 ? cluster : 0)) * MT * RP * 4 + terms * MT * VP * 2;
+  const uint32_t rest = (kLoraWarps + (cluster > 1 ? cluster : 0)) * MT * RP * 4 + kLoraTerms * MT * VP * 2;
   const uint32_t room = (rest + 2 * step <= 112 * 1024 ? 112 * 1024 : 220 * 1024) - rest;
   const uint32_t ring = std::min(4u, room / step) * step;
   static std::atomic<bool> configured[kMaxDevices];
   cudaError_t e = raise_smem_limit(lora_kernel<NT>, 220 * 1024, configured);
   if (e != cudaSuccess) return e;
-  return lora_launch_cluster(lora_kernel<NT>, tiles, cluster, kLoraThreads, ring + rest, false, s, a, terms, ring);
+  return lora_launch_cluster(lora_kernel<NT>, tiles, cluster, kLoraThreads, ring + rest, false, s, a, ring);
 }
 
 }  // namespace

@@ -17,6 +17,12 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = 16;              // tokens a thread of the sorting kernel
 constexpr int kPlanSlice = kPlanThreads * kPlanPer;
 
+// v goes into the second product as a sum of this many bf16 terms, each the rounding of what is left: all 24 bits of
+// its fp32 value, for a bf16 out too (where y cancels most of B v, the 16 bits of two terms show there as well).  Two
+// against three, us on a GB300: 16384 tokens, 4096 to 2048, ranks to 64 74.5 / 76.1; 4096 to 4096, rank 128 121 / 130;
+// 32 tokens no difference.
+constexpr int kLoraTerms = 3;
+
 // Sorted tokens and group starts; bucket n_adapters holds the tokens without
 // an adapter.
 struct LoraPlan {

@@ -19,11 +19,12 @@
 //   first product:  D1[128 tokens][ranks] += x chunk . A chunk^T, 64 columns of
 //     in_features a step (the tokens' rows are gathered: 8 lanes copy 128 bytes
 //     of one); each half has a D1, and they are added at the end.
-//   v = scale D1 as a sum of two bf16 terms (three for an fp32 out), each
-//     term a K-major operand in shared memory.
+//   v = scale D1 as a sum of three bf16 terms, each a K-major operand in shared
+//     memory.
 //   second product: D2[128][a block of 64 columns, 32 where y or out is fp32] =
 //     sum over terms of v . B rows^T.  y comes in and out leaves through shared
-//     memory, so that both move in whole 128-byte lines.
+//     memory, so that both move in whole 128-byte lines.  Above 64 ranks, where v
+//     takes 96 KB, a bf16 out takes a bf16 y's place there.
 #include "lora.cuh"
 
 namespace moe {
@@ -65,10 +66,20 @@ __host__ __device__ inline uint32_t mma_step2(bool has_y, int32_t rank_blocks, i
   return (has_y ? kOperandTile : 0) + (uint32_t)rank_blocks * columns * 128;
 }
 
+// Whether out takes y's place in its ring step (the same types; each thread writes what it has read), which leaves room
+// for a second step beside v; else the halves have an out block each.
+__host__ __device__ inline bool out_over_y(const moe_lora_args& a, int rank_blocks) {
+  return rank_blocks > 1 && a.y.data && a.y_dtype == MOE_DTYPE_BF16 && a.out_dtype == MOE_DTYPE_BF16;
+}
+// Bytes of the out blocks and v.
+__host__ __device__ inline uint32_t mma_fixed(bool over_y, int rank_blocks) {
+  return ((over_y ? 0u : 2u) + kLoraTerms * rank_blocks) * kOperandTile;
+}
+
 // RB: blocks of 64 ranks (1 or 2).
 template <int RB>
 __global__ void __launch_bounds__(kMmaThreads, 1)
-    lora_mma_kernel(const moe_lora_args a, const LoraPlan plan, int32_t terms, uint32_t ring_bytes) {
+    lora_mma_kernel(const moe_lora_args a, const LoraPlan plan, uint32_t ring_bytes) {
   extern __shared__ __align__(16) char sm_raw[];
   __shared__ int32_t row[kMmaTile];
   __shared__ __align__(8) uint64_t done1[2][kMmaMaxStages], done2[2];
@@ -104,12 +115,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const uint32_t tmem = tmem_slot;
   const int32_t rank = t.rank, ranks16 = (rank + 15) / 16;
   // First product: each half's ring is half of the space.  Then: the first half's ring, the halves' out blocks, v
-  // [terms][RB] operand tiles, the second half's ring (which each half may fill when its own part of the first
+  // [kLoraTerms][RB] operand tiles, the second half's ring (which each half may fill when its own part of the first
   // product is done).
-  const uint32_t sm_u32 = smem_u32(sm), space = 2 * ring_bytes + (2 + terms * RB) * kOperandTile;
+  const bool over_y = out_over_y(a, RB);
+  const uint32_t sm_u32 = smem_u32(sm), space = 2 * ring_bytes + mma_fixed(over_y, RB);
   const uint32_t ring1_bytes = space / 2 / 1024 * 1024, ring1 = half * ring1_bytes;
-  const uint32_t ring = half * (space - ring_bytes), out_at = ring_bytes, v_at = ring_bytes + 2 * kOperandTile;
-  char* obuf = sm + out_at + half * kOperandTile;
+  const uint32_t ring = half * (space - ring_bytes), out_at = ring_bytes;
+  const uint32_t v_at = ring_bytes + (over_y ? 0 : 2 * kOperandTile);
   const uint32_t quadrant = (uint32_t)(32 * (warp & 3)) << 16;  // this warp's lanes of tensor memory
   const int m = 32 * (warp & 3) + lane;                         // its thread's token
   const int p8 = htid & 7, r8 = htid >> 3;  // copies of 128-byte rows: piece, first row (the others 32, 64, 96 further)
@@ -238,7 +250,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     if (mine < chunks && !dead && !mbar_wait(&done1[half][last], last_parity, &g_lora_flags)) dead = true;
     ring_wait(0);
-    // the CTAs' sums of a cluster meet in the (still unused) out blocks, those of two blocks of ranks in the rings
+    // the CTAs' sums of a cluster meet in the (still unused) out blocks, those of two blocks of ranks in the 64 KB
+    // before v: the first ring, and out blocks where there are any
     const bool ring_meets = RB > 1 && C > 1;
     if (!dead && !ring_meets)
       for (int s = 0; s + 1 < out_stages; ++s) fetch_out(mine + jump * s, s);
@@ -294,7 +307,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       if (j >= ranks16 || dead) continue;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[b][i] = 16 * j + i < rank ? s[b][i] * t.scale : 0.f;
-      for (int k = 0; k < terms; ++k) {  // s = a sum of bf16 terms, each the rounding of what is left
+      for (int k = 0; k < kLoraTerms; ++k) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t o[4];
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   }
 
   // adds y (in ring step `stage`) to the half's D2, 16 of a thread's columns from `first` on, into the out block
-  auto finish = [&](uint32_t first, int stage) {
+  auto finish = [&](uint32_t first, int stage, char* obuf) {
     uint32_t d[16];
     if (rank > 0) {
       tmem_ld16(tmem + quadrant + kD2 + half * 64 + first, d);
@@ -369,12 +382,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     fence_proxy_async_smem();
     dead = half_or(half, dead);  // block ob has landed, and the out block before it has been written out
     if (dead) break;
+    char* obuf = sm + (over_y ? ring + stage * out_step : out_at + half * kOperandTile);
     if (rank > 0) {
       if (hwarp == 0) {
         tc_fence_after();
         if (elect_one()) {
           const uint32_t b = sm_u32 + ring + stage * out_step + b_at;
-          for (int k = 0; k < terms; ++k)
+          for (int k = 0; k < kLoraTerms; ++k)
             for (int32_t j = 0; j < ranks16; ++j)
               tc_mma_bf16(tmem + kD2 + half * 64, smem_desc_k128(sm_u32 + v_at + (uint32_t)(k * RB + j / 4) * kOperandTile + (j % 4) * 32),
                           smem_desc_k128(b + (uint32_t)(j / 4) * b_tile + (j % 4) * 32), out_idesc, (k | j) != 0);
@@ -391,7 +405,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       __syncwarp();
       tc_fence_after();
     }
-    for (int32_t u = (hwarp >> 2) * 16; u < columns; u += 32) finish(u, stage);
+    for (int32_t u = (hwarp >> 2) * 16; u < columns; u += 32) finish(u, stage, obuf);
     tc_fence_before();
     if (half_or(half, dead)) {
       dead = true;
@@ -425,15 +439,14 @@ cudaError_t lora_mma_launch(const moe_lora_args& a, const LoraPlan& p, int32_t t
   int32_t cluster = 1;
   e = lora_cluster(lora_mma_kernel<RB>, kMmaThreads, kMmaSmem, expected, held, &cluster);
   if (e != cudaSuccess) return e;
-  const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const uint32_t step = std::max(mma_step1((a.max_rank + 15) / 16),
                                  mma_step2(a.y.data != nullptr, RB, block_columns(a.y_dtype == MOE_DTYPE_F32,
                                                                                   a.out_dtype == MOE_DTYPE_F32)));
-  const uint32_t rest = 1024 + 2 * kOperandTile + terms * RB * kOperandTile;
-  // (two steps at least: 2 x 24 KB of 72, or with RB 2 and two terms 2 x 32 of 64)
+  // (two steps of the second product at least, and with RB 2 v from 64 KB on: 3 x 24 KB of 72; with RB 2 and out over y
+  // 2 x 32 of 64, else 2 x 24 of 48 before out blocks of 32)
+  const uint32_t rest = 1024 + mma_fixed(out_over_y(a, RB), RB);
   const uint32_t ring = std::min((kMmaSmem - rest) / 2 / 1024 * 1024, kMmaMaxStages * step);
-  return lora_launch_cluster(lora_mma_kernel<RB>, tiles, cluster, kMmaThreads, 2 * ring + rest, true, s, a, p, terms,
-                             ring);
+  return lora_launch_cluster(lora_mma_kernel<RB>, tiles, cluster, kMmaThreads, 2 * ring + rest, true, s, a, p, ring);
 }
 
 }  // namespace

@@ -37,7 +37,7 @@ __host__ __device__ inline uint32_t expand_step(int32_t ranks32, uint32_t y_vecs
 constexpr int kPass = 64, kPartPitch = kPass + 8;  // ranks of a pass of the first product; pitch of its sums
 
 __global__ void __launch_bounds__(kLoraThreads, 2)
-    lora_rows_kernel(const moe_lora_args a, const LoraPlan plan, int32_t terms, uint32_t ring_bytes) {
+    lora_rows_kernel(const moe_lora_args a, const LoraPlan plan, uint32_t ring_bytes) {
   extern __shared__ __align__(128) char sm[];
   __shared__ int32_t row[kRowsTile];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
@@ -47,14 +47,14 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
   if (!planned_tile<kRowsTile>(a, plan, (int32_t)(blockIdx.x / C), row, t)) return;
   const int32_t rank = t.rank;
   const float scale = t.scale;
-  // ring; v [terms][64][VP] bf16; in a cluster the CTA's sums [64][kPartPitch].  Between the loops the ring holds
+  // ring; v [kLoraTerms][64][VP] bf16; in a cluster the CTA's sums [64][kPartPitch].  Between the loops the ring holds
   // the halves' sums [2][64][kPartPitch].
   const int32_t kwins = (rank + 31) / 32;
   const uint32_t v_pitch = (uint32_t)((a.max_rank + 63) / 64) * 128;  // bytes
   const uint32_t sm_u32 = smem_u32(sm), v_at = ring_bytes;  // (offsets in sm; cp.async takes addresses)
   char* v_base = sm + ring_bytes;
   float* part = reinterpret_cast<float*>(sm);
-  float* sum = reinterpret_cast<float*>(v_base + terms * kRowsTile * v_pitch);
+  float* sum = reinterpret_cast<float*>(v_base + kLoraTerms * kRowsTile * v_pitch);
   int32_t tok[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) tok[h] = row[group * 16 + h * 8 + g];
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
         float s0 = used ? s[i].x * scale : 0.f, s1 = r0 + r + 1 < rank ? s[i].y * scale : 0.f;
         char* to = v_base + m * v_pitch + (uint32_t)(r0 / kPass) * 128 + (((lane >> 2) ^ ((m & 1) << 2)) * 16) +
                    (lane & 3) * 4;
-        for (int k = 0; k < terms; ++k, to += kRowsTile * v_pitch) {  // a sum of bf16 terms, each the rounding of the rest
+        for (int k = 0; k < kLoraTerms; ++k, to += kRowsTile * v_pitch) {
           const uint32_t b = pack2(s0, s1);
           *reinterpret_cast<uint32_t*>(to) = b;
           s0 -= bf16lo(b);
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
           }
         }
       const uint32_t vp = v_at + (group * 16 + g) * v_pitch + (k / 2) * 128 + ((((k & 1) * 4 + q) ^ ((g & 1) << 2)) * 16);
-      for (int i = 0; i < terms; ++i) {
+      for (int i = 0; i < kLoraTerms; ++i) {
         const uint4 lo = slot16(sm, vp + i * kRowsTile * v_pitch), hi = slot16(sm, vp + (i * kRowsTile + 8) * v_pitch);
         __syncwarp();
 #pragma unroll
@@ -355,9 +355,8 @@ cudaError_t launch_lora_rows(const moe_lora_args& a, const LoraPlan& p, int32_t 
   int32_t cluster = 1;
   e = lora_cluster(lora_rows_kernel, kLoraThreads, 225 * 1024, expected, held, &cluster);
   if (e != cudaSuccess) return e;
-  const int32_t terms = a.out_dtype == MOE_DTYPE_BF16 ? 2 : 3;
   const uint32_t y_vecs = !a.y.data ? 0 : a.y_dtype == MOE_DTYPE_F32 ? 2 : 1;
-  const uint32_t rest = terms * kRowsTile * ((a.max_rank + 63) / 64) * 128 +
+  const uint32_t rest = kLoraTerms * kRowsTile * ((a.max_rank + 63) / 64) * 128 +
                         (cluster > 1 ? kRowsTile * kPartPitch * 4 : 0);
   // up to four ring steps, at least two: without a cluster as many as let two CTAs share an SM if those are two or
   // more, else as many as fit one
@@ -365,7 +364,7 @@ cudaError_t launch_lora_rows(const moe_lora_args& a, const LoraPlan& p, int32_t 
   const uint32_t two = 112 * 1024, one = 224 * 1024;
   uint32_t ring = std::min(4 * step, (cluster == 1 && rest + 2 * step <= two ? two : one) - rest);
   ring = std::max<uint32_t>(ring, 2 * kRowsTile * kPartPitch * 4) / 128 * 128;
-  return lora_launch_cluster(lora_rows_kernel, tiles, cluster, kLoraThreads, ring + rest, true, s, a, p, terms, ring);
+  return lora_launch_cluster(lora_rows_kernel, tiles, cluster, kLoraThreads, ring + rest, true, s, a, p, ring);
 }
 
 }  // namespace moe
