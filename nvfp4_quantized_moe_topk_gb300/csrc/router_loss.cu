@@ -182,8 +182,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // From the logits of TOK tokens (-inf past the last expert) the numerators of
 // their softmax, z <- e^(z - max) in place, and the lane's part of their sums; a
 // row without any logit above -inf gives 0.  s_bias: the bias in shared memory,
-// or nullptr.  e^(z - max) is 2^(z log2 e - c) with c = max log2 e rounded: one
-// fma, and c's rounding cancels in the quotient.  p is good to 1e-6.
+// or nullptr.  e^(z - max) is 2^((z - max) log2 e): the largest logit's is exactly
+// 1, and differences count alone, whatever the logits' size (with max log2 e
+// taken from z log2 e in one fma, its rounding is an exponent of 100 and more
+// from |max| 2e9 on, and no time is gained).  A p is good to 2.3 |z - max| 2^-24
+// of itself and a few units in the last place.
 template <bool VEC, int N, int TOK>
 __device__ __forceinline__ void softmax_parts(const float* s_bias, int32_t E, int lane, F2 (&z)[TOK][N / 2],
                                               float (&sum)[TOK]) {
@@ -213,11 +216,11 @@ __device__ __forceinline__ void softmax_parts(const float* s_bias, int32_t E, in
     for (int u = 0; u < TOK; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    const F2 c = f2(m[u] == -INFINITY ? 0.f : -m[u] * kLog2e);
+    const F2 c = f2(m[u] == -INFINITY ? 0.f : -m[u]);
     F2 s = f2(0.f);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const F2 x = fma2(z[u][i], f2(kLog2e), c);
+      const F2 x = mul2(add2(z[u][i], c), f2(kLog2e));
       z[u][i] = {exp2_fast(x.x), exp2_fast(x.y)};
       s = add2(s, z[u][i]);
     }
