@@ -470,7 +470,9 @@ MOE_API size_t moe_router_workspace_bytes(int32_t n, int32_t n_experts, int32_t 
  *     out[t][o] = y[t][o] + scale[l] * sum_i b[l][o][i] * v[i]
  * for every token and out[t] = y[t] without an adapter.  Products of bf16 are
  * exact and summed in fp32; scale * v keeps its 24 bits on the way to the
- * second product, and the result is rounded once. */
+ * second product (an infinity stays one), and the result is rounded once.
+ * Infinities and NaN in x stay in their token's row, those in b in their
+ * column, where an infinite b gives an infinity or NaN. */
 typedef struct moe_lora_args {
   int32_t n;            /* tokens */
   int32_t in_features;  /* multiple of 8, at most 2^24 */

@@ -401,11 +401,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
       for (int i = 0; i < M; ++i) {
         float s = r0 + r + i < rank ? sum[i] * t.scale : 0.f;
         if (r0 + r + i < R32)
-          for (int k = 0; k < kLoraTerms; ++k) {
-            const uint16_t b = f2bf_rn(s);
-            v[(k * MT + m) * VP + r0 + r + i] = b;
-            s -= bf16lo(b);
-          }
+          for (int k = 0; k < kLoraTerms; ++k) v[(k * MT + m) * VP + r0 + r + i] = (uint16_t)(take_term(s) >> 16);
       }
       if (NT == 2)  // the second half of the window of 32
         for (int k = 0; k < kLoraTerms; ++k) v[(k * MT + (tid >> 4)) * VP + 16 + (tid & 15)] = 0;

@@ -17,11 +17,24 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = 16;              // tokens a thread of the sorting kernel
 constexpr int kPlanSlice = kPlanThreads * kPlanPer;
 
-// v goes into the second product as a sum of this many bf16 terms, each the rounding of what is left: all 24 bits of
+// v goes into the second product as a sum of this many bf16 terms, each the upper half of what is left: all 24 bits of
 // its fp32 value, for a bf16 out too (where y cancels most of B v, the 16 bits of two terms show there as well).  Two
 // against three, us on a GB300: 16384 tokens, 4096 to 2048, ranks to 64 74.5 / 76.1; 4096 to 4096, rank 128 121 / 130;
 // 32 tokens no difference.
 constexpr int kLoraTerms = 3;
+// Takes the next term off s; the result's upper 16 bits are it.  (Cut off, not rounded: a v above the largest bf16 would
+// round to infinity.  Of an infinity nothing is left, where a subtraction gives NaN; a NaN has bits in its upper half, as
+// every result of arithmetic has.)
+__device__ __forceinline__ uint32_t take_term(float& s) {
+  const uint32_t t = __float_as_uint(s) & 0xffff0000u;
+  s = (t & 0x7fffffffu) == 0x7f800000u ? 0.f : s - __uint_as_float(t);
+  return t;
+}
+// Of two values, as a bf16 pair.
+__device__ __forceinline__ uint32_t take_terms(float& lo, float& hi) {
+  const uint32_t l = take_term(lo);
+  return take_term(hi) | l >> 16;
+}
 
 // Sorted tokens and group starts; bucket n_adapters holds the tokens without
 // an adapter.

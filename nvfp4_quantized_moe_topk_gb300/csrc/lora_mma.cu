@@ -312,12 +312,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         for (int h = 0; h < 2; ++h) {
           uint32_t o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float &lo = s[b][8 * h + 2 * i], &hi = s[b][8 * h + 2 * i + 1];
-            o[i] = pack2(lo, hi);
-            lo -= bf16lo(o[i]);
-            hi -= bf16hi(o[i]);
-          }
+          for (int i = 0; i < 4; ++i) o[i] = take_terms(s[b][8 * h + 2 * i], s[b][8 * h + 2 * i + 1]);
           *reinterpret_cast<uint4*>(sm + v_at + (uint32_t)(k * RB + b) * kOperandTile + swizzled(m, j0 * 2 + h)) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }

@@ -175,12 +175,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
         float s0 = used ? s[i].x * scale : 0.f, s1 = r0 + r + 1 < rank ? s[i].y * scale : 0.f;
         char* to = v_base + m * v_pitch + (uint32_t)(r0 / kPass) * 128 + (((lane >> 2) ^ ((m & 1) << 2)) * 16) +
                    (lane & 3) * 4;
-        for (int k = 0; k < kLoraTerms; ++k, to += kRowsTile * v_pitch) {
-          const uint32_t b = pack2(s0, s1);
-          *reinterpret_cast<uint32_t*>(to) = b;
-          s0 -= bf16lo(b);
-          s1 -= bf16hi(b);
-        }
+        for (int k = 0; k < kLoraTerms; ++k, to += kRowsTile * v_pitch)
+          *reinterpret_cast<uint32_t*>(to) = take_terms(s0, s1);
       }
       if (C > 1)
         cluster_sync();  // the peers have read this CTA's sums
