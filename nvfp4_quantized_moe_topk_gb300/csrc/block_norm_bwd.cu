@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(MAXT, 768 / MAXT)
     }
     float s[3] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y};
     cta_sums3(s[0], s[1], s[2], red[buf]);
-    const float m1 = ru * ru * ru * (s[0] * a.inv_h);
+    // (from the sum outward: with a small eps ru^3 of a row of zeros is more than fp32 holds, where its sum is 0)
+    const float m1 = ru * (ru * (ru * (s[0] * a.inv_h)));
     const float T = rp * (s[1] - s[2] * m1);  // sum(c y rp G)
     if (token && d.d_gate.p && threadIdx.x == 0)
       reinterpret_cast<float*>(d.d_gate.p)[t] = a.gate_sigmoid ? T * gt * (1.f - gt) : T;
-    const float kc = rp * gt, ky = post ? rp * rp * gt * T * a.inv_h : 0.f;
+    const float kc = rp * gt, ky = post ? rp * (rp * (gt * (T * a.inv_h))) : 0.f;
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
       const Lane<Q> l(i, a.H);
