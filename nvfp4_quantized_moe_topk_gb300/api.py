@@ -297,6 +297,13 @@ def _binding():
     return _native
 
 
+def _on_gpu(t, dims: int) -> bool:
+    """Whether t is a CUDA tensor of so many dimensions, for which a workspace can be made (else the call refuses it)."""
+    import torch
+
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == dims
+
+
 def _new_workspace(size: int, like=None, stream=None):
     """size bytes on the current device; for a call on another stream than the current one, allocated on that."""
     import torch
@@ -337,8 +344,8 @@ def block_norm_backward(d_residual_out, d_x, residual_out, branch=None, gate=Non
     None: zero).  residual_out, rstd_post and rstd_pre are what block_norm left."""
     native = _native or _binding()
     if workspace is None:
-        lead = next((t for t in (d_residual_out, residual_out, branch) if t is not None and t.dim() == 2), None)
-        if lead is not None and lead.is_cuda:
+        lead = next((t for t in (d_residual_out, residual_out, branch) if _on_gpu(t, 2)), None)
+        if lead is not None:
             workspace = _new_workspace(_lib.moe_block_norm_workspace_bytes(*lead.shape), lead, stream)
     native.block_norm_backward(d_residual_out, d_x, residual_out, branch, gate, post_weight, pre_weight, rstd_post,
                                rstd_pre, d_residual, d_branch, d_gate, d_post_weight, d_pre_weight, eps,
@@ -352,7 +359,7 @@ def router_workspace(n: int, n_experts: int, n_seqs: int = 1):
 
 
 def _router_workspace_for(logits, seq_offsets, stream):
-    if logits is None or logits.dim() != 2 or not logits.is_cuda:
+    if not _on_gpu(logits, 2) or not (seq_offsets is None or _on_gpu(seq_offsets, 1)):
         return None  # refused by the call
     seqs = 1 if seq_offsets is None else max(1, seq_offsets.numel() - 1)
     return _new_workspace(load().moe_router_workspace_bytes(*logits.shape, seqs), logits, stream)
@@ -393,7 +400,7 @@ def lora_apply(x, adapter_ids, a, b, y, out, *, scale=None, ranks=None, workspac
     bank, such as -1: out[t] = y[t]).  x [n, in] bf16, a [L, R, in] and b [L, out, R] bf16, y [n, out] (None: zero)
     and out [n, out] bf16 or fp32 (out may be y), scale [L] fp32, ranks [L] int32."""
     native = _native or _binding()
-    if workspace is None and x is not None and x.dim() == 2 and x.is_cuda and a is not None:
+    if workspace is None and _on_gpu(x, 2) and _on_gpu(a, 3):
         workspace = _new_workspace(_lib.moe_lora_workspace_bytes(x.shape[0], a.shape[0]), x, stream)
     native.lora_apply(x, adapter_ids, a, b, y, out, scale, ranks, workspace, stream)
     return out
