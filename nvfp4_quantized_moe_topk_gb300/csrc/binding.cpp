@@ -99,8 +99,7 @@ struct Call {
   }
   moe_stream_t stream(PyObject* o) const {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-    if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+    PyObject* h = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
     if (!h) throw Raised();
     void* p = PyLong_AsVoidPtr(h);
     Py_DECREF(h);

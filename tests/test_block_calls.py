@@ -48,3 +48,18 @@ def test_tensors_of_other_dimensions():
     for offsets in (torch.zeros((), dtype=torch.int32, device=dev), ids[:0], ids[None]):
         with pytest.raises(api.MoeError):
             api.balance_loss(logits, None, ids[:, None], logits[0, :1], ids, logits, ids, coef=1.0, seq_offsets=offsets)
+
+
+@pytest.mark.gpu
+def test_stream_that_is_no_handle():
+    """Nothing is enqueued on another stream in its place."""
+    import torch
+
+    dev = torch.device("cuda:0")
+    r = torch.ones(4, 64, dtype=torch.bfloat16, device=dev)
+    w, x = torch.ones(64, dtype=torch.bfloat16, device=dev), torch.full_like(r, 7.0)
+    for stream in (1 << 70, "main", object()):
+        with pytest.raises((api.MoeError, TypeError, OverflowError, AttributeError)):
+            api.block_norm(r, pre_weight=w, x_out=x, stream=stream)
+    torch.cuda.synchronize()
+    assert bool((x == 7.0).all())
