@@ -5,7 +5,9 @@ shared library with the CUDA runtime linked statically.  The driver API entry
 point needed for tensor maps is resolved at run time, so the library does not
 link libcuda.  ``csrc/binding.cpp``, the Python module with the argument checks
 of the operators around the layer, is compiled beside it by g++ against the
-installed torch and linked to the library.
+installed torch and linked to the library.  The library needs nvcc alone: where
+the binding cannot be built (no torch, no Python headers), the library still is,
+and build() warns.
 Usage: ``python -m nvfp4_quantized_moe_topk_gb300.build``.
 """
 from __future__ import annotations
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -39,22 +42,34 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+def _newer(target: str, inputs: list[str]) -> bool:
+    """Whether target is there and no older than its inputs, the header and this file."""
+    if not os.path.exists(target):
+        return False
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in
+               [*inputs, *glob.glob(os.path.join(ROOT, "include", "*.h")), os.path.abspath(__file__)])
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+def _binding_up_to_date() -> bool:
+    return _newer(BINDING, glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def _torch_dir() -> str:
     import importlib.util
 
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        raise RuntimeError("torch is not installed")
+    return os.path.dirname(spec.origin)
 
 
 def _compile_binding() -> str:
@@ -100,16 +115,23 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stderr)
         return obj
 
+    library = force or not _library_up_to_date()
     with cf.ThreadPoolExecutor(max_workers=min(16, len(sources()) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, sources()))
-        binding_obj = binding.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+        binding = ex.submit(_compile_binding) if force or not _binding_up_to_date() else None
+        objs = list(ex.map(compile_one, sources())) if library else []
+    if library:
+        tmp = LIB + f".tmp{os.getpid()}"
+        r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if binding is not None:
+        try:
+            _link_binding(binding.result())
+        except (RuntimeError, OSError) as e:
+            if os.path.exists(BINDING):  # of other sources than the library's
+                os.remove(BINDING)
+            warnings.warn(f"{LIB} is built, the Python calls of the operators around the layer are not: {e}")
     return LIB
 
 
