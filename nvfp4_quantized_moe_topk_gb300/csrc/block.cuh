@@ -30,27 +30,6 @@ __device__ __forceinline__ void unpack8(const uint4& d, float (&v)[8]) {
   v[6] = bf16lo(d.w);
   v[7] = bf16hi(d.w);
 }
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  unpack8(*reinterpret_cast<const uint4*>(p), v);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x;
-  v[1] = a.y;
-  v[2] = a.z;
-  v[3] = a.w;
-  v[4] = b.x;
-  v[5] = b.y;
-  v[6] = b.z;
-  v[7] = b.w;
-}
-// 8 parameters from column c on, of a type known at run time.
-__device__ __forceinline__ void load8_param(const void* p, int32_t dtype, int32_t c, float (&v)[8]) {
-  if (dtype == MOE_DTYPE_BF16)
-    load8(static_cast<const uint16_t*>(p) + c, v);
-  else
-    load8(static_cast<const float*>(p) + c, v);
-}
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   uint4 d;
   d.x = pack2(v[0], v[1]);
@@ -58,10 +37,6 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   d.z = pack2(v[4], v[5]);
   d.w = pack2(v[6], v[7]);
   *reinterpret_cast<uint4*>(p) = d;
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 // Two fp32 values that one instruction works on.
