@@ -187,6 +187,8 @@ constexpr int32_t kSmallTokens = 2048, kSmallTokensWide = 512;  // max_rank up t
 // 16384 tokens, counting gains nothing (4314 32.8 / 31.7, 16384 75.5 / 74.5).
 constexpr int32_t kRankedTokens = 128;
 static_assert(kRankedTokens <= kLoraThreads, "one token a thread");
+// Batches without a workspace never reach a kernel that reads a plan from one (its pointers would be null).
+static_assert(kSmallTokensWide <= kSmallTokens, "lora_workspace is 0 bytes up to kSmallTokensWide");
 inline int32_t small_tokens(int32_t max_rank) { return max_rank <= 32 ? kSmallTokens : kSmallTokensWide; }
 
 // Set where a bounded wait ran out.
