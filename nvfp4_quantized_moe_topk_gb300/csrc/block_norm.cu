@@ -16,7 +16,7 @@
 // what its warp copied, so the copies need no barrier and no registers; the
 // weights stay in registers over all rows.  Measured on a GB300: 16384 rows of
 // 4096, fp32 residual, bf16 branch: 136 us, 5.9 TB/s (87 % of a copy's rate); 1536
-// threads an SM or two vectors a thread gain nothing.  One row of 2688: 2.9 us,
+// threads an SM or two vectors a thread gain nothing.  One row of 2688: 2.8 us,
 // latency of a launch, one load and two sums over the CTA (a kernel without
 // the ring, a CTA a row, takes as long, and with 304 rows of 8192 9.7 us
 // instead of 7.6, so there is none).

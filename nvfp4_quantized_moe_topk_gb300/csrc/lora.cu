@@ -9,7 +9,7 @@
 // (lora_rows.cu); here tiles are 16 tokens.  Both products are bf16 warp matrix
 // instructions with tokens as rows.  What bounds a call of few tokens is
 // latency: finding the tile, two chains of copies and a meeting of the cluster
-// between them (32 tokens, 2688 to 1856, ranks to 32: 6.7 us on a GB300, of which
+// between them (32 tokens, 2688 to 1856, ranks to 32: 6.4 us on a GB300, of which
 // the bytes are 0.5), so what counts is how many bytes are in flight at once.
 // Every thread
 // copies the 16-byte pieces of the operands that its own fragments are made of
@@ -177,10 +177,10 @@ __global__ void __launch_bounds__(kPlanThreads)
 // there the adapter's matrices are read less often, which counts the more the
 // larger the rank, but fewer CTAs share a small batch.  Tiles of 16 against
 // 128, us on a GB300:
-//   4096 to 4096, rank 16: 1024 tokens 13.2 / 21.0, 2048 21.6 / 26.8, 3000 37.5 / 29.8
-//   4096 to 1024, rank 32: 1024 10.8 / 19.5, 2048 15.1 / 19.5, 3000 23.6 / 21.3
-//   4096 to 4096, rank 64: 300 23.2 / 30.3, 640 35.4 / 31.4, 1536 50.8 / 33.8
-//   the same, rank 128: 300 31.9 / 41.0, 512 42.3 / 41.6, 768 52.5 / 43.3
+//   4096 to 4096, rank 16: 1024 tokens 13.4 / 24.5, 2048 21.6 / 28.6, 3000 33.9 / 31.9
+//   4096 to 1024, rank 32: 1024 10.8 / 19.3, 2048 15.0 / 19.7, 3000 23.4 / 21.1
+//   4096 to 4096, rank 64: 300 22.4 / 31.5, 512 25.1 / 31.6, 640 34.1 / 32.3, 1536 49.5 / 34.3
+//   the same, rank 128: 300 30.9 / 43.3, 512 40.8 / 43.9, 768 50.7 / 45.7
 constexpr int32_t kSmallTokens = 2048, kSmallTokensWide = 512;  // max_rank up to 32, above
 // Comparing against counting: 64 tokens 7.3 / 8.0 us, 128 8.1 / 8.1, 256 10.2 / 8.9; counting against a sorting
 // kernel before: 384 9.6 / 12.1, 1024 13.4 / 16.1 (4096 to 4096, rank 16, 16 adapters); in lora_mma.cu, with up to
@@ -524,7 +524,7 @@ size_t lora_workspace(int32_t n, int32_t n_adapters) {
 
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s) {
   const int32_t n = a.n, L = a.n_adapters;
-  const bool small = n <= small_tokens(a.max_rank), mma = !small && lora_mma_fits(a);
+  const bool small = n <= small_tokens(a.max_rank), mma = !small && lora_mma_takes(a);
   const int32_t mt = mma ? kMmaTokens : small ? 16 : kRowsTile;
   const LoraPlan p = small ? LoraPlan{} : lora_plan(workspace, n, L);
   if (!small) {

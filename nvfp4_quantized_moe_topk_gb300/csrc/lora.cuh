@@ -385,9 +385,10 @@ cudaError_t lora_cluster(void (*kernel)(KArgs...), int threads, size_t smem, int
   return cudaSuccess;
 }
 
-// lora_mma.cu: at most `tiles` tiles of kMmaTokens tokens; whether a call's sizes fit its shared memory.
+// lora_mma.cu: at most `tiles` tiles of kMmaTokens tokens; whether it takes a call's larger batches (lora_rows.cu the
+// others, with both sides measured there).
 constexpr int kMmaTokens = 128;
-bool lora_mma_fits(const moe_lora_args& a);
+bool lora_mma_takes(const moe_lora_args& a);
 cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s);
 
 // Reads and clears the flags of lora.cu's bounded waits.

@@ -10,8 +10,8 @@
 // one after the other; so two halves of the CTA (8 warps each) take alternate
 // steps with barriers, rings and accumulators of their own, and one half's
 // copies run beside the other's waits (16384 tokens, 4096 to 2048, rank 64,
-// bf16: 92 us with one half of 512 threads, 75 with two, of which the bytes are
-// 40; 3.7 TB/s).  Where there are fewer tiles than SMs, the CTAs of a cluster
+// bf16: 92 us with one half of 512 threads, 75 with two, and 76 since v has three
+// terms, of which the bytes are 40; 3.6 TB/s).  Where there are fewer tiles than SMs, the CTAs of a cluster
 // take turns with the steps of both products and add their D1 through each
 // other's shared memory (4096 tokens, 4096 to 4096, rank 64: 94 us with a CTA a
 // tile, 43 with three, 38 with four).
@@ -446,7 +446,7 @@ cudaError_t lora_mma_launch(const moe_lora_args& a, const LoraPlan& p, int32_t t
 
 }  // namespace
 
-bool lora_mma_fits(const moe_lora_args& a) { return a.max_rank <= 64 || a.out_dtype == MOE_DTYPE_BF16; }
+bool lora_mma_takes(const moe_lora_args& a) { return a.max_rank <= 64 || a.out_dtype == MOE_DTYPE_BF16; }
 
 cudaError_t launch_lora_mma(const moe_lora_args& a, const LoraPlan& p, int32_t tiles, int32_t expected, cudaStream_t s) {
   return a.max_rank <= 64 ? lora_mma_launch<1>(a, p, tiles, expected, s) : lora_mma_launch<2>(a, p, tiles, expected, s);

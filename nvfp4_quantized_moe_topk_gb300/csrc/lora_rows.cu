@@ -1,6 +1,5 @@
-// lora_rows.cu -- the adapters for many tokens where lora_mma.cu's operands do
-// not fit its shared memory (ranks above 64 with an fp32 out: three terms of v):
-// a CTA, or a cluster of CTAs, takes 64 tokens of one adapter through both
+// lora_rows.cu -- the adapters for many tokens of ranks above 64 with an fp32
+// out: a CTA, or a cluster of CTAs, takes 64 tokens of one adapter through both
 // products with warp matrix instructions.
 //
 // With 64 tokens a tile A and B are read once per 64 rows of x and y.  Warps
@@ -10,8 +9,10 @@
 // in shared memory, copied by all of them and met at one barrier a step; their
 // own tokens' 16-byte pieces of x (or y) go through thread-private slots of the
 // same ring steps.  Every 16 tokens reread A and B from shared memory, which at
-// these ranks is what bounds it: 4096 tokens, 4096 to 4096, rank 128 99 us with
-// a bf16 out, 16384 349 (lora_mma.cu: 47 and 121; the bytes are 15 and 60).
+// these ranks is what bounds it: 4096 tokens, 4096 to 4096, rank 128, fp32 y and
+// out 104 us, 16384 380 on a GB300 (the bytes are 27 and 102).  It is not the
+// faster way: lora_mma.cu, whose three terms of v fit beside two steps of 24 KB
+// here too, takes 74 and 186 in a trial, and is still to take this case over.
 //
 // Shared rows of A, B and v are read as 16 bytes by lane (row g, piece q); rows
 // whose pitch is a multiple of 128 bytes are stored with pieces 0-3 and 4-7

@@ -16,9 +16,9 @@
 // every run.  Batches that one block holds need no join: one launch.
 //
 // Measured on a GB300: loss of 16384 tokens, 128 experts, 7 sequences, two
-// launches 11.7 us (what it reads takes 1.3 at a copy's rate; latency: two
+// launches 11.4 us (what it reads takes 1.3 at a copy's rate; latency: two
 // launches, sequence lookup, a group's loads and softmax, the join; 4.2 us for 33
-// tokens in one launch); backward of 16384 tokens, 512 experts 20.3 us, of which 11
+// tokens in one launch); backward of 16384 tokens, 512 experts 21.2 us, of which 11
 // at 5.9 TB/s and the rest before the first logits and after the last; of 4314
 // tokens, 128 experts 7.9.
 //
