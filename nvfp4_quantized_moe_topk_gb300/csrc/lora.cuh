@@ -22,9 +22,9 @@ constexpr int kPlanSlice = kPlanThreads * kPlanPer;
 // against three, us on a GB300: 16384 tokens, 4096 to 2048, ranks to 64 74.5 / 76.1; 4096 to 4096, rank 128 121 / 130;
 // 32 tokens no difference.
 constexpr int kLoraTerms = 3;
-// Takes the next term off s; the result's upper 16 bits are it.  (Cut off, not rounded: a v above the largest bf16 would
-// round to infinity.  Of an infinity nothing is left, where a subtraction gives NaN; a NaN has bits in its upper half, as
-// every result of arithmetic has.)
+// Takes the next term off s; the result's upper 16 bits are it.  (Cut off, not rounded: a v above the largest bf16
+// would round to infinity.  Of an infinity nothing is left, where a subtraction gives NaN; a NaN has bits in its upper
+// half, as every result of arithmetic has.)
 __device__ __forceinline__ uint32_t take_term(float& s) {
   const uint32_t t = __float_as_uint(s) & 0xffff0000u;
   s = (t & 0x7fffffffu) == 0x7f800000u ? 0.f : s - __uint_as_float(t);

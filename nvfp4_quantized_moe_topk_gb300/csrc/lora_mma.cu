@@ -62,7 +62,7 @@ __device__ __forceinline__ bool half_or(int half, bool any) {
 __host__ __device__ inline int32_t block_columns(bool y_f32, bool out_f32) { return y_f32 || out_f32 ? 32 : 64; }
 // Bytes of a half's ring steps: x and A; y and B.
 __host__ __device__ inline uint32_t mma_step1(int32_t ranks16) { return kOperandTile + (uint32_t)ranks16 * 16 * 128; }
-__host__ __device__ inline uint32_t mma_step2(bool has_y, int32_t rank_blocks, int32_t columns) {
+__host__ __device__ constexpr uint32_t mma_step2(bool has_y, int32_t rank_blocks, int32_t columns) {
   return (has_y ? kOperandTile : 0) + (uint32_t)rank_blocks * columns * 128;
 }
 
@@ -72,9 +72,19 @@ __host__ __device__ inline bool out_over_y(const moe_lora_args& a, int rank_bloc
   return rank_blocks > 1 && a.y.data && a.y_dtype == MOE_DTYPE_BF16 && a.out_dtype == MOE_DTYPE_BF16;
 }
 // Bytes of the out blocks and v.
-__host__ __device__ inline uint32_t mma_fixed(bool over_y, int rank_blocks) {
+__host__ __device__ constexpr uint32_t mma_fixed(bool over_y, int rank_blocks) {
   return ((over_y ? 0u : 2u) + kLoraTerms * rank_blocks) * kOperandTile;
 }
+// Bytes of a half's ring in the second product.
+constexpr uint32_t mma_ring(bool over_y, int rank_blocks) {
+  return (kMmaSmem - 1024 - mma_fixed(over_y, rank_blocks)) / 2 / 1024 * 1024;
+}
+// (the waits are for all but the newest step; the sums of a cluster meet in the 64 KB before v)
+static_assert(mma_ring(false, 1) >= 2 * mma_step2(true, 1, 64) && mma_ring(true, 2) >= 2 * mma_step2(true, 2, 64) &&
+                  mma_ring(false, 2) >= 2 * mma_step2(true, 2, 32) && mma_ring(false, 2) >= 2 * mma_step2(false, 2, 64),
+              "two steps of the second product have to fit");
+static_assert(mma_ring(true, 2) >= 128 * kMmaTile * 4 && mma_ring(false, 2) + 2 * kOperandTile >= 128 * kMmaTile * 4,
+              "the sums of 128 ranks have to end before v");
 
 // RB: blocks of 64 ranks (1 or 2).
 template <int RB>
@@ -437,10 +447,8 @@ cudaError_t lora_mma_launch(const moe_lora_args& a, const LoraPlan& p, int32_t t
   const uint32_t step = std::max(mma_step1((a.max_rank + 15) / 16),
                                  mma_step2(a.y.data != nullptr, RB, block_columns(a.y_dtype == MOE_DTYPE_F32,
                                                                                   a.out_dtype == MOE_DTYPE_F32)));
-  // (two steps of the second product at least, and with RB 2 v from 64 KB on: 3 x 24 KB of 72; with RB 2 and out over y
-  // 2 x 32 of 64, else 2 x 24 of 48 before out blocks of 32)
-  const uint32_t rest = 1024 + mma_fixed(out_over_y(a, RB), RB);
-  const uint32_t ring = std::min((kMmaSmem - rest) / 2 / 1024 * 1024, kMmaMaxStages * step);
+  const bool over_y = out_over_y(a, RB);
+  const uint32_t rest = 1024 + mma_fixed(over_y, RB), ring = std::min(mma_ring(over_y, RB), kMmaMaxStages * step);
   return lora_launch_cluster(lora_mma_kernel<RB>, tiles, cluster, kMmaThreads, 2 * ring + rest, true, s, a, p, ring);
 }
 
