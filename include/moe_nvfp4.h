@@ -505,6 +505,81 @@ MOE_API size_t moe_lora_workspace_bytes(int32_t n, int32_t n_adapters);
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 MOE_API moe_status moe_lora_get_device_error(int32_t *flags);
 
+/* The norms of queries and keys for each head, with the rotation of their
+ * positions, in one call.  For every token t and head vector h of head_dim
+ * values:
+ *     y = h * r * (weight_offset + weight),  r = 1 / sqrt(mean(h^2) + eps)
+ *         (y = h where the side's weight is NULL)
+ * and the first rotary_dim values of y are rotated in pairs,
+ *     (a, b) -> rotary_scale * (a cos - b sin, b cos + a sin)
+ *     angle of pair i = positions[axis(i)][t] * inv_freq[i]
+ * the others stay.  Pair i is (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ * pairs_interleaved.  With several axes of positions (time, height, width of
+ * images and video) sections[j] pairs turn by axis j: the first sections[0]
+ * pairs by axis 0, the next by axis 1 and so on, or, with
+ * sections_interleaved, pair i by axis j = i mod n_axes while i / n_axes <
+ * sections[j], and by axis 0 after that.  The angle's product is exact to
+ * 2^-54 turns times the position, however far that is.  Statistics are held
+ * in fp32, each output is rounded once.  Infinities and NaN stay in their
+ * head; an inv_freq that is not finite gives an arbitrary rotation. */
+#define MOE_MAX_AXES 4
+typedef struct moe_qk_args {
+  int32_t n;                      /* tokens */
+  int32_t q_heads;                /* 0 without q */
+  int32_t k_heads;                /* 0 without k */
+  int32_t head_dim;               /* multiple of 8, at most 256 */
+  int32_t rotary_dim;             /* multiple of 16, at most head_dim; 0: no rotation */
+  int32_t n_axes;                 /* 1..MOE_MAX_AXES */
+  int32_t pairs_interleaved;      /* 0 or 1 */
+  int32_t sections_interleaved;   /* 0 or 1 */
+  int32_t sections[MOE_MAX_AXES]; /* n_axes of them, none negative, rotary_dim / 2 in all; not looked at with one axis */
+  int32_t dtype;                  /* MOE_DTYPE_ of q, k, their outputs and gradients */
+  int32_t param_dtype;            /* MOE_DTYPE_ of the weights */
+  float eps;                      /* > 0 */
+  float weight_offset;
+  float rotary_scale;             /* of the rotated values */
+  const int32_t *positions;       /* [n_axes][n], of any sign */
+  const float *inv_freq;          /* [rotary_dim / 2] */
+  const void *q_weight;           /* [head_dim] or NULL: no norm */
+  const void *k_weight;
+  moe_rows q;                     /* [n][q_heads * head_dim] */
+  moe_rows k;                     /* [n][k_heads * head_dim] */
+  moe_rows q_out;                 /* data may be q's (in place) where the strides are the same */
+  moe_rows k_out;
+} moe_qk_args;
+
+/* Enqueues the forward pass on `stream`; one launch, no workspace.
+ * Errors: MOE_ERR_INVALID_ARG (null, misaligned or missing pointer, negative
+ * n, bad enum value, sections that do not add up, eps not above zero, a
+ * stride below the row), MOE_ERR_UNSUPPORTED (head_dim, rotary_dim, more than
+ * 65536 heads), MOE_ERR_CUDA.  n = 0 enqueues nothing. */
+MOE_API moe_status moe_qk_norm_rope(const moe_qk_args *args, moe_stream_t stream);
+
+/* The backward pass, from q and k as they were before the forward (q_out and
+ * k_out are not looked at).  With g the gradient of a head's output, dy = g
+ * turned back (by -angle, times rotary_scale) and w = weight_offset + weight:
+ *     d_h      = r * (w * dy - h r * mean(w * dy * h r))     (dy without a norm)
+ *     d_weight = sum over tokens and heads of dy * h r
+ * The sums run in fp32 in a fixed order.  A NULL d_q_out or d_k_out is a zero
+ * gradient, whose side is left out: its other outputs are NULL too.  A NULL
+ * output is not computed.  d_q may be d_q_out and d_k may be d_k_out (in
+ * place) where the strides are the same. */
+typedef struct moe_qk_grads {
+  moe_rows d_q_out;  /* in */
+  moe_rows d_k_out;  /* in */
+  moe_rows d_q;      /* out */
+  moe_rows d_k;      /* out */
+  float *d_q_weight; /* out [head_dim] */
+  float *d_k_weight; /* out [head_dim] */
+} moe_qk_grads;
+
+/* Errors: as moe_qk_norm_rope, and MOE_ERR_CAPACITY (workspace too small; a
+ * call without d_q_weight and d_k_weight needs none).  n = 0 writes zeros to
+ * the gradients of the weights. */
+MOE_API moe_status moe_qk_norm_rope_backward(const moe_qk_args *args, const moe_qk_grads *grads, void *workspace,
+                                             size_t workspace_bytes, moe_stream_t stream);
+MOE_API size_t moe_qk_workspace_bytes(int32_t n, int32_t q_heads, int32_t k_heads, int32_t head_dim);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,7 +28,7 @@ ENTRY_POINTS = ("moe_nvfp4_status_string", "moe_nvfp4_create", "moe_nvfp4_destro
                 "moe_nvfp4_shared_expert_forward", "moe_nvfp4_debug_offset_grid_barrier", "moe_block_norm",
                 "moe_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_balance_loss", "moe_router_backward",
                 "moe_router_workspace_bytes", "moe_lora_apply", "moe_lora_workspace_bytes",
-                "moe_lora_get_device_error")
+                "moe_lora_get_device_error", "moe_qk_norm_rope", "moe_qk_norm_rope_backward", "moe_qk_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +102,9 @@ def load(build_if_missing: bool = False):
         L.moe_lora_apply.argtypes = [vp, vp, sz, vp]
         L.moe_lora_workspace_bytes.argtypes = [i32, i32]
         L.moe_lora_get_device_error.argtypes = [ctypes.POINTER(i32)]
+        L.moe_qk_norm_rope.argtypes = [vp, vp]
+        L.moe_qk_norm_rope_backward.argtypes = [vp, vp, vp, sz, vp]
+        L.moe_qk_workspace_bytes.argtypes = [i32, i32, i32, i32]
         for name in ENTRY_POINTS:
             if name.endswith("_workspace_bytes"):
                 getattr(L, name).restype = sz
@@ -411,3 +414,40 @@ def lora_device_error() -> int:
     f = ctypes.c_int32()
     _check(load().moe_lora_get_device_error(ctypes.byref(f)), "moe_lora_get_device_error")
     return f.value
+
+
+def qk_norm_rope(q, k, q_out, k_out, positions=None, inv_freq=None, q_weight=None, k_weight=None, *, eps: float = 1e-6,
+                 weight_offset: float = 0.0, rotary_scale: float = 1.0, sections=None,
+                 sections_interleaved: bool = False, pairs_interleaved: bool = False, stream=None):
+    """``moe_qk_norm_rope``: the norms of queries and keys for each head and the rotation of their positions, in one
+    pass.  q [n, heads, head_dim] and k [n, k_heads, head_dim] (either may be None) and their outputs are bf16 or fp32
+    (views into a projection's rows will do; an output may be its input), the weights [head_dim] (None: no norm).
+    inv_freq [rotary_dim / 2] fp32 and positions [n] or [axes, n] int32 (both None: no rotation); several axes turn
+    ``sections`` pairs each, one after another or, with ``sections_interleaved``, in turn."""
+    (_native or _binding()).qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, eps,
+                                         weight_offset, rotary_scale, sections, sections_interleaved,
+                                         pairs_interleaved, stream)
+    return q_out, k_out
+
+
+def qk_workspace(n: int, q_heads: int, k_heads: int, head_dim: int):
+    """A workspace for qk_norm_rope_backward of up to n tokens."""
+    return _new_workspace(load().moe_qk_workspace_bytes(n, q_heads, k_heads, head_dim))
+
+
+def qk_norm_rope_backward(d_q_out, d_k_out, q, k, d_q, d_k, positions=None, inv_freq=None, q_weight=None,
+                          k_weight=None, d_q_weight=None, d_k_weight=None, *, eps: float = 1e-6,
+                          weight_offset: float = 0.0, rotary_scale: float = 1.0, sections=None,
+                          sections_interleaved: bool = False, pairs_interleaved: bool = False, workspace=None,
+                          stream=None):
+    """``moe_qk_norm_rope_backward``: fills the given gradients from those of q_out and k_out (either may be None: its
+    side is left out).  q and k are the forward's inputs; a side without a norm does not need its own."""
+    native = _native or _binding()
+    if workspace is None and not (d_q_weight is None and d_k_weight is None):
+        lead = next((t for t in (d_q_out, d_k_out) if _on_gpu(t, 3)), None)
+        if lead is not None:
+            workspace = _new_workspace(_lib.moe_qk_workspace_bytes(lead.shape[0], 1, 1, lead.shape[2]), lead, stream)
+    native.qk_norm_rope_backward(d_q_out, d_k_out, q, k, d_q, d_k, positions, inv_freq, q_weight, k_weight, d_q_weight,
+                                 d_k_weight, eps, weight_offset, rotary_scale, sections, sections_interleaved,
+                                 pairs_interleaved, workspace, stream)
+    return d_q, d_k

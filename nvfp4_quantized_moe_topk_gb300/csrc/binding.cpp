@@ -338,6 +338,120 @@ PyObject* lora_apply(PyObject*, PyObject* const* p, Py_ssize_t count) {
   });
 }
 
+// n heads of [n, heads, dim] as rows: heads contiguous, tokens at any stride.
+moe_rows heads(const Call& c, const at::Tensor* t, const char* name, at::ScalarType want, int64_t n, int64_t count,
+               int64_t dim) {
+  if (!t) return {nullptr, 0};
+  c.type(*t, name, want);
+  if (t->dim() != 3 || t->size(0) != n || t->size(1) != count || t->size(2) != dim)
+    c.refuse(std::string(name) + " is " + shape_of(t->sizes()) + ", not " + shape_of({n, count, dim}));
+  if (t->is_contiguous()) return {t->data_ptr(), 0};
+  if ((dim > 1 && t->stride(2) != 1) || (count > 1 && t->stride(1) != dim) || (n > 1 && t->stride(0) < count * dim))
+    c.refuse(std::string(name) + " has strides " + shape_of(t->strides()) +
+             ": a token's heads must be contiguous and must not overlap");
+  return {t->data_ptr(), n > 1 ? t->stride(0) : 0};
+}
+
+// What both calls share.  q, k: the inputs, or the tensors that stand for their shapes.  scalars: eps, weight_offset,
+// rotary_scale, sections, sections_interleaved, pairs_interleaved.
+moe_qk_args qk_args(Call& c, const at::Tensor* q, const at::Tensor* k, PyObject* positions, PyObject* inv_freq,
+                    PyObject* q_weight, PyObject* k_weight, PyObject* const* scalars) {
+  const at::Tensor* lead = q ? q : k;
+  if (!lead || (q && q->dim() != 3) || (k && k->dim() != 3)) c.refuse("q and k are not [n, heads, head_dim] tensors");
+  c.lead(*lead);
+  moe_qk_args a = {};
+  a.n = c.i32(lead->size(0), "n");
+  a.head_dim = c.i32(lead->size(2), "head_dim");
+  a.q_heads = q ? c.i32(q->size(1), "q_heads") : 0;
+  a.k_heads = k ? c.i32(k->size(1), "k_heads") : 0;
+  a.dtype = c.dtype(*lead, q ? "q" : "k");
+  const at::Tensor *pos = c.tensor(positions, "positions"), *freq = c.tensor(inv_freq, "inv_freq"),
+                   *qw = c.tensor(q_weight, "q_weight"), *kw = c.tensor(k_weight, "k_weight");
+  if ((pos != nullptr) != (freq != nullptr)) c.refuse("positions and inv_freq go together");
+  a.n_axes = 1;
+  if (pos) {
+    if (freq->dim() != 1) c.refuse("inv_freq is not [rotary_dim / 2]");
+    a.rotary_dim = c.i32(2 * freq->size(0), "rotary_dim");
+    a.inv_freq = static_cast<float*>(c.array(freq, "inv_freq", at::kFloat, freq->sizes()));
+    if (pos->dim() == 2) a.n_axes = c.i32(pos->size(0), "axes");
+    if (pos->dim() == 2)
+      a.positions = static_cast<int32_t*>(c.array(pos, "positions", at::kInt, {a.n_axes, a.n}));
+    else
+      a.positions = static_cast<int32_t*>(c.array(pos, "positions", at::kInt, {a.n}));
+  }
+  if (scalars[3] != Py_None) {
+    PyObject* seq = PySequence_Fast(scalars[3], "sections is not a sequence");
+    if (!seq) throw Raised();
+    const Py_ssize_t len = PySequence_Fast_GET_SIZE(seq);
+    bool fits = len == a.n_axes && len <= MOE_MAX_AXES;
+    for (Py_ssize_t i = 0; fits && i < len; ++i) {
+      const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(seq, i));
+      if (v == -1 && PyErr_Occurred()) {
+        Py_DECREF(seq);
+        throw Raised();
+      }
+      fits = v >= 0 && v <= INT32_MAX;
+      a.sections[i] = (int32_t)v;
+    }
+    Py_DECREF(seq);
+    if (!fits) c.refuse("sections does not hold one number of pairs for each axis of positions");
+    if (pos && len == 1 && a.sections[0] != a.rotary_dim / 2) c.refuse("sections does not add up to the pairs");
+  } else if (a.n_axes > 1) {
+    c.refuse("several axes of positions need sections");
+  }
+  const at::Tensor* par = qw ? qw : kw;
+  a.param_dtype = par ? c.dtype(*par, "the weights") : MOE_DTYPE_F32;
+  a.q_weight = c.array(qw, "q_weight", scalar_type(a.param_dtype), {a.head_dim});
+  a.k_weight = c.array(kw, "k_weight", scalar_type(a.param_dtype), {a.head_dim});
+  a.eps = number(scalars[0]);
+  a.weight_offset = number(scalars[1]);
+  a.rotary_scale = number(scalars[2]);
+  a.sections_interleaved = truth(scalars[4]);
+  a.pairs_interleaved = truth(scalars[5]);
+  const at::ScalarType t = scalar_type(a.dtype);
+  a.q = heads(c, q, "q", t, a.n, a.q_heads, a.head_dim);
+  a.k = heads(c, k, "k", t, a.n, a.k_heads, a.head_dim);
+  return a;
+}
+
+// q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, eps, weight_offset, rotary_scale, sections,
+// sections_interleaved, pairs_interleaved, stream
+PyObject* qk_norm_rope(PyObject*, PyObject* const* p, Py_ssize_t count) {
+  return guarded(count, 15, [&] {
+    Call c{"moe_qk_norm_rope"};
+    moe_qk_args a = qk_args(c, c.tensor(p[0], "q"), c.tensor(p[1], "k"), p[4], p[5], p[6], p[7], p + 8);
+    const at::ScalarType t = scalar_type(a.dtype);
+    a.q_out = heads(c, c.tensor(p[2], "q_out"), "q_out", t, a.n, a.q_heads, a.head_dim);
+    a.k_out = heads(c, c.tensor(p[3], "k_out"), "k_out", t, a.n, a.k_heads, a.head_dim);
+    return c.done(moe_qk_norm_rope(&a, c.stream(p[14])));
+  });
+}
+
+// d_q_out, d_k_out, q, k, d_q, d_k, positions, inv_freq, q_weight, k_weight, d_q_weight, d_k_weight, eps,
+// weight_offset, rotary_scale, sections, sections_interleaved, pairs_interleaved, workspace, stream
+PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+  return guarded(count, 20, [&] {
+    Call c{"moe_qk_norm_rope_backward"};
+    const at::Tensor *dq = c.tensor(p[0], "d_q_out"), *dk = c.tensor(p[1], "d_k_out"), *q = c.tensor(p[2], "q"),
+                     *k = c.tensor(p[3], "k");
+    moe_qk_args a = qk_args(c, q ? q : dq, k ? k : dk, p[6], p[7], p[8], p[9], p + 12);
+    if (!q) a.q.data = nullptr;
+    if (!k) a.k.data = nullptr;
+    const at::ScalarType t = scalar_type(a.dtype);
+    moe_qk_grads d = {};
+    d.d_q_out = heads(c, dq, "d_q_out", t, a.n, a.q_heads, a.head_dim);
+    d.d_k_out = heads(c, dk, "d_k_out", t, a.n, a.k_heads, a.head_dim);
+    d.d_q = heads(c, c.tensor(p[4], "d_q"), "d_q", t, a.n, a.q_heads, a.head_dim);
+    d.d_k = heads(c, c.tensor(p[5], "d_k"), "d_k", t, a.n, a.k_heads, a.head_dim);
+    d.d_q_weight = static_cast<float*>(c.array(p[10], "d_q_weight", at::kFloat, {a.head_dim}));
+    d.d_k_weight = static_cast<float*>(c.array(p[11], "d_k_weight", at::kFloat, {a.head_dim}));
+    void* ws;
+    size_t bytes;
+    c.workspace(p[18], &ws, &bytes);
+    return c.done(moe_qk_norm_rope_backward(&a, &d, ws, bytes, c.stream(p[19])));
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XSETREF(g_error, cls);
@@ -351,6 +465,8 @@ PyMethodDef kMethods[] = {FAST(block_norm),
                           FAST(balance_loss),
                           FAST(router_backward),
                           FAST(lora_apply),
+                          FAST(qk_norm_rope),
+                          FAST(qk_norm_rope_backward),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "moe_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

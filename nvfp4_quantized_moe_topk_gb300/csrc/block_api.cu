@@ -59,6 +59,41 @@ moe_status check_router(const moe_router_args& a) {
   return MOE_OK;
 }
 
+constexpr int32_t kQkMaxHeads = 1 << 16;  // a row's elements stay below 2^31
+
+// One side's arrays: its heads, input and the array that goes with it in a call.
+bool qk_side_ok(const moe_qk_args& a, int32_t heads, const moe_rows& in, const moe_rows& other, const void* weight) {
+  const int64_t cols = (int64_t)heads * a.head_dim;
+  return rows_ok(in, cols, a.dtype) && rows_ok(other, cols, a.dtype) && aligned(weight, 4) &&
+         (heads > 0 || (!in.data && !other.data && !weight));
+}
+bool same_rows(const moe_rows& r, const moe_rows& o, int64_t cols) {
+  return (r.stride ? r.stride : cols) == (o.stride ? o.stride : cols);
+}
+
+moe_status check_qk(const moe_qk_args& a) {
+  if (a.n < 0 || a.q_heads < 0 || a.k_heads < 0 || a.q_heads + (int64_t)a.k_heads == 0 || a.head_dim <= 0 ||
+      a.rotary_dim < 0 || a.rotary_dim > a.head_dim)
+    return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(a.dtype) || !is_dtype(a.param_dtype) || a.n_axes < 1 || a.n_axes > MOE_MAX_AXES ||
+      (a.pairs_interleaved | a.sections_interleaved) & ~1)
+    return MOE_ERR_INVALID_ARG;
+  if (!(a.eps > 0.f)) return MOE_ERR_INVALID_ARG;
+  if (a.n_axes > 1 && a.rotary_dim > 0) {
+    int64_t pairs = 0;
+    for (int i = 0; i < a.n_axes; ++i) {
+      if (a.sections[i] < 0) return MOE_ERR_INVALID_ARG;
+      pairs += a.sections[i];
+    }
+    if (pairs != a.rotary_dim / 2) return MOE_ERR_INVALID_ARG;
+  }
+  if (a.head_dim % 8 || a.head_dim > kQkMaxDim || a.rotary_dim % 16 || a.q_heads > kQkMaxHeads || a.k_heads > kQkMaxHeads)
+    return MOE_ERR_UNSUPPORTED;
+  if (!aligned(a.positions, 4) || !aligned(a.inv_freq, 4)) return MOE_ERR_INVALID_ARG;
+  if (a.rotary_dim > 0 && (!a.inv_freq || (a.n > 0 && !a.positions))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -176,6 +211,58 @@ moe_status moe_lora_apply(const moe_lora_args* args, void* workspace, size_t wor
 moe_status moe_lora_get_device_error(int32_t* flags) {
   if (!flags) return MOE_ERR_INVALID_ARG;
   return status_of(lora_device_flags(flags));
+}
+
+moe_status moe_qk_norm_rope(const moe_qk_args* args, moe_stream_t stream) {
+  if (!args) return MOE_ERR_INVALID_ARG;
+  const moe_qk_args& a = *args;
+  const moe_status st = check_qk(a);
+  if (st != MOE_OK) return st;
+  if (!qk_side_ok(a, a.q_heads, a.q, a.q_out, a.q_weight) || !qk_side_ok(a, a.k_heads, a.k, a.k_out, a.k_weight))
+    return MOE_ERR_INVALID_ARG;
+  if (a.n == 0) return MOE_OK;
+  if ((a.q_heads && (!a.q.data || !a.q_out.data)) || (a.k_heads && (!a.k.data || !a.k_out.data)))
+    return MOE_ERR_INVALID_ARG;
+  if ((a.q_heads && a.q.data == a.q_out.data && !same_rows(a.q, a.q_out, (int64_t)a.q_heads * a.head_dim)) ||
+      (a.k_heads && a.k.data == a.k_out.data && !same_rows(a.k, a.k_out, (int64_t)a.k_heads * a.head_dim)))
+    return MOE_ERR_INVALID_ARG;
+  return status_of(launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_qk_workspace_bytes(int32_t n, int32_t q_heads, int32_t k_heads, int32_t head_dim) {
+  if (n < 0 || q_heads < 0 || k_heads < 0 || head_dim <= 0 || head_dim > kQkMaxDim) return 0;
+  return (size_t)(kQkBackwardCtas + 2) * (size_t)head_dim * sizeof(float);
+}
+
+moe_status moe_qk_norm_rope_backward(const moe_qk_args* args, const moe_qk_grads* grads, void* workspace,
+                                     size_t workspace_bytes, moe_stream_t stream) {
+  if (!args || !grads) return MOE_ERR_INVALID_ARG;
+  moe_qk_args a = *args;
+  const moe_qk_grads& d = *grads;
+  const moe_status st = check_qk(a);
+  if (st != MOE_OK) return st;
+  if (!qk_side_ok(a, a.q_heads, a.q, d.d_q_out, a.q_weight) || !qk_side_ok(a, a.k_heads, a.k, d.d_k_out, a.k_weight) ||
+      !qk_side_ok(a, a.q_heads, a.q, d.d_q, d.d_q_weight) || !qk_side_ok(a, a.k_heads, a.k, d.d_k, d.d_k_weight))
+    return MOE_ERR_INVALID_ARG;
+  if ((d.d_q_weight && !a.q_weight) || (d.d_k_weight && !a.k_weight)) return MOE_ERR_INVALID_ARG;
+  if (a.n > 0) {
+    if ((!d.d_q_out.data && (d.d_q.data || d.d_q_weight)) || (!d.d_k_out.data && (d.d_k.data || d.d_k_weight)))
+      return MOE_ERR_INVALID_ARG;
+    if ((d.d_q_out.data && a.q_weight && !a.q.data) || (d.d_k_out.data && a.k_weight && !a.k.data))
+      return MOE_ERR_INVALID_ARG;
+    if ((d.d_q.data && d.d_q.data == d.d_q_out.data && !same_rows(d.d_q, d.d_q_out, (int64_t)a.q_heads * a.head_dim)) ||
+        (d.d_k.data && d.d_k.data == d.d_k_out.data && !same_rows(d.d_k, d.d_k_out, (int64_t)a.k_heads * a.head_dim)))
+      return MOE_ERR_INVALID_ARG;
+    // a side without a gradient, or without anything to compute, is left out
+    if (!d.d_q.data && !d.d_q_weight) a.q_heads = 0;
+    if (!d.d_k.data && !d.d_k_weight) a.k_heads = 0;
+  }
+  if (!aligned(workspace, 16) || (!workspace && workspace_bytes)) return MOE_ERR_INVALID_ARG;
+  if (a.n > 0 && (d.d_q_weight || d.d_k_weight) &&
+      (!workspace || workspace_bytes < moe_qk_workspace_bytes(a.n, a.q_heads, a.k_heads, a.head_dim)))
+    return MOE_ERR_CAPACITY;
+  if (a.n > 0 && !a.q_heads && !a.k_heads) return MOE_OK;
+  return status_of(launch_qk_norm_rope_backward(a, d, static_cast<float*>(workspace), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

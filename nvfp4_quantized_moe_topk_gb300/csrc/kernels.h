@@ -242,6 +242,12 @@ size_t lora_workspace(int32_t n, int32_t n_adapters);  // bytes
 cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s);
 cudaError_t lora_device_flags(int32_t* flags);  // synchronizes the device; reads and clears
 
+constexpr int kQkMaxDim = 256;
+constexpr int kQkBackwardCtas = 608;  // CTAs of the backward pass, but for one a side at least
+cudaError_t launch_qk_norm_rope(const moe_qk_args& a, cudaStream_t s);
+// part: [kQkBackwardCtas + 2][head_dim] floats, where a weight's gradient is wanted.
+cudaError_t launch_qk_norm_rope_backward(const moe_qk_args& a, const moe_qk_grads& d, float* part, cudaStream_t s);
+
 // Host helpers for tensor maps (driver entry point resolved at run time).
 cudaError_t make_tmap_act(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K);
 cudaError_t make_tmap_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K);

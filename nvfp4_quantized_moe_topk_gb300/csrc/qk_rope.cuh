@@ -1,0 +1,169 @@
+// qk_rope.cuh -- what the forward and the backward pass of the queries' and
+// keys' norms with rotation share.
+//
+// A head vector of D elements is cut into units of 16, two vectors of 8: where
+// it is rotated, unit u holds pairs 8u .. 8u + 7, (vectors u and u + rot / 16
+// where a pair's members are half the rotated part apart, 2u and 2u + 1 where
+// they are side by side), so that no pair is split over lanes; past the rotated
+// part it holds vectors 2u and 2u + 1.  A lane takes one unit, GROUP lanes (a
+// power of two) a head.
+//
+// Angles: pair i of a token at position p turns by p * inv_freq[i].  In fp32 that
+// product is off by 2^-24 of itself, a whole turn's tenth for positions in the
+// millions; instead each frequency becomes a 64-bit fixed-point part of a turn
+// (rounded once from fp64), whose product with the position wraps at whole
+// turns by itself.  The result is within 2^-54 turns times the position of the
+// exact one: 2^-34 turns a million tokens in.
+#pragma once
+
+#include "block.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+constexpr int kQkThreads = 256, kQkWarps = kQkThreads / 32;
+constexpr int kQkMaxPairs = kQkMaxDim / 2;
+
+struct QkSide {  // the queries or the keys
+  moe_rows in, out;       // (backward: the forward's input; its gradient)
+  moe_rows grad;          // backward: gradient of the forward's output
+  const void* weight;     // [D] or NULL: no norm
+  int32_t heads;
+};
+struct QkParams {
+  int32_t n, D, rot, axes, pairs_interleaved, sections_interleaved, param_dtype;
+  int32_t sections[MOE_MAX_AXES];
+  float eps, offset, scale, inv_D;
+  const int32_t* positions;  // [axes][n]
+  const float* inv_freq;     // [rot / 2]
+  QkSide side[2];
+};
+
+// Which axis turns pair i.
+__device__ __forceinline__ int32_t axis_of_pair(const QkParams& a, int32_t i) {
+  int32_t axis = 0;
+  if (a.sections_interleaved) {
+    const int32_t turn = i % a.axes;
+    if (i / a.axes < a.sections[turn]) axis = turn;
+  } else {
+    for (int32_t end = a.sections[0]; axis + 1 < a.axes && i >= end; end += a.sections[axis]) ++axis;
+  }
+  return axis;
+}
+
+// A pair's step in turns, as 64-bit fixed point, and its axis.
+struct QkTable {
+  uint64_t step[kQkMaxPairs];
+  int32_t axis[kQkMaxPairs];
+};
+__device__ __forceinline__ void fill_table(const QkParams& a, QkTable& t) {
+  for (int32_t i = threadIdx.x; i < a.rot / 2; i += blockDim.x) {
+    double turns = (double)a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+    turns -= floor(turns);
+    t.step[i] = __double2ull_rn(turns * 18446744073709551616.0);
+    t.axis[i] = axis_of_pair(a, i);
+  }
+}
+// cos and sin of a token's pair, times the rotation's scale.
+__device__ __forceinline__ void turn_of(const QkParams& a, const QkTable& t, int32_t i, int32_t token, float& c, float& s) {
+  const int64_t p = a.positions[(int64_t)t.axis[i] * a.n + token];
+  // the upper 32 bits of the part of a turn, signed: half turns in [-1, 1)
+  const float half_turns = (float)(int32_t)(((uint64_t)p * t.step[i]) >> 32) * 0x1p-31f;
+  sincospif(half_turns, &s, &c);
+  c *= a.scale;
+  s *= a.scale;
+}
+
+// A lane's 16 elements: two vectors of 8 at element offsets at[0], at[1] (< 0: not there).
+struct QkUnit {
+  int32_t at[2];
+  bool rotated;
+};
+template <bool INTERLEAVED>
+__device__ __forceinline__ QkUnit unit_of(int32_t u, int32_t D, int32_t rot) {
+  QkUnit r;
+  r.rotated = 16 * u < rot;
+  const bool apart = !INTERLEAVED && r.rotated;
+  r.at[0] = apart ? 8 * u : 16 * u;
+  r.at[1] = apart ? rot / 2 + 8 * u : 16 * u + 8;
+  if (r.at[0] >= D) r.at[0] = -1;
+  if (r.at[1] >= D) r.at[1] = -1;
+  return r;
+}
+
+template <typename T>
+struct QkRaw {
+  uint4 v[2][sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ QkRaw<T> qk_load(const T* head, const QkUnit& u, bool live) {
+  QkRaw<T> r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < (int)sizeof(T) / 2; ++q) {
+      r.v[h][q] = make_uint4(0, 0, 0, 0);
+      if (live && u.at[h] >= 0) r.v[h][q] = *(reinterpret_cast<const uint4*>(head + u.at[h]) + q);
+    }
+  return r;
+}
+__device__ __forceinline__ void qk_values(const QkRaw<uint16_t>& r, float (&v)[2][8]) {
+  unpack8(r.v[0][0], v[0]);
+  unpack8(r.v[1][0], v[1]);
+}
+__device__ __forceinline__ void qk_values(const QkRaw<float>& r, float (&v)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      v[h][4 * q] = __uint_as_float(r.v[h][q].x);
+      v[h][4 * q + 1] = __uint_as_float(r.v[h][q].y);
+      v[h][4 * q + 2] = __uint_as_float(r.v[h][q].z);
+      v[h][4 * q + 3] = __uint_as_float(r.v[h][q].w);
+    }
+}
+__device__ __forceinline__ void qk_store(uint16_t* head, const QkUnit& u, const float (&v)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (u.at[h] >= 0) store8(head + u.at[h], v[h]);
+}
+__device__ __forceinline__ void qk_store(float* head, const QkUnit& u, const float (&v)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (u.at[h] >= 0) {
+      *reinterpret_cast<float4*>(head + u.at[h]) = make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
+      *reinterpret_cast<float4*>(head + u.at[h] + 4) = make_float4(v[h][4], v[h][5], v[h][6], v[h][7]);
+    }
+}
+// offset + weight of the lane's elements (0 where it has none).
+__device__ __forceinline__ void qk_weight(const QkParams& a, const void* w, const QkUnit& u, float (&v)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[h][j] = 0.f;
+      if (u.at[h] >= 0)
+        v[h][j] = a.offset + (a.param_dtype == MOE_DTYPE_BF16 ? bf16lo(static_cast<const uint16_t*>(w)[u.at[h] + j])
+                                                              : static_cast<const float*>(w)[u.at[h] + j]);
+    }
+}
+// (a, b) -> (a c - b s, b c + a s) of the lane's eight pairs; sign -1: the inverse.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void qk_turn(float (&v)[2][8], const float (&c)[8], const float (&s)[8], float sign) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float& x = INTERLEAVED ? v[j / 4][2 * (j % 4)] : v[0][j];
+    float& y = INTERLEAVED ? v[j / 4][2 * (j % 4) + 1] : v[1][j];
+    const float sj = sign * s[j], t = x * c[j] - y * sj;
+    y = y * c[j] + x * sj;
+    x = t;
+  }
+}
+template <int GROUP>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int off = GROUP / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+}  // namespace moe
