@@ -505,6 +505,76 @@ MOE_API size_t moe_lora_workspace_bytes(int32_t n, int32_t n_adapters);
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 MOE_API moe_status moe_lora_get_device_error(int32_t *flags);
 
+/* A projection: a matrix product with bias, activation and residual in its
+ * epilogue,
+ *     z[t][o]   = sum_c x[t][c] * weight[o][c] + bias[o]
+ *     out[t][o] = act(z[t][o]) + residual_scale * residual[t][o]
+ * Products of bf16 are exact and summed in fp32; the activation is taken of
+ * the fp32 z, each output is rounded once.  z itself can be kept for the
+ * backward pass.  With an fp32 out and nothing else it gives a router's
+ * logits, or the shared projection's y of moe_lora_apply.  Infinities and NaN
+ * in x stay in their token's row, those of weight in their column. */
+#define MOE_LINEAR_NONE 0      /* z */
+#define MOE_LINEAR_RELU2 1     /* max(z, 0)^2 */
+#define MOE_LINEAR_SILU 2      /* z / (1 + exp(-z)) */
+#define MOE_LINEAR_GELU_TANH 3 /* z / 2 * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) */
+typedef struct moe_linear_args {
+  int32_t n;              /* tokens */
+  int32_t in_features;    /* multiple of 8, at most 2^24 */
+  int32_t out_features;   /* multiple of 8, at most 2^24 */
+  int32_t activation;     /* MOE_LINEAR_ */
+  int32_t bias_dtype;     /* MOE_DTYPE_ of bias */
+  int32_t residual_dtype; /* of residual */
+  int32_t z_dtype;        /* of z */
+  int32_t out_dtype;      /* of out */
+  float residual_scale;
+  const uint16_t *weight; /* bf16 [out_features][in_features] */
+  const void *bias;       /* [out_features] or NULL */
+  moe_rows x;             /* bf16 [n][in_features] */
+  moe_rows residual;      /* [n][out_features]; data may be NULL */
+  moe_rows z;             /* [n][out_features]; data may be NULL: not kept */
+  moe_rows out;           /* [n][out_features]; data may be residual's where the types and strides are the same */
+} moe_linear_args;
+
+/* Enqueues the product on `stream`; one launch, no workspace.  Errors:
+ * MOE_ERR_INVALID_ARG (null, misaligned or missing pointer, negative n, bad
+ * enum value, a stride below the row), MOE_ERR_UNSUPPORTED (sizes outside the
+ * above), MOE_ERR_CUDA.  n = 0 enqueues nothing. */
+MOE_API moe_status moe_linear(const moe_linear_args *args, moe_stream_t stream);
+
+/* The backward pass.  With dz = d_out * act'(z), z as moe_linear kept it (not
+ * looked at without an activation),
+ *     d_x[t][c]      = sum_o dz[t][o] * weight[o][c]
+ *     d_weight[o][c] = sum_t dz[t][o] * x[t][c]
+ *     d_bias[o]      = sum_t dz[t][o]
+ * (the gradient of the residual is residual_scale * d_out).  args' bias,
+ * residual and out are not looked at.  A gradient in bf16 is summed from dz
+ * rounded to bf16, one in fp32 from dz with its 24 bits; where d_out is bf16
+ * and there is no activation dz is d_out, exactly.  The sums run in a fixed
+ * order.  A NULL output is not computed; x is needed for d_weight, weight for
+ * d_x. */
+typedef struct moe_linear_grads {
+  int32_t d_out_dtype;    /* MOE_DTYPE_ of d_out */
+  int32_t d_x_dtype;      /* of d_x */
+  int32_t d_weight_dtype; /* of d_weight */
+  moe_rows d_out;         /* in [n][out_features] */
+  moe_rows d_x;           /* out [n][in_features] */
+  void *d_weight;         /* out [out_features][in_features] */
+  float *d_bias;          /* out [out_features] */
+} moe_linear_grads;
+
+/* Errors: as moe_linear, and MOE_ERR_CAPACITY (workspace too small).  n = 0
+ * writes zeros to d_weight and d_bias. */
+MOE_API moe_status moe_linear_backward(const moe_linear_args *args, const moe_linear_grads *grads, void *workspace,
+                                       size_t workspace_bytes, moe_stream_t stream);
+MOE_API size_t moe_linear_workspace_bytes(int32_t n, int32_t in_features, int32_t out_features);
+
+/* Reads and clears the current device's error flags of moe_linear and
+ * moe_linear_backward: 0, or MOE_DEVFLAG_TIMEOUT where a bounded wait inside
+ * their kernels ran out (that call's outputs are then undefined).
+ * Synchronizes the device.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+MOE_API moe_status moe_linear_get_device_error(int32_t *flags);
+
 /* The norms of queries and keys for each head, with the rotation of their
  * positions, in one call.  For every token t and head vector h of head_dim
  * values:

@@ -28,7 +28,8 @@ ENTRY_POINTS = ("moe_nvfp4_status_string", "moe_nvfp4_create", "moe_nvfp4_destro
                 "moe_nvfp4_shared_expert_forward", "moe_nvfp4_debug_offset_grid_barrier", "moe_block_norm",
                 "moe_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_balance_loss", "moe_router_backward",
                 "moe_router_workspace_bytes", "moe_lora_apply", "moe_lora_workspace_bytes",
-                "moe_lora_get_device_error", "moe_qk_norm_rope", "moe_qk_norm_rope_backward", "moe_qk_workspace_bytes")
+                "moe_lora_get_device_error", "moe_qk_norm_rope", "moe_qk_norm_rope_backward", "moe_qk_workspace_bytes",
+                "moe_linear", "moe_linear_backward", "moe_linear_workspace_bytes", "moe_linear_get_device_error")
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +103,10 @@ def load(build_if_missing: bool = False):
         L.moe_lora_apply.argtypes = [vp, vp, sz, vp]
         L.moe_lora_workspace_bytes.argtypes = [i32, i32]
         L.moe_lora_get_device_error.argtypes = [ctypes.POINTER(i32)]
+        L.moe_linear.argtypes = [vp, vp]
+        L.moe_linear_backward.argtypes = [vp, vp, vp, sz, vp]
+        L.moe_linear_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_linear_get_device_error.argtypes = [ctypes.POINTER(i32)]
         L.moe_qk_norm_rope.argtypes = [vp, vp]
         L.moe_qk_norm_rope_backward.argtypes = [vp, vp, vp, sz, vp]
         L.moe_qk_workspace_bytes.argtypes = [i32, i32, i32, i32]
@@ -413,6 +418,52 @@ def lora_device_error() -> int:
     """Reads and clears lora_apply's device error flags (DEVFLAG_TIMEOUT); synchronizes the device."""
     f = ctypes.c_int32()
     _check(load().moe_lora_get_device_error(ctypes.byref(f)), "moe_lora_get_device_error")
+    return f.value
+
+
+ACTIVATIONS = {"none": 0, "relu2": 1, "silu": 2, "gelu_tanh": 3}
+
+
+def _activation(name, where: str) -> int:
+    if not isinstance(name, str) or name not in ACTIVATIONS:
+        raise MoeError(1, where, f"activation {name!r} is none of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def linear(x, weight, out, bias=None, residual=None, z_out=None, *, activation: str = "none",
+           residual_scale: float = 1.0, stream=None):
+    """``moe_linear``: out = act(x weight^T + bias) + residual_scale * residual.  x [n, in] and weight [out, in] bf16,
+    out [n, out], residual [n, out] (may be out) and bias [out] bf16 or fp32; ``z_out`` [n, out] keeps the activation's
+    argument for linear_backward; activation "none", "relu2", "silu" or "gelu_tanh"."""
+    (_native or _binding()).linear(x, weight, out, bias, residual, z_out, _activation(activation, "moe_linear"),
+                                   residual_scale, stream)
+    return out
+
+
+def linear_workspace(n: int, in_features: int, out_features: int):
+    """A workspace for linear_backward of up to n tokens."""
+    return _new_workspace(load().moe_linear_workspace_bytes(n, in_features, out_features))
+
+
+def linear_backward(d_out, x, weight, z=None, d_x=None, d_weight=None, d_bias=None, *, activation: str = "none",
+                    workspace=None, stream=None):
+    """``moe_linear_backward``: fills the given gradients from d_out [n, out] (bf16 or fp32).  z is what linear kept
+    (needed with an activation); d_x [n, in] and d_weight [out, in] are bf16 or fp32, d_bias [out] fp32.  The gradient
+    of the residual is residual_scale * d_out."""
+    native = _native or _binding()
+    if workspace is None and _on_gpu(d_out, 2) and _on_gpu(weight, 2):
+        workspace = _new_workspace(_lib.moe_linear_workspace_bytes(d_out.shape[0], *reversed(weight.shape)), d_out,
+                                   stream)
+    native.linear_backward(d_out, x, weight, z, d_x, d_weight, d_bias, _activation(activation, "moe_linear_backward"),
+                           workspace, stream)
+    return d_x, d_weight, d_bias
+
+
+def linear_device_error() -> int:
+    """Reads and clears the device error flags of linear and linear_backward (DEVFLAG_TIMEOUT); synchronizes the
+    device."""
+    f = ctypes.c_int32()
+    _check(load().moe_linear_get_device_error(ctypes.byref(f)), "moe_linear_get_device_error")
     return f.value
 
 

@@ -452,6 +452,66 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* p, Py_ssize_t count)
   });
 }
 
+// What both projection calls share: sizes, weight, x, z and the activation.
+moe_linear_args linear_args(Call& c, const at::Tensor* lead, const at::Tensor* x, const at::Tensor* w,
+                            const at::Tensor* z, PyObject* activation) {
+  if (!lead || lead->dim() != 2 || !w || w->dim() != 2) c.refuse("no [n, features] tensor, or weight is not [out, in]");
+  c.lead(*lead);
+  moe_linear_args a = {};
+  a.n = c.i32(lead->size(0), "n");
+  a.in_features = c.i32(w->size(1), "in");
+  a.out_features = c.i32(w->size(0), "out");
+  const long act = PyLong_AsLong(activation);
+  if (act == -1 && PyErr_Occurred()) throw Raised();
+  a.activation = (int32_t)act;
+  a.weight = static_cast<uint16_t*>(c.array(w, "weight", at::kBFloat16, w->sizes()));
+  a.x = c.rows(x, "x", at::kBFloat16, a.n, a.in_features);
+  a.z_dtype = z ? c.dtype(*z, "z") : MOE_DTYPE_BF16;
+  a.z = c.rows(z, "z", scalar_type(a.z_dtype), a.n, a.out_features);
+  return a;
+}
+
+// x, weight, out, bias, residual, z_out, activation, residual_scale, stream
+PyObject* linear(PyObject*, PyObject* const* p, Py_ssize_t count) {
+  return guarded(count, 9, [&] {
+    Call c{"moe_linear"};
+    const at::Tensor *x = c.tensor(p[0], "x"), *out = c.tensor(p[2], "out"), *bias = c.tensor(p[3], "bias"),
+                     *res = c.tensor(p[4], "residual");
+    moe_linear_args a = linear_args(c, x, x, c.tensor(p[1], "weight"), c.tensor(p[5], "z_out"), p[6]);
+    if (!out) c.refuse("out is missing");
+    a.out_dtype = c.dtype(*out, "out");
+    a.out = c.rows(out, "out", scalar_type(a.out_dtype), a.n, a.out_features);
+    a.bias_dtype = bias ? c.dtype(*bias, "bias") : MOE_DTYPE_F32;
+    a.bias = c.array(bias, "bias", scalar_type(a.bias_dtype), {a.out_features});
+    a.residual_dtype = res ? c.dtype(*res, "residual") : MOE_DTYPE_BF16;
+    a.residual = c.rows(res, "residual", scalar_type(a.residual_dtype), a.n, a.out_features);
+    a.residual_scale = number(p[7]);
+    return c.done(moe_linear(&a, c.stream(p[8])));
+  });
+}
+
+// d_out, x, weight, z, d_x, d_weight, d_bias, activation, workspace, stream
+PyObject* linear_backward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+  return guarded(count, 10, [&] {
+    Call c{"moe_linear_backward"};
+    const at::Tensor *dy = c.tensor(p[0], "d_out"), *x = c.tensor(p[1], "x"), *w = c.tensor(p[2], "weight"),
+                     *z = c.tensor(p[3], "z"), *dx = c.tensor(p[4], "d_x"), *dw = c.tensor(p[5], "d_weight");
+    moe_linear_args a = linear_args(c, dy, x, w, z, p[7]);
+    moe_linear_grads d = {};
+    d.d_out_dtype = c.dtype(*dy, "d_out");
+    d.d_x_dtype = dx ? c.dtype(*dx, "d_x") : MOE_DTYPE_BF16;
+    d.d_weight_dtype = dw ? c.dtype(*dw, "d_weight") : MOE_DTYPE_BF16;
+    d.d_out = c.rows(dy, "d_out", scalar_type(d.d_out_dtype), a.n, a.out_features);
+    d.d_x = c.rows(dx, "d_x", scalar_type(d.d_x_dtype), a.n, a.in_features);
+    d.d_weight = c.array(dw, "d_weight", scalar_type(d.d_weight_dtype), {a.out_features, a.in_features});
+    d.d_bias = static_cast<float*>(c.array(p[6], "d_bias", at::kFloat, {a.out_features}));
+    void* ws;
+    size_t bytes;
+    c.workspace(p[8], &ws, &bytes);
+    return c.done(moe_linear_backward(&a, &d, ws, bytes, c.stream(p[9])));
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XSETREF(g_error, cls);
@@ -465,6 +525,8 @@ PyMethodDef kMethods[] = {FAST(block_norm),
                           FAST(balance_loss),
                           FAST(router_backward),
                           FAST(lora_apply),
+                          FAST(linear),
+                          FAST(linear_backward),
                           FAST(qk_norm_rope),
                           FAST(qk_norm_rope_backward),
                           {"set_error", set_error, METH_O, nullptr},

@@ -94,6 +94,18 @@ moe_status check_qk(const moe_qk_args& a) {
   return MOE_OK;
 }
 
+moe_status check_linear(const moe_linear_args& a) {
+  if (a.n < 0 || a.in_features <= 0 || a.out_features <= 0) return MOE_ERR_INVALID_ARG;
+  if (a.activation < MOE_LINEAR_NONE || a.activation > MOE_LINEAR_GELU_TANH || !is_dtype(a.bias_dtype) ||
+      !is_dtype(a.residual_dtype) || !is_dtype(a.z_dtype) || !is_dtype(a.out_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (a.in_features % 8 || a.out_features % 8 || a.in_features > kLinearMaxFeatures || a.out_features > kLinearMaxFeatures)
+    return MOE_ERR_UNSUPPORTED;
+  if (!rows_ok(a.x, a.in_features, MOE_DTYPE_BF16) || !rows_ok(a.z, a.out_features, a.z_dtype) || !aligned(a.weight, 16))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -263,6 +275,52 @@ moe_status moe_qk_norm_rope_backward(const moe_qk_args* args, const moe_qk_grads
     return MOE_ERR_CAPACITY;
   if (a.n > 0 && !a.q_heads && !a.k_heads) return MOE_OK;
   return status_of(launch_qk_norm_rope_backward(a, d, static_cast<float*>(workspace), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear(const moe_linear_args* args, moe_stream_t stream) {
+  if (!args) return MOE_ERR_INVALID_ARG;
+  const moe_linear_args& a = *args;
+  const moe_status st = check_linear(a);
+  if (st != MOE_OK) return st;
+  if (!rows_ok(a.residual, a.out_features, a.residual_dtype) || !rows_ok(a.out, a.out_features, a.out_dtype) ||
+      !aligned(a.bias, a.bias_dtype == MOE_DTYPE_F32 ? 4 : 2))
+    return MOE_ERR_INVALID_ARG;
+  if (a.n == 0) return MOE_OK;
+  if (!a.x.data || !a.weight || !a.out.data || a.z.data == a.out.data) return MOE_ERR_INVALID_ARG;
+  if (a.residual.data == a.out.data &&
+      (a.residual_dtype != a.out_dtype || !same_rows(a.residual, a.out, a.out_features)))
+    return MOE_ERR_INVALID_ARG;
+  return status_of(launch_linear(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_linear_workspace_bytes(int32_t n, int32_t in_features, int32_t out_features) {
+  if (n < 0 || in_features <= 0 || out_features <= 0) return 0;
+  return linear_workspace(n, in_features, out_features);
+}
+
+moe_status moe_linear_backward(const moe_linear_args* args, const moe_linear_grads* grads, void* workspace,
+                               size_t workspace_bytes, moe_stream_t stream) {
+  if (!args || !grads) return MOE_ERR_INVALID_ARG;
+  const moe_linear_args& a = *args;
+  const moe_linear_grads& d = *grads;
+  const moe_status st = check_linear(a);
+  if (st != MOE_OK) return st;
+  if (!is_dtype(d.d_out_dtype) || !is_dtype(d.d_x_dtype) || !is_dtype(d.d_weight_dtype)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(d.d_out, a.out_features, d.d_out_dtype) || !rows_ok(d.d_x, a.in_features, d.d_x_dtype) ||
+      !aligned(d.d_weight, 16) || !aligned(d.d_bias, 4) || !aligned(workspace, 16) || (!workspace && workspace_bytes))
+    return MOE_ERR_INVALID_ARG;
+  if (a.n > 0) {
+    if (!d.d_out.data || (a.activation != MOE_LINEAR_NONE && !a.z.data) || (d.d_weight && !a.x.data) ||
+        (d.d_x.data && !a.weight))
+      return MOE_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < linear_workspace(a.n, a.in_features, a.out_features)) return MOE_ERR_CAPACITY;
+  }
+  return status_of(launch_linear_backward(a, d, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear_get_device_error(int32_t* flags) {
+  if (!flags) return MOE_ERR_INVALID_ARG;
+  return status_of(linear_device_flags(flags));
 }
 
 }  // extern "C"

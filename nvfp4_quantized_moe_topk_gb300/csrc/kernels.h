@@ -248,9 +248,19 @@ cudaError_t launch_qk_norm_rope(const moe_qk_args& a, cudaStream_t s);
 // part: [kQkBackwardCtas + 2][head_dim] floats, where a weight's gradient is wanted.
 cudaError_t launch_qk_norm_rope_backward(const moe_qk_args& a, const moe_qk_grads& d, float* part, cudaStream_t s);
 
+constexpr int32_t kLinearMaxFeatures = 1 << 24;
+size_t linear_workspace(int32_t n, int32_t in, int32_t out);  // bytes, of the backward pass
+cudaError_t launch_linear(const moe_linear_args& a, cudaStream_t s);
+cudaError_t launch_linear_backward(const moe_linear_args& a, const moe_linear_grads& d, void* workspace, cudaStream_t s);
+cudaError_t linear_device_flags(int32_t* flags);  // synchronizes the device; reads and clears
+
 // Host helpers for tensor maps (driver entry point resolved at run time).
 cudaError_t make_tmap_act(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K);
 cudaError_t make_tmap_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K);
+// A bf16 matrix [outer][inner], rows `stride` elements apart, in boxes of box_inner (64) by box_outer (up to 256), 128-byte
+// swizzle; what lies outside reads as zero.
+cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t stride,
+                           uint32_t box_inner, uint32_t box_outer);
 
 // Launch with the programmatic-stream-serialization attribute when pdl is set.
 template <typename... KArgs, typename... Args>

@@ -1,0 +1,43 @@
+// linear_act.cuh -- the activations of the matrix product's epilogue and their slopes.
+#pragma once
+
+#include "../../include/moe_nvfp4.h"
+#include "common.cuh"
+
+namespace moe {
+
+// 1 / (1 + exp(-v)), 0 and 1 where the exponential overflows or vanishes.
+__device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + __expf(-v)); }
+
+// gelu_tanh: z / 2 (1 + tanh(u)) = z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
+constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluCube = 0.044715f;
+
+__device__ __forceinline__ float linear_act(float z, int32_t act) {
+  switch (act) {
+    case MOE_LINEAR_RELU2: {
+      const float r = z > 0.f ? z : z == z ? 0.f : z;
+      return r * r;
+    }
+    case MOE_LINEAR_SILU: return z * logistic(z);
+    case MOE_LINEAR_GELU_TANH: return z * logistic(kGelu * z * fmaf(kGeluCube * z, z, 1.f));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float linear_slope(float z, int32_t act) {
+  switch (act) {
+    case MOE_LINEAR_RELU2: return z > 0.f ? 2.f * z : z == z ? 0.f : z;
+    case MOE_LINEAR_SILU: {
+      const float p = logistic(z);
+      return p * fmaf(z, 1.f - p, 1.f);
+    }
+    case MOE_LINEAR_GELU_TANH: {
+      const float p = logistic(kGelu * z * fmaf(kGeluCube * z, z, 1.f));
+      z = fminf(fmaxf(z, -1e4f), 1e4f);  // (1 - p or p is 0 long before; the square does not overflow)
+      return fmaf(z * p * (1.f - p), kGelu * fmaf(3.f * kGeluCube * z, z, 1.f), p);
+    }
+    default: return 1.f;
+  }
+}
+
+}  // namespace moe

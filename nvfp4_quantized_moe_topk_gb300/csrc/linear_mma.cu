@@ -1,0 +1,482 @@
+// linear_mma.cu -- matrix products of bf16 with an epilogue, on the tensor cores'
+// asynchronous path (tcgen05, operands by TMA, accumulators in tensor memory).
+//
+// The features (a weight's rows) are the instruction's M and the rows of x its
+// N, so that one kernel serves a single token (N = 16: the weights stream
+// through) and thousands (N = 256), and a warp of the epilogue, whose lanes hold
+// consecutive features of one row, reads and writes whole sectors without a
+// turn through shared memory.
+//
+// Large products: a pair of CTAs (cta_group::2) shares an instruction of 256
+// features, each holding its own features and half of the rows; a persistent
+// grid takes the tiles in an order that keeps a few rows' and all weights' tiles
+// in L2, and two accumulators let a tile's epilogue run beside the next tile's
+// products.  Small ones: a CTA a tile of 128 features; where there are fewer
+// tiles than SMs, the CTAs of a cluster split the columns and add their sums
+// through each other's shared memory, in order.
+#include <algorithm>
+
+#include "block.cuh"
+#include "linear_act.cuh"
+#include "linear_mma.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 384, kEpilogueWarps = 8;  // warp 0: copies, 1: products, 2: tensor memory, 4..11: epilogue
+constexpr int kMaxStages = 8;
+constexpr uint32_t kSmem = 227 * 1024, kBarBytes = 1024;
+constexpr uint32_t kPBytes = 128 * 128;  // a stage's features: 128 of 64 columns
+constexpr int kMaxSplit = 8;
+
+// Set where a bounded wait ran out; read by moe_linear_get_device_error.
+__device__ int32_t g_linear_flags;
+
+struct Plan {
+  int32_t R, F, KB, terms;    // KB: blocks of 64 columns; terms: of q
+  int32_t rows;               // of a tile: the instruction's N
+  int32_t tiles_r, tiles, group;
+  int32_t split, stages;
+  uint32_t stage_bytes;
+  LinearFinish e;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 peer_float4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait that also gives up when another role of the CTA has.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+  if (try_wait_cluster(bar, parity, 0)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 8; ++i)
+      if (try_wait_cluster(bar, parity, 1000u)) return true;
+    if (*gave_up) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *gave_up = 1;
+      atomicOr(&g_linear_flags, kFlagTimeout);
+      return false;
+    }
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  if (CG == 2)  // the barrier is the pair's first CTA's
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    tc_mma_bf16(d, a, b, idesc, accumulate);
+}
+// Arrives on the barrier of each CTA of the pair once the products issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc_commit(bar);
+}
+template <int CG>
+__device__ __forceinline__ void tmem_allocate(uint32_t* slot, uint32_t cols) {
+  if (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(slot, cols);
+    tmem_relinquish();
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  else
+    tmem_dealloc(addr, cols);
+}
+// Descriptor of an operand with its M or N side contiguous: blocks of 64 (128 bytes) by 64 columns, 8 KB each, 128-byte
+// swizzle; the leading offset goes from block to block, the stride offset from one group of 8 columns to the next.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(8192u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+struct Maps {
+  CUtensorMap p, q[kLinearTerms];
+};
+
+struct Tile {
+  int32_t f0, r0;
+};
+// Tiles in bands of `group` row tiles, within a band all row tiles of one feature tile side by side.
+__device__ __forceinline__ Tile tile_at(const Plan& p, int32_t t, int32_t feats) {
+  const int32_t tiles_f = p.tiles / p.tiles_r, band = t / (p.group * tiles_f), in = t - band * p.group * tiles_f;
+  const int32_t high = min(p.group, p.tiles_r - band * p.group);
+  return {in / high * feats, (band * p.group + in % high) * p.rows};
+}
+
+__device__ __forceinline__ float read_value(const void* p, int64_t at, int32_t f32) {
+  return f32 ? static_cast<const float*>(p)[at] : bf16lo(static_cast<const uint16_t*>(p)[at]);
+}
+__device__ __forceinline__ void write_value(void* p, int64_t at, int32_t f32, float v) {
+  if (f32)
+    static_cast<float*>(p)[at] = v;
+  else
+    static_cast<uint16_t*>(p)[at] = f2bf_rn(v);
+}
+
+// The sums of feature f in 16 rows from r0 on (as many as there are).
+__device__ __forceinline__ void finish16(const Plan& p, const uint32_t (&d)[16], int32_t r0, int32_t f, float bias) {
+  const LinearFinish& e = p.e;
+  const int32_t rows = min(16, p.R - r0);
+  float res[16];
+  if (e.residual) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      res[i] = i < rows ? read_value(e.residual, (int64_t)(r0 + i) * e.residual_stride + f, e.residual_f32) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (i >= rows) break;
+    const float z = __uint_as_float(d[i]) + bias;
+    if (e.z) write_value(e.z, (int64_t)(r0 + i) * e.z_stride + f, e.z_f32, z);
+    float v = linear_act(z, e.act);
+    if (e.residual) v = fmaf(e.scale, res[i], v);
+    write_value(e.out, (int64_t)(r0 + i) * e.out_stride + f, e.out_f32, v);
+  }
+}
+
+template <int CG, bool P_MN, bool Q_MN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], t_full[2], t_empty[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int gave_up;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank(), cta = CG == 2 ? rank : 0, part = CG == 2 ? 0 : rank;
+  const int32_t units = CG == 2 ? gridDim.x / 2 : gridDim.x / p.split, unit = CG == 2 ? blockIdx.x / 2 : blockIdx.x / p.split;
+  const uint32_t cols = p.rows <= 16 ? 32 : p.rows <= 32 ? 64 : p.rows <= 64 ? 128 : p.rows <= 128 ? 256 : 512;
+  const int32_t kb0 = (int32_t)((int64_t)p.KB * p.terms * part / p.split);
+  const int32_t kb1 = (int32_t)((int64_t)p.KB * p.terms * (part + 1) / p.split);
+  const int32_t my_rows = p.rows / CG;  // rows that this CTA holds
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&t_full[s], 1);
+      mbar_init(&t_empty[s], CG * kEpilogueWarps);
+    }
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&maps.p);
+    prefetch_tensormap(&maps.q[0]);
+  }
+  if (warp == 2) tmem_allocate<CG>(&tmem_slot, cols);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int32_t t = unit; t < p.tiles && ok; t += units) {
+        const Tile ti = tile_at(p, t, 128 * CG);
+        const int32_t f = ti.f0 + 128 * cta, r = ti.r0 + my_rows * cta;
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+          if (!wait_for(&empty[s], ph ^ 1u, &gave_up)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = CG == 2 ? peer_addr(&full[s], 0) : smem_u32(&full[s]);
+          if (cta == 0) mbar_arrive_expect_tx(&full[s], CG * p.stage_bytes);
+          const uint32_t at = smem_u32(sm) + s * p.stage_bytes;
+          const int32_t term = kb / p.KB, c = (kb - term * p.KB) * 64;
+          const CUtensorMap* mq = &maps.q[term];
+          if (P_MN) {
+            load_2d<CG>(at, &maps.p, f, c, bar);
+            load_2d<CG>(at + 8192, &maps.p, f + 64, c, bar);
+          } else {
+            load_2d<CG>(at, &maps.p, c, f, bar);
+          }
+          if (Q_MN) {
+            for (int32_t j = 0; j < my_rows; j += 64) load_2d<CG>(at + kPBytes + j * 128, mq, r + j, c, bar);
+          } else {
+            load_2d<CG>(at + kPBytes, mq, c, r, bar);
+          }
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok) {  // copies in flight land before the CTA goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && cta == 0) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128 * CG, (uint32_t)p.rows) | (P_MN ? 1u << 15 : 0u) | (Q_MN ? 1u << 16 : 0u);
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int32_t t = unit; t < p.tiles && ok; t += units, ++it) {
+        const uint32_t acc = it & 1;
+        ok = wait_for(&t_empty[acc], ((it >> 1) & 1) ^ 1u, &gave_up);
+        tc_fence_after();
+        for (int32_t kb = kb0; kb < kb1 && ok; ++kb) {
+          ok = wait_for(&full[s], ph, &gave_up);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(sm) + s * p.stage_bytes, b = a + kPBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma<CG>(tmem + acc * p.rows, P_MN ? smem_desc_mn128(a + 2048 * k) : smem_desc_k128(a + 32 * k),
+                    Q_MN ? smem_desc_mn128(b + 2048 * k) : smem_desc_k128(b + 32 * k), idesc, kb != kb0 || k != 0);
+          commit<CG>(&empty[s]);
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) commit<CG>(&t_full[acc]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    int it = 0;
+    for (int32_t t = unit; t < p.tiles; t += units, ++it) {
+      const Tile ti = tile_at(p, t, 128 * CG);
+      const uint32_t acc = it & 1;
+      const int32_t f = ti.f0 + 128 * cta + 32 * q + lane;
+      const float bias = p.split == 1 && p.e.bias && f < p.F ? read_value(p.e.bias, f, p.e.bias_f32) : 0.f;
+      if (!wait_for(&t_full[acc], (it >> 1) & 1, &gave_up)) break;
+      __syncwarp();
+      tc_fence_after();
+      for (int32_t c0 = 16 * half; c0 < p.rows && ti.r0 + c0 < p.R; c0 += 32) {
+        uint32_t d[16];
+        tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + acc * p.rows + c0, d);
+        tmem_ld_wait();
+        if (p.split > 1) {  // (every copy has been read by now: the sums take the stages' place)
+          float* to = reinterpret_cast<float*>(sm) + c0 * 128 + 32 * q + lane;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) to[i * 128] = __uint_as_float(d[i]);
+        } else if (f < p.F) {
+          finish16(p, d, ti.r0 + c0, f, bias);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          peer_arrive(peer_addr(&t_empty[acc], 0));
+        else
+          mbar_arrive(&t_empty[acc]);
+      }
+    }
+  }
+  __syncwarp();
+  if (CG == 1 && p.split > 1) {
+    cluster_sync();
+    const Tile ti = tile_at(p, unit, 128);
+    const int32_t rows = min(p.rows, p.R - ti.r0);
+    // four features of a row a thread; the CTAs' sums are added in order
+    for (int32_t i = (int32_t)part * kThreads + threadIdx.x; i < rows * 32 && !gave_up; i += p.split * kThreads) {
+      const int32_t r = ti.r0 + i / 32, f = ti.f0 + 4 * (i & 31);
+      if (f >= p.F) continue;
+      float v[4] = {};
+      for (int c = 0; c < p.split; ++c) {
+        const float4 x = peer_float4(peer_addr(sm + i * 16, c));
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
+      }
+      const LinearFinish& e = p.e;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float z = v[j] + (e.bias ? read_value(e.bias, f + j, e.bias_f32) : 0.f);
+        if (e.z) write_value(e.z, (int64_t)r * e.z_stride + f + j, e.z_f32, z);
+        v[j] = linear_act(z, e.act);
+        if (e.residual)
+          v[j] = fmaf(e.scale, read_value(e.residual, (int64_t)r * e.residual_stride + f + j, e.residual_f32), v[j]);
+      }
+      if (e.out_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(e.out) + (int64_t)r * e.out_stride + f) =
+            make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(e.out) + (int64_t)r * e.out_stride + f) =
+            make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2 || p.split > 1) cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_free<CG>(tmem, cols);
+  }
+}
+
+template <int CG, bool P_MN, bool Q_MN>
+cudaError_t launch(const Plan& p, const Maps& m, int32_t units, cudaStream_t s) {
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = raise_smem_limit(linear_kernel<CG, P_MN, Q_MN>, kSmem - kBarBytes, configured);
+  if (e != cudaSuccess) return e;
+  const uint32_t cluster = CG == 2 ? 2 : (uint32_t)p.split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)units * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 1024 + p.stages * p.stage_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<CG, P_MN, Q_MN>, m, p);
+}
+template <int CG>
+cudaError_t launch_cg(bool p_mn, bool q_mn, const Plan& p, const Maps& m, int32_t units, cudaStream_t s) {
+  if (p_mn) return q_mn ? launch<CG, true, true>(p, m, units, s) : launch<CG, true, false>(p, m, units, s);
+  return q_mn ? cudaErrorInvalidValue : launch<CG, false, false>(p, m, units, s);
+}
+
+// An operand of `outer` features or rows and C columns, in boxes of `box` of them by 64 columns.
+cudaError_t operand_map(CUtensorMap* map, const LinearOperand& o, int32_t outer, int32_t C, int32_t box) {
+  return o.c_inner ? make_tmap_bf16(map, o.data, C, outer, o.stride, 64, box)
+                   : make_tmap_bf16(map, o.data, outer, C, o.stride, 64, 64);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  Plan p = {};
+  p.R = a.R;
+  p.F = a.F;
+  p.KB = (a.C + 63) / 64;
+  p.terms = a.terms;
+  p.e = a.finish;
+  p.split = 1;
+  int cg = 1;
+  const int64_t f128 = (a.F + 127) / 128;
+  if ((int64_t)(a.R + 255) / 256 * ((a.F + 255) / 256) >= sms / 2) {
+    cg = 2;
+    p.rows = 256;
+  } else {
+    const int32_t least = a.q[0].c_inner ? 16 : 64;
+    p.rows = least;
+    while (p.rows < 256 && p.rows < a.R && f128 * ((a.R + p.rows - 1) / p.rows) > sms / 2) p.rows *= 2;
+    while (p.rows < 64 && p.rows < a.R) p.rows *= 2;
+  }
+  const int32_t feats = 128 * cg;
+  p.tiles_r = (a.R + p.rows - 1) / p.rows;
+  const int64_t tiles = (int64_t)p.tiles_r * ((a.F + feats - 1) / feats);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  p.tiles = (int32_t)tiles;
+  p.group = std::min(8, p.tiles_r);
+  p.stage_bytes = kPBytes + (uint32_t)(p.rows / cg) * 128;
+  p.stages = std::min<int32_t>(kMaxStages, (kSmem - kBarBytes - 1024) / p.stage_bytes);
+  int32_t units = cg == 2 ? sms / 2 : sms;
+  if (cg == 1 && p.tiles < sms) {
+    p.split = (int32_t)std::min<int64_t>({kMaxSplit, sms / p.tiles, p.KB * p.terms});
+    p.split = std::max(p.split, 1);
+  }
+  units = p.split > 1 ? p.tiles : std::min(units, p.tiles);
+  Maps m;
+  e = operand_map(&m.p, a.p, a.F, a.C, 128);
+  for (int i = 0; i < kLinearTerms && e == cudaSuccess; ++i) {
+    if (i < p.terms)
+      e = operand_map(&m.q[i], a.q[i], a.R, a.C, p.rows / cg);
+    else
+      m.q[i] = m.q[0];
+  }
+  if (e != cudaSuccess) return e;
+  return cg == 2 ? launch_cg<2>(!a.p.c_inner, !a.q[0].c_inner, p, m, units, s)
+                 : launch_cg<1>(!a.p.c_inner, !a.q[0].c_inner, p, m, units, s);
+}
+
+cudaError_t linear_mma_flags(int32_t* flags) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_linear_flags, sizeof(int32_t));
+  const int32_t zero = 0;
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_linear_flags, &zero, sizeof(int32_t));
+  return e;
+}
+
+}  // namespace moe
