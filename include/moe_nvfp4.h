@@ -650,6 +650,43 @@ MOE_API moe_status moe_qk_norm_rope_backward(const moe_qk_args *args, const moe_
                                              size_t workspace_bytes, moe_stream_t stream);
 MOE_API size_t moe_qk_workspace_bytes(int32_t n, int32_t q_heads, int32_t k_heads, int32_t head_dim);
 
+/* The whole layer from the tokens on: router, shared experts, routed experts
+ * and residual in one call.  The handle's last shared_experts experts are
+ * taken by every token at weight 1 (a shared expert of m times the
+ * intermediate size is m of them, its rows and columns cut into m parts), the
+ * E = n_experts - shared_experts before them are routed, k = top_k -
+ * shared_experts a token:
+ *     logits[t][e] = sum_c x[t][c] * router_weight[e][c]     (fp32)
+ *     topk of logits + router_bias, weights as moe_router_topk
+ *     dst[t] = bf16_rne(residual[t] + sum_j w[t][j] * y_(t,j) + sum_s y_(t,s))
+ * with y as at the top of the file, j in order, then s in order.  A batch that
+ * moe_nvfp4_forward runs as one launch takes two here (the router, which also
+ * picks, and the layer); a larger one takes the router's product on the tensor
+ * cores (bf16 router_weight and E a multiple of 8; otherwise on the plain
+ * cores), the picks and moe_nvfp4_forward's launches.  After the call
+ * moe_nvfp4_debug_routing and _intermediates describe the launch's own
+ * arrangement of the shared experts. */
+typedef struct moe_layer_args {
+  int32_t n_tokens;
+  int32_t shared_experts;    /* 0..top_k - 1 */
+  int32_t router_dtype;      /* MOE_DTYPE_ of router_weight */
+  const uint16_t *x;         /* bf16 [n][H] */
+  const void *router_weight; /* [E][H] */
+  const float *router_bias;  /* [E] or NULL; picks and weights see logits + bias */
+  const uint16_t *residual;  /* bf16 [n][H] or NULL: zero; may be dst or x */
+  uint16_t *dst;             /* bf16 [n][H], written; not x */
+  int32_t *topk_ids;         /* [n][k] receives the picks, or NULL */
+  float *topk_weights;       /* [n][k] receives their weights, or NULL */
+  float *logits;             /* [n][E] receives the logits (without the bias), or NULL */
+} moe_layer_args;
+
+/* Errors: MOE_ERR_INVALID_ARG (null, misaligned or missing pointer, negative
+ * n, bad enum value, shared_experts outside its range, k > E),
+ * MOE_ERR_CAPACITY (n > max_tokens), MOE_ERR_UNSUPPORTED (more than 64 tokens
+ * without logits and E > top_k * H), MOE_ERR_CUDA.  n = 0 enqueues nothing.
+ * One call at a time a handle, as moe_nvfp4_forward. */
+MOE_API moe_status moe_nvfp4_layer_forward(moe_nvfp4_t handle, const moe_layer_args *args, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,8 @@ ENTRY_POINTS = ("moe_nvfp4_status_string", "moe_nvfp4_create", "moe_nvfp4_destro
                 "moe_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_balance_loss", "moe_router_backward",
                 "moe_router_workspace_bytes", "moe_lora_apply", "moe_lora_workspace_bytes",
                 "moe_lora_get_device_error", "moe_qk_norm_rope", "moe_qk_norm_rope_backward", "moe_qk_workspace_bytes",
-                "moe_linear", "moe_linear_backward", "moe_linear_workspace_bytes", "moe_linear_get_device_error")
+                "moe_linear", "moe_linear_backward", "moe_linear_workspace_bytes", "moe_linear_get_device_error",
+                "moe_nvfp4_layer_forward")
 
 _lock = threading.Lock()
 _lib = None
@@ -103,6 +104,7 @@ def load(build_if_missing: bool = False):
         L.moe_lora_apply.argtypes = [vp, vp, sz, vp]
         L.moe_lora_workspace_bytes.argtypes = [i32, i32]
         L.moe_lora_get_device_error.argtypes = [ctypes.POINTER(i32)]
+        L.moe_nvfp4_layer_forward.argtypes = [vp, vp, vp]
         L.moe_linear.argtypes = [vp, vp]
         L.moe_linear_backward.argtypes = [vp, vp, vp, sz, vp]
         L.moe_linear_workspace_bytes.argtypes = [i32, i32, i32]
@@ -196,6 +198,19 @@ class MoeLayer:
         n = x.shape[0] if n_tokens is None else n_tokens
         _check(load().moe_nvfp4_forward_host(self._h, _ptr(x), _ptr(topk_ids), _ptr(topk_weights), _ptr(dst), n,
                                              _stream(stream)), "moe_nvfp4_forward_host")
+        return dst
+
+    def layer_forward(self, x, router_weight, dst, residual=None, router_bias=None, *, shared_experts: int = 0,
+                      topk_ids=None, topk_weights=None, logits=None, stream=None):
+        """``moe_nvfp4_layer_forward``: the whole layer from the tokens on, dst = residual + routed + shared experts.
+
+        The layer's last ``shared_experts`` experts are taken by every token; router_weight [E, hidden] (bf16 or fp32)
+        and router_bias [E] route the E others, top_k - shared_experts a token.  topk_ids and topk_weights [n, k] and
+        logits [n, E] receive what the router found, where given."""
+        h = self._h.value if self._h else None
+        (_native or _binding()).layer_forward(h, self.hidden, self.n_experts, self.top_k, x, router_weight, dst,
+                                              residual, router_bias, shared_experts, topk_ids, topk_weights, logits,
+                                              stream)
         return dst
 
     def device_error(self) -> int:
@@ -463,7 +478,8 @@ def linear_device_error() -> int:
     """Reads and clears the device error flags of linear and linear_backward (DEVFLAG_TIMEOUT); synchronizes the
     device."""
     f = ctypes.c_int32()
-    _check(load().moe_linear_get_device_error(ctypes.byref(f)), "moe_linear_get_device_error")
+    _check(load().moe_linear_get_device_error(ctypes.byref(f)), "moe_linear_get_device_error",
+                "moe_nvfp4_layer_forward")
     return f.value
 
 

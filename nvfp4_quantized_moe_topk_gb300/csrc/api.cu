@@ -93,6 +93,9 @@ struct moe_nvfp4 {
   float* dense_w = nullptr;
   uint16_t *Xp = nullptr, *Ap = nullptr;
   float* Yp = nullptr;
+  // the whole-layer call: logits of a few tokens, and its router's block count
+  float* logits = nullptr;
+  int32_t *router_count = nullptr, *part_of = nullptr;
   // staging for forward_host
   uint16_t *x_stage = nullptr, *dst_stage = nullptr;
   int32_t* ids_stage = nullptr;
@@ -126,7 +129,8 @@ void free_handle(moe_nvfp4* h) {
                   h->Ap,       h->Yp,        h->x_stage,   h->dst_stage, h->ids_stage, h->w_stage,
                   h->up_tiles, h->dn_tiles,  h->col_done,  h->grid_bar,  h->up_blocks, h->dn_blocks,
                   h->up_tiles16, h->dn_tiles16, h->dec_partial,
-                  h->gate_codes, h->gate_scales, h->gate_g, h->blk_hist, h->dense_ids, h->dense_w};
+                  h->gate_codes, h->gate_scales, h->gate_g, h->blk_hist, h->dense_ids, h->dense_w,
+                  h->logits, h->router_count, h->part_of};
   for (void* p : ptrs)
     if (p) cudaFree(p);
   if (h->small_dev) cudaFree(h->small_dev);
@@ -253,8 +257,11 @@ moe_status moe_nvfp4_create(const moe_nvfp4_config* config, const moe_nvfp4_weig
   TRY(cudaMalloc(&h->dn_scales, mat_scales));
   TRY(cudaMalloc(&h->up_g, E * sizeof(float)));
   TRY(cudaMalloc(&h->dn_g, E * sizeof(float)));
-  TRY(cudaMalloc(&h->counts, E * sizeof(int32_t)));
-  TRY(cudaMalloc(&h->offsets, (E + 1) * sizeof(int32_t)));
+  TRY(cudaMalloc(&h->counts, (E + kLayerMaxParts) * sizeof(int32_t)));
+  TRY(cudaMalloc(&h->offsets, (E + kLayerMaxParts + 1) * sizeof(int32_t)));
+  TRY(cudaMalloc(&h->logits, (size_t)kLayerFusedTokens * E * sizeof(float)));
+  TRY(cudaMalloc(&h->router_count, sizeof(int32_t)));
+  TRY(cudaMalloc(&h->part_of, kLayerMaxParts * sizeof(int32_t)));
   TRY(cudaMalloc(&h->perm_pair, Rr * sizeof(int32_t)));
   TRY(cudaMalloc(&h->inv, Rr * sizeof(int32_t)));
   TRY(cudaMalloc(&h->err, sizeof(int32_t)));
@@ -303,6 +310,7 @@ moe_status moe_nvfp4_create(const moe_nvfp4_config* config, const moe_nvfp4_weig
   TRY(cudaMemcpyAsync(h->up_g, w->up_global, E * sizeof(float), cudaMemcpyDeviceToDevice, s));
   TRY(cudaMemcpyAsync(h->dn_g, w->down_global, E * sizeof(float), cudaMemcpyDeviceToDevice, s));
   TRY(cudaMemsetAsync(h->err, 0, sizeof(int32_t), s));
+  TRY(cudaMemsetAsync(h->router_count, 0, sizeof(int32_t), s));
   if (E == 1 && c.top_k == 1) {
     const size_t nt = c.max_tokens > 0 ? (size_t)c.max_tokens : 1;
     TRY(cudaMalloc(&h->dense_ids, nt * sizeof(int32_t)));
@@ -374,9 +382,22 @@ moe_status moe_nvfp4_destroy(moe_nvfp4_t h) {
 // dst_out (may be null): where the single-launch kernel writes the result
 // (a device-visible copy of dst, e.g. mapped pinned host memory); *wrote_out
 // tells whether that path ran.  Other paths update dst in place.
+// layer (may be null): the whole-layer call's, which has the experts' sums
+// added onto `base` (null: zero) in the single launch, among `experts` experts
+// and further parts of them.
+struct LayerForward {
+  const uint16_t* base;
+  int32_t experts;
+};
+static bool runs_as_one(const moe_nvfp4* h, int32_t n, int32_t experts) {
+  const int64_t R = (int64_t)n * h->cfg.top_k;
+  return n <= h->single_max_tokens && R <= kDecMaxPairs &&
+         decode_layout(experts, (int32_t)R, decode_can_stage(n, 0)).warps >= 4;
+}
 static moe_status forward_impl(moe_nvfp4* h, const uint16_t* x, const int32_t* ids, const float* tw, uint16_t* dst,
                                int32_t n, cudaStream_t s, cudaEvent_t dst_ready = nullptr,
-                               bool* combine_left = nullptr, uint16_t* dst_out = nullptr, bool* wrote_out = nullptr) {
+                               bool* combine_left = nullptr, uint16_t* dst_out = nullptr, bool* wrote_out = nullptr,
+                               const LayerForward* layer = nullptr) {
   const moe_nvfp4_config& c = h->cfg;
   const int32_t k = c.top_k, E = c.n_experts, H = c.hidden, I = c.inter;
   const int32_t R = n * k;
@@ -413,9 +434,15 @@ static moe_status forward_impl(moe_nvfp4* h, const uint16_t* x, const int32_t* i
   d.I = I;
   d.E = E;
   d.k = k;
+  d.part_first = E;
+  d.part_of = h->part_of;
   if (n <= h->single_max_tokens && R <= kDecMaxPairs) {
     // the whole layer in one launch
-    d.L = decode_layout(E, R, decode_can_stage(n, 0));
+    if (layer) {
+      d.E = layer->experts;
+      d.dst = layer->base;
+    }
+    d.L = decode_layout(d.E, R, decode_can_stage(n, 0));
     if (d.L.warps >= 4) {
       if (dst_ready && cudaStreamWaitEvent(s, dst_ready, 0) != cudaSuccess) return MOE_ERR_CUDA;
       if (dst_out) {
@@ -542,6 +569,75 @@ moe_status moe_nvfp4_forward(moe_nvfp4_t h, const uint16_t* x, const int32_t* id
   if (!x || !ids || !tw || !dst) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(dst, 16) || !aligned(ids, 4) || !aligned(tw, 4)) return MOE_ERR_INVALID_ARG;
   return forward_impl(h, x, ids, tw, dst, n, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, moe_stream_t stream) {
+  if (!h || !args) return MOE_ERR_INVALID_ARG;
+  const moe_layer_args& a = *args;
+  const moe_nvfp4_config& c = h->cfg;
+  const int32_t n = a.n_tokens, S = a.shared_experts, k = c.top_k - S, E = c.n_experts - S, H = c.hidden;
+  if (n < 0 || S < 0 || k < 1 || k > E || (a.router_dtype != MOE_DTYPE_BF16 && a.router_dtype != MOE_DTYPE_F32))
+    return MOE_ERR_INVALID_ARG;
+  if (n > c.max_tokens) return MOE_ERR_CAPACITY;
+  // more tokens than one launch takes: their logits lie where the experts' rows will
+  if (n > kLayerFusedTokens && !a.logits && (int64_t)E > (int64_t)c.top_k * H) return MOE_ERR_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (!a.x || !a.router_weight || !a.dst || a.x == a.dst) return MOE_ERR_INVALID_ARG;
+  if (!aligned(a.x, 16) || !aligned(a.router_weight, 16) || !aligned(a.dst, 16) || !aligned(a.residual, 16) ||
+      !aligned(a.router_bias, 4) || !aligned(a.topk_ids, 4) || !aligned(a.topk_weights, 4) || !aligned(a.logits, 16))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // experts in parts of 8 tokens, where all of them are few enough for one launch
+  const int32_t more = layer_parts(n, k, S);
+  const bool parts = more <= kLayerMaxParts && c.n_experts + more <= 1024 && runs_as_one(h, n, c.n_experts + more);
+  const bool one = parts || runs_as_one(h, n, c.n_experts);
+  LayerRouterArgs r = {};
+  r.x = a.x;
+  r.weight = a.router_weight;
+  r.bias = a.router_bias;
+  r.logits = a.logits ? a.logits : n <= kLayerFusedTokens ? h->logits : h->Yp;
+  r.ids = h->ids_stage;
+  r.w = h->w_stage;
+  r.ids_out = a.topk_ids;
+  r.w_out = a.topk_weights;
+  r.count = h->router_count;
+  r.n = n;
+  r.H = H;
+  r.E = E;
+  r.k = k;
+  r.shared = S;
+  r.part_of = parts && more > 0 ? h->part_of : nullptr;
+  r.weight_f32 = a.router_dtype == MOE_DTYPE_F32;
+  {
+    TimedLaunch tl(h, s, kKRouting);
+    cudaError_t e = cudaSuccess;
+    const bool product = n > kLayerFusedTokens && !r.weight_f32 && E % 8 == 0;
+    if (product) {  // many tokens: the logits by the tensor cores
+      moe_linear_args l = {};
+      l.n = n;
+      l.in_features = H;
+      l.out_features = E;
+      l.out_dtype = MOE_DTYPE_F32;
+      l.weight = static_cast<const uint16_t*>(a.router_weight);
+      l.x.data = const_cast<uint16_t*>(a.x);
+      l.out.data = r.logits;
+      e = launch_linear(l, s);
+    }
+    if (e == cudaSuccess) e = launch_layer_router(r, product, s);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (one) {
+    const LayerForward layer = {a.residual, r.part_of ? c.n_experts + more : c.n_experts};
+    return forward_impl(h, a.x, h->ids_stage, h->w_stage, a.dst, n, s, nullptr, nullptr, nullptr, nullptr, &layer);
+  }
+  const size_t bytes = (size_t)n * H * 2;
+  if (!a.residual) {
+    if (cudaMemsetAsync(a.dst, 0, bytes, s) != cudaSuccess) return MOE_ERR_CUDA;
+  } else if (a.residual != a.dst &&
+             cudaMemcpyAsync(a.dst, a.residual, bytes, cudaMemcpyDeviceToDevice, s) != cudaSuccess) {
+    return MOE_ERR_CUDA;
+  }
+  return forward_impl(h, a.x, h->ids_stage, h->w_stage, a.dst, n, s);
 }
 
 moe_status moe_nvfp4_shared_expert_forward(moe_nvfp4_t h, const uint16_t* x, uint16_t* dst, int32_t n,

@@ -512,6 +512,40 @@ PyObject* linear_backward(PyObject*, PyObject* const* p, Py_ssize_t count) {
   });
 }
 
+// handle, hidden, n_experts, top_k, x, router_weight, dst, residual, router_bias, shared_experts, topk_ids, topk_weights,
+// logits, stream
+PyObject* layer_forward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+  return guarded(count, 14, [&] {
+    Call c{"moe_nvfp4_layer_forward"};
+    int64_t v[5] = {};
+    PyObject* const ints[5] = {p[0], p[1], p[2], p[3], p[9]};
+    for (int i = 0; i < 5; ++i) {
+      if (i == 0 && ints[i] == Py_None) c.refuse("the layer is closed");
+      v[i] = PyLong_AsLongLong(ints[i]);
+      if (v[i] == -1 && PyErr_Occurred()) throw Raised();
+    }
+    const int64_t H = v[1], S = v[4], E = v[2] - S, k = v[3] - S;
+    if (S < 0 || k < 1 || E < k) c.refuse("shared_experts leaves no routed experts to pick from");
+    const at::Tensor *x = c.tensor(p[4], "x"), *w = c.tensor(p[5], "router_weight");
+    if (!x || x->dim() != 2 || !w) c.refuse("x is not [n, hidden], or router_weight is missing");
+    c.lead(*x);
+    const int64_t n = x->size(0);
+    moe_layer_args a = {};
+    a.n_tokens = c.i32(n, "n");
+    a.shared_experts = (int32_t)S;
+    a.router_dtype = c.dtype(*w, "router_weight");
+    a.x = static_cast<uint16_t*>(c.array(x, "x", at::kBFloat16, {n, H}));
+    a.router_weight = c.array(w, "router_weight", scalar_type(a.router_dtype), {E, H});
+    a.dst = static_cast<uint16_t*>(c.array(p[6], "dst", at::kBFloat16, {n, H}));
+    a.residual = static_cast<uint16_t*>(c.array(p[7], "residual", at::kBFloat16, {n, H}));
+    a.router_bias = static_cast<float*>(c.array(p[8], "router_bias", at::kFloat, {E}));
+    a.topk_ids = static_cast<int32_t*>(c.array(p[10], "topk_ids", at::kInt, {n, k}));
+    a.topk_weights = static_cast<float*>(c.array(p[11], "topk_weights", at::kFloat, {n, k}));
+    a.logits = static_cast<float*>(c.array(p[12], "logits", at::kFloat, {n, E}));
+    return c.done(moe_nvfp4_layer_forward(reinterpret_cast<moe_nvfp4_t>(v[0]), &a, c.stream(p[13])));
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XSETREF(g_error, cls);
@@ -527,6 +561,7 @@ PyMethodDef kMethods[] = {FAST(block_norm),
                           FAST(lora_apply),
                           FAST(linear),
                           FAST(linear_backward),
+                          FAST(layer_forward),
                           FAST(qk_norm_rope),
                           FAST(qk_norm_rope_backward),
                           {"set_error", set_error, METH_O, nullptr},

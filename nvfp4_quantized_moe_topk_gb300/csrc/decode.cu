@@ -354,7 +354,7 @@ struct DecodeCtx {
   __device__ __forceinline__ const uint8_t* chunk_src(const Cur& c) const {
     const int32_t KT = c.ph ? KTd : KTu, NT = c.ph ? NTd : NTu;
     const uint8_t* base = S ? (c.ph ? a.dn_tiles16 : a.up_tiles16) : (c.ph ? a.dn_tiles : a.up_tiles);
-    return base + ((size_t)((size_t)c.e * NT + c.rt) * KT + c.kt) * kTileBytes;
+    return base + ((size_t)((size_t)a.weights_of(c.e) * NT + c.rt) * KT + c.kt) * kTileBytes;
   }
   __device__ __forceinline__ int32_t kts(const Cur& c) const { return min(kDecCK, c.kt_end - c.kt); }
   __device__ __forceinline__ bool two(const Cur& c) const {
@@ -762,10 +762,10 @@ __device__ __forceinline__ void decode_epilogue(const DecodeCtx& cx, const Cur& 
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] *= rowscale[cur.srow + min(2 * t + (q & 1), nt - 1)];
   }
-  const float alpha = (up ? a.up_g : a.dn_g)[cur.e] * wfix;
+  const float alpha = (up ? a.up_g : a.dn_g)[a.weights_of(cur.e)] * wfix;
   if (up && a.gated) {
     // the pair is (gate tile, up tile) of the same 16 intermediate rows
-    const float ag = a.gate_g[cur.e] * wfix;
+    const float ag = a.gate_g[a.weights_of(cur.e)] * wfix;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int32_t col = 2 * t + (q & 1);
@@ -813,7 +813,7 @@ __device__ __forceinline__ void decode_epilogue(const DecodeCtx& cx, const Cur& 
     const int32_t c = rt * 16 + (lane & 15);
     for (int32_t tk = lane >> 4; tk < a.n; tk += 2) {
       const size_t o = (size_t)tk * a.H + c;
-      float acc = __uint_as_float((uint32_t)a.dst[o] << 16);
+      float acc = a.dst ? __uint_as_float((uint32_t)a.dst[o] << 16) : 0.f;
       for (int32_t j = 0; j < a.k; ++j) {
         const int32_t r = s_inv[tk * a.k + j];
         if (r >= 0) acc = __fmaf_rn(a.tw[tk * a.k + j], ld_cg_f32(a.Yp + (size_t)r * a.H + c), acc);
@@ -827,7 +827,7 @@ __device__ __forceinline__ void decode_epilogue(const DecodeCtx& cx, const Cur& 
 // element, j in order; the k row loads are issued before the FMA chain.
 __device__ __forceinline__ void combine_one(const DecodeArgs& a, const int32_t* s_inv, int32_t tk, int32_t c) {
   const size_t o = (size_t)tk * a.H + c;
-  float acc = __uint_as_float((uint32_t)a.dst[o] << 16);
+  float acc = a.dst ? __uint_as_float((uint32_t)a.dst[o] << 16) : 0.f;
   for (int32_t j0 = 0; j0 < a.k; j0 += 8) {
     int32_t r[8];
     float y[8], w[8];
@@ -1097,7 +1097,7 @@ __global__ void __launch_bounds__(kDecMaxWarps * 32, 1) decode_kernel(const __gr
         const uint32_t j = lo / per, off = lo - j * per;
         const uint32_t len = min(min(per - off, hi - lo), 65536u);
         const int32_t e = __ldg(a.ids + j);
-        if (e >= 0 && e < E && len >= 16) prefetch_l2_bulk(tiles + (size_t)e * per + off, len & ~15u);
+        if (e >= 0 && e < E && len >= 16) prefetch_l2_bulk(tiles + (size_t)a.weights_of(e) * per + off, len & ~15u);
         lo += len;
       }
     }

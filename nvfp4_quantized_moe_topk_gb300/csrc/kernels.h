@@ -189,7 +189,7 @@ struct DecodeArgs {
   const uint16_t* x;          // [n][H] bf16
   const int32_t* ids;         // [n][k]
   const float* tw;            // [n][k]
-  uint16_t* dst;              // [n][H] bf16
+  const uint16_t* dst;        // [n][H] bf16 that the experts are added onto, or nullptr: zero
   uint16_t* dst_out;          // [n][H] bf16: where the in-kernel combine writes (dst, or a host-mapped copy of it)
   uint16_t* Ap;               // [R][I] bf16 (workspace)
   float* Yp;                  // [R][H] fp32 (workspace)
@@ -206,8 +206,20 @@ struct DecodeArgs {
   // routing kernel), only experts with 0 < count <= max_rows are processed,
   // and the combine is left to the WeightedRowSum kernel.
   int32_t ext, max_rows;
+  // Experts from part_first on (>= E: none) have the weights of part_of[e -
+  // part_first]: the whole-layer call serves an expert of more than 8 tokens as
+  // several of at most 8, so that it neither keeps the others from staging nor
+  // makes a warp pass over its tiles again and again.
+  int32_t part_first;
+  const int32_t* part_of;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int32_t weights_of(int32_t e) const {
+    return e < part_first ? e : __ldg(part_of + (e - part_first));
+  }
+#endif
   DecLayout L;
 };
+constexpr int kLayerMaxParts = 256;  // such further parts, at most (counts and offsets have room for them)
 
 cudaError_t launch_repack_frag(const uint8_t* codes, const uint8_t* scales, int32_t G, int32_t N, int32_t K,
                                uint8_t* out, cudaStream_t s);
@@ -220,6 +232,29 @@ DecLayout decode_layout(int32_t E, int32_t R, bool can_stage);
 // external routing); one-token batches take the per-chunk kernel alone.
 inline bool decode_can_stage(int32_t n, int32_t ext) { return n > 1 || ext; }
 cudaError_t launch_decode(const DecodeArgs& args, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------- the whole layer (layer.cu)
+struct LayerRouterArgs {
+  const uint16_t* x;    // [n][H] bf16
+  const void* weight;   // [E][H] bf16 or fp32
+  const float* bias;    // [E] or nullptr
+  float* logits;        // [n][E]
+  int32_t* ids;         // [n][k + shared]: the picks, then the shared experts (E on), or their parts (E + shared on)
+  float* w;             // [n][k + shared]: the picks' weights, then ones
+  int32_t *ids_out;     // [n][k] or nullptr
+  float* w_out;         // [n][k] or nullptr
+  int32_t* count;       // blocks that have finished; zero between launches
+  int32_t* part_of;     // [kLayerMaxParts]: each further part's expert; nullptr: experts are not cut
+  int32_t n, H, E, k, shared;
+  int32_t weight_f32;
+};
+// Further parts that n tokens may need.
+inline int32_t layer_parts(int32_t n, int32_t k, int32_t shared) {
+  return n <= kDecPassTok ? 0 : shared * ((n + kDecPassTok - 1) / kDecPassTok - 1) + n * k / kDecPassTok;
+}
+constexpr int kLayerFusedTokens = 64;  // logits and picks in one launch
+// Logits (where not `have_logits`) and picks.
+cudaError_t launch_layer_router(const LayerRouterArgs& a, bool have_logits, cudaStream_t s);
 
 // ------------------------------------------------- operators around the layer
 constexpr int kNormMaxHidden = 8192;
