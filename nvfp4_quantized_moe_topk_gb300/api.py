@@ -478,8 +478,7 @@ def linear_device_error() -> int:
     """Reads and clears the device error flags of linear and linear_backward (DEVFLAG_TIMEOUT); synchronizes the
     device."""
     f = ctypes.c_int32()
-    _check(load().moe_linear_get_device_error(ctypes.byref(f)), "moe_linear_get_device_error",
-                "moe_nvfp4_layer_forward")
+    _check(load().moe_linear_get_device_error(ctypes.byref(f)), "moe_linear_get_device_error")
     return f.value
 
 

@@ -15,6 +15,8 @@
 // tiles than SMs, the CTAs of a cluster split the columns and add their sums
 // through each other's shared memory, in order.
 #include <algorithm>
+#include <cstdlib>
+#include <cstdio>
 
 #include "block.cuh"
 #include "linear_act.cuh"
@@ -28,7 +30,12 @@ constexpr int kThreads = 384, kEpilogueWarps = 8;  // warp 0: copies, 1: product
 constexpr int kMaxStages = 8;
 constexpr uint32_t kSmem = 227 * 1024, kBarBytes = 1024;
 constexpr uint32_t kPBytes = 128 * 128;  // a stage's features: 128 of 64 columns
-constexpr int kMaxSplit = 8;
+constexpr int kMaxCluster = 8;
+// The tensor core cuts what it adds to a sum where it would round, which costs a sum of C products about 1e-9 C of its
+// size, always towards zero.  A result in fp32 is therefore summed in tensor memory for 8 blocks of 64 columns at a time,
+// and from there on in registers (4314 columns: 4.7e-6 off without, XXXX so).
+constexpr int32_t kChain = 8;
+constexpr int kChainBlocks = 6, kChainRows = 32 * kChainBlocks;  // (a thread holds 96 sums)
 
 // Set where a bounded wait ran out; read by moe_linear_get_device_error.
 __device__ int32_t g_linear_flags;
@@ -38,7 +45,9 @@ struct Plan {
   int32_t rows;               // of a tile: the instruction's N
   int32_t tiles_r, tiles, group;
   int32_t split, stages;
+  int32_t chain;              // blocks of 64 columns that tensor memory sums before their sum moves to registers
   uint32_t stage_bytes;
+  uint32_t z_at, slot_bytes;  // of an epilogue warp's staging slot: out's block, then z's
   LinearFinish e;
 };
 
@@ -119,12 +128,12 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 }
 // Arrives on the barrier of each CTA of the pair once the products issued so far are done.
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t first_cta) {
   if (CG == 2)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << first_cta))
         : "memory");
   else
     tc_commit(bar);
@@ -155,7 +164,7 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
 }
 
 struct Maps {
-  CUtensorMap p, q[kLinearTerms];
+  CUtensorMap p, q[kLinearTerms], out, z;
 };
 
 struct Tile {
@@ -178,28 +187,74 @@ __device__ __forceinline__ void write_value(void* p, int64_t at, int32_t f32, fl
     static_cast<uint16_t*>(p)[at] = f2bf_rn(v);
 }
 
-// The sums of feature f in 16 rows from r0 on (as many as there are).
-__device__ __forceinline__ void finish16(const Plan& p, const uint32_t (&d)[16], int32_t r0, int32_t f, float bias) {
+// The residual of feature f in 16 rows from r0 on, as it lies in memory.
+__device__ __forceinline__ void load_residual(const Plan& p, int32_t r0, int32_t f, uint32_t (&raw)[16]) {
   const LinearFinish& e = p.e;
-  const int32_t rows = min(16, p.R - r0);
-  float res[16];
+  const int32_t rows = f < p.F ? min(16, p.R - r0) : 0;
+  if (e.residual_f32) {
+    const uint32_t* at = static_cast<const uint32_t*>(e.residual) + (int64_t)r0 * e.residual_stride + f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, at += e.residual_stride) raw[i] = i < rows ? *at : 0u;
+  } else {
+    const uint16_t* at = static_cast<const uint16_t*>(e.residual) + (int64_t)r0 * e.residual_stride + f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, at += e.residual_stride) raw[i] = i < rows ? *at : 0u;
+  }
+}
+// A block of 16 rows by 32 features for the copy that takes it to memory: a lane its feature.
+__device__ __forceinline__ void stage16(uint8_t* to, int lane, int32_t f32, const float (&v)[16]) {
+  if (f32) {
+    float* at = reinterpret_cast<float*>(to) + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) at[32 * i] = v[i];
+  } else {
+    uint16_t* at = reinterpret_cast<uint16_t*>(to) + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) at[32 * i] = f2bf_rn(v[i]);
+  }
+}
+__device__ __forceinline__ void store_2d(const CUtensorMap* map, const void* from, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+               "r"(smem_u32(from))
+               : "memory");
+}
+template <int ACT>
+__device__ __forceinline__ void act16(float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = linear_act(v[i], ACT);
+}
+// Finishes a warp's sums of 32 features (from f0 on) in 16 rows from r0 on through its staging slot.
+__device__ __forceinline__ void finish16(const Plan& p, const Maps& maps, float (&v)[16], const uint32_t (&raw)[16],
+                                         int32_t r0, int32_t f0, int lane, float bias, uint8_t* slot) {
+  const LinearFinish& e = p.e;
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the slot's last block has left it
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += bias;
+  if (e.z) stage16(slot + p.z_at, lane, e.z_f32, v);
+  if (e.act == MOE_LINEAR_RELU2)
+    act16<MOE_LINEAR_RELU2>(v);
+  else if (e.act == MOE_LINEAR_SILU)
+    act16<MOE_LINEAR_SILU>(v);
+  else if (e.act == MOE_LINEAR_GELU_TANH)
+    act16<MOE_LINEAR_GELU_TANH>(v);
   if (e.residual) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      res[i] = i < rows ? read_value(e.residual, (int64_t)(r0 + i) * e.residual_stride + f, e.residual_f32) : 0.f;
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(e.scale, e.residual_f32 ? __uint_as_float(raw[i]) : bf16lo(raw[i]), v[i]);
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (i >= rows) break;
-    const float z = __uint_as_float(d[i]) + bias;
-    if (e.z) write_value(e.z, (int64_t)(r0 + i) * e.z_stride + f, e.z_f32, z);
-    float v = linear_act(z, e.act);
-    if (e.residual) v = fmaf(e.scale, res[i], v);
-    write_value(e.out, (int64_t)(r0 + i) * e.out_stride + f, e.out_f32, v);
+  stage16(slot, lane, e.out_f32, v);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (f0 < p.F) {  // (what lies past the last row or feature is not written)
+      store_2d(&maps.out, slot, f0, r0);
+      if (e.z) store_2d(&maps.z, slot + p.z_at, f0, r0);
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 }
 
-template <int CG, bool P_MN, bool Q_MN>
+template <int CG, bool P_MN, bool Q_MN, bool CHAIN>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan p) {
   extern __shared__ uint8_t raw[];
@@ -208,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int gave_up;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank(), cta = CG == 2 ? rank : 0, part = CG == 2 ? 0 : rank;
-  const int32_t units = CG == 2 ? gridDim.x / 2 : gridDim.x / p.split, unit = CG == 2 ? blockIdx.x / 2 : blockIdx.x / p.split;
+  const uint32_t rank = cluster_rank(), cta = rank % CG, part = rank / CG, first_cta = rank - cta;  // of the pair
+  const int32_t units = gridDim.x / (CG * p.split), unit = blockIdx.x / (CG * p.split);
   const uint32_t cols = p.rows <= 16 ? 32 : p.rows <= 32 ? 64 : p.rows <= 64 ? 128 : p.rows <= 128 ? 256 : 512;
   const int32_t kb0 = (int32_t)((int64_t)p.KB * p.terms * part / p.split);
   const int32_t kb1 = (int32_t)((int64_t)p.KB * p.terms * (part + 1) / p.split);
@@ -253,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t bar = CG == 2 ? peer_addr(&full[s], 0) : smem_u32(&full[s]);
+          const uint32_t bar = CG == 2 ? peer_addr(&full[s], first_cta) : smem_u32(&full[s]);
           if (cta == 0) mbar_arrive_expect_tx(&full[s], CG * p.stage_bytes);
           const uint32_t at = smem_u32(sm) + s * p.stage_bytes;
           const int32_t term = kb / p.KB, c = (kb - term * p.KB) * 64;
@@ -264,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             load_2d<CG>(at, &maps.p, c, f, bar);
           }
-          if (Q_MN) {
+          if (Q_MN) {  // (whole boxes of 64 rows)
             for (int32_t j = 0; j < my_rows; j += 64) load_2d<CG>(at + kPBytes + j * 128, mq, r + j, c, bar);
           } else {
             load_2d<CG>(at + kPBytes, mq, c, r, bar);
@@ -289,10 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int32_t t = unit; t < p.tiles && ok; t += units, ++it) {
-        const uint32_t acc = it & 1;
-        ok = wait_for(&t_empty[acc], ((it >> 1) & 1) ^ 1u, &gave_up);
-        tc_fence_after();
+        uint32_t acc = 0;
         for (int32_t kb = kb0; kb < kb1 && ok; ++kb) {
+          const bool first = kb == kb0 || (CHAIN && (kb - kb0) % p.chain == 0);
+          if (first) {
+            if (kb != kb0) {
+              commit<CG>(&t_full[acc], first_cta);
+              ++it;
+            }
+            acc = it & 1;
+            ok = wait_for(&t_empty[acc], ((it >> 1) & 1) ^ 1u, &gave_up);
+            if (!ok) break;
+          }
           ok = wait_for(&full[s], ph, &gave_up);
           if (!ok) break;
           tc_fence_after();
@@ -300,54 +363,109 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma<CG>(tmem + acc * p.rows, P_MN ? smem_desc_mn128(a + 2048 * k) : smem_desc_k128(a + 32 * k),
-                    Q_MN ? smem_desc_mn128(b + 2048 * k) : smem_desc_k128(b + 32 * k), idesc, kb != kb0 || k != 0);
-          commit<CG>(&empty[s]);
+                    Q_MN ? smem_desc_mn128(b + 2048 * k) : smem_desc_k128(b + 32 * k), idesc, !first || k != 0);
+          commit<CG>(&empty[s], first_cta);
           if (++s == p.stages) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (ok) commit<CG>(&t_full[acc]);
+        if (ok) commit<CG>(&t_full[acc], first_cta);
       }
     }
     __syncwarp();
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
-    int it = 0;
-    for (int32_t t = unit; t < p.tiles; t += units, ++it) {
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    uint8_t* slots = sm + p.stages * p.stage_bytes + (warp - 4) * 2 * p.slot_bytes;
+    int it = 0, slot = 0;
+    bool ok = true;
+    for (int32_t t = unit; t < p.tiles && ok; t += units) {
       const Tile ti = tile_at(p, t, 128 * CG);
-      const uint32_t acc = it & 1;
-      const int32_t f = ti.f0 + 128 * cta + 32 * q + lane;
-      const float bias = p.split == 1 && p.e.bias && f < p.F ? read_value(p.e.bias, f, p.e.bias_f32) : 0.f;
-      if (!wait_for(&t_full[acc], (it >> 1) & 1, &gave_up)) break;
-      __syncwarp();
-      tc_fence_after();
-      for (int32_t c0 = 16 * half; c0 < p.rows && ti.r0 + c0 < p.R; c0 += 32) {
-        uint32_t d[16];
-        tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + acc * p.rows + c0, d);
-        tmem_ld_wait();
-        if (p.split > 1) {  // (every copy has been read by now: the sums take the stages' place)
+      const int32_t f0 = ti.f0 + 128 * cta + 32 * q, f = f0 + lane, rows = min(p.rows, p.R - ti.r0);
+      const bool direct = p.split == 1;
+      const float bias = direct && p.e.bias && f < p.F ? read_value(p.e.bias, f, p.e.bias_f32) : 0.f;
+      const bool residual = direct && p.e.residual;
+      uint32_t raw[16] = {};
+      if (residual && 16 * half < rows) load_residual(p, ti.r0 + 16 * half, f, raw);
+      // a block's sums: finished, or to shared memory where a cluster's meet (every copy has been read by then: they take
+      // the stages' place)
+      auto out = [&](float (&v)[16], int32_t c0) {
+        if (!direct) {
           float* to = reinterpret_cast<float*>(sm) + c0 * 128 + 32 * q + lane;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) to[i * 128] = __uint_as_float(d[i]);
-        } else if (f < p.F) {
-          finish16(p, d, ti.r0 + c0, f, bias);
+          for (int i = 0; i < 16; ++i) to[i * 128] = v[i];
+          return;
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 2)
-          peer_arrive(peer_addr(&t_empty[acc], 0));
-        else
-          mbar_arrive(&t_empty[acc]);
+        uint32_t now[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) now[i] = raw[i];
+        if (residual && c0 + 32 < rows) load_residual(p, ti.r0 + c0 + 32, f, raw);  // the next block's
+        finish16(p, maps, v, now, ti.r0 + c0, f0, lane, bias, slots + slot * p.slot_bytes);
+        slot ^= 1;
+      };
+      auto arrive = [&](uint32_t acc) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            peer_arrive(peer_addr(&t_empty[acc], first_cta));
+          else
+            mbar_arrive(&t_empty[acc]);
+        }
+      };
+      if (CHAIN) {
+        float sum[kChainBlocks][16];
+        for (int32_t kb = kb0; kb < kb1; kb += p.chain, ++it) {
+          const uint32_t acc = it & 1;
+          ok = wait_for(&t_full[acc], (it >> 1) & 1, &gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int b = 0; b < kChainBlocks; ++b) {
+            const int32_t c0 = 16 * half + 32 * b;
+            if (c0 >= rows) continue;
+            uint32_t d[16];
+            tmem_ld16(tmem + lanes + acc * p.rows + c0, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[b][i] = (kb == kb0 ? 0.f : sum[b][i]) + __uint_as_float(d[i]);
+          }
+          arrive(acc);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int b = 0; b < kChainBlocks; ++b) {
+          const int32_t c0 = 16 * half + 32 * b;
+          if (c0 < rows) out(sum[b], c0);
+        }
+      } else {
+        const uint32_t acc = it & 1;
+        ok = wait_for(&t_full[acc], (it >> 1) & 1, &gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        for (int32_t c0 = 16 * half; c0 < rows; c0 += 32) {
+          uint32_t d[16];
+          tmem_ld16(tmem + lanes + acc * p.rows + c0, d);
+          tmem_ld_wait();
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(d[i]);
+          out(v, c0);
+        }
+        arrive(acc);
+        ++it;
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
   __syncwarp();
-  if (CG == 1 && p.split > 1) {
+  if (p.split > 1) {
     cluster_sync();
-    const Tile ti = tile_at(p, unit, 128);
+    Tile ti = tile_at(p, unit, 128 * CG);
+    ti.f0 += 128 * cta;
     const int32_t rows = min(p.rows, p.R - ti.r0);
     // four features of a row a thread; the CTAs' sums are added in order
     for (int32_t i = (int32_t)part * kThreads + threadIdx.x; i < rows * 32 && !gave_up; i += p.split * kThreads) {
@@ -355,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (f >= p.F) continue;
       float v[4] = {};
       for (int c = 0; c < p.split; ++c) {
-        const float4 x = peer_float4(peer_addr(sm + i * 16, c));
+        const float4 x = peer_float4(peer_addr(sm + i * 16, c * CG + cta));
         v[0] += x.x;
         v[1] += x.y;
         v[2] += x.z;
@@ -387,16 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int CG, bool P_MN, bool Q_MN>
+template <int CG, bool P_MN, bool Q_MN, bool CHAIN>
 cudaError_t launch(const Plan& p, const Maps& m, int32_t units, cudaStream_t s) {
   static std::atomic<bool> configured[kMaxDevices];
-  const cudaError_t e = raise_smem_limit(linear_kernel<CG, P_MN, Q_MN>, kSmem - kBarBytes, configured);
+  const cudaError_t e = raise_smem_limit(linear_kernel<CG, P_MN, Q_MN, CHAIN>, kSmem - kBarBytes, configured);
   if (e != cudaSuccess) return e;
-  const uint32_t cluster = CG == 2 ? 2 : (uint32_t)p.split;
+  const uint32_t cluster = (uint32_t)(CG * p.split);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units * cluster);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 1024 + p.stages * p.stage_bytes;
+  cfg.dynamicSmemBytes = 1024 + p.stages * p.stage_bytes + 2 * kEpilogueWarps * p.slot_bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -406,12 +524,12 @@ cudaError_t launch(const Plan& p, const Maps& m, int32_t units, cudaStream_t s) 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<CG, P_MN, Q_MN>, m, p);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<CG, P_MN, Q_MN, CHAIN>, m, p);
 }
-template <int CG>
-cudaError_t launch_cg(bool p_mn, bool q_mn, const Plan& p, const Maps& m, int32_t units, cudaStream_t s) {
-  if (p_mn) return q_mn ? launch<CG, true, true>(p, m, units, s) : launch<CG, true, false>(p, m, units, s);
-  return q_mn ? cudaErrorInvalidValue : launch<CG, false, false>(p, m, units, s);
+template <int CG, bool CHAIN>
+cudaError_t launch_as(bool p_mn, bool q_mn, const Plan& p, const Maps& m, int32_t units, cudaStream_t s) {
+  if (p_mn) return q_mn ? launch<CG, true, true, CHAIN>(p, m, units, s) : launch<CG, true, false, CHAIN>(p, m, units, s);
+  return q_mn ? cudaErrorInvalidValue : launch<CG, false, false, CHAIN>(p, m, units, s);
 }
 
 // An operand of `outer` features or rows and C columns, in boxes of `box` of them by 64 columns.
@@ -420,12 +538,77 @@ cudaError_t operand_map(CUtensorMap* map, const LinearOperand& o, int32_t outer,
                    : make_tmap_bf16(map, o.data, outer, C, o.stride, 64, 64);
 }
 
+// How many clusters of each size the device holds at once, asked for once a device.
+cudaError_t held_clusters(int32_t (&held)[kMaxCluster + 1]) {
+  static std::atomic<int32_t> known[kMaxDevices][kMaxCluster + 1];
+  static std::atomic<bool> configured[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!known[dev][kMaxCluster].load(std::memory_order_acquire)) {
+    e = raise_smem_limit(linear_kernel<1, false, false, false>, kSmem - kBarBytes, configured);
+    for (int n = 1; n <= kMaxCluster && e == cudaSuccess; ++n) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)n);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kSmem - kBarBytes;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = (unsigned)n;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int most = 0;
+      e = cudaOccupancyMaxActiveClusters(&most, linear_kernel<1, false, false, false>, &cfg);
+      if (e == cudaSuccess) known[dev][n].store(std::max(most, 1), std::memory_order_release);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  for (int n = 1; n <= kMaxCluster; ++n) held[n] = known[dev][n].load(std::memory_order_acquire);
+  if (getenv("LINEAR_SHOW")) { for (int n = 1; n <= kMaxCluster; ++n) printf("clusters of %d: %d\n", n, held[n]); }
+  return cudaSuccess;
+}
+
+struct Shape {
+  int32_t cg, rows, split;
+};
+// The tiles that should take least, in clocks: a block of 64 columns costs an SM 2 clocks a row of its tile for the
+// products or its bytes from L2 (64 a clock), whichever is more; a tile its start and its epilogue; a split the meeting of
+// its sums.
+Shape choose(int32_t R, int32_t F, int32_t blocks, bool q_mn, bool f32, const int32_t (&clusters)[kMaxCluster + 1]) {
+  if (const char* force = getenv("LINEAR_FORCE")) {
+    Shape s = {};
+    if (sscanf(force, "%d,%d,%d", &s.cg, &s.rows, &s.split) == 3) { s.split = std::max(1, std::min(s.split, blocks)); return s; }
+  }
+  static const int32_t kRows[] = {16, 32, 64, 96, 128, 160, 192, 224, 256};
+  Shape best = {};
+  double least = 0;
+  for (int cg = 1; cg <= 2; ++cg)
+    for (const int32_t rows : kRows) {
+      if (rows % (16 * cg) || (f32 && blocks > kChain && rows > kChainRows) || (q_mn && rows < 64 * cg)) continue;
+      if (rows >= 2 * R && rows > 64 * cg) continue;
+      const int64_t tiles = (int64_t)((R + rows - 1) / rows) * ((F + 128 * cg - 1) / (128 * cg));
+      const int32_t held = rows / cg, units = clusters[cg];
+      const double block = std::max(2.0 * rows, (16384.0 + 128.0 * (q_mn ? (held + 63) / 64 * 64 : held)) / 64);
+      for (int split = 1; split <= kMaxCluster / cg && split <= blocks; ++split) {
+        if (split > 1 && tiles > clusters[cg * split]) break;
+        const double waves = split > 1 ? 1 : (double)((tiles + units - 1) / units);
+        const double cost = waves * ((blocks + split - 1) / split * block + 1000) + 2000 + 16.0 * rows + (split > 1 ? 1500 + 16.0 * rows : 0);
+        if (!best.cg || cost < least) {
+          least = cost;
+          best = {cg, rows, split};
+        }
+      }
+    }
+  return best;
+}
+
 }  // namespace
 
 cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int32_t clusters[kMaxCluster + 1];
+  cudaError_t e = held_clusters(clusters);
   if (e != cudaSuccess) return e;
   Plan p = {};
   p.R = a.R;
@@ -434,31 +617,30 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
   p.terms = a.terms;
   p.e = a.finish;
   p.split = 1;
-  int cg = 1;
-  const int64_t f128 = (a.F + 127) / 128;
-  if ((int64_t)(a.R + 255) / 256 * ((a.F + 255) / 256) >= sms / 2) {
-    cg = 2;
-    p.rows = 256;
-  } else {
-    const int32_t least = a.q[0].c_inner ? 16 : 64;
-    p.rows = least;
-    while (p.rows < 256 && p.rows < a.R && f128 * ((a.R + p.rows - 1) / p.rows) > sms / 2) p.rows *= 2;
-    while (p.rows < 64 && p.rows < a.R) p.rows *= 2;
-  }
-  const int32_t feats = 128 * cg;
+  const LinearFinish& f = a.finish;
+  const bool q_mn = !a.q[0].c_inner, p_mn = !a.p.c_inner;
+  const bool f32 = f.out_f32 || (f.z && f.z_f32);
+  const Shape shape = choose(a.R, a.F, p.KB * p.terms, q_mn, f32, clusters);
+  const int cg = shape.cg;
+  if (getenv("LINEAR_SHOW")) printf("R %d F %d blocks %d: cg %d rows %d split %d\n", a.R, a.F, p.KB * p.terms, shape.cg, shape.rows, shape.split);
+  p.rows = shape.rows;
+  p.split = shape.split;
+  const int32_t feats = 128 * cg, q_rows = q_mn ? (p.rows / cg + 63) / 64 * 64 : p.rows / cg;
   p.tiles_r = (a.R + p.rows - 1) / p.rows;
   const int64_t tiles = (int64_t)p.tiles_r * ((a.F + feats - 1) / feats);
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  if (tiles > INT32_MAX / kMaxCluster) return cudaErrorInvalidValue;
   p.tiles = (int32_t)tiles;
   p.group = std::min(8, p.tiles_r);
-  p.stage_bytes = kPBytes + (uint32_t)(p.rows / cg) * 128;
-  p.stages = std::min<int32_t>(kMaxStages, (kSmem - kBarBytes - 1024) / p.stage_bytes);
-  int32_t units = cg == 2 ? sms / 2 : sms;
-  if (cg == 1 && p.tiles < sms) {
-    p.split = (int32_t)std::min<int64_t>({kMaxSplit, sms / p.tiles, p.KB * p.terms});
-    p.split = std::max(p.split, 1);
+  p.stage_bytes = kPBytes + (uint32_t)q_rows * 128;
+  const int32_t units = p.split > 1 ? p.tiles : std::min(clusters[cg], p.tiles);
+  if (p.split == 1) {
+    p.z_at = 16 * 32 * (f.out_f32 ? 4 : 2);
+    p.slot_bytes = p.z_at + (f.z ? 16 * 32 * (f.z_f32 ? 4 : 2) : 0);
   }
-  units = p.split > 1 ? p.tiles : std::min(units, p.tiles);
+  p.stages = std::min<int32_t>(kMaxStages, (kSmem - kBarBytes - 1024 - 2 * kEpilogueWarps * p.slot_bytes) / p.stage_bytes);
+  const int32_t own = (p.KB * p.terms + p.split - 1) / p.split;
+  const bool chain = f32 && own > kChain;
+  p.chain = chain ? kChain : own;
   Maps m;
   e = operand_map(&m.p, a.p, a.F, a.C, 128);
   for (int i = 0; i < kLinearTerms && e == cudaSuccess; ++i) {
@@ -467,9 +649,14 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
     else
       m.q[i] = m.q[0];
   }
+  m.out = m.z = m.p;
+  if (p.split == 1) {
+    if (e == cudaSuccess) e = make_tmap_block(&m.out, f.out, f.out_f32, a.F, a.R, f.out_stride, 32, 16);
+    if (e == cudaSuccess && f.z) e = make_tmap_block(&m.z, f.z, f.z_f32, a.F, a.R, f.z_stride, 32, 16);
+  }
   if (e != cudaSuccess) return e;
-  return cg == 2 ? launch_cg<2>(!a.p.c_inner, !a.q[0].c_inner, p, m, units, s)
-                 : launch_cg<1>(!a.p.c_inner, !a.q[0].c_inner, p, m, units, s);
+  if (cg == 2) return chain ? launch_as<2, true>(p_mn, q_mn, p, m, units, s) : launch_as<2, false>(p_mn, q_mn, p, m, units, s);
+  return chain ? launch_as<1, true>(p_mn, q_mn, p, m, units, s) : launch_as<1, false>(p_mn, q_mn, p, m, units, s);
 }
 
 cudaError_t linear_mma_flags(int32_t* flags) {
