@@ -243,7 +243,7 @@ moe_status moe_qk_norm_rope(const moe_qk_args* args, moe_stream_t stream) {
 
 size_t moe_qk_workspace_bytes(int32_t n, int32_t q_heads, int32_t k_heads, int32_t head_dim) {
   if (n < 0 || q_heads < 0 || k_heads < 0 || head_dim <= 0 || head_dim > kQkMaxDim) return 0;
-  return (size_t)(kQkBackwardCtas + 2) * (size_t)head_dim * sizeof(float);
+  return (size_t)kQkBackwardCtas * 2 * (size_t)head_dim * sizeof(float);
 }
 
 moe_status moe_qk_norm_rope_backward(const moe_qk_args* args, const moe_qk_grads* grads, void* workspace,

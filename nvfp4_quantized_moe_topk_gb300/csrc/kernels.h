@@ -278,9 +278,9 @@ cudaError_t launch_lora(const moe_lora_args& a, void* workspace, cudaStream_t s)
 cudaError_t lora_device_flags(int32_t* flags);  // synchronizes the device; reads and clears
 
 constexpr int kQkMaxDim = 256;
-constexpr int kQkBackwardCtas = 608;  // CTAs of the backward pass, but for one a side at least
+constexpr int kQkBackwardCtas = 640;  // CTAs of the backward pass, at most
 cudaError_t launch_qk_norm_rope(const moe_qk_args& a, cudaStream_t s);
-// part: [kQkBackwardCtas + 2][head_dim] floats, where a weight's gradient is wanted.
+// part: [kQkBackwardCtas][2][head_dim] floats, where a weight's gradient is wanted.
 cudaError_t launch_qk_norm_rope_backward(const moe_qk_args& a, const moe_qk_grads& d, float* part, cudaStream_t s);
 
 constexpr int32_t kLinearMaxFeatures = 1 << 24;

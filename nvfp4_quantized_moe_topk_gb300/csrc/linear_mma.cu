@@ -27,7 +27,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 384, kEpilogueWarps = 8;  // warp 0: copies, 1: products, 2: tensor memory, 4..11: epilogue
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
 constexpr uint32_t kSmem = 227 * 1024, kBarBytes = 1024;
 constexpr uint32_t kPBytes = 128 * 128;  // a stage's features: 128 of 64 columns
 constexpr int kMaxCluster = 8;
@@ -75,23 +75,13 @@ __device__ __forceinline__ float4 peer_float4(uint32_t addr) {
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-      : "memory");
-  return ok != 0;
-}
 // Bounded wait that also gives up when another role of the CTA has.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  if (try_wait_cluster(bar, parity, 0)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     for (int i = 0; i < 8; ++i)
-      if (try_wait_cluster(bar, parity, 1000u)) return true;
+      if (mbar_try_wait_sleep(bar, parity, 1000u)) return true;
     if (*gave_up) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *gave_up = 1;
@@ -161,6 +151,17 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(8192u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Warps 1 and 2 meet; whether warp 2 gave up.
+__device__ __forceinline__ bool hand_over(bool gave_up) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, 64, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)gave_up)
+      : "memory");
+  return r != 0;
 }
 
 struct Maps {
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t t = unit; t < p.tiles && ok; t += units) {
         const Tile ti = tile_at(p, t, 128 * CG);
         const int32_t f = ti.f0 + 128 * cta, r = ti.r0 + my_rows * cta;
+        int32_t term = kb0 / p.KB, c = (kb0 - term * p.KB) * 64;
         for (int32_t kb = kb0; kb < kb1; ++kb) {
           if (!wait_for(&empty[s], ph ^ 1u, &gave_up)) {
             ok = false;
@@ -311,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = CG == 2 ? peer_addr(&full[s], first_cta) : smem_u32(&full[s]);
           if (cta == 0) mbar_arrive_expect_tx(&full[s], CG * p.stage_bytes);
           const uint32_t at = smem_u32(sm) + s * p.stage_bytes;
-          const int32_t term = kb / p.KB, c = (kb - term * p.KB) * 64;
           const CUtensorMap* mq = &maps.q[term];
           if (P_MN) {
             load_2d<CG>(at, &maps.p, f, c, bar);
@@ -323,6 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int32_t j = 0; j < my_rows; j += 64) load_2d<CG>(at + kPBytes + j * 128, mq, r + j, c, bar);
           } else {
             load_2d<CG>(at + kPBytes, mq, c, r, bar);
+          }
+          if ((c += 64) >= 64 * p.KB) {
+            c = 0;
+            ++term;
           }
           if (++s == p.stages) {
             s = 0;
@@ -338,42 +343,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1 && cta == 0) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(128 * CG, (uint32_t)p.rows) | (P_MN ? 1u << 15 : 0u) | (Q_MN ? 1u << 16 : 0u);
-      int s = 0, it = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int32_t t = unit; t < p.tiles && ok; t += units, ++it) {
-        uint32_t acc = 0;
-        for (int32_t kb = kb0; kb < kb1 && ok; ++kb) {
-          const bool first = kb == kb0 || (CHAIN && (kb - kb0) % p.chain == 0);
-          if (first) {
-            if (kb != kb0) {
-              commit<CG>(&t_full[acc], first_cta);
-              ++it;
-            }
-            acc = it & 1;
-            ok = wait_for(&t_empty[acc], ((it >> 1) & 1) ^ 1u, &gave_up);
-            if (!ok) break;
-          }
-          ok = wait_for(&full[s], ph, &gave_up);
-          if (!ok) break;
+    // A shared-memory access by the thread that issues the products waits until those before it have read their operands;
+    // so this warp makes none: warp 2 waits on the barriers and hands each block of 64 columns over.
+    const uint32_t idesc = idesc_bf16(128 * CG, (uint32_t)p.rows) | (P_MN ? 1u << 15 : 0u) | (Q_MN ? 1u << 16 : 0u);
+    const uint64_t desc_p = P_MN ? smem_desc_mn128(smem_u32(sm)) : smem_desc_k128(smem_u32(sm));
+    const uint64_t desc_q = Q_MN ? smem_desc_mn128(smem_u32(sm) + kPBytes) : smem_desc_k128(smem_u32(sm) + kPBytes);
+    int s = 0, it = 0;
+    bool ok = true;
+    for (int32_t t = unit; t < p.tiles && ok; t += units, ++it) {
+      for (int32_t kb = kb0; kb < kb1; ++kb) {
+        const bool first = kb == kb0 || (CHAIN && (kb - kb0) % p.chain == 0);
+        if (first && kb != kb0) {
+          if (lane == 0) commit<CG>(&t_full[it & 1], first_cta);
+          ++it;
+        }
+        ok = !hand_over(false);
+        if (!ok) break;
+        if (lane == 0) {
           tc_fence_after();
-          const uint32_t a = smem_u32(sm) + s * p.stage_bytes, b = a + kPBytes;
+          const uint64_t at = (uint64_t)((uint32_t)(s * p.stage_bytes) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma<CG>(tmem + acc * p.rows, P_MN ? smem_desc_mn128(a + 2048 * k) : smem_desc_k128(a + 32 * k),
-                    Q_MN ? smem_desc_mn128(b + 2048 * k) : smem_desc_k128(b + 32 * k), idesc, !first || k != 0);
+            mma<CG>(tmem + (it & 1) * p.rows, desc_p + at + (P_MN ? 128 : 2) * k, desc_q + at + (Q_MN ? 128 : 2) * k,
+                    idesc, !first || k != 0);
           commit<CG>(&empty[s], first_cta);
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-        if (ok) commit<CG>(&t_full[acc], first_cta);
+        if (++s == p.stages) s = 0;
       }
+      if (ok && lane == 0) commit<CG>(&t_full[it & 1], first_cta);
     }
     __syncwarp();
+  } else if (warp == 2 && cta == 0) {
+    int s = 0, it = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int32_t t = unit; t < p.tiles && ok; t += units, ++it) {
+      for (int32_t kb = kb0; kb < kb1 && ok; ++kb) {
+        const bool first = kb == kb0 || (CHAIN && (kb - kb0) % p.chain == 0);
+        if (first && kb != kb0) ++it;
+        if (lane == 0) {
+          if (first) ok = wait_for(&t_empty[it & 1], ((it >> 1) & 1) ^ 1u, &gave_up);
+          ok = ok && wait_for(&full[s], ph, &gave_up);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (hand_over(!ok)) break;
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
@@ -638,9 +657,12 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
     p.slot_bytes = p.z_at + (f.z ? 16 * 32 * (f.z_f32 ? 4 : 2) : 0);
   }
   p.stages = std::min<int32_t>(kMaxStages, (kSmem - kBarBytes - 1024 - 2 * kEpilogueWarps * p.slot_bytes) / p.stage_bytes);
+  // (the sums of a cluster meet where the stages were)
+  if (p.split > 1 && (uint32_t)p.rows * 512 > p.stages * p.stage_bytes) return cudaErrorInvalidConfiguration;
   const int32_t own = (p.KB * p.terms + p.split - 1) / p.split;
-  const bool chain = f32 && own > kChain;
-  p.chain = chain ? kChain : own;
+  const int32_t kc = getenv("LINEAR_CHAIN") ? atoi(getenv("LINEAR_CHAIN")) : kChain;
+  const bool chain = f32 && own > kc;
+  p.chain = chain ? kc : own;
   Maps m;
   e = operand_map(&m.p, a.p, a.F, a.C, 128);
   for (int i = 0; i < kLinearTerms && e == cudaSuccess; ++i) {

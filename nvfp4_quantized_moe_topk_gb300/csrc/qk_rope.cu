@@ -12,149 +12,295 @@ namespace moe {
 
 namespace {
 
+// Slots of a warp's ring, for the forward's one array or the backward's two.
+template <typename T>
+constexpr int qk_stages(int arrays) {
+  return sizeof(T) == 2 ? (arrays == 1 ? 6 : 4) : (arrays == 1 ? 4 : 3);
+}
+
+// A warp's way through its work: items of one token's steps (the queries', then the keys', kHeads heads a step), cut
+// into slices, every jump-th item its own.
+struct QkWalk {
+  int64_t item;
+  int32_t token, st, end;  // the steps of the token, in both sides' count
+};
+struct QkPlan {
+  int64_t items, jump;
+  int32_t slices, q_steps, steps;
+};
+template <int GROUP>
+__device__ __forceinline__ QkPlan plan_of(const QkParams& a, int32_t slices) {
+  constexpr int kHeads = 32 / GROUP;
+  QkPlan p;
+  p.slices = slices;
+  p.items = (int64_t)a.n * slices;
+  p.jump = (int64_t)gridDim.x * kQkWarps;
+  p.q_steps = (a.side[0].heads + kHeads - 1) / kHeads;
+  p.steps = p.q_steps + (a.side[1].heads + kHeads - 1) / kHeads;
+  return p;
+}
+__device__ __forceinline__ void enter(const QkPlan& p, QkWalk& w) {
+  if (w.item >= p.items) return;
+  w.token = (int32_t)(w.item / p.slices);
+  const int32_t slice = (int32_t)(w.item - (int64_t)w.token * p.slices);
+  w.st = (int32_t)((int64_t)p.steps * slice / p.slices);
+  w.end = (int32_t)((int64_t)p.steps * (slice + 1) / p.slices);
+}
+__device__ __forceinline__ void advance(const QkPlan& p, QkWalk& w) {
+  if (++w.st < w.end) return;
+  w.item += p.jump;
+  enter(p, w);
+}
+// The lane's head at a step, where it starts in each array, and whether it is there.
+struct QkHead {
+  int32_t which, head;
+  bool live;
+};
+template <int GROUP>
+__device__ __forceinline__ QkHead head_at(const QkParams& a, const QkPlan& p, const QkWalk& w, int sub) {
+  QkHead h;
+  h.which = w.st >= p.q_steps;
+  h.head = (w.st - (h.which ? p.q_steps : 0)) * (32 / GROUP) + sub;
+  h.live = h.head < a.side[h.which].heads;
+  return h;
+}
+template <typename T>
+__device__ __forceinline__ T* head_ptr(const QkParams& a, const moe_rows& r, const QkHead& h, int32_t token) {
+  return row_ptr<T>(r, token, (int64_t)a.side[h.which].heads * a.D) + (int64_t)h.head * a.D;
+}
+
 template <typename T, int GROUP, bool INTERLEAVED>
-__global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const QkParams a, int32_t slices) {
+__global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const __grid_constant__ QkParams a, int32_t slices) {
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ QkTable table;
-  constexpr int kHeads = 32 / GROUP;  // heads a step
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / GROUP;
+  __shared__ __align__(16) QkTurns turns[kQkWarps];
+  constexpr int kStages = qk_stages<T>(1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / GROUP, unit = lane % GROUP;
+  const QkUnit u = unit_of<INTERLEAVED>(unit, a.D, a.rot);
+  const QkPlan plan = plan_of<GROUP>(a, slices);
+  const uint32_t slots = smem_u32(ring) + warp * kStages * kQkSlot<T>;
+  pdl_wait();
+  pdl_launch_dependents();
+  QkWalk ahead = {(int64_t)blockIdx.x * kQkWarps + warp};
+  enter(plan, ahead);
+  QkWalk w = ahead;
+  auto fetch = [&](int stage) {
+    if (ahead.item < plan.items) {
+      const QkHead h = head_at<GROUP>(a, plan, ahead, sub);
+      qk_fetch(slots + stage * kQkSlot<T>, lane, head_ptr<const T>(a, a.side[h.which].in, h, ahead.token), u, h.live);
+      advance(plan, ahead);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i + 1 < kStages; ++i) fetch(i);
   fill_table(a, table);
   __syncthreads();
-  const QkUnit u = unit_of<INTERLEAVED>(lane % GROUP, a.D, a.rot);
-  const int32_t steps0 = (a.side[0].heads + kHeads - 1) / kHeads, steps1 = (a.side[1].heads + kHeads - 1) / kHeads;
-  const int64_t items = (int64_t)a.n * slices, jump = (int64_t)gridDim.x * kQkWarps;
-  for (int64_t item = (int64_t)blockIdx.x * kQkWarps + warp; item < items; item += jump) {
-    const int32_t t = (int32_t)(item / slices), slice = (int32_t)(item % slices);
-    const int32_t lo = (int32_t)((int64_t)(steps0 + steps1) * slice / slices);
-    const int32_t hi = (int32_t)((int64_t)(steps0 + steps1) * (slice + 1) / slices);
-    float c[8], s[8];
-    if (u.rotated)
+  // a pair's members (a, b) become r (a k0 + b k1), r (b k2 + a k3): weight and turn in one
+  float k[4][8];
+  int32_t token = -1, which = -1;
+  int stage = 0;
+  while (w.item < plan.items) {
+    const QkHead h = head_at<GROUP>(a, plan, w, sub);
+    const QkSide& side = a.side[h.which];
+    const bool norm = side.weight != nullptr;
+    if (w.token != token && a.rot > 0) fill_turns(a, table, w.token, lane, turns[warp]);
+    if (w.token != token || h.which != which) {
+      float wt[2][8], c[8], s[8];
+      if (norm) {
+        qk_weight(a, side.weight, u, wt);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) turn_of(a, table, 8 * (lane % GROUP) + j, t, c[j], s[j]);
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const QkSide& side = a.side[which];
-      const int32_t first = which ? max(lo - steps0, 0) : lo, last = which ? hi - steps0 : min(hi, steps0);
-      if (first >= last) continue;
-      float w[2][8];
-      if (side.weight) qk_weight(a, side.weight, u, w);
-      const T* in = row_ptr<const T>(side.in, t, (int64_t)side.heads * a.D);
-      T* out = row_ptr<T>(side.out, t, (int64_t)side.heads * a.D);
-      for (int32_t st = first; st < last; ++st) {
-        const int32_t head = st * kHeads + sub;
-        const bool live = head < side.heads;
-        float v[2][8];
-        qk_values(qk_load(in + (int64_t)head * a.D, u, live), v);
-        if (side.weight) {
-          float ss = 0.f;
+        for (int j = 0; j < 8; ++j) wt[0][j] = wt[1][j] = 1.f;
+      }
+      if (u.rotated) {
+        load8(turns[warp].c + 8 * unit, c);
+        load8(turns[warp].s + 8 * unit, s);
+      }
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+      for (int j = 0; j < 8; ++j) {
+        const float wa = member<INTERLEAVED>(wt, 0, j), wb = member<INTERLEAVED>(wt, 1, j);
+        k[0][j] = u.rotated ? wa * c[j] : wa;
+        k[1][j] = u.rotated ? -wb * s[j] : 0.f;
+        k[2][j] = u.rotated ? wb * c[j] : wb;
+        k[3][j] = u.rotated ? wa * s[j] : 0.f;
+      }
+      token = w.token;
+      which = h.which;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    float v[2][8];
+    qk_values(qk_slot<T>(slots + stage * kQkSlot<T>, lane, u, h.live), v);
+    fetch(stage == 0 ? kStages - 1 : stage - 1);  // into the slot of the step before
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    float r = 1.f;
+    if (norm) {
+      float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v[h][j], v[h][j], ss);
-          const float r = rsqrtf(group_sum<GROUP>(ss) * a.inv_D + a.eps);
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[m][j], v[m][j], ss);
+      r = rsqrtf(group_sum<GROUP>(ss) * a.inv_D + a.eps);
+    }
+    if (u.rotated) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[h][j] = v[h][j] * r * w[h][j];
-        }
-        if (u.rotated) qk_turn<INTERLEAVED>(v, c, s, 1.f);
-        if (live) qk_store(out + (int64_t)head * a.D, u, v);
+      for (int j = 0; j < 8; ++j) {
+        float &x = member<INTERLEAVED>(v, 0, j), &y = member<INTERLEAVED>(v, 1, j);
+        const float t = r * fmaf(y, k[1][j], x * k[0][j]);
+        y = r * fmaf(x, k[3][j], y * k[2][j]);
+        x = t;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        member<INTERLEAVED>(v, 0, j) *= r * k[0][j];
+        member<INTERLEAVED>(v, 1, j) *= r * k[2][j];
       }
     }
+    if (h.live) qk_store(head_ptr<T>(a, side.out, h, w.token), u, v);
+    advance(plan, w);
   }
 }
 
-// d_weight of one side: the lanes' sums over their heads and tokens, added over the CTA's warps and groups in order.
+// d_weight: the lanes' sums over a token's heads, kept in shared memory from one token to the next and added over the
+// CTA's warps and groups in order at the end.
 template <typename T, int GROUP, bool INTERLEAVED>
 __global__ void __launch_bounds__(kQkThreads)
-    qk_rope_backward_kernel(const QkParams a, int32_t ctas0, float* __restrict__ part) {
+    qk_rope_backward_kernel(const __grid_constant__ QkParams a, int32_t slices, float* __restrict__ part) {
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ QkTable table;
-  __shared__ float sums[kQkWarps][16][33];
-  constexpr int kHeads = 32 / GROUP;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / GROUP;
-  const int which = (int)blockIdx.x >= ctas0;
-  const int32_t cta = which ? blockIdx.x - ctas0 : blockIdx.x, ctas = which ? gridDim.x - ctas0 : ctas0;
-  const QkSide& side = a.side[which];
+  __shared__ __align__(16) QkTurns turns[kQkWarps];
+  __shared__ float sums[2][kQkWarps][16][33];
+  constexpr int kHeads = 32 / GROUP, kStages = qk_stages<T>(2);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / GROUP, unit = lane % GROUP;
+  const QkUnit u = unit_of<INTERLEAVED>(unit, a.D, a.rot);
+  const QkPlan plan = plan_of<GROUP>(a, slices);
+  const uint32_t slots = smem_u32(ring) + warp * kStages * 2 * kQkSlot<T>;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sums[0][warp][i][lane] = sums[1][warp][i][lane] = 0.f;
+  pdl_wait();
+  pdl_launch_dependents();
+  QkWalk ahead = {(int64_t)blockIdx.x * kQkWarps + warp};
+  enter(plan, ahead);
+  QkWalk w = ahead;
+  auto fetch = [&](int stage) {
+    if (ahead.item < plan.items) {
+      const QkHead h = head_at<GROUP>(a, plan, ahead, sub);
+      const QkSide& side = a.side[h.which];
+      const uint32_t slot = slots + stage * 2 * kQkSlot<T>;
+      qk_fetch(slot, lane, head_ptr<const T>(a, side.grad, h, ahead.token), u, h.live);
+      if (side.weight)
+        qk_fetch(slot + kQkSlot<T>, lane, head_ptr<const T>(a, side.in, h, ahead.token), u, h.live);
+      advance(plan, ahead);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i + 1 < kStages; ++i) fetch(i);
   fill_table(a, table);
   __syncthreads();
-  const QkUnit u = unit_of<INTERLEAVED>(lane % GROUP, a.D, a.rot);
-  const int32_t steps = (side.heads + kHeads - 1) / kHeads;
-  const int64_t items = (int64_t)a.n * steps;
-  float w[2][8], acc[2][8] = {};
-  if (side.weight) qk_weight(a, side.weight, u, w);
-  // every warp a run of (token, step) items, so that it computes a token's angles once
-  const int64_t of = (int64_t)ctas * kQkWarps, me = (int64_t)cta * kQkWarps + warp;
-  const int64_t begin = items * me / of, end = items * (me + 1) / of;
-  float c[8], s[8];
-  int32_t have = -1;
-  for (int64_t item = begin; item < end; ++item) {
-    const int32_t t = (int32_t)(item / steps), head = (int32_t)(item % steps) * kHeads + sub;
-    if (t != have && u.rotated) {
+  float wt[2][8], c[8], s[8], acc[2][8] = {};
+  int32_t token = -1, which = 0;
+  auto keep = [&]() {  // the sums of the side that ends
+    if (!part || !a.side[which].weight) return;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) turn_of(a, table, 8 * (lane % GROUP) + j, t, c[j], s[j]);
+    for (int i = 0; i < 16; ++i) {
+      sums[which][warp][i][lane] += acc[i / 8][i % 8];
+      acc[i / 8][i % 8] = 0.f;
     }
-    have = t;
-    const bool live = head < side.heads;
-    const int64_t cols = (int64_t)side.heads * a.D, at = (int64_t)head * a.D;
-    float g[2][8];
-    qk_values(qk_load(row_ptr<const T>(side.grad, t, cols) + at, u, live), g);
-    if (side.weight) {
-      float v[2][8];
-      qk_values(qk_load(row_ptr<const T>(side.in, t, cols) + at, u, live), v);
-      if (u.rotated) qk_turn<INTERLEAVED>(g, c, s, -1.f);
+  };
+  int stage = 0;
+  while (w.item < plan.items) {
+    const QkHead h = head_at<GROUP>(a, plan, w, sub);
+    const QkSide& side = a.side[h.which];
+    const bool norm = side.weight != nullptr;
+    if (w.token != token || h.which != which) {
+      if (token >= 0) keep();
+      if (w.token != token && a.rot > 0) {
+        fill_turns(a, table, w.token, lane, turns[warp]);
+        if (u.rotated) {
+          load8(turns[warp].c + 8 * unit, c);
+          load8(turns[warp].s + 8 * unit, s);
+        }
+      }
+      if (norm) qk_weight(a, side.weight, u, wt);
+      token = w.token;
+      which = h.which;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    float g[2][8], v[2][8];
+    const uint32_t slot = slots + stage * 2 * kQkSlot<T>;
+    qk_values(qk_slot<T>(slot, lane, u, h.live), g);
+    qk_values(qk_slot<T>(slot + kQkSlot<T>, lane, u, h.live && norm), v);
+    fetch(stage == 0 ? kStages - 1 : stage - 1);  // into the slot of the step before
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    if (u.rotated) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float &x = member<INTERLEAVED>(g, 0, j), &y = member<INTERLEAVED>(g, 1, j);
+        const float t = fmaf(y, s[j], x * c[j]);
+        y = fmaf(-x, s[j], y * c[j]);
+        x = t;
+      }
+    }
+    if (norm) {
       float ss = 0.f, dot = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          ss = fmaf(v[h][j], v[h][j], ss);
-          dot = fmaf(g[h][j] * w[h][j], v[h][j], dot);
+          ss = fmaf(v[m][j], v[m][j], ss);
+          dot = fmaf(g[m][j] * wt[m][j], v[m][j], dot);
         }
       ss = group_sum<GROUP>(ss);
       dot = group_sum<GROUP>(dot);
-      const float r = rsqrtf(ss * a.inv_D + a.eps), m = r * dot * a.inv_D;
+      const float r = rsqrtf(ss * a.inv_D + a.eps), mean = r * dot * a.inv_D;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float y = v[h][j] * r;
-          acc[h][j] = fmaf(g[h][j], y, acc[h][j]);
-          g[h][j] = r * (g[h][j] * w[h][j] - y * m);
+          const float y = v[m][j] * r;
+          acc[m][j] = fmaf(g[m][j], y, acc[m][j]);
+          g[m][j] = r * fmaf(-y, mean, g[m][j] * wt[m][j]);
         }
-    } else if (u.rotated) {
-      qk_turn<INTERLEAVED>(g, c, s, -1.f);
     }
-    if (live && side.out.data) qk_store(row_ptr<T>(side.out, t, cols) + at, u, g);
+    if (h.live && side.out.data) qk_store(head_ptr<T>(a, side.out, h, w.token), u, g);
+    advance(plan, w);
   }
-  if (!side.weight || !part) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) sums[warp][i][lane] = acc[i / 8][i % 8];
+  if (token >= 0) keep();
+  if (!part) return;
   __syncthreads();
-  // part[CTA][D]: thread i of the unit's 16 elements adds the warps and their groups
-  for (int32_t e = threadIdx.x; e < 16 * GROUP; e += kQkThreads) {
-    const QkUnit v = unit_of<INTERLEAVED>(e / 16, a.D, a.rot);
-    const int32_t at = v.at[(e % 16) / 8];
+  // part[CTA][side][D]: a thread a side's element
+  for (int32_t e = threadIdx.x; e < 2 * 16 * GROUP; e += kQkThreads) {
+    const int32_t side = e / (16 * GROUP), in = e % (16 * GROUP);
+    const QkUnit v = unit_of<INTERLEAVED>(in / 16, a.D, a.rot);
+    const int32_t at = v.at[(in % 16) / 8];
     if (at < 0) continue;
     float x = 0.f;
+#pragma unroll
     for (int k = 0; k < kQkWarps; ++k)
-      for (int q = 0; q < kHeads; ++q) x += sums[k][e % 16][q * GROUP + e / 16];
-    part[(int64_t)blockIdx.x * a.D + at + e % 8] = x;
+#pragma unroll
+      for (int q = 0; q < kHeads; ++q) x += sums[side][k][in % 16][q * GROUP + in / 16];
+    part[((int64_t)blockIdx.x * 2 + side) * a.D + at + in % 8] = x;
   }
 }
 
 // Joins the CTAs' sums, 32 columns a CTA (blockIdx.y: the queries' or the keys').
 __global__ void __launch_bounds__(kJoinThreads)
-    qk_weight_sum_kernel(const float* __restrict__ part, int32_t ctas0, int32_t ctas, int32_t D, float* d_q, float* d_k) {
+    qk_weight_sum_kernel(const float* __restrict__ part, int32_t ctas, int32_t D, float* d_q, float* d_k) {
   __shared__ float sum[kJoinWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y;
   float* to = which ? d_k : d_q;
   if (!to) return;
   const int32_t c = blockIdx.x * 32 + lane, mine = blockIdx.x * 32 + warp;
   pdl_wait();
-  sum[warp][lane] = join_part<10>(part, which ? ctas0 : 0, (which ? ctas : ctas0) - 1, D, c, c < D);
+  sum[warp][lane] = join_part<10>(part + (int64_t)which * D, 0, ctas - 1, 2 * D, c, c < D);
   __syncthreads();
   const float v = join_parts(sum);
   if (lane == 0 && mine < D) to[mine] = v;
 }
+
+constexpr int64_t kQkItems = 4;
 
 int qk_sms() {
   int dev = 0, sms = 0;
@@ -184,34 +330,62 @@ QkParams qk_params(const moe_qk_args& a) {
   return p;
 }
 
+// CTAs that an SM holds, asked for once a device.
+template <typename Kernel>
+cudaError_t resident(Kernel* kernel, size_t smem, std::atomic<int32_t> (&known)[kMaxDevices], int32_t* ctas) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  int32_t v = known[dev].load(std::memory_order_acquire);
+  if (!v) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, kQkThreads, smem);
+    if (e != cudaSuccess) return e;
+    v = std::max(v, 1) * qk_sms();
+    known[dev].store(v, std::memory_order_release);
+  }
+  *ctas = v;
+  return cudaSuccess;
+}
+
+// Slices of a token's steps: enough that each warp has a few items, so that they come out even.
+int32_t qk_slices(const QkParams& p, int32_t heads, int64_t warps) {
+  const int32_t steps = (p.side[0].heads + heads - 1) / heads + (p.side[1].heads + heads - 1) / heads;
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>(steps, kQkItems * warps / p.n));
+}
+
 template <typename T, int GROUP, bool INTERLEAVED>
 cudaError_t qk_forward(const QkParams& p, cudaStream_t s) {
-  constexpr int kHeads = 32 / GROUP;
-  const int32_t steps = (p.side[0].heads + kHeads - 1) / kHeads + (p.side[1].heads + kHeads - 1) / kHeads;
-  const int64_t wave = (int64_t)qk_sms() * 4 * kQkWarps;
-  const int32_t slices = (int32_t)std::max<int64_t>(1, std::min<int64_t>(steps, wave / p.n));
-  const int64_t ctas = ((int64_t)p.n * slices + kQkWarps - 1) / kQkWarps;
-  qk_rope_kernel<T, GROUP, INTERLEAVED><<<(unsigned)std::min<int64_t>(ctas, qk_sms() * 8), kQkThreads, 0, s>>>(p, slices);
-  return cudaGetLastError();
+  static std::atomic<bool> configured[kMaxDevices];
+  static std::atomic<int32_t> known[kMaxDevices];
+  const size_t smem = (size_t)kQkWarps * qk_stages<T>(1) * kQkSlot<T>;
+  cudaError_t e = raise_smem_limit(qk_rope_kernel<T, GROUP, INTERLEAVED>, (int)smem, configured);
+  int32_t most = 0;
+  if (e == cudaSuccess) e = resident(qk_rope_kernel<T, GROUP, INTERLEAVED>, smem, known, &most);
+  if (e != cudaSuccess) return e;
+  const int32_t slices = qk_slices(p, 32 / GROUP, (int64_t)most * kQkWarps);
+  const int64_t ctas = std::min<int64_t>(((int64_t)p.n * slices + kQkWarps - 1) / kQkWarps, most);
+  return launch_ex(qk_rope_kernel<T, GROUP, INTERLEAVED>, dim3((unsigned)ctas), dim3(kQkThreads), smem, s, true, p, slices);
 }
 
 template <typename T, int GROUP, bool INTERLEAVED>
 cudaError_t qk_backward(const QkParams& p, float* d_q_weight, float* d_k_weight, float* part, cudaStream_t s) {
-  constexpr int kHeads = 32 / GROUP;
-  int32_t ctas[2];
-  const int64_t all = (int64_t)p.side[0].heads + p.side[1].heads;
-  for (int i = 0; i < 2; ++i) {
-    const int64_t items = (int64_t)p.n * ((p.side[i].heads + kHeads - 1) / kHeads);
-    const int64_t share = std::max<int64_t>(1, (int64_t)kQkBackwardCtas * p.side[i].heads / all);
-    ctas[i] = (int32_t)std::min((items + kQkWarps - 1) / kQkWarps, share);
-  }
+  static std::atomic<bool> configured[kMaxDevices];
+  static std::atomic<int32_t> known[kMaxDevices];
+  const size_t smem = (size_t)kQkWarps * qk_stages<T>(2) * 2 * kQkSlot<T>;
+  cudaError_t e = raise_smem_limit(qk_rope_backward_kernel<T, GROUP, INTERLEAVED>, (int)smem, configured);
+  int32_t most = 0;
+  if (e == cudaSuccess) e = resident(qk_rope_backward_kernel<T, GROUP, INTERLEAVED>, smem, known, &most);
+  if (e != cudaSuccess) return e;
+  most = std::min(most, kQkBackwardCtas);
+  const int32_t slices = qk_slices(p, 32 / GROUP, (int64_t)most * kQkWarps);
+  const int32_t ctas = (int32_t)std::min<int64_t>(((int64_t)p.n * slices + kQkWarps - 1) / kQkWarps, most);
   const bool sums = d_q_weight || d_k_weight;
-  qk_rope_backward_kernel<T, GROUP, INTERLEAVED>
-      <<<(unsigned)(ctas[0] + ctas[1]), kQkThreads, 0, s>>>(p, ctas[0], sums ? part : nullptr);
-  cudaError_t e = cudaGetLastError();
+  e = launch_ex(qk_rope_backward_kernel<T, GROUP, INTERLEAVED>, dim3((unsigned)ctas), dim3(kQkThreads), smem, s, true, p,
+                slices, sums ? part : nullptr);
   if (e != cudaSuccess || !sums) return e;
-  return launch_ex(qk_weight_sum_kernel, dim3((p.D + 31) / 32, 2), dim3(kJoinThreads), 0, s, true, (const float*)part,
-                   ctas[0], ctas[0] + ctas[1], p.D, d_q_weight, d_k_weight);
+  return launch_ex(qk_weight_sum_kernel, dim3((p.D + 31) / 32, 2), dim3(kJoinThreads), 0, s, true, (const float*)part, ctas,
+                   p.D, d_q_weight, d_k_weight);
 }
 
 // Calls f<T, GROUP, INTERLEAVED>.

@@ -21,7 +21,7 @@
 
 namespace moe {
 
-constexpr int kQkThreads = 256, kQkWarps = kQkThreads / 32;
+constexpr int kQkThreads = 128, kQkWarps = kQkThreads / 32;
 constexpr int kQkMaxPairs = kQkMaxDim / 2;
 
 struct QkSide {  // the queries or the keys
@@ -64,14 +64,33 @@ __device__ __forceinline__ void fill_table(const QkParams& a, QkTable& t) {
     t.axis[i] = axis_of_pair(a, i);
   }
 }
-// cos and sin of a token's pair, times the rotation's scale.
-__device__ __forceinline__ void turn_of(const QkParams& a, const QkTable& t, int32_t i, int32_t token, float& c, float& s) {
-  const int64_t p = a.positions[(int64_t)t.axis[i] * a.n + token];
-  // the upper 32 bits of the part of a turn, signed: half turns in [-1, 1)
-  const float half_turns = (float)(int32_t)(((uint64_t)p * t.step[i]) >> 32) * 0x1p-31f;
-  sincospif(half_turns, &s, &c);
-  c *= a.scale;
-  s *= a.scale;
+// cos and sin of a token's pairs, times the rotation's scale, by one warp for itself: [pairs] cosines, [pairs] sines.
+struct QkTurns {
+  float c[kQkMaxPairs], s[kQkMaxPairs];
+};
+__device__ __forceinline__ void fill_turns(const QkParams& a, const QkTable& t, int32_t token, int lane, QkTurns& o) {
+  __syncwarp();
+  for (int32_t i = lane; i < a.rot / 2; i += 32) {
+    const int64_t p = __ldg(a.positions + (int64_t)t.axis[i] * a.n + token);
+    // the upper 32 bits of the part of a turn, signed: half turns in [-1, 1)
+    const float half_turns = (float)(int32_t)(((uint64_t)p * t.step[i]) >> 32) * 0x1p-31f;
+    float c, s;
+    sincospif(half_turns, &s, &c);
+    o.c[i] = c * a.scale;
+    o.s[i] = s * a.scale;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = a.z;
+  v[3] = a.w;
+  v[4] = b.x;
+  v[5] = b.y;
+  v[6] = b.z;
+  v[7] = b.w;
 }
 
 // A lane's 16 elements: two vectors of 8 at element offsets at[0], at[1] (< 0: not there).
@@ -91,19 +110,39 @@ __device__ __forceinline__ QkUnit unit_of(int32_t u, int32_t D, int32_t rot) {
   return r;
 }
 
+// A lane's unit as it lies in memory, and its way through a ring in shared memory by asynchronous copies: every lane reads
+// what it has copied itself, so the ring needs no barrier.
 template <typename T>
 struct QkRaw {
   uint4 v[2][sizeof(T) / 2];
 };
 template <typename T>
-__device__ __forceinline__ QkRaw<T> qk_load(const T* head, const QkUnit& u, bool live) {
+constexpr uint32_t kQkSlot = 32 * sizeof(QkRaw<T>);  // bytes of a warp's slot
+template <typename T>
+__device__ __forceinline__ void qk_fetch(uint32_t slot, int lane, const T* head, const QkUnit& u, bool live) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < (int)sizeof(T) / 2; ++q)
+      if (live && u.at[h] >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + ((h * (uint32_t)sizeof(T) / 2 + q) * 32 + lane) * 16),
+                     "l"(reinterpret_cast<const uint4*>(head + u.at[h]) + q)
+                     : "memory");
+}
+template <typename T>
+__device__ __forceinline__ QkRaw<T> qk_slot(uint32_t slot, int lane, const QkUnit& u, bool live) {
   QkRaw<T> r;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int q = 0; q < (int)sizeof(T) / 2; ++q) {
-      r.v[h][q] = make_uint4(0, 0, 0, 0);
-      if (live && u.at[h] >= 0) r.v[h][q] = *(reinterpret_cast<const uint4*>(head + u.at[h]) + q);
+      uint4& v = r.v[h][q];
+      v = make_uint4(0, 0, 0, 0);
+      if (live && u.at[h] >= 0)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(slot + ((h * (uint32_t)sizeof(T) / 2 + q) * 32 + lane) * 16)
+                     : "memory");
     }
   return r;
 }
@@ -147,17 +186,10 @@ __device__ __forceinline__ void qk_weight(const QkParams& a, const void* w, cons
                                                               : static_cast<const float*>(w)[u.at[h] + j]);
     }
 }
-// (a, b) -> (a c - b s, b c + a s) of the lane's eight pairs; sign -1: the inverse.
+// Member 0 or 1 of the lane's pair j.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void qk_turn(float (&v)[2][8], const float (&c)[8], const float (&s)[8], float sign) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float& x = INTERLEAVED ? v[j / 4][2 * (j % 4)] : v[0][j];
-    float& y = INTERLEAVED ? v[j / 4][2 * (j % 4) + 1] : v[1][j];
-    const float sj = sign * s[j], t = x * c[j] - y * sj;
-    y = y * c[j] + x * sj;
-    x = t;
-  }
+__device__ __forceinline__ float& member(float (&v)[2][8], int m, int j) {
+  return INTERLEAVED ? v[j / 4][2 * (j % 4) + m] : v[m][j];
 }
 template <int GROUP>
 __device__ __forceinline__ float group_sum(float v) {
