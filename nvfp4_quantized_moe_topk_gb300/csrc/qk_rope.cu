@@ -1,9 +1,10 @@
 // qk_rope.cu -- the norms of queries and keys for each head with the rotation
 // of their positions, forward and backward, in one pass over the data.
 //
-// Moving the heads bounds it (16 flops a value).  A warp takes a token's heads,
-// 32 / GROUP at a time, and computes the token's cosines and sines once; a few
-// tokens are cut further, a warp a step, so that all SMs have work.
+// Moving the heads bounds it.  A warp takes a token's heads, 32 / GROUP at a time,
+// through a ring of asynchronous copies, and computes the token's cosines and
+// sines once; every warp has the same number of steps, which may begin and end
+// inside a token.
 #include "qk_rope.cuh"
 
 #include <algorithm>
@@ -18,261 +19,253 @@ constexpr int qk_stages(int arrays) {
   return sizeof(T) == 2 ? (arrays == 1 ? 6 : 4) : (arrays == 1 ? 4 : 3);
 }
 
-// A warp's way through its work: items of one token's steps (the queries', then the keys', kHeads heads a step), cut
-// into slices, every jump-th item its own.
-struct QkWalk {
-  int64_t item;
-  int32_t token, st, end;  // the steps of the token, in both sides' count
-};
+// A warp's way through its work: a run of all tokens' steps (a token's queries, then its keys, kHeads heads a step), as
+// many as any other warp's; a segment is the run's part on one side of one token.
 struct QkPlan {
-  int64_t items, jump;
-  int32_t slices, q_steps, steps;
+  int32_t q_steps, steps;
 };
+struct QkSegment {
+  int64_t at, end;                    // the run's next step and its end
+  int32_t token, which, first, left;  // the side's steps: the first, and how many (0: no work left)
+};
+__device__ __forceinline__ void next(const QkPlan& p, QkSegment& g) {
+  g.left = 0;
+  if (g.at >= g.end) return;
+  g.token = (int32_t)(g.at / p.steps);
+  const int32_t st = (int32_t)(g.at - (int64_t)g.token * p.steps);
+  g.which = st >= p.q_steps;
+  g.first = g.which ? st - p.q_steps : st;
+  g.left = (int32_t)min((int64_t)((g.which ? p.steps : p.q_steps) - st), g.end - g.at);
+  g.at += g.left;
+}
 template <int GROUP>
-__device__ __forceinline__ QkPlan plan_of(const QkParams& a, int32_t slices) {
+__device__ __forceinline__ QkSegment run_of(const QkParams& a, int warp, QkPlan& p) {
   constexpr int kHeads = 32 / GROUP;
-  QkPlan p;
-  p.slices = slices;
-  p.items = (int64_t)a.n * slices;
-  p.jump = (int64_t)gridDim.x * kQkWarps;
   p.q_steps = (a.side[0].heads + kHeads - 1) / kHeads;
   p.steps = p.q_steps + (a.side[1].heads + kHeads - 1) / kHeads;
-  return p;
+  const int64_t all = (int64_t)a.n * p.steps, warps = (int64_t)gridDim.x * kQkWarps;
+  const int64_t me = (int64_t)blockIdx.x * kQkWarps + warp, each = all / warps, more = all % warps;
+  QkSegment g;
+  g.at = me * each + min(me, more);
+  g.end = g.at + each + (me < more);
+  next(p, g);
+  return g;
 }
-__device__ __forceinline__ void enter(const QkPlan& p, QkWalk& w) {
-  if (w.item >= p.items) return;
-  w.token = (int32_t)(w.item / p.slices);
-  const int32_t slice = (int32_t)(w.item - (int64_t)w.token * p.slices);
-  w.st = (int32_t)((int64_t)p.steps * slice / p.slices);
-  w.end = (int32_t)((int64_t)p.steps * (slice + 1) / p.slices);
-}
-__device__ __forceinline__ void advance(const QkPlan& p, QkWalk& w) {
-  if (++w.st < w.end) return;
-  w.item += p.jump;
-  enter(p, w);
-}
-// The lane's head at a step, where it starts in each array, and whether it is there.
-struct QkHead {
-  int32_t which, head;
-  bool live;
-};
-template <int GROUP>
-__device__ __forceinline__ QkHead head_at(const QkParams& a, const QkPlan& p, const QkWalk& w, int sub) {
-  QkHead h;
-  h.which = w.st >= p.q_steps;
-  h.head = (w.st - (h.which ? p.q_steps : 0)) * (32 / GROUP) + sub;
-  h.live = h.head < a.side[h.which].heads;
-  return h;
-}
-template <typename T>
-__device__ __forceinline__ T* head_ptr(const QkParams& a, const moe_rows& r, const QkHead& h, int32_t token) {
-  return row_ptr<T>(r, token, (int64_t)a.side[h.which].heads * a.D) + (int64_t)h.head * a.D;
+// A lane's place in an array over a segment's steps.
+template <typename T, int GROUP>
+__device__ __forceinline__ T* place(const QkParams& a, const moe_rows& r, const QkSegment& g, int sub) {
+  return row_ptr<T>(r, g.token, (int64_t)a.side[g.which].heads * a.D) + (int64_t)(g.first * (32 / GROUP) + sub) * a.D;
 }
 
 template <typename T, int GROUP, bool INTERLEAVED>
-__global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const __grid_constant__ QkParams a, int32_t slices) {
+__global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const __grid_constant__ QkParams a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ QkTable table;
   __shared__ __align__(16) QkTurns turns[kQkWarps];
-  constexpr int kStages = qk_stages<T>(1);
+  __shared__ __align__(16) float weights[2][kQkMaxDim];
+  constexpr int kStages = qk_stages<T>(1), kHeads = 32 / GROUP;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / GROUP, unit = lane % GROUP;
   const QkUnit u = unit_of<INTERLEAVED>(unit, a.D, a.rot);
-  const QkPlan plan = plan_of<GROUP>(a, slices);
+  QkPlan plan;
   const uint32_t slots = smem_u32(ring) + warp * kStages * kQkSlot<T>;
+  const int32_t jump_head = kHeads * a.D;
   pdl_wait();
   pdl_launch_dependents();
-  QkWalk ahead = {(int64_t)blockIdx.x * kQkWarps + warp};
-  enter(plan, ahead);
-  QkWalk w = ahead;
+  QkSegment ahead = run_of<GROUP>(a, warp, plan), g = ahead;
+  const T* src = nullptr;
+  int32_t src_head = 0, src_left = 0;
+  auto start = [&]() {
+    src_left = ahead.left;
+    if (!src_left) return;
+    src = place<const T, GROUP>(a, a.side[ahead.which].in, ahead, sub);
+    src_head = a.side[ahead.which].heads - ahead.first * kHeads - sub;  // heads from the lane's on
+  };
+  start();
   auto fetch = [&](int stage) {
-    if (ahead.item < plan.items) {
-      const QkHead h = head_at<GROUP>(a, plan, ahead, sub);
-      qk_fetch(slots + stage * kQkSlot<T>, lane, head_ptr<const T>(a, a.side[h.which].in, h, ahead.token), u, h.live);
-      advance(plan, ahead);
+    if (src_left) {
+      qk_fetch(slots + stage * kQkSlot<T>, lane, src, u, src_head > 0);
+      src += jump_head;
+      src_head -= kHeads;
+      if (--src_left == 0) {
+        next(plan, ahead);
+        start();
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i + 1 < kStages; ++i) fetch(i);
   fill_table(a, table);
+  fill_weights(a, weights);
   __syncthreads();
-  // a pair's members (a, b) become r (a k0 + b k1), r (b k2 + a k3): weight and turn in one
-  float k[4][8];
-  int32_t token = -1, which = -1;
+  int32_t token = -1;
   int stage = 0;
-  while (w.item < plan.items) {
-    const QkHead h = head_at<GROUP>(a, plan, w, sub);
-    const QkSide& side = a.side[h.which];
+  for (; g.left > 0; next(plan, g)) {
+    const QkSide& side = a.side[g.which];
     const bool norm = side.weight != nullptr;
-    if (w.token != token && a.rot > 0) fill_turns(a, table, w.token, lane, turns[warp]);
-    if (w.token != token || h.which != which) {
-      float wt[2][8], c[8], s[8];
+    if (g.token != token && a.rot > 0) fill_turns(a, table, g.token, lane, turns[warp]);
+    token = g.token;
+    QkTurn k = turn_of<INTERLEAVED>(turns[warp], u, unit);  // and the weights: of a value, and of its partner
+    {
+      const QkVals w = qk_floats(weights[g.which], u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        k.own.v[i] = mul2(k.own.v[i], w.v[i]);
+        k.other.v[i] = mul2(k.other.v[i], partner<INTERLEAVED>(w, i));
+      }
+    }
+    T* out = place<T, GROUP>(a, side.out, g, sub);
+    int32_t heads = side.heads - g.first * kHeads - sub;
+    for (int32_t left = g.left; left > 0; --left) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      QkVals v = qk_values(qk_slot<T>(slots + stage * kQkSlot<T>, lane, u, heads > 0));
+      fetch(stage == 0 ? kStages - 1 : stage - 1);  // into the slot of the step before
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      float r = 1.f;
       if (norm) {
-        qk_weight(a, side.weight, u, wt);
-      } else {
+        F2 ss = mul2(v.v[0], v.v[0]), st = mul2(v.v[4], v.v[4]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) wt[0][j] = wt[1][j] = 1.f;
+        for (int i = 1; i < 4; ++i) {
+          ss = fma2(v.v[i], v.v[i], ss);
+          st = fma2(v.v[4 + i], v.v[4 + i], st);
+        }
+        r = rsqrtf(group_sum<GROUP>(ss.x + ss.y + (st.x + st.y)) * a.inv_D + a.eps);
       }
+      QkVals o;
       if (u.rotated) {
-        load8(turns[warp].c + 8 * unit, c);
-        load8(turns[warp].s + 8 * unit, s);
-      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float wa = member<INTERLEAVED>(wt, 0, j), wb = member<INTERLEAVED>(wt, 1, j);
-        k[0][j] = u.rotated ? wa * c[j] : wa;
-        k[1][j] = u.rotated ? -wb * s[j] : 0.f;
-        k[2][j] = u.rotated ? wb * c[j] : wb;
-        k[3][j] = u.rotated ? wa * s[j] : 0.f;
+        for (int i = 0; i < 8; ++i)
+          o.v[i] = mul2(f2(r), fma2(partner<INTERLEAVED>(v, i), k.other.v[i], mul2(v.v[i], k.own.v[i])));
+      } else {  // (a partner would bring its infinities along)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.v[i] = mul2(f2(r), mul2(v.v[i], k.own.v[i]));
       }
-      token = w.token;
-      which = h.which;
+      if (heads > 0) qk_store(out, u, o);
+      out += jump_head;
+      heads -= kHeads;
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    float v[2][8];
-    qk_values(qk_slot<T>(slots + stage * kQkSlot<T>, lane, u, h.live), v);
-    fetch(stage == 0 ? kStages - 1 : stage - 1);  // into the slot of the step before
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-    float r = 1.f;
-    if (norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[m][j], v[m][j], ss);
-      r = rsqrtf(group_sum<GROUP>(ss) * a.inv_D + a.eps);
-    }
-    if (u.rotated) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float &x = member<INTERLEAVED>(v, 0, j), &y = member<INTERLEAVED>(v, 1, j);
-        const float t = r * fmaf(y, k[1][j], x * k[0][j]);
-        y = r * fmaf(x, k[3][j], y * k[2][j]);
-        x = t;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        member<INTERLEAVED>(v, 0, j) *= r * k[0][j];
-        member<INTERLEAVED>(v, 1, j) *= r * k[2][j];
-      }
-    }
-    if (h.live) qk_store(head_ptr<T>(a, side.out, h, w.token), u, v);
-    advance(plan, w);
   }
 }
 
 // d_weight: the lanes' sums over a token's heads, kept in shared memory from one token to the next and added over the
 // CTA's warps and groups in order at the end.
 template <typename T, int GROUP, bool INTERLEAVED>
-__global__ void __launch_bounds__(kQkThreads)
-    qk_rope_backward_kernel(const __grid_constant__ QkParams a, int32_t slices, float* __restrict__ part) {
+__global__ void __launch_bounds__(kQkThreads, 3)
+    qk_rope_backward_kernel(const __grid_constant__ QkParams a, float* __restrict__ part) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ QkTable table;
   __shared__ __align__(16) QkTurns turns[kQkWarps];
+  __shared__ __align__(16) float weights[2][kQkMaxDim];
   __shared__ float sums[2][kQkWarps][16][33];
   constexpr int kHeads = 32 / GROUP, kStages = qk_stages<T>(2);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / GROUP, unit = lane % GROUP;
   const QkUnit u = unit_of<INTERLEAVED>(unit, a.D, a.rot);
-  const QkPlan plan = plan_of<GROUP>(a, slices);
+  QkPlan plan;
   const uint32_t slots = smem_u32(ring) + warp * kStages * 2 * kQkSlot<T>;
+  const int32_t jump_head = kHeads * a.D;
 #pragma unroll
   for (int i = 0; i < 16; ++i) sums[0][warp][i][lane] = sums[1][warp][i][lane] = 0.f;
   pdl_wait();
   pdl_launch_dependents();
-  QkWalk ahead = {(int64_t)blockIdx.x * kQkWarps + warp};
-  enter(plan, ahead);
-  QkWalk w = ahead;
+  QkSegment ahead = run_of<GROUP>(a, warp, plan), g = ahead;
+  const T *src = nullptr, *src_in = nullptr;
+  int32_t src_head = 0, src_left = 0;
+  auto start = [&]() {
+    src_left = ahead.left;
+    if (!src_left) return;
+    const QkSide& side = a.side[ahead.which];
+    src = place<const T, GROUP>(a, side.grad, ahead, sub);
+    src_in = side.weight ? place<const T, GROUP>(a, side.in, ahead, sub) : nullptr;
+    src_head = side.heads - ahead.first * kHeads - sub;
+  };
+  start();
   auto fetch = [&](int stage) {
-    if (ahead.item < plan.items) {
-      const QkHead h = head_at<GROUP>(a, plan, ahead, sub);
-      const QkSide& side = a.side[h.which];
+    if (src_left) {
       const uint32_t slot = slots + stage * 2 * kQkSlot<T>;
-      qk_fetch(slot, lane, head_ptr<const T>(a, side.grad, h, ahead.token), u, h.live);
-      if (side.weight)
-        qk_fetch(slot + kQkSlot<T>, lane, head_ptr<const T>(a, side.in, h, ahead.token), u, h.live);
-      advance(plan, ahead);
+      qk_fetch(slot, lane, src, u, src_head > 0);
+      src += jump_head;
+      if (src_in) {
+        qk_fetch(slot + kQkSlot<T>, lane, src_in, u, src_head > 0);
+        src_in += jump_head;
+      }
+      src_head -= kHeads;
+      if (--src_left == 0) {
+        next(plan, ahead);
+        start();
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i + 1 < kStages; ++i) fetch(i);
   fill_table(a, table);
+  fill_weights(a, weights);
   __syncthreads();
-  float wt[2][8], c[8], s[8], acc[2][8] = {};
-  int32_t token = -1, which = 0;
-  auto keep = [&]() {  // the sums of the side that ends
-    if (!part || !a.side[which].weight) return;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      sums[which][warp][i][lane] += acc[i / 8][i % 8];
-      acc[i / 8][i % 8] = 0.f;
-    }
-  };
+  int32_t token = -1;
   int stage = 0;
-  while (w.item < plan.items) {
-    const QkHead h = head_at<GROUP>(a, plan, w, sub);
-    const QkSide& side = a.side[h.which];
+  for (; g.left > 0; next(plan, g)) {
+    const QkSide& side = a.side[g.which];
     const bool norm = side.weight != nullptr;
-    if (w.token != token || h.which != which) {
-      if (token >= 0) keep();
-      if (w.token != token && a.rot > 0) {
-        fill_turns(a, table, w.token, lane, turns[warp]);
-        if (u.rotated) {
-          load8(turns[warp].c + 8 * unit, c);
-          load8(turns[warp].s + 8 * unit, s);
+    if (g.token != token && a.rot > 0) fill_turns(a, table, g.token, lane, turns[warp]);
+    token = g.token;
+    const QkTurn k = turn_of<INTERLEAVED>(turns[warp], u, unit);
+    const QkVals w = qk_floats(weights[g.which], u);
+    QkVals acc;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc.v[i] = f2(0.f);
+    T* out = side.out.data ? place<T, GROUP>(a, side.out, g, sub) : nullptr;
+    int32_t heads = side.heads - g.first * kHeads - sub;
+    for (int32_t left = g.left; left > 0; --left) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      const uint32_t slot = slots + stage * 2 * kQkSlot<T>;
+      QkVals d = qk_values(qk_slot<T>(slot, lane, u, heads > 0));
+      QkVals v = qk_values(qk_slot<T>(slot + kQkSlot<T>, lane, u, heads > 0 && norm));
+      fetch(stage == 0 ? kStages - 1 : stage - 1);  // into the slot of the step before
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (u.rotated) {  // turned back: the partner's part with the other sign
+        QkVals t;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          t.v[i] = fma2(partner<INTERLEAVED>(d, i), mul2(f2(-1.f), k.other.v[i]), mul2(d.v[i], k.own.v[i]));
+        d = t;
+      }
+      if (norm) {
+        F2 ss = f2(0.f), dot = f2(0.f);
+        QkVals dw;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dw.v[i] = mul2(d.v[i], w.v[i]);
+          ss = fma2(v.v[i], v.v[i], ss);
+          dot = fma2(dw.v[i], v.v[i], dot);
+        }
+        const float sq = group_sum<GROUP>(ss.x + ss.y), dt = group_sum<GROUP>(dot.x + dot.y);
+        const float r = rsqrtf(sq * a.inv_D + a.eps), mean = r * dt * a.inv_D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const F2 y = mul2(v.v[i], f2(r));
+          acc.v[i] = fma2(d.v[i], y, acc.v[i]);
+          d.v[i] = mul2(f2(r), fma2(y, f2(-mean), dw.v[i]));
         }
       }
-      if (norm) qk_weight(a, side.weight, u, wt);
-      token = w.token;
-      which = h.which;
+      if (out) {
+        if (heads > 0) qk_store(out, u, d);
+        out += jump_head;
+      }
+      heads -= kHeads;
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    float g[2][8], v[2][8];
-    const uint32_t slot = slots + stage * 2 * kQkSlot<T>;
-    qk_values(qk_slot<T>(slot, lane, u, h.live), g);
-    qk_values(qk_slot<T>(slot + kQkSlot<T>, lane, u, h.live && norm), v);
-    fetch(stage == 0 ? kStages - 1 : stage - 1);  // into the slot of the step before
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-    if (u.rotated) {
+    if (norm && part) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float &x = member<INTERLEAVED>(g, 0, j), &y = member<INTERLEAVED>(g, 1, j);
-        const float t = fmaf(y, s[j], x * c[j]);
-        y = fmaf(-x, s[j], y * c[j]);
-        x = t;
+      for (int i = 0; i < 8; ++i) {
+        sums[g.which][warp][2 * i][lane] += acc.v[i].x;
+        sums[g.which][warp][2 * i + 1][lane] += acc.v[i].y;
       }
     }
-    if (norm) {
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ss = fmaf(v[m][j], v[m][j], ss);
-          dot = fmaf(g[m][j] * wt[m][j], v[m][j], dot);
-        }
-      ss = group_sum<GROUP>(ss);
-      dot = group_sum<GROUP>(dot);
-      const float r = rsqrtf(ss * a.inv_D + a.eps), mean = r * dot * a.inv_D;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float y = v[m][j] * r;
-          acc[m][j] = fmaf(g[m][j], y, acc[m][j]);
-          g[m][j] = r * fmaf(-y, mean, g[m][j] * wt[m][j]);
-        }
-    }
-    if (h.live && side.out.data) qk_store(head_ptr<T>(a, side.out, h, w.token), u, g);
-    advance(plan, w);
   }
-  if (token >= 0) keep();
   if (!part) return;
   __syncthreads();
   // part[CTA][side][D]: a thread a side's element
   for (int32_t e = threadIdx.x; e < 2 * 16 * GROUP; e += kQkThreads) {
-    const int32_t side = e / (16 * GROUP), in = e % (16 * GROUP);
+    const int32_t which = e / (16 * GROUP), in = e % (16 * GROUP);
     const QkUnit v = unit_of<INTERLEAVED>(in / 16, a.D, a.rot);
     const int32_t at = v.at[(in % 16) / 8];
     if (at < 0) continue;
@@ -280,8 +273,8 @@ __global__ void __launch_bounds__(kQkThreads)
 #pragma unroll
     for (int k = 0; k < kQkWarps; ++k)
 #pragma unroll
-      for (int q = 0; q < kHeads; ++q) x += sums[side][k][in % 16][q * GROUP + in / 16];
-    part[((int64_t)blockIdx.x * 2 + side) * a.D + at + in % 8] = x;
+      for (int q = 0; q < kHeads; ++q) x += sums[which][k][in % 16][q * GROUP + in / 16];
+    part[((int64_t)blockIdx.x * 2 + which) * a.D + at + in % 8] = x;
   }
 }
 
@@ -299,8 +292,6 @@ __global__ void __launch_bounds__(kJoinThreads)
   const float v = join_parts(sum);
   if (lane == 0 && mine < D) to[mine] = v;
 }
-
-constexpr int64_t kQkItems = 4;
 
 int qk_sms() {
   int dev = 0, sms = 0;
@@ -348,10 +339,10 @@ cudaError_t resident(Kernel* kernel, size_t smem, std::atomic<int32_t> (&known)[
   return cudaSuccess;
 }
 
-// Slices of a token's steps: enough that each warp has a few items, so that they come out even.
-int32_t qk_slices(const QkParams& p, int32_t heads, int64_t warps) {
-  const int32_t steps = (p.side[0].heads + heads - 1) / heads + (p.side[1].heads + heads - 1) / heads;
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>(steps, kQkItems * warps / p.n));
+// CTAs for the steps there are, a warp a step at least.
+int32_t qk_ctas(const QkParams& p, int32_t heads, int32_t most) {
+  const int64_t steps = (p.side[0].heads + heads - 1) / heads + (p.side[1].heads + heads - 1) / heads;
+  return (int32_t)std::min<int64_t>((p.n * steps + kQkWarps - 1) / kQkWarps, most);
 }
 
 template <typename T, int GROUP, bool INTERLEAVED>
@@ -363,9 +354,8 @@ cudaError_t qk_forward(const QkParams& p, cudaStream_t s) {
   int32_t most = 0;
   if (e == cudaSuccess) e = resident(qk_rope_kernel<T, GROUP, INTERLEAVED>, smem, known, &most);
   if (e != cudaSuccess) return e;
-  const int32_t slices = qk_slices(p, 32 / GROUP, (int64_t)most * kQkWarps);
-  const int64_t ctas = std::min<int64_t>(((int64_t)p.n * slices + kQkWarps - 1) / kQkWarps, most);
-  return launch_ex(qk_rope_kernel<T, GROUP, INTERLEAVED>, dim3((unsigned)ctas), dim3(kQkThreads), smem, s, true, p, slices);
+  return launch_ex(qk_rope_kernel<T, GROUP, INTERLEAVED>, dim3((unsigned)qk_ctas(p, 32 / GROUP, most)), dim3(kQkThreads),
+                   smem, s, true, p);
 }
 
 template <typename T, int GROUP, bool INTERLEAVED>
@@ -378,11 +368,10 @@ cudaError_t qk_backward(const QkParams& p, float* d_q_weight, float* d_k_weight,
   if (e == cudaSuccess) e = resident(qk_rope_backward_kernel<T, GROUP, INTERLEAVED>, smem, known, &most);
   if (e != cudaSuccess) return e;
   most = std::min(most, kQkBackwardCtas);
-  const int32_t slices = qk_slices(p, 32 / GROUP, (int64_t)most * kQkWarps);
-  const int32_t ctas = (int32_t)std::min<int64_t>(((int64_t)p.n * slices + kQkWarps - 1) / kQkWarps, most);
+  const int32_t ctas = qk_ctas(p, 32 / GROUP, most);
   const bool sums = d_q_weight || d_k_weight;
   e = launch_ex(qk_rope_backward_kernel<T, GROUP, INTERLEAVED>, dim3((unsigned)ctas), dim3(kQkThreads), smem, s, true, p,
-                slices, sums ? part : nullptr);
+                sums ? part : nullptr);
   if (e != cudaSuccess || !sums) return e;
   return launch_ex(qk_weight_sum_kernel, dim3((p.D + 31) / 32, 2), dim3(kJoinThreads), 0, s, true, (const float*)part, ctas,
                    p.D, d_q_weight, d_k_weight);

@@ -64,6 +64,16 @@ __device__ __forceinline__ void fill_table(const QkParams& a, QkTable& t) {
     t.axis[i] = axis_of_pair(a, i);
   }
 }
+// offset + weight of both sides (1 without a norm), by the CTA's threads.
+__device__ __forceinline__ void fill_weights(const QkParams& a, float (&w)[2][kQkMaxDim]) {
+  for (int32_t i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
+    const int32_t which = i >= a.D, e = i - which * a.D;
+    const void* from = a.side[which].weight;
+    w[which][e] = !from ? 1.f
+                        : a.offset + (a.param_dtype == MOE_DTYPE_BF16 ? bf16lo(static_cast<const uint16_t*>(from)[e])
+                                                                      : static_cast<const float*>(from)[e]);
+  }
+}
 // cos and sin of a token's pairs, times the rotation's scale, by one warp for itself: [pairs] cosines, [pairs] sines.
 struct QkTurns {
   float c[kQkMaxPairs], s[kQkMaxPairs];
@@ -81,18 +91,6 @@ __device__ __forceinline__ void fill_turns(const QkParams& a, const QkTable& t, 
   }
   __syncwarp();
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x;
-  v[1] = a.y;
-  v[2] = a.z;
-  v[3] = a.w;
-  v[4] = b.x;
-  v[5] = b.y;
-  v[6] = b.z;
-  v[7] = b.w;
-}
-
 // A lane's 16 elements: two vectors of 8 at element offsets at[0], at[1] (< 0: not there).
 struct QkUnit {
   int32_t at[2];
@@ -146,50 +144,108 @@ __device__ __forceinline__ QkRaw<T> qk_slot(uint32_t slot, int lane, const QkUni
     }
   return r;
 }
-__device__ __forceinline__ void qk_values(const QkRaw<uint16_t>& r, float (&v)[2][8]) {
-  unpack8(r.v[0][0], v[0]);
-  unpack8(r.v[1][0], v[1]);
-}
-__device__ __forceinline__ void qk_values(const QkRaw<float>& r, float (&v)[2][8]) {
+// The lane's 16 values as pairs of neighbours: vector m's are [4 m] to [4 m + 3].
+struct QkVals {
+  F2 v[8];
+};
+__device__ __forceinline__ QkVals qk_values(const QkRaw<uint16_t>& r) {
+  QkVals o;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int m = 0; m < 2; ++m) {
+    const uint4& d = r.v[m][0];
+    o.v[4 * m] = {bf16lo(d.x), bf16hi(d.x)};
+    o.v[4 * m + 1] = {bf16lo(d.y), bf16hi(d.y)};
+    o.v[4 * m + 2] = {bf16lo(d.z), bf16hi(d.z)};
+    o.v[4 * m + 3] = {bf16lo(d.w), bf16hi(d.w)};
+  }
+  return o;
+}
+__device__ __forceinline__ QkVals qk_values(const QkRaw<float>& r) {
+  QkVals o;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      v[h][4 * q] = __uint_as_float(r.v[h][q].x);
-      v[h][4 * q + 1] = __uint_as_float(r.v[h][q].y);
-      v[h][4 * q + 2] = __uint_as_float(r.v[h][q].z);
-      v[h][4 * q + 3] = __uint_as_float(r.v[h][q].w);
+      const uint4& d = r.v[m][q];
+      o.v[4 * m + 2 * q] = {__uint_as_float(d.x), __uint_as_float(d.y)};
+      o.v[4 * m + 2 * q + 1] = {__uint_as_float(d.z), __uint_as_float(d.w)};
+    }
+  return o;
+}
+// The unit's values of an array of floats by element (0 where it has none).
+__device__ __forceinline__ QkVals qk_floats(const float* p, const QkUnit& u) {
+  QkVals o;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (u.at[m] >= 0) d = *reinterpret_cast<const float4*>(p + u.at[m] + 4 * q);
+      o.v[4 * m + 2 * q] = {d.x, d.y};
+      o.v[4 * m + 2 * q + 1] = {d.z, d.w};
+    }
+  return o;
+}
+__device__ __forceinline__ void qk_store(uint16_t* head, const QkUnit& u, const QkVals& o) {
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+    if (u.at[m] >= 0) {
+      uint4 d;
+      d.x = pack2(o.v[4 * m].x, o.v[4 * m].y);
+      d.y = pack2(o.v[4 * m + 1].x, o.v[4 * m + 1].y);
+      d.z = pack2(o.v[4 * m + 2].x, o.v[4 * m + 2].y);
+      d.w = pack2(o.v[4 * m + 3].x, o.v[4 * m + 3].y);
+      *reinterpret_cast<uint4*>(head + u.at[m]) = d;
     }
 }
-__device__ __forceinline__ void qk_store(uint16_t* head, const QkUnit& u, const float (&v)[2][8]) {
+__device__ __forceinline__ void qk_store(float* head, const QkUnit& u, const QkVals& o) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (u.at[h] >= 0) store8(head + u.at[h], v[h]);
+  for (int m = 0; m < 2; ++m)
+    if (u.at[m] >= 0)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<float4*>(head + u.at[m] + 4 * q) =
+            make_float4(o.v[4 * m + 2 * q].x, o.v[4 * m + 2 * q].y, o.v[4 * m + 2 * q + 1].x, o.v[4 * m + 2 * q + 1].y);
 }
-__device__ __forceinline__ void qk_store(float* head, const QkUnit& u, const float (&v)[2][8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (u.at[h] >= 0) {
-      *reinterpret_cast<float4*>(head + u.at[h]) = make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
-      *reinterpret_cast<float4*>(head + u.at[h] + 4) = make_float4(v[h][4], v[h][5], v[h][6], v[h][7]);
-    }
-}
-// offset + weight of the lane's elements (0 where it has none).
-__device__ __forceinline__ void qk_weight(const QkParams& a, const void* w, const QkUnit& u, float (&v)[2][8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[h][j] = 0.f;
-      if (u.at[h] >= 0)
-        v[h][j] = a.offset + (a.param_dtype == MOE_DTYPE_BF16 ? bf16lo(static_cast<const uint16_t*>(w)[u.at[h] + j])
-                                                              : static_cast<const float*>(w)[u.at[h] + j]);
-    }
-}
-// Member 0 or 1 of the lane's pair j.
+// A turn of the lane's pairs as out = v * own + partner * other: the partner of a value is the other member of its pair.
+struct QkTurn {
+  QkVals own, other;
+};
+// The other members: of the other vector, or of the same pair of neighbours.
 template <bool INTERLEAVED>
-__device__ __forceinline__ float& member(float (&v)[2][8], int m, int j) {
-  return INTERLEAVED ? v[j / 4][2 * (j % 4) + m] : v[m][j];
+__device__ __forceinline__ F2 partner(const QkVals& v, int i) {
+  return INTERLEAVED ? F2{v.v[i].y, v.v[i].x} : v.v[(i + 4) % 8];
+}
+// cos and -sin (first members), cos and sin (second) of the unit's pairs; 1 and 0 past the rotated part.
+template <bool INTERLEAVED>
+__device__ __forceinline__ QkTurn turn_of(const QkTurns& t, const QkUnit& u, int unit) {
+  QkTurn r;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {  // pairs 8 unit + 4 q ..
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (u.rotated) {
+      c = *reinterpret_cast<const float4*>(t.c + 8 * unit + 4 * q);
+      s = *reinterpret_cast<const float4*>(t.s + 8 * unit + 4 * q);
+    }
+    if (INTERLEAVED) {
+      r.own.v[4 * q] = f2(c.x);
+      r.own.v[4 * q + 1] = f2(c.y);
+      r.own.v[4 * q + 2] = f2(c.z);
+      r.own.v[4 * q + 3] = f2(c.w);
+      r.other.v[4 * q] = {-s.x, s.x};
+      r.other.v[4 * q + 1] = {-s.y, s.y};
+      r.other.v[4 * q + 2] = {-s.z, s.z};
+      r.other.v[4 * q + 3] = {-s.w, s.w};
+    } else {
+      r.own.v[2 * q] = r.own.v[4 + 2 * q] = {c.x, c.y};
+      r.own.v[2 * q + 1] = r.own.v[4 + 2 * q + 1] = {c.z, c.w};
+      r.other.v[2 * q] = {-s.x, -s.y};
+      r.other.v[2 * q + 1] = {-s.z, -s.w};
+      r.other.v[4 + 2 * q] = {s.x, s.y};
+      r.other.v[4 + 2 * q + 1] = {s.z, s.w};
+    }
+  }
+  return r;
 }
 template <int GROUP>
 __device__ __forceinline__ float group_sum(float v) {
