@@ -504,20 +504,6 @@ cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t inner, u
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_block(CUtensorMap* map, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t stride,
-                            uint32_t box_inner, uint32_t box_outer) {
-  auto enc = get_encode();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {stride * (f32 ? 4 : 2)};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 cudaError_t make_tmap_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K) {
   auto enc = get_encode();
   if (!enc) return cudaErrorNotSupported;

@@ -296,9 +296,6 @@ cudaError_t make_tmap_codes(CUtensorMap* map, const void* base, uint64_t rows, u
 // swizzle; what lies outside reads as zero.
 cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t stride,
                            uint32_t box_inner, uint32_t box_outer);
-// The same for blocks of bf16 or fp32 as they are stored, no swizzle.
-cudaError_t make_tmap_block(CUtensorMap* map, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t stride,
-                            uint32_t box_inner, uint32_t box_outer);
 
 // Launch with the programmatic-stream-serialization attribute when pdl is set.
 template <typename... KArgs, typename... Args>

@@ -6,8 +6,9 @@
 
 namespace moe {
 
-// 1 / (1 + exp(-v)), 0 and 1 where the exponential overflows or vanishes.
-__device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + __expf(-v)); }
+// z / (1 + exp(-v)) for finite z: 0 and z where the exponential overflows or vanishes.  The fast exponential and quotient
+// are within (4 + 1.2 |v|) 2^-23 of the value.
+__device__ __forceinline__ float logistic(float v, float z = 1.f) { return __fdividef(z, 1.f + __expf(-v)); }
 
 // gelu_tanh: z / 2 (1 + tanh(u)) = z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -19,8 +20,8 @@ __device__ __forceinline__ float linear_act(float z, int32_t act) {
       const float r = z > 0.f ? z : z == z ? 0.f : z;
       return r * r;
     }
-    case MOE_LINEAR_SILU: return z * logistic(z);
-    case MOE_LINEAR_GELU_TANH: return z * logistic(kGelu * z * fmaf(kGeluCube * z, z, 1.f));
+    case MOE_LINEAR_SILU: return logistic(z, z);
+    case MOE_LINEAR_GELU_TANH: return logistic(kGelu * z * fmaf(kGeluCube * z, z, 1.f), z);
     default: return z;
   }
 }

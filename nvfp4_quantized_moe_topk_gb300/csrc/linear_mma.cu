@@ -15,8 +15,6 @@
 // tiles than SMs, the CTAs of a cluster split the columns and add their sums
 // through each other's shared memory, in order.
 #include <algorithm>
-#include <cstdlib>
-#include <cstdio>
 
 #include "block.cuh"
 #include "linear_act.cuh"
@@ -30,12 +28,13 @@ constexpr int kThreads = 384, kEpilogueWarps = 8;  // warp 0: copies, 1: product
 constexpr int kMaxStages = 12;
 constexpr uint32_t kSmem = 227 * 1024, kBarBytes = 1024;
 constexpr uint32_t kPBytes = 128 * 128;  // a stage's features: 128 of 64 columns
+constexpr uint32_t kSlotBytes = 16 * 36 * 4;  // of an epilogue warp
 constexpr int kMaxCluster = 8;
 // The tensor core cuts what it adds to a sum where it would round, which costs a sum of C products about 1e-9 C of its
 // size, always towards zero.  A result in fp32 is therefore summed in tensor memory for 8 blocks of 64 columns at a time,
-// and from there on in registers (4314 columns: 4.7e-6 off without, XXXX so).
+// and from there on in registers (4314 columns: 4.7e-6 off without, 4.7e-7 so).
 constexpr int32_t kChain = 8;
-constexpr int kChainBlocks = 6, kChainRows = 32 * kChainBlocks;  // (a thread holds 96 sums)
+constexpr int kChainBlocks = 4;  // of 32 sums a thread
 
 // Set where a bounded wait ran out; read by moe_linear_get_device_error.
 __device__ int32_t g_linear_flags;
@@ -47,7 +46,6 @@ struct Plan {
   int32_t split, stages;
   int32_t chain;              // blocks of 64 columns that tensor memory sums before their sum moves to registers
   uint32_t stage_bytes;
-  uint32_t z_at, slot_bytes;  // of an epilogue warp's staging slot: out's block, then z's
   LinearFinish e;
 };
 
@@ -153,6 +151,19 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// 32 lanes x 32 bit, 32 consecutive columns: fewer and wider reads, since each waits behind the products under way.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Warps 1 and 2 meet; whether warp 2 gave up.
 __device__ __forceinline__ bool hand_over(bool gave_up) {
   uint32_t r;
@@ -165,7 +176,7 @@ __device__ __forceinline__ bool hand_over(bool gave_up) {
 }
 
 struct Maps {
-  CUtensorMap p, q[kLinearTerms], out, z;
+  CUtensorMap p, q[kLinearTerms];
 };
 
 struct Tile {
@@ -188,71 +199,121 @@ __device__ __forceinline__ void write_value(void* p, int64_t at, int32_t f32, fl
     static_cast<uint16_t*>(p)[at] = f2bf_rn(v);
 }
 
-// The residual of feature f in 16 rows from r0 on, as it lies in memory.
-__device__ __forceinline__ void load_residual(const Plan& p, int32_t r0, int32_t f, uint32_t (&raw)[16]) {
-  const LinearFinish& e = p.e;
-  const int32_t rows = f < p.F ? min(16, p.R - r0) : 0;
-  if (e.residual_f32) {
-    const uint32_t* at = static_cast<const uint32_t*>(e.residual) + (int64_t)r0 * e.residual_stride + f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i, at += e.residual_stride) raw[i] = i < rows ? *at : 0u;
-  } else {
-    const uint16_t* at = static_cast<const uint16_t*>(e.residual) + (int64_t)r0 * e.residual_stride + f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i, at += e.residual_stride) raw[i] = i < rows ? *at : 0u;
-  }
+// A block of 32 rows by 32 features between memory, where a lane moves 16 bytes of a row, and the sums, where a lane has a
+// feature.  It turns in the warp's slot of shared memory: bf16 as words of two rows, so that a lane writes 16 words and
+// reads 16; fp32 in two rounds.  Rows of the slot are 36 words apart, which keeps both sides off each other's banks.
+constexpr int kSlotRow = 36;
+struct BlockRows {  // the warp's 32 features of the rows from the tile's first on
+  char* at;
+  int64_t row;
+};
+__device__ __forceinline__ BlockRows block_rows(void* base, int64_t stride, int32_t f32, int32_t r0, int32_t f0) {
+  const int64_t size = f32 ? 4 : 2;
+  return {static_cast<char*>(base) + ((int64_t)r0 * stride + f0) * size, stride * size};
 }
-// A block of 16 rows by 32 features for the copy that takes it to memory: a lane its feature.
-__device__ __forceinline__ void stage16(uint8_t* to, int lane, int32_t f32, const float (&v)[16]) {
+__device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, uint32_t which) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(which));
+  return d;
+}
+constexpr uint32_t kLowHalves = 0x5410, kHighHalves = 0x7632;
+// rows: how many there are from row c0 on; feats: from the warp's first feature on.
+__device__ __forceinline__ void store32(const BlockRows& to, int32_t f32, const float (&v)[32], int32_t c0, int32_t rows,
+                                        int32_t feats, int lane, uint32_t* slot) {
+  char* at = to.at + c0 * to.row;
   if (f32) {
-    float* at = reinterpret_cast<float*>(to) + lane;
+    at += (lane >> 3) * to.row + 16 * (lane & 7);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) at[32 * i] = v[i];
-  } else {
-    uint16_t* at = reinterpret_cast<uint16_t*>(to) + lane;
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) at[32 * i] = f2bf_rn(v[i]);
+      for (int i = 0; i < 16; ++i) slot[i * kSlotRow + lane] = __float_as_uint(v[16 * h + i]);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k, at += 4 * to.row)
+        if (16 * h + 4 * k + (lane >> 3) < rows && 4 * (lane & 7) < feats)
+          *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(slot + (4 * k + (lane >> 3)) * kSlotRow + 4 * (lane & 7));
+      __syncwarp();
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) slot[i * kSlotRow + lane] = pack2(v[2 * i], v[2 * i + 1]);
+  __syncwarp();
+  at += 2 * (lane >> 2) * to.row + 16 * (lane & 3);
+#pragma unroll
+  for (int k = 0; k < 2; ++k, at += 16 * to.row) {
+    const uint32_t* from = slot + (8 * k + (lane >> 2)) * kSlotRow + 8 * (lane & 3);
+    const uint4 a = *reinterpret_cast<const uint4*>(from), b = *reinterpret_cast<const uint4*>(from + 4);
+    const int32_t r = 16 * k + 2 * (lane >> 2);
+    if (8 * (lane & 3) < feats) {
+      if (r < rows)
+        *reinterpret_cast<uint4*>(at) = make_uint4(halves(a.x, a.y, kLowHalves), halves(a.z, a.w, kLowHalves),
+                                                   halves(b.x, b.y, kLowHalves), halves(b.z, b.w, kLowHalves));
+      if (r + 1 < rows)
+        *reinterpret_cast<uint4*>(at + to.row) = make_uint4(halves(a.x, a.y, kHighHalves), halves(a.z, a.w, kHighHalves),
+                                                            halves(b.x, b.y, kHighHalves), halves(b.z, b.w, kHighHalves));
+    }
+  }
+  __syncwarp();
+}
+// The bf16 residual of a block as it lies in memory, on its way to the lanes that will put it into the slot.
+__device__ __forceinline__ void load_residual(const BlockRows& from, int32_t c0, int32_t rows, int32_t feats, int lane,
+                                              uint4 (&raw)[4]) {
+  const char* at = from.at + (c0 + 2 * (lane >> 2)) * from.row + 16 * (lane & 3);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int32_t r = 16 * (k / 2) + 2 * (lane >> 2) + k % 2;
+    raw[k] = make_uint4(0, 0, 0, 0);
+    if (8 * (lane & 3) < feats && r < rows)
+      raw[k] = *reinterpret_cast<const uint4*>(at + (16 * (k / 2) + k % 2) * from.row);
   }
 }
-__device__ __forceinline__ void store_2d(const CUtensorMap* map, const void* from, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
-               "r"(smem_u32(from))
-               : "memory");
+// v += scale times the residual; a bf16 one from raw.
+__device__ __forceinline__ void add_residual(const BlockRows& from, int32_t f32, float scale, const uint4 (&raw)[4],
+                                             int32_t c0, int32_t rows, int32_t feats, int lane, uint32_t* slot,
+                                             float (&v)[32]) {
+  if (f32) {
+    const char* at = from.at + (c0 + (lane >> 3)) * from.row + 16 * (lane & 7);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k, at += 4 * from.row) {
+        d[k] = make_uint4(0, 0, 0, 0);
+        if (16 * h + 4 * k + (lane >> 3) < rows && 4 * (lane & 7) < feats) d[k] = *reinterpret_cast<const uint4*>(at);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(slot + (4 * k + (lane >> 3)) * kSlotRow + 4 * (lane & 7)) = d[k];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[16 * h + i] = fmaf(scale, __uint_as_float(slot[i * kSlotRow + lane]), v[16 * h + i]);
+      __syncwarp();
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t* to = slot + (8 * k + (lane >> 2)) * kSlotRow + 8 * (lane & 3);
+    const uint4 &a = raw[2 * k], &b = raw[2 * k + 1];  // the first and the second of two rows
+    *reinterpret_cast<uint4*>(to) = make_uint4(halves(a.x, b.x, kLowHalves), halves(a.x, b.x, kHighHalves),
+                                               halves(a.y, b.y, kLowHalves), halves(a.y, b.y, kHighHalves));
+    *reinterpret_cast<uint4*>(to + 4) = make_uint4(halves(a.z, b.z, kLowHalves), halves(a.z, b.z, kHighHalves),
+                                                   halves(a.w, b.w, kLowHalves), halves(a.w, b.w, kHighHalves));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t d = slot[i * kSlotRow + lane];
+    v[2 * i] = fmaf(scale, bf16lo(d), v[2 * i]);
+    v[2 * i + 1] = fmaf(scale, bf16hi(d), v[2 * i + 1]);
+  }
+  __syncwarp();
 }
 template <int ACT>
-__device__ __forceinline__ void act16(float (&v)[16]) {
+__device__ __forceinline__ void act32(float (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = linear_act(v[i], ACT);
-}
-// Finishes a warp's sums of 32 features (from f0 on) in 16 rows from r0 on through its staging slot.
-__device__ __forceinline__ void finish16(const Plan& p, const Maps& maps, float (&v)[16], const uint32_t (&raw)[16],
-                                         int32_t r0, int32_t f0, int lane, float bias, uint8_t* slot) {
-  const LinearFinish& e = p.e;
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the slot's last block has left it
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] += bias;
-  if (e.z) stage16(slot + p.z_at, lane, e.z_f32, v);
-  if (e.act == MOE_LINEAR_RELU2)
-    act16<MOE_LINEAR_RELU2>(v);
-  else if (e.act == MOE_LINEAR_SILU)
-    act16<MOE_LINEAR_SILU>(v);
-  else if (e.act == MOE_LINEAR_GELU_TANH)
-    act16<MOE_LINEAR_GELU_TANH>(v);
-  if (e.residual) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = fmaf(e.scale, e.residual_f32 ? __uint_as_float(raw[i]) : bf16lo(raw[i]), v[i]);
-  }
-  stage16(slot, lane, e.out_f32, v);
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    if (f0 < p.F) {  // (what lies past the last row or feature is not written)
-      store_2d(&maps.out, slot, f0, r0);
-      if (e.z) store_2d(&maps.z, slot + p.z_at, f0, r0);
-    }
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
+  for (int i = 0; i < 32; ++i) v[i] = linear_act(v[i], ACT);
 }
 
 template <int CG, bool P_MN, bool Q_MN, bool CHAIN>
@@ -266,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank(), cta = rank % CG, part = rank / CG, first_cta = rank - cta;  // of the pair
   const int32_t units = gridDim.x / (CG * p.split), unit = blockIdx.x / (CG * p.split);
-  const uint32_t cols = p.rows <= 16 ? 32 : p.rows <= 32 ? 64 : p.rows <= 64 ? 128 : p.rows <= 128 ? 256 : 512;
+  const uint32_t cols = p.rows <= 32 ? 64 : p.rows <= 64 ? 128 : p.rows <= 128 ? 256 : 512;
   const int32_t kb0 = (int32_t)((int64_t)p.KB * p.terms * part / p.split);
   const int32_t kb1 = (int32_t)((int64_t)p.KB * p.terms * (part + 1) / p.split);
   const int32_t my_rows = p.rows / CG;  // rows that this CTA holds
@@ -396,32 +457,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    uint8_t* slots = sm + p.stages * p.stage_bytes + (warp - 4) * 2 * p.slot_bytes;
-    int it = 0, slot = 0;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(sm + p.stages * p.stage_bytes + (warp - 4) * kSlotBytes);
+    int it = 0;
     bool ok = true;
     for (int32_t t = unit; t < p.tiles && ok; t += units) {
       const Tile ti = tile_at(p, t, 128 * CG);
       const int32_t f0 = ti.f0 + 128 * cta + 32 * q, f = f0 + lane, rows = min(p.rows, p.R - ti.r0);
       const bool direct = p.split == 1;
       const float bias = direct && p.e.bias && f < p.F ? read_value(p.e.bias, f, p.e.bias_f32) : 0.f;
-      const bool residual = direct && p.e.residual;
-      uint32_t raw[16] = {};
-      if (residual && 16 * half < rows) load_residual(p, ti.r0 + 16 * half, f, raw);
+      const BlockRows to_out = block_rows(p.e.out, p.e.out_stride, p.e.out_f32, ti.r0, f0),
+                      to_z = block_rows(p.e.z, p.e.z_stride, p.e.z_f32, ti.r0, f0),
+                      from_res = block_rows(const_cast<void*>(p.e.residual), p.e.residual_stride, p.e.residual_f32, ti.r0, f0);
+      const int32_t feats = p.F - f0;
+      const bool ahead = !CHAIN && direct && p.e.residual && !p.e.residual_f32;  // the next block's residual
+      uint4 raw[4];
+      if (ahead && 32 * half < rows) load_residual(from_res, 32 * half, rows - 32 * half, feats, lane, raw);
       // a block's sums: finished, or to shared memory where a cluster's meet (every copy has been read by then: they take
       // the stages' place)
-      auto out = [&](float (&v)[16], int32_t c0) {
+      auto out = [&](float (&v)[32], int32_t c0) {
+        const int32_t left = rows - c0;
         if (!direct) {
           float* to = reinterpret_cast<float*>(sm) + c0 * 128 + 32 * q + lane;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) to[i * 128] = v[i];
+          for (int i = 0; i < 32; ++i)
+            if (i < p.rows) to[i * 128] = v[i];
           return;
         }
-        uint32_t now[16];
+        if (p.e.bias) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) now[i] = raw[i];
-        if (residual && c0 + 32 < rows) load_residual(p, ti.r0 + c0 + 32, f, raw);  // the next block's
-        finish16(p, maps, v, now, ti.r0 + c0, f0, lane, bias, slots + slot * p.slot_bytes);
-        slot ^= 1;
+          for (int i = 0; i < 32; ++i) v[i] += bias;
+        }
+        if (p.e.z) store32(to_z, p.e.z_f32, v, c0, left, feats, lane, slot);
+        if (p.e.act == MOE_LINEAR_RELU2)
+          act32<MOE_LINEAR_RELU2>(v);
+        else if (p.e.act == MOE_LINEAR_SILU)
+          act32<MOE_LINEAR_SILU>(v);
+        else if (p.e.act == MOE_LINEAR_GELU_TANH)
+          act32<MOE_LINEAR_GELU_TANH>(v);
+        if (p.e.residual) {
+          if (!ahead && !p.e.residual_f32) load_residual(from_res, c0, left, feats, lane, raw);
+          add_residual(from_res, p.e.residual_f32, p.e.scale, raw, c0, left, feats, lane, slot, v);
+          if (ahead && left > 64) load_residual(from_res, c0 + 64, left - 64, feats, lane, raw);
+        }
+        store32(to_out, p.e.out_f32, v, c0, left, feats, lane, slot);
       };
       auto arrive = [&](uint32_t acc) {
         tc_fence_before();
@@ -434,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (CHAIN) {
-        float sum[kChainBlocks][16];
+        float sum[kChainBlocks][32];
         for (int32_t kb = kb0; kb < kb1; kb += p.chain, ++it) {
           const uint32_t acc = it & 1;
           ok = wait_for(&t_full[acc], (it >> 1) & 1, &gave_up);
@@ -443,20 +521,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int b = 0; b < kChainBlocks; ++b) {
-            const int32_t c0 = 16 * half + 32 * b;
+            const int32_t c0 = 32 * half + 64 * b;
             if (c0 >= rows) continue;
-            uint32_t d[16];
-            tmem_ld16(tmem + lanes + acc * p.rows + c0, d);
-            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[b][i] = (kb == kb0 ? 0.f : sum[b][i]) + __uint_as_float(d[i]);
+            for (int h = 0; h < 2; ++h) {  // (wider reads would not leave the sums their registers)
+              uint32_t d[16];
+              tmem_ld16(tmem + lanes + acc * p.rows + c0 + 16 * h, d);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                sum[b][16 * h + i] = (kb == kb0 ? 0.f : sum[b][16 * h + i]) + __uint_as_float(d[i]);
+            }
           }
           arrive(acc);
         }
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < kChainBlocks; ++b) {
-          const int32_t c0 = 16 * half + 32 * b;
+          const int32_t c0 = 32 * half + 64 * b;
           if (c0 < rows) out(sum[b], c0);
         }
       } else {
@@ -465,20 +547,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        for (int32_t c0 = 16 * half; c0 < rows; c0 += 32) {
-          uint32_t d[16];
-          tmem_ld16(tmem + lanes + acc * p.rows + c0, d);
+        for (int32_t c0 = 32 * half; c0 < rows; c0 += 64) {
+          uint32_t d[32];
+          tmem_ld32(tmem + lanes + acc * p.rows + c0, d);
           tmem_ld_wait();
-          float v[16];
+          float v[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(d[i]);
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
           out(v, c0);
         }
         arrive(acc);
         ++it;
       }
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
   __syncwarp();
   if (p.split > 1) {
@@ -533,7 +614,7 @@ cudaError_t launch(const Plan& p, const Maps& m, int32_t units, cudaStream_t s) 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units * cluster);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 1024 + p.stages * p.stage_bytes + 2 * kEpilogueWarps * p.slot_bytes;
+  cfg.dynamicSmemBytes = 1024 + p.stages * p.stage_bytes + kEpilogueWarps * kSlotBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -585,7 +666,6 @@ cudaError_t held_clusters(int32_t (&held)[kMaxCluster + 1]) {
     if (e != cudaSuccess) return e;
   }
   for (int n = 1; n <= kMaxCluster; ++n) held[n] = known[dev][n].load(std::memory_order_acquire);
-  if (getenv("LINEAR_SHOW")) { for (int n = 1; n <= kMaxCluster; ++n) printf("clusters of %d: %d\n", n, held[n]); }
   return cudaSuccess;
 }
 
@@ -596,16 +676,12 @@ struct Shape {
 // products or its bytes from L2 (64 a clock), whichever is more; a tile its start and its epilogue; a split the meeting of
 // its sums.
 Shape choose(int32_t R, int32_t F, int32_t blocks, bool q_mn, bool f32, const int32_t (&clusters)[kMaxCluster + 1]) {
-  if (const char* force = getenv("LINEAR_FORCE")) {
-    Shape s = {};
-    if (sscanf(force, "%d,%d,%d", &s.cg, &s.rows, &s.split) == 3) { s.split = std::max(1, std::min(s.split, blocks)); return s; }
-  }
   static const int32_t kRows[] = {16, 32, 64, 96, 128, 160, 192, 224, 256};
   Shape best = {};
   double least = 0;
   for (int cg = 1; cg <= 2; ++cg)
     for (const int32_t rows : kRows) {
-      if (rows % (16 * cg) || (f32 && blocks > kChain && rows > kChainRows) || (q_mn && rows < 64 * cg)) continue;
+      if (rows % (16 * cg) || (q_mn && rows < 64 * cg)) continue;
       if (rows >= 2 * R && rows > 64 * cg) continue;
       const int64_t tiles = (int64_t)((R + rows - 1) / rows) * ((F + 128 * cg - 1) / (128 * cg));
       const int32_t held = rows / cg, units = clusters[cg];
@@ -641,7 +717,6 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
   const bool f32 = f.out_f32 || (f.z && f.z_f32);
   const Shape shape = choose(a.R, a.F, p.KB * p.terms, q_mn, f32, clusters);
   const int cg = shape.cg;
-  if (getenv("LINEAR_SHOW")) printf("R %d F %d blocks %d: cg %d rows %d split %d\n", a.R, a.F, p.KB * p.terms, shape.cg, shape.rows, shape.split);
   p.rows = shape.rows;
   p.split = shape.split;
   const int32_t feats = 128 * cg, q_rows = q_mn ? (p.rows / cg + 63) / 64 * 64 : p.rows / cg;
@@ -652,17 +727,12 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
   p.group = std::min(8, p.tiles_r);
   p.stage_bytes = kPBytes + (uint32_t)q_rows * 128;
   const int32_t units = p.split > 1 ? p.tiles : std::min(clusters[cg], p.tiles);
-  if (p.split == 1) {
-    p.z_at = 16 * 32 * (f.out_f32 ? 4 : 2);
-    p.slot_bytes = p.z_at + (f.z ? 16 * 32 * (f.z_f32 ? 4 : 2) : 0);
-  }
-  p.stages = std::min<int32_t>(kMaxStages, (kSmem - kBarBytes - 1024 - 2 * kEpilogueWarps * p.slot_bytes) / p.stage_bytes);
+  p.stages = std::min<int32_t>(kMaxStages, (kSmem - kBarBytes - 1024 - kEpilogueWarps * kSlotBytes) / p.stage_bytes);
   // (the sums of a cluster meet where the stages were)
   if (p.split > 1 && (uint32_t)p.rows * 512 > p.stages * p.stage_bytes) return cudaErrorInvalidConfiguration;
   const int32_t own = (p.KB * p.terms + p.split - 1) / p.split;
-  const int32_t kc = getenv("LINEAR_CHAIN") ? atoi(getenv("LINEAR_CHAIN")) : kChain;
-  const bool chain = f32 && own > kc;
-  p.chain = chain ? kc : own;
+  const bool chain = f32 && own > kChain;
+  p.chain = chain ? kChain : own;
   Maps m;
   e = operand_map(&m.p, a.p, a.F, a.C, 128);
   for (int i = 0; i < kLinearTerms && e == cudaSuccess; ++i) {
@@ -670,11 +740,6 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
       e = operand_map(&m.q[i], a.q[i], a.R, a.C, p.rows / cg);
     else
       m.q[i] = m.q[0];
-  }
-  m.out = m.z = m.p;
-  if (p.split == 1) {
-    if (e == cudaSuccess) e = make_tmap_block(&m.out, f.out, f.out_f32, a.F, a.R, f.out_stride, 32, 16);
-    if (e == cudaSuccess && f.z) e = make_tmap_block(&m.z, f.z, f.z_f32, a.F, a.R, f.z_stride, 32, 16);
   }
   if (e != cudaSuccess) return e;
   if (cg == 2) return chain ? launch_as<2, true>(p_mn, q_mn, p, m, units, s) : launch_as<2, false>(p_mn, q_mn, p, m, units, s);
