@@ -533,7 +533,8 @@ typedef struct moe_linear_args {
   moe_rows x;             /* bf16 [n][in_features] */
   moe_rows residual;      /* [n][out_features]; data may be NULL */
   moe_rows z;             /* [n][out_features]; data may be NULL: not kept */
-  moe_rows out;           /* [n][out_features]; data may be residual's where the types and strides are the same */
+  moe_rows out;           /* [n][out_features]; data may be residual's where the types and strides are the same, and
+                             no other input's */
 } moe_linear_args;
 
 /* Enqueues the product on `stream`; one launch, no workspace.  Errors:
@@ -552,7 +553,7 @@ MOE_API moe_status moe_linear(const moe_linear_args *args, moe_stream_t stream);
  * rounded to bf16, one in fp32 from dz with its 24 bits; where d_out is bf16
  * and there is no activation dz is d_out, exactly.  The sums run in a fixed
  * order.  A NULL output is not computed; x is needed for d_weight, weight for
- * d_x. */
+ * d_x.  No output may be an input. */
 typedef struct moe_linear_grads {
   int32_t d_out_dtype;    /* MOE_DTYPE_ of d_out */
   int32_t d_x_dtype;      /* of d_x */

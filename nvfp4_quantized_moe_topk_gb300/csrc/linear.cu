@@ -17,85 +17,111 @@ namespace moe {
 
 namespace {
 
-constexpr int kDzThreads = 256, kDzLanes = 32, kDzRows = kDzThreads / kDzLanes;  // 8 columns a lane
-constexpr int kDzColumns = 8 * kDzLanes;
-constexpr int kDzMostChunks = 64;
+constexpr int kDzThreads = 256;
+constexpr int kDzMostChunks = 304, kDzOneChunk = 96;
 
 struct DzParams {
   int32_t n, out, act, chunks;
-  int32_t d_f32, z_f32;
+  int32_t lanes;  // of 8 columns each, side by side in a CTA; the other threads take other rows
   moe_rows d_out, z;
   uint16_t* terms;    // [kLinearTerms][n][out] or NULL
   int32_t n_terms;
   float* part;        // [chunks][out] or NULL
 };
 
-__device__ __forceinline__ void load_row8(const moe_rows& r, int64_t t, int32_t cols, int32_t at, int32_t f32,
-                                          float (&v)[8]) {
-  if (f32) {
-    const float4* p = reinterpret_cast<const float4*>(row_ptr<const float>(r, t, cols) + at);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = a.z;
-    v[3] = a.w;
-    v[4] = b.x;
-    v[5] = b.y;
-    v[6] = b.z;
-    v[7] = b.w;
-  } else {
-    unpack8(*reinterpret_cast<const uint4*>(row_ptr<const uint16_t>(r, t, cols) + at), v);
+// 8 values of a row as they lie in memory.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const moe_rows& r, int64_t t, int32_t cols, int32_t at) {
+  const uint4* p = reinterpret_cast<const uint4*>(row_ptr<const T>(r, t, cols) + at);
+  Raw8<T> o;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) o.v[i] = __ldg(p + i);
+  return o;
+}
+__device__ __forceinline__ void values8(const Raw8<uint16_t>& r, float (&v)[8]) { unpack8(r.v[0], v); }
+__device__ __forceinline__ void values8(const Raw8<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.v[i].x);
+    v[4 * i + 1] = __uint_as_float(r.v[i].y);
+    v[4 * i + 2] = __uint_as_float(r.v[i].z);
+    v[4 * i + 3] = __uint_as_float(r.v[i].w);
   }
 }
 
-// dz of 256 columns and a chunk of tokens, and its column sums.
+// dz of 8 lanes' columns and a chunk of tokens, and its column sums.
+constexpr int kDzAhead = 4;  // rows of a thread on their way at once
+template <bool ACT, typename DT, typename ZT>
 __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzParams a) {
-  __shared__ float sums[kDzRows][kDzColumns];
-  const int lane = threadIdx.x % kDzLanes, row = threadIdx.x / kDzLanes;
-  const int32_t col = blockIdx.x * kDzColumns + 8 * lane;
+  __shared__ float sums[8 * kDzThreads];
+  const int lane = threadIdx.x % a.lanes, row = threadIdx.x / a.lanes, rows = kDzThreads / a.lanes;
+  const int32_t columns = 8 * a.lanes, col = blockIdx.x * columns + 8 * lane;
   const int32_t begin = (int32_t)((int64_t)a.n * blockIdx.y / a.chunks), end = (int32_t)((int64_t)a.n * (blockIdx.y + 1) / a.chunks);
   float sum[8] = {};
+  pdl_wait();
+  pdl_launch_dependents();
   if (col < a.out) {
-    for (int32_t t = begin + row; t < end; t += kDzRows) {
-      float d[8];
-      load_row8(a.d_out, t, a.out, col, a.d_f32, d);
-      if (a.act != MOE_LINEAR_NONE) {
-        float z[8];
-        load_row8(a.z, t, a.out, col, a.z_f32, z);
+    for (int32_t t0 = begin + row; t0 < end; t0 += kDzAhead * rows) {
+      Raw8<DT> rd[kDzAhead];
+      Raw8<ZT> rz[kDzAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= linear_slope(z[i], a.act);
+      for (int k = 0; k < kDzAhead; ++k) {
+        const int32_t t = min(t0 + k * rows, end - 1);
+        rd[k] = raw8<DT>(a.d_out, t, a.out, col);
+        if (ACT) rz[k] = raw8<ZT>(a.z, t, a.out, col);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += d[i];
-      for (int k = 0; k < a.n_terms; ++k) {
-        store8(a.terms + ((int64_t)k * a.n + t) * a.out + col, d);
+      for (int k = 0; k < kDzAhead; ++k) {
+        const int32_t t = t0 + k * rows;
+        if (t >= end) break;
+        float d[8], z[8];
+        values8(rd[k], d);
+        if (ACT) values8(rz[k], z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float h = __bfloat162float(__float2bfloat16_rn(d[i]));
-          d[i] = isfinite(h) ? d[i] - h : 0.f;  // (an infinity stays one)
+          if (ACT) d[i] *= linear_slope(z[i], a.act);
+          sum[i] += d[i];
+        }
+        for (int m = 0; m < a.n_terms; ++m) {
+          store8(a.terms + ((int64_t)m * a.n + t) * a.out + col, d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float h = __bfloat162float(__float2bfloat16_rn(d[i]));
+            d[i] = isfinite(h) ? d[i] - h : 0.f;  // (an infinity stays one)
+          }
         }
       }
     }
   }
   if (!a.part) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[row][8 * lane + i] = sum[i];
+  for (int i = 0; i < 8; ++i) sums[row * columns + 8 * lane + i] = sum[i];
   __syncthreads();
-  const int32_t c = blockIdx.x * kDzColumns + threadIdx.x;
-  if (c >= a.out) return;
-  float v = 0.f;
-#pragma unroll
-  for (int r = 0; r < kDzRows; ++r) v += sums[r][threadIdx.x];
-  a.part[(int64_t)blockIdx.y * a.out + c] = v;
+  for (int32_t i = threadIdx.x; i < columns; i += kDzThreads) {
+    const int32_t c = blockIdx.x * columns + i;
+    if (c >= a.out) return;
+    float v = 0.f;
+    for (int r = 0; r < rows; ++r) v += sums[r * columns + i];
+    a.part[(int64_t)blockIdx.y * a.out + c] = v;
+  }
 }
 
-__global__ void __launch_bounds__(kDzThreads)
+// d_bias: the chunks' sums, 32 columns a CTA.
+__global__ void __launch_bounds__(kJoinThreads)
     linear_bias_kernel(const float* __restrict__ part, int32_t chunks, int32_t out, float* __restrict__ d_bias) {
-  const int32_t c = blockIdx.x * kDzThreads + threadIdx.x;
-  if (c >= out) return;
-  float v = 0.f;
-  for (int32_t k = 0; k < chunks; ++k) v += part[(int64_t)k * out + c];
-  d_bias[c] = v;
+  __shared__ float sum[kJoinWarps][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t c = blockIdx.x * 32 + lane, mine = blockIdx.x * 32 + warp;
+  pdl_wait();
+  pdl_launch_dependents();
+  sum[warp][lane] = join_part<2>(part, 0, chunks - 1, out, c, c < out);
+  __syncthreads();
+  const float v = join_parts(sum);
+  if (lane == 0 && mine < out) d_bias[mine] = v;
 }
 
 int64_t stride_of(const moe_rows& r, int64_t cols) { return r.stride ? r.stride : cols; }
@@ -130,7 +156,11 @@ cudaError_t launch_linear(const moe_linear_args& a, cudaStream_t s) {
   e.bias_f32 = a.bias_dtype == MOE_DTYPE_F32;
   e.act = a.activation;
   e.scale = a.residual_scale;
-  return launch_linear_mma(p, s);
+  // Few tokens: up to 16, and up to 64 where the features' CTAs leave half the SMs free (64 tokens of 2688 to 128: 6.3 us,
+  // by launch_linear_mma 7.2; 24 of 4096 to 4096 13.4 / 11.6); not where rows are so short and many that a CTA's start
+  // counts (16 tokens of 512 to 16384: 8.9 / 7.1; of 2688 to 4608 7.0 / 10.3, one 6.1 / 9.9).
+  const bool few = a.n <= 16 ? a.out_features <= 16 * (int64_t)a.in_features : a.n <= 64 && a.out_features <= 16 * 76;
+  return few ? launch_linear_rows(p, s) : launch_linear_mma(p, s);
 }
 
 cudaError_t launch_linear_backward(const moe_linear_args& a, const moe_linear_grads& d, void* workspace, cudaStream_t s) {
@@ -153,22 +183,24 @@ cudaError_t launch_linear_backward(const moe_linear_args& a, const moe_linear_gr
     z.n = a.n;
     z.out = a.out_features;
     z.act = a.activation;
-    z.d_f32 = d.d_out_dtype == MOE_DTYPE_F32;
-    z.z_f32 = a.z_dtype == MOE_DTYPE_F32;
     z.d_out = d.d_out;
     z.z = a.z;
     z.terms = terms;
     z.n_terms = same ? 0 : std::max(d.d_x.data ? terms_x : 0, d.d_weight ? terms_w : 0);
-    if (d.d_bias) z.part = part;
-    const int32_t strips = (a.out_features + kDzColumns - 1) / kDzColumns;
-    z.chunks = std::max(1, std::min({kDzMostChunks, (a.n + 31) / 32, 1216 / strips}));
-    linear_dz_kernel<<<dim3(strips, z.chunks), kDzThreads, 0, s>>>(z);
-    e = cudaGetLastError();
-    if (e == cudaSuccess && d.d_bias) {
-      linear_bias_kernel<<<(a.out_features + kDzThreads - 1) / kDzThreads, kDzThreads, 0, s>>>(part, z.chunks,
-                                                                                               a.out_features, d.d_bias);
-      e = cudaGetLastError();
-    }
+    // A chunk of tokens a CTA, four CTAs an SM (16384 tokens of 8192: 42 us, with two 58, with eight 44); few tokens in one
+    // chunk, whose sums are d_bias, and narrower CTAs.
+    z.lanes = a.n <= kDzOneChunk ? 8 : 32;
+    const int32_t strips = (a.out_features + 8 * z.lanes - 1) / (8 * z.lanes);
+    z.chunks = a.n <= kDzOneChunk ? 1 : std::max(1, std::min({kDzMostChunks, (a.n + 15) / 16, 608 / strips}));
+    if (d.d_bias) z.part = z.chunks == 1 ? d.d_bias : part;
+    const bool d32 = d.d_out_dtype == MOE_DTYPE_F32, z32 = a.z_dtype == MOE_DTYPE_F32, act = a.activation != MOE_LINEAR_NONE;
+    auto kernel = !act  ? (d32 ? linear_dz_kernel<false, float, float> : linear_dz_kernel<false, uint16_t, float>)
+                  : z32 ? (d32 ? linear_dz_kernel<true, float, float> : linear_dz_kernel<true, uint16_t, float>)
+                        : (d32 ? linear_dz_kernel<true, float, uint16_t> : linear_dz_kernel<true, uint16_t, uint16_t>);
+    e = launch_ex(kernel, dim3(strips, z.chunks), dim3(kDzThreads), 0, s, true, z);
+    if (e == cudaSuccess && d.d_bias && z.chunks > 1)
+      e = launch_ex(linear_bias_kernel, dim3((a.out_features + 31) / 32), dim3(kJoinThreads), 0, s, true, (const float*)part,
+                    z.chunks, a.out_features, d.d_bias);
     if (e != cudaSuccess) return e;
   }
   auto operands = [&](LinearProduct& p, int count, bool c_inner) {
@@ -184,6 +216,7 @@ cudaError_t launch_linear_backward(const moe_linear_args& a, const moe_linear_gr
     p.C = a.out_features;
     p.p = {a.weight, a.in_features, false};
     operands(p, terms_x, true);
+    p.share = 2;  // (whichever outputs are asked for, so that their bits do not depend on it)
     p.finish.out = d.d_x.data;
     p.finish.out_stride = stride_of(d.d_x, a.in_features);
     p.finish.out_f32 = d.d_x_dtype == MOE_DTYPE_F32;
@@ -197,6 +230,8 @@ cudaError_t launch_linear_backward(const moe_linear_args& a, const moe_linear_gr
     p.C = a.n;
     p.p = {a.x.data, stride_of(a.x, a.in_features), false};
     operands(p, terms_w, false);
+    p.beside = d.d_x.data != nullptr;
+    p.share = 2;
     p.finish.out = d.d_weight;
     p.finish.out_stride = a.in_features;
     p.finish.out_f32 = d.d_weight_dtype == MOE_DTYPE_F32;

@@ -41,4 +41,14 @@ __device__ __forceinline__ float linear_slope(float z, int32_t act) {
   }
 }
 
+__device__ __forceinline__ float linear_read(const void* p, int64_t at, int32_t f32) {
+  return f32 ? static_cast<const float*>(p)[at] : bf16lo(static_cast<const uint16_t*>(p)[at]);
+}
+__device__ __forceinline__ void linear_write(void* p, int64_t at, int32_t f32, float v) {
+  if (f32)
+    static_cast<float*>(p)[at] = v;
+  else
+    static_cast<uint16_t*>(p)[at] = f2bf_rn(v);
+}
+
 }  // namespace moe

@@ -44,6 +44,7 @@ struct Plan {
   int32_t rows;               // of a tile: the instruction's N
   int32_t tiles_r, tiles, group;
   int32_t split, stages;
+  int32_t beside;             // 1: runs beside the kernel before it, whose results it does not take
   int32_t chain;              // blocks of 64 columns that tensor memory sums before their sum moves to registers
   uint32_t stage_bytes;
   LinearFinish e;
@@ -187,16 +188,6 @@ __device__ __forceinline__ Tile tile_at(const Plan& p, int32_t t, int32_t feats)
   const int32_t tiles_f = p.tiles / p.tiles_r, band = t / (p.group * tiles_f), in = t - band * p.group * tiles_f;
   const int32_t high = min(p.group, p.tiles_r - band * p.group);
   return {in / high * feats, (band * p.group + in % high) * p.rows};
-}
-
-__device__ __forceinline__ float read_value(const void* p, int64_t at, int32_t f32) {
-  return f32 ? static_cast<const float*>(p)[at] : bf16lo(static_cast<const uint16_t*>(p)[at]);
-}
-__device__ __forceinline__ void write_value(void* p, int64_t at, int32_t f32, float v) {
-  if (f32)
-    static_cast<float*>(p)[at] = v;
-  else
-    static_cast<uint16_t*>(p)[at] = f2bf_rn(v);
 }
 
 // A block of 32 rows by 32 features between memory, where a lane moves 16 bytes of a row, and the sums, where a lane has a
@@ -354,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  pdl_wait();
+  if (!p.beside) pdl_wait();
   pdl_launch_dependents();
 
   if (warp == 0) {
@@ -464,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile ti = tile_at(p, t, 128 * CG);
       const int32_t f0 = ti.f0 + 128 * cta + 32 * q, f = f0 + lane, rows = min(p.rows, p.R - ti.r0);
       const bool direct = p.split == 1;
-      const float bias = direct && p.e.bias && f < p.F ? read_value(p.e.bias, f, p.e.bias_f32) : 0.f;
+      const float bias = direct && p.e.bias && f < p.F ? linear_read(p.e.bias, f, p.e.bias_f32) : 0.f;
       const BlockRows to_out = block_rows(p.e.out, p.e.out_stride, p.e.out_f32, ti.r0, f0),
                       to_z = block_rows(p.e.z, p.e.z_stride, p.e.z_f32, ti.r0, f0),
                       from_res = block_rows(const_cast<void*>(p.e.residual), p.e.residual_stride, p.e.residual_f32, ti.r0, f0);
@@ -582,11 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const LinearFinish& e = p.e;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float z = v[j] + (e.bias ? read_value(e.bias, f + j, e.bias_f32) : 0.f);
-        if (e.z) write_value(e.z, (int64_t)r * e.z_stride + f + j, e.z_f32, z);
+        const float z = v[j] + (e.bias ? linear_read(e.bias, f + j, e.bias_f32) : 0.f);
+        if (e.z) linear_write(e.z, (int64_t)r * e.z_stride + f + j, e.z_f32, z);
         v[j] = linear_act(z, e.act);
         if (e.residual)
-          v[j] = fmaf(e.scale, read_value(e.residual, (int64_t)r * e.residual_stride + f + j, e.residual_f32), v[j]);
+          v[j] = fmaf(e.scale, linear_read(e.residual, (int64_t)r * e.residual_stride + f + j, e.residual_f32), v[j]);
       }
       if (e.out_f32)
         *reinterpret_cast<float4*>(static_cast<float*>(e.out) + (int64_t)r * e.out_stride + f) =
@@ -603,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_free<CG>(tmem, cols);
   }
+  if (p.beside) pdl_wait();  // (what follows this kernel follows the one before it too)
 }
 
 template <int CG, bool P_MN, bool Q_MN, bool CHAIN>
@@ -671,11 +663,12 @@ cudaError_t held_clusters(int32_t (&held)[kMaxCluster + 1]) {
 
 struct Shape {
   int32_t cg, rows, split;
+  double cost;
 };
 // The tiles that should take least, in clocks: a block of 64 columns costs an SM 2 clocks a row of its tile for the
-// products or its bytes from L2 (64 a clock), whichever is more; a tile its start and its epilogue; a split the meeting of
-// its sums.
-Shape choose(int32_t R, int32_t F, int32_t blocks, bool q_mn, bool f32, const int32_t (&clusters)[kMaxCluster + 1]) {
+// products or its bytes from L2 (64 a clock), and never less than 500 (128 rows of 4096 columns to 4096: 22.5 us in tiles of
+// 32 rows, 22.2 in one of 128); a tile its start and its epilogue; a split the meeting of its sums.  share: of the SMs, a split takes one part of so many.
+Shape choose(int32_t R, int32_t F, int32_t blocks, bool q_mn, int32_t share, const int32_t (&clusters)[kMaxCluster + 1]) {
   static const int32_t kRows[] = {16, 32, 64, 96, 128, 160, 192, 224, 256};
   Shape best = {};
   double least = 0;
@@ -685,14 +678,14 @@ Shape choose(int32_t R, int32_t F, int32_t blocks, bool q_mn, bool f32, const in
       if (rows >= 2 * R && rows > 64 * cg) continue;
       const int64_t tiles = (int64_t)((R + rows - 1) / rows) * ((F + 128 * cg - 1) / (128 * cg));
       const int32_t held = rows / cg, units = clusters[cg];
-      const double block = std::max(2.0 * rows, (16384.0 + 128.0 * (q_mn ? (held + 63) / 64 * 64 : held)) / 64);
+      const double block = std::max({2.0 * rows, (16384.0 + 128.0 * (q_mn ? (held + 63) / 64 * 64 : held)) / 64, 500.0});
       for (int split = 1; split <= kMaxCluster / cg && split <= blocks; ++split) {
-        if (split > 1 && tiles > clusters[cg * split]) break;
+        if (split > 1 && tiles > clusters[cg * split] / share) break;
         const double waves = split > 1 ? 1 : (double)((tiles + units - 1) / units);
         const double cost = waves * ((blocks + split - 1) / split * block + 1000) + 2000 + 16.0 * rows + (split > 1 ? 1500 + 16.0 * rows : 0);
         if (!best.cg || cost < least) {
           least = cost;
-          best = {cg, rows, split};
+          best = {cg, rows, split, cost};
         }
       }
     }
@@ -711,11 +704,16 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
   p.KB = (a.C + 63) / 64;
   p.terms = a.terms;
   p.e = a.finish;
+  p.beside = a.beside;
   p.split = 1;
   const LinearFinish& f = a.finish;
   const bool q_mn = !a.q[0].c_inner, p_mn = !a.p.c_inner;
   const bool f32 = f.out_f32 || (f.z && f.z_f32);
-  const Shape shape = choose(a.R, a.F, p.KB * p.terms, q_mn, f32, clusters);
+  Shape shape = choose(a.R, a.F, p.KB * p.terms, q_mn, 1, clusters);
+  if (a.share > 1) {  // half of the SMs where that costs less than the other product would lose
+    const Shape half = choose(a.R, a.F, p.KB * p.terms, q_mn, a.share, clusters);
+    if (half.cost < 1.25 * shape.cost) shape = half;
+  }
   const int cg = shape.cg;
   p.rows = shape.rows;
   p.split = shape.split;

@@ -27,8 +27,15 @@ struct LinearProduct {
   int32_t R, F, C, terms;
   LinearOperand p, q[kLinearTerms];
   LinearFinish finish;
+  // Launched right after a product of the same call, whose operands it shares and whose results it does not take: it
+  // begins where that one leaves SMs free.  (That one waits for what came before it before it lets this one begin, so
+  // that the operands are there.)
+  bool beside;
+  int32_t share = 1;  // products that run beside one another
 };
 cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s);
+// For a few rows (linear_rows.cu): one term, both operands with their columns contiguous, R <= 64.
+cudaError_t launch_linear_rows(const LinearProduct& a, cudaStream_t s);
 cudaError_t linear_mma_flags(int32_t* flags);  // reads and clears; the device is idle
 
 }  // namespace moe

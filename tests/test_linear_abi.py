@@ -14,9 +14,9 @@ from nvfp4_quantized_moe_topk_gb300 import build as B
 ARGS = struct.Struct("@8if4xPPPqPqPqPq")
 GRADS = struct.Struct("@3i4xPqPqPP")
 A = 4096  # an aligned address that is never looked at
-GOOD = dict(n=4, inp=64, out_=32, act=0, bt=1, rt=0, zt=0, ot=0, scale=1.0, w=A, bias=A, x=A, xst=0, res=A, rst=0, z=A,
-            zst=0, out=2 * A, ost=0)
-GRAD = dict(dyt=0, dxt=0, dwt=1, dy=A, dyst=0, dx=A, dxst=0, dw=A, db=A)
+GOOD = dict(n=4, inp=64, out_=32, act=0, bt=1, rt=0, zt=0, ot=0, scale=1.0, w=6 * A, bias=A, x=7 * A, xst=0, res=A, rst=0,
+            z=A, zst=0, out=2 * A, ost=0)
+GRAD = dict(dyt=0, dxt=0, dwt=1, dy=A, dyst=0, dx=3 * A, dxst=0, dw=4 * A, db=5 * A)
 
 
 def args(**kw):
@@ -58,6 +58,7 @@ BAD = [(1, dict(n=-1)), (1, dict(inp=0)), (1, dict(out_=-8)), (2, dict(inp=60)),
 @pytest.mark.parametrize("want,kw", BAD + [
     (1, dict(bt=3)), (1, dict(rt=-1)), (1, dict(ot=2)), (1, dict(x=0)), (1, dict(w=0)), (1, dict(out=0)),
     (1, dict(out=A + 8)), (1, dict(bias=A + 2)), (1, dict(bias=A + 1, bt=0)), (1, dict(res=A + 2)), (1, dict(rst=31)),
+    (1, dict(out=7 * A)), (1, dict(out=6 * A)), (1, dict(z=7 * A)),
     (1, dict(out=A, ot=1, z=0)), (1, dict(out=A, ost=64, z=0)), (1, dict(out=A, res=0))])
 def test_refusals(lib, want, kw):
     assert lib.moe_linear(args(**kw), None) == want
@@ -66,9 +67,10 @@ def test_refusals(lib, want, kw):
 @pytest.mark.parametrize("want,kw,gk", [(w, kw, {}) for w, kw in BAD] + [
     (1, {}, dict(dyt=2)), (1, {}, dict(dxt=-1)), (1, {}, dict(dwt=9)), (1, {}, dict(dy=0)), (1, {}, dict(dy=A + 2)),
     (1, {}, dict(dxst=8)), (1, {}, dict(dw=A + 4)), (1, {}, dict(db=A + 2)), (1, dict(act=2, z=0), {}),
-    (1, dict(x=0), {}), (1, dict(w=0), {})])
+    (1, dict(x=0), {}), (1, dict(w=0), {}), (1, {}, dict(dx=A)), (1, {}, dict(dx=7 * A)), (1, {}, dict(dw=6 * A)),
+    (1, {}, dict(db=A))])
 def test_backward_refusals(lib, want, kw, gk):
-    assert lib.moe_linear_backward(args(**kw), grads(**gk), A, 1 << 40, None) == want
+    assert lib.moe_linear_backward(args(**kw), grads(**gk), 8 * A, 1 << 40, None) == want
 
 
 def test_null_empty_and_workspace(lib):
@@ -78,8 +80,8 @@ def test_null_empty_and_workspace(lib):
     assert lib.moe_linear(args(n=0, x=0, w=0, out=0, res=0, z=0), None) == 0
     assert lib.moe_linear_backward(None, grads(), A, need, None) == 1
     assert lib.moe_linear_backward(args(), None, A, need, None) == 1
-    assert lib.moe_linear_backward(args(), grads(), A + 8, need, None) == 1
-    assert lib.moe_linear_backward(args(), grads(), A, need - 1, None) == 3
+    assert lib.moe_linear_backward(args(), grads(), 8 * A + 8, need, None) == 1
+    assert lib.moe_linear_backward(args(), grads(), 8 * A, need - 1, None) == 3
     assert lib.moe_linear_backward(args(), grads(), None, 0, None) == 3
     assert lib.moe_linear_backward(args(n=0), grads(dw=0, db=0), None, 0, None) == 0
     assert lib.moe_linear_get_device_error(ctypes.POINTER(ctypes.c_int32)()) == 1
