@@ -96,6 +96,8 @@ struct moe_nvfp4 {
   // the whole-layer call: logits of a few tokens, and its router's block count
   float* logits = nullptr;
   int32_t *router_count = nullptr, *part_of = nullptr;
+  LayerFewPlan* few = nullptr;
+  float* few_part = nullptr;
   // staging for forward_host
   uint16_t *x_stage = nullptr, *dst_stage = nullptr;
   int32_t* ids_stage = nullptr;
@@ -130,7 +132,7 @@ void free_handle(moe_nvfp4* h) {
                   h->up_tiles, h->dn_tiles,  h->col_done,  h->grid_bar,  h->up_blocks, h->dn_blocks,
                   h->up_tiles16, h->dn_tiles16, h->dec_partial,
                   h->gate_codes, h->gate_scales, h->gate_g, h->blk_hist, h->dense_ids, h->dense_w,
-                  h->logits, h->router_count, h->part_of};
+                  h->logits, h->router_count, h->part_of, h->few, h->few_part};
   for (void* p : ptrs)
     if (p) cudaFree(p);
   if (h->small_dev) cudaFree(h->small_dev);
@@ -262,6 +264,8 @@ moe_status moe_nvfp4_create(const moe_nvfp4_config* config, const moe_nvfp4_weig
   TRY(cudaMalloc(&h->logits, (size_t)kLayerFusedTokens * E * sizeof(float)));
   TRY(cudaMalloc(&h->router_count, sizeof(int32_t)));
   TRY(cudaMalloc(&h->part_of, kLayerMaxParts * sizeof(int32_t)));
+  TRY(cudaMalloc(&h->few, sizeof(LayerFewPlan)));
+  TRY(cudaMalloc(&h->few_part, (size_t)kFewParts * kFewTokens * H * sizeof(float)));
   TRY(cudaMalloc(&h->perm_pair, Rr * sizeof(int32_t)));
   TRY(cudaMalloc(&h->inv, Rr * sizeof(int32_t)));
   TRY(cudaMalloc(&h->err, sizeof(int32_t)));
@@ -591,6 +595,7 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
   const int32_t more = layer_parts(n, k, S);
   const bool parts = more <= kLayerMaxParts && c.n_experts + more <= 1024 && runs_as_one(h, n, c.n_experts + more);
   const bool one = parts || runs_as_one(h, n, c.n_experts);
+  const bool few = one && layer_few_takes(n, c.top_k, H, c.inter, h->gated);
   LayerRouterArgs r = {};
   r.x = a.x;
   r.weight = a.router_weight;
@@ -607,6 +612,7 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
   r.k = k;
   r.shared = S;
   r.part_of = parts && more > 0 ? h->part_of : nullptr;
+  r.few = few ? h->few : nullptr;
   r.weight_f32 = a.router_dtype == MOE_DTYPE_F32;
   {
     TimedLaunch tl(h, s, kKRouting);
@@ -625,6 +631,30 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
     }
     if (e == cudaSuccess) e = launch_layer_router(r, product, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (few) {
+    LayerFewArgs f = {};
+    f.up_tiles = h->up_tiles;
+    f.dn_tiles = h->dn_tiles;
+    f.up_g = h->up_g;
+    f.dn_g = h->dn_g;
+    f.gate_g = h->gate_g;
+    f.x = a.x;
+    f.residual = a.residual;
+    f.dst = a.dst;
+    f.Ap = h->Ap;
+    f.part = h->few_part;
+    f.col_done = h->col_done;
+    f.plan = h->few;
+    f.err = h->err;
+    f.n = n;
+    f.H = H;
+    f.I = c.inter;
+    f.slots = c.top_k;
+    f.parts = layer_few_parts(n, c.top_k, c.inter);
+    h->last_n = n;
+    TimedLaunch tl(h, s, kKDecode);
+    return cuda_status(launch_layer_few(f, h->gated, s));
   }
   if (one) {
     const LayerForward layer = {a.residual, r.part_of ? c.n_experts + more : c.n_experts};

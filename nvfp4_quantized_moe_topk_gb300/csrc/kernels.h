@@ -233,7 +233,33 @@ DecLayout decode_layout(int32_t E, int32_t R, bool can_stage);
 inline bool decode_can_stage(int32_t n, int32_t ext) { return n > 1 || ext; }
 cudaError_t launch_decode(const DecodeArgs& args, int num_sms, cudaStream_t s);
 
-// ---------------------------------------------------------- the whole layer (layer.cu)
+// ------------------------------------------------ the whole layer (layer.cu, layer_few.cu)
+constexpr int kFewTokens = 8, kFewPairs = 96;  // and pairs (tokens times picks and shared experts), at most
+constexpr int kFewParts = 48;                   // parts of the down product's experts, at most
+constexpr int kFewSmem = 190 * 1024;  // (beside 35 KB of static shared memory)
+struct LayerFewPlan {                           // written by the router
+  int32_t experts;              // that any token takes
+  int32_t ticket;               // work items handed out
+  int32_t expert[kFewPairs];
+  int32_t done[kFewPairs];      // row tiles of the expert's up product that are finished
+  int32_t pair[kFewPairs][kDecPassTok];  // the token's pair with the expert, or -1
+  float weight[kFewPairs][kDecPassTok];
+};
+struct LayerFewArgs {
+  const uint8_t *up_tiles, *dn_tiles;  // as DecodeArgs
+  const float *up_g, *dn_g, *gate_g;
+  const uint16_t *x, *residual;        // [n][H] bf16; residual may be nullptr
+  uint16_t* dst;                       // [n][H]
+  uint16_t* Ap;                        // [pairs][I] bf16 (workspace)
+  float* part;                         // [kFewParts][kFewTokens][H] (workspace)
+  int32_t* col_done;                   // [H/16], zero between launches
+  LayerFewPlan* plan;
+  int32_t* err;
+  int32_t n, H, I, slots, parts;
+};
+int32_t layer_few_parts(int32_t n, int32_t slots, int32_t I);
+bool layer_few_takes(int32_t n, int32_t slots, int32_t H, int32_t I, bool gated);
+cudaError_t launch_layer_few(const LayerFewArgs& a, bool gated, cudaStream_t s);
 struct LayerRouterArgs {
   const uint16_t* x;    // [n][H] bf16
   const void* weight;   // [E][H] bf16 or fp32
@@ -245,6 +271,7 @@ struct LayerRouterArgs {
   float* w_out;         // [n][k] or nullptr
   int32_t* count;       // blocks that have finished; zero between launches
   int32_t* part_of;     // [kLayerMaxParts]: each further part's expert; nullptr: experts are not cut
+  LayerFewPlan* few;    // the work of launch_layer_few (no ids and w then); or nullptr
   int32_t n, H, E, k, shared;
   int32_t weight_f32;
 };

@@ -1,30 +1,35 @@
 // layer.cu -- the router of the whole-layer call: logits and picks in one launch.
 //
 // For a few tokens the router is all latency: its weights (0.7 MB for 128
-// experts of 2688) take 0.1 us to read.  A block takes four experts, four warps
-// each; a warp holds its part of an expert's row in registers and goes over the
-// tokens.  The block that finishes last routes the tokens, a warp a token, from
-// the logits the others left in L2, and adds the shared experts to the picks, so
-// that the streaming kernel that follows serves them beside the routed ones; an
-// expert of more than 8 tokens it cuts into parts (a decode batch of 32, gated,
-// two shared experts, an expert of 10 tokens: 461 us with the shared ones cut alone, 200 so).
+// experts of 2688) take 0.1 us to read.  A block takes 16 experts, each of its 32
+// warps two or three steps of 32 columns, whose loads are all in flight at once;
+// warp-level matrix instructions take 16 experts by 8 tokens, and the warps' sums
+// meet in shared memory, in order.  An fp32 weight goes in as three bf16 terms,
+// which keep its 24 bits, as products with bf16 x are exact.  The block that
+// finishes last routes the tokens, a warp a token, from the logits that the others
+// left in L2, adds the shared experts to the picks, and lays out the work for the
+// kernel that follows: up to 8 tokens as the experts that any of them takes
+// (layer_few.cu), more with experts of more than 8 tokens cut into parts, which
+// would keep the streaming kernel (decode.cu) from staging and have its warps pass
+// over their tiles again and again (a decode batch of 32, gated, two shared
+// experts, an expert of 10 tokens: 461 us with the shared ones cut alone, 200 so).
 #include <algorithm>
 
 #include "block.cuh"
 #include "kernels.h"
 #include "router.cuh"
+#include "tile.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kLayerThreads = 512, kLayerWarps = kLayerThreads / 32;
-constexpr int kSplit = 4, kLayerExperts = kLayerWarps / kSplit;  // warps an expert, experts a block
-constexpr int kMaxVecs = 4;  // 16-byte vectors of a row a lane holds at once: 32 lanes x 4 warps x 4 x 8 values = 4096
+constexpr int kLayerThreads = 1024, kLayerWarps = kLayerThreads / 32, kLayerExperts = 16;
 
 // One token's picks: k of the logits, then the shared experts.
+// (ids, w: the token's.)
 template <int SLOTS>
-__device__ __forceinline__ void pick_token(const LayerRouterArgs& a, int32_t t, int lane) {
+__device__ __forceinline__ void pick_token(const LayerRouterArgs& a, int32_t t, int lane, int32_t* ids, float* w) {
   float z[SLOTS];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
@@ -32,9 +37,6 @@ __device__ __forceinline__ void pick_token(const LayerRouterArgs& a, int32_t t, 
     z[i] = 0.f;
     if (e < a.E) z[i] = __ldcg(a.logits + (int64_t)t * a.E + e) + (a.bias ? __ldg(a.bias + e) : 0.f);
   }
-  const int32_t slots = a.k + a.shared;
-  int32_t* ids = a.ids + (int64_t)t * slots;
-  float* w = a.w + (int64_t)t * slots;
   route_token<SLOTS>(z, a.E, a.k, lane, ids, w, nullptr);
   __syncwarp();
   if (lane < a.k) {
@@ -47,17 +49,17 @@ __device__ __forceinline__ void pick_token(const LayerRouterArgs& a, int32_t t, 
     w[a.k + lane] = 1.f;
   }
 }
-__device__ __forceinline__ void pick_any(const LayerRouterArgs& a, int32_t t, int lane) {
+__device__ __noinline__ void pick_any(const LayerRouterArgs& a, int32_t t, int lane, int32_t* ids, float* w) {
   if (a.E <= 64)
-    pick_token<2>(a, t, lane);
+    pick_token<2>(a, t, lane, ids, w);
   else if (a.E <= 128)
-    pick_token<4>(a, t, lane);
+    pick_token<4>(a, t, lane, ids, w);
   else if (a.E <= 256)
-    pick_token<8>(a, t, lane);
+    pick_token<8>(a, t, lane, ids, w);
   else if (a.E <= 512)
-    pick_token<16>(a, t, lane);
+    pick_token<16>(a, t, lane, ids, w);
   else
-    pick_token<32>(a, t, lane);
+    pick_token<32>(a, t, lane, ids, w);
 }
 
 // After the picks, by one block: an expert's tokens beyond each 8 move to a further part of it.  Parts are dealt in the
@@ -103,64 +105,142 @@ __device__ void deal_parts(const LayerRouterArgs& a, PartSpace& sp) {
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const LayerRouterArgs a, int32_t pick) {
-  __shared__ union {
-    float sums[kLayerWarps][kLayerFusedTokens];
-    PartSpace parts;
-  } sm;
-  __shared__ int32_t last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp % kSplit;
-  const int32_t e = blockIdx.x * kLayerExperts + warp / kSplit, vecs = a.H / 8;
-  const int32_t t0 = blockIdx.y * kLayerFusedTokens, tokens = min(kLayerFusedTokens, a.n - t0);
-  const T* row = static_cast<const T*>(a.weight) + (int64_t)min(e, a.E - 1) * a.H;
-  float w[kMaxVecs][8];
-#pragma unroll
-  for (int i = 0; i < kMaxVecs; ++i) {
-    const int32_t v = (i * kSplit + slice) * 32 + lane;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = 0.f;
-    if (v < vecs) {
-      if (sizeof(T) == 2) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(row) + v), w[i]);
-      } else {
-        const float4 lo = __ldg(reinterpret_cast<const float4*>(row) + 2 * v), hi = __ldg(reinterpret_cast<const float4*>(row) + 2 * v + 1);
-        w[i][0] = lo.x;
-        w[i][1] = lo.y;
-        w[i][2] = lo.z;
-        w[i][3] = lo.w;
-        w[i][4] = hi.x;
-        w[i][5] = hi.y;
-        w[i][6] = hi.z;
-        w[i][7] = hi.w;
-      }
-    }
+// After the picks of a few tokens, by one block: the experts that any of them takes, in the order of their first pair,
+// and each token's pair of them.  (The plan's pairs and counts have been cleared.)
+struct FewSpace {
+  int32_t id[kFewPairs];
+  float w[kFewPairs];
+  int32_t at[1024], count[kLayerWarps];
+};
+__device__ void list_experts(const LayerRouterArgs& a, FewSpace& sp) {
+  const int32_t slots = a.k + a.shared, pairs = a.n * slots, p = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  LayerFewPlan& f = *a.few;
+  const int32_t e = p < pairs ? sp.id[p] : -1;
+  bool first = e >= 0;
+  for (int32_t q = 0; first && q < p; ++q) first = sp.id[q] != e;
+  const uint32_t who = __ballot_sync(0xffffffffu, first);
+  if (lane == 0) sp.count[warp] = __popc(who);
+  __syncthreads();
+  int32_t at = __popc(who & ((1u << lane) - 1)), all = 0;
+  for (int32_t w = 0; w < (kFewPairs + 31) / 32; ++w) {
+    if (w < warp) at += sp.count[w];
+    all += sp.count[w];
   }
-  for (int32_t t = 0; t < tokens; ++t) {
-    const uint4* x = reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + t) * a.H);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMaxVecs; ++i) {
-      const int32_t v = (i * kSplit + slice) * 32 + lane;
-      if (v < vecs) {
-        float xv[8];
-        unpack8(__ldg(x + v), xv);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(xv[j], w[i][j], sum);
-      }
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) sm.sums[warp][t] = sum;
+  if (first) {
+    f.expert[at] = e;
+    sp.at[e] = at;
+  }
+  if (threadIdx.x == 0) {
+    f.experts = all;
+    f.ticket = 0;
   }
   __syncthreads();
-  for (int32_t i = threadIdx.x; i < tokens * kLayerExperts; i += kLayerThreads) {
-    const int32_t t = i / kLayerExperts, q = i % kLayerExperts, to = blockIdx.x * kLayerExperts + q;
-    if (to >= a.E) continue;
-    float v = 0.f;
+  if (p < pairs) {
+    f.pair[sp.at[e]][p / slots] = p;
+    f.weight[sp.at[e]][p / slots] = sp.w[p];
+  }
+}
+
+// Eight consecutive values of a weight row as bf16 terms whose sum they are.
+template <typename T>
+struct RouterTerms {
+  static constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
+  uint4 v[kTerms];
+};
+__device__ __forceinline__ RouterTerms<uint16_t> router_terms(const uint16_t* p) {
+  return {{__ldg(reinterpret_cast<const uint4*>(p))}};
+}
+__device__ __forceinline__ RouterTerms<float> router_terms(const float* p) {
+  const float4 lo = __ldg(reinterpret_cast<const float4*>(p)), hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  RouterTerms<float> r;
 #pragma unroll
-    for (int s = 0; s < kSplit; ++s) v += sm.sums[q * kSplit + s][t];
-    a.logits[(int64_t)(t0 + t) * a.E + to] = v;
+  for (int k = 0; k < 3; ++k) {
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d[i] = pack2(v[2 * i], v[2 * i + 1]);
+      v[2 * i] -= bf16lo(d[i]);
+      v[2 * i + 1] -= bf16hi(d[i]);
+    }
+    r.v[k] = make_uint4(d[0], d[1], d[2], d[3]);
+  }
+  return r;
+}
+
+// TILES: tiles of 8 tokens that a pass over the weights serves; with one, a warp's steps are all in flight at once.
+template <typename T, int TILES>
+__global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __grid_constant__ LayerRouterArgs a, int32_t pick) {
+  extern __shared__ __align__(16) float dyn[];  // [warps][8 TILES][17], then the last block's work
+  __shared__ int32_t last;
+  constexpr int kGroup = 8 * TILES, kAhead = TILES == 1 && sizeof(T) == 2 ? 4 : 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int32_t e0 = blockIdx.x * kLayerExperts, steps = (a.H + 31) / 32;
+  const int32_t s0 = steps * warp / kLayerWarps, s1 = steps * (warp + 1) / kLayerWarps;
+  const T* ra = static_cast<const T*>(a.weight) + (int64_t)min(e0 + g, a.E - 1) * a.H + 8 * t;
+  const T* rb = static_cast<const T*>(a.weight) + (int64_t)min(e0 + g + 8, a.E - 1) * a.H + 8 * t;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.few && blockIdx.x == 0) {  // (the last block writes the pairs, after this one has finished or is it)
+    for (int32_t i = threadIdx.x; i < kFewPairs * kDecPassTok; i += kLayerThreads)
+      a.few->pair[i / kDecPassTok][i % kDecPassTok] = -1;
+    if (threadIdx.x < kFewPairs) a.few->done[threadIdx.x] = 0;
+  }
+  const int32_t end = min(a.n, ((int32_t)blockIdx.y + 1) * kLayerFusedTokens);
+  for (int32_t t0 = blockIdx.y * kLayerFusedTokens; t0 < end; t0 += kGroup) {
+    const int32_t tokens = min(kGroup, end - t0);
+    float acc[TILES][4] = {};
+    for (int32_t s = s0; s < s1; s += kAhead) {  // (a step is whole: H is a multiple of 64)
+      RouterTerms<T> wa[kAhead], wb[kAhead];
+      uint4 x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s + i >= s1) break;
+        wa[i] = router_terms(ra + 32 * (s + i));
+        wb[i] = router_terms(rb + 32 * (s + i));
+        if (TILES == 1) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (g < tokens) x[i] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + g) * a.H + 32 * (s + i) + 8 * t));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s + i >= s1) break;
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+          if (8 * j >= tokens) break;
+          if (TILES > 1) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (8 * j + g < tokens)
+              x[i] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + 8 * j + g) * a.H + 32 * (s + i) + 8 * t));
+          }
+#pragma unroll
+          for (int k = 0; k < RouterTerms<T>::kTerms; ++k) {
+            mma_bf16_16816(acc[j], wa[i].v[k].x, wb[i].v[k].x, wa[i].v[k].y, wb[i].v[k].y, x[i].x, x[i].y);
+            mma_bf16_16816(acc[j], wa[i].v[k].z, wb[i].v[k].z, wa[i].v[k].w, wb[i].v[k].w, x[i].z, x[i].w);
+          }
+        }
+      }
+    }
+    float(*sums)[kGroup][17] = reinterpret_cast<float(*)[kGroup][17]>(dyn);
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+      if (8 * j >= tokens) break;
+      sums[warp][8 * j + 2 * t][g] = acc[j][0];
+      sums[warp][8 * j + 2 * t + 1][g] = acc[j][1];
+      sums[warp][8 * j + 2 * t][g + 8] = acc[j][2];
+      sums[warp][8 * j + 2 * t + 1][g + 8] = acc[j][3];
+    }
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < tokens * kLayerExperts; i += kLayerThreads) {
+      const int32_t e = e0 + i % kLayerExperts;
+      if (e >= a.E) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kLayerWarps; ++w) v += sums[w][i / kLayerExperts][i % kLayerExperts];
+      a.logits[(int64_t)(t0 + i / kLayerExperts) * a.E + e] = v;
+    }
+    __syncthreads();
   }
   if (!pick) return;
   __threadfence();
@@ -172,28 +252,44 @@ __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const Layer
   }
   __syncthreads();
   if (!last) return;
-  for (int32_t t = warp; t < a.n; t += kLayerWarps) pick_any(a, t, lane);
-  if (!a.part_of || a.n <= kDecPassTok) return;
+  const int32_t slots = a.k + a.shared;
+  FewSpace& few = *reinterpret_cast<FewSpace*>(dyn);
+  for (int32_t k = warp; k < a.n; k += kLayerWarps)
+    pick_any(a, k, lane, a.few ? few.id + k * slots : a.ids + (int64_t)k * slots, a.few ? few.w + k * slots : a.w + (int64_t)k * slots);
   __syncthreads();
-  deal_parts(a, sm.parts);
+  if (a.few)
+    list_experts(a, few);
+  else if (a.part_of && a.n > kDecPassTok)
+    deal_parts(a, *reinterpret_cast<PartSpace*>(dyn));
 }
 
 __global__ void __launch_bounds__(256) layer_pick_kernel(const LayerRouterArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t < a.n) pick_any(a, (int32_t)t, threadIdx.x & 31);
+  if (t < a.n) pick_any(a, (int32_t)t, threadIdx.x & 31, a.ids + t * (a.k + a.shared), a.w + t * (a.k + a.shared));
+}
+
+}  // namespace
+
+namespace {
+
+template <typename T, int TILES>
+cudaError_t router_launch(const LayerRouterArgs& a, bool pick, cudaStream_t s) {
+  static std::atomic<bool> configured[kMaxDevices];
+  constexpr size_t smem = std::max({(size_t)kLayerWarps * 8 * TILES * 17 * sizeof(float), sizeof(PartSpace), sizeof(FewSpace)});
+  const cudaError_t e = raise_smem_limit(layer_router_kernel<T, TILES>, (int)smem, configured);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((a.E + kLayerExperts - 1) / kLayerExperts),
+                  (unsigned)((a.n + kLayerFusedTokens - 1) / kLayerFusedTokens));
+  return launch_ex(layer_router_kernel<T, TILES>, grid, dim3(kLayerThreads), smem, s, true, a, (int32_t)pick);
 }
 
 }  // namespace
 
 cudaError_t launch_layer_router(const LayerRouterArgs& a, bool have_logits, cudaStream_t s) {
   if (!have_logits) {
-    const int32_t pick = a.n <= kLayerFusedTokens;
-    const dim3 grid((unsigned)((a.E + kLayerExperts - 1) / kLayerExperts), (unsigned)((a.n + kLayerFusedTokens - 1) / kLayerFusedTokens));
-    if (a.weight_f32)
-      layer_router_kernel<float><<<grid, kLayerThreads, 0, s>>>(a, pick);
-    else
-      layer_router_kernel<uint16_t><<<grid, kLayerThreads, 0, s>>>(a, pick);
-    const cudaError_t e = cudaGetLastError();
+    const bool pick = a.n <= kLayerFusedTokens;
+    const cudaError_t e = a.n <= 8 ? (a.weight_f32 ? router_launch<float, 1>(a, pick, s) : router_launch<uint16_t, 1>(a, pick, s))
+                                   : (a.weight_f32 ? router_launch<float, 4>(a, pick, s) : router_launch<uint16_t, 4>(a, pick, s));
     if (e != cudaSuccess || pick) return e;
   }
   layer_pick_kernel<<<(unsigned)((a.n + 7) / 8), 256, 0, s>>>(a);

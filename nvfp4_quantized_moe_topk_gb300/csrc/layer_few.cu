@@ -1,0 +1,434 @@
+// layer_few.cu -- the experts of the whole-layer call for a few tokens, both
+// products and the sum in one launch.
+//
+// Reading the picked experts' weights bounds it (one token, 6 + 1 experts of 2688
+// x 1856: 39 MB), and whatever keeps those reads from being in flight.  Work comes
+// in items of 16 rows, whose weights are one run of memory that a bulk copy brings
+// to one of a block's three slots while the block works on another.  Eight warps
+// multiply, each an eighth of the item's columns; a ninth draws the items, asks
+// for their weights and brings a down item's rows, a tenth finishes the sums, so
+// that the eight wait for none of that.
+// First come the up product's items (an expert's 16 rows; gated: its gate and up
+// tiles), then the down product's (16 columns of the output over a part of the
+// experts' rows, so that there are a few items an SM).
+//
+// A block draws its items' numbers in order.  A down item's weights
+// are on their way before its block waits for the up items of the experts that it
+// needs; those have lower numbers, so their blocks are under way, and a block
+// waits only when it has finished its own up items: every wait ends (and is
+// bounded all the same).  The last part to finish 16 columns adds the parts in
+// order, so that the bits do not depend on timing.
+//
+// The tokens are the matrix instruction's columns: token t is column t of every
+// expert's product, its activations zero where it does not take the expert.
+#include <algorithm>
+
+#include "kernels.h"
+#include "tile.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kFewWarps = 8, kFewMath = 32 * kFewWarps, kFewThreads = kFewMath + 64;
+constexpr int kFewSlots = 3;
+
+// Shared memory after the slots of weights: x [n][H], slots of rows [n][part's tiles x 64], rows padded by 16 bytes.
+struct FewLayout {
+  uint32_t slot, x_row, a_row, x_at, a_at, total;
+};
+__host__ __device__ inline FewLayout few_layout(int32_t n, int32_t H, int32_t I, int32_t up_tiles, int32_t part_tiles) {
+  FewLayout l;
+  const int32_t up = up_tiles * (H / 64), most = up > part_tiles ? up : part_tiles;
+  l.slot = ((uint32_t)most * kTileBytes + 127) / 128 * 128;
+  l.x_row = 2 * H + 16;
+  l.a_row = part_tiles * 128 + 16;
+  l.x_at = kFewSlots * l.slot;
+  l.a_at = l.x_at + n * l.x_row;
+  l.total = l.a_at + kFewSlots * n * l.a_row;
+  return l;
+}
+
+template <bool GATED>
+struct FewSums {  // gated: the gate's, then the up's
+  float v[GATED ? 2 : 1][kFewWarps][16][kDecPassTok + 1];
+};
+// The router's plan, brought to shared memory once.
+struct FewWork {
+  int32_t expert[kFewPairs];
+  int16_t pair[kFewPairs][kDecPassTok];
+  float weight[kFewPairs][kDecPassTok];
+  float up_g[kFewPairs], dn_g[kFewPairs], gate_g[kFewPairs];  // times 2^8: the tiles carry 2^-8
+  int32_t experts;
+};
+// Named barriers, one of each for a slot: the next item from the drawing warp, its sums' place free from the finishing
+// one; the sums to the finishing warp; the slot back to the drawing one.
+__device__ __forceinline__ void bar_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+constexpr int kBarItem = 1, kBarSums = kBarItem + kFewSlots, kBarFree = kBarSums + kFewSlots, kBarMath = kBarFree + kFewSlots;
+static_assert(kBarMath < 16, "named barriers");
+__device__ __forceinline__ void red_release(int32_t* p) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+
+__device__ __forceinline__ int32_t ld_acquire(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+template <bool GATED>
+__device__ __forceinline__ void keep(FewSums<GATED>& sums, int which, int warp, int lane, const float (&acc)[4]) {
+  const int g = lane >> 2, t = lane & 3;
+  sums.v[which][warp][g][2 * t] = acc[0];
+  sums.v[which][warp][g][2 * t + 1] = acc[1];
+  sums.v[which][warp][g + 8][2 * t] = acc[2];
+  sums.v[which][warp][g + 8][2 * t + 1] = acc[3];
+}
+template <bool GATED>
+__device__ __forceinline__ float sum_of(const FewSums<GATED>& sums, int which, int row, int col) {
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kFewWarps; ++w) v += sums.v[which][w][row][col];
+  return v;
+}
+// The lane's 16 values of a k-tile of its token's row.
+struct FewX {
+  uint4 x0, x1;
+};
+__device__ __forceinline__ FewX load_x(const uint8_t* row, int32_t tile, bool live) {
+  FewX x = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (live) {
+    x.x0 = *reinterpret_cast<const uint4*>(row + tile * 128);
+    x.x1 = *reinterpret_cast<const uint4*>(row + tile * 128 + 16);
+  }
+  return x;
+}
+
+// A part's tiles: [first, last) of all experts' (expert by expert).
+__device__ __forceinline__ int32_t part_begin(const LayerFewArgs& a, int32_t tiles, int32_t part) {
+  return (int32_t)((int64_t)tiles * part / a.parts);
+}
+
+// One thread: asks for an item's weights.
+template <bool GATED>
+__device__ __forceinline__ void issue(const LayerFewArgs& a, const FewWork& p, int32_t item, int32_t up, uint8_t* slot,
+                                      uint64_t* bar) {
+  fence_proxy_async_smem();
+  if (item < up) {
+    const int32_t KT = (GATED ? 2 : 1) * (a.H / 64), NT = a.I / 16;
+    const uint32_t bytes = (uint32_t)KT * kTileBytes;
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_g2s(slot, a.up_tiles + ((int64_t)p.expert[item / NT] * NT + item % NT) * bytes, bytes, bar);
+    return;
+  }
+  const int32_t KT = a.I / 64, NT = a.H / 16, ct = (item - up) % NT, part = (item - up) / NT, all = p.experts * KT;
+  const int32_t p0 = part_begin(a, all, part), p1 = part_begin(a, all, part + 1);
+  mbar_arrive_expect_tx(bar, (uint32_t)(p1 - p0) * kTileBytes);
+  for (int32_t i = p0; i < p1;) {
+    const int32_t ai = i / KT, kt = i - ai * KT, run = min(KT - kt, p1 - i);
+    bulk_g2s(slot + (i - p0) * kTileBytes, a.dn_tiles + (((int64_t)p.expert[ai] * NT + ct) * KT + kt) * kTileBytes,
+             (uint32_t)run * kTileBytes, bar);
+    i += run;
+  }
+}
+
+// The warps' sums of an up item.
+template <bool GATED>
+__device__ __forceinline__ void up_sums(const LayerFewArgs& a, const FewWork& p, int32_t ai, const uint8_t* slot,
+                                        const uint8_t* xs, uint32_t x_row, const uint32_t* lut, FewSums<GATED>& sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int32_t KT = a.H / 64, k0 = KT * warp / kFewWarps, k1 = KT * (warp + 1) / kFewWarps;
+  constexpr int kTiles = GATED ? 2 : 1;  // the gate's, then the up's
+  const bool mine = g < a.n && p.pair[ai][g] >= 0;
+  const uint8_t* row = xs + g * x_row + 32 * t;
+  float acc[kTiles][4] = {}, acc2[kTiles][4] = {};
+#pragma unroll 2
+  for (int32_t k = k0; k < k1; ++k) {
+    const FewX x = load_x(row, k, mine);
+#pragma unroll
+    for (int h = 0; h < kTiles; ++h)
+      tile_mma(slot + (h * KT + k) * kTileBytes, x.x0, x.x1, lane, lut, acc[h], acc2[h]);
+  }
+#pragma unroll
+  for (int h = 0; h < kTiles; ++h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[h][i] += acc2[h][i];
+    keep(sums, h, warp, lane, acc[h]);
+  }
+}
+// By the finishing warp: the expert's rows, and word that they are there.
+template <bool GATED>
+__device__ __forceinline__ void up_finish(const LayerFewArgs& a, const FewWork& p, int32_t ai, int32_t rt, const FewSums<GATED>& sums) {
+  const int lane = threadIdx.x & 31;
+  for (int32_t i = lane; i < 16 * a.n; i += 32) {
+    const int32_t r = i & 15, col = i >> 4, pair = p.pair[ai][col];
+    if (pair < 0) continue;
+    const float h = sum_of(sums, GATED ? 1 : 0, r, col) * p.up_g[ai];
+    float v;
+    if (GATED) {
+      const float q = sum_of(sums, 0, r, col) * p.gate_g[ai];
+      v = q / (1.f + expf(-q)) * h;
+    } else {
+      const float m = h > 0.f ? h : 0.f;
+      v = m * m;
+    }
+    a.Ap[(int64_t)pair * a.I + 16 * rt + r] = f2bf_rn(v);
+  }
+  __syncwarp();
+  if (lane == 0) red_release(&a.plan->done[ai]);
+}
+
+// By the drawing warp: the rows of a down item's experts, once they are there.
+__device__ __forceinline__ void down_rows(const LayerFewArgs& a, const FewWork& p, int32_t part, uint8_t* as, uint32_t a_row) {
+  const int lane = threadIdx.x & 31;
+  const int32_t KT = a.I / 64, all = p.experts * KT;
+  const int32_t p0 = part_begin(a, all, part), p1 = part_begin(a, all, part + 1);
+  for (int32_t i = p0; i < p1;) {  // expert by expert
+    const int32_t ai = i / KT, kt = i - ai * KT, run = min(KT - kt, p1 - i);
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (ld_acquire(&a.plan->done[ai]) < a.I / 16) {
+        __nanosleep(40);
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          atomicOr(a.err, kFlagTimeout);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+    for (int32_t col = 0; col < a.n; ++col) {
+      const int32_t pair = p.pair[ai][col];
+      uint8_t* to = as + col * a_row + (i - p0) * 128;
+      const uint16_t* from = a.Ap + (int64_t)pair * a.I + 64 * kt;
+      for (int32_t k0 = lane; k0 < 8 * run; k0 += 8 * 32) {
+        uint4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q] = make_uint4(0, 0, 0, 0);
+          if (pair >= 0 && k0 + 32 * q < 8 * run) v[q] = ld_cg_v4(from + 8 * (k0 + 32 * q));
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (k0 + 32 * q < 8 * run) *reinterpret_cast<uint4*>(to + 16 * (k0 + 32 * q)) = v[q];
+      }
+    }
+    i += run;
+  }
+}
+
+// The warps' sums of a down item.
+template <bool GATED>
+__device__ __forceinline__ void down_sums(const LayerFewArgs& a, const FewWork& p, int32_t part, const uint8_t* slot,
+                                          const uint8_t* as, uint32_t a_row, const uint32_t* lut, FewSums<GATED>& sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int32_t KT = a.I / 64, all = p.experts * KT;
+  const int32_t p0 = part_begin(a, all, part), tiles = part_begin(a, all, part + 1) - p0;
+  const int32_t i0 = tiles * warp / kFewWarps, i1 = tiles * (warp + 1) / kFewWarps;
+  const uint8_t* row = as + g * a_row + 32 * t;
+  float total[4] = {}, acc[4] = {}, acc2[4] = {};
+  for (int32_t i = i0; i < i1;) {  // expert by expert
+    const int32_t ai = (p0 + i) / KT, end = min(i1, (ai + 1) * KT - p0);
+#pragma unroll 2
+    for (; i < end; ++i) {
+      const FewX x = load_x(row, i, g < a.n);
+      tile_mma(slot + i * kTileBytes, x.x0, x.x1, lane, lut, acc, acc2);
+    }
+    const float dg = p.dn_g[ai];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t col = 2 * t + (k & 1);
+      if (col < a.n && p.pair[ai][col] >= 0) total[k] = fmaf(p.weight[ai][col] * dg, acc[k] + acc2[k], total[k]);
+      acc[k] = acc2[k] = 0.f;
+    }
+  }
+  keep(sums, 0, warp, lane, total);
+}
+// By the finishing warp: the part's sums, and from the last part of its columns the output.
+template <bool GATED>
+__device__ __forceinline__ void down_finish(const LayerFewArgs& a, int32_t ct, int32_t part, const FewSums<GATED>& sums) {
+  const int lane = threadIdx.x & 31;
+  for (int32_t i = lane; i < 16 * a.n; i += 32) {
+    const int64_t at = (int64_t)(i >> 4) * a.H + 16 * ct + (i & 15);
+    a.part[(int64_t)part * a.n * a.H + at] = sum_of(sums, 0, i & 15, i >> 4);
+  }
+  __syncwarp();
+  int32_t last = 0;
+  if (lane == 0) {
+    last = atom_add_acq_rel_gpu(&a.col_done[ct], 1) == a.parts - 1;
+    if (last) a.col_done[ct] = 0;
+  }
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
+  __syncwarp();
+  for (int32_t i = lane; i < 16 * a.n; i += 32) {
+    const int64_t at = (int64_t)(i >> 4) * a.H + 16 * ct + (i & 15);
+    float v = 0.f;
+#pragma unroll 8
+    for (int32_t q = 0; q < a.parts; ++q) v += ld_cg_f32(a.part + (int64_t)q * a.n * a.H + at);
+    if (a.residual) v += __uint_as_float((uint32_t)a.residual[at] << 16);
+    a.dst[at] = f2bf_rn(v);
+  }
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kFewThreads, 2) layer_few_kernel(const __grid_constant__ LayerFewArgs a, const FewLayout l) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ uint32_t lut[256];
+  __shared__ FewSums<GATED> sums[kFewSlots];
+  __shared__ FewWork work;
+  __shared__ __align__(8) uint64_t full[kFewSlots];
+  __shared__ int32_t item[kFewSlots], summed[kFewSlots];  // drawn; whose sums lie there
+  __shared__ volatile int32_t finished;  // up items that the block has finished
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 256; i += kFewThreads) lut[i] = scale_bf16_2p118((uint32_t)i) * 0x10001u;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFewSlots; ++s) mbar_init(&full[s], 1);
+    finished = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  int32_t ticket = 0;
+  if (threadIdx.x == kFewMath) ticket = atomicAdd(&a.plan->ticket, 1);
+  const int32_t most = a.n * a.slots;  // experts, at most (the rest of the plan is not looked at)
+  for (int32_t i = threadIdx.x; i < most; i += kFewThreads) work.expert[i] = a.plan->expert[i];
+  for (int32_t i = threadIdx.x; i < most * kDecPassTok; i += kFewThreads) {
+    work.pair[i / kDecPassTok][i % kDecPassTok] = (int16_t)a.plan->pair[i / kDecPassTok][i % kDecPassTok];
+    work.weight[i / kDecPassTok][i % kDecPassTok] = a.plan->weight[i / kDecPassTok][i % kDecPassTok];
+  }
+  const int32_t experts = a.plan->experts;
+  if (threadIdx.x == 0) work.experts = experts;
+  __syncthreads();
+  const int32_t NT = a.I / 16, CT = a.H / 16, up = experts * NT, items = up + a.parts * CT;
+
+  if (threadIdx.x >= kFewMath + 32) {  // the finishing warp
+    for (int32_t i = lane; i < experts; i += 32) {
+      work.up_g[i] = 256.f * a.up_g[work.expert[i]];
+      work.dn_g[i] = 256.f * a.dn_g[work.expert[i]];
+      if (GATED) work.gate_g[i] = 256.f * a.gate_g[work.expert[i]];
+    }
+    __syncwarp();
+    for (int s = 0; s < kFewSlots; ++s) bar_arrive(kBarItem + s, kFewThreads);
+    for (int s = 0;; s = s + 1 == kFewSlots ? 0 : s + 1) {
+      bar_sync(kBarSums + s, kFewMath + 32);
+      const int32_t now = summed[s];  // (item[s] may be the next already)
+      if (now >= items) break;
+      if (now < up) {
+        up_finish<GATED>(a, work, now / NT, now % NT, sums[s]);
+        if (lane == 0) finished = finished + 1;
+      } else {
+        down_finish<GATED>(a, (now - up) % CT, (now - up) / CT, sums[s]);
+      }
+      __syncwarp();
+      bar_arrive(kBarItem + s, kFewThreads);
+    }
+    return;
+  }
+  if (threadIdx.x >= kFewMath) {  // the drawing warp
+    int32_t drawn = 0;  // up items
+    // The next item into slot s: its weights asked for, then a down item's rows, for which it waits only when the block
+    // has no up item of its own left to finish.
+    auto draw = [&](int s) {
+      const int32_t now = __shfl_sync(0xffffffffu, ticket, 0);
+      if (lane == 0) {
+        item[s] = now;
+        if (now < items) issue<GATED>(a, work, now, up, sm + s * l.slot, &full[s]);
+        ticket = atomicAdd(&a.plan->ticket, 1);
+      }
+      if (now < up) {
+        ++drawn;
+      } else if (now < items) {
+        const uint64_t t0 = globaltimer_ns();
+        while (finished < drawn && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(20);
+        down_rows(a, work, (now - up) / CT, sm + l.a_at + s * a.n * l.a_row, l.a_row);
+      }
+      __syncwarp();
+      bar_arrive(kBarItem + s, kFewThreads);
+      return now;
+    };
+    int32_t held[kFewSlots];
+#pragma unroll
+    for (int s = 0; s < kFewSlots; ++s) held[s] = draw(s);
+    for (bool more = true; more;) {
+#pragma unroll
+      for (int s = 0; s < kFewSlots; ++s) {
+        if (held[s] >= items) {
+          more = false;
+          break;
+        }
+        bar_sync(kBarFree + s, kFewMath + 32);
+        held[s] = draw(s);
+      }
+    }
+    return;
+  }
+
+  for (int32_t i = threadIdx.x; i < a.n * (a.H / 8); i += kFewMath) {
+    const int32_t col = i / (a.H / 8), at = i - col * (a.H / 8);
+    *reinterpret_cast<uint4*>(sm + l.x_at + col * l.x_row + 16 * at) =
+        __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)col * a.H) + at);
+  }
+  bar_sync(kBarMath, kFewMath);
+  uint32_t parity = 0;
+  for (int s = 0;;) {
+    bar_sync(kBarItem + s, kFewThreads);
+    const int32_t now = item[s];
+    if (threadIdx.x == 0) summed[s] = now;
+    if (now >= items) {
+      bar_arrive(kBarSums + s, kFewMath + 32);
+      break;
+    }
+    mbar_wait(&full[s], parity, a.err);
+    const uint8_t* slot = sm + s * l.slot;
+    if (now < up)
+      up_sums<GATED>(a, work, now / NT, slot, sm + l.x_at, l.x_row, lut, sums[s]);
+    else
+      down_sums<GATED>(a, work, (now - up) / CT, slot, sm + l.a_at + s * a.n * l.a_row, l.a_row, lut, sums[s]);
+    bar_arrive(kBarSums + s, kFewMath + 32);
+    bar_arrive(kBarFree + s, kFewMath + 32);
+    if (++s == kFewSlots) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+}
+
+template <bool GATED>
+cudaError_t few_launch(const LayerFewArgs& a, const FewLayout& l, int sms, cudaStream_t s) {
+  static std::atomic<bool> configured[kMaxDevices];
+  cudaError_t e = raise_smem_limit(layer_few_kernel<GATED>, kFewSmem, configured);
+  int per = 0;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, layer_few_kernel<GATED>, kFewThreads, l.total);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)a.n * a.slots * (a.I / 16) + (int64_t)a.parts * (a.H / 16);
+  return launch_ex(layer_few_kernel<GATED>, dim3((unsigned)std::min<int64_t>(items, (int64_t)std::max(per, 1) * sms)),
+                   dim3(kFewThreads), l.total, s, true, a, l);
+}
+
+int32_t part_tiles(int32_t n, int32_t slots, int32_t I, int32_t parts) { return (n * slots * (I / 64) + parts - 1) / parts; }
+
+}  // namespace
+
+// Parts of about 40 tiles where every pair takes an expert of its own.
+int32_t layer_few_parts(int32_t n, int32_t slots, int32_t I) {
+  return std::max(1, std::min((n * slots * (I / 64) + 39) / 40, kFewParts));
+}
+
+bool layer_few_takes(int32_t n, int32_t slots, int32_t H, int32_t I, bool gated) {
+  if (n > kFewTokens || n * slots > kFewPairs) return false;
+  const int32_t parts = layer_few_parts(n, slots, I);
+  return few_layout(n, H, I, gated ? 2 : 1, part_tiles(n, slots, I, parts)).total <= kFewSmem;
+}
+
+cudaError_t launch_layer_few(const LayerFewArgs& a, bool gated, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const FewLayout l = few_layout(a.n, a.H, a.I, gated ? 2 : 1, part_tiles(a.n, a.slots, a.I, a.parts));
+  return gated ? few_launch<true>(a, l, sms, s) : few_launch<false>(a, l, sms, s);
+}
+
+}  // namespace moe

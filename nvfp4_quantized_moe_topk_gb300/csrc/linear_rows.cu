@@ -16,6 +16,7 @@
 #include "block.cuh"
 #include "linear_act.cuh"
 #include "linear_mma.cuh"
+#include "tile.cuh"
 
 namespace moe {
 
@@ -31,13 +32,6 @@ struct RowsPlan {
   LinearFinish e;
 };
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint4 stream16(const uint16_t* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -80,8 +74,8 @@ __global__ void __launch_bounds__(kRowsThreads, TILES <= 2 ? 2 : 1) linear_rows_
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        mma_16816(acc[j], a[i].x, b[i].x, a[i].y, b[i].y, x[i].x, x[i].y);
-        mma_16816(acc[j], a[i].z, b[i].z, a[i].w, b[i].w, x[i].z, x[i].w);
+        mma_bf16_16816(acc[j], a[i].x, b[i].x, a[i].y, b[i].y, x[i].x, x[i].y);
+        mma_bf16_16816(acc[j], a[i].z, b[i].z, a[i].w, b[i].w, x[i].z, x[i].w);
       }
     }
   }

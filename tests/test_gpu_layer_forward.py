@@ -97,30 +97,35 @@ def test_layer(n, kw):
 @pytest.mark.parametrize("kw,n", [(dict(H=2688, I=1856, E=128, k=6), 1), (dict(H=2688, I=1856, E=128, k=6, S=2, gated=True), 32),
                                   (dict(E=3, k=1, S=3), 64), (dict(H=4096, I=64, E=300, k=8, S=1), 17),
                                   (dict(H=64, I=64, E=1000, k=3, S=1), 40), (dict(H=64, I=64, E=1000, k=30, S=2), 33),
+                                  (dict(H=2688, I=1856, E=128, k=6, S=2, gated=True), 1), (dict(H=1024, I=192, E=64, k=6), 8),
+                                  (dict(H=64, I=64, E=1000, k=30, S=2), 8), (dict(H=4096, I=64, E=300, k=8, S=2, gated=True), 5),
                                   (dict(single=-1), 5), (dict(single=8), 9), (dict(E=40, router="fp32"), 130),
                                   (dict(H=64, I=64, E=768, k=12, S=1), 70)])
 def test_sizes(kw, n):
     Layer(**kw).check(n)
 
 
-@pytest.mark.parametrize("n", [1, 7, 100])
+@pytest.mark.parametrize("n", [100, 200])
 def test_without_shared_experts_it_is_the_forward(n):
-    """The same picks through moe_nvfp4_forward onto the same residual: the same bits where no expert is cut into parts (up
-    to 8 tokens, and where one launch does not take the batch)."""
+    """The same picks through moe_nvfp4_forward onto the same residual: the same bits where one launch does not take the
+    batch (a smaller one sums in another order)."""
     layer = Layer(S=0)
     x, res = layer.randn(n, 256).to(torch.bfloat16), layer.randn(n, 256).to(torch.bfloat16)
     dst, ids, weights, _ = layer.call(x, res)
     want = res.clone()
     layer.layer.forward(x, ids, weights, want)
     assert torch.equal(dst, want)
-    # in place, onto x, and without a residual
+
+
+@pytest.mark.parametrize("n", [1, 7, 20, 100])
+def test_residuals(n):
+    """In place, x itself, and none: as with buffers of their own."""
+    layer = Layer(S=1)
+    x, res = layer.randn(n, 256).to(torch.bfloat16), layer.randn(n, 256).to(torch.bfloat16)
+    want = layer.call(x, res)[0]
     assert torch.equal(layer.call(x, dst=res, residual=res)[0], want)
-    onto = x.clone()
-    layer.layer.forward(x, ids, weights, onto)
-    assert torch.equal(layer.call(x, x)[0], onto)
-    zero = torch.zeros_like(x)
-    layer.layer.forward(x, ids, weights, zero)
-    assert torch.equal(layer.call(x)[0], zero)
+    assert torch.equal(layer.call(x, x)[0], layer.call(x, x.clone())[0])
+    assert torch.equal(layer.call(x)[0], layer.call(x, torch.zeros_like(x))[0])
 
 
 @pytest.mark.parametrize("n", [3, 30, 80])
