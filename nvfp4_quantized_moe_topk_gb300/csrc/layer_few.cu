@@ -5,9 +5,12 @@
 // x 1856: 39 MB), and whatever keeps those reads from being in flight.  Work comes
 // in items of 16 rows, whose weights are one run of memory that a bulk copy brings
 // to one of a block's three slots while the block works on another.  Eight warps
-// multiply, each an eighth of the item's columns; a ninth draws the items, asks
-// for their weights and brings a down item's rows, a tenth finishes the sums, so
-// that the eight wait for none of that.
+// multiply, each an eighth of the item's columns; a ninth draws the items and asks
+// for their weights and a down item's rows, and one more a slot finishes its sums,
+// which the others would spend most of their time waiting for.  The whole call for
+// one token: 43 us with the eight doing all, 35 with a drawing and a finishing
+// warp, 31.5 with one a slot and the rows by bulk copies (by the drawing warp's own
+// loads, a down item every 3 us though multiplying it takes 1.5: 35).
 // First come the up product's items (an expert's 16 rows; gated: its gate and up
 // tiles), then the down product's (16 columns of the output over a part of the
 // experts' rows, so that there are a few items an SM).
@@ -30,8 +33,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kFewWarps = 8, kFewMath = 32 * kFewWarps, kFewThreads = kFewMath + 64;
-constexpr int kFewSlots = 3;
+constexpr int kFewWarps = 8, kFewMath = 32 * kFewWarps, kFewSlots = 3;
+constexpr int kFewThreads = kFewMath + 32 + 32 * kFewSlots;
 
 // Shared memory after the slots of weights: x [n][H], slots of rows [n][part's tiles x 64], rows padded by 16 bytes.
 struct FewLayout {
@@ -59,7 +62,9 @@ struct FewWork {
   int16_t pair[kFewPairs][kDecPassTok];
   float weight[kFewPairs][kDecPassTok];
   float up_g[kFewPairs], dn_g[kFewPairs], gate_g[kFewPairs];  // times 2^8: the tiles carry 2^-8
+  int32_t tokens[kFewPairs];  // that take the expert
   int32_t experts;
+  float up_part, columns_part, tiles_part;  // reciprocals of I / 16, H / 16 and I / 64
 };
 // Named barriers, one of each for a slot: the next item from the drawing warp, its sums' place free from the finishing
 // one; the sums to the finishing warp; the slot back to the drawing one.
@@ -68,7 +73,8 @@ __device__ __forceinline__ void bar_arrive(int id, int count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 constexpr int kBarItem = 1, kBarSums = kBarItem + kFewSlots, kBarFree = kBarSums + kFewSlots, kBarMath = kBarFree + kFewSlots;
-static_assert(kBarMath < 16, "named barriers");
+static_assert(kBarMath + 1 < 16, "named barriers");
+constexpr int kBarItemCount = kFewMath + 64;  // the multiplying, the drawing and the slot's finishing warps
 __device__ __forceinline__ void red_release(int32_t* p) {
   asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
 }
@@ -106,30 +112,56 @@ __device__ __forceinline__ FewX load_x(const uint8_t* row, int32_t tile, bool li
   return x;
 }
 
+// x / d of whole numbers below 2^20, r = 1 / d: exact, and shorter than a division for a warp that everyone waits for.
+__device__ __forceinline__ int32_t quotient(int32_t x, float r) { return (int32_t)(((float)x + 0.5f) * r); }
+
 // A part's tiles: [first, last) of all experts' (expert by expert).
 __device__ __forceinline__ int32_t part_begin(const LayerFewArgs& a, int32_t tiles, int32_t part) {
-  return (int32_t)((int64_t)tiles * part / a.parts);
+  return (int32_t)((uint32_t)tiles * (uint32_t)part / (uint32_t)a.parts);  // (tiles < 2^13, parts < 2^6)
 }
 
-// One thread: asks for an item's weights.
+// One thread: asks for an item's weights, and announces a down item's rows with them.
 template <bool GATED>
 __device__ __forceinline__ void issue(const LayerFewArgs& a, const FewWork& p, int32_t item, int32_t up, uint8_t* slot,
                                       uint64_t* bar) {
   fence_proxy_async_smem();
   if (item < up) {
-    const int32_t KT = (GATED ? 2 : 1) * (a.H / 64), NT = a.I / 16;
+    const int32_t KT = (GATED ? 2 : 1) * (a.H / 64), NT = a.I / 16, ai = quotient(item, p.up_part);
     const uint32_t bytes = (uint32_t)KT * kTileBytes;
     mbar_arrive_expect_tx(bar, bytes);
-    bulk_g2s(slot, a.up_tiles + ((int64_t)p.expert[item / NT] * NT + item % NT) * bytes, bytes, bar);
+    bulk_g2s(slot, a.up_tiles + ((int64_t)p.expert[ai] * NT + (item - ai * NT)) * bytes, bytes, bar);
     return;
   }
-  const int32_t KT = a.I / 64, NT = a.H / 16, ct = (item - up) % NT, part = (item - up) / NT, all = p.experts * KT;
-  const int32_t p0 = part_begin(a, all, part), p1 = part_begin(a, all, part + 1);
-  mbar_arrive_expect_tx(bar, (uint32_t)(p1 - p0) * kTileBytes);
-  for (int32_t i = p0; i < p1;) {
-    const int32_t ai = i / KT, kt = i - ai * KT, run = min(KT - kt, p1 - i);
-    bulk_g2s(slot + (i - p0) * kTileBytes, a.dn_tiles + (((int64_t)p.expert[ai] * NT + ct) * KT + kt) * kTileBytes,
+  const int32_t KT = a.I / 64, NT = a.H / 16, part = quotient(item - up, p.columns_part), ct = item - up - part * NT;
+  const int32_t all = p.experts * KT, p0 = part_begin(a, all, part), p1 = part_begin(a, all, part + 1);
+  uint32_t bytes = (uint32_t)(p1 - p0) * kTileBytes;
+  for (int32_t i = p0, ai = quotient(p0, p.tiles_part); i < p1; ++ai) {
+    const int32_t run = min((ai + 1) * KT, p1) - i;
+    bytes += (uint32_t)run * 128u * p.tokens[ai];
+    i += run;
+  }
+  mbar_arrive_expect_tx(bar, bytes);
+  for (int32_t i = p0, ai = quotient(p0, p.tiles_part); i < p1; ++ai) {
+    const int32_t run = min((ai + 1) * KT, p1) - i;
+    bulk_g2s(slot + (i - p0) * kTileBytes, a.dn_tiles + (((int64_t)p.expert[ai] * NT + ct) * KT + (i - ai * KT)) * kTileBytes,
              (uint32_t)run * kTileBytes, bar);
+    i += run;
+  }
+}
+// The rows that a down item multiplies (they are there).
+__device__ __forceinline__ void issue_rows(const LayerFewArgs& a, const FewWork& p, int32_t item, int32_t up, uint8_t* as,
+                                           uint32_t a_row, uint64_t* bar) {
+  // (written by ordinary stores, read by a bulk copy)
+  asm volatile("fence.proxy.async;" ::: "memory");
+  const int32_t KT = a.I / 64, part = quotient(item - up, p.columns_part);
+  const int32_t all = p.experts * KT, p0 = part_begin(a, all, part), p1 = part_begin(a, all, part + 1);
+  for (int32_t i = p0, ai = quotient(p0, p.tiles_part); i < p1; ++ai) {
+    const int32_t run = min((ai + 1) * KT, p1) - i;
+    for (int32_t col = 0; col < a.n; ++col) {
+      const int32_t pair = p.pair[ai][col];
+      if (pair >= 0)
+        bulk_g2s(as + col * a_row + (i - p0) * 128, a.Ap + (int64_t)pair * a.I + 64 * (i - ai * KT), (uint32_t)run * 128u, bar);
+    }
     i += run;
   }
 }
@@ -180,44 +212,19 @@ __device__ __forceinline__ void up_finish(const LayerFewArgs& a, const FewWork& 
   if (lane == 0) red_release(&a.plan->done[ai]);
 }
 
-// By the drawing warp: the rows of a down item's experts, once they are there.
-__device__ __forceinline__ void down_rows(const LayerFewArgs& a, const FewWork& p, int32_t part, uint8_t* as, uint32_t a_row) {
-  const int lane = threadIdx.x & 31;
-  const int32_t KT = a.I / 64, all = p.experts * KT;
-  const int32_t p0 = part_begin(a, all, part), p1 = part_begin(a, all, part + 1);
-  for (int32_t i = p0; i < p1;) {  // expert by expert
-    const int32_t ai = i / KT, kt = i - ai * KT, run = min(KT - kt, p1 - i);
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer_ns();
-      while (ld_acquire(&a.plan->done[ai]) < a.I / 16) {
-        __nanosleep(40);
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-          atomicOr(a.err, kFlagTimeout);
-          break;
-        }
+// By the drawing warp, once: every expert's rows are there.
+__device__ __forceinline__ void wait_rows(const LayerFewArgs& a, int32_t experts) {
+  const uint64_t t0 = globaltimer_ns();
+  for (int32_t ai = threadIdx.x & 31; ai < experts; ai += 32)
+    while (ld_acquire(&a.plan->done[ai]) < a.I / 16) {
+      __nanosleep(40);
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        atomicOr(a.err, kFlagTimeout);
+        break;
       }
     }
-    __syncwarp();
-    for (int32_t col = 0; col < a.n; ++col) {
-      const int32_t pair = p.pair[ai][col];
-      uint8_t* to = as + col * a_row + (i - p0) * 128;
-      const uint16_t* from = a.Ap + (int64_t)pair * a.I + 64 * kt;
-      for (int32_t k0 = lane; k0 < 8 * run; k0 += 8 * 32) {
-        uint4 v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          v[q] = make_uint4(0, 0, 0, 0);
-          if (pair >= 0 && k0 + 32 * q < 8 * run) v[q] = ld_cg_v4(from + 8 * (k0 + 32 * q));
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (k0 + 32 * q < 8 * run) *reinterpret_cast<uint4*>(to + 16 * (k0 + 32 * q)) = v[q];
-      }
-    }
-    i += run;
-  }
+  __syncwarp();
 }
-
 // The warps' sums of a down item.
 template <bool GATED>
 __device__ __forceinline__ void down_sums(const LayerFewArgs& a, const FewWork& p, int32_t part, const uint8_t* slot,
@@ -229,10 +236,11 @@ __device__ __forceinline__ void down_sums(const LayerFewArgs& a, const FewWork& 
   const uint8_t* row = as + g * a_row + 32 * t;
   float total[4] = {}, acc[4] = {}, acc2[4] = {};
   for (int32_t i = i0; i < i1;) {  // expert by expert
-    const int32_t ai = (p0 + i) / KT, end = min(i1, (ai + 1) * KT - p0);
+    const int32_t ai = quotient(p0 + i, p.tiles_part), end = min(i1, (ai + 1) * KT - p0);
+    const bool mine = g < a.n && p.pair[ai][g] >= 0;
 #pragma unroll 2
     for (; i < end; ++i) {
-      const FewX x = load_x(row, i, g < a.n);
+      const FewX x = load_x(row, i, mine);
       tile_mma(slot + i * kTileBytes, x.x0, x.x1, lane, lut, acc, acc2);
     }
     const float dg = p.dn_g[ai];
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) layer_few_kernel(const __grid_
   __shared__ FewWork work;
   __shared__ __align__(8) uint64_t full[kFewSlots];
   __shared__ int32_t item[kFewSlots], summed[kFewSlots];  // drawn; whose sums lie there
-  __shared__ volatile int32_t finished;  // up items that the block has finished
+  __shared__ int32_t finished;  // up items that the block has finished
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 256; i += kFewThreads) lut[i] = scale_bf16_2p118((uint32_t)i) * 0x10001u;
   if (threadIdx.x == 0) {
@@ -299,35 +307,50 @@ __global__ void __launch_bounds__(kFewThreads, 2) layer_few_kernel(const __grid_
     work.weight[i / kDecPassTok][i % kDecPassTok] = a.plan->weight[i / kDecPassTok][i % kDecPassTok];
   }
   const int32_t experts = a.plan->experts;
-  if (threadIdx.x == 0) work.experts = experts;
+  if (threadIdx.x == 0) {
+    work.experts = experts;
+    work.up_part = 16.f / (float)a.I;
+    work.columns_part = 16.f / (float)a.H;
+    work.tiles_part = 64.f / (float)a.I;
+  }
+  __syncthreads();
+  if (threadIdx.x < experts) {
+    int32_t tokens = 0;
+    for (int32_t col = 0; col < a.n; ++col) tokens += work.pair[threadIdx.x][col] >= 0;
+    work.tokens[threadIdx.x] = tokens;
+  }
   __syncthreads();
   const int32_t NT = a.I / 16, CT = a.H / 16, up = experts * NT, items = up + a.parts * CT;
 
-  if (threadIdx.x >= kFewMath + 32) {  // the finishing warp
-    for (int32_t i = lane; i < experts; i += 32) {
+  if (threadIdx.x >= kFewMath + 32) {  // a slot's finishing warp
+    const int s = (threadIdx.x - kFewMath - 32) / 32;
+    for (int32_t i = lane + 32 * s; i < experts; i += 32 * kFewSlots) {
       work.up_g[i] = 256.f * a.up_g[work.expert[i]];
       work.dn_g[i] = 256.f * a.dn_g[work.expert[i]];
       if (GATED) work.gate_g[i] = 256.f * a.gate_g[work.expert[i]];
     }
-    __syncwarp();
-    for (int s = 0; s < kFewSlots; ++s) bar_arrive(kBarItem + s, kFewThreads);
-    for (int s = 0;; s = s + 1 == kFewSlots ? 0 : s + 1) {
+    bar_sync(kBarMath + 1, 32 * kFewSlots);
+    bar_arrive(kBarItem + s, kBarItemCount);
+    while (true) {
       bar_sync(kBarSums + s, kFewMath + 32);
       const int32_t now = summed[s];  // (item[s] may be the next already)
       if (now >= items) break;
       if (now < up) {
-        up_finish<GATED>(a, work, now / NT, now % NT, sums[s]);
-        if (lane == 0) finished = finished + 1;
+        const int32_t ai = quotient(now, work.up_part);
+        up_finish<GATED>(a, work, ai, now - ai * NT, sums[s]);
+        if (lane == 0) atomicAdd(&finished, 1);
       } else {
-        down_finish<GATED>(a, (now - up) % CT, (now - up) / CT, sums[s]);
+        const int32_t part = quotient(now - up, work.columns_part);
+        down_finish<GATED>(a, now - up - part * CT, part, sums[s]);
       }
       __syncwarp();
-      bar_arrive(kBarItem + s, kFewThreads);
+      bar_arrive(kBarItem + s, kBarItemCount);
     }
     return;
   }
   if (threadIdx.x >= kFewMath) {  // the drawing warp
     int32_t drawn = 0;  // up items
+    bool waited = false;
     // The next item into slot s: its weights asked for, then a down item's rows, for which it waits only when the block
     // has no up item of its own left to finish.
     auto draw = [&](int s) {
@@ -340,12 +363,16 @@ __global__ void __launch_bounds__(kFewThreads, 2) layer_few_kernel(const __grid_
       if (now < up) {
         ++drawn;
       } else if (now < items) {
-        const uint64_t t0 = globaltimer_ns();
-        while (finished < drawn && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(20);
-        down_rows(a, work, (now - up) / CT, sm + l.a_at + s * a.n * l.a_row, l.a_row);
+        if (!waited) {
+          const uint64_t t0 = globaltimer_ns();
+          while (*(volatile int32_t*)&finished < drawn && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(20);
+          wait_rows(a, experts);
+          waited = true;
+        }
+        if (lane == 0) issue_rows(a, work, now, up, sm + l.a_at + s * a.n * l.a_row, l.a_row, &full[s]);
       }
       __syncwarp();
-      bar_arrive(kBarItem + s, kFewThreads);
+      bar_arrive(kBarItem + s, kBarItemCount);
       return now;
     };
     int32_t held[kFewSlots];
@@ -373,19 +400,25 @@ __global__ void __launch_bounds__(kFewThreads, 2) layer_few_kernel(const __grid_
   bar_sync(kBarMath, kFewMath);
   uint32_t parity = 0;
   for (int s = 0;;) {
-    bar_sync(kBarItem + s, kFewThreads);
+    bar_sync(kBarItem + s, kBarItemCount);
     const int32_t now = item[s];
-    if (threadIdx.x == 0) summed[s] = now;
     if (now >= items) {
-      bar_arrive(kBarSums + s, kFewMath + 32);
+      // no further item: each slot's finishing warp, this one's first, learns it when it is through with its last
+      for (int k = 0; k < kFewSlots; ++k) {
+        if (k > 0) bar_sync(kBarItem + s, kBarItemCount);
+        if (threadIdx.x == 0) summed[s] = items;
+        bar_arrive(kBarSums + s, kFewMath + 32);
+        s = s + 1 == kFewSlots ? 0 : s + 1;
+      }
       break;
     }
+    if (threadIdx.x == 0) summed[s] = now;
     mbar_wait(&full[s], parity, a.err);
     const uint8_t* slot = sm + s * l.slot;
     if (now < up)
-      up_sums<GATED>(a, work, now / NT, slot, sm + l.x_at, l.x_row, lut, sums[s]);
+      up_sums<GATED>(a, work, quotient(now, work.up_part), slot, sm + l.x_at, l.x_row, lut, sums[s]);
     else
-      down_sums<GATED>(a, work, (now - up) / CT, slot, sm + l.a_at + s * a.n * l.a_row, l.a_row, lut, sums[s]);
+      down_sums<GATED>(a, work, quotient(now - up, work.columns_part), slot, sm + l.a_at + s * a.n * l.a_row, l.a_row, lut, sums[s]);
     bar_arrive(kBarSums + s, kFewMath + 32);
     bar_arrive(kBarFree + s, kFewMath + 32);
     if (++s == kFewSlots) {
@@ -419,6 +452,7 @@ int32_t layer_few_parts(int32_t n, int32_t slots, int32_t I) {
 bool layer_few_takes(int32_t n, int32_t slots, int32_t H, int32_t I, bool gated) {
   if (n > kFewTokens || n * slots > kFewPairs) return false;
   const int32_t parts = layer_few_parts(n, slots, I);
+  if ((int64_t)n * slots * (I / 16) + (int64_t)parts * (H / 16) >= 1 << 20) return false;  // quotient's range
   return few_layout(n, H, I, gated ? 2 : 1, part_tiles(n, slots, I, parts)).total <= kFewSmem;
 }
 
