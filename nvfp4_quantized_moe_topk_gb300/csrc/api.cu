@@ -600,7 +600,7 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
   r.x = a.x;
   r.weight = a.router_weight;
   r.bias = a.router_bias;
-  r.logits = a.logits ? a.logits : n <= kLayerFusedTokens ? h->logits : h->Yp;
+  r.logits = r.logits_out = a.logits ? a.logits : n <= kLayerFusedTokens ? h->logits : h->Yp;
   r.ids = h->ids_stage;
   r.w = h->w_stage;
   r.ids_out = a.topk_ids;
@@ -626,7 +626,7 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
       l.out_dtype = MOE_DTYPE_F32;
       l.weight = static_cast<const uint16_t*>(a.router_weight);
       l.x.data = const_cast<uint16_t*>(a.x);
-      l.out.data = r.logits;
+      l.out.data = r.logits_out;
       e = launch_linear(l, s);
     }
     if (e == cudaSuccess) e = launch_layer_router(r, product, s);
@@ -647,6 +647,7 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
     f.col_done = h->col_done;
     f.plan = h->few;
     f.err = h->err;
+    f.pick = r;
     f.n = n;
     f.H = H;
     f.I = c.inter;

@@ -237,13 +237,18 @@ cudaError_t launch_decode(const DecodeArgs& args, int num_sms, cudaStream_t s);
 constexpr int kFewTokens = 8, kFewPairs = 96;  // and pairs (tokens times picks and shared experts), at most
 constexpr int kFewParts = 48;                   // parts of the down product's experts, at most
 constexpr int kFewSmem = 190 * 1024;  // (beside 35 KB of static shared memory)
-struct LayerFewPlan {                           // written by the router
-  int32_t experts;              // that any token takes
-  int32_t ticket;               // work items handed out
-  int32_t expert[kFewPairs];
-  int32_t done[kFewPairs];      // row tiles of the expert's up product that are finished
-  int32_t pair[kFewPairs][kDecPassTok];  // the token's pair with the expert, or -1
-  float weight[kFewPairs][kDecPassTok];
+struct LayerFewPlan {  // zeroed by the router
+  int32_t ticket;           // work items handed out
+  int32_t done[kFewPairs];  // row tiles of an expert's up product that are finished
+};
+// What a token's picks are made from, and where the caller wants them.
+struct LayerPick {
+  const float* logits;  // [n][E]
+  const float* bias;    // [E] or nullptr
+  int32_t* ids_out;     // [n][k] or nullptr
+  float* w_out;         // [n][k] or nullptr
+  int32_t* part_of;     // [kLayerMaxParts]: each further part's expert; nullptr: experts are not cut
+  int32_t n, E, k, shared;
 };
 struct LayerFewArgs {
   const uint8_t *up_tiles, *dn_tiles;  // as DecodeArgs
@@ -255,24 +260,21 @@ struct LayerFewArgs {
   int32_t* col_done;                   // [H/16], zero between launches
   LayerFewPlan* plan;
   int32_t* err;
+  LayerPick pick;
   int32_t n, H, I, slots, parts;
 };
 int32_t layer_few_parts(int32_t n, int32_t slots, int32_t I);
 bool layer_few_takes(int32_t n, int32_t slots, int32_t H, int32_t I, bool gated);
 cudaError_t launch_layer_few(const LayerFewArgs& a, bool gated, cudaStream_t s);
-struct LayerRouterArgs {
+struct LayerRouterArgs : LayerPick {
   const uint16_t* x;    // [n][H] bf16
   const void* weight;   // [E][H] bf16 or fp32
-  const float* bias;    // [E] or nullptr
-  float* logits;        // [n][E]
+  float* logits_out;    // the same as logits
   int32_t* ids;         // [n][k + shared]: the picks, then the shared experts (E on), or their parts (E + shared on)
   float* w;             // [n][k + shared]: the picks' weights, then ones
-  int32_t *ids_out;     // [n][k] or nullptr
-  float* w_out;         // [n][k] or nullptr
   int32_t* count;       // blocks that have finished; zero between launches
-  int32_t* part_of;     // [kLayerMaxParts]: each further part's expert; nullptr: experts are not cut
-  LayerFewPlan* few;    // the work of launch_layer_few (no ids and w then); or nullptr
-  int32_t n, H, E, k, shared;
+  LayerFewPlan* few;    // launch_layer_few follows, which makes the picks (no ids and w then); or nullptr
+  int32_t H;
   int32_t weight_f32;
 };
 // Further parts that n tokens may need.

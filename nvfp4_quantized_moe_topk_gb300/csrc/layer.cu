@@ -5,11 +5,11 @@
 // warps two or three steps of 32 columns, whose loads are all in flight at once;
 // warp-level matrix instructions take 16 experts by 8 tokens, and the warps' sums
 // meet in shared memory, in order.  An fp32 weight goes in as three bf16 terms,
-// which keep its 24 bits, as products with bf16 x are exact.  The block that
+// which keep its 24 bits, as products with bf16 x are exact.  Of up to 8 tokens the
+// kernel that follows picks the experts itself (layer_few.cu).  Otherwise the block that
 // finishes last routes the tokens, a warp a token, from the logits that the others
-// left in L2, adds the shared experts to the picks, and lays out the work for the
-// kernel that follows: up to 8 tokens as the experts that any of them takes
-// (layer_few.cu), more with experts of more than 8 tokens cut into parts, which
+// left in L2, adds the shared experts to the picks, and cuts experts of more than 8
+// tokens into parts, as one such expert
 // would keep the streaming kernel (decode.cu) from staging and have its warps pass
 // over their tiles again and again (a decode batch of 32, gated, two shared
 // experts, an expert of 10 tokens: 461 us with the shared ones cut alone, 200 so).
@@ -17,7 +17,7 @@
 
 #include "block.cuh"
 #include "kernels.h"
-#include "router.cuh"
+#include "layer_pick.cuh"
 #include "tile.cuh"
 
 namespace moe {
@@ -25,42 +25,6 @@ namespace moe {
 namespace {
 
 constexpr int kLayerThreads = 1024, kLayerWarps = kLayerThreads / 32, kLayerExperts = 16;
-
-// One token's picks: k of the logits, then the shared experts.
-// (ids, w: the token's.)
-template <int SLOTS>
-__device__ __forceinline__ void pick_token(const LayerRouterArgs& a, int32_t t, int lane, int32_t* ids, float* w) {
-  float z[SLOTS];
-#pragma unroll
-  for (int i = 0; i < SLOTS; ++i) {
-    const int32_t e = lane + 32 * i;
-    z[i] = 0.f;
-    if (e < a.E) z[i] = __ldcg(a.logits + (int64_t)t * a.E + e) + (a.bias ? __ldg(a.bias + e) : 0.f);
-  }
-  route_token<SLOTS>(z, a.E, a.k, lane, ids, w, nullptr);
-  __syncwarp();
-  if (lane < a.k) {
-    if (a.ids_out) a.ids_out[(int64_t)t * a.k + lane] = ids[lane];
-    if (a.w_out) a.w_out[(int64_t)t * a.k + lane] = w[lane];
-  }
-  if (lane < a.shared) {
-    const int32_t part = a.part_of ? t / kDecPassTok : 0, more = (a.n + kDecPassTok - 1) / kDecPassTok - 1;
-    ids[a.k + lane] = part == 0 ? a.E + lane : a.E + a.shared + lane * more + part - 1;
-    w[a.k + lane] = 1.f;
-  }
-}
-__device__ __noinline__ void pick_any(const LayerRouterArgs& a, int32_t t, int lane, int32_t* ids, float* w) {
-  if (a.E <= 64)
-    pick_token<2>(a, t, lane, ids, w);
-  else if (a.E <= 128)
-    pick_token<4>(a, t, lane, ids, w);
-  else if (a.E <= 256)
-    pick_token<8>(a, t, lane, ids, w);
-  else if (a.E <= 512)
-    pick_token<16>(a, t, lane, ids, w);
-  else
-    pick_token<32>(a, t, lane, ids, w);
-}
 
 // After the picks, by one block: an expert's tokens beyond each 8 move to a further part of it.  Parts are dealt in the
 // order of shared experts, then experts, and tokens in their order, so that the layer's bits do not depend on timing.
@@ -105,42 +69,6 @@ __device__ void deal_parts(const LayerRouterArgs& a, PartSpace& sp) {
   }
 }
 
-// After the picks of a few tokens, by one block: the experts that any of them takes, in the order of their first pair,
-// and each token's pair of them.  (The plan's pairs and counts have been cleared.)
-struct FewSpace {
-  int32_t id[kFewPairs];
-  float w[kFewPairs];
-  int32_t at[1024], count[kLayerWarps];
-};
-__device__ void list_experts(const LayerRouterArgs& a, FewSpace& sp) {
-  const int32_t slots = a.k + a.shared, pairs = a.n * slots, p = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  LayerFewPlan& f = *a.few;
-  const int32_t e = p < pairs ? sp.id[p] : -1;
-  bool first = e >= 0;
-  for (int32_t q = 0; first && q < p; ++q) first = sp.id[q] != e;
-  const uint32_t who = __ballot_sync(0xffffffffu, first);
-  if (lane == 0) sp.count[warp] = __popc(who);
-  __syncthreads();
-  int32_t at = __popc(who & ((1u << lane) - 1)), all = 0;
-  for (int32_t w = 0; w < (kFewPairs + 31) / 32; ++w) {
-    if (w < warp) at += sp.count[w];
-    all += sp.count[w];
-  }
-  if (first) {
-    f.expert[at] = e;
-    sp.at[e] = at;
-  }
-  if (threadIdx.x == 0) {
-    f.experts = all;
-    f.ticket = 0;
-  }
-  __syncthreads();
-  if (p < pairs) {
-    f.pair[sp.at[e]][p / slots] = p;
-    f.weight[sp.at[e]][p / slots] = sp.w[p];
-  }
-}
-
 // Eight consecutive values of a weight row as bf16 terms whose sum they are.
 template <typename T>
 struct RouterTerms {
@@ -173,7 +101,7 @@ template <typename T, int TILES>
 __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __grid_constant__ LayerRouterArgs a, int32_t pick) {
   extern __shared__ __align__(16) float dyn[];  // [warps][8 TILES][17], then the last block's work
   __shared__ int32_t last;
-  constexpr int kGroup = 8 * TILES, kAhead = TILES == 1 && sizeof(T) == 2 ? 4 : 1;
+  constexpr int kGroup = 8 * TILES, kAhead = TILES == 1 && sizeof(T) == 2 ? 3 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int32_t e0 = blockIdx.x * kLayerExperts, steps = (a.H + 31) / 32;
   const int32_t s0 = steps * warp / kLayerWarps, s1 = steps * (warp + 1) / kLayerWarps;
@@ -181,9 +109,8 @@ __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __gri
   const T* rb = static_cast<const T*>(a.weight) + (int64_t)min(e0 + g + 8, a.E - 1) * a.H + 8 * t;
   pdl_wait();
   pdl_launch_dependents();
-  if (a.few && blockIdx.x == 0) {  // (the last block writes the pairs, after this one has finished or is it)
-    for (int32_t i = threadIdx.x; i < kFewPairs * kDecPassTok; i += kLayerThreads)
-      a.few->pair[i / kDecPassTok][i % kDecPassTok] = -1;
+  if (a.few && blockIdx.x == 0) {
+    if (threadIdx.x == 0) a.few->ticket = 0;
     if (threadIdx.x < kFewPairs) a.few->done[threadIdx.x] = 0;
   }
   const int32_t end = min(a.n, ((int32_t)blockIdx.y + 1) * kLayerFusedTokens);
@@ -238,7 +165,7 @@ __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __gri
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kLayerWarps; ++w) v += sums[w][i / kLayerExperts][i % kLayerExperts];
-      a.logits[(int64_t)(t0 + i / kLayerExperts) * a.E + e] = v;
+      a.logits_out[(int64_t)(t0 + i / kLayerExperts) * a.E + e] = v;
     }
     __syncthreads();
   }
@@ -253,19 +180,15 @@ __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __gri
   __syncthreads();
   if (!last) return;
   const int32_t slots = a.k + a.shared;
-  FewSpace& few = *reinterpret_cast<FewSpace*>(dyn);
   for (int32_t k = warp; k < a.n; k += kLayerWarps)
-    pick_any(a, k, lane, a.few ? few.id + k * slots : a.ids + (int64_t)k * slots, a.few ? few.w + k * slots : a.w + (int64_t)k * slots);
+    pick_any(a, k, lane, a.ids + (int64_t)k * slots, a.w + (int64_t)k * slots, true);
   __syncthreads();
-  if (a.few)
-    list_experts(a, few);
-  else if (a.part_of && a.n > kDecPassTok)
-    deal_parts(a, *reinterpret_cast<PartSpace*>(dyn));
+  if (a.part_of && a.n > kDecPassTok) deal_parts(a, *reinterpret_cast<PartSpace*>(dyn));
 }
 
 __global__ void __launch_bounds__(256) layer_pick_kernel(const LayerRouterArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t < a.n) pick_any(a, (int32_t)t, threadIdx.x & 31, a.ids + t * (a.k + a.shared), a.w + t * (a.k + a.shared));
+  if (t < a.n) pick_any(a, (int32_t)t, threadIdx.x & 31, a.ids + t * (a.k + a.shared), a.w + t * (a.k + a.shared), true);
 }
 
 }  // namespace
@@ -275,7 +198,7 @@ namespace {
 template <typename T, int TILES>
 cudaError_t router_launch(const LayerRouterArgs& a, bool pick, cudaStream_t s) {
   static std::atomic<bool> configured[kMaxDevices];
-  constexpr size_t smem = std::max({(size_t)kLayerWarps * 8 * TILES * 17 * sizeof(float), sizeof(PartSpace), sizeof(FewSpace)});
+  constexpr size_t smem = std::max({(size_t)kLayerWarps * 8 * TILES * 17 * sizeof(float), sizeof(PartSpace)});
   const cudaError_t e = raise_smem_limit(layer_router_kernel<T, TILES>, (int)smem, configured);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((a.E + kLayerExperts - 1) / kLayerExperts),
@@ -287,10 +210,10 @@ cudaError_t router_launch(const LayerRouterArgs& a, bool pick, cudaStream_t s) {
 
 cudaError_t launch_layer_router(const LayerRouterArgs& a, bool have_logits, cudaStream_t s) {
   if (!have_logits) {
-    const bool pick = a.n <= kLayerFusedTokens;
+    const bool pick = a.n <= kLayerFusedTokens && !a.few;
     const cudaError_t e = a.n <= 8 ? (a.weight_f32 ? router_launch<float, 1>(a, pick, s) : router_launch<uint16_t, 1>(a, pick, s))
                                    : (a.weight_f32 ? router_launch<float, 4>(a, pick, s) : router_launch<uint16_t, 4>(a, pick, s));
-    if (e != cudaSuccess || pick) return e;
+    if (e != cudaSuccess || pick || a.few) return e;
   }
   layer_pick_kernel<<<(unsigned)((a.n + 7) / 8), 256, 0, s>>>(a);
   return cudaGetLastError();

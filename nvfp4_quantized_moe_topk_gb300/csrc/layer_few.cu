@@ -26,7 +26,7 @@
 // expert's product, its activations zero where it does not take the expert.
 #include <algorithm>
 
-#include "kernels.h"
+#include "layer_pick.cuh"
 #include "tile.cuh"
 
 namespace moe {
@@ -56,15 +56,20 @@ template <bool GATED>
 struct FewSums {  // gated: the gate's, then the up's
   float v[GATED ? 2 : 1][kFewWarps][16][kDecPassTok + 1];
 };
-// The router's plan, brought to shared memory once.
+// The experts that any token takes, in the order of their first pair, and each token's pair with them.
 struct FewWork {
   int32_t expert[kFewPairs];
-  int16_t pair[kFewPairs][kDecPassTok];
+  int16_t pair[kFewPairs][kDecPassTok];  // or -1
   float weight[kFewPairs][kDecPassTok];
   float up_g[kFewPairs], dn_g[kFewPairs], gate_g[kFewPairs];  // times 2^8: the tiles carry 2^-8
   int32_t tokens[kFewPairs];  // that take the expert
   int32_t experts;
   float up_part, columns_part, tiles_part;  // reciprocals of I / 16, H / 16 and I / 64
+};
+struct FewPicks {
+  int32_t id[kFewPairs], first[1024];
+  float w[kFewPairs];
+  int32_t at[1024], count[(kFewPairs + 31) / 32];
 };
 // Named barriers, one of each for a slot: the next item from the drawing warp, its sums' place free from the finishing
 // one; the sums to the finishing warp; the slot back to the drawing one.
@@ -72,8 +77,8 @@ __device__ __forceinline__ void bar_sync(int id, int count) { asm volatile("bar.
 __device__ __forceinline__ void bar_arrive(int id, int count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
-constexpr int kBarItem = 1, kBarSums = kBarItem + kFewSlots, kBarFree = kBarSums + kFewSlots, kBarMath = kBarFree + kFewSlots;
-static_assert(kBarMath + 1 < 16, "named barriers");
+constexpr int kBarItem = 1, kBarSums = kBarItem + kFewSlots, kBarFree = kBarSums + kFewSlots;
+static_assert(kBarFree + kFewSlots <= 16, "named barriers");
 constexpr int kBarItemCount = kFewMath + 64;  // the multiplying, the drawing and the slot's finishing warps
 __device__ __forceinline__ void red_release(int32_t* p) {
   asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
@@ -83,6 +88,45 @@ __device__ __forceinline__ int32_t ld_acquire(const int32_t* p) {
   int32_t v;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
+}
+// Every block's own: the tokens' picks from the logits, a warp a token, and the experts among them (one token, 128
+// experts: 2 us; by the router's last block, for all, it took as long, and 3 more until they all had it).
+template <bool GATED>
+__device__ __forceinline__ void pick_work(const LayerFewArgs& a, FewWork& work, FewPicks& picks) {
+  const int32_t pairs = a.n * a.slots, p = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kFewThreads / 32 >= kFewTokens && kFewThreads >= kFewPairs, "a warp a token, a thread a pair");
+  if (warp < a.n)
+    pick_any(a.pick, warp, lane, picks.id + warp * a.slots, picks.w + warp * a.slots, blockIdx.x == 0);
+  __syncthreads();
+  const int32_t e = p < pairs ? picks.id[p] : 0;
+  if (p < pairs) picks.first[e] = pairs;
+  __syncthreads();
+  if (p < pairs) atomicMin(&picks.first[e], p);
+  __syncthreads();
+  const bool first = p < pairs && picks.first[e] == p;
+  const uint32_t who = __ballot_sync(0xffffffffu, first);
+  if (lane == 0 && warp < (kFewPairs + 31) / 32) picks.count[warp] = __popc(who);
+  __syncthreads();
+  int32_t at = __popc(who & ((1u << lane) - 1)), all = 0;
+  for (int32_t w = 0; w < (kFewPairs + 31) / 32; ++w) {
+    if (w < warp) at += picks.count[w];
+    all += picks.count[w];
+  }
+  if (first) {
+    work.expert[at] = e;
+    picks.at[e] = at;
+    work.up_g[at] = 256.f * a.up_g[e];
+    work.dn_g[at] = 256.f * a.dn_g[e];
+    if (GATED) work.gate_g[at] = 256.f * a.gate_g[e];
+  }
+  if (p == 0) work.experts = all;
+  __syncthreads();
+  if (p < pairs) {
+    work.pair[picks.at[e]][p / a.slots] = (int16_t)p;
+    work.weight[picks.at[e]][p / a.slots] = picks.w[p];
+    atomicAdd(&work.tokens[picks.at[e]], 1);
+  }
+  __syncthreads();
 }
 template <bool GATED>
 __device__ __forceinline__ void keep(FewSums<GATED>& sums, int which, int warp, int lane, const float (&acc)[4]) {
@@ -295,41 +339,31 @@ __global__ void __launch_bounds__(kFewThreads, 2) layer_few_kernel(const __grid_
     finished = 0;
     fence_mbar_init();
   }
+  for (int i = threadIdx.x; i < kFewPairs * kDecPassTok; i += kFewThreads) work.pair[i / kDecPassTok][i % kDecPassTok] = -1;
+  for (int i = threadIdx.x; i < kFewPairs; i += kFewThreads) work.tokens[i] = 0;
+  if (threadIdx.x == 0) {
+    work.up_part = 16.f / (float)a.I;
+    work.columns_part = 16.f / (float)a.H;
+    work.tiles_part = 64.f / (float)a.I;
+  }
+  // x is there: the router, which lets this kernel begin, does so when all before it has finished
+  for (int32_t i = threadIdx.x; i < a.n * (a.H / 8); i += kFewThreads) {
+    const int32_t col = i / (a.H / 8), at = i - col * (a.H / 8);
+    *reinterpret_cast<uint4*>(sm + l.x_at + col * l.x_row + 16 * at) =
+        __ldcg(reinterpret_cast<const uint4*>(a.x + (int64_t)col * a.H) + at);
+  }
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   int32_t ticket = 0;
   if (threadIdx.x == kFewMath) ticket = atomicAdd(&a.plan->ticket, 1);
-  const int32_t most = a.n * a.slots;  // experts, at most (the rest of the plan is not looked at)
-  for (int32_t i = threadIdx.x; i < most; i += kFewThreads) work.expert[i] = a.plan->expert[i];
-  for (int32_t i = threadIdx.x; i < most * kDecPassTok; i += kFewThreads) {
-    work.pair[i / kDecPassTok][i % kDecPassTok] = (int16_t)a.plan->pair[i / kDecPassTok][i % kDecPassTok];
-    work.weight[i / kDecPassTok][i % kDecPassTok] = a.plan->weight[i / kDecPassTok][i % kDecPassTok];
-  }
-  const int32_t experts = a.plan->experts;
-  if (threadIdx.x == 0) {
-    work.experts = experts;
-    work.up_part = 16.f / (float)a.I;
-    work.columns_part = 16.f / (float)a.H;
-    work.tiles_part = 64.f / (float)a.I;
-  }
-  __syncthreads();
-  if (threadIdx.x < experts) {
-    int32_t tokens = 0;
-    for (int32_t col = 0; col < a.n; ++col) tokens += work.pair[threadIdx.x][col] >= 0;
-    work.tokens[threadIdx.x] = tokens;
-  }
-  __syncthreads();
+  static_assert(sizeof(FewPicks) <= sizeof(sums), "the picks lie where the sums will");
+  pick_work<GATED>(a, work, *reinterpret_cast<FewPicks*>(sums));
+  const int32_t experts = work.experts;
   const int32_t NT = a.I / 16, CT = a.H / 16, up = experts * NT, items = up + a.parts * CT;
 
   if (threadIdx.x >= kFewMath + 32) {  // a slot's finishing warp
     const int s = (threadIdx.x - kFewMath - 32) / 32;
-    for (int32_t i = lane + 32 * s; i < experts; i += 32 * kFewSlots) {
-      work.up_g[i] = 256.f * a.up_g[work.expert[i]];
-      work.dn_g[i] = 256.f * a.dn_g[work.expert[i]];
-      if (GATED) work.gate_g[i] = 256.f * a.gate_g[work.expert[i]];
-    }
-    bar_sync(kBarMath + 1, 32 * kFewSlots);
     bar_arrive(kBarItem + s, kBarItemCount);
     while (true) {
       bar_sync(kBarSums + s, kFewMath + 32);
@@ -392,12 +426,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) layer_few_kernel(const __grid_
     return;
   }
 
-  for (int32_t i = threadIdx.x; i < a.n * (a.H / 8); i += kFewMath) {
-    const int32_t col = i / (a.H / 8), at = i - col * (a.H / 8);
-    *reinterpret_cast<uint4*>(sm + l.x_at + col * l.x_row + 16 * at) =
-        __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)col * a.H) + at);
-  }
-  bar_sync(kBarMath, kFewMath);
   uint32_t parity = 0;
   for (int s = 0;;) {
     bar_sync(kBarItem + s, kBarItemCount);
