@@ -477,11 +477,16 @@ int32_t layer_few_parts(int32_t n, int32_t slots, int32_t I) {
   return std::max(1, std::min((n * slots * (I / 64) + 39) / 40, kFewParts));
 }
 
+// One token, and a few where two blocks fit an SM.  Against the streaming kernel (decode.cu), whole calls of 6 + 1
+// experts: of 2688 x 1856, one token 28.0 us and 35.5 (gated 37.6 and 38.3), but two tokens, a block an SM, 49.8 and
+// 40.1 (gated 61.7 and 47.1); of 1024 x 512, two blocks, one token 14.1 and 22.4, two 18.2 and 27.7, six 28.5 and 35.7.
 bool layer_few_takes(int32_t n, int32_t slots, int32_t H, int32_t I, bool gated) {
   if (n > kFewTokens || n * slots > kFewPairs) return false;
   const int32_t parts = layer_few_parts(n, slots, I);
   if ((int64_t)n * slots * (I / 16) + (int64_t)parts * (H / 16) >= 1 << 20) return false;  // quotient's range
-  return few_layout(n, H, I, gated ? 2 : 1, part_tiles(n, slots, I, parts)).total <= kFewSmem;
+  const size_t total = few_layout(n, H, I, gated ? 2 : 1, part_tiles(n, slots, I, parts)).total;
+  const size_t fixed = sizeof(FewWork) + kFewSlots * (gated ? sizeof(FewSums<true>) : sizeof(FewSums<false>)) + 2048;
+  return total <= kFewSmem && (n == 1 || 2 * (total + fixed) <= 227 * 1024);
 }
 
 cudaError_t launch_layer_few(const LayerFewArgs& a, bool gated, cudaStream_t s) {
