@@ -96,7 +96,10 @@ __device__ __forceinline__ RouterTerms<float> router_terms(const float* p) {
   return r;
 }
 
-// TILES: tiles of 8 tokens that a pass over the weights serves; with one, a warp's steps are all in flight at once.
+// TILES: tiles of 8 tokens that a pass over the weights serves.  Up to 64 tokens a block takes 8 of them, and a bf16
+// weight's steps are all in flight at once (32 tokens, 128 experts in fp32: 20 us, most of it the last block's work; a
+// block for all of them 29).  More read the weights once for 64.
+constexpr int32_t block_tokens(int tiles) { return tiles == 1 ? 8 : 64; }
 template <typename T, int TILES>
 __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __grid_constant__ LayerRouterArgs a, int32_t pick) {
   extern __shared__ __align__(16) float dyn[];  // [warps][8 TILES][17], then the last block's work
@@ -109,12 +112,13 @@ __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __gri
   const T* rb = static_cast<const T*>(a.weight) + (int64_t)min(e0 + g + 8, a.E - 1) * a.H + 8 * t;
   pdl_wait();
   pdl_launch_dependents();
-  if (a.few && blockIdx.x == 0) {
+  if (a.few && blockIdx.x == 0) {  // (one group of tokens)
     if (threadIdx.x == 0) a.few->ticket = 0;
     if (threadIdx.x < kFewPairs) a.few->done[threadIdx.x] = 0;
   }
-  const int32_t end = min(a.n, ((int32_t)blockIdx.y + 1) * kLayerFusedTokens);
-  for (int32_t t0 = blockIdx.y * kLayerFusedTokens; t0 < end; t0 += kGroup) {
+  constexpr int32_t kTokens = block_tokens(TILES);
+  const int32_t end = min(a.n, ((int32_t)blockIdx.y + 1) * kTokens);
+  for (int32_t t0 = blockIdx.y * kTokens; t0 < end; t0 += kGroup) {
     const int32_t tokens = min(kGroup, end - t0);
     float acc[TILES][4] = {};
     for (int32_t s = s0; s < s1; s += kAhead) {  // (a step is whole: H is a multiple of 64)
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kLayerThreads) layer_router_kernel(const __gri
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    last = atomicAdd(a.count, 1) == (int32_t)gridDim.x - 1;
+    last = atomicAdd(a.count, 1) == (int32_t)(gridDim.x * gridDim.y) - 1;
     if (last) *a.count = 0;
     __threadfence();
   }
@@ -202,7 +206,7 @@ cudaError_t router_launch(const LayerRouterArgs& a, bool pick, cudaStream_t s) {
   const cudaError_t e = raise_smem_limit(layer_router_kernel<T, TILES>, (int)smem, configured);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((a.E + kLayerExperts - 1) / kLayerExperts),
-                  (unsigned)((a.n + kLayerFusedTokens - 1) / kLayerFusedTokens));
+                  (unsigned)((a.n + block_tokens(TILES) - 1) / block_tokens(TILES)));
   return launch_ex(layer_router_kernel<T, TILES>, grid, dim3(kLayerThreads), smem, s, true, a, (int32_t)pick);
 }
 
@@ -211,8 +215,10 @@ cudaError_t router_launch(const LayerRouterArgs& a, bool pick, cudaStream_t s) {
 cudaError_t launch_layer_router(const LayerRouterArgs& a, bool have_logits, cudaStream_t s) {
   if (!have_logits) {
     const bool pick = a.n <= kLayerFusedTokens && !a.few;
-    const cudaError_t e = a.n <= 8 ? (a.weight_f32 ? router_launch<float, 1>(a, pick, s) : router_launch<uint16_t, 1>(a, pick, s))
-                                   : (a.weight_f32 ? router_launch<float, 4>(a, pick, s) : router_launch<uint16_t, 4>(a, pick, s));
+    const bool few = a.n <= kLayerFusedTokens;
+    const cudaError_t e =
+        a.weight_f32 ? (few ? router_launch<float, 1>(a, pick, s) : router_launch<float, 4>(a, pick, s))
+                     : (few ? router_launch<uint16_t, 1>(a, pick, s) : router_launch<uint16_t, 4>(a, pick, s));
     if (e != cudaSuccess || pick || a.few) return e;
   }
   layer_pick_kernel<<<(unsigned)((a.n + 7) / 8), 256, 0, s>>>(a);
