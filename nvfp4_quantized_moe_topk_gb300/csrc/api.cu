@@ -114,6 +114,7 @@ struct moe_nvfp4 {
   // tensor maps
   CUtensorMap tm_xp{}, tm_ap{};  // kGemmTileRows-row activation tiles of the grouped GEMM
   int32_t last_n = 0;
+  bool last_few = false;  // the last call packed no rows (launch_layer_few)
   // per-kernel timing
   bool timing = false;
   std::vector<TimingSlot> slots;
@@ -408,6 +409,7 @@ static moe_status forward_impl(moe_nvfp4* h, const uint16_t* x, const int32_t* i
   const bool gemm = n > h->threshold;
   const bool pdl = !h->timing;
   h->last_n = n;
+  h->last_few = false;
   cudaError_t e;
   DecodeArgs d{};
   d.up_tiles = h->up_tiles;
@@ -654,6 +656,7 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
     f.slots = c.top_k;
     f.parts = layer_few_parts(n, c.top_k, c.inter);
     h->last_n = n;
+    h->last_few = true;
     TimedLaunch tl(h, s, kKDecode);
     return cuda_status(launch_layer_few(f, h->gated, s));
   }
@@ -786,6 +789,7 @@ moe_status moe_nvfp4_get_device_error(moe_nvfp4_t h, int32_t* flags) {
 moe_status moe_nvfp4_debug_routing(moe_nvfp4_t h, int32_t* counts, int32_t* offsets, int32_t* perm_pair,
                                    int32_t* inv, moe_stream_t stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
+  if (h->last_few) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const size_t E = h->cfg.n_experts, R = (size_t)h->last_n * h->cfg.top_k;
   cudaError_t e = cudaSuccess;
@@ -800,6 +804,7 @@ moe_status moe_nvfp4_debug_routing(moe_nvfp4_t h, int32_t* counts, int32_t* offs
 
 moe_status moe_nvfp4_debug_intermediates(moe_nvfp4_t h, uint16_t* a_rows, float* y_rows, moe_stream_t stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
+  if (h->last_few) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const size_t R = (size_t)h->last_n * h->cfg.top_k;
   cudaError_t e = cudaSuccess;

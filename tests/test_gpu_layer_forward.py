@@ -205,3 +205,18 @@ def test_experts_that_many_tokens_pick(n, kw):
     layer.check(n)
     first = layer.call(layer.randn(n, layer.H).to(torch.bfloat16))
     assert int(torch.bincount(first[1].view(-1).long()).max()) > 8
+
+
+def test_a_few_tokens_leave_no_packed_rows():
+    """One token packs no rows, so there are none to look at; a call that packs some brings them back."""
+    b = Layer()
+    x = b.randn(40, b.H).to(torch.bfloat16)
+    b.call(x)
+    counts = torch.zeros(b.E + b.S, dtype=torch.int32, device=DEV)
+    b.call(x[:1])
+    for read in (b.layer.debug_routing, b.layer.debug_intermediates):
+        with pytest.raises(api.MoeError, match="UNSUPPORTED"):
+            read()
+    b.call(x)
+    b.layer.debug_routing(counts)
+    assert int(counts.sum()) > 0
