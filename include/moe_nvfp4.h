@@ -532,7 +532,7 @@ typedef struct moe_linear_args {
   const void *bias;       /* [out_features] or NULL */
   moe_rows x;             /* bf16 [n][in_features] */
   moe_rows residual;      /* [n][out_features]; data may be NULL */
-  moe_rows z;             /* [n][out_features]; data may be NULL: not kept */
+  moe_rows z;             /* [n][out_features]; data may be NULL: not kept; no input's */
   moe_rows out;           /* [n][out_features]; data may be residual's where the types and strides are the same, and
                              no other input's */
 } moe_linear_args;

@@ -287,7 +287,8 @@ moe_status moe_linear(const moe_linear_args* args, moe_stream_t stream) {
     return MOE_ERR_INVALID_ARG;
   if (a.n == 0) return MOE_OK;
   if (!a.x.data || !a.weight || !a.out.data || a.z.data == a.out.data) return MOE_ERR_INVALID_ARG;
-  if (a.out.data == a.x.data || a.out.data == a.weight || (a.z.data && (a.z.data == a.x.data || a.z.data == a.weight)))
+  if (a.out.data == a.x.data || a.out.data == a.weight ||
+      (a.z.data && (a.z.data == a.x.data || a.z.data == a.weight || a.z.data == a.residual.data)))
     return MOE_ERR_INVALID_ARG;
   if (a.residual.data == a.out.data &&
       (a.residual_dtype != a.out_dtype || !same_rows(a.residual, a.out, a.out_features)))

