@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int32_t t = unit; t < p.tiles && ok; t += units, ++it) {
       for (int32_t kb = kb0, chained = 0; kb < kb1; ++kb, ++chained) {
         if (CHAIN && chained == p.chain) chained = 0;
-        const bool first = chained == 0;
+        const bool first = CHAIN ? chained == 0 : kb == kb0;
         if (first && kb != kb0) {
           if (lane == 0) commit<CG>(&t_full[it & 1], first_cta);
           ++it;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int32_t t = unit; t < p.tiles && ok; t += units, ++it) {
       for (int32_t kb = kb0, chained = 0; kb < kb1 && ok; ++kb, ++chained) {
         if (CHAIN && chained == p.chain) chained = 0;
-        const bool first = chained == 0;
+        const bool first = CHAIN ? chained == 0 : kb == kb0;
         if (first && kb != kb0) ++it;
         if (lane == 0) {
           if (first) ok = wait_for(&t_empty[it & 1], ((it >> 1) & 1) ^ 1u, &gave_up);
