@@ -16,10 +16,10 @@
 // through each other's shared memory, in order.
 //
 // The products bound large ones: 16384 tokens of 4096 to 8192 with bias and relu2,
-// its argument kept, 648 us, 1.70 PFLOP/s (88 % of what the library reaches for a
-// product alone); 4314 tokens of 4096 to 2688 with a residual 67 us, 1.42.  Small
+// its argument kept, 642 us, 1.71 PFLOP/s (88 % of what the library reaches for a
+// product alone); 4314 tokens of 4096 to 2688 with a residual 65 us, 1.47.  Small
 // ones are bound by their start, 4 us until the first result: 33 tokens 5 us.  A
-// backward pass of 4314 tokens of 2688 to 4608, d_weight in fp32, takes 167 us for
+// backward pass of 4314 tokens of 2688 to 4608, d_weight in fp32, takes 166 us for
 // 214 GFLOP, 1.28 PFLOP/s.
 #include <algorithm>
 
