@@ -36,6 +36,10 @@ struct LinearProduct {
 cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s);
 // For a few rows (linear_rows.cu): one term, both operands with their columns contiguous, R <= 64.
 cudaError_t launch_linear_rows(const LinearProduct& a, cudaStream_t s);
+// d_weight of a few tokens (linear_outer.cu): C <= kLinearOuterTokens, neither operand with its columns contiguous, a plain
+// finish.
+constexpr int32_t kLinearOuterTokens = 128;
+cudaError_t launch_linear_outer(const LinearProduct& a, cudaStream_t s);
 cudaError_t linear_mma_flags(int32_t* flags);  // reads and clears; the device is idle
 
 }  // namespace moe

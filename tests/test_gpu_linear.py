@@ -289,3 +289,37 @@ def test_refusals():
         with pytest.raises(api.MoeError):
             call()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 47, 48, 49, 64, 100, 128, 129])
+@pytest.mark.parametrize("kw", [
+    dict(inp=8, out=8, dw="fp32"), dict(inp=136, out=72, wide=8), dict(inp=264, out=200, o="fp32", dw="fp32", wide=16),
+    dict(inp=1032, out=1096, activation="silu", z="fp32", dw="fp32"), dict(inp=72, out=1000, activation="relu2", dx="fp32")])
+def test_gradients_of_few_tokens(n, kw):
+    """Either way to d_weight: the sum of few outer products, and the larger product."""
+    Case(n=n, **kw).check_backward()
+
+
+@pytest.mark.parametrize("n", [5, 48, 128])
+@pytest.mark.parametrize("dw", ["bf16", "fp32"])
+def test_the_weight_gradient_ends_with_its_last_row(n, dw):
+    c = Case(n, 136, 72, dw=dw)
+    c.backward_inputs()
+    room = torch.full((200, 136), 7.0, dtype=c.dw, device=DEV)
+    api.linear_backward(c.dy, c.x, c.w, None, None, room[64:136], None)
+    assert bool((room[:64] == 7).all()) and bool((room[136:] == 7).all())
+    want = c.backward()[1]
+    assert torch.equal(room[64:136], want)
+
+
+@pytest.mark.parametrize("n", [3, 100])
+def test_infinities_and_nan_in_few_tokens_reach_their_rows_and_columns_alone(n):
+    c = Case(n, 136, 72)
+    c.backward_inputs()
+    clean = c.backward()[1]
+    c.dy[1, 5], c.x[2, 7] = float("inf"), float("nan")
+    d_w = c.backward()[1]
+    touched = torch.zeros_like(clean, dtype=torch.bool)
+    touched[5], touched[:, 7] = True, True
+    assert not bool(torch.isfinite(d_w[5]).any()) and bool(torch.isnan(d_w[:, 7]).all())
+    assert torch.equal(d_w[~touched], clean[~touched])
