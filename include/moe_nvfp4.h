@@ -661,8 +661,8 @@ MOE_API size_t moe_qk_workspace_bytes(int32_t n, int32_t q_heads, int32_t k_head
  *     topk of logits + router_bias, weights as moe_router_topk
  *     dst[t] = bf16_rne(residual[t] + sum_j w[t][j] * y_(t,j) + sum_s y_(t,s))
  * with y as at the top of the file, in fp32 and in a fixed order.  A batch that
- * moe_nvfp4_forward runs as one launch takes two here (the router, which also
- * picks, and the layer); a larger one takes the router's product on the tensor
+ * moe_nvfp4_forward runs as one launch takes two here (the router and the
+ * layer); a larger one takes the router's product on the tensor
  * cores (bf16 router_weight and E a multiple of 8; otherwise on the plain
  * cores), the picks and moe_nvfp4_forward's launches.  A few tokens have a
  * kernel of their own, which packs no rows: moe_nvfp4_debug_routing and

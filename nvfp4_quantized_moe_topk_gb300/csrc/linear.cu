@@ -3,6 +3,7 @@
 //
 // Backward: dz = d_out * act'(z), then d_x = dz W and d_weight = dz^T x by the same
 // products, their operands read as they lie in memory (no transposed copies).
+// Few tokens go other ways: forward linear_rows.cu, d_weight linear_outer.cu.
 // Where dz is not d_out itself it goes through the workspace: as one bf16 term for a
 // gradient in bf16, whose own rounding (2^-8 of a value) hides what the terms' roundings,
 // of either sign, leave in the sum; as three for a gradient in fp32, which keep dz's 24 bits.
