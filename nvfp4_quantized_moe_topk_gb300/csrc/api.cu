@@ -316,6 +316,7 @@ moe_status moe_nvfp4_create(const moe_nvfp4_config* config, const moe_nvfp4_weig
   TRY(cudaMemcpyAsync(h->dn_g, w->down_global, E * sizeof(float), cudaMemcpyDeviceToDevice, s));
   TRY(cudaMemsetAsync(h->err, 0, sizeof(int32_t), s));
   TRY(cudaMemsetAsync(h->router_count, 0, sizeof(int32_t), s));
+  TRY(cudaMemsetAsync(h->part_of, 0, kLayerMaxParts * sizeof(int32_t), s));
   if (E == 1 && c.top_k == 1) {
     const size_t nt = c.max_tokens > 0 ? (size_t)c.max_tokens : 1;
     TRY(cudaMalloc(&h->dense_ids, nt * sizeof(int32_t)));
@@ -593,9 +594,11 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
       !aligned(a.router_bias, 4) || !aligned(a.topk_ids, 4) || !aligned(a.topk_weights, 4) || !aligned(a.logits, 16))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // experts in parts of 8 tokens, where all of them are few enough for one launch
+  // experts in parts of 8 tokens, where all of them are few enough for one launch, and the router's last block deals them
+  // (a handle may run more tokens as one launch than that block routes: their experts stay whole)
   const int32_t more = layer_parts(n, k, S);
-  const bool parts = more <= kLayerMaxParts && c.n_experts + more <= 1024 && runs_as_one(h, n, c.n_experts + more);
+  const bool parts = n <= kLayerFusedTokens && more <= kLayerMaxParts && c.n_experts + more <= 1024 &&
+                     runs_as_one(h, n, c.n_experts + more);
   const bool one = parts || runs_as_one(h, n, c.n_experts);
   const bool few = one && layer_few_takes(n, c.top_k, H, c.inter, h->gated);
   LayerRouterArgs r = {};

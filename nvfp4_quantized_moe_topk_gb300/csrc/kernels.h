@@ -281,7 +281,7 @@ struct LayerRouterArgs : LayerPick {
 inline int32_t layer_parts(int32_t n, int32_t k, int32_t shared) {
   return n <= kDecPassTok ? 0 : shared * ((n + kDecPassTok - 1) / kDecPassTok - 1) + n * k / kDecPassTok;
 }
-constexpr int kLayerFusedTokens = 64;  // logits and picks in one launch
+constexpr int kLayerFusedTokens = 64;  // logits and picks in one launch; the parts are dealt there alone
 // Logits (where not `have_logits`) and picks.
 cudaError_t launch_layer_router(const LayerRouterArgs& a, bool have_logits, cudaStream_t s);
 
