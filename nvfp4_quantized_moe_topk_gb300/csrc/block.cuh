@@ -39,6 +39,20 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = d;
 }
 
+// An fp32 value as a sum of bf16 terms, each the upper half of what is left: three hold its 24 bits.  Takes the next term
+// off s; the result's upper 16 bits are it.  (Cut off, not rounded: a value above the largest bf16 would round to
+// infinity.  Of an infinity nothing is left, where a subtraction gives NaN; a NaN leaves one.)
+__device__ __forceinline__ uint32_t take_term(float& s) {
+  const uint32_t t = __float_as_uint(s) & 0xffff0000u;
+  s = (__float_as_uint(s) & 0x7fffffffu) == 0x7f800000u ? 0.f : s - __uint_as_float(t);
+  return t;
+}
+// Of two values, as a bf16 pair.
+__device__ __forceinline__ uint32_t take_terms(float& lo, float& hi) {
+  const uint32_t l = take_term(lo);
+  return take_term(hi) | l >> 16;
+}
+
 // Two fp32 values that one instruction works on.
 struct F2 {
   float x, y;

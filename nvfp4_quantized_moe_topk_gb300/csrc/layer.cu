@@ -86,11 +86,7 @@ __device__ __forceinline__ RouterTerms<float> router_terms(const float* p) {
   for (int k = 0; k < 3; ++k) {
     uint32_t d[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      d[i] = pack2(v[2 * i], v[2 * i + 1]);
-      v[2 * i] -= bf16lo(d[i]);
-      v[2 * i + 1] -= bf16hi(d[i]);
-    }
+    for (int i = 0; i < 4; ++i) d[i] = take_terms(v[2 * i], v[2 * i + 1]);
     r.v[k] = make_uint4(d[0], d[1], d[2], d[3]);
   }
   return r;
