@@ -55,6 +55,15 @@ __device__ __forceinline__ void values8(const Raw8<float>& r, float (&v)[8]) {
   }
 }
 
+// The next bf16 term of a value, taken off it.  Rounded, so that a first term alone is the nearest; but a finite value
+// above the largest bf16 stays finite, and of an infinity nothing is left, where a subtraction gives NaN.
+__device__ __forceinline__ float take_rounded(float& s) {
+  float t = __bfloat162float(__float2bfloat16_rn(s));
+  if (isinf(t)) t = isinf(s) ? s : copysignf(0x1.fep127f, s);
+  s = isinf(s) ? 0.f : s - t;
+  return t;
+}
+
 // dz of 8 lanes' columns and a chunk of tokens, and its column sums.
 constexpr int kDzAhead = 4;  // rows of a thread on their way at once
 template <bool ACT, typename DT, typename ZT>
@@ -89,12 +98,10 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzParams a)
           sum[i] += d[i];
         }
         for (int m = 0; m < a.n_terms; ++m) {
-          store8(a.terms + ((int64_t)m * a.n + t) * a.out + col, d);
+          float term[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float h = __bfloat162float(__float2bfloat16_rn(d[i]));
-            d[i] = isfinite(h) ? d[i] - h : 0.f;  // (an infinity stays one)
-          }
+          for (int i = 0; i < 8; ++i) term[i] = take_rounded(d[i]);
+          store8(a.terms + ((int64_t)m * a.n + t) * a.out + col, term);
         }
       }
     }
