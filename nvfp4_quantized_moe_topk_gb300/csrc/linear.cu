@@ -55,13 +55,30 @@ __device__ __forceinline__ void values8(const Raw8<float>& r, float (&v)[8]) {
   }
 }
 
-// The next bf16 term of a value, taken off it.  Rounded, so that a first term alone is the nearest; but a finite value
-// above the largest bf16 stays finite, and of an infinity nothing is left, where a subtraction gives NaN.
-__device__ __forceinline__ float take_rounded(float& s) {
-  float t = __bfloat162float(__float2bfloat16_rn(s));
-  if (isinf(t)) t = isinf(s) ? s : copysignf(0x1.fep127f, s);
-  s = isinf(s) ? 0.f : s - t;
-  return t;
+// The next bf16 term of 8 values, taken off them.  Rounded, so that a first term alone is the nearest; but (`plain`: there is none) a
+// finite value above the largest bf16 stays finite, and of an infinity nothing is left, where a subtraction gives NaN.
+constexpr float kRoundsToInfinity = 0x1.ffp127f;  // the smallest that does
+__device__ __forceinline__ uint4 take_rounded(float (&v)[8], bool plain) {
+  uint32_t t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!plain) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float& s = v[2 * i + k];
+        const float most = copysignf(0x1.fep127f, s);
+        const bool large = fabsf(s) >= kRoundsToInfinity, infinite = isinf(s);
+        const uint32_t h = __float_as_uint(large ? (infinite ? s : most) : __bfloat162float(__float2bfloat16_rn(s))) >> 16;
+        s = infinite ? 0.f : s - __uint_as_float(h << 16);
+        t[i] = k ? t[i] | h << 16 : h;
+      }
+      continue;
+    }
+    t[i] = pack2(v[2 * i], v[2 * i + 1]);
+    v[2 * i] -= bf16lo(t[i]);
+    v[2 * i + 1] -= bf16hi(t[i]);
+  }
+  return make_uint4(t[0], t[1], t[2], t[3]);
 }
 
 // dz of 8 lanes' columns and a chunk of tokens, and its column sums.
@@ -97,12 +114,11 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzParams a)
           if (ACT) d[i] *= linear_slope(z[i], a.act);
           sum[i] += d[i];
         }
-        for (int m = 0; m < a.n_terms; ++m) {
-          float term[8];
+        float most = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) term[i] = take_rounded(d[i]);
-          store8(a.terms + ((int64_t)m * a.n + t) * a.out + col, term);
-        }
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(d[i]));
+        for (int m = 0; m < a.n_terms; ++m)
+          *reinterpret_cast<uint4*>(a.terms + ((int64_t)m * a.n + t) * a.out + col) = take_rounded(d, most < kRoundsToInfinity);
       }
     }
   }
