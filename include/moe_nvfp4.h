@@ -550,8 +550,8 @@ MOE_API moe_status moe_linear(const moe_linear_args *args, moe_stream_t stream);
  *     d_bias[o]      = sum_t dz[t][o]
  * (the gradient of the residual is residual_scale * d_out).  args' bias,
  * residual and out are not looked at.  A gradient in bf16 is summed from dz
- * rounded to bf16, one in fp32 from dz with its 24 bits; where d_out is bf16
- * and there is no activation dz is d_out, exactly.  The sums run in a fixed
+ * within 2^-16 of itself, one in fp32 from dz with its 24 bits; where d_out is
+ * bf16 and there is no activation dz is d_out, exactly.  The sums run in a fixed
  * order.  A NULL output is not computed; x is needed for d_weight, weight for
  * d_x.  No output may be an input. */
 typedef struct moe_linear_grads {

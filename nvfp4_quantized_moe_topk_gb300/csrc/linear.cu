@@ -4,10 +4,13 @@
 // Backward: dz = d_out * act'(z), then d_x = dz W and d_weight = dz^T x by the same
 // products, their operands read as they lie in memory (no transposed copies).
 // Few tokens go other ways: forward linear_rows.cu, d_weight linear_outer.cu.
-// Where dz is not d_out itself it goes through the workspace: as one bf16 term for a
-// gradient in bf16, whose own rounding (2^-8 of a value) hides what the terms' roundings,
-// of either sign, leave in the sum; as three for a gradient in fp32, which keep dz's 24 bits.
-// d_bias comes from dz in 32 bits, in the pass that makes it.
+// Where dz is not d_out itself it goes through the workspace as a sum of bf16 terms: two
+// for a gradient in bf16, within 2^-16 of each dz, which leaves in a sum of thousands of
+// products what the tensor core's own cutting does (linear_mma.cu); three for a gradient
+// in fp32, which keep dz's 24 bits.  (One term for a gradient in bf16, 2^-8 of each dz,
+// halves the products' time, but a gradient's distance from 64 bits is 1.41 times that of
+// rounding it alone, and small gradients among large ones are lost.)  d_bias comes from
+// dz in 32 bits, in the pass that makes it.
 #include <algorithm>
 
 #include "block.cuh"
@@ -55,7 +58,7 @@ __device__ __forceinline__ void values8(const Raw8<float>& r, float (&v)[8]) {
   }
 }
 
-// The next bf16 term of 8 values, taken off them.  Rounded, so that a first term alone is the nearest; but (`plain`: there is none) a
+// The next bf16 term of 8 values, taken off them.  Rounded, so that the first two are nearest; but (`plain`: there is none) a
 // finite value above the largest bf16 stays finite, and of an infinity nothing is left, where a subtraction gives NaN.
 constexpr float kRoundsToInfinity = 0x1.ffp127f;  // the smallest that does
 __device__ __forceinline__ uint4 take_rounded(float (&v)[8], bool plain) {
@@ -202,8 +205,8 @@ cudaError_t launch_linear_backward(const moe_linear_args& a, const moe_linear_gr
   }
   const bool same = a.activation == MOE_LINEAR_NONE && d.d_out_dtype == MOE_DTYPE_BF16;  // dz is d_out
   const bool products = d.d_x.data || d.d_weight;
-  const int terms_x = !same && d.d_x_dtype == MOE_DTYPE_F32 ? kLinearTerms : 1;
-  const int terms_w = !same && d.d_weight_dtype == MOE_DTYPE_F32 ? kLinearTerms : 1;
+  const int terms_x = same ? 1 : d.d_x_dtype == MOE_DTYPE_F32 ? kLinearTerms : 2;
+  const int terms_w = same ? 1 : d.d_weight_dtype == MOE_DTYPE_F32 ? kLinearTerms : 2;
   uint16_t* terms = static_cast<uint16_t*>(workspace);
   const size_t term = (size_t)a.n * a.out_features;
   float* part = reinterpret_cast<float*>(terms + kLinearTerms * term);

@@ -5,7 +5,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from nvfp4_quantized_moe_topk_gb300 import api  # noqa: E402
-from test_gpu_linear import D, DEV, T, U, Case, half, sum_error  # noqa: E402
+from test_gpu_linear import D, DEV, T, U, Case, half, slope, sum_error  # noqa: E402
 
 MOST = torch.finfo(torch.float32).max
 
@@ -44,3 +44,40 @@ def test_an_infinite_gradient_stays_infinite(n, t):
     assert torch.equal(d_x[rows], clean[0][rows]) and torch.equal(d_w[outs], clean[1][outs])
     assert float(d_b[5]) == float("inf") and torch.equal(d_b[outs], clean[2][outs])
     assert api.linear_device_error() == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=512, inp=1024, out=1024, activation="silu"), dict(n=40, inp=1024, out=1024, activation="gelu_tanh", z="fp32"),
+    dict(n=1000, inp=1032, out=520, activation="relu2", dw="fp32"), dict(n=700, inp=264, out=1032, o="fp32", dx="bf16")])
+def test_a_bf16_gradient_is_off_by_its_own_rounding(kw):
+    """The whole gradient's distance from 64 bits against that of rounding it alone.  dz in two terms adds 2^-16 of each term at
+    most, 2^-17 in the mean square, against 2^-10 of the rounding: less than a thousandth; a hundredth is allowed for the sums.
+    (With dz rounded to one term: 1.41 times.)"""
+    c = Case(**kw)
+    c.backward_inputs()
+    if c.zs is not None:
+        c.zs.clamp_(-3, 3)
+    d_x, d_w, _ = c.backward()
+    dz = c.dy.to(D)
+    if c.act != "none":
+        dz = dz * slope(c.zs.to(D), c.act)
+    for got, ref in ((d_x, dz @ c.w.to(D)), (d_w, dz.t() @ c.x.to(D))):
+        if got.dtype == torch.bfloat16:
+            own = float((ref.bfloat16().to(D) - ref).norm())
+            assert float((got.to(D) - ref).norm()) < 1.01 * own
+
+
+@pytest.mark.parametrize("n", [64, 600])
+def test_gradients_that_cancel(n):
+    """Two features with the same weights and opposite gradients, but for 2^-12 of them: what is left is right to 2^-2 where dz
+    holds 2^-16 of each term, and nothing is where it holds 2^-8."""
+    c = Case(n, 264, 136, o="fp32", dx="bf16", dw="bf16")
+    c.backward_inputs()
+    c.w[1::2] = c.w[0::2]
+    c.dy[:, 1::2] = -c.dy[:, 0::2] * (1 + 2.0 ** -12)
+    d_x = c.backward()[0]
+    dz, w = c.dy.to(D), c.w.to(D)
+    ref, size = dz @ w, dz.abs() @ w.abs()
+    bound = 2.0 ** -16 * size + sum_error(2 * (136 + 64), size)
+    assert bool(((d_x.to(D) - ref).abs() <= 2.0 ** -8 * (ref.abs() + bound) + bound).all())
+    assert float((d_x.to(D) - ref).norm()) < 2.0 ** -2 * float(ref.norm())
