@@ -37,10 +37,12 @@ constexpr uint32_t kSmem = 227 * 1024, kBarBytes = 1024;
 constexpr uint32_t kPBytes = 128 * 128;  // a stage's features: 128 of 64 columns
 constexpr uint32_t kSlotBytes = 16 * 36 * 4;  // of an epilogue warp
 constexpr int kMaxCluster = 8;
-// The tensor core cuts what it adds to a sum where it would round, which costs a sum of C products about 1e-9 C of its
-// size, always towards zero.  A result in fp32 is therefore summed in tensor memory for 8 blocks of 64 columns at a time,
-// and from there on in registers (4314 columns: 4.7e-6 off without, 4.7e-7 so).
-constexpr int32_t kChain = 8;
+// The tensor core cuts what it adds to a sum where it would round, always towards zero, which costs a sum of C products
+// about 1e-9 C of its size, 5e-9 C where all have one sign.  A result in fp32 is therefore summed in tensor memory for 8
+// blocks of 64 columns at a time, and from there on in registers (4314 columns: 4.7e-6 off without, 4.7e-7 so).  So is a
+// result in bf16 of more than 512 blocks: 32768 columns of one sign lose a twentieth of half a step (131072: a fifth), for
+// which reading the sums back is too dear (2048 x 32768 to 2048: 150 us, 183 so).
+constexpr int32_t kChain = 8, kLongSum = 512;
 constexpr int kChainBlocks = 4;  // of 32 sums a thread
 
 // Set where a bounded wait ran out; read by moe_linear_get_device_error.
@@ -744,7 +746,7 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
   // (the sums of a cluster meet where the stages were)
   if (p.split > 1 && (uint32_t)p.rows * 512 > p.stages * p.stage_bytes) return cudaErrorInvalidConfiguration;
   const int32_t own = (p.KB * p.terms + p.split - 1) / p.split;
-  const bool chain = f32 && own > kChain;
+  const bool chain = own > (f32 ? kChain : kLongSum);
   p.chain = chain ? kChain : own;
   Maps m;
   e = operand_map(&m.p, a.p, a.F, a.C, 128);

@@ -25,6 +25,10 @@ namespace {
 
 constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32, kRowsFeatures = 16;
 constexpr int kBatch = 6;  // steps of 32 columns in flight
+// Batches that an instruction's sums run through before they move on: the tensor cores cut what they add to a sum where it
+// would round, always towards zero (linear_mma.cu).  Shorter rows do without (16 tokens of 4096 to 4096: 7.7 us, with a
+// second set of sums 8.1; of 16384 columns, which need it, 20.7 and 21.2).
+constexpr int kChainBatches = 3, kChainColumns = kChainBatches * kBatch * 32 * kRowsWarps;
 
 struct RowsPlan {
   int32_t n, in, out;
@@ -39,8 +43,8 @@ __device__ __forceinline__ uint4 stream16(const uint16_t* p) {
   return v;
 }
 
-// TILES: tiles of 8 tokens.
-template <int TILES>
+// TILES: tiles of 8 tokens.  CHAIN: rows of more than kChainColumns.
+template <int TILES, bool CHAIN>
 __global__ void __launch_bounds__(kRowsThreads, TILES <= 2 ? 2 : 1) linear_rows_kernel(const __grid_constant__ RowsPlan p) {
   __shared__ float sums[kRowsWarps][8 * TILES][kRowsFeatures + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -51,9 +55,10 @@ __global__ void __launch_bounds__(kRowsThreads, TILES <= 2 ? 2 : 1) linear_rows_
   const uint16_t* xr[TILES];
 #pragma unroll
   for (int i = 0; i < TILES; ++i) xr[i] = p.x + (int64_t)min(8 * i + g, p.n - 1) * p.x_stride + 8 * t;
-  float acc[TILES][4] = {};
+  float acc[TILES][4] = {}, total[TILES][4] = {};
   pdl_wait();
   pdl_launch_dependents();
+  int chained = 0;
   for (int32_t s = s0; s < s1; s += kBatch) {
     uint4 a[kBatch], b[kBatch];
 #pragma unroll
@@ -79,6 +84,22 @@ __global__ void __launch_bounds__(kRowsThreads, TILES <= 2 ? 2 : 1) linear_rows_
         mma_bf16_16816(acc[j], a[i].z, b[i].z, a[i].w, b[i].w, x[i].z, x[i].w);
       }
     }
+    if (CHAIN && ++chained == kChainBatches) {
+      chained = 0;
+#pragma unroll
+      for (int j = 0; j < TILES; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          total[j][i] += acc[j][i];
+          acc[j][i] = 0.f;
+        }
+    }
+  }
+  if (CHAIN) {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] += total[j][i];
   }
 #pragma unroll
   for (int j = 0; j < TILES; ++j) {
@@ -109,10 +130,12 @@ cudaError_t launch_linear_rows(const LinearProduct& a, cudaStream_t s) {
   const RowsPlan p = {a.R, a.C, a.F, static_cast<const uint16_t*>(a.p.data), static_cast<const uint16_t*>(a.q[0].data),
                       a.q[0].stride, a.finish};
   const dim3 grid((unsigned)((a.F + kRowsFeatures - 1) / kRowsFeatures)), block(kRowsThreads);
-  if (a.R <= 8) return launch_ex(linear_rows_kernel<1>, grid, block, 0, s, true, p);
-  if (a.R <= 16) return launch_ex(linear_rows_kernel<2>, grid, block, 0, s, true, p);
-  if (a.R <= 32) return launch_ex(linear_rows_kernel<4>, grid, block, 0, s, true, p);
-  return launch_ex(linear_rows_kernel<8>, grid, block, 0, s, true, p);
+  const bool chain = a.C > kChainColumns;
+  auto kernel = a.R <= 8    ? (chain ? linear_rows_kernel<1, true> : linear_rows_kernel<1, false>)
+                : a.R <= 16 ? (chain ? linear_rows_kernel<2, true> : linear_rows_kernel<2, false>)
+                : a.R <= 32 ? (chain ? linear_rows_kernel<4, true> : linear_rows_kernel<4, false>)
+                            : (chain ? linear_rows_kernel<8, true> : linear_rows_kernel<8, false>);
+  return launch_ex(kernel, grid, block, 0, s, true, p);
 }
 
 }  // namespace moe

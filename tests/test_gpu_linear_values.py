@@ -81,3 +81,44 @@ def test_gradients_that_cancel(n):
     bound = 2.0 ** -16 * size + sum_error(2 * (136 + 64), size)
     assert bool(((d_x.to(D) - ref).abs() <= 2.0 ** -8 * (ref.abs() + bound) + bound).all())
     assert float((d_x.to(D) - ref).norm()) < 2.0 ** -2 * float(ref.norm())
+
+
+def _long(n, inp, out, o):
+    """All values positive, rows of many sizes: a sum that is cut on the way shows in full."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    x = (torch.rand(n, inp, generator=g, device=DEV) + 0.5) * (1 + torch.rand(n, 1, generator=g, device=DEV))
+    w = torch.rand(out, inp, generator=g, device=DEV) + 0.5
+    return x.bfloat16(), w.bfloat16(), torch.empty(n, out, dtype=T[o], device=DEV)
+
+
+def _exact(x, w):
+    ref = torch.zeros(x.shape[0], w.shape[0], dtype=D, device=DEV)
+    for c in range(0, x.shape[1], 1 << 16):
+        ref += x[:, c: c + (1 << 16)].to(D) @ w[:, c: c + (1 << 16)].to(D).t()
+    return ref
+
+
+@pytest.mark.parametrize("n,inp,out,o", [(200, 1 << 20, 8, "bf16"), (200, 1 << 20, 264, "bf16"), (40, (1 << 20) + 72, 4096, "bf16"),
+                                         (4, 1 << 22, 8, "fp32"), (4, 1 << 22, 8, "bf16"), (33, 1 << 21, 24, "fp32")])
+def test_long_sums(n, inp, out, o):
+    """Short chains, each within 36 steps of 2^-22 of itself, whose sums are added in fp32, a rounding of 2^-24 each: C / 512 of
+    them, in the way of up to 16 tokens and 64 features an eighth as many in each of 8 warps.  (A sum cut all the way is 1e-9 a
+    column off.)"""
+    x, w, out_t = _long(n, inp, out, o)
+    api.linear(x, w, out_t)
+    ref = _exact(x, w)
+    own = 36 * 2.0 ** -22 + (inp / 512 / (8 if out <= 64 and n <= 64 else 1) + 16) * U
+    assert bool(((out_t.to(D) - ref).abs() <= (half(T[o]) + own) * (1 + 2.0 ** -7) * ref).all())
+    assert api.linear_device_error() == 0
+
+
+@pytest.mark.parametrize("dw", ["bf16", "fp32"])
+def test_long_sums_of_tokens(dw):
+    n = (1 << 20) + 24
+    x, w, _ = _long(16, n, 72, "bf16")
+    x, dy = x.t().contiguous(), w.t().contiguous()  # d_weight [72, 16] of n tokens
+    d_w = torch.empty(72, 16, dtype=T[dw], device=DEV)
+    api.linear_backward(dy, x, torch.zeros(72, 16, dtype=torch.bfloat16, device=DEV), None, None, d_w)
+    ref = _exact(dy.t(), x.t())
+    own = 36 * 2.0 ** -22 + (n / 512 + 16) * U
+    assert bool(((d_w.to(D) - ref).abs() <= (half(T[dw]) + own) * (1 + 2.0 ** -7) * ref).all())
