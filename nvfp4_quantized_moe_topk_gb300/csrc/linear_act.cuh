@@ -6,9 +6,13 @@
 
 namespace moe {
 
-// z / (1 + exp(-v)) for finite z: 0 and z where the exponential overflows or vanishes.  The fast exponential and quotient
-// are within (4 + 1.2 |v|) 2^-23 of the value.
-__device__ __forceinline__ float logistic(float v, float z = 1.f) { return __fdividef(z, 1.f + __expf(-v)); }
+// z / (1 + exp(-v)), by the exponential of -|v|, which neither overflows nor leaves the fast quotient's range (it is 0 for a
+// divisor above 2^126).  The fast exponential and quotient are within (5 + 1.2 |v|) 2^-23 of the value, and within 2^-149
+// |z| where that exponential is subnormal.
+__device__ __forceinline__ float logistic(float v, float z = 1.f) {
+  const float e = __expf(-fabsf(v));
+  return __fdividef(v >= 0.f ? z : z * e, 1.f + e);
+}
 
 // gelu_tanh: z / 2 (1 + tanh(u)) = z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)

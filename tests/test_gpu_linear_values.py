@@ -5,7 +5,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from nvfp4_quantized_moe_topk_gb300 import api  # noqa: E402
-from test_gpu_linear import D, DEV, T, U, Case, half, slope, sum_error  # noqa: E402
+from test_gpu_linear import D, DEV, GELU, T, U, Case, act, half, slope, sum_error  # noqa: E402
 
 MOST = torch.finfo(torch.float32).max
 
@@ -122,3 +122,29 @@ def test_long_sums_of_tokens(dw):
     ref = _exact(dy.t(), x.t())
     own = 36 * 2.0 ** -22 + (n / 512 + 16) * U
     assert bool(((d_w.to(D) - ref).abs() <= (half(T[dw]) + own) * (1 + 2.0 ** -7) * ref).all())
+
+
+@pytest.mark.parametrize("activation", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("n", [1, 40, 100, 2500])
+def test_activations_far_below_zero(n, activation):
+    """Where exp(-v) overflows or nears it, the value is still a number that fp32 holds.  To test_gpu_linear's (8 + 6 |v|) 2^-23
+    an exponential below the smallest normal number adds 2^-149 of its factor."""
+    out = 2056
+    lo, hi = (-104.0, -60.0) if activation == "silu" else (-10.6, -8.8)
+    z = torch.linspace(lo, hi, out, device=DEV)
+    x, w = torch.zeros(n, 8, dtype=torch.bfloat16, device=DEV), torch.zeros(out, 8, dtype=torch.bfloat16, device=DEV)
+    got, kept = torch.empty(n, out, device=DEV), torch.empty(n, out, device=DEV)
+    api.linear(x, w, got, z, None, kept, activation=activation)
+    assert torch.equal(kept, z.expand(n, out))
+    zd = z.to(D)
+    v = (zd if activation == "silu" else GELU * (zd + 0.044715 * zd ** 3)).abs()
+    ref = act(zd, activation)
+    assert bool(((got.to(D) - ref).abs() <= (8 + 6 * v) * 2.0 ** -23 * ref.abs() + 2.0 ** -148 * (1 + zd.abs())).all())
+    assert bool((got[:, ref.abs() > 2.0 ** -126] != 0).all())
+    dy, d_b = torch.ones(n, out, device=DEV), torch.empty(out, device=DEV)
+    api.linear_backward(dy, None, w, kept, None, None, d_b, activation=activation)
+    s = slope(zd, activation)
+    size = v if activation == "silu" else GELU * zd.abs() * (1 + 3 * 0.044715 * zd ** 2)  # of p and of z p
+    bound = (8 + 6 * v + n / 8 + 80) * 2.0 ** -23 * s.abs() + 2.0 ** -148 * (1 + size)
+    assert bool(((d_b.to(D) - n * s).abs() <= n * bound).all())
+    assert bool((d_b[s.abs() > 2.0 ** -126] != 0).all())
