@@ -86,13 +86,15 @@ __device__ __forceinline__ uint4 take_rounded(float (&v)[8], bool plain) {
 
 // dz of 8 lanes' columns and a chunk of tokens, and its column sums.
 constexpr int kDzAhead = 4;  // rows of a thread on their way at once
+constexpr int kDzRun = 16;    // such turns whose sums are added one after another, so that a sum's error does not grow with n
 template <bool ACT, typename DT, typename ZT>
 __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzParams a) {
   __shared__ float sums[8 * kDzThreads];
   const int lane = threadIdx.x % a.lanes, row = threadIdx.x / a.lanes, rows = kDzThreads / a.lanes;
   const int32_t columns = 8 * a.lanes, col = blockIdx.x * columns + 8 * lane;
   const int32_t begin = (int32_t)((int64_t)a.n * blockIdx.y / a.chunks), end = (int32_t)((int64_t)a.n * (blockIdx.y + 1) / a.chunks);
-  float sum[8] = {};
+  float sum[8] = {}, total[8] = {};
+  int turns = 0;
   if (!a.beside) pdl_wait();
   pdl_launch_dependents();
   if (col < a.out) {
@@ -123,11 +125,19 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzParams a)
         for (int m = 0; m < a.n_terms; ++m)
           *reinterpret_cast<uint4*>(a.terms + ((int64_t)m * a.n + t) * a.out + col) = take_rounded(d, most < kRoundsToInfinity);
       }
+      if (++turns == kDzRun) {
+        turns = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          total[i] += sum[i];
+          sum[i] = 0.f;
+        }
+      }
     }
   }
   if (a.part) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[row * columns + 8 * lane + i] = sum[i];
+    for (int i = 0; i < 8; ++i) sums[row * columns + 8 * lane + i] = total[i] + sum[i];
     __syncthreads();
     for (int32_t i = threadIdx.x; i < columns; i += kDzThreads) {
       const int32_t c = blockIdx.x * columns + i;

@@ -148,3 +148,15 @@ def test_activations_far_below_zero(n, activation):
     bound = (8 + 6 * v + n / 8 + 80) * 2.0 ** -23 * s.abs() + 2.0 ** -148 * (1 + size)
     assert bool(((d_b.to(D) - n * s).abs() <= n * bound).all())
     assert bool((d_b[s.abs() > 2.0 ** -126] != 0).all())
+
+
+@pytest.mark.parametrize("n", [1 << 12, (1 << 20) + 5, 1 << 24])
+def test_column_sums_of_many_tokens(n):
+    """d_bias of equal gradients, which round the same way at every addition once their sum has few bits left for them.  A thread
+    adds 64 rows, such sums of its n / 2432 rows, then 8 threads', 304 chunks' by 32 warps and those: a rounding of 2^-24 each."""
+    dy = torch.full((n, 8), 1 + 0.98 * 2.0 ** -12, device=DEV)
+    dy[:, 4:] *= -3
+    w, d_b = torch.zeros(8, 8, dtype=torch.bfloat16, device=DEV), torch.empty(8, device=DEV)
+    api.linear_backward(dy, None, w, None, None, None, d_b)
+    ref = dy[0].to(D) * n
+    assert bool(((d_b.to(D) - ref).abs() <= (64 + n / 2432 / 64 + 1 + 8 + 10 + 5) * U * ref.abs()).all())
