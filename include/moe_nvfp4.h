@@ -589,9 +589,10 @@ MOE_API moe_status moe_linear_get_device_error(int32_t *flags);
  * images and video) sections[j] pairs turn by axis j: the first sections[0]
  * pairs by axis 0, the next by axis 1 and so on, or, with
  * sections_interleaved, pair i by axis j = i mod n_axes while i / n_axes <
- * sections[j], and by axis 0 after that.  The angle's product is exact to
- * 2^-54 turns times the position, however far that is.  Statistics are held
- * in fp32, each output is rounded once.  Infinities and NaN stay in their
+ * sections[j], and by axis 0 after that.  The angle is exact to 2^-54 turns
+ * (times inv_freq where that is above 1) times the position, however far that
+ * is, and then rounded to fp32 once.  Statistics are held in fp32, each output
+ * is rounded once.  Infinities and NaN stay in their
  * head; an inv_freq that is not finite gives an arbitrary rotation. */
 #define MOE_MAX_AXES 4
 typedef struct moe_qk_args {

@@ -12,8 +12,10 @@
 // product is off by 2^-24 of itself, a whole turn's tenth for positions in the
 // millions; instead each frequency becomes a 64-bit fixed-point part of a turn
 // (rounded once from fp64), whose product with the position wraps at whole
-// turns by itself.  The result is within 2^-54 turns times the position of the
-// exact one: 2^-34 turns a million tokens in.
+// turns by itself.  That is within 2^-54 turns (times inv_freq where it is above
+// 1) times the position of the exact one, 2^-34 turns a million tokens in, and is
+// rounded to fp32's 24 bits once, as a part of half a turn: a small angle keeps
+// them all.
 #pragma once
 
 #include "block.cuh"
@@ -82,8 +84,8 @@ __device__ __forceinline__ void fill_turns(const QkParams& a, const QkTable& t, 
   __syncwarp();
   for (int32_t i = lane; i < a.rot / 2; i += 32) {
     const int64_t p = __ldg(a.positions + (int64_t)t.axis[i] * a.n + token);
-    // the upper 32 bits of the part of a turn, signed: half turns in [-1, 1)
-    const float half_turns = (float)(int32_t)(((uint64_t)p * t.step[i]) >> 32) * 0x1p-31f;
+    // the part of a turn, signed: half turns in [-1, 1]
+    const float half_turns = __ll2float_rn((int64_t)((uint64_t)p * t.step[i])) * 0x1p-63f;
     float c, s;
     sincospif(half_turns, &s, &c);
     o.c[i] = c * a.scale;
