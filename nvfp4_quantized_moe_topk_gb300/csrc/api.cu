@@ -632,7 +632,7 @@ moe_status moe_nvfp4_layer_forward(moe_nvfp4_t h, const moe_layer_args* args, mo
       l.weight = static_cast<const uint16_t*>(a.router_weight);
       l.x.data = const_cast<uint16_t*>(a.x);
       l.out.data = r.logits_out;
-      e = launch_linear(l, s);
+      e = launch_linear(l, s, h->err);
     }
     if (e == cudaSuccess) e = launch_layer_router(r, product, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;

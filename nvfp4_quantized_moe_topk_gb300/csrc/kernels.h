@@ -314,7 +314,8 @@ cudaError_t launch_qk_norm_rope_backward(const moe_qk_args& a, const moe_qk_grad
 
 constexpr int32_t kLinearMaxFeatures = 1 << 24;
 size_t linear_workspace(int32_t n, int32_t in, int32_t out);  // bytes, of the backward pass
-cudaError_t launch_linear(const moe_linear_args& a, cudaStream_t s);
+// flags: device memory for the error flags, or nullptr: linear_device_flags'.
+cudaError_t launch_linear(const moe_linear_args& a, cudaStream_t s, int32_t* flags = nullptr);
 cudaError_t launch_linear_backward(const moe_linear_args& a, const moe_linear_grads& d, void* workspace, cudaStream_t s);
 cudaError_t linear_device_flags(int32_t* flags);  // synchronizes the device; reads and clears
 

@@ -176,8 +176,9 @@ size_t linear_workspace(int32_t n, int32_t in, int32_t out) {
   return kLinearTerms * term_bytes(n, out) + (size_t)kDzMostChunks * (size_t)out * sizeof(float);
 }
 
-cudaError_t launch_linear(const moe_linear_args& a, cudaStream_t s) {
+cudaError_t launch_linear(const moe_linear_args& a, cudaStream_t s, int32_t* flags) {
   LinearProduct p = {};
+  p.flags = flags;
   p.R = a.n;
   p.F = a.out_features;
   p.C = a.in_features;

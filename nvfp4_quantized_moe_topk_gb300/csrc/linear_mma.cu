@@ -45,7 +45,7 @@ constexpr int kMaxCluster = 8;
 constexpr int32_t kChain = 8, kLongSum = 512;
 constexpr int kChainBlocks = 4;  // of 32 sums a thread
 
-// Set where a bounded wait ran out; read by moe_linear_get_device_error.
+// Set where a bounded wait ran out of a product that has no flags of its own; read by moe_linear_get_device_error.
 __device__ int32_t g_linear_flags;
 
 struct Plan {
@@ -56,6 +56,7 @@ struct Plan {
   int32_t beside;             // 1: runs beside the kernel before it, whose results it does not take
   int32_t chain;              // blocks of 64 columns that tensor memory sums before their sum moves to registers
   uint32_t stage_bytes;
+  int32_t* flags;             // or nullptr: g_linear_flags
   LinearFinish e;
 };
 
@@ -86,7 +87,7 @@ __device__ __forceinline__ void peer_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Bounded wait that also gives up when another role of the CTA has.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool wait_for(const Plan& p, uint64_t* bar, uint32_t parity, volatile int* gave_up) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
@@ -95,7 +96,7 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
     if (*gave_up) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *gave_up = 1;
-      atomicOr(&g_linear_flags, kFlagTimeout);
+      atomicOr(p.flags ? p.flags : &g_linear_flags, kFlagTimeout);
       return false;
     }
   }
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t f = ti.f0 + 128 * cta, r = ti.r0 + my_rows * cta;
         int32_t term = kb0 / p.KB, c = (kb0 - term * p.KB) * 64;
         for (int32_t kb = kb0; kb < kb1; ++kb) {
-          if (!wait_for(&empty[s], ph ^ 1u, &gave_up)) {
+          if (!wait_for(p, &empty[s], ph ^ 1u, &gave_up)) {
             ok = false;
             break;
           }
@@ -447,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = CHAIN ? chained == 0 : kb == kb0;
         if (first && kb != kb0) ++it;
         if (lane == 0) {
-          if (first) ok = wait_for(&t_empty[it & 1], ((it >> 1) & 1) ^ 1u, &gave_up);
-          ok = ok && wait_for(&full[s], ph, &gave_up);
+          if (first) ok = wait_for(p, &t_empty[it & 1], ((it >> 1) & 1) ^ 1u, &gave_up);
+          ok = ok && wait_for(p, &full[s], ph, &gave_up);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (hand_over(!ok)) break;
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum[kChainBlocks][32];
         for (int32_t kb = kb0; kb < kb1; kb += p.chain, ++it) {
           const uint32_t acc = it & 1;
-          ok = wait_for(&t_full[acc], (it >> 1) & 1, &gave_up);
+          ok = wait_for(p, &t_full[acc], (it >> 1) & 1, &gave_up);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const uint32_t acc = it & 1;
-        ok = wait_for(&t_full[acc], (it >> 1) & 1, &gave_up);
+        ok = wait_for(p, &t_full[acc], (it >> 1) & 1, &gave_up);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -722,6 +723,7 @@ cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s) {
   p.terms = a.terms;
   p.e = a.finish;
   p.beside = a.beside;
+  p.flags = a.flags;
   p.split = 1;
   const LinearFinish& f = a.finish;
   const bool q_mn = !a.q[0].c_inner, p_mn = !a.p.c_inner;

@@ -32,6 +32,7 @@ struct LinearProduct {
   // that the operands are there.)
   bool beside;
   int32_t share = 1;  // products that run beside one another
+  int32_t* flags = nullptr;  // device memory that a wait that ran out is written to; nullptr: linear_mma_flags'
 };
 cudaError_t launch_linear_mma(const LinearProduct& a, cudaStream_t s);
 // For a few rows (linear_rows.cu): one term, both operands with their columns contiguous, R <= 64.
