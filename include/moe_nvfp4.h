@@ -553,7 +553,8 @@ MOE_API moe_status moe_linear(const moe_linear_args *args, moe_stream_t stream);
  * within 2^-16 of itself, one in fp32 from dz with its 24 bits; where d_out is
  * bf16 and there is no activation dz is d_out, exactly.  The sums run in a fixed
  * order.  A NULL output is not computed; x is needed for d_weight, weight for
- * d_x.  No output may be an input. */
+ * d_x.  No output may be an input or another output, nor the workspace any of
+ * them. */
 typedef struct moe_linear_grads {
   int32_t d_out_dtype;    /* MOE_DTYPE_ of d_out */
   int32_t d_x_dtype;      /* of d_x */

@@ -288,7 +288,8 @@ moe_status moe_linear(const moe_linear_args* args, moe_stream_t stream) {
   if (a.n == 0) return MOE_OK;
   if (!a.x.data || !a.weight || !a.out.data || a.z.data == a.out.data) return MOE_ERR_INVALID_ARG;
   if (a.out.data == a.x.data || a.out.data == a.weight ||
-      (a.z.data && (a.z.data == a.x.data || a.z.data == a.weight || a.z.data == a.residual.data)))
+      (a.z.data && (a.z.data == a.x.data || a.z.data == a.weight || a.z.data == a.residual.data)) ||
+      (a.bias && (a.bias == a.out.data || a.bias == a.z.data)))
     return MOE_ERR_INVALID_ARG;
   if (a.residual.data == a.out.data &&
       (a.residual_dtype != a.out_dtype || !same_rows(a.residual, a.out, a.out_features)))
@@ -316,10 +317,15 @@ moe_status moe_linear_backward(const moe_linear_args* args, const moe_linear_gra
     if (!d.d_out.data || (a.activation != MOE_LINEAR_NONE && !a.z.data) || (d.d_weight && !a.x.data) ||
         (d.d_x.data && !a.weight))
       return MOE_ERR_INVALID_ARG;
-    // the outputs are written while the inputs are read
-    for (const void* out : {(const void*)d.d_x.data, (const void*)d.d_weight, (const void*)d.d_bias})
-      if (out && (out == d.d_out.data || out == a.x.data || out == a.z.data || out == a.weight || out == workspace))
-        return MOE_ERR_INVALID_ARG;
+    // the outputs, and the workspace, are written while the inputs are read
+    const void* const written[] = {d.d_x.data, d.d_weight, d.d_bias, workspace};
+    for (int i = 0; i < 4; ++i) {
+      const void* out = written[i];
+      if (!out) continue;
+      if (out == d.d_out.data || out == a.x.data || out == a.z.data || out == a.weight) return MOE_ERR_INVALID_ARG;
+      for (int k = 0; k < i; ++k)
+        if (out == written[k]) return MOE_ERR_INVALID_ARG;
+    }
     if (!workspace || workspace_bytes < linear_workspace(a.n, a.in_features, a.out_features)) return MOE_ERR_CAPACITY;
   }
   return status_of(launch_linear_backward(a, d, workspace, reinterpret_cast<cudaStream_t>(stream)));
