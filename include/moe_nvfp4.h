@@ -519,7 +519,7 @@ MOE_API moe_status moe_lora_get_device_error(int32_t *flags);
 #define MOE_LINEAR_SILU 2      /* z / (1 + exp(-z)) */
 #define MOE_LINEAR_GELU_TANH 3 /* z / 2 * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) */
 typedef struct moe_linear_args {
-  int32_t n;              /* tokens */
+  int32_t n;              /* tokens, at most 2^31 - 2^10 */
   int32_t in_features;    /* multiple of 8, at most 2^24 */
   int32_t out_features;   /* multiple of 8, at most 2^24 */
   int32_t activation;     /* MOE_LINEAR_ */

@@ -99,7 +99,8 @@ moe_status check_linear(const moe_linear_args& a) {
   if (a.activation < MOE_LINEAR_NONE || a.activation > MOE_LINEAR_GELU_TANH || !is_dtype(a.bias_dtype) ||
       !is_dtype(a.residual_dtype) || !is_dtype(a.z_dtype) || !is_dtype(a.out_dtype))
     return MOE_ERR_INVALID_ARG;
-  if (a.in_features % 8 || a.out_features % 8 || a.in_features > kLinearMaxFeatures || a.out_features > kLinearMaxFeatures)
+  if (a.in_features % 8 || a.out_features % 8 || a.in_features > kLinearMaxFeatures || a.out_features > kLinearMaxFeatures ||
+      a.n > kLinearMaxTokens)
     return MOE_ERR_UNSUPPORTED;
   if (!rows_ok(a.x, a.in_features, MOE_DTYPE_BF16) || !rows_ok(a.z, a.out_features, a.z_dtype) || !aligned(a.weight, 16))
     return MOE_ERR_INVALID_ARG;

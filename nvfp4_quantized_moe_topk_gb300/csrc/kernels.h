@@ -313,6 +313,7 @@ cudaError_t launch_qk_norm_rope(const moe_qk_args& a, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_backward(const moe_qk_args& a, const moe_qk_grads& d, float* part, cudaStream_t s);
 
 constexpr int32_t kLinearMaxFeatures = 1 << 24;
+constexpr int32_t kLinearMaxTokens = INT32_MAX - 1023;  // rows are counted in 32 bits, to the end of a tile or a turn
 size_t linear_workspace(int32_t n, int32_t in, int32_t out);  // bytes, of the backward pass
 // flags: device memory for the error flags, or nullptr: linear_device_flags'.
 cudaError_t launch_linear(const moe_linear_args& a, cudaStream_t s, int32_t* flags = nullptr);

@@ -691,7 +691,7 @@ Shape choose(int32_t R, int32_t F, int32_t blocks, bool q_mn, int32_t share, con
   for (int cg = 1; cg <= 2; ++cg)
     for (const int32_t rows : kRows) {
       if (rows % (16 * cg) || (q_mn && rows < 64 * cg)) continue;
-      if (rows >= 2 * R && rows > 64 * cg) continue;
+      if (rows >= 2 * (int64_t)R && rows > 64 * cg) continue;
       const int64_t tiles = (int64_t)((R + rows - 1) / rows) * ((F + 128 * cg - 1) / (128 * cg));
       const int32_t held = rows / cg, units = clusters[cg];
       const double block = std::max({2.0 * rows, (16384.0 + 128.0 * (q_mn ? (held + 63) / 64 * 64 : held)) / 64, 500.0});

@@ -1,4 +1,4 @@
-"""The projections' arrays that may not be one another, without a GPU (no accepted call is made here: the addresses are not
+"""The projections' arrays that may not be one another, and more tokens than they count, without a GPU (no accepted call is made here: the addresses are not
 memory)."""
 import pytest
 
@@ -22,3 +22,10 @@ def test_no_gradient_is_another(lib, gk):  # noqa: F811
 def test_the_workspace_is_its_own(lib, at):  # noqa: F811
     """d_out, x, weight and z are read after the workspace has been written."""
     assert lib.moe_linear_backward(args(act=1, **OWN), grads(dy=19 * A), at, 1 << 40, None) == 1
+
+
+@pytest.mark.parametrize("n", [(1 << 31) - 1023, (1 << 31) - 1])
+def test_tokens_that_32_bits_do_not_count(lib, n):  # noqa: F811
+    """The last rows' numbers, rounded up to a tile or a turn, would pass 2^31."""
+    assert lib.moe_linear(args(n=n, **OWN), None) == 2
+    assert lib.moe_linear_backward(args(n=n, **OWN), grads(dy=19 * A), 8 * A, 1 << 60, None) == 2
