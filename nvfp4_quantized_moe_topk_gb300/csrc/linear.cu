@@ -29,7 +29,7 @@ struct DzParams {
   int32_t lanes;  // of 8 columns each, side by side in a CTA; the other threads take other rows
   moe_rows d_out, z;
   uint16_t* terms;    // [kLinearTerms][n][out] or NULL
-  int32_t n_terms;
+  int32_t n_terms;    // none, two or three
   float* part;        // [chunks][out] or NULL
   int32_t beside;     // 1: launched after products whose results it does not take (LinearProduct::beside)
 };
@@ -58,28 +58,24 @@ __device__ __forceinline__ void values8(const Raw8<float>& r, float (&v)[8]) {
   }
 }
 
-// The next bf16 term of 8 values, taken off them.  Rounded, so that the first two are nearest; but (`plain`: there is none) a
-// finite value above the largest bf16 stays finite, and of an infinity nothing is left, where a subtraction gives NaN.
-constexpr float kRoundsToInfinity = 0x1.ffp127f;  // the smallest that does
-__device__ __forceinline__ uint4 take_rounded(float (&v)[8], bool plain) {
+// The next bf16 term of 8 values, taken off them, rounded to nearest, cut to `most`: the first to bf16's range, so that a
+// large finite value has finite terms.  (An infinity's second term is infinite; nothing is left of it then, or of a NaN,
+// where a subtraction gives NaN.)
+constexpr float kMostBf16 = 0x1.fep127f;
+__device__ __forceinline__ float within(float v, float most) {
+  asm("{\n .reg .f32 t;\n min.NaN.f32 t, %0, %1;\n neg.f32 %0, %1;\n max.NaN.f32 %0, t, %0;\n}\n" : "+f"(v) : "f"(most));
+  return v;
+}
+__device__ __forceinline__ uint4 take_rounded(float (&v)[8], float most) {
   uint32_t t[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (!plain) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float& s = v[2 * i + k];
-        const float most = copysignf(0x1.fep127f, s);
-        const bool large = fabsf(s) >= kRoundsToInfinity, infinite = isinf(s);
-        const uint32_t h = __float_as_uint(large ? (infinite ? s : most) : __bfloat162float(__float2bfloat16_rn(s))) >> 16;
-        s = infinite ? 0.f : s - __uint_as_float(h << 16);
-        t[i] = k ? t[i] | h << 16 : h;
-      }
-      continue;
-    }
-    t[i] = pack2(v[2 * i], v[2 * i + 1]);
-    v[2 * i] -= bf16lo(t[i]);
-    v[2 * i + 1] -= bf16hi(t[i]);
+    float &a = v[2 * i], &b = v[2 * i + 1];
+    t[i] = pack2(within(a, most), within(b, most));
+    a -= bf16lo(t[i]);
+    b -= bf16hi(t[i]);
+    a = a == a ? a : 0.f;
+    b = b == b ? b : 0.f;
   }
   return make_uint4(t[0], t[1], t[2], t[3]);
 }
@@ -93,51 +89,53 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzParams a)
   const int lane = threadIdx.x % a.lanes, row = threadIdx.x / a.lanes, rows = kDzThreads / a.lanes;
   const int32_t columns = 8 * a.lanes, col = blockIdx.x * columns + 8 * lane;
   const int32_t begin = (int32_t)((int64_t)a.n * blockIdx.y / a.chunks), end = (int32_t)((int64_t)a.n * (blockIdx.y + 1) / a.chunks);
-  float sum[8] = {}, total[8] = {};
-  int turns = 0;
+  float sum[8] = {};
+  float* const total = sums + row * columns + 8 * lane;  // the thread's own until the CTA's sums meet
+  bool runs = false;
   if (!a.beside) pdl_wait();
   pdl_launch_dependents();
   if (col < a.out) {
-    for (int32_t t0 = begin + row; t0 < end; t0 += kDzAhead * rows) {
-      Raw8<DT> rd[kDzAhead];
-      Raw8<ZT> rz[kDzAhead];
+    int32_t t0 = begin + row;
+    while (true) {
+      const int32_t run = kDzRun * kDzAhead * rows, stop = end - t0 > run ? t0 + run : end;
+      for (; t0 < stop; t0 += kDzAhead * rows) {
+        Raw8<DT> rd[kDzAhead];
+        Raw8<ZT> rz[kDzAhead];
 #pragma unroll
-      for (int k = 0; k < kDzAhead; ++k) {
-        const int32_t t = min(t0 + k * rows, end - 1);
-        rd[k] = raw8<DT>(a.d_out, t, a.out, col);
-        if (ACT) rz[k] = raw8<ZT>(a.z, t, a.out, col);
-      }
-#pragma unroll
-      for (int k = 0; k < kDzAhead; ++k) {
-        const int32_t t = t0 + k * rows;
-        if (t >= end) break;
-        float d[8], z[8];
-        values8(rd[k], d);
-        if (ACT) values8(rz[k], z);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (ACT) d[i] *= linear_slope(z[i], a.act);
-          sum[i] += d[i];
+        for (int k = 0; k < kDzAhead; ++k) {
+          const int32_t t = min(t0 + k * rows, end - 1);
+          rd[k] = raw8<DT>(a.d_out, t, a.out, col);
+          if (ACT) rz[k] = raw8<ZT>(a.z, t, a.out, col);
         }
-        float most = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(d[i]));
-        for (int m = 0; m < a.n_terms; ++m)
-          *reinterpret_cast<uint4*>(a.terms + ((int64_t)m * a.n + t) * a.out + col) = take_rounded(d, most < kRoundsToInfinity);
-      }
-      if (++turns == kDzRun) {
-        turns = 0;
+        for (int k = 0; k < kDzAhead; ++k) {
+          const int32_t t = t0 + k * rows;
+          if (t >= end) break;
+          float d[8], z[8];
+          values8(rd[k], d);
+          if (ACT) values8(rz[k], z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          total[i] += sum[i];
-          sum[i] = 0.f;
+          for (int i = 0; i < 8; ++i) {
+            if (ACT) d[i] *= linear_slope(z[i], a.act);
+            sum[i] += d[i];
+          }
+          uint16_t* to = a.terms + (int64_t)t * a.out + col;
+          for (int m = 0; m < a.n_terms; ++m, to += (int64_t)a.n * a.out)
+            *reinterpret_cast<uint4*>(to) = take_rounded(d, m == 0 ? kMostBf16 : INFINITY);
         }
       }
+      if (t0 >= end) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        total[i] = sum[i] + (runs ? total[i] : 0.f);
+        sum[i] = 0.f;
+      }
+      runs = true;
     }
   }
   if (a.part) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[row * columns + 8 * lane + i] = total[i] + sum[i];
+    for (int i = 0; i < 8; ++i) total[i] = sum[i] + (runs ? total[i] : 0.f);
     __syncthreads();
     for (int32_t i = threadIdx.x; i < columns; i += kDzThreads) {
       const int32_t c = blockIdx.x * columns + i;

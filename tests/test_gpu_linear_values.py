@@ -160,3 +160,19 @@ def test_column_sums_of_many_tokens(n):
     api.linear_backward(dy, None, w, None, None, None, d_b)
     ref = dy[0].to(D) * n
     assert bool(((d_b.to(D) - ref).abs() <= (64 + n / 2432 / 64 + 1 + 8 + 10 + 5) * U * ref.abs()).all())
+
+
+@pytest.mark.parametrize("n", [3, 100])
+@pytest.mark.parametrize("value", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("dx,dw", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "bf16")])
+def test_a_gradient_that_is_no_number_stays_in_its_row(n, value, dx, dw):
+    c = Case(n, 136, 72, activation="relu2", z="fp32", o="fp32", dx=dx, dw=dw)
+    c.backward_inputs()
+    c.w[5], c.x[1], c.zs[1, 5] = c.w[5].abs() + 0.5, c.x[1].abs() + 0.5, 1.0
+    clean = c.backward()
+    c.dy[1, 5] = value
+    d_x, d_w, d_b = c.backward()
+    rows, outs = torch.arange(n, device=DEV) != 1, torch.arange(72, device=DEV) != 5
+    assert torch.equal(d_x[rows], clean[0][rows]) and torch.equal(d_w[outs], clean[1][outs])
+    for got in (d_x[1], d_w[5], d_b[5]):
+        assert bool((got.isnan() if value != value else got == value).all())
