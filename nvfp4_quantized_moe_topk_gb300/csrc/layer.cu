@@ -82,6 +82,24 @@ __device__ __forceinline__ RouterTerms<float> router_terms(const float* p) {
   const float4 lo = __ldg(reinterpret_cast<const float4*>(p)), hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
   float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   RouterTerms<float> r;
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
+  // None of them rounds to infinity: by rounding, which takes fewer instructions than cutting off (32 tokens: 20.7 us, 22.4).
+  if (most < 0x1.ffp127f) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      uint32_t d[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[i] = pack2(v[2 * i], v[2 * i + 1]);
+        v[2 * i] -= bf16lo(d[i]);
+        v[2 * i + 1] -= bf16hi(d[i]);
+      }
+      r.v[k] = make_uint4(d[0], d[1], d[2], d[3]);
+    }
+    return r;
+  }
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     uint32_t d[4];
