@@ -552,9 +552,10 @@ MOE_API moe_status moe_linear(const moe_linear_args *args, moe_stream_t stream);
  * residual and out are not looked at.  A gradient in bf16 is summed from dz
  * within 2^-16 of itself, one in fp32 from dz with its 24 bits; where d_out is
  * bf16 and there is no activation dz is d_out, exactly.  The sums run in a fixed
- * order.  A NULL output is not computed; x is needed for d_weight, weight for
- * d_x.  No output may be an input or another output, nor the workspace any of
- * them. */
+ * order.  An infinity in weight or x meets each term of dz: it leaves NaN where
+ * one of them is 0.  A NULL output is not computed; x is needed for d_weight,
+ * weight for d_x.  No output may be an input or another output, nor the
+ * workspace any of them. */
 typedef struct moe_linear_grads {
   int32_t d_out_dtype;    /* MOE_DTYPE_ of d_out */
   int32_t d_x_dtype;      /* of d_x */
@@ -565,8 +566,10 @@ typedef struct moe_linear_grads {
   float *d_bias;          /* out [out_features] */
 } moe_linear_grads;
 
-/* Errors: as moe_linear, and MOE_ERR_CAPACITY (workspace too small).  n = 0
- * writes zeros to d_weight and d_bias. */
+/* Errors: as moe_linear, and MOE_ERR_CAPACITY (workspace too small).  The
+ * workspace has the size for these features and any types and outputs (up to
+ * three bf16 terms of dz), whether or not the call needs all of it, so that one
+ * serves every call of a projection.  n = 0 writes zeros to d_weight and d_bias. */
 MOE_API moe_status moe_linear_backward(const moe_linear_args *args, const moe_linear_grads *grads, void *workspace,
                                        size_t workspace_bytes, moe_stream_t stream);
 MOE_API size_t moe_linear_workspace_bytes(int32_t n, int32_t in_features, int32_t out_features);
@@ -665,8 +668,9 @@ MOE_API size_t moe_qk_workspace_bytes(int32_t n, int32_t q_heads, int32_t k_head
  * with y as at the top of the file, in fp32 and in a fixed order.  A batch that
  * moe_nvfp4_forward runs as one launch takes two here (the router and the
  * layer); a larger one takes the router's product on the tensor
- * cores (bf16 router_weight and E a multiple of 8; otherwise on the plain
- * cores), the picks and moe_nvfp4_forward's launches.  A few tokens have a
+ * cores' asynchronous path (bf16 router_weight and E a multiple of 8;
+ * otherwise by warp-level products, an fp32 weight in three bf16 terms), the
+ * picks and moe_nvfp4_forward's launches.  A few tokens have a
  * kernel of their own, which packs no rows: moe_nvfp4_debug_routing and
  * _intermediates return MOE_ERR_UNSUPPORTED after it; after a larger batch they
  * describe the launch's own arrangement of the shared experts. */

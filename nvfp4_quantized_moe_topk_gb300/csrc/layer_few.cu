@@ -15,9 +15,9 @@
 // tiles), then the down product's (16 columns of the output over a part of the
 // experts' rows, so that there are a few items an SM).
 //
-// A block draws its items' numbers in order.  A down item's weights
-// are on their way before its block waits for the up items of the experts that it
-// needs; those have lower numbers, so their blocks are under way, and a block
+// A block draws its items' numbers in order.  Its first down item's weights
+// are on their way before the block waits, once, for the up items of all experts;
+// those have lower numbers, so their blocks are under way, and a block
 // waits only when it has finished its own up items: every wait ends (and is
 // bounded all the same).  The last part to finish 16 columns adds the parts in
 // order, so that the bits do not depend on timing.

@@ -16,11 +16,12 @@
 // through each other's shared memory, in order.
 //
 // The products bound large ones: 16384 tokens of 4096 to 8192 with bias and relu2,
-// its argument kept, 642 us, 1.71 PFLOP/s (88 % of what the library reaches for a
-// product alone); 4314 tokens of 4096 to 2688 with a residual 65 us, 1.47.  Small
-// ones are bound by their start, 4 us until the first result: 33 tokens 5 us.  A
-// backward pass of 4314 tokens of 2688 to 4608, d_weight in fp32, takes 166 us for
-// 214 GFLOP, 1.28 PFLOP/s.
+// its argument kept, 655 us back to back in a graph (1.68 PFLOP/s), 690 as called
+// with inputs that change; 4314 tokens of 4096 to 2688 with a residual 64 us (1.48)
+// and 71.  Small ones are bound by their start, 4 us until the first result, and a
+// cluster's meeting: 24 tokens of 4096 to 4096 11.6 us.  A backward pass of 4314
+// tokens of 2688 to 4608, d_weight in fp32, takes 164 us (1.30 PFLOP/s for 214
+// GFLOP) and 170.
 #include <algorithm>
 
 #include "block.cuh"

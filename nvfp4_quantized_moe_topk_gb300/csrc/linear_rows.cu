@@ -7,7 +7,7 @@
 // warps an eighth of the columns each, all of a batch's loads in flight before
 // the first product; warp-level matrix instructions take 16 features by 8
 // tokens, and the warps' sums meet once in shared memory, in order.  One token of
-// 2688 to 4608 (25 MB of weights, not in L2): 6.1 us, 4.1 TB/s; with weights in L2 3.6.
+// 2688 to 4608 (25 MB of weights, not in L2): 5.5 us, 4.5 TB/s; with weights in L2 3.6.
 //
 // A lane's 16 bytes of a row are 8 consecutive columns; which of them an
 // instruction pairs with which only has to be the same for weights and x, so
