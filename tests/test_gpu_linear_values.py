@@ -176,3 +176,24 @@ def test_a_gradient_that_is_no_number_stays_in_its_row(n, value, dx, dw):
     assert torch.equal(d_x[rows], clean[0][rows]) and torch.equal(d_w[outs], clean[1][outs])
     for got in (d_x[1], d_w[5], d_b[5]):
         assert bool((got.isnan() if value != value else got == value).all())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=100, inp=(1 << 19) + 8, out=136, activation="relu2", z="bf16", bias="fp32", residual="bf16"),
+    dict(n=70, inp=1 << 19, out=72, activation="silu", bias="bf16", residual="fp32", scale=0.5, wide=8),
+    dict(n=9, inp=40000, out=520, activation="gelu_tanh", z="fp32", residual="bf16", o="fp32")])
+def test_epilogues_behind_long_sums(kw):
+    Case(**kw).check()
+
+
+@pytest.mark.parametrize("n", [20, 100, 700])
+def test_gradients_of_two_types_are_those_of_each_alone(n):
+    """dz in three terms for one gradient: the other takes the first two, the same as by itself."""
+    c = Case(n, 264, 520, activation="silu", dx="bf16", dw="fp32")
+    c.backward_inputs()
+    d_x, d_w, d_b = c.backward()
+    x, w, b = torch.empty_like(d_x), torch.empty_like(d_w), torch.empty_like(d_b)
+    api.linear_backward(c.dy, None, c.w, c.zs, x, activation="silu")
+    api.linear_backward(c.dy, c.x, c.w, c.zs, None, w, activation="silu")
+    api.linear_backward(c.dy, None, c.w, c.zs, None, None, b, activation="silu")
+    assert torch.equal(x, d_x) and torch.equal(w, d_w) and torch.equal(b, d_b)
