@@ -82,7 +82,7 @@ __device__ __forceinline__ uint4 take_rounded(float (&v)[8], float most) {
 
 // dz of 8 lanes' columns and a chunk of tokens, and its column sums.
 constexpr int kDzAhead = 4;  // rows of a thread on their way at once
-constexpr int kDzRun = 16;    // such turns whose sums are added one after another, so that a sum's error does not grow with n
+constexpr int kDzRun = 16;   // such turns that are added one after another, so that a sum's error does not grow with n
 template <bool ACT, typename DT, typename ZT>
 __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzParams a) {
   __shared__ float sums[8 * kDzThreads];

@@ -1,5 +1,5 @@
-"""The projections' arrays that may not be one another, and more tokens than they count, without a GPU (no accepted call is made here: the addresses are not
-memory)."""
+"""The projections' arrays that may not be one another, and more tokens than they count, without a GPU (no accepted call is
+made here: the addresses are not memory)."""
 import pytest
 
 from test_linear_abi import A, args, grads, lib  # noqa: F401
